@@ -1,6 +1,8 @@
 /*
  * gs.h -- C ABI of libgs, GB300 (sm_103a) kernels for spatial-transformer
- * sampling: AffineGrid, GridSample, the two fused, and DeformConv.
+ * sampling: AffineGrid, GridSample, the two fused, and DeformConv; and for the
+ * transformer block over the sampled tokens: layer norm, dropout and attention
+ * with a relative position bias, with their gradients.
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -404,6 +406,187 @@ gs_status gs_resize_output_shape(int rank, const int64_t *x_shape, const int64_t
 gs_status gs_resize(const void *X, int rank, const int64_t *x_shape, const int64_t *axes,
                     int naxes, const float *scales, const int64_t *sizes, const float *roi,
                     const gs_resize_attrs *attrs, gs_dtype dt, void *Y, cudaStream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Operators of a transformer block over sampled tokens.  A sampled map or
+ * glimpse is a grid of tokens; these calls normalise them, let them attend to
+ * one another with a learned bias by relative grid position, and drop and sum
+ * the branch, each with its gradient.  Sums, statistics and softmax run in
+ * fp32 and are rounded once, at the store.  No sum depends on the order in
+ * which threads finish: a call repeated on the same inputs gives the same bits.
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * gs_layer_norm -- LayerNormalization (ai.onnx, since version 17): Inputs X,
+ * Scale, B; Attributes epsilon; Outputs Y, Mean, InvStdDev (stash_type 1).
+ *
+ *   X        device, (rows, D): the axes from `axis` on are flattened into D.
+ *   Scale    device, (D).          B  device, (D), or NULL for zeros.
+ *   rows     < 2^31.               D  <= 2^20.
+ *   epsilon  >= 0, added to the variance.
+ *   Y        device output, (rows, D).
+ *   Mean, InvStdDev  device outputs, (rows) fp32, or NULL.  The backward pass
+ *            takes both.
+ *
+ * mean = sum x / D, var = sum (x - mean)^2 / D (two passes over the row, held
+ * on chip up to D = 8192), InvStdDev = 1 / sqrt(var + epsilon),
+ * Y = (x - mean) * InvStdDev * Scale + B.
+ */
+gs_status gs_layer_norm(const void *X, const void *Scale, const void *B, int64_t rows, int64_t D,
+                        gs_dtype dt, float epsilon, void *Y, float *Mean, float *InvStdDev,
+                        cudaStream_t stream);
+
+/* Device workspace gs_layer_norm_backward needs (host output `bytes`). */
+gs_status gs_layer_norm_backward_workspace_size(int64_t rows, int64_t D, size_t *bytes);
+
+/*
+ * gs_layer_norm_backward -- the gradient of gs_layer_norm.
+ *
+ *   dY       device, (rows, D).     X, Scale, Mean, InvStdDev as above.
+ *   workspace  device, 16-byte aligned (GS_ERR_ALIGN), at least the size
+ *            gs_layer_norm_backward_workspace_size reports (GS_ERR_SHAPE for
+ *            less, GS_ERR_NULL for none) unless dScale and dB are both NULL.
+ *   dX       device output, (rows, D).
+ *   dScale, dB  device outputs, (D) of `dt`, each or both NULL.  With rows = 0
+ *            they are written as zeros.
+ *
+ * xhat = (x - Mean) * InvStdDev, g = dY * Scale,
+ * dX = InvStdDev * (g - mean(g) - xhat * mean(g * xhat)),
+ * dScale = sum over rows of dY * xhat, dB = sum over rows of dY.
+ */
+gs_status gs_layer_norm_backward(const void *dY, const void *X, const void *Scale,
+                                 const float *Mean, const float *InvStdDev, int64_t rows,
+                                 int64_t D, gs_dtype dt, void *workspace, size_t workspace_bytes,
+                                 void *dX, void *dScale, void *dB, cudaStream_t stream);
+
+/*
+ * gs_dropout -- Dropout (ai.onnx, since version 13) in training mode, with an
+ * optional residual sum: Y = residual + (kept ? X / (1 - ratio) : 0).
+ *
+ *   X, residual, Y  device, n elements; residual may be NULL.  Y may be X or
+ *            residual itself (in place); other overlaps are not allowed.
+ *   n        <= 2^40.
+ *   ratio    in [0, 1): the probability of dropping, to 2^-32.
+ *   seed, offset  the generator's key and stream.  Take another offset for
+ *            every layer and step.
+ *
+ * Element i draws word i % 4 of Philox4x32-10 (Salmon et al., SC 2011) with
+ * key `seed` and counter (i / 4, offset), low words first, and is kept when
+ * word >= round(ratio * 2^32).  The mask is a function of these numbers alone
+ * and is stored nowhere.  The gradient with respect to X is the same call on
+ * dY (no residual) with the same ratio, seed and offset; the gradient with
+ * respect to the residual is dY.
+ */
+gs_status gs_dropout(const void *X, const void *residual, int64_t n, gs_dtype dt, double ratio,
+                     uint64_t seed, uint64_t offset, void *Y, cudaStream_t stream);
+
+/*
+ * Shapes of gs_attention.  Queries lie on a grid of q_extent = (Hq, Wq) tokens
+ * and keys on one of k_extent = (Hk, Wk), both row-major, Lq = Hq * Wq and
+ * Lk = Hk * Wk; a plain sequence is (1, L).
+ *   N, H, D     batch, heads, head width (1 to 128).
+ *   *_strides   strides of Q, K and V in elements for (batch, token, head);
+ *               the D elements of a head are contiguous.  This covers
+ *               (N, L, H, D) and (N, H, L, D) tensors, a packed
+ *               (N, L, 3, H, D) projection and heads that share keys (stride
+ *               0).  O, dO, dQ, dK and dV are dense (N, L, H, D).
+ *   num_buckets rows of the bias table, or 0 for no bias.
+ *   scale       of the scores, usually 1 / sqrt(D); finite.
+ * Limits (GS_ERR_SHAPE): extents and strides >= 0, N * H * Lq and N * H * Lk
+ * < 2^31, (Hq+Hk-1) * (Wq+Wk-1) <= 2^24, num_buckets * H < 2^31.
+ */
+typedef struct {
+    int64_t N, H, D;
+    int64_t q_extent[2], k_extent[2];
+    int64_t q_strides[3], k_strides[3], v_strides[3];
+    int64_t num_buckets;
+    float scale;
+} gs_attention_attrs;
+
+/*
+ * gs_relative_buckets -- a bucket map for gs_attention (host only).
+ *
+ *   q_extent, k_extent  host, the two grids.
+ *   q_origin   host, the key-grid position of query (0, 0), or NULL for
+ *              (0, 0): one new token at the end of a sequence of L keys has
+ *              q_extent (1, 1) and q_origin (0, L - 1).
+ *   num_buckets  buckets per axis, or 0 to give every relative position its
+ *              own.  Otherwise even, >= 4 (a multiple of 2 whose half has a
+ *              first half): per axis, half of the buckets belong to keys at or
+ *              before the query (offset query - key >= 0) and half to keys
+ *              after it; in each, the first half hold one distance each and
+ *              the rest grow by a constant ratio up to max_distance, from which
+ *              on the last one is taken: with m = num_buckets / 2 and e = m / 2,
+ *              bucket e + k starts at distance ceil(e * (max_distance / e)^(k / (m - e))).
+ *              An axis on which both grids have extent 1 takes no part; with
+ *              two axes the bucket is by * num_buckets + bx.
+ *   max_distance  > num_buckets / 4.
+ *   causal     0, or 1: keys after the query in token order of the key grid
+ *              get -1, which masks them.  Needs grids of one row
+ *              (GS_ERR_UNSUPPORTED otherwise).
+ *   buckets    host output, (Hq+Hk-1) * (Wq+Wk-1) int32.
+ *   count      host output: rows the bias table needs.
+ */
+gs_status gs_relative_buckets(const int64_t *q_extent, const int64_t *k_extent,
+                              const int64_t *q_origin, int num_buckets, int64_t max_distance,
+                              int causal, int32_t *buckets, int64_t *count);
+
+/* Device workspace gs_attention and gs_attention_backward need (host output
+ * `bytes`; 0: none). */
+gs_status gs_attention_workspace_size(const gs_attention_attrs *attrs, gs_dtype dt, size_t *bytes);
+gs_status gs_attention_backward_workspace_size(const gs_attention_attrs *attrs, gs_dtype dt,
+                                               size_t *bytes);
+
+/*
+ * gs_attention -- softmax attention with a learned bias by relative position.
+ *
+ *   Q, K, V   device, (N, Lq | Lk, H, D) through their strides.
+ *   table     device, (num_buckets, H) of `dt`, or NULL with num_buckets = 0.
+ *   buckets   device, (Hq+Hk-1, Wq+Wk-1) int32: entry
+ *             (yq - yk + Hk-1, xq - xk + Wk-1) names the pair's row of the
+ *             table.  A value outside [0, num_buckets) masks the pair, and so
+ *             does a table entry of -inf (causal and local attention are
+ *             bucket maps).
+ *   k_len     device, (N) int32, or NULL: keys from k_len[n] on are masked
+ *             (clamped to [0, Lk]); what K and V hold there is never used.
+ *   workspace device, 256-byte aligned (GS_ERR_ALIGN), at least the size
+ *             gs_attention_workspace_size reports (GS_ERR_NULL for none,
+ *             GS_ERR_SHAPE for less).
+ *   O         device output, (N, Lq, H, D).
+ *   LSE       device output, (N, H, Lq) fp32, or NULL: the natural logarithm
+ *             of the sum of exponentials, which the backward pass takes.
+ *
+ * s = scale * q . k + table[bucket][h];  O = softmax(s) V.  A row whose mask
+ * leaves no key gives O = 0 and LSE = -inf.  A row of finite entries as low as
+ * the type allows is an ordinary softmax.
+ */
+gs_status gs_attention(const void *Q, const void *K, const void *V, const void *table,
+                       const int32_t *buckets, const int32_t *k_len,
+                       const gs_attention_attrs *attrs, gs_dtype dt, void *workspace,
+                       size_t workspace_bytes, void *O, float *LSE, cudaStream_t stream);
+
+/*
+ * gs_attention_backward -- the gradient of gs_attention.
+ *
+ *   dO, O     device, (N, Lq, H, D).       LSE  device, (N, H, Lq) fp32.
+ *   dQ, dK, dV  device outputs, dense (N, Lq | Lk, H, D).  Rows of masked keys
+ *             and of queries with no key are zero.
+ *   dTable    device output, (num_buckets, H) of `dt`; NULL without a table.
+ *   Other arguments as gs_attention; the workspace's size is
+ *   gs_attention_backward_workspace_size.
+ *
+ * With p = exp(s - LSE) and delta = dO . O per query:
+ * dS = p * (dO . v - delta);  dQ = scale * dS K;  dK = scale * dS^T Q;
+ * dV = p^T dO;  dTable[b][h] = sum of dS over the batch and bucket b's pairs.
+ */
+gs_status gs_attention_backward(const void *dO, const void *Q, const void *K, const void *V,
+                                const void *O, const float *LSE, const void *table,
+                                const int32_t *buckets, const int32_t *k_len,
+                                const gs_attention_attrs *attrs, gs_dtype dt, void *workspace,
+                                size_t workspace_bytes, void *dQ, void *dK, void *dV,
+                                void *dTable, cudaStream_t stream);
 
 /* Human-readable name of a status code (static storage). */
 const char *gs_status_str(gs_status s);

@@ -13,6 +13,8 @@ Operators (see the docstrings and include/gs.h):
                    zeros / border / reflection; both align_corners)
   gs_affine_sample GridSample(X, AffineGrid(theta, size)) fused
   gs_deform_conv   DeformConv 2-D
+  gs_layer_norm, gs_dropout, gs_attention (and their gradients)
+                   a transformer block over the sampled tokens (block.py)
 
 Host-memory variants (gs_affine_sample_from_host, gs_grid_sample_from_host)
 stream a batch from pinned host memory in chunks, overlapping the copies in
@@ -24,7 +26,8 @@ import os
 __all__ = ["gs_affine_grid", "gs_grid_sample", "gs_affine_sample", "gs_deform_conv",
            "gs_status_str", "gs_device_status", "GsError", "library_path", "load_library",
            "EXPORTED_SYMBOLS", "HostStreamer", "gs_affine_sample_from_host",
-           "gs_grid_sample_from_host"]
+           "gs_grid_sample_from_host", "gs_layer_norm", "gs_layer_norm_backward", "gs_dropout",
+           "gs_attention", "gs_attention_backward", "gs_relative_buckets"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "_build", "libgs.so")
@@ -32,7 +35,8 @@ _LIB_PATH = os.path.join(_HERE, "_build", "libgs.so")
 EXPORTED_SYMBOLS = ("gs_affine_grid", "gs_grid_sample", "gs_affine_sample",
                     "gs_affine_sample_from_host", "gs_deform_conv",
                     "gs_resize", "gs_resize_output_shape", "gs_grid_sample_int", "gs_status_str",
-                    "gs_device_status",
+                    "gs_device_status", "gs_layer_norm", "gs_layer_norm_backward", "gs_dropout",
+                    "gs_relative_buckets", "gs_attention", "gs_attention_backward",
                     "gs_version")
 
 MODES = {"linear": 0, "bilinear": 0, "nearest": 1, "cubic": 2, "bicubic": 2}
@@ -68,6 +72,15 @@ class DeformAttrs(ctypes.Structure):
     _fields_ = [("kernel", ctypes.c_int64 * 2), ("pads", ctypes.c_int64 * 4),
                 ("strides", ctypes.c_int64 * 2), ("dilations", ctypes.c_int64 * 2),
                 ("group", ctypes.c_int64), ("offset_group", ctypes.c_int64)]
+
+
+class AttentionAttrs(ctypes.Structure):
+    """gs_attention_attrs (include/gs.h)."""
+    _fields_ = [("N", ctypes.c_int64), ("H", ctypes.c_int64), ("D", ctypes.c_int64),
+                ("q_extent", ctypes.c_int64 * 2), ("k_extent", ctypes.c_int64 * 2),
+                ("q_strides", ctypes.c_int64 * 3), ("k_strides", ctypes.c_int64 * 3),
+                ("v_strides", ctypes.c_int64 * 3), ("num_buckets", ctypes.c_int64),
+                ("scale", ctypes.c_float)]
 
 
 def library_path():
@@ -106,6 +119,19 @@ def load_library(path=None):
                                          ctypes.POINTER(ResizeAttrs), i64p]
     L.gs_resize.argtypes = [vp, ci, i64p, i64p, ci, f32p, i64p, f32p, ctypes.POINTER(ResizeAttrs),
                             ci, vp, vp]
+    i64, u64, sz = ctypes.c_int64, ctypes.c_uint64, ctypes.c_size_t
+    szp, atp = ctypes.POINTER(ctypes.c_size_t), ctypes.POINTER(AttentionAttrs)
+    L.gs_layer_norm.argtypes = [vp, vp, vp, i64, i64, ci, cf, vp, vp, vp, vp]
+    L.gs_layer_norm_backward_workspace_size.argtypes = [i64, i64, szp]
+    L.gs_layer_norm_backward.argtypes = [vp, vp, vp, vp, vp, i64, i64, ci, vp, sz, vp, vp, vp, vp]
+    L.gs_dropout.argtypes = [vp, vp, i64, ci, ctypes.c_double, u64, u64, vp, vp]
+    L.gs_relative_buckets.argtypes = [i64p, i64p, i64p, ci, i64, ci,
+                                      ctypes.POINTER(ctypes.c_int32), i64p]
+    L.gs_attention_workspace_size.argtypes = [atp, ci, szp]
+    L.gs_attention_backward_workspace_size.argtypes = [atp, ci, szp]
+    L.gs_attention.argtypes = [vp, vp, vp, vp, vp, vp, atp, ci, vp, sz, vp, vp, vp]
+    L.gs_attention_backward.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, atp, ci, vp, sz, vp, vp,
+                                        vp, vp, vp]
     L.gs_status_str.argtypes = [ci]
     L.gs_status_str.restype = ctypes.c_char_p
     L.gs_device_status.argtypes = [vp]
@@ -116,7 +142,10 @@ def load_library(path=None):
               "gs_affine_sample_from_host", "gs_deform_conv",
               "gs_deform_conv_workspace_size", "gs_deform_conv_ws", "gs_device_status",
               "gs_resize_output_shape", "gs_resize", "gs_grid_sample_int",
-              "gs_test_bounded_wait_expires"):
+              "gs_test_bounded_wait_expires", "gs_layer_norm",
+              "gs_layer_norm_backward_workspace_size", "gs_layer_norm_backward", "gs_dropout",
+              "gs_relative_buckets", "gs_attention_workspace_size",
+              "gs_attention_backward_workspace_size", "gs_attention", "gs_attention_backward"):
         getattr(L, f).restype = ci
     if path is None:
         _lib = L
@@ -641,3 +670,9 @@ def gs_grid_sample_from_host(X, grid, mode="linear", padding_mode="zeros", align
         return gs_grid_sample(x, g, mode, padding_mode, align_corners, cubic_coeff_a, out=out,
                               workspace=ws)
     return st.run(fn, [X, grid], out, [0, 0])
+
+
+from .block import (gs_attention, gs_attention_backward,  # noqa: E402
+                    gs_attention_backward_workspace_size, gs_attention_workspace_size, gs_dropout,
+                    gs_layer_norm, gs_layer_norm_backward,
+                    gs_layer_norm_backward_workspace_size, gs_relative_buckets)

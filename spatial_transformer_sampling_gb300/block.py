@@ -1,0 +1,262 @@
+"""Binding of the transformer-block operators of libgs (include/gs.h): layer norm,
+dropout with a residual sum, and attention with a learned bias by relative grid
+position, each with its gradient.  As in the rest of the package the functions
+only check and marshal; every step of the computation runs in libgs's kernels.
+"""
+import ctypes
+
+from . import (AttentionAttrs, _check_tensors, _dtype_code, _i64, _ok, _shape_error, _torch,
+               load_library)
+
+
+def _p(t):
+    return t.data_ptr() if t is not None else None
+
+
+def _current(t):
+    return _torch().cuda.current_stream(t.device).cuda_stream
+
+
+def _scratch(workspace, nbytes, like):
+    """(pointer, bytes) of a caller's workspace tensor, or with "auto" of one of `nbytes` from
+    torch's allocator, and the tensor that keeps it alive."""
+    if isinstance(workspace, str):
+        if workspace != "auto":
+            raise ValueError(f"workspace must be a tensor, None or 'auto', not {workspace!r}")
+        torch = _torch()
+        workspace = (torch.empty(nbytes, dtype=torch.uint8, device=like.device) if nbytes
+                     else None)
+    elif workspace is not None and (workspace.device != like.device
+                                    or not workspace.is_contiguous()):
+        raise ValueError("workspace must be a contiguous tensor on the inputs' device")
+    if workspace is None:
+        return None, 0, None
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+def _check_f32(t, shape, what, like):
+    torch = _torch()
+    if t.dtype != torch.float32 or t.device != like.device or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous float32 tensor on the inputs' device")
+    if tuple(t.shape) != tuple(shape):
+        _shape_error(what, t.shape, shape)
+
+
+# ------------------------------------------------------------------ layer norm
+
+def _norm_dims(X, axis):
+    if not -X.dim() <= axis < X.dim():
+        raise ValueError(f"axis {axis} out of range for X of shape {tuple(X.shape)}")
+    axis %= X.dim()
+    rows = D = 1
+    for n in X.shape[:axis]:
+        rows *= n
+    for n in X.shape[axis:]:
+        D *= n
+    return axis, rows, D
+
+
+def _check_norm_vectors(X, axis, **vectors):
+    for what, t in vectors.items():
+        if t is not None and t.shape != X.shape[axis:]:
+            _shape_error(what, t.shape, X.shape[axis:])
+
+
+def gs_layer_norm(X, Scale, B=None, axis=-1, epsilon=1e-5, out=None):
+    """LayerNormalization of X over its axes from ``axis`` on: (Y, Mean, InvStdDev).  Scale and B
+    have the shape of the normalised axes; Mean and InvStdDev are float32 with X's leading axes
+    and ones in the place of the normalised ones."""
+    torch = _torch()
+    axis, rows, D = _norm_dims(X, axis)
+    _check_tensors(X, Scale, B, out)
+    _check_norm_vectors(X, axis, Scale=Scale, B=B)
+    if out is None:
+        out = torch.empty_like(X)
+    elif out.shape != X.shape:
+        _shape_error("out", out.shape, X.shape)
+    kept = tuple(X.shape[:axis]) + (1,) * (X.dim() - axis)
+    stats = torch.empty((2,) + kept, dtype=torch.float32, device=X.device)
+    mean, inv = stats.unbind(0)
+    _ok(load_library().gs_layer_norm(X.data_ptr(), Scale.data_ptr(), _p(B), rows, D,
+                                     _dtype_code(X), epsilon, out.data_ptr(), mean.data_ptr(),
+                                     inv.data_ptr(), _current(X)), "gs_layer_norm")
+    return out, mean, inv
+
+
+def gs_layer_norm_backward_workspace_size(rows, D):
+    """Workspace bytes gs_layer_norm_backward needs."""
+    n = ctypes.c_size_t(0)
+    _ok(load_library().gs_layer_norm_backward_workspace_size(rows, D, ctypes.byref(n)),
+        "gs_layer_norm_backward_workspace_size")
+    return int(n.value)
+
+
+def gs_layer_norm_backward(dY, X, Scale, Mean, InvStdDev, axis=-1, workspace="auto"):
+    """Gradient of gs_layer_norm: (dX, dScale, dB).  ``workspace``: "auto", or a device tensor of
+    at least gs_layer_norm_backward_workspace_size bytes."""
+    torch = _torch()
+    axis, rows, D = _norm_dims(X, axis)
+    _check_tensors(X, dY, Scale)
+    if dY.shape != X.shape:
+        _shape_error("dY", dY.shape, X.shape)
+    _check_norm_vectors(X, axis, Scale=Scale)
+    kept = tuple(X.shape[:axis]) + (1,) * (X.dim() - axis)
+    _check_f32(Mean, kept, "Mean", X)
+    _check_f32(InvStdDev, kept, "InvStdDev", X)
+    dX, dScale, dB = torch.empty_like(X), torch.empty_like(Scale), torch.empty_like(Scale)
+    nbytes = gs_layer_norm_backward_workspace_size(rows, D)
+    ws, have, _keep = _scratch(workspace, nbytes, X)
+    _ok(load_library().gs_layer_norm_backward(
+        dY.data_ptr(), X.data_ptr(), Scale.data_ptr(), Mean.data_ptr(), InvStdDev.data_ptr(), rows,
+        D, _dtype_code(X), ws, have, dX.data_ptr(), dScale.data_ptr(), dB.data_ptr(),
+        _current(X)), "gs_layer_norm_backward")
+    return dX, dScale, dB
+
+
+# ------------------------------------------------------------------ dropout
+
+def gs_dropout(X, ratio=0.5, seed=0, offset=0, residual=None, out=None):
+    """residual + dropout(X) with the mask of (seed, offset), which is stored nowhere.  The
+    gradient with respect to X is ``gs_dropout(dY, ratio, seed, offset)``.  ``out`` may be X or
+    residual itself."""
+    _check_tensors(X, residual, out)
+    for what, t in (("residual", residual), ("out", out)):
+        if t is not None and t.shape != X.shape:
+            _shape_error(what, t.shape, X.shape)
+    if not 0 <= seed < 1 << 64 or not 0 <= offset < 1 << 64:
+        raise ValueError("seed and offset are unsigned 64-bit numbers")
+    if out is None:
+        out = _torch().empty_like(X)
+    _ok(load_library().gs_dropout(X.data_ptr(), _p(residual), X.numel(), _dtype_code(X), ratio,
+                                  seed, offset, out.data_ptr(), _current(X)), "gs_dropout")
+    return out
+
+
+# ------------------------------------------------------------------ attention
+
+def gs_relative_buckets(q_extent, k_extent, num_buckets=0, max_distance=128, causal=False,
+                        q_origin=(0, 0), device="cuda"):
+    """Bucket map for gs_attention: (int32 tensor (Hq+Hk-1, Wq+Wk-1) on ``device``, rows of the
+    bias table).  ``num_buckets`` 0 gives every relative position a row of its own."""
+    torch = _torch()
+    rows, cols = q_extent[0] + k_extent[0] - 1, q_extent[1] + k_extent[1] - 1
+    m = torch.empty((max(rows, 0), max(cols, 0)), dtype=torch.int32)
+    count = ctypes.c_int64(0)
+    _ok(load_library().gs_relative_buckets(
+        _i64(q_extent), _i64(k_extent), _i64(q_origin), int(num_buckets), int(max_distance),
+        int(causal), ctypes.cast(m.data_ptr(), ctypes.POINTER(ctypes.c_int32)),
+        ctypes.byref(count)), "gs_relative_buckets")
+    return m.to(device), int(count.value)
+
+
+def _head_strides(t, what):
+    if t.dim() != 4:
+        raise ValueError(f"{what} must be (N, L, H, D), got {tuple(t.shape)}")
+    s = t.stride()
+    if s[3] != 1 and t.shape[3] != 1:
+        raise ValueError(f"the last axis of {what} must be contiguous")
+    return s[:3]
+
+
+def _attention_attrs(Q, K, V, table, buckets, q_extent, k_extent, k_len, scale):
+    torch = _torch()
+    qs, ks, vs = _head_strides(Q, "Q"), _head_strides(K, "K"), _head_strides(V, "V")
+    N, Lq, H, D = Q.shape
+    Lk = K.shape[1]
+    if K.shape != (N, Lk, H, D):
+        _shape_error("K", K.shape, (N, Lk, H, D))
+    if V.shape != K.shape:
+        _shape_error("V", V.shape, K.shape)
+    for t in (K, V, table):
+        if t is not None and (t.dtype != Q.dtype or t.device != Q.device):
+            raise ValueError("all tensors of one call share dtype and device")
+    if not Q.is_cuda:
+        raise ValueError("libgs takes CUDA tensors")
+    q_extent = (1, Lq) if q_extent is None else tuple(q_extent)
+    k_extent = (1, Lk) if k_extent is None else tuple(k_extent)
+    if q_extent[0] * q_extent[1] != Lq or k_extent[0] * k_extent[1] != Lk:
+        raise ValueError(f"extents {q_extent} and {k_extent} do not hold {Lq} and {Lk} tokens")
+    if (table is None) != (buckets is None):
+        raise ValueError("table and buckets go together")
+    nb = 0
+    if table is not None:
+        if table.dim() != 2 or table.shape[1] != H or not table.is_contiguous():
+            raise ValueError(f"table must be contiguous (buckets, H={H}), got "
+                             f"{tuple(table.shape)}")
+        nb = table.shape[0]
+        R = (q_extent[0] + k_extent[0] - 1) * (q_extent[1] + k_extent[1] - 1)
+        if (buckets.dtype != torch.int32 or buckets.device != Q.device
+                or not buckets.is_contiguous() or (Lq and Lk and buckets.numel() != R)):
+            raise ValueError(f"buckets must be a contiguous int32 tensor of {R} entries on the "
+                             f"inputs' device")
+    if k_len is not None and (k_len.dtype != torch.int32 or k_len.device != Q.device
+                              or not k_len.is_contiguous() or tuple(k_len.shape) != (N,)):
+        raise ValueError(f"k_len must be a contiguous int32 tensor of N={N} entries on the "
+                         f"inputs' device")
+    i3, i2 = ctypes.c_int64 * 3, ctypes.c_int64 * 2
+    return AttentionAttrs(N, H, D, i2(*q_extent), i2(*k_extent), i3(*qs), i3(*ks), i3(*vs), nb,
+                          D ** -0.5 if scale is None else scale)
+
+
+def gs_attention_workspace_size(attrs, dtype_code, backward=False):
+    """Workspace bytes gs_attention (or gs_attention_backward) needs for an AttentionAttrs."""
+    n = ctypes.c_size_t(0)
+    name = "gs_attention_backward_workspace_size" if backward else "gs_attention_workspace_size"
+    _ok(getattr(load_library(), name)(ctypes.byref(attrs), dtype_code, ctypes.byref(n)), name)
+    return n.value
+
+
+def gs_attention_backward_workspace_size(attrs, dtype_code):
+    """Workspace bytes gs_attention_backward needs for an AttentionAttrs."""
+    return gs_attention_workspace_size(attrs, dtype_code, True)
+
+
+def gs_attention(Q, K, V, table=None, buckets=None, q_extent=None, k_extent=None, k_len=None,
+                 scale=None, out=None, workspace="auto"):
+    """softmax(scale Q K^T + table[bucket]) V over grids of tokens: (O, LSE).
+
+    Q (N, Lq, H, D), K and V (N, Lk, H, D), any strides with a contiguous last axis; ``table``
+    (buckets, H) and ``buckets`` (int32, see gs_relative_buckets) name each pair's bias;
+    ``q_extent`` / ``k_extent`` are the tokens' grids (default (1, L)); ``k_len`` (N) int32 masks
+    the keys from there on; ``scale`` defaults to 1 / sqrt(D).  O is dense (N, Lq, H, D), LSE
+    float32 (N, H, Lq)."""
+    torch = _torch()
+    at = _attention_attrs(Q, K, V, table, buckets, q_extent, k_extent, k_len, scale)
+    if out is None:
+        out = torch.empty(Q.shape, dtype=Q.dtype, device=Q.device)
+    elif (out.shape != Q.shape or not out.is_contiguous() or out.dtype != Q.dtype
+          or out.device != Q.device):
+        raise ValueError(f"out must be dense {tuple(Q.shape)} of Q's dtype and device")
+    lse = torch.empty((at.N, at.H, Q.shape[1]), dtype=torch.float32, device=Q.device)
+    code = _dtype_code(Q)
+    ws, have, _keep = _scratch(workspace, gs_attention_workspace_size(at, code), Q)
+    _ok(load_library().gs_attention(Q.data_ptr(), K.data_ptr(), V.data_ptr(), _p(table),
+                                    _p(buckets), _p(k_len), ctypes.byref(at), code, ws, have,
+                                    out.data_ptr(), lse.data_ptr(), _current(Q)), "gs_attention")
+    return out, lse
+
+
+def gs_attention_backward(dO, Q, K, V, O, LSE, table=None, buckets=None, q_extent=None,
+                          k_extent=None, k_len=None, scale=None, workspace="auto"):
+    """Gradient of gs_attention: [dQ, dK, dV, dTable] (the first three without a table); dQ, dK
+    and dV are dense (N, L, H, D)."""
+    torch = _torch()
+    at = _attention_attrs(Q, K, V, table, buckets, q_extent, k_extent, k_len, scale)
+    _check_tensors(dO, O)
+    for what, t in (("dO", dO), ("O", O)):
+        if t.shape != Q.shape:
+            _shape_error(what, t.shape, Q.shape)
+    if dO.dtype != Q.dtype or dO.device != Q.device:
+        raise ValueError("all tensors of one call share dtype and device")
+    _check_f32(LSE, (at.N, at.H, Q.shape[1]), "LSE", Q)
+    made = [torch.empty(t.shape, dtype=Q.dtype, device=Q.device) for t in (Q, K, V)]
+    if table is not None:
+        made.append(torch.empty(table.shape, dtype=Q.dtype, device=Q.device))
+    code = _dtype_code(Q)
+    ws, have, _keep = _scratch(workspace, gs_attention_workspace_size(at, code, True), Q)
+    _ok(load_library().gs_attention_backward(
+        dO.data_ptr(), Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(), LSE.data_ptr(),
+        _p(table), _p(buckets), _p(k_len), ctypes.byref(at), code, ws, have, made[0].data_ptr(),
+        made[1].data_ptr(), made[2].data_ptr(), made[3].data_ptr() if table is not None else None,
+        _current(Q)), "gs_attention_backward")
+    return made

@@ -64,6 +64,12 @@ void *static_workspace() {
     return symbol_address(cache, g_gs_static_ws);
 }
 
+}  // namespace
+
+unsigned *gs::device_error_word() { return error_word(); }
+
+namespace {
+
 constexpr int64_t kMaxExtent = int64_t(1) << 20;
 constexpr int64_t kMaxSlab = (int64_t(1) << 31) - 1;
 

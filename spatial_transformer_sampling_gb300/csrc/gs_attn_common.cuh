@@ -1,0 +1,47 @@
+// gs_attn_common.cuh -- what the attention kernels share: token geometry, the
+// expanded bias and the base-2 exponential.
+#pragma once
+
+#include "gs_common.cuh"
+#include "gs_internal.h"
+
+namespace gs {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// 2^x; x = -inf gives 0.
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Relative index of a token on its side (see AttnArgs).
+__device__ __forceinline__ int rel_q(const AttnArgs &a, int i) {
+    const int y = i / a.Wq;
+    return (y + a.Hk - 1) * a.P + (i - y * a.Wq) + a.Wk - 1;
+}
+__device__ __forceinline__ int rel_k(const AttnArgs &a, int j) {
+    const int y = j / a.Wk;
+    return y * a.P + (j - y * a.Wk);
+}
+
+// Keys of batch item n that may be attended to.
+__device__ __forceinline__ int keys_of(const AttnArgs &a, int n) {
+    return a.k_len ? min(max(__ldg(a.k_len + n), 0), a.Lk) : a.Lk;
+}
+
+// One bias entry in base-2 units: table[b][h] * log2(e), -inf where the bucket
+// lies outside the table (the pair is masked).  A finite entry stays finite:
+// the lowest value of a type times log2(e) would leave fp32's range, and a row
+// of such entries is a uniform softmax, not an empty one.
+template <typename T>
+__device__ __forceinline__ float bias2_of(const T *table, int bucket, int nb, int H, int h) {
+    if ((unsigned)bucket >= (unsigned)nb) return -INFINITY;
+    const float b = IO<T>::ld(table + (int64_t)bucket * H + h);
+    if (isinf(b) || isnan(b)) return b;
+    return fminf(fmaxf(b * kLog2e, -3.4028234e38f), 3.4028234e38f);
+}
+
+}  // namespace gs

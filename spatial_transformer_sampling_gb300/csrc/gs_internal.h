@@ -152,4 +152,69 @@ template <typename TX>
 cudaError_t launch_sample_int(const void *X, const void *grid, int grid_dt, void *Y,
                               const SampleArgs &args, int r, int mode, cudaStream_t s);
 
+// ------------------------------------------------ transformer-block operators
+
+// Device address of the library's error word on the current device.
+unsigned *device_error_word();
+
+// Layer norm over the last axis of `rows` x `D` elements (gs_norm.cu).
+struct NormArgs {
+    int64_t rows;
+    int D;
+    float eps;
+};
+template <typename T>
+cudaError_t launch_layer_norm(const void *X, const void *scale, const void *B, void *Y, float *mean,
+                              float *inv, const NormArgs &args, cudaStream_t s);
+template <typename T>
+cudaError_t launch_layer_norm_backward(const void *dY, const void *X, const void *scale,
+                                       const float *mean, const float *inv, void *dX, void *dScale,
+                                       void *dB, float *partials, const NormArgs &args,
+                                       cudaStream_t s);
+// Row blocks whose column sums the backward pass keeps apart: it needs
+// 2 * blocks * D floats of workspace.
+int layer_norm_partial_blocks(int64_t rows, int64_t D);
+
+// Dropout with an optional residual sum over `n` elements (gs_dropout.cu).
+struct DropoutArgs {
+    int64_t n;
+    uint32_t threshold;      // a word below it drops its element
+    float scale;             // 1 / (1 - ratio)
+    uint64_t seed, offset;
+};
+template <typename T>
+cudaError_t launch_dropout(const void *X, const void *residual, void *Y, const DropoutArgs &args,
+                           cudaStream_t s);
+
+// Attention with a relative position bias (gs_attn*.cu).  Token i of the
+// queries sits at (i / Wq, i % Wq) of its grid, token j of the keys at
+// (j / Wk, j % Wk); the pair's relative index is
+//   rel_q(i) - rel_k(j),  rel_q(i) = yi * P + xi + (Hk-1) * P + Wk-1,
+//   rel_k(j) = yj * P + xj,  P = Wq + Wk - 1,
+// in [0, R), R = (Hq+Hk-1) * P.
+struct AttnArgs {
+    int N, H, D;
+    int Hq, Wq, Hk, Wk, Lq, Lk, P, R;
+    int nb;                             // rows of the bias table (0: no bias)
+    int64_t qs[3], ks[3], vs[3];        // strides of batch, token, head in elements
+    float scale;                        // of the scores
+    const int *buckets;                 // device (R) or nullptr
+    const int *k_len;                   // device (N) or nullptr
+    unsigned *err;
+};
+struct AttnPtrs {                       // device pointers; backward only from dO on
+    const void *Q, *K, *V, *table;
+    void *O;
+    float *lse;
+    const void *dO;
+    void *dQ, *dK, *dV, *dTable;
+};
+// Workspace bytes (a multiple of 256) of the forward and backward calls.
+template <typename T> size_t attn_ws_bytes(const AttnArgs &args, bool backward);
+template <typename T>
+cudaError_t launch_attn(const AttnArgs &args, const AttnPtrs &p, void *ws, cudaStream_t s);
+template <typename T>
+cudaError_t launch_attn_backward(const AttnArgs &args, const AttnPtrs &p, void *ws,
+                                 cudaStream_t s);
+
 }  // namespace gs
