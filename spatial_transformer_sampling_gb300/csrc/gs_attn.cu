@@ -8,6 +8,7 @@
 //   dk_j = scale sum_i ds q_i,  dv_j = sum_i p do_i,
 //   dtable[b][h] = sum of ds over the batch and the pairs of bucket b.
 #include "gs_attn_common.cuh"
+#include "gs_attn_tc_fwd.cuh"
 
 namespace gs {
 namespace {
@@ -229,6 +230,11 @@ size_t attn_ws_bytes(const AttnArgs &a, bool backward) {
 template <typename T>
 cudaError_t launch_attn(const AttnArgs &a, const AttnPtrs &p, void *ws, cudaStream_t s) {
     const float *bias = expand_bias<T>(a, p, ws, s);
+    if constexpr (sizeof(T) == 2) {
+        bool used = false;
+        const cudaError_t e = launch_attn_tc_fwd<T>(a, p, bias, s, &used);
+        if (used || e != cudaSuccess) return e;
+    }
     attn_fwd_kernel<T><<<warp_blocks((int64_t)a.N * a.H * a.Lq), kWarps * 32, 0, s>>>(a, p, bias);
     return cudaGetLastError();
 }

@@ -1,0 +1,235 @@
+// gs_attn_tc.cuh -- tensor-core building blocks of the attention kernels
+// (fp16 / bf16): tiles staged by TMA with the 128-byte swizzle, tcgen05.mma
+// with both operands in shared memory or the first in tensor memory (TMEM),
+// and the TMEM loads and stores the softmax warps use.
+//
+// A tile of R tokens holds DP / 64 chunks of R rows x 128 bytes (64 elements
+// of the head width; what lies beyond D arrives as zeros).  The same bytes
+// serve as a K-major operand (contraction over the head width: scores) and as
+// an MN-major one (contraction over tokens: the weighted sums), so nothing is
+// transposed in memory.
+#pragma once
+
+#include "gs_attn_common.cuh"
+#include "gs_ptx.cuh"
+#include "gs_tma.cuh"
+
+namespace gs {
+
+constexpr int kTcM = 128;            // rows of a score tile: one per softmax thread
+constexpr int kTcN = 64;             // columns of a score tile
+constexpr int kTcThreads = 160;      // four softmax warps and one that issues copies and MMAs
+
+// Shared-memory descriptor of an MN-major operand with the 128-byte swizzle:
+// tokens are rows of 128 bytes, eight of them make a 1024-byte atom; `lbo` is
+// the distance between 64-element chunks along the head width.
+__device__ __forceinline__ uint64_t umma_desc_mnmajor_sw128(uint32_t smem_addr, uint32_t lbo) {
+    uint64_t d = 0;
+    d |= (uint64_t)((smem_addr >> 4) & 0x3FFFu);
+    d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
+    d |= (uint64_t)(1024u >> 4) << 32;                    // next eight tokens
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+
+// umma_idesc_f16 with the second operand MN-major.
+__host__ __device__ constexpr uint32_t umma_idesc_f16_bmn(bool is_bf16, int M, int N) {
+    return umma_idesc_f16(is_bf16, M, N) | (1u << 16);
+}
+
+// D[tmem] (+)= A[tmem] * B[smem]: row r of A is lane r, two 16-bit elements of
+// the contraction per 32-bit column.
+__device__ __forceinline__ void umma_f16_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc,
+                                            uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
+        "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+#define GS_R32(r, o)                                                                              \
+    "=r"(r[o + 0]), "=r"(r[o + 1]), "=r"(r[o + 2]), "=r"(r[o + 3]), "=r"(r[o + 4]), "=r"(r[o + 5]), \
+        "=r"(r[o + 6]), "=r"(r[o + 7]), "=r"(r[o + 8]), "=r"(r[o + 9]), "=r"(r[o + 10]),          \
+        "=r"(r[o + 11]), "=r"(r[o + 12]), "=r"(r[o + 13]), "=r"(r[o + 14]), "=r"(r[o + 15]),      \
+        "=r"(r[o + 16]), "=r"(r[o + 17]), "=r"(r[o + 18]), "=r"(r[o + 19]), "=r"(r[o + 20]),      \
+        "=r"(r[o + 21]), "=r"(r[o + 22]), "=r"(r[o + 23]), "=r"(r[o + 24]), "=r"(r[o + 25]),      \
+        "=r"(r[o + 26]), "=r"(r[o + 27]), "=r"(r[o + 28]), "=r"(r[o + 29]), "=r"(r[o + 30]),      \
+        "=r"(r[o + 31])
+
+// Starts loading 32 consecutive columns of this thread's lane into r[O..O+31];
+// the values may be used after tmem_wait_ld on the same registers.
+template <int O, int N>
+__device__ __forceinline__ void tmem_ld_x32(uint32_t taddr, uint32_t (&r)[N]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+        "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
+        "%28, %29, %30, %31}, [%32];"
+        : GS_R32(r, O)
+        : "r"(taddr)
+        : "memory");
+}
+#undef GS_R32
+
+// Waits for this thread's TMEM loads.  r[O..O+31] pass through, so that no use
+// of them can be moved ahead of the wait.
+template <int O, int N>
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[N]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[O + 0]), "+r"(r[O + 1]), "+r"(r[O + 2]), "+r"(r[O + 3]), "+r"(r[O + 4]),
+                   "+r"(r[O + 5]), "+r"(r[O + 6]), "+r"(r[O + 7]), "+r"(r[O + 8]), "+r"(r[O + 9]),
+                   "+r"(r[O + 10]), "+r"(r[O + 11]), "+r"(r[O + 12]), "+r"(r[O + 13]),
+                   "+r"(r[O + 14]), "+r"(r[O + 15]), "+r"(r[O + 16]), "+r"(r[O + 17]),
+                   "+r"(r[O + 18]), "+r"(r[O + 19]), "+r"(r[O + 20]), "+r"(r[O + 21]),
+                   "+r"(r[O + 22]), "+r"(r[O + 23]), "+r"(r[O + 24]), "+r"(r[O + 25]),
+                   "+r"(r[O + 26]), "+r"(r[O + 27]), "+r"(r[O + 28]), "+r"(r[O + 29]),
+                   "+r"(r[O + 30]), "+r"(r[O + 31])
+                 :
+                 : "memory");
+}
+
+// Starts storing r[0..31] to 32 consecutive columns of this thread's lane.
+__device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+        "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
+        "%28, %29, %30, %31, %32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+        "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+        "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+        "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_wait_st() {
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// Two fp32 values rounded to nearest even and packed, `lo` in the low half.
+template <typename T> __device__ __forceinline__ uint32_t pack2(float lo, float hi);
+template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+template <> __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// A TMA view of one (N, L, H, D) operand: a map and factors that are 0 for a
+// batch or head axis of stride 0 (it is one entry long in the map).
+struct TcView {
+    CUtensorMap map;
+    int by_n, by_h;
+};
+
+// Makes the view of an operand with the given (batch, token, head) strides in
+// elements and boxes of `rows` tokens; false when TMA cannot read it (base or
+// strides not multiples of 16 bytes, a token stride of 0).  The stride of an
+// axis of length 1 does not matter.
+inline bool tc_view(TcView *v, const void *base, bool bf16, int N, int L, int H, int D,
+                    const int64_t (&stride)[3], int rows) {
+    v->by_n = stride[0] == 0 ? 0 : 1;
+    v->by_h = stride[2] == 0 ? 0 : 1;
+    const uint64_t dims[4] = {(uint64_t)D, v->by_h ? (uint64_t)H : 1, (uint64_t)L,
+                              v->by_n ? (uint64_t)N : 1};
+    const int64_t by[3] = {stride[2], stride[1], stride[0]};
+    uint64_t bytes[3];
+    for (int d = 0; d < 3; ++d) {
+        bytes[d] = dims[d + 1] == 1 ? 16 : (uint64_t)by[d] * 2;
+        if (bytes[d] == 0 || bytes[d] >= (uint64_t(1) << 40)) return false;
+    }
+    const uint32_t box[4] = {64, 1, (uint32_t)rows, 1};
+    return tmap_encode(&v->map, 2, bf16, 4, base, dims, bytes, box, true);
+}
+
+// Loads `DP / 64` chunks of ROWS tokens from `row` on; completes on `bar`,
+// which the calling thread arms here.
+template <int DP, int ROWS>
+__device__ __forceinline__ void tc_load(unsigned char *dst, const TcView &v, int n, int h, int row,
+                                        uint64_t *bar) {
+    mbar_arrive_expect_tx(bar, (DP / 64) * ROWS * 128);
+#pragma unroll
+    for (int c = 0; c < DP / 64; ++c)
+        tma_load_4d(dst + c * ROWS * 128, &v.map, c * 64, h * v.by_h, row, n * v.by_n, bar);
+}
+
+// Scores: D[128 x N] (+)= A[128 x D] B[N x D]^T over `steps` steps of 16.
+template <int N>
+__device__ __forceinline__ void tc_scores(uint32_t tmem_d, uint32_t a_smem, uint32_t b_smem,
+                                          uint32_t idesc, int steps) {
+    for (int k = 0; k < steps; ++k) {
+        const uint32_t c = k / 4, o = (k % 4) * 32;
+        umma_f16(tmem_d, umma_desc_kmajor_sw128(a_smem + c * kTcM * 128 + o, 1024),
+                 umma_desc_kmajor_sw128(b_smem + c * N * 128 + o, 1024), idesc, k > 0);
+    }
+}
+
+// Weighted sums: D[128 x width] (+)= A[tmem, 128 x TOKENS] B[TOKENS x width].
+template <int TOKENS>
+__device__ __forceinline__ void tc_weighted(uint32_t tmem_d, uint32_t tmem_a, uint32_t b_smem,
+                                            uint32_t idesc, bool accumulate) {
+#pragma unroll
+    for (int k = 0; k < TOKENS / 16; ++k)
+        umma_f16_ts(tmem_d, tmem_a + k * 8,
+                    umma_desc_mnmajor_sw128(b_smem + k * 2048, TOKENS * 128), idesc,
+                    accumulate || k > 0);
+}
+
+// Clears token rows [from, ROWS) of a tile (a whole warp calls it): masked
+// keys may hold NaN, which a weight of zero would not silence.
+template <int DP, int ROWS>
+__device__ __forceinline__ void tc_clear_rows(unsigned char *tile, int from) {
+    const int lane = threadIdx.x % 32;
+#pragma unroll
+    for (int c = 0; c < DP / 64; ++c)
+        for (int i = from * 8 + lane; i < ROWS * 8; i += 32)
+            *reinterpret_cast<uint4 *>(tile + c * ROWS * 128 + i * 16) = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+    __syncwarp();
+}
+
+// The bias of one row of scores against 64 consecutive columns, of which the
+// first `live` count: f(c, bias) for those, dead(c) for the rest.  Column c sits
+// at `row[-rel(c)]` (SIGN = -1: this thread holds a query, columns are keys) or
+// `row[rel(c)]` (SIGN = +1: a key against queries); rel grows by one per token
+// and by `P - W` more at the end of a grid row.  `x` and `rel` belong to the
+// first column, for which x = token % W.
+template <int SIGN, typename F, typename G>
+__device__ __forceinline__ void for_each_bias(const float *row, int x, int rel, int W, int P,
+                                              int live, F &&f, G &&dead) {
+#pragma unroll
+    for (int c = 0; c < kTcN; c += 8) {
+        if (x + 8 <= W && c + 8 <= live) {   // a run inside one grid row: immediate offsets
+            const float *at = row + SIGN * rel;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) f(c + k, at[SIGN * k]);
+            rel += 8;
+            x += 8;
+            if (x == W) {
+                x = 0;
+                rel += P - W;
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                if (c + k < live)
+                    f(c + k, row[SIGN * rel]);
+                else
+                    dead(c + k);
+                ++rel;
+                if (++x == W) {
+                    x = 0;
+                    rel += P - W;
+                }
+            }
+        }
+    }
+}
+
+}  // namespace gs

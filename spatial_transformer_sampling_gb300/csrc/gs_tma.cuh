@@ -38,13 +38,16 @@ inline TmapEncodeTiledFn tmap_encoder() {
 
 // A tiled map over a dense tensor of `rank` dimensions (dims[0] innermost,
 // elements of `elem_bytes` = 2 or 4 bytes), a box of box[] elements per
-// dimension, no swizzle, zeros outside the tensor.  strides[i] is the byte
+// dimension, no swizzle (or, with `swizzle128`, the 128-byte one: the box is
+// 128 bytes wide and chunk c of row r lands at chunk c ^ (r % 8)), zeros
+// outside the tensor.  strides[i] is the byte
 // distance between consecutive indices of dimension i+1.  Returns false when
 // the encoder is missing or rejects the arguments (the caller then takes
 // another path); it checks the base's 16-byte alignment, the strides'
 // multiples of 16 and each box extent against 256 itself.
 inline bool tmap_encode(CUtensorMap *map, int elem_bytes, bool bf16, int rank, const void *base,
-                        const uint64_t *dims, const uint64_t *strides, const uint32_t *box) {
+                        const uint64_t *dims, const uint64_t *strides, const uint32_t *box,
+                        bool swizzle128 = false) {
     TmapEncodeTiledFn enc = tmap_encoder();
     if (!enc || rank < 1 || rank > 5 || ((uintptr_t)base & 15u)) return false;
     cuuint64_t gd[5], gs[4];
@@ -64,7 +67,8 @@ inline bool tmap_encode(CUtensorMap *map, int elem_bytes, bool bf16, int rank, c
                                    : bf16          ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                                    : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     return enc(map, dt, (cuuint32_t)rank, const_cast<void *>(base), gd, gs, bx, es,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+               CU_TENSOR_MAP_INTERLEAVE_NONE,
+               swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

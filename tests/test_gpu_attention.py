@@ -335,3 +335,25 @@ def test_offsets_beyond_32_bits(gs_cuda):
                           tail], 1)
         o, lse, A = ref.attention(Q, keys, keys, D ** -0.5)
         ref.check(whole, o, A, "bfloat16", "whole")
+
+
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+def test_many_tiles_give_the_same_bits_every_time(gs_cuda, dtype):
+    # thousands of blocks whose warps drift apart over 64 key tiles: a wait that lets one warp
+    # read a sum too early shows as a run that differs
+    g = torch.Generator(device="cuda")
+    g.manual_seed(9)
+    q, k = (16, 64), (64, 64)
+    m, rows = gs_cuda.gs_relative_buckets(q, k, 16, 64)
+    mk = lambda *s: torch.randn(s, generator=g, device="cuda").to(DT[dtype])
+    Q, K, V, table = mk(16, 1024, 8, 64), mk(16, 4096, 8, 64), mk(16, 4096, 8, 64), mk(rows, 8)
+    call = lambda: gs_cuda.gs_attention(Q, K, V, table, m, q, k)
+    O, LSE = call()
+    for _ in range(12):
+        O2, LSE2 = call()
+        assert torch.equal(O, O2) and torch.equal(LSE, LSE2)
+    for n, h in ((0, 0), (15, 7)):   # two heads in full
+        bias, _ = ref.pair_bias(table[:, h:h + 1], m, q, k)
+        o, lse, A = ref.attention(Q[n:n + 1, :, h:h + 1], K[n:n + 1, :, h:h + 1],
+                                  V[n:n + 1, :, h:h + 1], 0.125, bias)
+        ref.check(O[n:n + 1, :, h:h + 1], o, A, dtype, "O")
