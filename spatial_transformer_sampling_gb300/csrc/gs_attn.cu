@@ -8,6 +8,7 @@
 //   dk_j = scale sum_i ds q_i,  dv_j = sum_i p do_i,
 //   dtable[b][h] = sum of ds over the batch and the pairs of bucket b.
 #include "gs_attn_common.cuh"
+#include "gs_attn_tc_bwd.cuh"
 #include "gs_attn_tc_fwd.cuh"
 
 namespace gs {
@@ -219,13 +220,103 @@ const float *expand_bias(const AttnArgs &a, const AttnPtrs &p, void *ws, cudaStr
     return (const float *)ws;
 }
 
+// The tensor-core kernels take 16-bit types and head widths that are multiples
+// of 8 (their 16-byte rows); they also want aligned pointers and strides, which
+// tc_view checks.
+template <typename T> bool tc_takes(const AttnArgs &a) { return sizeof(T) == 2 && a.D % 8 == 0; }
+
+// The workspace's parts, in order; offsets in bytes.
+struct Workspace {
+    size_t bias, rel, lse2, delta, part, end;
+};
+template <typename T> Workspace workspace_of(const AttnArgs &a, bool backward) {
+    Workspace w;
+    const size_t per_rel = a.nb ? round256((size_t)a.H * a.R * sizeof(float)) : 0;
+    w.bias = 0;
+    w.rel = w.bias + per_rel;
+    w.lse2 = w.delta = w.part = w.end = w.rel;
+    if (!backward) return w;
+    w.lse2 = w.rel + per_rel;
+    const bool tc = tc_takes<T>(a);
+    const size_t per_row = tc ? round256((size_t)a.N * a.H * rows64(a.Lq) * sizeof(float)) : 0;
+    w.delta = w.lse2 + per_row;
+    w.part = w.delta + per_row;
+    const bool rel = tc && a.nb && tc_rel_window(a) > 0;
+    w.end = w.part + (rel ? round256((size_t)tc_rel_heads(a) * ((a.Lq + 31) / 32) *
+                                     tc_rel_stride(a) * sizeof(float))
+                          : 0);
+    return w;
+}
+
 }  // namespace
 
 template <typename T>
 size_t attn_ws_bytes(const AttnArgs &a, bool backward) {
-    if (a.nb == 0) return 0;
-    return round256((size_t)a.H * a.R * sizeof(float)) * (backward ? 2 : 1);
+    return workspace_of<T>(a, backward).end;
 }
+
+namespace {
+
+// The tensor-core backward pass; *used reports whether it takes the call, and
+// *rel_done whether rel holds the bias gradient by relative index.
+template <typename T>
+cudaError_t launch_tc_backward(const AttnArgs &a, const AttnPtrs &ptr, const float *bias, char *ws,
+                               cudaStream_t s, bool *used, bool *rel_done) {
+    *used = *rel_done = false;
+    if (!tc_takes<T>(a)) return cudaSuccess;
+    for (const void *p : {(const void *)ptr.O, ptr.dO, (const void *)ptr.dQ, (const void *)ptr.dK,
+                          (const void *)ptr.dV})
+        if ((uintptr_t)p & 15u) return cudaSuccess;
+    constexpr bool bf16 = __is_same(T, __nv_bfloat16);
+    const int64_t dense[3] = {(int64_t)a.Lq * a.H * a.D, (int64_t)a.H * a.D, a.D};
+    TcBwdArgs kv, q;   // keys against queries; queries against keys
+    if (!tc_view(&kv.r1, ptr.K, bf16, a.N, a.Lk, a.H, a.D, a.ks, kTcM) ||
+        !tc_view(&kv.r2, ptr.V, bf16, a.N, a.Lk, a.H, a.D, a.vs, kTcM) ||
+        !tc_view(&kv.c1, ptr.Q, bf16, a.N, a.Lq, a.H, a.D, a.qs, kTcN) ||
+        !tc_view(&kv.c2, ptr.dO, bf16, a.N, a.Lq, a.H, a.D, dense, kTcN) ||
+        !tc_view(&q.r1, ptr.Q, bf16, a.N, a.Lq, a.H, a.D, a.qs, kTcM) ||
+        !tc_view(&q.r2, ptr.dO, bf16, a.N, a.Lq, a.H, a.D, dense, kTcM) ||
+        !tc_view(&q.c1, ptr.K, bf16, a.N, a.Lk, a.H, a.D, a.ks, kTcN) ||
+        !tc_view(&q.c2, ptr.V, bf16, a.N, a.Lk, a.H, a.D, a.vs, kTcN))
+        return cudaSuccess;
+    *used = true;
+    const Workspace w = workspace_of<T>(a, true);
+    float *lse2 = (float *)(ws + w.lse2), *delta = (float *)(ws + w.delta);
+    const int64_t rows = (int64_t)a.N * rows64(a.Lq) * a.H;
+    attn_delta_kernel<T><<<(unsigned)((rows + 15) / 16), 256, 0, s>>>(
+        a, (const T *)ptr.dO, (const T *)ptr.O, ptr.lse, lse2, delta);
+    kv.a = q.a = a;
+    kv.bias = q.bias = bias;
+    kv.lse2 = q.lse2 = lse2;
+    kv.delta = q.delta = delta;
+    kv.out1 = ptr.dK;
+    kv.out2 = ptr.dV;
+    q.out1 = ptr.dQ;
+    q.out2 = nullptr;
+    kv.rel_window = kv.rel_stride = kv.head0 = 0;
+    kv.rel_part = nullptr;
+    const int pairs = a.N * a.H;
+    cudaError_t e = launch_attn_tc_bwd_kernel<T, true>(kv, pairs, s);
+    if (e != cudaSuccess) return e;
+    q.rel_window = bias ? tc_rel_window(a) : 0;
+    q.rel_part = (float *)(ws + w.part);
+    q.rel_stride = q.rel_window ? (int)tc_rel_stride(a) : 0;
+    const int heads = q.rel_window ? (int)tc_rel_heads(a) : pairs;
+    float *rel = (float *)(ws + w.rel);
+    for (int head0 = 0; head0 < pairs; head0 += heads) {
+        const int now = std::min(heads, pairs - head0);
+        q.head0 = head0;
+        e = launch_attn_tc_bwd_kernel<T, false>(q, now, s);
+        if (e != cudaSuccess) return e;
+        if (q.rel_window)
+            attn_rel_sum_kernel<<<dim3((a.R + 127) / 128, a.H), 128, 0, s>>>(
+                a, q.rel_part, q.rel_stride, head0, now, rel);
+    }
+    *rel_done = q.rel_window > 0;
+    return cudaGetLastError();
+}
+
+}  // namespace
 
 template <typename T>
 cudaError_t launch_attn(const AttnArgs &a, const AttnPtrs &p, void *ws, cudaStream_t s) {
@@ -243,11 +334,19 @@ template <typename T>
 cudaError_t launch_attn_backward(const AttnArgs &a, const AttnPtrs &p, void *ws, cudaStream_t s) {
     const float *bias = expand_bias<T>(a, p, ws, s);
     const int threads = kWarps * 32;
-    attn_dq_kernel<T><<<warp_blocks((int64_t)a.N * a.H * a.Lq), threads, 0, s>>>(a, p, bias);
-    attn_dkv_kernel<T><<<warp_blocks((int64_t)a.N * a.H * a.Lk), threads, 0, s>>>(a, p, bias);
+    bool used = false, rel_done = false;
+    if constexpr (sizeof(T) == 2) {
+        const cudaError_t e = launch_tc_backward<T>(a, p, bias, (char *)ws, s, &used, &rel_done);
+        if (e != cudaSuccess) return e;
+    }
+    if (!used) {
+        attn_dq_kernel<T><<<warp_blocks((int64_t)a.N * a.H * a.Lq), threads, 0, s>>>(a, p, bias);
+        attn_dkv_kernel<T><<<warp_blocks((int64_t)a.N * a.H * a.Lk), threads, 0, s>>>(a, p, bias);
+    }
     if (a.nb) {
-        float *rel = (float *)((char *)ws + round256((size_t)a.H * a.R * sizeof(float)));
-        attn_dbias_kernel<T><<<warp_blocks((int64_t)a.H * a.R), threads, 0, s>>>(a, p, bias, rel);
+        float *rel = (float *)((char *)ws + workspace_of<T>(a, true).rel);
+        if (!rel_done)
+            attn_dbias_kernel<T><<<warp_blocks((int64_t)a.H * a.R), threads, 0, s>>>(a, p, bias, rel);
         attn_dtable_kernel<T><<<warp_blocks((int64_t)a.nb * a.H), threads, 0, s>>>(a, rel,
                                                                                   (T *)p.dTable);
     }

@@ -10,6 +10,8 @@
 // transposed in memory.
 #pragma once
 
+#include <algorithm>
+
 #include "gs_attn_common.cuh"
 #include "gs_ptx.cuh"
 #include "gs_tma.cuh"
@@ -148,12 +150,10 @@ inline bool tc_view(TcView *v, const void *base, bool bf16, int N, int L, int H,
     return tmap_encode(&v->map, 2, bf16, 4, base, dims, bytes, box, true);
 }
 
-// Loads `DP / 64` chunks of ROWS tokens from `row` on; completes on `bar`,
-// which the calling thread arms here.
+// Loads `DP / 64` chunks of ROWS tokens from `row` on, counted in bytes on `bar`.
 template <int DP, int ROWS>
 __device__ __forceinline__ void tc_load(unsigned char *dst, const TcView &v, int n, int h, int row,
                                         uint64_t *bar) {
-    mbar_arrive_expect_tx(bar, (DP / 64) * ROWS * 128);
 #pragma unroll
     for (int c = 0; c < DP / 64; ++c)
         tma_load_4d(dst + c * ROWS * 128, &v.map, c * 64, h * v.by_h, row, n * v.by_n, bar);
@@ -231,5 +231,29 @@ __device__ __forceinline__ void for_each_bias(const float *row, int x, int rel, 
         }
     }
 }
+
+// Relative indices between the first and the last of `tokens` consecutive
+// tokens of a grid of `rows` rows of W, at most: one per token and P - W more
+// at each end of a grid row.
+inline int64_t tc_span(int tokens, int L, int rows, int W, int P) {
+    const int64_t t = std::min(tokens, L) - 1;
+    const int64_t crossings = t <= 0 ? 0 : std::min<int64_t>((t - 1) / W + 1, rows - 1);
+    return t + crossings * (P - W);
+}
+
+// Floats of the largest bias window of a CTA: 128 tokens of one grid (queries,
+// or keys with `by_key`) against all of the other.
+inline int64_t tc_bias_window(const AttnArgs &a, bool by_key) {
+    const int64_t q = by_key ? (int64_t)(a.Hq - 1) * a.P + a.Wq - 1
+                             : tc_span(kTcM, a.Lq, a.Hq, a.Wq, a.P);
+    const int64_t k = by_key ? tc_span(kTcM, a.Lk, a.Hk, a.Wk, a.P)
+                             : (int64_t)(a.Hk - 1) * a.P + a.Wk - 1;
+    return std::min<int64_t>(q + k + 1, a.R);
+}
+
+// Dynamic shared memory that lets two CTAs share an SM (227 KB, 1 KB of it
+// kept back per CTA, and the kernels' barriers), and the most for one.
+constexpr int kTcSmemTwo = 227 * 1024 / 2 - 1024 - 256;
+constexpr int kTcSmemOne = 227 * 1024 - 256;
 
 }  // namespace gs

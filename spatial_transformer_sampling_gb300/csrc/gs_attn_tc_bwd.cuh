@@ -1,0 +1,540 @@
+// gs_attn_tc_bwd.cuh -- attention backward on the tensor cores (fp16 / bf16).
+//
+// Two kernels of one shape, so that every gradient is summed by one CTA in one
+// order (no atomics):
+//   DKV: 128 keys per CTA against the queries, 64 at a time;
+//   DQ:  128 queries per CTA against the keys, 64 at a time.
+// With rows R1, R2 (DKV: K, V; DQ: Q, dO) resident and columns C1, C2 (DKV:
+// Q, dO; DQ: K, V) streamed by TMA, each step computes
+//   S  = R1 C1^T,  dP = R2 C2^T             tcgen05.mma, fp32 in TMEM
+//   p  = 2^(c S + bias - lse),  ds = p (dP - delta)   one thread per row
+//   acc1 += ds C1  (dK or dQ),  acc2 += p C2  (dV)    tcgen05.mma
+// p and ds are rounded to the 16-bit type and read back from TMEM, where they
+// overwrite dP; S is free as soon as it is loaded, so the next step's S is
+// computed while the softmax warps work.  The scores are computed in both
+// kernels (7 products instead of 5): the alternative, dQ summed across CTAs,
+// needs fp32 atomics, whose order would change the result.
+//
+// Bias gradient (DQ).  For one column the relative indices of a warp's rows
+// are all different, so each warp adds ds to a private window in shared memory
+// without atomics, four columns at a time in four copies.  Going along the
+// keys the window moves down; indices above it are final and are written once
+// per warp to `rel_part`, which attn_rel_sum_kernel adds up in a fixed order.
+#pragma once
+
+#include "gs_attn_tc.cuh"
+
+namespace gs {
+
+struct TcBwdArgs {
+    AttnArgs a;
+    TcView r1, r2, c1, c2;
+    const float *bias;        // expanded (H, R), or nullptr
+    int bias_window;          // floats of shared memory for the bias (0: read global memory)
+    const float *lse2;        // (N, H, rows64(Lq)): lse * log2(e), +inf where nothing counts
+    const float *delta;       // same shape: dO . O
+    void *out1, *out2;        // dK, dV or dQ
+    int rel_window;           // DQ: floats of a warp's bias-gradient window, a power of two (0: none)
+    float *rel_part;          // DQ: (heads of this launch, query warps, rel_stride)
+    int rel_stride;
+    int head0;                // first (batch, head) pair of this launch
+};
+
+__host__ __device__ inline int rows64(int L) { return (L + 63) / 64 * 64; }
+
+template <int DP, bool DKV> struct TcBwdShape {
+    static constexpr int kStages = 2;
+    static constexpr int kRowBytes = kTcM * DP * 2;
+    static constexpr int kTileBytes = kTcN * DP * 2;
+    static constexpr int kVecBytes = DKV ? 2 * kTcN * 4 : 0;   // lse2, delta of the columns
+    static constexpr int kTileSmem = 2 * kRowBytes + 2 * kStages * kTileBytes;
+    static constexpr int kSmem = kTileSmem + kStages * kVecBytes + 1024;
+    static constexpr int kTmemS = 0, kTmemP = kTcN, kTmemAcc1 = 2 * kTcN, kTmemAcc2 = 2 * kTcN + DP;
+    static constexpr int kTmemCols = DKV && DP == 128 ? 512 : 256;
+    static constexpr int kCtas = kSmem <= 227 * 1024 / 2 - 1024 ? 2 : 1;
+};
+constexpr int kRelCopies = 4;
+
+// Weights are at most 1: fp16 ones are scaled by 2^12 on their way to the
+// tensor cores (and dV back), so that those below 2^-14 keep their precision.
+template <typename T> constexpr float kWeightScale = 1.0f;
+template <> constexpr float kWeightScale<__half> = 4096.0f;
+
+// Shared memory of a bias-gradient window of `w` floats: per warp four copies,
+// the moving window and the columns' relative indices.
+inline __host__ __device__ int rel_smem(int w) {
+    return w ? 4 * ((kRelCopies + 1) * w + kTcN) * 4 : 0;
+}
+
+// Adds one step's ds (fp32, 64 columns of this thread's query) to the warp's
+// bias-gradient window and writes out the indices that are final.
+struct RelWindow {
+    float *copies, *ring;
+    int *rel;
+    int size, rq, rq_min, rq_max, top;
+    bool mine;
+
+    __device__ __forceinline__ void init(const AttnArgs &a, float *smem, int w, int i0) {
+        const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, iw = i0 + warp * 32;
+        size = w;
+        copies = smem + warp * ((kRelCopies + 1) * w + kTcN);
+        ring = copies + kRelCopies * w;
+        rel = reinterpret_cast<int *>(ring + w);
+        for (int k = lane; k < (kRelCopies + 1) * w; k += 32) copies[k] = 0.0f;
+        mine = iw + lane < a.Lq;
+        rq = rel_q(a, min(iw + lane, a.Lq - 1));
+        rq_min = rel_q(a, min(iw, a.Lq - 1));
+        rq_max = rel_q(a, min(iw + 31, a.Lq - 1));
+        top = rq_max;
+        __syncwarp();
+    }
+
+    // keys j0 .. j0 + live - 1 of `keys`; `out` is indexed by relative index
+    __device__ __forceinline__ void add(const AttnArgs &a, const float (&ds)[kTcN], int j0, int live,
+                                        int keys, float *out) {
+        const int lane = threadIdx.x % 32;
+        live = min(live, kTcN);
+#pragma unroll
+        for (int k = 0; k < kTcN; k += 32) rel[k + lane] = rel_k(a, min(j0 + k + lane, keys - 1));
+        __syncwarp();
+        const int lo = rq_min - rel[live - 1];
+        const int span = rq_max - rel[0] - lo + 1;
+        float *at = copies + (rq - lo);
+#pragma unroll
+        for (int s = 0; s < kTcN / kRelCopies; ++s) {
+            float v[kRelCopies];
+            int k[kRelCopies];
+#pragma unroll
+            for (int g = 0; g < kRelCopies; ++g) {
+                const int c = s + g * (kTcN / kRelCopies);
+                k[g] = g * size - rel[c];
+                if (c < live && mine) v[g] = at[k[g]] + ds[c];
+            }
+#pragma unroll
+            for (int g = 0; g < kRelCopies; ++g)
+                if (s + g * (kTcN / kRelCopies) < live && mine) at[k[g]] = v[g];
+            __syncwarp();
+        }
+        // join the copies into the ring, which is indexed by the relative index
+        for (int k = lane; k < span; k += 32) {
+            float v = 0.0f;
+#pragma unroll
+            for (int g = 0; g < kRelCopies; ++g) {
+                v += copies[g * size + k];
+                copies[g * size + k] = 0.0f;
+            }
+            ring[(lo + k) & (size - 1)] += v;
+        }
+        __syncwarp();
+        const int final_above = j0 + live < keys ? rq_max - rel_k(a, j0 + live) : lo - 1;
+        for (int r = final_above + 1 + lane; r <= top; r += 32) {
+            out[r] = ring[r & (size - 1)];
+            ring[r & (size - 1)] = 0.0f;
+        }
+        top = final_above;
+        __syncwarp();
+    }
+};
+
+template <typename T, int DP, bool BIAS, bool DKV>
+__global__ void __launch_bounds__(kTcThreads, TcBwdShape<DP, DKV>::kCtas)
+    attn_tc_bwd_kernel(const __grid_constant__ TcBwdArgs p) {
+    using Sh = TcBwdShape<DP, DKV>;
+    constexpr int NS = Sh::kStages;
+    constexpr bool kBf16 = __is_same(T, __nv_bfloat16);
+    extern __shared__ unsigned char smem_raw[];
+    __shared__ uint64_t r_full, c_full[NS], s_full, s_free, dp_full, pd_ready, done, finished;
+    __shared__ uint32_t tmem_base;
+
+    const AttnArgs &a = p.a;
+    unsigned char *tiles = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+    unsigned char *sR1 = tiles, *sR2 = sR1 + Sh::kRowBytes, *sC1 = sR2 + Sh::kRowBytes,
+                  *sC2 = sC1 + NS * Sh::kTileBytes;
+    float *sVec = reinterpret_cast<float *>(tiles + Sh::kTileSmem);
+    float *sRel = sVec + NS * Sh::kVecBytes / 4;
+    float *sBias = sRel + rel_smem(p.rel_window) / 4;
+
+    const int rows = DKV ? a.Lk : a.Lq;
+    const int row_tiles = (rows + kTcM - 1) / kTcM;
+    const int i0 = (int)(blockIdx.x % row_tiles) * kTcM;
+    const int nh = p.head0 + (int)(blockIdx.x / row_tiles);
+    const int h = nh % a.H, n = nh / a.H;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int keys = keys_of(a, n);
+    const int live_rows = DKV ? keys : a.Lq;    // rows from here on get zeros
+    const int cols = i0 < live_rows ? (DKV ? a.Lq : keys) : 0;
+    const int steps = (cols + kTcN - 1) / kTcN;
+    const float *lse2 = p.lse2 + (int64_t)nh * rows64(a.Lq);
+    const float *delta = p.delta + (int64_t)nh * rows64(a.Lq);
+
+    if (warp == 4) {
+        if (lane == 0) {
+            mbar_init(&r_full, 1);
+            for (int s = 0; s < NS; ++s) mbar_init(&c_full[s], 1);
+            mbar_init(&s_full, 1);
+            mbar_init(&s_free, kTcM);
+            mbar_init(&dp_full, 1);
+            mbar_init(&pd_ready, kTcM);
+            mbar_init(&done, 1);
+            mbar_init(&finished, 1);
+            fence_mbar_init();
+        }
+        __syncwarp();
+        tmem_alloc(&tmem_base, Sh::kTmemCols);
+        tcgen05_fence_before_sync();
+    }
+    // the window of relative indices that this CTA's pairs fall into
+    const float *bias = nullptr;
+    int rel_base = 0;
+    if (BIAS && steps > 0) {
+        bias = p.bias + (int64_t)h * a.R;
+        if (p.bias_window) {
+            const int last = min(i0 + kTcM, live_rows) - 1;
+            rel_base = DKV ? rel_q(a, 0) - rel_k(a, last) : rel_q(a, i0) - rel_k(a, keys - 1);
+            const int end = DKV ? rel_q(a, a.Lq - 1) - rel_k(a, i0) : rel_q(a, last);
+            for (int r = threadIdx.x; r <= end - rel_base; r += kTcThreads)
+                sBias[r] = __ldg(bias + rel_base + r);
+            bias = sBias;
+        }
+    }
+    __syncthreads();
+    tcgen05_fence_after_sync();
+    const uint32_t tmem = tmem_base;
+    bool ok = true;
+
+    if (warp == 4) {
+        // ---------------------------------------------------- copies and MMAs
+        const uint32_t idesc_s = umma_idesc_f16(kBf16, kTcM, kTcN);
+        const int width = (a.D + 15) / 16 * 16;
+        const uint32_t idesc_o = umma_idesc_f16_bmn(kBf16, kTcM, width);
+        const uint32_t r1_at = smem_u32(sR1), r2_at = smem_u32(sR2);
+        const uint32_t c1_at = smem_u32(sC1), c2_at = smem_u32(sC2);
+        const auto load = [&](int t) {   // one lane
+            const int s = t % NS;
+            mbar_arrive_expect_tx(&c_full[s], 2 * Sh::kTileBytes + Sh::kVecBytes);
+            tc_load<DP, kTcN>(sC1 + s * Sh::kTileBytes, p.c1, n, h, t * kTcN, &c_full[s]);
+            tc_load<DP, kTcN>(sC2 + s * Sh::kTileBytes, p.c2, n, h, t * kTcN, &c_full[s]);
+            if (DKV) {
+                bulk_copy_g2s(sVec + s * 2 * kTcN, lse2 + t * kTcN, kTcN * 4, &c_full[s]);
+                bulk_copy_g2s(sVec + s * 2 * kTcN + kTcN, delta + t * kTcN, kTcN * 4, &c_full[s]);
+            }
+        };
+        // tile t is in shared memory, masked keys cleared
+        const auto arrived = [&](int t) {
+            bool good = mbar_wait_bounded(&c_full[t % NS], (t / NS) & 1, a.err);
+            if (__any_sync(0xffffffffu, !good)) return false;
+            if (!DKV && keys - t * kTcN < kTcN) {
+                tc_clear_rows<DP, kTcN>(sC1 + t % NS * Sh::kTileBytes, keys - t * kTcN);
+                tc_clear_rows<DP, kTcN>(sC2 + t % NS * Sh::kTileBytes, keys - t * kTcN);
+            }
+            return true;
+        };
+        int loaded = min(NS, steps);
+        if (steps > 0) {
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&r_full, 2 * Sh::kRowBytes);
+                tc_load<DP, kTcM>(sR1, p.r1, n, h, i0, &r_full);
+                tc_load<DP, kTcM>(sR2, p.r2, n, h, i0, &r_full);
+                for (int t = 0; t < loaded; ++t) load(t);
+            }
+            __syncwarp();
+            ok = mbar_wait_bounded(&r_full, 0, a.err);
+            ok = __all_sync(0xffffffffu, ok) && arrived(0);
+            if (ok && lane == 0) {
+                tc_scores<kTcN>(tmem + Sh::kTmemS, r1_at, c1_at, idesc_s, width / 16);
+                umma_commit(&s_full);
+                tc_scores<kTcN>(tmem + Sh::kTmemP, r2_at, c2_at, idesc_s, width / 16);
+                umma_commit(&dp_full);
+            }
+        }
+        for (int t = 0; t < steps && ok; ++t) {
+            const int s = t % NS, s1 = (t + 1) % NS;
+            if (t + 1 < steps) {   // the next scores, once this step's are loaded
+                ok = arrived(t + 1);
+                if (!ok) break;
+                ok = mbar_wait_bounded(&s_free, t & 1, a.err);
+                if (__any_sync(0xffffffffu, !ok)) break;
+                if (lane == 0) {
+                    tcgen05_fence_after_sync();
+                    tc_scores<kTcN>(tmem + Sh::kTmemS, r1_at, c1_at + s1 * Sh::kTileBytes, idesc_s,
+                                    width / 16);
+                    umma_commit(&s_full);
+                }
+            }
+            ok = mbar_wait_bounded(&pd_ready, t & 1, a.err);
+            if (__any_sync(0xffffffffu, !ok)) break;
+            if (lane == 0) {
+                tcgen05_fence_after_sync();
+                if (DKV)
+                    tc_weighted<kTcN>(tmem + Sh::kTmemAcc2, tmem + Sh::kTmemP,
+                                      c2_at + s * Sh::kTileBytes, idesc_o, t > 0);
+                tc_weighted<kTcN>(tmem + Sh::kTmemAcc1, tmem + Sh::kTmemP + kTcN / 2,
+                                  c1_at + s * Sh::kTileBytes, idesc_o, t > 0);
+                umma_commit(t + 1 < steps ? &done : &finished);
+            }
+            if (t + 1 < steps) {   // p and ds are consumed: dP may be overwritten
+                ok = mbar_wait_bounded(&done, t & 1, a.err);
+                if (__any_sync(0xffffffffu, !ok)) break;
+                if (lane == 0) {
+                    if (loaded < steps) load(loaded);
+                    tc_scores<kTcN>(tmem + Sh::kTmemP, r2_at, c2_at + s1 * Sh::kTileBytes, idesc_s,
+                                    width / 16);
+                    umma_commit(&dp_full);
+                }
+                if (loaded < steps) ++loaded;
+            }
+        }
+        if (!__all_sync(0xffffffffu, ok)) {
+            // a wait gave up: let this CTA's copies and MMAs end before it leaves
+            if (lane == 0) umma_commit(&finished);
+            mbar_wait_bounded(&finished, 0, a.err);
+            for (int t = max(0, loaded - NS); t < loaded; ++t)
+                mbar_wait_bounded(&c_full[t % NS], (t / NS) & 1, a.err);
+        }
+    } else {
+        // ---------------------------------------------------- a row per thread
+        const uint32_t my_tmem = (uint32_t)(warp * 32) << 16;   // this warp's TMEM lanes
+        const int i = i0 + threadIdx.x, ic = min(i, live_rows - 1);
+        const float c2 = a.scale * kLog2e;
+        const float *row = nullptr;
+        if (BIAS && steps > 0) row = DKV ? bias - rel_k(a, ic) - rel_base : bias + rel_q(a, ic) - rel_base;
+        const bool counts = i < live_rows && steps > 0;
+        const float row_lse = !DKV ? (counts ? lse2[i] : INFINITY) : 0.0f;
+        const float row_delta = !DKV && counts ? delta[i] : 0.0f;
+        const bool with_rel = !DKV && BIAS && p.rel_window > 0 && i0 + warp * 32 < a.Lq && steps > 0;
+        RelWindow win;
+        float *rel_out = nullptr;
+        if (!DKV && BIAS) {
+            if (with_rel) {
+                win.init(a, sRel, p.rel_window, i0);
+                // indexed by the relative index: the lowest is rq_min - rel_k(Lk - 1)
+                const int warps = (a.Lq + 31) / 32;
+                rel_out = p.rel_part +
+                          ((int64_t)(nh - p.head0) * warps + i0 / 32 + warp) * p.rel_stride -
+                          (win.rq_min - rel_k(a, a.Lk - 1));
+            }
+        }
+        for (int t = 0; t < steps; ++t) {
+            const int live = cols - t * kTcN;
+            uint32_t r[64], d[64];
+            ok = mbar_wait_bounded(&s_full, t & 1, a.err);
+            if (__any_sync(0xffffffffu, !ok)) break;
+            tcgen05_fence_after_sync();
+            tmem_ld_x32<0>(tmem + Sh::kTmemS + my_tmem, r);
+            tmem_ld_x32<32>(tmem + Sh::kTmemS + my_tmem + 32, r);
+            tmem_wait_ld<0>(r);
+            tmem_wait_ld<32>(r);
+            tcgen05_fence_before_sync();
+            mbar_arrive(&s_free);
+            if (DKV) {   // lse2 and delta of the columns came with the tile
+                ok = mbar_wait_bounded(&c_full[t % NS], (t / NS) & 1, a.err);
+                if (__any_sync(0xffffffffu, !ok)) break;
+            }
+            const float *vec = sVec + t % NS * 2 * kTcN;
+            const auto score = [&](int c, float b) {
+                r[c] = __float_as_uint(fmaf(__uint_as_float(r[c]), c2, b));
+            };
+            const auto dead = [&](int c) { r[c] = __float_as_uint(-INFINITY); };
+            if (BIAS) {
+                const int W = DKV ? a.Wq : a.Wk, y = t * kTcN / W, x = t * kTcN - y * W;
+                if (DKV)
+                    for_each_bias<+1>(row, x, rel_q(a, t * kTcN), W, a.P, live, score, dead);
+                else
+                    for_each_bias<-1>(row, x, y * a.P + x, W, a.P, live, score, dead);
+            } else {
+#pragma unroll
+                for (int c = 0; c < kTcN; ++c)
+                    if (c < live)
+                        score(c, 0.0f);
+                    else
+                        dead(c);
+            }
+            if (DKV) {
+#pragma unroll
+                for (int c = 0; c < kTcN; c += 4) {
+                    const float4 l = *reinterpret_cast<const float4 *>(vec + c);
+                    r[c] = __float_as_uint(exp2_approx(__uint_as_float(r[c]) - l.x));
+                    r[c + 1] = __float_as_uint(exp2_approx(__uint_as_float(r[c + 1]) - l.y));
+                    r[c + 2] = __float_as_uint(exp2_approx(__uint_as_float(r[c + 2]) - l.z));
+                    r[c + 3] = __float_as_uint(exp2_approx(__uint_as_float(r[c + 3]) - l.w));
+                }
+            } else {
+#pragma unroll
+                for (int c = 0; c < kTcN; ++c)
+                    r[c] = __float_as_uint(exp2_approx(__uint_as_float(r[c]) - row_lse));
+            }
+            ok = mbar_wait_bounded(&dp_full, t & 1, a.err);
+            if (__any_sync(0xffffffffu, !ok)) break;
+            tcgen05_fence_after_sync();
+            tmem_ld_x32<0>(tmem + Sh::kTmemP + my_tmem, d);
+            tmem_ld_x32<32>(tmem + Sh::kTmemP + my_tmem + 32, d);
+            tmem_wait_ld<0>(d);
+            tmem_wait_ld<32>(d);
+            float ds[kTcN];
+#pragma unroll
+            for (int c = 0; c < kTcN; c += 4) {
+                float4 e = make_float4(row_delta, row_delta, row_delta, row_delta);
+                if (DKV) e = *reinterpret_cast<const float4 *>(vec + kTcN + c);
+                ds[c] = __uint_as_float(r[c]) * (__uint_as_float(d[c]) - e.x);
+                ds[c + 1] = __uint_as_float(r[c + 1]) * (__uint_as_float(d[c + 1]) - e.y);
+                ds[c + 2] = __uint_as_float(r[c + 2]) * (__uint_as_float(d[c + 2]) - e.z);
+                ds[c + 3] = __uint_as_float(r[c + 3]) * (__uint_as_float(d[c + 3]) - e.w);
+            }
+            uint32_t w[32];
+            if (DKV) {
+                const float2 up = make_float2(kWeightScale<T>, kWeightScale<T>);
+#pragma unroll
+                for (int c = 0; c < 32; ++c) {
+                    const float2 e = mul_f32x2(
+                        make_float2(__uint_as_float(r[2 * c]), __uint_as_float(r[2 * c + 1])), up);
+                    w[c] = pack2<T>(e.x, e.y);
+                }
+                tmem_st_x32(tmem + Sh::kTmemP + my_tmem, w);
+            }
+#pragma unroll
+            for (int c = 0; c < 32; ++c) w[c] = pack2<T>(ds[2 * c], ds[2 * c + 1]);
+            tmem_st_x32(tmem + Sh::kTmemP + my_tmem + kTcN / 2, w);
+            tmem_wait_st();
+            tcgen05_fence_before_sync();
+            mbar_arrive(&pd_ready);
+            if (!DKV && BIAS) {
+                if (with_rel) win.add(a, ds, t * kTcN, live, keys, rel_out);
+            }
+        }
+        if (__all_sync(0xffffffffu, ok) && steps > 0) ok = mbar_wait_bounded(&finished, 0, a.err);
+        if (__all_sync(0xffffffffu, ok)) {
+            tcgen05_fence_after_sync();
+            const int64_t at = (((int64_t)n * rows + i) * a.H + h) * a.D;
+            for (int which = 0; which < (DKV ? 2 : 1); ++which) {
+                T *out = (T *)(which ? p.out2 : p.out1) + at;
+                const float f = counts ? (which ? 1.0f / kWeightScale<T> : a.scale) : 0.0f;
+                const uint32_t acc = tmem + (which ? Sh::kTmemAcc2 : Sh::kTmemAcc1) + my_tmem;
+#pragma unroll 1
+                for (int c = 0; c < a.D; c += 32) {
+                    uint32_t o[32];
+                    if (steps > 0) {
+                        tmem_ld_x32<0>(acc + c, o);
+                        tmem_wait_ld<0>(o);
+                    }
+                    if (i < rows) {
+#pragma unroll
+                        for (int k = 0; k < 32; k += 8)
+                            if (c + k < a.D) {   // D is a multiple of 8
+                                uint4 w = make_uint4(0, 0, 0, 0);
+                                if (counts) {    // other rows may hold anything
+                                    uint32_t *u = &w.x;
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e)
+                                        u[e] = pack2<T>(__uint_as_float(o[k + 2 * e]) * f,
+                                                        __uint_as_float(o[k + 2 * e + 1]) * f);
+                                }
+                                *reinterpret_cast<uint4 *>(out + c + k) = w;
+                            }
+                    }
+                }
+            }
+        }
+    }
+    tcgen05_fence_before_sync();
+    __syncthreads();
+    if (warp == 4) tmem_dealloc(tmem, Sh::kTmemCols);
+}
+
+// lse2 and delta of every query: sixteen threads per row, 16 bytes each.
+template <typename T>
+__global__ void attn_delta_kernel(AttnArgs a, const T *dO, const T *O, const float *lse,
+                                  float *lse2, float *delta) {
+    const int L64 = rows64(a.Lq), part = threadIdx.x % 16;
+    const int64_t row = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / 16;   // (n, i, h)
+    if (row >= (int64_t)a.N * L64 * a.H) return;
+    const int h = (int)(row % a.H), i = (int)(row / a.H % L64), n = (int)(row / a.H / L64);
+    float s = 0.0f;
+    if (i < a.Lq && part * 8 < a.D) {
+        const int64_t at = (((int64_t)n * a.Lq + i) * a.H + h) * a.D + part * 8;
+        const uint4 u = __ldg(reinterpret_cast<const uint4 *>(dO + at));
+        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(O + at));
+        const T *x = reinterpret_cast<const T *>(&u), *y = reinterpret_cast<const T *>(&v);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) s = fmaf(IO<T>::to_f(x[k]), IO<T>::to_f(y[k]), s);
+    }
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (part == 0) {
+        const int64_t nh = (int64_t)n * a.H + h;
+        const float v = i < a.Lq ? lse[nh * a.Lq + i] : -INFINITY;
+        lse2[nh * L64 + i] = v == -INFINITY ? INFINITY : v * kLog2e;   // no key: weights of 0
+        delta[nh * L64 + i] = s;
+    }
+}
+
+// rel[h][r] (+)= the warps' sums, batch items and query warps in order; `heads`
+// (batch, head) pairs from head0 on are in `part`.
+__global__ void attn_rel_sum_kernel(AttnArgs a, const float *part, int stride, int head0, int heads,
+                                    float *rel) {
+    const int r = blockIdx.x * blockDim.x + threadIdx.x, h = blockIdx.y;
+    if (r >= a.R) return;
+    const int warps = (a.Lq + 31) / 32, k_end = rel_k(a, a.Lk - 1);
+    float sum = head0 > 0 ? rel[(int64_t)h * a.R + r] : 0.0f;
+    for (int nh = head0 + (h - head0 % a.H + a.H) % a.H; nh < head0 + heads; nh += a.H) {
+        const int keys = keys_of(a, nh / a.H);
+        if (keys == 0) continue;
+        const int k_last = rel_k(a, keys - 1);
+        for (int w = 0; w < warps; ++w) {
+            const int lo = rel_q(a, w * 32), hi = rel_q(a, min(w * 32 + 31, a.Lq - 1));
+            if (r > hi) continue;
+            if (r < lo - k_last) break;   // and below the windows of the warps that follow
+            sum += __ldg(part + ((int64_t)(nh - head0) * warps + w) * stride + (r - lo + k_end));
+        }
+    }
+    rel[(int64_t)h * a.R + r] = sum;
+}
+
+// Power of two that holds the relative indices of a warp's 32 queries against
+// 64 keys; 0 when that is more than 1024 (rows of hundreds of tokens that end
+// inside a tile): 20 KB of windows per 256 floats.
+inline int tc_rel_window(const AttnArgs &a) {
+    const int64_t span = tc_span(32, a.Lq, a.Hq, a.Wq, a.P) + tc_span(kTcN, a.Lk, a.Hk, a.Wk, a.P) + 1;
+    int w = 128;
+    while (w < span) w *= 2;
+    return w <= 1024 ? w : 0;
+}
+// Floats a query warp writes to rel_part.
+inline int64_t tc_rel_stride(const AttnArgs &a) {
+    return tc_span(32, a.Lq, a.Hq, a.Wq, a.P) + (int64_t)(a.Hk - 1) * a.P + a.Wk;
+}
+// (batch, head) pairs of one DQ launch: all, or as many as keep rel_part within
+// 256 MB (one at least); their sums are added launch by launch.
+inline int64_t tc_rel_heads(const AttnArgs &a) {
+    const int64_t per = (int64_t)((a.Lq + 31) / 32) * tc_rel_stride(a) * 4;
+    return std::max<int64_t>(1, std::min<int64_t>((int64_t)a.N * a.H, (int64_t(256) << 20) / per));
+}
+
+template <typename T, int DP, bool BIAS, bool DKV>
+cudaError_t launch_attn_tc_bwd_as(TcBwdArgs &p, int heads, cudaStream_t s) {
+    using Sh = TcBwdShape<DP, DKV>;
+    auto kernel = attn_tc_bwd_kernel<T, DP, BIAS, DKV>;
+    static DeviceFlags ready;
+    cudaError_t e = once_per_device(ready, [&] {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmemOne);
+    });
+    if (e != cudaSuccess) return e;
+    const int base = Sh::kSmem + rel_smem(p.rel_window);
+    const int64_t window = BIAS ? tc_bias_window(p.a, DKV) : 0;
+    const int limit = base <= kTcSmemTwo ? kTcSmemTwo : kTcSmemOne;
+    p.bias_window = base + window * 4 <= limit ? (int)window : 0;
+    const int rows = DKV ? p.a.Lk : p.a.Lq;
+    const int64_t blocks = (int64_t)((rows + kTcM - 1) / kTcM) * heads;
+    kernel<<<(unsigned)blocks, kTcThreads, base + p.bias_window * 4, s>>>(p);
+    return cudaGetLastError();
+}
+
+template <typename T, bool DKV>
+cudaError_t launch_attn_tc_bwd_kernel(TcBwdArgs &p, int heads, cudaStream_t s) {
+    if (p.a.D <= 64)
+        return p.bias ? launch_attn_tc_bwd_as<T, 64, true, DKV>(p, heads, s)
+                      : launch_attn_tc_bwd_as<T, 64, false, DKV>(p, heads, s);
+    return p.bias ? launch_attn_tc_bwd_as<T, 128, true, DKV>(p, heads, s)
+                  : launch_attn_tc_bwd_as<T, 128, false, DKV>(p, heads, s);
+}
+
+}  // namespace gs

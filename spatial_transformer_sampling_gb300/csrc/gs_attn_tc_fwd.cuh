@@ -19,8 +19,6 @@
 // when it fits beside the tiles of two CTAs per SM, else read through L1.
 #pragma once
 
-#include <algorithm>
-
 #include "gs_attn_tc.cuh"
 
 namespace gs {
@@ -34,7 +32,12 @@ struct TcFwdArgs {
     float *lse;
 };
 
-constexpr float kLazyGrowth = 8.0f;   // log2 of how far weights may exceed 1
+constexpr float kLazyGrowth = 8.0f;   // log2 of how far the maximum may outgrow the reference
+
+// log2 of the weight at the reference: fp16 weights are kept 2^6 up, so that
+// small ones stay clear of the type's subnormal range (2^14 at most).
+template <typename T> constexpr float kWeightShift = 0.0f;
+template <> constexpr float kWeightShift<__half> = 6.0f;
 
 template <int DP> struct TcFwdShape {
     static constexpr int kStages = DP == 64 ? 3 : 2;
@@ -110,15 +113,18 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         const int width = (a.D + 15) / 16 * 16;
         const uint32_t idesc_o = umma_idesc_f16_bmn(kBf16, kTcM, width);
         const uint32_t q_at = smem_u32(sQ), k_at = smem_u32(sK), v_at = smem_u32(sV);
+        const auto load = [&](int t) {   // one lane
+            const int s = t % NS;
+            mbar_arrive_expect_tx(&k_full[s], Sh::kTileBytes);
+            tc_load<DP, kTcN>(sK + s * Sh::kTileBytes, p.k, n, h, t * kTcN, &k_full[s]);
+            mbar_arrive_expect_tx(&v_full[s], Sh::kTileBytes);
+            tc_load<DP, kTcN>(sV + s * Sh::kTileBytes, p.v, n, h, t * kTcN, &v_full[s]);
+        };
         int loaded = 0;   // tiles whose copies were issued
         if (lane == 0 && T_tiles > 0) {
+            mbar_arrive_expect_tx(&q_full, Sh::kQBytes);
             tc_load<DP, kTcM>(sQ, p.q, n, h, i0, &q_full);
-            for (; loaded < NS && loaded < T_tiles; ++loaded) {
-                tc_load<DP, kTcN>(sK + loaded * Sh::kTileBytes, p.k, n, h, loaded * kTcN,
-                                  &k_full[loaded]);
-                tc_load<DP, kTcN>(sV + loaded * Sh::kTileBytes, p.v, n, h, loaded * kTcN,
-                                  &v_full[loaded]);
-            }
+            for (; loaded < NS && loaded < T_tiles; ++loaded) load(loaded);
         }
         loaded = __shfl_sync(0xffffffffu, loaded, 0);
         if (T_tiles > 0) {
@@ -135,13 +141,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                 ok = mbar_wait_bounded(&pv_done, (j - 1) & 1, a.err);
                 if (__any_sync(0xffffffffu, !ok)) break;
                 if (loaded < T_tiles) {
-                    if (lane == 0) {
-                        const int t = (j - 1) % NS;
-                        tc_load<DP, kTcN>(sK + t * Sh::kTileBytes, p.k, n, h, loaded * kTcN,
-                                          &k_full[t]);
-                        tc_load<DP, kTcN>(sV + t * Sh::kTileBytes, p.v, n, h, loaded * kTcN,
-                                          &v_full[t]);
-                    }
+                    if (lane == 0) load(loaded);
                     ++loaded;
                 }
             }
@@ -235,7 +235,8 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                 l *= keep;
                 m = top;
             }
-            const float ref = m == -INFINITY ? 0.0f : m;   // a row with no key yet: weights 0
+            // a row with no key yet: weights 0
+            const float ref = m == -INFINITY ? 0.0f : m - kWeightShift<T>;
             float2 sum[4] = {};
             const float2 one = make_float2(1.0f, 1.0f), shift = make_float2(-ref, -ref);
             uint32_t w[32];
@@ -292,27 +293,13 @@ __global__ void __launch_bounds__(kTcThreads, 2)
             }
             if (i < a.Lq && p.lse)
                 p.lse[((int64_t)n * a.H + h) * a.Lq + i] =
-                    l != 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
+                    l != 0.0f ? (m - kWeightShift<T> + log2f(l)) * kLn2 : -INFINITY;
         }
     }
     tcgen05_fence_before_sync();
     __syncthreads();
     if (warp == 4) tmem_dealloc(tmem, Sh::kTmemCols);
 }
-
-// Floats of the largest bias window of a CTA: its queries span at most 127
-// tokens and the grid rows between them, its keys all of the key grid.
-inline int64_t tc_bias_window(const AttnArgs &a) {
-    const int64_t crossings = a.Hq == 1 ? 0 : std::min<int64_t>((kTcM - 2) / a.Wq + 1, a.Hq - 1);
-    const int64_t tokens = std::min<int64_t>(kTcM, a.Lq) - 1;
-    const int64_t q_span = tokens + crossings * (a.P - a.Wq);
-    const int64_t k_span = (int64_t)(a.Hk - 1) * a.P + a.Wk - 1;
-    return std::min<int64_t>(q_span + k_span + 1, a.R);
-}
-
-// Dynamic shared memory that lets two CTAs share an SM (227 KB, 1 KB of it
-// kept back per CTA, and this kernel's barriers).
-constexpr int kTcTwoPerSm = 227 * 1024 / 2 - 1024 - 256;
 
 template <typename T, int DP, bool BIAS>
 cudaError_t launch_attn_tc_fwd_as(TcFwdArgs &p, cudaStream_t s) {
@@ -321,11 +308,11 @@ cudaError_t launch_attn_tc_fwd_as(TcFwdArgs &p, cudaStream_t s) {
     static DeviceFlags ready;
     cudaError_t e = once_per_device(ready, [&] {
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    kTcTwoPerSm);
+                                    kTcSmemTwo);
     });
     if (e != cudaSuccess) return e;
-    const int64_t window = BIAS ? tc_bias_window(p.a) : 0;
-    p.bias_window = Sh::kSmem + window * 4 <= kTcTwoPerSm ? (int)window : 0;
+    const int64_t window = BIAS ? tc_bias_window(p.a, false) : 0;
+    p.bias_window = Sh::kSmem + window * 4 <= kTcSmemTwo ? (int)window : 0;
     const int64_t blocks = (int64_t)((p.a.Lq + kTcM - 1) / kTcM) * p.a.H * p.a.N;
     kernel<<<(unsigned)blocks, kTcThreads, Sh::kSmem + p.bias_window * 4, s>>>(p);
     return cudaGetLastError();

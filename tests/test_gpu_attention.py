@@ -357,3 +357,56 @@ def test_many_tiles_give_the_same_bits_every_time(gs_cuda, dtype):
         o, lse, A = ref.attention(Q[n:n + 1, :, h:h + 1], K[n:n + 1, :, h:h + 1],
                                   V[n:n + 1, :, h:h + 1], 0.125, bias)
         ref.check(O[n:n + 1, :, h:h + 1], o, A, dtype, "O")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("q,k", [((3, 400), (3, 400)), ((2, 700), (3, 700)), ((300, 2), (150, 4))])
+def test_grids_whose_rows_end_inside_tiles(gs_cuda, q, k, dtype):
+    # the relative indices of one tile then lie far apart
+    Problem(gs_cuda, 330, dtype, 1, 1, 32, q, k, 16).both()
+
+
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+def test_gradient_of_many_tiles_gives_the_same_bits_every_time(gs_cuda, dtype):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(10)
+    q = k = (32, 64)
+    m, rows = gs_cuda.gs_relative_buckets(q, k, 16, 64)
+    mk = lambda *s: torch.randn(s, generator=g, device="cuda").to(DT[dtype])
+    Q, K, V, dO = (mk(8, 2048, 8, 64) for _ in range(4))
+    table = mk(rows, 8)
+    k_len = torch.tensor([2048, 2000, 1, 64, 1024, 2047, 700, 65], dtype=torch.int32, device="cuda")
+    args = (table, m, q, k, k_len)
+    O, LSE = gs_cuda.gs_attention(Q, K, V, *args)
+    call = lambda: gs_cuda.gs_attention_backward(dO, Q, K, V, O, LSE, *args)
+    first = call()
+    for _ in range(8):
+        for a, b in zip(first, call()):
+            assert torch.equal(a, b)
+    for n, h in ((1, 0), (7, 5)):    # two heads in full; the table's gradient takes all of them
+        one = lambda t: t[n:n + 1, :, h:h + 1]
+        bias, which = ref.pair_bias(table[:, h:h + 1], m, q, k)
+        grads, sums = ref.attention_backward(one(dO), one(Q), one(K), one(V), one(O),
+                                             LSE[n:n + 1, h:h + 1], 0.125, bias, k_len[n:n + 1])
+        for name, a, r, A in zip(("dQ", "dK", "dV"), first, grads, sums):
+            ref.check(one(a), r, A, dtype, name)
+
+
+def test_bias_gradient_summed_over_several_launches(gs_cuda):
+    # 68 heads of 64 x 64 tokens: more partial sums than one launch keeps
+    g = torch.Generator(device="cuda")
+    g.manual_seed(12)
+    N, H, q = 4, 17, (64, 64)
+    m, rows = gs_cuda.gs_relative_buckets(q, q, 16, 64)
+    mk = lambda *s: torch.randn(s, generator=g, device="cuda").half()
+    Q, K, V, dO = (mk(N, 4096, H, 16) for _ in range(4))
+    table = mk(rows, H)
+    O, LSE = gs_cuda.gs_attention(Q, K, V, table, m, q, q)
+    dT = gs_cuda.gs_attention_backward(dO, Q, K, V, O, LSE, table, m, q, q)[3].double()
+    parts = [gs_cuda.gs_attention_backward(dO[n:n + 1], Q[n:n + 1], K[n:n + 1], V[n:n + 1],
+                                           O[n:n + 1], LSE[n:n + 1], table, m, q, q)[3].double()
+             for n in range(N)]
+    # each side rounds to fp16: half an ulp of every part and of the whole; fp32 sums of 2^24
+    # pairs beside it, far below the smallest of those
+    lim = ref.U["float16"] / 2 * (dT.abs() + sum(p.abs() for p in parts)) * 1.1 + 1e-2
+    assert ((dT - sum(parts)).abs() <= lim).all()
