@@ -486,7 +486,7 @@ gs_status gs_dropout(const void *X, const void *residual, int64_t n, gs_dtype dt
  * Shapes of gs_attention.  Queries lie on a grid of q_extent = (Hq, Wq) tokens
  * and keys on one of k_extent = (Hk, Wk), both row-major, Lq = Hq * Wq and
  * Lk = Hk * Wk; a plain sequence is (1, L).
- *   N, H, D     batch, heads, head width (1 to 128).
+ *   N, H, D     batch, heads (at most 65535), head width (1 to 128).
  *   *_strides   strides of Q, K and V in elements for (batch, token, head);
  *               the D elements of a head are contiguous.  This covers
  *               (N, L, H, D) and (N, H, L, D) tensors, a packed

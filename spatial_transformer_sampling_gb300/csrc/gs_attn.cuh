@@ -1,0 +1,231 @@
+// gs_attn.cuh -- attention with a learned bias by relative position: which
+// kernel takes a call, and the steps around them.
+//
+//   s[n,h,i,j] = scale * q[n,i,h] . k[n,j,h] + table[bucket(i, j)][h]
+//   p = softmax over j,  o = sum_j p v,  lse = log sum_j exp(s)
+// Backward, with delta_i = do_i . o_i:
+//   ds = p * (do_i . v_j - delta_i),  dq_i = scale sum_j ds k_j,
+//   dk_j = scale sum_i ds q_i,  dv_j = sum_i p do_i,
+//   dtable[b][h] = sum of ds over the batch and the pairs of bucket b.
+//
+// Forward: up to kFewQueries queries run on attn_few_kernel, which reads K and
+// V once and splits the keys over a cluster.  Otherwise 16-bit types whose rows
+// TMA can read run on the tensor cores, the rest on fp32 FMAs.  The bias is
+// expanded once per call to (H, R) in base-2 units, R relative indices, so that
+// the kernels look up one float per pair.
+#pragma once
+
+#include "gs_attn_common.cuh"
+#include "gs_attn_few.cuh"
+#include "gs_attn_simt.cuh"
+#include "gs_attn_tc_bwd.cuh"
+#include "gs_attn_tc_fwd.cuh"
+
+namespace gs {
+namespace {
+
+// bias[h][r] for every relative index, in base-2 units.
+template <typename T>
+__global__ void attn_bias_kernel(const T *table, AttnArgs a, float *bias) {
+    const int r = blockIdx.x * blockDim.x + threadIdx.x;
+    if (r >= a.R) return;
+    const int b = __ldg(a.buckets + r);
+    for (int h = blockIdx.y; h < a.H; h += gridDim.y)
+        bias[(int64_t)h * a.R + r] = bias2_of(table, b, a.nb, a.H, h);
+}
+
+// Sum of ds over the batch and the pairs of one relative index, one warp per
+// index: for the grids whose indices do not fit the query kernels' windows.
+template <typename T>
+__global__ void attn_dbias_kernel(AttnArgs a, AttnPtrs p, const float *bias, const float *lse2,
+                                  const float *delta, float *rel) {
+    const int64_t w = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / 32;
+    const int lane = threadIdx.x % 32;
+    if (w >= (int64_t)a.H * a.R) return;
+    const int r = (int)(w % a.R), h = (int)(w / a.R);
+    const int dy = r / a.P - (a.Hk - 1), dx = r % a.P - (a.Wk - 1);
+    const float b = __ldg(bias + w);
+    float sum = 0.0f;
+    for (int n = 0; n < a.N && b != -INFINITY; ++n) {
+        const int keys = keys_of(a, n);
+        const T *q = (const T *)p.Q + n * a.qs[0] + h * a.qs[2];
+        const T *k = (const T *)p.K + n * a.ks[0] + h * a.ks[2];
+        const T *v = (const T *)p.V + n * a.vs[0] + h * a.vs[2];
+        const T *g = (const T *)p.dO + ((int64_t)n * a.Lq * a.H + h) * a.D;
+        const int64_t row0 = ((int64_t)n * a.H + h) * rows64(a.Lq);
+        for (int y = max(0, dy); y < min(a.Hq, a.Hk + dy); ++y)
+            for (int x = max(0, dx); x < min(a.Wq, a.Wk + dx); ++x) {
+                const int i = y * a.Wq + x, j = (y - dy) * a.Wk + x - dx;
+                if (j >= keys) continue;
+                float s = 0.0f, dp = 0.0f;
+                for (int d = lane; d < a.D; d += 32) {
+                    s = fmaf(IO<T>::ld(q + i * a.qs[1] + d), IO<T>::ld(k + j * a.ks[1] + d), s);
+                    dp = fmaf(IO<T>::ld(g + (int64_t)i * a.H * a.D + d),
+                              IO<T>::ld(v + j * a.vs[1] + d), dp);
+                }
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) {
+                    s += __shfl_xor_sync(0xffffffffu, s, o);
+                    dp += __shfl_xor_sync(0xffffffffu, dp, o);
+                }
+                sum += exp2_approx(fmaf(s, a.scale * kLog2e, b) - lse2[row0 + i]) *
+                       (dp - delta[row0 + i]);
+            }
+    }
+    if (lane == 0) rel[w] = sum;
+}
+
+// dtable[b][h]: a lane per bucket goes through the relative indices in order,
+// eight warps an eighth each.
+template <typename T>
+__global__ void __launch_bounds__(256) attn_dtable_kernel(AttnArgs a, const float *rel, T *dTable) {
+    __shared__ float s_sum[8][32];
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, h = blockIdx.y;
+    const int b = blockIdx.x * 32 + lane;
+    const int each = (a.R + 7) / 8, lo = warp * each, hi = min(lo + each, a.R);
+    float sum = 0.0f;
+#pragma unroll 8
+    for (int r = lo; r < hi; ++r)
+        if (__ldg(a.buckets + r) == b) sum += rel[(int64_t)h * a.R + r];
+    s_sum[warp][lane] = sum;
+    __syncthreads();
+    if (warp == 0 && b < a.nb) {
+        for (int w = 1; w < 8; ++w) sum += s_sum[w][lane];
+        dTable[(int64_t)b * a.H + h] = IO<T>::st(sum);
+    }
+}
+
+size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+
+// The workspace's parts, in order; offsets in bytes.
+struct Workspace {
+    size_t bias, rel, lse2, delta, part, end;
+};
+Workspace workspace_of(const AttnArgs &a, bool backward) {
+    Workspace w = {};
+    if (!backward && few_takes(a)) return w;
+    const size_t per_rel = a.nb ? round256((size_t)a.H * a.R * sizeof(float)) : 0;
+    w.rel = w.end = w.bias + per_rel;
+    if (!backward) return w;
+    const size_t per_row = round256((size_t)a.N * a.H * rows64(a.Lq) * sizeof(float));
+    w.lse2 = w.rel + per_rel;
+    w.delta = w.lse2 + per_row;
+    w.part = w.end = w.delta + per_row;
+    if (a.nb && rel_window_of(a) > 0)
+        w.end += round256((size_t)rel_heads_of(a) * ((a.Lq + 31) / 32) * rel_stride_of(a) *
+                          sizeof(float));
+    return w;
+}
+
+template <typename T>
+const float *expand_bias(const AttnArgs &a, const AttnPtrs &p, char *ws, cudaStream_t s) {
+    if (a.nb == 0) return nullptr;
+    float *bias = (float *)(ws + workspace_of(a, false).bias);
+    attn_bias_kernel<T><<<dim3((a.R + 255) / 256, a.H < 65535 ? a.H : 65535), 256, 0, s>>>(
+        (const T *)p.table, a, bias);
+    return bias;
+}
+
+// Tensor-core views of the backward pass (16-bit types); false when its kernels
+// do not take the call (rows that are not multiples of 16 bytes).
+template <typename T>
+bool tc_backward_views(const AttnArgs &a, const AttnPtrs &ptr, TcBwdArgs &kv, TcBwdArgs &q) {
+    if (a.D % 8 != 0) return false;
+    for (const void *p : {(const void *)ptr.O, ptr.dO, (const void *)ptr.dQ, (const void *)ptr.dK,
+                          (const void *)ptr.dV})
+        if ((uintptr_t)p & 15u) return false;
+    constexpr bool bf16 = __is_same(T, __nv_bfloat16);
+    const int64_t dense[3] = {(int64_t)a.Lq * a.H * a.D, (int64_t)a.H * a.D, a.D};
+    return tc_view(&kv.r1, ptr.K, bf16, a.N, a.Lk, a.H, a.D, a.ks, kTcM) &&
+           tc_view(&kv.r2, ptr.V, bf16, a.N, a.Lk, a.H, a.D, a.vs, kTcM) &&
+           tc_view(&kv.c1, ptr.Q, bf16, a.N, a.Lq, a.H, a.D, a.qs, kTcN) &&
+           tc_view(&kv.c2, ptr.dO, bf16, a.N, a.Lq, a.H, a.D, dense, kTcN) &&
+           tc_view(&q.r1, ptr.Q, bf16, a.N, a.Lq, a.H, a.D, a.qs, kTcM) &&
+           tc_view(&q.r2, ptr.dO, bf16, a.N, a.Lq, a.H, a.D, dense, kTcM) &&
+           tc_view(&q.c1, ptr.K, bf16, a.N, a.Lk, a.H, a.D, a.ks, kTcN) &&
+           tc_view(&q.c2, ptr.V, bf16, a.N, a.Lk, a.H, a.D, a.vs, kTcN);
+}
+
+}  // namespace
+
+template <typename T>
+size_t attn_ws_bytes(const AttnArgs &a, bool backward) {
+    return workspace_of(a, backward).end;
+}
+
+template <typename T>
+cudaError_t launch_attn(const AttnArgs &a, const AttnPtrs &p, void *ws, cudaStream_t s) {
+    if (few_takes(a)) return launch_attn_few<T>(a, p, s);
+    const float *bias = expand_bias<T>(a, p, (char *)ws, s);
+    if constexpr (sizeof(T) == 2) {
+        bool used = false;
+        const cudaError_t e = launch_attn_tc_fwd<T>(a, p, bias, s, &used);
+        if (used || e != cudaSuccess) return e;
+    }
+    return launch_attn_simt_fwd<T>(a, p, bias, s);
+}
+
+template <typename T>
+cudaError_t launch_attn_backward(const AttnArgs &a, const AttnPtrs &p, void *ws_, cudaStream_t s) {
+    char *ws = (char *)ws_;
+    const Workspace w = workspace_of(a, true);
+    const float *bias = expand_bias<T>(a, p, ws, s);
+    float *rel = (float *)(ws + w.rel), *lse2 = (float *)(ws + w.lse2);
+    float *delta = (float *)(ws + w.delta);
+    TcBwdArgs kv, q;
+    bool tc = false;
+    if constexpr (sizeof(T) == 2) tc = tc_backward_views<T>(a, p, kv, q);
+    const int64_t rows = (int64_t)a.N * rows64(a.Lq) * a.H;
+    auto delta_kernel = tc ? attn_delta_kernel<T, sizeof(T) == 2> : attn_delta_kernel<T, false>;
+    delta_kernel<<<(unsigned)((rows + 15) / 16), 256, 0, s>>>(a, (const T *)p.dO, (const T *)p.O, p.lse,
+                                                              lse2, delta);
+    const int pairs = a.N * a.H;
+    RelArgs none = {}, part = {};
+    cudaError_t e;
+    if constexpr (sizeof(T) == 2) {
+        if (tc) {
+            kv.a = q.a = a;
+            kv.bias = q.bias = bias;
+            kv.lse2 = q.lse2 = lse2;
+            kv.delta = q.delta = delta;
+            kv.out1 = p.dK;
+            kv.out2 = p.dV;
+            q.out1 = p.dQ;
+            q.out2 = nullptr;
+            kv.rel = none;
+        }
+    }
+    const auto run = [&](auto dkv, const RelArgs &r, int heads) {
+        constexpr bool DKV = decltype(dkv)::value;
+        if constexpr (sizeof(T) == 2) {
+            if (tc) {
+                TcBwdArgs &args = DKV ? kv : q;
+                args.rel = r;
+                return launch_attn_tc_bwd_kernel<T, DKV>(args, heads, s);
+            }
+        }
+        return launch_attn_simt_bwd<T, DKV>(a, p, bias, lse2, delta, r, heads, s);
+    };
+    e = run(std::true_type(), none, pairs);
+    if (e != cudaSuccess) return e;
+    part.window = bias ? rel_window_of(a) : 0;
+    part.stride = part.window ? (int)rel_stride_of(a) : 0;
+    part.part = (float *)(ws + w.part);
+    const int heads = part.window ? (int)rel_heads_of(a) : pairs;
+    for (part.head0 = 0; part.head0 < pairs; part.head0 += heads) {
+        const int now = std::min(heads, pairs - part.head0);
+        e = run(std::false_type(), part, now);
+        if (e != cudaSuccess) return e;
+        if (part.window)
+            attn_rel_sum_kernel<<<dim3((a.R + 127) / 128, a.H), 128, 0, s>>>(a, part, now, rel);
+    }
+    if (bias) {
+        if (!part.window)
+            attn_dbias_kernel<T><<<(unsigned)(((int64_t)a.H * a.R + 7) / 8), 256, 0, s>>>(
+                a, p, bias, lse2, delta, rel);
+        attn_dtable_kernel<T><<<dim3((a.nb + 31) / 32, a.H), 256, 0, s>>>(a, rel, (T *)p.dTable);
+    }
+    return cudaGetLastError();
+}
+
+}  // namespace gs

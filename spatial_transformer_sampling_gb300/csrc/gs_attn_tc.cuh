@@ -10,9 +10,7 @@
 // transposed in memory.
 #pragma once
 
-#include <algorithm>
-
-#include "gs_attn_common.cuh"
+#include "gs_attn_rel.cuh"
 #include "gs_ptx.cuh"
 #include "gs_tma.cuh"
 
@@ -232,21 +230,12 @@ __device__ __forceinline__ void for_each_bias(const float *row, int x, int rel, 
     }
 }
 
-// Relative indices between the first and the last of `tokens` consecutive
-// tokens of a grid of `rows` rows of W, at most: one per token and P - W more
-// at each end of a grid row.
-inline int64_t tc_span(int tokens, int L, int rows, int W, int P) {
-    const int64_t t = std::min(tokens, L) - 1;
-    const int64_t crossings = t <= 0 ? 0 : std::min<int64_t>((t - 1) / W + 1, rows - 1);
-    return t + crossings * (P - W);
-}
-
 // Floats of the largest bias window of a CTA: 128 tokens of one grid (queries,
 // or keys with `by_key`) against all of the other.
 inline int64_t tc_bias_window(const AttnArgs &a, bool by_key) {
     const int64_t q = by_key ? (int64_t)(a.Hq - 1) * a.P + a.Wq - 1
-                             : tc_span(kTcM, a.Lq, a.Hq, a.Wq, a.P);
-    const int64_t k = by_key ? tc_span(kTcM, a.Lk, a.Hk, a.Wk, a.P)
+                             : rel_span(kTcM, a.Lq, a.Hq, a.Wq, a.P);
+    const int64_t k = by_key ? rel_span(kTcM, a.Lk, a.Hk, a.Wk, a.P)
                              : (int64_t)(a.Hk - 1) * a.P + a.Wk - 1;
     return std::min<int64_t>(q + k + 1, a.R);
 }

@@ -14,14 +14,9 @@
 // computed while the softmax warps work.  The scores are computed in both
 // kernels (7 products instead of 5): the alternative, dQ summed across CTAs,
 // needs fp32 atomics, whose order would change the result.
-//
-// Bias gradient (DQ).  For one column the relative indices of a warp's rows
-// are all different, so each warp adds ds to a private window in shared memory
-// without atomics, four columns at a time in four copies.  Going along the
-// keys the window moves down; indices above it are final and are written once
-// per warp to `rel_part`, which attn_rel_sum_kernel adds up in a fixed order.
 #pragma once
 
+#include "gs_attn_rel.cuh"
 #include "gs_attn_tc.cuh"
 
 namespace gs {
@@ -34,13 +29,8 @@ struct TcBwdArgs {
     const float *lse2;        // (N, H, rows64(Lq)): lse * log2(e), +inf where nothing counts
     const float *delta;       // same shape: dO . O
     void *out1, *out2;        // dK, dV or dQ
-    int rel_window;           // DQ: floats of a warp's bias-gradient window, a power of two (0: none)
-    float *rel_part;          // DQ: (heads of this launch, query warps, rel_stride)
-    int rel_stride;
-    int head0;                // first (batch, head) pair of this launch
+    RelArgs rel;              // DQ: the bias gradient
 };
-
-__host__ __device__ inline int rows64(int L) { return (L + 63) / 64 * 64; }
 
 template <int DP, bool DKV> struct TcBwdShape {
     static constexpr int kStages = 2;
@@ -53,88 +43,11 @@ template <int DP, bool DKV> struct TcBwdShape {
     static constexpr int kTmemCols = DKV && DP == 128 ? 512 : 256;
     static constexpr int kCtas = kSmem <= 227 * 1024 / 2 - 1024 ? 2 : 1;
 };
-constexpr int kRelCopies = 4;
 
 // Weights are at most 1: fp16 ones are scaled by 2^12 on their way to the
 // tensor cores (and dV back), so that those below 2^-14 keep their precision.
 template <typename T> constexpr float kWeightScale = 1.0f;
 template <> constexpr float kWeightScale<__half> = 4096.0f;
-
-// Shared memory of a bias-gradient window of `w` floats: per warp four copies,
-// the moving window and the columns' relative indices.
-inline __host__ __device__ int rel_smem(int w) {
-    return w ? 4 * ((kRelCopies + 1) * w + kTcN) * 4 : 0;
-}
-
-// Adds one step's ds (fp32, 64 columns of this thread's query) to the warp's
-// bias-gradient window and writes out the indices that are final.
-struct RelWindow {
-    float *copies, *ring;
-    int *rel;
-    int size, rq, rq_min, rq_max, top;
-    bool mine;
-
-    __device__ __forceinline__ void init(const AttnArgs &a, float *smem, int w, int i0) {
-        const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, iw = i0 + warp * 32;
-        size = w;
-        copies = smem + warp * ((kRelCopies + 1) * w + kTcN);
-        ring = copies + kRelCopies * w;
-        rel = reinterpret_cast<int *>(ring + w);
-        for (int k = lane; k < (kRelCopies + 1) * w; k += 32) copies[k] = 0.0f;
-        mine = iw + lane < a.Lq;
-        rq = rel_q(a, min(iw + lane, a.Lq - 1));
-        rq_min = rel_q(a, min(iw, a.Lq - 1));
-        rq_max = rel_q(a, min(iw + 31, a.Lq - 1));
-        top = rq_max;
-        __syncwarp();
-    }
-
-    // keys j0 .. j0 + live - 1 of `keys`; `out` is indexed by relative index
-    __device__ __forceinline__ void add(const AttnArgs &a, const float (&ds)[kTcN], int j0, int live,
-                                        int keys, float *out) {
-        const int lane = threadIdx.x % 32;
-        live = min(live, kTcN);
-#pragma unroll
-        for (int k = 0; k < kTcN; k += 32) rel[k + lane] = rel_k(a, min(j0 + k + lane, keys - 1));
-        __syncwarp();
-        const int lo = rq_min - rel[live - 1];
-        const int span = rq_max - rel[0] - lo + 1;
-        float *at = copies + (rq - lo);
-#pragma unroll
-        for (int s = 0; s < kTcN / kRelCopies; ++s) {
-            float v[kRelCopies];
-            int k[kRelCopies];
-#pragma unroll
-            for (int g = 0; g < kRelCopies; ++g) {
-                const int c = s + g * (kTcN / kRelCopies);
-                k[g] = g * size - rel[c];
-                if (c < live && mine) v[g] = at[k[g]] + ds[c];
-            }
-#pragma unroll
-            for (int g = 0; g < kRelCopies; ++g)
-                if (s + g * (kTcN / kRelCopies) < live && mine) at[k[g]] = v[g];
-            __syncwarp();
-        }
-        // join the copies into the ring, which is indexed by the relative index
-        for (int k = lane; k < span; k += 32) {
-            float v = 0.0f;
-#pragma unroll
-            for (int g = 0; g < kRelCopies; ++g) {
-                v += copies[g * size + k];
-                copies[g * size + k] = 0.0f;
-            }
-            ring[(lo + k) & (size - 1)] += v;
-        }
-        __syncwarp();
-        const int final_above = j0 + live < keys ? rq_max - rel_k(a, j0 + live) : lo - 1;
-        for (int r = final_above + 1 + lane; r <= top; r += 32) {
-            out[r] = ring[r & (size - 1)];
-            ring[r & (size - 1)] = 0.0f;
-        }
-        top = final_above;
-        __syncwarp();
-    }
-};
 
 template <typename T, int DP, bool BIAS, bool DKV>
 __global__ void __launch_bounds__(kTcThreads, TcBwdShape<DP, DKV>::kCtas)
@@ -152,12 +65,12 @@ __global__ void __launch_bounds__(kTcThreads, TcBwdShape<DP, DKV>::kCtas)
                   *sC2 = sC1 + NS * Sh::kTileBytes;
     float *sVec = reinterpret_cast<float *>(tiles + Sh::kTileSmem);
     float *sRel = sVec + NS * Sh::kVecBytes / 4;
-    float *sBias = sRel + rel_smem(p.rel_window) / 4;
+    float *sBias = sRel + rel_smem(p.rel.window, 4) / 4;
 
     const int rows = DKV ? a.Lk : a.Lq;
     const int row_tiles = (rows + kTcM - 1) / kTcM;
     const int i0 = (int)(blockIdx.x % row_tiles) * kTcM;
-    const int nh = p.head0 + (int)(blockIdx.x / row_tiles);
+    const int nh = p.rel.head0 + (int)(blockIdx.x / row_tiles);
     const int h = nh % a.H, n = nh / a.H;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int keys = keys_of(a, n);
@@ -301,18 +214,11 @@ __global__ void __launch_bounds__(kTcThreads, TcBwdShape<DP, DKV>::kCtas)
         const bool counts = i < live_rows && steps > 0;
         const float row_lse = !DKV ? (counts ? lse2[i] : INFINITY) : 0.0f;
         const float row_delta = !DKV && counts ? delta[i] : 0.0f;
-        const bool with_rel = !DKV && BIAS && p.rel_window > 0 && i0 + warp * 32 < a.Lq && steps > 0;
+        const bool with_rel = !DKV && BIAS && p.rel.window > 0 && i0 + warp * 32 < a.Lq && steps > 0;
         RelWindow win;
         float *rel_out = nullptr;
         if (!DKV && BIAS) {
-            if (with_rel) {
-                win.init(a, sRel, p.rel_window, i0);
-                // indexed by the relative index: the lowest is rq_min - rel_k(Lk - 1)
-                const int warps = (a.Lq + 31) / 32;
-                rel_out = p.rel_part +
-                          ((int64_t)(nh - p.head0) * warps + i0 / 32 + warp) * p.rel_stride -
-                          (win.rq_min - rel_k(a, a.Lk - 1));
-            }
+            if (with_rel) rel_out = win.init(a, sRel, p.rel, i0, nh);
         }
         for (int t = 0; t < steps; ++t) {
             const int live = cols - t * kTcN;
@@ -440,75 +346,6 @@ __global__ void __launch_bounds__(kTcThreads, TcBwdShape<DP, DKV>::kCtas)
     if (warp == 4) tmem_dealloc(tmem, Sh::kTmemCols);
 }
 
-// lse2 and delta of every query: sixteen threads per row, 16 bytes each.
-template <typename T>
-__global__ void attn_delta_kernel(AttnArgs a, const T *dO, const T *O, const float *lse,
-                                  float *lse2, float *delta) {
-    const int L64 = rows64(a.Lq), part = threadIdx.x % 16;
-    const int64_t row = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / 16;   // (n, i, h)
-    if (row >= (int64_t)a.N * L64 * a.H) return;
-    const int h = (int)(row % a.H), i = (int)(row / a.H % L64), n = (int)(row / a.H / L64);
-    float s = 0.0f;
-    if (i < a.Lq && part * 8 < a.D) {
-        const int64_t at = (((int64_t)n * a.Lq + i) * a.H + h) * a.D + part * 8;
-        const uint4 u = __ldg(reinterpret_cast<const uint4 *>(dO + at));
-        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(O + at));
-        const T *x = reinterpret_cast<const T *>(&u), *y = reinterpret_cast<const T *>(&v);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) s = fmaf(IO<T>::to_f(x[k]), IO<T>::to_f(y[k]), s);
-    }
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (part == 0) {
-        const int64_t nh = (int64_t)n * a.H + h;
-        const float v = i < a.Lq ? lse[nh * a.Lq + i] : -INFINITY;
-        lse2[nh * L64 + i] = v == -INFINITY ? INFINITY : v * kLog2e;   // no key: weights of 0
-        delta[nh * L64 + i] = s;
-    }
-}
-
-// rel[h][r] (+)= the warps' sums, batch items and query warps in order; `heads`
-// (batch, head) pairs from head0 on are in `part`.
-__global__ void attn_rel_sum_kernel(AttnArgs a, const float *part, int stride, int head0, int heads,
-                                    float *rel) {
-    const int r = blockIdx.x * blockDim.x + threadIdx.x, h = blockIdx.y;
-    if (r >= a.R) return;
-    const int warps = (a.Lq + 31) / 32, k_end = rel_k(a, a.Lk - 1);
-    float sum = head0 > 0 ? rel[(int64_t)h * a.R + r] : 0.0f;
-    for (int nh = head0 + (h - head0 % a.H + a.H) % a.H; nh < head0 + heads; nh += a.H) {
-        const int keys = keys_of(a, nh / a.H);
-        if (keys == 0) continue;
-        const int k_last = rel_k(a, keys - 1);
-        for (int w = 0; w < warps; ++w) {
-            const int lo = rel_q(a, w * 32), hi = rel_q(a, min(w * 32 + 31, a.Lq - 1));
-            if (r > hi) continue;
-            if (r < lo - k_last) break;   // and below the windows of the warps that follow
-            sum += __ldg(part + ((int64_t)(nh - head0) * warps + w) * stride + (r - lo + k_end));
-        }
-    }
-    rel[(int64_t)h * a.R + r] = sum;
-}
-
-// Power of two that holds the relative indices of a warp's 32 queries against
-// 64 keys; 0 when that is more than 1024 (rows of hundreds of tokens that end
-// inside a tile): 20 KB of windows per 256 floats.
-inline int tc_rel_window(const AttnArgs &a) {
-    const int64_t span = tc_span(32, a.Lq, a.Hq, a.Wq, a.P) + tc_span(kTcN, a.Lk, a.Hk, a.Wk, a.P) + 1;
-    int w = 128;
-    while (w < span) w *= 2;
-    return w <= 1024 ? w : 0;
-}
-// Floats a query warp writes to rel_part.
-inline int64_t tc_rel_stride(const AttnArgs &a) {
-    return tc_span(32, a.Lq, a.Hq, a.Wq, a.P) + (int64_t)(a.Hk - 1) * a.P + a.Wk;
-}
-// (batch, head) pairs of one DQ launch: all, or as many as keep rel_part within
-// 256 MB (one at least); their sums are added launch by launch.
-inline int64_t tc_rel_heads(const AttnArgs &a) {
-    const int64_t per = (int64_t)((a.Lq + 31) / 32) * tc_rel_stride(a) * 4;
-    return std::max<int64_t>(1, std::min<int64_t>((int64_t)a.N * a.H, (int64_t(256) << 20) / per));
-}
-
 template <typename T, int DP, bool BIAS, bool DKV>
 cudaError_t launch_attn_tc_bwd_as(TcBwdArgs &p, int heads, cudaStream_t s) {
     using Sh = TcBwdShape<DP, DKV>;
@@ -518,7 +355,7 @@ cudaError_t launch_attn_tc_bwd_as(TcBwdArgs &p, int heads, cudaStream_t s) {
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmemOne);
     });
     if (e != cudaSuccess) return e;
-    const int base = Sh::kSmem + rel_smem(p.rel_window);
+    const int base = Sh::kSmem + rel_smem(p.rel.window, 4);
     const int64_t window = BIAS ? tc_bias_window(p.a, DKV) : 0;
     const int limit = base <= kTcSmemTwo ? kTcSmemTwo : kTcSmemOne;
     p.bias_window = base + window * 4 <= limit ? (int)window : 0;

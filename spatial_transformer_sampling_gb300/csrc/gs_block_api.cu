@@ -15,6 +15,7 @@ constexpr int64_t kMaxNormWidth = int64_t(1) << 20;
 constexpr int64_t kMaxDropout = int64_t(1) << 40;
 constexpr int64_t kMaxRelative = int64_t(1) << 24;
 constexpr int64_t kMaxHeadWidth = 128;
+constexpr int64_t kMaxHeads = 65535;
 
 size_t elem_size(gs_dtype dt) { return dt == GS_F32 ? 4 : 2; }
 bool dtype_ok(int dt) { return dt == GS_F32 || dt == GS_F16 || dt == GS_BF16; }
@@ -56,7 +57,7 @@ gs_status check_attention(const gs_attention_attrs *at, gs_dtype dt, gs::AttnArg
     if (!at) return GS_ERR_NULL;
     if (!dtype_ok(dt)) return GS_ERR_DTYPE;
     if (!isfinite(at->scale)) return GS_ERR_ATTR;
-    if (at->N < 0 || at->H < 0 || at->D < 1 || at->D > kMaxHeadWidth) return GS_ERR_SHAPE;
+    if (at->N < 0 || at->H < 0 || at->H > kMaxHeads || at->D < 1 || at->D > kMaxHeadWidth) return GS_ERR_SHAPE;
     for (int d = 0; d < 2; ++d)
         if (at->q_extent[d] < 0 || at->q_extent[d] > kMax31 || at->k_extent[d] < 0 ||
             at->k_extent[d] > kMax31)
