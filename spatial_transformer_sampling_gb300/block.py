@@ -4,6 +4,7 @@ position, each with its gradient.  As in the rest of the package the functions
 only check and marshal; every step of the computation runs in libgs's kernels.
 """
 import ctypes
+import functools
 
 from . import (AttentionAttrs, _check_tensors, _dtype_code, _i64, _ok, _shape_error, _torch,
                load_library)
@@ -14,7 +15,9 @@ def _p(t):
 
 
 def _current(t):
-    return _torch().cuda.current_stream(t.device).cuda_stream
+    """Handle of the current stream of t's device.  The lookup behind
+    torch.cuda.current_stream, without making a Stream object (2 us of a call's 15)."""
+    return _torch()._C._cuda_getCurrentRawStream(t.device.index)
 
 
 def _scratch(workspace, nbytes, like):
@@ -75,14 +78,15 @@ def gs_layer_norm(X, Scale, B=None, axis=-1, epsilon=1e-5, out=None):
     elif out.shape != X.shape:
         _shape_error("out", out.shape, X.shape)
     kept = tuple(X.shape[:axis]) + (1,) * (X.dim() - axis)
-    stats = torch.empty((2,) + kept, dtype=torch.float32, device=X.device)
-    mean, inv = stats.unbind(0)
+    mean = torch.empty(kept, dtype=torch.float32, device=X.device)
+    inv = torch.empty_like(mean)
     _ok(load_library().gs_layer_norm(X.data_ptr(), Scale.data_ptr(), _p(B), rows, D,
                                      _dtype_code(X), epsilon, out.data_ptr(), mean.data_ptr(),
                                      inv.data_ptr(), _current(X)), "gs_layer_norm")
     return out, mean, inv
 
 
+@functools.lru_cache(maxsize=256)
 def gs_layer_norm_backward_workspace_size(rows, D):
     """Workspace bytes gs_layer_norm_backward needs."""
     n = ctypes.c_size_t(0)
@@ -149,53 +153,92 @@ def gs_relative_buckets(q_extent, k_extent, num_buckets=0, max_distance=128, cau
     return m.to(device), int(count.value)
 
 
-def _head_strides(t, what):
-    if t.dim() != 4:
-        raise ValueError(f"{what} must be (N, L, H, D), got {tuple(t.shape)}")
-    s = t.stride()
-    if s[3] != 1 and t.shape[3] != 1:
-        raise ValueError(f"the last axis of {what} must be contiguous")
-    return s[:3]
-
-
-def _attention_attrs(Q, K, V, table, buckets, q_extent, k_extent, k_len, scale):
-    torch = _torch()
-    qs, ks, vs = _head_strides(Q, "Q"), _head_strides(K, "K"), _head_strides(V, "V")
+def _attention_attrs(Q, K, V, table, q_extent, k_extent, scale):
+    """AttentionAttrs of tensors whose shapes and strides fit together."""
+    for t, what in ((Q, "Q"), (K, "K"), (V, "V")):
+        if t.dim() != 4:
+            raise ValueError(f"{what} must be (N, L, H, D), got {tuple(t.shape)}")
+        if t.stride(3) != 1 and t.shape[3] != 1:
+            raise ValueError(f"the last axis of {what} must be contiguous")
     N, Lq, H, D = Q.shape
     Lk = K.shape[1]
     if K.shape != (N, Lk, H, D):
         _shape_error("K", K.shape, (N, Lk, H, D))
     if V.shape != K.shape:
         _shape_error("V", V.shape, K.shape)
-    for t in (K, V, table):
-        if t is not None and (t.dtype != Q.dtype or t.device != Q.device):
-            raise ValueError("all tensors of one call share dtype and device")
-    if not Q.is_cuda:
-        raise ValueError("libgs takes CUDA tensors")
     q_extent = (1, Lq) if q_extent is None else tuple(q_extent)
     k_extent = (1, Lk) if k_extent is None else tuple(k_extent)
     if q_extent[0] * q_extent[1] != Lq or k_extent[0] * k_extent[1] != Lk:
         raise ValueError(f"extents {q_extent} and {k_extent} do not hold {Lq} and {Lk} tokens")
-    if (table is None) != (buckets is None):
-        raise ValueError("table and buckets go together")
     nb = 0
     if table is not None:
-        if table.dim() != 2 or table.shape[1] != H or not table.is_contiguous():
-            raise ValueError(f"table must be contiguous (buckets, H={H}), got "
-                             f"{tuple(table.shape)}")
+        if table.dim() != 2 or table.shape[1] != H:
+            raise ValueError(f"table must be (buckets, H={H}), got {tuple(table.shape)}")
         nb = table.shape[0]
-        R = (q_extent[0] + k_extent[0] - 1) * (q_extent[1] + k_extent[1] - 1)
-        if (buckets.dtype != torch.int32 or buckets.device != Q.device
-                or not buckets.is_contiguous() or (Lq and Lk and buckets.numel() != R)):
-            raise ValueError(f"buckets must be a contiguous int32 tensor of {R} entries on the "
-                             f"inputs' device")
-    if k_len is not None and (k_len.dtype != torch.int32 or k_len.device != Q.device
-                              or not k_len.is_contiguous() or tuple(k_len.shape) != (N,)):
-        raise ValueError(f"k_len must be a contiguous int32 tensor of N={N} entries on the "
-                         f"inputs' device")
     i3, i2 = ctypes.c_int64 * 3, ctypes.c_int64 * 2
-    return AttentionAttrs(N, H, D, i2(*q_extent), i2(*k_extent), i3(*qs), i3(*ks), i3(*vs), nb,
+    return AttentionAttrs(N, H, D, i2(*q_extent), i2(*k_extent), i3(*Q.stride()[:3]),
+                          i3(*K.stride()[:3]), i3(*V.stride()[:3]), nb,
                           D ** -0.5 if scale is None else scale)
+
+
+class _Plan:
+    """What a call's shapes, strides and dtype alone decide: the C attributes and the workspace
+    sizes.  Kept per signature, since building and checking them takes longer than a launch."""
+
+    def __init__(self, Q, K, V, table, q_extent, k_extent, scale):
+        self.attrs = _attention_attrs(Q, K, V, table, q_extent, k_extent, scale)
+        self.ref = ctypes.byref(self.attrs)
+        self.code = _dtype_code(Q)
+        at = self.attrs
+        self.lse_shape = (at.N, at.H, Q.shape[1])
+        self.entries = ((at.q_extent[0] + at.k_extent[0] - 1)
+                        * (at.q_extent[1] + at.k_extent[1] - 1) if Q.shape[1] and K.shape[1] else 0)
+        self._bytes = {}
+
+    def workspace(self, backward):
+        if backward not in self._bytes:
+            self._bytes[backward] = gs_attention_workspace_size(self.attrs, self.code, backward)
+        return self._bytes[backward]
+
+
+_PLANS = {}
+_MOST_PLANS = 256
+
+
+def _plan(Q, K, V, table, buckets, q_extent, k_extent, k_len, scale):
+    torch = _torch()
+    key = (Q.shape, Q.stride(), K.shape, K.stride(), V.shape, V.stride(), Q.dtype,
+           None if table is None else table.shape, q_extent, k_extent, scale)
+    try:
+        plan = _PLANS.get(key)
+    except TypeError:        # extents given as lists
+        return _plan(Q, K, V, table, buckets, tuple(q_extent), tuple(k_extent), k_len, scale)
+    if plan is None:
+        plan = _Plan(Q, K, V, table, q_extent, k_extent, scale)
+        if len(_PLANS) >= _MOST_PLANS:
+            _PLANS.clear()
+        _PLANS[key] = plan
+    device = Q.device
+    if device.type != "cuda":
+        raise ValueError("libgs takes CUDA tensors")
+    if (K.dtype != Q.dtype or V.dtype != Q.dtype or K.device != device or V.device != device
+            or (table is not None and (table.dtype != Q.dtype or table.device != device))):
+        raise ValueError("all tensors of one call share dtype and device")
+    if table is None:
+        if buckets is not None:
+            raise ValueError("table and buckets go together")
+    elif buckets is None:
+        raise ValueError("table and buckets go together")
+    elif (buckets.dtype != torch.int32 or buckets.device != device
+          or not buckets.is_contiguous() or not table.is_contiguous()
+          or (plan.entries and buckets.numel() != plan.entries)):
+        raise ValueError(f"table must be contiguous, buckets a contiguous int32 tensor of "
+                         f"{plan.entries} entries on the inputs' device")
+    if k_len is not None and (k_len.dtype != torch.int32 or k_len.device != device
+                              or not k_len.is_contiguous() or k_len.shape != Q.shape[:1]):
+        raise ValueError(f"k_len must be a contiguous int32 tensor of N={Q.shape[0]} entries on "
+                         f"the inputs' device")
+    return plan
 
 
 def gs_attention_workspace_size(attrs, dtype_code, backward=False):
@@ -221,17 +264,16 @@ def gs_attention(Q, K, V, table=None, buckets=None, q_extent=None, k_extent=None
     the keys from there on; ``scale`` defaults to 1 / sqrt(D).  O is dense (N, Lq, H, D), LSE
     float32 (N, H, Lq)."""
     torch = _torch()
-    at = _attention_attrs(Q, K, V, table, buckets, q_extent, k_extent, k_len, scale)
+    plan = _plan(Q, K, V, table, buckets, q_extent, k_extent, k_len, scale)
     if out is None:
         out = torch.empty(Q.shape, dtype=Q.dtype, device=Q.device)
     elif (out.shape != Q.shape or not out.is_contiguous() or out.dtype != Q.dtype
           or out.device != Q.device):
         raise ValueError(f"out must be dense {tuple(Q.shape)} of Q's dtype and device")
-    lse = torch.empty((at.N, at.H, Q.shape[1]), dtype=torch.float32, device=Q.device)
-    code = _dtype_code(Q)
-    ws, have, _keep = _scratch(workspace, gs_attention_workspace_size(at, code), Q)
+    lse = torch.empty(plan.lse_shape, dtype=torch.float32, device=Q.device)
+    ws, have, _keep = _scratch(workspace, plan.workspace(False), Q)
     _ok(load_library().gs_attention(Q.data_ptr(), K.data_ptr(), V.data_ptr(), _p(table),
-                                    _p(buckets), _p(k_len), ctypes.byref(at), code, ws, have,
+                                    _p(buckets), _p(k_len), plan.ref, plan.code, ws, have,
                                     out.data_ptr(), lse.data_ptr(), _current(Q)), "gs_attention")
     return out, lse
 
@@ -241,22 +283,19 @@ def gs_attention_backward(dO, Q, K, V, O, LSE, table=None, buckets=None, q_exten
     """Gradient of gs_attention: [dQ, dK, dV, dTable] (the first three without a table); dQ, dK
     and dV are dense (N, L, H, D)."""
     torch = _torch()
-    at = _attention_attrs(Q, K, V, table, buckets, q_extent, k_extent, k_len, scale)
-    _check_tensors(dO, O)
+    plan = _plan(Q, K, V, table, buckets, q_extent, k_extent, k_len, scale)
     for what, t in (("dO", dO), ("O", O)):
         if t.shape != Q.shape:
             _shape_error(what, t.shape, Q.shape)
-    if dO.dtype != Q.dtype or dO.device != Q.device:
-        raise ValueError("all tensors of one call share dtype and device")
-    _check_f32(LSE, (at.N, at.H, Q.shape[1]), "LSE", Q)
-    made = [torch.empty(t.shape, dtype=Q.dtype, device=Q.device) for t in (Q, K, V)]
-    if table is not None:
-        made.append(torch.empty(table.shape, dtype=Q.dtype, device=Q.device))
-    code = _dtype_code(Q)
-    ws, have, _keep = _scratch(workspace, gs_attention_workspace_size(at, code, True), Q)
+        if not t.is_contiguous() or t.dtype != Q.dtype or t.device != Q.device:
+            raise ValueError(f"{what} must be dense, of Q's dtype and device")
+    _check_f32(LSE, plan.lse_shape, "LSE", Q)
+    made = [torch.empty(t.shape, dtype=Q.dtype, device=Q.device)
+            for t in ((Q, K, V) if table is None else (Q, K, V, table))]
+    ws, have, _keep = _scratch(workspace, plan.workspace(True), Q)
     _ok(load_library().gs_attention_backward(
         dO.data_ptr(), Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(), LSE.data_ptr(),
-        _p(table), _p(buckets), _p(k_len), ctypes.byref(at), code, ws, have, made[0].data_ptr(),
+        _p(table), _p(buckets), _p(k_len), plan.ref, plan.code, ws, have, made[0].data_ptr(),
         made[1].data_ptr(), made[2].data_ptr(), made[3].data_ptr() if table is not None else None,
         _current(Q)), "gs_attention_backward")
     return made

@@ -2,33 +2,97 @@
 // residual sum: Y = residual + (kept ? X / (1 - ratio) : 0).
 //
 // The mask is a function of (seed, offset, element index) and is never stored:
-// the backward pass calls the same kernel on the gradient.
-#include "gs_common.cuh"
+// the backward pass calls the same kernel on the gradient.  Bound by memory:
+// ten Philox rounds cost about 45 instructions per four elements, a third of
+// the issue slots that moving them leaves.  A thread moves 16-byte runs, kRuns
+// of them a block apart, all loads first.
 #include "gs_internal.h"
 #include "gs_philox.cuh"
+#include "gs_vec.cuh"
 
 namespace gs {
+namespace {
 
-template <typename T>
-__global__ void dropout_kernel(const T *X, const T *residual, T *Y, DropoutArgs a) {
-    const int64_t quad = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    const int64_t i0 = quad * 4;
-    if (i0 >= a.n) return;
-    uint32_t w[4];
-    philox4x32_10((uint64_t)quad, a.offset, a.seed, w);
-    for (int k = 0; k < 4 && i0 + k < a.n; ++k) {
-        const float x = IO<T>::to_f(X[i0 + k]);
-        float y = w[k] >= a.threshold ? x * a.scale : 0.0f;
-        if (residual) y += IO<T>::to_f(residual[i0 + k]);
-        Y[i0 + k] = IO<T>::st(y);
+constexpr int kDropThreads = 256;
+constexpr int kRuns = 4;
+
+// The kept and scaled value of E consecutive elements from element i0 on (a
+// multiple of four), plus r.
+template <int E>
+__device__ __forceinline__ void drop(float (&x)[E], const float (&r)[E], int64_t i0, bool residual,
+                                     const DropoutArgs &a) {
+#pragma unroll
+    for (int e = 0; e < E; e += 4) {
+        uint32_t w[4];
+        philox4x32_10((uint64_t)(i0 + e) / 4, a.offset, a.seed, w);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const float y = w[q] >= a.threshold ? x[e + q] * a.scale : 0.0f;
+            x[e + q] = residual ? r[e + q] + y : y;
+        }
     }
 }
+
+// Runs of 16 bytes (VEC), or where a base is not aligned and at the end of the
+// tensor four elements (one generator call) moved one by one.  X, residual and
+// Y may be the same memory: a thread reads an element before it writes it, and
+// no other does.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kDropThreads)
+    dropout_kernel(const T *X, const T *residual, T *Y, DropoutArgs a) {
+    constexpr int E = VEC ? kVec<T> : 4;
+    const int64_t run0 = (int64_t)blockIdx.x * (kDropThreads * kRuns) + threadIdx.x;
+    if constexpr (VEC) {
+        if ((run0 + (kRuns - 1) * kDropThreads + 1) * E <= a.n) {
+            using IOV = Run<T, E>;
+            typename IOV::Raw rx[kRuns], rr[kRuns];
+#pragma unroll
+            for (int k = 0; k < kRuns; ++k) {
+                const int64_t i = (run0 + k * kDropThreads) * E;
+                rx[k] = IOV::load(X + i);
+                rr[k] = residual ? IOV::load(residual + i) : IOV::zero();
+            }
+#pragma unroll
+            for (int k = 0; k < kRuns; ++k) {
+                const int64_t i = (run0 + k * kDropThreads) * E;
+                float x[E], r[E];
+                IOV::widen(rx[k], x);
+                IOV::widen(rr[k], r);
+                drop(x, r, i, residual != nullptr, a);
+                IOV::store(Y + i, x);
+            }
+            return;
+        }
+    }
+#pragma unroll 1
+    for (int k = 0; k < kRuns; ++k)
+#pragma unroll 1
+        for (int part = 0; part < E; part += 4) {
+            const int64_t i = (run0 + k * kDropThreads) * E + part;
+            float x[4], r[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                x[e] = i + e < a.n ? IO<T>::to_f(X[i + e]) : 0.0f;
+                r[e] = i + e < a.n && residual ? IO<T>::to_f(residual[i + e]) : 0.0f;
+            }
+            if (i >= a.n) return;
+            drop(x, r, i, residual != nullptr, a);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (i + e < a.n) Y[i + e] = IO<T>::st(x[e]);
+        }
+}
+
+}  // namespace
 
 template <typename T>
 cudaError_t launch_dropout(const void *X, const void *residual, void *Y, const DropoutArgs &a,
                            cudaStream_t s) {
-    const int64_t blocks = ((a.n + 3) / 4 + 255) / 256;
-    dropout_kernel<T><<<(unsigned)blocks, 256, 0, s>>>((const T *)X, (const T *)residual, (T *)Y, a);
+    const bool vec = aligned16(X) && aligned16(residual) && aligned16(Y);
+    const int64_t per_block = (int64_t)kDropThreads * kRuns * (vec ? kVec<T> : 4);
+    auto kernel = vec ? dropout_kernel<T, true> : dropout_kernel<T, false>;
+    kernel<<<(unsigned)((a.n + per_block - 1) / per_block), kDropThreads, 0, s>>>(
+        (const T *)X, (const T *)residual, (T *)Y, a);
     return cudaGetLastError();
 }
 

@@ -6,119 +6,371 @@
 // Backward, with xhat = (x - mean) * inv and g = dy * scale:
 //   dx = inv * (g - sum(g) / D - xhat * sum(g * xhat) / D),
 //   dscale = sum over rows of dy * xhat,  dB = sum over rows of dy.
-#include "gs_common.cuh"
+//
+// Both read their inputs once: a row stays in the registers of the L threads
+// that share it (8, 16, 32 or a block of 256), NV runs of V elements each, up
+// to D = 8192; longer rows are read again for each pass.  The backward pass
+// walks rows with a fixed set of blocks, so that a thread keeps the sums of its
+// columns over all its rows; a second kernel adds the blocks in order.
 #include "gs_internal.h"
+#include "gs_vec.cuh"
 
 namespace gs {
 namespace {
 
 constexpr int kNormThreads = 256;
+constexpr int kNormOnChip = 8192;      // widest row held in registers
+constexpr int kNormSms = 152;
 
-__device__ __forceinline__ float warp_sum(float v) {
+// Sum over the L threads of a row.  L = 256 uses shared memory, two slots in
+// turn so that one barrier per sum suffices.
+template <int L> __device__ __forceinline__ float row_sum(float v, int slot) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    for (int o = (L < 32 ? L : 32) / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (L > 32) {
+        __shared__ float s[2][L / 32 > 0 ? L / 32 : 1];
+        if (threadIdx.x % 32 == 0) s[slot][threadIdx.x / 32] = v;
+        __syncthreads();
+        v = 0.0f;
+#pragma unroll
+        for (int w = 0; w < L / 32; ++w) v += s[slot][w];
+    }
     return v;
 }
 
-// One warp per row.
-template <typename T>
+// R rows per group of L threads, loads of all of them first.
+template <typename T, int V, int L, int NV, int R>
 __global__ void __launch_bounds__(kNormThreads)
     layer_norm_kernel(const T *X, const T *scale, const T *B, T *Y, float *mean, float *inv,
                       NormArgs a) {
-    const int64_t row = (int64_t)blockIdx.x * (kNormThreads / 32) + threadIdx.x / 32;
-    const int lane = threadIdx.x % 32;
-    if (row >= a.rows) return;
+    using IOV = Run<T, V>;
+    constexpr int kGroups = kNormThreads / L;
+    const int part = threadIdx.x % L;
+    const int64_t row0 = ((int64_t)blockIdx.x * kGroups + threadIdx.x / L) * R;
+    typename IOV::Raw raw[R][NV];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int d = (k * L + part) * V;
+            raw[r][k] = row0 + r < a.rows && d < a.D ? IOV::load(X + (row0 + r) * a.D + d) : IOV::zero();
+        }
+    float x[R][NV][V], m[R], iv[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        float s = 0.0f;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            IOV::widen(raw[r][k], x[r][k]);
+#pragma unroll
+            for (int e = 0; e < V; ++e) s += x[r][k][e];
+        }
+        m[r] = row_sum<L>(s, 0) / (float)a.D;
+        s = 0.0f;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const bool on = (k * L + part) * V < a.D;
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                x[r][k][e] -= m[r];
+                if (on) s = fmaf(x[r][k][e], x[r][k][e], s);
+            }
+        }
+        iv[r] = 1.0f / sqrtf(row_sum<L>(s, 1) / (float)a.D + a.eps);
+    }
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int d = (k * L + part) * V;
+        if (d >= a.D) continue;
+        float g[V], b[V] = {};
+        IOV::widen(IOV::load(scale + d), g);
+        if (B) IOV::widen(IOV::load(B + d), b);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            if (row0 + r >= a.rows) continue;
+            float y[V];
+#pragma unroll
+            for (int e = 0; e < V; ++e) y[e] = fmaf(x[r][k][e] * iv[r], g[e], b[e]);
+            IOV::store(Y + (row0 + r) * a.D + d, y);
+        }
+    }
+    if (part == 0) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            if (row0 + r >= a.rows) continue;
+            if (mean) mean[row0 + r] = m[r];
+            if (inv) inv[row0 + r] = iv[r];
+        }
+    }
+}
+
+// Rows wider than kNormOnChip: a block per row, three passes.
+template <typename T>
+__global__ void __launch_bounds__(kNormThreads)
+    layer_norm_wide_kernel(const T *X, const T *scale, const T *B, T *Y, float *mean, float *inv,
+                           NormArgs a) {
+    const int64_t row = blockIdx.x;
     const T *x = X + row * a.D;
     float s = 0.0f;
-    for (int i = lane; i < a.D; i += 32) s += IO<T>::ld(x + i);
-    const float m = warp_sum(s) / (float)a.D;
-    float v = 0.0f;
-    for (int i = lane; i < a.D; i += 32) {
-        const float d = IO<T>::ld(x + i) - m;
-        v = fmaf(d, d, v);
+    for (int d = threadIdx.x; d < a.D; d += kNormThreads) s += IO<T>::ld(x + d);
+    const float m = row_sum<kNormThreads>(s, 0) / (float)a.D;
+    s = 0.0f;
+    for (int d = threadIdx.x; d < a.D; d += kNormThreads) {
+        const float c = IO<T>::ld(x + d) - m;
+        s = fmaf(c, c, s);
     }
-    const float r = 1.0f / sqrtf(warp_sum(v) / (float)a.D + a.eps);
-    for (int i = lane; i < a.D; i += 32) {
-        const float b = B ? IO<T>::ld(B + i) : 0.0f;
-        Y[row * a.D + i] = IO<T>::st(fmaf((IO<T>::ld(x + i) - m) * r, IO<T>::ld(scale + i), b));
+    const float r = 1.0f / sqrtf(row_sum<kNormThreads>(s, 1) / (float)a.D + a.eps);
+    for (int d = threadIdx.x; d < a.D; d += kNormThreads) {
+        const float b = B ? IO<T>::ld(B + d) : 0.0f;
+        Y[row * a.D + d] = IO<T>::st(fmaf((IO<T>::ld(x + d) - m) * r, IO<T>::ld(scale + d), b));
     }
-    if (lane == 0) {
+    if (threadIdx.x == 0) {
         if (mean) mean[row] = m;
         if (inv) inv[row] = r;
     }
 }
 
+// dX of the block's rows and, into partials[block], its column sums (the sums
+// for dScale, then those for dB).
+template <typename T, int V, int L, int NV>
+__global__ void __launch_bounds__(kNormThreads)
+    layer_norm_backward_kernel(const T *dY, const T *X, const T *scale, const float *mean,
+                               const float *inv, T *dX, float *partials, NormArgs a) {
+    using IOV = Run<T, V>;
+    constexpr int kGroups = kNormThreads / L;
+    const int part = threadIdx.x % L, group = threadIdx.x / L;
+    float ds[NV][V] = {}, db[NV][V] = {};
+    for (int64_t row0 = (int64_t)blockIdx.x * kGroups; row0 < a.rows;
+         row0 += (int64_t)gridDim.x * kGroups) {
+        const int64_t row = row0 + group;
+        const bool here = row < a.rows;
+        typename IOV::Raw rx[NV], rg[NV];
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int d = (k * L + part) * V;
+            const bool on = here && d < a.D;
+            rx[k] = on ? IOV::load(X + row * a.D + d) : IOV::zero();
+            rg[k] = on ? IOV::load(dY + row * a.D + d) : IOV::zero();
+        }
+        const float m = here ? __ldg(mean + row) : 0.0f, iv = here ? __ldg(inv + row) : 0.0f;
+        float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int d = (k * L + part) * V;
+            if (d >= a.D) continue;
+            float x[V], g[V], w[V];
+            IOV::widen(rx[k], x);
+            IOV::widen(rg[k], g);
+            IOV::widen(IOV::load(scale + d), w);
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const float xh = (x[e] - m) * iv;
+                ds[k][e] = fmaf(g[e], xh, ds[k][e]);
+                db[k][e] += g[e];
+                s0 = fmaf(g[e], w[e], s0);
+                s1 = fmaf(g[e] * w[e], xh, s1);
+            }
+        }
+        s0 = row_sum<L>(s0, 0) / (float)a.D;
+        s1 = row_sum<L>(s1, 1) / (float)a.D;
+        if (!here) continue;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int d = (k * L + part) * V;
+            if (d >= a.D) continue;
+            float x[V], g[V], w[V], out[V];
+            IOV::widen(rx[k], x);
+            IOV::widen(rg[k], g);
+            IOV::widen(IOV::load(scale + d), w);
+#pragma unroll
+            for (int e = 0; e < V; ++e) out[e] = iv * (g[e] * w[e] - s0 - (x[e] - m) * iv * s1);
+            IOV::store(dX + row * a.D + d, out);
+        }
+    }
+    if (!partials) return;
+    // the groups of the block in order; one column run of every thread at a time
+    float *out = partials + (int64_t)blockIdx.x * 2 * a.D;
+    __shared__ float s_ds[kNormThreads * V], s_db[kNormThreads * V];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        if (kGroups > 1) {
+            __syncthreads();
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                s_ds[threadIdx.x * V + e] = ds[k][e];
+                s_db[threadIdx.x * V + e] = db[k][e];
+            }
+            __syncthreads();
+            for (int c = threadIdx.x; c < L * V; c += kNormThreads) {
+                const int d = k * L * V + c;
+                float t0 = 0.0f, t1 = 0.0f;
+#pragma unroll
+                for (int g = 0; g < kGroups; ++g) {
+                    t0 += s_ds[g * L * V + c];
+                    t1 += s_db[g * L * V + c];
+                }
+                if (d < a.D) {
+                    out[d] = t0;
+                    out[a.D + d] = t1;
+                }
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const int d = (k * L + part) * V + e;
+                if (d < a.D) {
+                    out[d] = ds[k][e];
+                    out[a.D + d] = db[k][e];
+                }
+            }
+        }
+    }
+}
+
+// Rows wider than kNormOnChip: a block per row for dX, then a thread per column
+// for the sums of a block of rows.
 template <typename T>
 __global__ void __launch_bounds__(kNormThreads)
-    layer_norm_dx_kernel(const T *dY, const T *X, const T *scale, const float *mean,
-                         const float *inv, T *dX, NormArgs a) {
-    const int64_t row = (int64_t)blockIdx.x * (kNormThreads / 32) + threadIdx.x / 32;
-    const int lane = threadIdx.x % 32;
-    if (row >= a.rows) return;
+    layer_norm_wide_dx_kernel(const T *dY, const T *X, const T *scale, const float *mean,
+                              const float *inv, T *dX, NormArgs a) {
+    const int64_t row = blockIdx.x;
     const T *x = X + row * a.D, *dy = dY + row * a.D;
     const float m = mean[row], r = inv[row];
     float s0 = 0.0f, s1 = 0.0f;
-    for (int i = lane; i < a.D; i += 32) {
-        const float g = IO<T>::ld(dy + i) * IO<T>::ld(scale + i);
+    for (int d = threadIdx.x; d < a.D; d += kNormThreads) {
+        const float g = IO<T>::ld(dy + d) * IO<T>::ld(scale + d);
         s0 += g;
-        s1 = fmaf(g, (IO<T>::ld(x + i) - m) * r, s1);
+        s1 = fmaf(g, (IO<T>::ld(x + d) - m) * r, s1);
     }
-    s0 = warp_sum(s0) / (float)a.D;
-    s1 = warp_sum(s1) / (float)a.D;
-    for (int i = lane; i < a.D; i += 32) {
-        const float g = IO<T>::ld(dy + i) * IO<T>::ld(scale + i);
-        const float xh = (IO<T>::ld(x + i) - m) * r;
-        dX[row * a.D + i] = IO<T>::st(r * (g - s0 - xh * s1));
+    s0 = row_sum<kNormThreads>(s0, 0) / (float)a.D;
+    s1 = row_sum<kNormThreads>(s1, 1) / (float)a.D;
+    for (int d = threadIdx.x; d < a.D; d += kNormThreads) {
+        const float g = IO<T>::ld(dy + d) * IO<T>::ld(scale + d);
+        dX[row * a.D + d] = IO<T>::st(r * (g - s0 - (IO<T>::ld(x + d) - m) * r * s1));
     }
 }
-
-// Column sums of one block of rows: a thread per column, rows in order.
 template <typename T>
-__global__ void layer_norm_partial_kernel(const T *dY, const T *X, const float *mean,
-                                          const float *inv, float *partials, int64_t rows_per,
-                                          NormArgs a) {
-    const int col = blockIdx.x * blockDim.x + threadIdx.x;
-    if (col >= a.D) return;
-    const int64_t r0 = blockIdx.y * rows_per, r1 = min(r0 + rows_per, a.rows);
+__global__ void layer_norm_wide_partial_kernel(const T *dY, const T *X, const float *mean,
+                                               const float *inv, float *partials, NormArgs a) {
+    const int d = blockIdx.x * blockDim.x + threadIdx.x;
+    if (d >= a.D) return;
     float s0 = 0.0f, s1 = 0.0f;
-    for (int64_t row = r0; row < r1; ++row) {
-        const float dy = IO<T>::ld(dY + row * a.D + col);
-        s0 = fmaf(dy, (IO<T>::ld(X + row * a.D + col) - mean[row]) * inv[row], s0);
-        s1 += dy;
+    for (int64_t row = blockIdx.y; row < a.rows; row += gridDim.y) {
+        const float g = IO<T>::ld(dY + row * a.D + d);
+        s0 = fmaf(g, (IO<T>::ld(X + row * a.D + d) - mean[row]) * inv[row], s0);
+        s1 += g;
     }
-    partials[((int64_t)blockIdx.y * 2) * a.D + col] = s0;
-    partials[((int64_t)blockIdx.y * 2 + 1) * a.D + col] = s1;
+    partials[(int64_t)blockIdx.y * 2 * a.D + d] = s0;
+    partials[((int64_t)blockIdx.y * 2 + 1) * a.D + d] = s1;
 }
 
+// dScale (y = 0) and dB (y = 1) from the blocks' sums: 32 columns a block, 32
+// threads per column with every 32nd block each, joined in order.
 template <typename T>
-__global__ void layer_norm_finish_kernel(const float *partials, int blocks, T *dScale, T *dB,
-                                         int D) {
-    const int col = blockIdx.x * blockDim.x + threadIdx.x;
-    if (col >= D) return;
-    float s0 = 0.0f, s1 = 0.0f;
-    for (int b = 0; b < blocks; ++b) {
-        s0 += partials[((int64_t)b * 2) * D + col];
-        s1 += partials[((int64_t)b * 2 + 1) * D + col];
-    }
-    if (dScale) dScale[col] = IO<T>::st(s0);
-    if (dB) dB[col] = IO<T>::st(s1);
+__global__ void __launch_bounds__(1024)
+    layer_norm_finish_kernel(const float *partials, int blocks, T *dScale, T *dB, int D) {
+    __shared__ float s[32][33];
+    const int lane = threadIdx.x % 32, slice = threadIdx.x / 32, d = blockIdx.x * 32 + lane;
+    T *out = blockIdx.y ? dB : dScale;
+    if (!out) return;
+    float sum = 0.0f;
+#pragma unroll 4
+    for (int b = slice; b < blocks; b += 32)
+        if (d < D) sum += __ldg(partials + ((int64_t)b * 2 + blockIdx.y) * D + d);
+    s[slice][lane] = sum;
+    __syncthreads();
+    // a warp per column: lane `lane` holds slice `lane` of column `slice`
+    float v = s[lane][slice];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (lane == 0 && blockIdx.x * 32 + slice < D) out[blockIdx.x * 32 + slice] = IO<T>::st(v);
+}
+
+// Calls f(L, NV) with the threads per row and the runs per thread for a row of
+// `runs` runs: a warp or less while a thread's share is small (no barrier in
+// its sums), a block beyond that.
+template <int V, typename F> cudaError_t norm_shape(int runs, F &&f) {
+    using std::integral_constant;
+    if (runs <= 8) return f(integral_constant<int, 8>(), integral_constant<int, 1>());
+    if (runs <= 16) return f(integral_constant<int, 16>(), integral_constant<int, 1>());
+    if (runs <= 32) return f(integral_constant<int, 32>(), integral_constant<int, 1>());
+    if (runs <= 64) return f(integral_constant<int, 32>(), integral_constant<int, 2>());
+    if (runs <= 128) return f(integral_constant<int, 32>(), integral_constant<int, 4>());
+    if (runs <= 256 && V > 1) return f(integral_constant<int, 256>(), integral_constant<int, 1>());
+    if (runs <= 256) return f(integral_constant<int, 32>(), integral_constant<int, 8>());
+    if (runs <= 512 && V > 1) return f(integral_constant<int, 256>(), integral_constant<int, 2>());
+    if (runs <= 1024) return f(integral_constant<int, 256>(), integral_constant<int, 4>());
+    if constexpr (V <= 4)
+        if (runs <= 2048) return f(integral_constant<int, 256>(), integral_constant<int, 8>());
+    if constexpr (V == 1) return f(integral_constant<int, 256>(), integral_constant<int, 32>());
+    return cudaErrorInvalidValue;   // not reached: D <= kNormOnChip
+}
+
+// Row blocks of the backward pass: eight per SM while a thread holds one run
+// per row (few bytes in flight each), down to two with its registers full.
+int row_blocks(int64_t rows, int L, int NV) {
+    const int64_t b = (rows + kNormThreads / L - 1) / (kNormThreads / L);
+    const int most = kNormSms * (NV == 1 ? 8 : NV == 2 ? 4 : 2);
+    return (int)(b < most ? b : most);
+}
+constexpr int kWideNV = 32;   // rows wider than kNormOnChip: as the fullest
+template <int V> int row_blocks_of(int64_t rows, int64_t D) {
+    int blocks = row_blocks(rows, kNormThreads, kWideNV);
+    if (D <= kNormOnChip)
+        norm_shape<V>((int)((D + V - 1) / V), [&](auto l, auto nv) {
+            blocks = row_blocks(rows, decltype(l)::value, decltype(nv)::value);
+            return cudaSuccess;
+        });
+    return blocks;
+}
+
+template <typename T, int V>
+cudaError_t run_forward(const T *X, const T *scale, const T *B, T *Y, float *mean, float *inv,
+                        const NormArgs &a, cudaStream_t s) {
+    return norm_shape<V>((a.D + V - 1) / V, [&](auto l, auto nv) {
+        constexpr int L = decltype(l)::value, NV = decltype(nv)::value;
+        constexpr int R = L == 256 || NV > 2 ? 1 : NV == 2 ? 2 : 4;   // about four runs in flight
+        constexpr int kRows = kNormThreads / L * R;
+        layer_norm_kernel<T, V, L, NV, R>
+            <<<(unsigned)((a.rows + kRows - 1) / kRows), kNormThreads, 0, s>>>(X, scale, B, Y, mean,
+                                                                              inv, a);
+        return cudaGetLastError();
+    });
+}
+
+template <typename T, int V>
+cudaError_t run_backward(const T *dY, const T *X, const T *scale, const float *mean,
+                         const float *inv, T *dX, float *partials, int *blocks, const NormArgs &a,
+                         cudaStream_t s) {
+    return norm_shape<V>((a.D + V - 1) / V, [&](auto l, auto nv) {
+        constexpr int L = decltype(l)::value, NV = decltype(nv)::value;
+        *blocks = row_blocks(a.rows, L, NV);
+        layer_norm_backward_kernel<T, V, L, NV>
+            <<<*blocks, kNormThreads, 0, s>>>(dY, X, scale, mean, inv, dX, partials, a);
+        return cudaGetLastError();
+    });
 }
 
 }  // namespace
 
 int layer_norm_partial_blocks(int64_t rows, int64_t D) {
-    (void)D;
-    const int64_t b = (rows + 63) / 64;
-    return (int)(b < 1 ? 1 : b > 608 ? 608 : b);
+    // whatever the type and alignment will be
+    const int b1 = row_blocks_of<1>(rows, D), b4 = row_blocks_of<4>(rows, D);
+    const int b8 = row_blocks_of<8>(rows, D);
+    return b1 > b4 ? (b1 > b8 ? b1 : b8) : (b4 > b8 ? b4 : b8);
 }
 
 template <typename T>
 cudaError_t launch_layer_norm(const void *X, const void *scale, const void *B, void *Y, float *mean,
                               float *inv, const NormArgs &a, cudaStream_t s) {
-    const int64_t blocks = (a.rows + kNormThreads / 32 - 1) / (kNormThreads / 32);
-    layer_norm_kernel<T><<<(unsigned)blocks, kNormThreads, 0, s>>>(
-        (const T *)X, (const T *)scale, (const T *)B, (T *)Y, mean, inv, a);
-    return cudaGetLastError();
+    const T *x = (const T *)X, *g = (const T *)scale, *b = (const T *)B;
+    if (a.D > kNormOnChip) {
+        layer_norm_wide_kernel<T><<<(unsigned)a.rows, kNormThreads, 0, s>>>(x, g, b, (T *)Y, mean, inv, a);
+        return cudaGetLastError();
+    }
+    if (a.D % kVec<T> == 0 && aligned16(X) && aligned16(scale) && aligned16(B) && aligned16(Y))
+        return run_forward<T, kVec<T>>(x, g, b, (T *)Y, mean, inv, a, s);
+    return run_forward<T, 1>(x, g, b, (T *)Y, mean, inv, a, s);
 }
 
 template <typename T>
@@ -126,19 +378,27 @@ cudaError_t launch_layer_norm_backward(const void *dY, const void *X, const void
                                        const float *mean, const float *inv, void *dX, void *dScale,
                                        void *dB, float *partials, const NormArgs &a,
                                        cudaStream_t s) {
-    if (a.rows > 0) {
-        const int64_t blocks = (a.rows + kNormThreads / 32 - 1) / (kNormThreads / 32);
-        layer_norm_dx_kernel<T><<<(unsigned)blocks, kNormThreads, 0, s>>>(
-            (const T *)dY, (const T *)X, (const T *)scale, mean, inv, (T *)dX, a);
+    const T *dy = (const T *)dY, *x = (const T *)X, *g = (const T *)scale;
+    float *sums = dScale || dB ? partials : nullptr;
+    int blocks = 0;
+    cudaError_t e = cudaSuccess;
+    if (a.rows > 0 && a.D > kNormOnChip) {
+        layer_norm_wide_dx_kernel<T>
+            <<<(unsigned)a.rows, kNormThreads, 0, s>>>(dy, x, g, mean, inv, (T *)dX, a);
+        blocks = row_blocks(a.rows, kNormThreads, kWideNV);
+        if (sums)
+            layer_norm_wide_partial_kernel<T>
+                <<<dim3((a.D + 255) / 256, blocks), 256, 0, s>>>(dy, x, mean, inv, sums, a);
+        e = cudaGetLastError();
+    } else if (a.rows > 0) {
+        if (a.D % kVec<T> == 0 && aligned16(dY) && aligned16(X) && aligned16(scale) && aligned16(dX))
+            e = run_backward<T, kVec<T>>(dy, x, g, mean, inv, (T *)dX, sums, &blocks, a, s);
+        else
+            e = run_backward<T, 1>(dy, x, g, mean, inv, (T *)dX, sums, &blocks, a, s);
     }
-    if (dScale || dB) {
-        const int nb = a.rows > 0 ? layer_norm_partial_blocks(a.rows, a.D) : 0;
-        const unsigned cols = (unsigned)((a.D + 127) / 128);
-        if (nb > 0)
-            layer_norm_partial_kernel<T><<<dim3(cols, nb), 128, 0, s>>>(
-                (const T *)dY, (const T *)X, mean, inv, partials, (a.rows + nb - 1) / nb, a);
-        layer_norm_finish_kernel<T><<<cols, 128, 0, s>>>(partials, nb, (T *)dScale, (T *)dB, a.D);
-    }
+    if (e != cudaSuccess || !(dScale || dB)) return e;
+    layer_norm_finish_kernel<T>
+        <<<dim3((a.D + 31) / 32, 2), 1024, 0, s>>>(partials, blocks, (T *)dScale, (T *)dB, a.D);
     return cudaGetLastError();
 }
 
