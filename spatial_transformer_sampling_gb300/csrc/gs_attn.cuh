@@ -76,17 +76,31 @@ __global__ void attn_dbias_kernel(AttnArgs a, AttnPtrs p, const float *bias, con
 }
 
 // dtable[b][h]: a lane per bucket goes through the relative indices in order,
-// eight warps an eighth each.
+// eight warps a share each of what shared memory holds at a time.
 template <typename T>
 __global__ void __launch_bounds__(256) attn_dtable_kernel(AttnArgs a, const float *rel, T *dTable) {
+    constexpr int kHeld = 2048, kShare = kHeld / 8;
+    __shared__ __align__(16) int2 s_pair[kHeld];   // bucket, bits of the sum
     __shared__ float s_sum[8][32];
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, h = blockIdx.y;
     const int b = blockIdx.x * 32 + lane;
-    const int each = (a.R + 7) / 8, lo = warp * each, hi = min(lo + each, a.R);
     float sum = 0.0f;
+    for (int r0 = 0; r0 < a.R; r0 += kHeld) {
+        __syncthreads();
+        for (int k = threadIdx.x; k < kHeld; k += 256)
+            s_pair[k] = r0 + k < a.R ? make_int2(__ldg(a.buckets + r0 + k),
+                                                 __float_as_int(rel[(int64_t)h * a.R + r0 + k]))
+                                     : make_int2(-1, 0);
+        __syncthreads();
+        const int4 *at = reinterpret_cast<const int4 *>(s_pair + warp * kShare);
+        const int count = min(max(a.R - r0 - warp * kShare, 0), kShare);
 #pragma unroll 8
-    for (int r = lo; r < hi; ++r)
-        if (__ldg(a.buckets + r) == b) sum += rel[(int64_t)h * a.R + r];
+        for (int k = 0; k < (count + 1) / 2; ++k) {
+            const int4 v = at[k];
+            if (v.x == b) sum += __int_as_float(v.y);
+            if (v.z == b) sum += __int_as_float(v.w);
+        }
+    }
     s_sum[warp][lane] = sum;
     __syncthreads();
     if (warp == 0 && b < a.nb) {
@@ -175,13 +189,10 @@ cudaError_t launch_attn_backward(const AttnArgs &a, const AttnPtrs &p, void *ws_
     TcBwdArgs kv, q;
     bool tc = false;
     if constexpr (sizeof(T) == 2) tc = tc_backward_views<T>(a, p, kv, q);
-    const int64_t rows = (int64_t)a.N * rows64(a.Lq) * a.H;
-    auto delta_kernel = tc ? attn_delta_kernel<T, sizeof(T) == 2> : attn_delta_kernel<T, false>;
-    delta_kernel<<<(unsigned)((rows + 15) / 16), 256, 0, s>>>(a, (const T *)p.dO, (const T *)p.O, p.lse,
-                                                              lse2, delta);
     const int pairs = a.N * a.H;
     RelArgs none = {}, part = {};
-    cudaError_t e;
+    cudaError_t e = launch_attn_delta<T>(a, p, lse2, delta, s);
+    if (e != cudaSuccess) return e;
     if constexpr (sizeof(T) == 2) {
         if (tc) {
             kv.a = q.a = a;
@@ -217,7 +228,7 @@ cudaError_t launch_attn_backward(const AttnArgs &a, const AttnPtrs &p, void *ws_
         e = run(std::false_type(), part, now);
         if (e != cudaSuccess) return e;
         if (part.window)
-            attn_rel_sum_kernel<<<dim3((a.R + 127) / 128, a.H), 128, 0, s>>>(a, part, now, rel);
+            attn_rel_sum_kernel<<<dim3((a.R + 31) / 32, a.H), 512, 0, s>>>(a, part, now, rel);
     }
     if (bias) {
         if (!part.window)

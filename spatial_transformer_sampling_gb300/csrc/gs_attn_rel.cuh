@@ -109,30 +109,32 @@ struct RelWindow {
     }
 };
 
-// lse2 and delta of every query, sixteen threads per row (VEC: 16-bit types,
-// 16-byte rows).
+// lse2 and delta of every query, G lanes per row (a power of two; VEC: rows of
+// 16-byte runs, one per lane).  A block takes 256 / G rows of one batch item, in
+// memory order (token, head).
 template <typename T, bool VEC>
-__global__ void attn_delta_kernel(AttnArgs a, const T *dO, const T *O, const float *lse,
-                                  float *lse2, float *delta) {
-    const int L64 = rows64(a.Lq), part = threadIdx.x % 16;
-    const int64_t row = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / 16;   // (n, i, h)
-    if (row >= (int64_t)a.N * L64 * a.H) return;
-    const int h = (int)(row % a.H), i = (int)(row / a.H % L64), n = (int)(row / a.H / L64);
+__global__ void attn_delta_kernel(AttnArgs a, const T *dO, const T *O, const float *lse, int G,
+                                  int blocks_per_item, float *lse2, float *delta) {
+    constexpr int E = 16 / (int)sizeof(T);
+    const int L64 = rows64(a.Lq), part = threadIdx.x % G;
+    const int n = blockIdx.x / blocks_per_item;
+    const int64_t row = (int64_t)(blockIdx.x % blocks_per_item) * (256 / G) + threadIdx.x / G;
+    const int i = (int)(row / a.H), h = (int)(row - (int64_t)i * a.H);
     float s = 0.0f;
-    const int64_t at = (((int64_t)n * a.Lq + i) * a.H + h) * a.D;
-    if (!VEC) {
-        if (i < a.Lq)
-            for (int d = part; d < a.D; d += 16) s = fmaf(IO<T>::ld(dO + at + d), IO<T>::ld(O + at + d), s);
-    } else if (i < a.Lq && part * 8 < a.D) {
-        const uint4 u = __ldg(reinterpret_cast<const uint4 *>(dO + at + part * 8));
-        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(O + at + part * 8));
-        const T *x = reinterpret_cast<const T *>(&u), *y = reinterpret_cast<const T *>(&v);
+    if (i < a.Lq) {
+        const int64_t at = ((int64_t)n * a.Lq * a.H + row) * a.D;
+        if (!VEC) {
+            for (int d = part; d < a.D; d += G) s = fmaf(IO<T>::ld(dO + at + d), IO<T>::ld(O + at + d), s);
+        } else if (part * E < a.D) {
+            const uint4 u = __ldg(reinterpret_cast<const uint4 *>(dO + at + part * E));
+            const uint4 v = __ldg(reinterpret_cast<const uint4 *>(O + at + part * E));
+            const T *x = reinterpret_cast<const T *>(&u), *y = reinterpret_cast<const T *>(&v);
 #pragma unroll
-        for (int k = 0; k < 16 / (int)sizeof(T); ++k) s = fmaf(IO<T>::to_f(x[k]), IO<T>::to_f(y[k]), s);
+            for (int k = 0; k < E; ++k) s = fmaf(IO<T>::to_f(x[k]), IO<T>::to_f(y[k]), s);
+        }
     }
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (part == 0) {
+    for (int o = G / 2; o > 0; o /= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (part == 0 && i < L64) {
         const int64_t nh = (int64_t)n * a.H + h;
         const float v = i < a.Lq ? lse[nh * a.Lq + i] : -INFINITY;
         lse2[nh * L64 + i] = v == -INFINITY ? INFINITY : v * kLog2e;   // no key: weights of 0
@@ -140,32 +142,57 @@ __global__ void attn_delta_kernel(AttnArgs a, const T *dO, const T *O, const flo
     }
 }
 
-// rel[h][r] (+)= the warps' sums, query warps and batch items in a fixed order;
-// `heads` (batch, head) pairs from head0 on are in `part`.
-static __global__ void attn_rel_sum_kernel(AttnArgs a, RelArgs p, int heads, float *rel) {
-    constexpr int kThreads = 128;
-    __shared__ int s_lo[kThreads], s_hi[kThreads];   // relative indices of a warp's queries
-    const int r = blockIdx.x * kThreads + threadIdx.x, h = blockIdx.y;
+template <typename T>
+cudaError_t launch_attn_delta(const AttnArgs &a, const AttnPtrs &p, float *lse2, float *delta,
+                              cudaStream_t s) {
+    constexpr int E = 16 / (int)sizeof(T);
+    const bool vec = a.D % E == 0 && (((uintptr_t)p.dO | (uintptr_t)p.O) & 15u) == 0;
+    int G = vec ? 1 : 16;
+    while (vec && G * E < a.D) G *= 2;
+    const int64_t per_item = ((int64_t)rows64(a.Lq) * a.H * G + 255) / 256;
+    auto kernel = vec ? attn_delta_kernel<T, true> : attn_delta_kernel<T, false>;
+    kernel<<<(unsigned)(per_item * a.N), 256, 0, s>>>(a, (const T *)p.dO, (const T *)p.O, p.lse, G,
+                                                     (int)per_item, lse2, delta);
+    return cudaGetLastError();
+}
+
+// rel[h][r] (+)= the warps' sums; `heads` (batch, head) pairs from head0 on are
+// in `part`.  32 indices a block, 16 threads per index that take every 16th
+// query warp of every batch item and are joined in order.
+static __global__ void __launch_bounds__(512)
+    attn_rel_sum_kernel(AttnArgs a, RelArgs p, int heads, float *rel) {
+    constexpr int kSlices = 16, kChunk = 32 * kSlices;
+    __shared__ int s_lo[kChunk], s_hi[kChunk];   // relative indices of a warp's queries
+    __shared__ float s_sum[kSlices][32];
+    const int lane = threadIdx.x % 32, slice = threadIdx.x / 32;
+    const int r0 = blockIdx.x * 32, r = r0 + lane, h = blockIdx.y;
     const int warps = (a.Lq + 31) / 32, k_end = rel_k(a, a.Lk - 1);
-    float sum = p.head0 > 0 && r < a.R ? rel[(int64_t)h * a.R + r] : 0.0f;
-    for (int w0 = 0; w0 < warps; w0 += kThreads) {
+    float sum = 0.0f;
+    for (int w0 = 0; w0 < warps; w0 += kChunk) {
         const int mine = min(w0 + (int)threadIdx.x, warps - 1);
         __syncthreads();
         s_lo[threadIdx.x] = rel_q(a, mine * 32);
         s_hi[threadIdx.x] = rel_q(a, min(mine * 32 + 31, a.Lq - 1));
         __syncthreads();
-        const int count = min(kThreads, warps - w0);
+        const int count = min(kChunk, warps - w0);
         for (int nh = p.head0 + (h - p.head0 % a.H + a.H) % a.H; nh < p.head0 + heads; nh += a.H) {
             const int keys = keys_of(a, nh / a.H);
-            const int low = keys > 0 ? rel_k(a, keys - 1) : -1;   // of r below the queries' lowest
+            if (keys == 0) continue;
+            const int low = rel_k(a, keys - 1);   // how far r reaches below the queries' lowest
             const float *at = p.part + ((int64_t)(nh - p.head0) * warps + w0) * p.stride + r + k_end;
-#pragma unroll 8
-            for (int w = 0; w < count; ++w)
-                if (keys > 0 && r <= s_hi[w] && r >= s_lo[w] - low)
+#pragma unroll 4
+            for (int w = slice; w < count; w += kSlices)
+                if (r <= s_hi[w] && r >= s_lo[w] - low)
                     sum += __ldg(at + (int64_t)w * p.stride - s_lo[w]);
         }
     }
-    if (r < a.R) rel[(int64_t)h * a.R + r] = sum;
+    s_sum[slice][lane] = sum;
+    __syncthreads();
+    if (slice == 0 && r < a.R) {
+        for (int k = 1; k < kSlices; ++k) sum += s_sum[k][lane];
+        float *out = rel + (int64_t)h * a.R + r;
+        *out = p.head0 > 0 ? *out + sum : sum;
+    }
 }
 
 // Relative indices between the first and the last of `tokens` consecutive
