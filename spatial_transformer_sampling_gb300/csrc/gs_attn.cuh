@@ -24,14 +24,15 @@
 namespace gs {
 namespace {
 
-// bias[h][r] for every relative index, in base-2 units.
+// bias[h][pad + r] for every relative index, in base-2 units, and zeros around.
 template <typename T>
-__global__ void attn_bias_kernel(const T *table, AttnArgs a, float *bias) {
-    const int r = blockIdx.x * blockDim.x + threadIdx.x;
-    if (r >= a.R) return;
-    const int b = __ldg(a.buckets + r);
+__global__ void attn_bias_kernel(const T *table, AttnArgs a, int pad, float *bias) {
+    const int at = blockIdx.x * blockDim.x + threadIdx.x, r = at - pad;
+    if (at >= a.bias_stride) return;
+    const int b = r >= 0 && r < a.R ? __ldg(a.buckets + r) : 0;
     for (int h = blockIdx.y; h < a.H; h += gridDim.y)
-        bias[(int64_t)h * a.R + r] = bias2_of(table, b, a.nb, a.H, h);
+        bias[(int64_t)h * a.bias_stride + at] =
+            r >= 0 && r < a.R ? bias2_of(table, b, a.nb, a.H, h) : 0.0f;
 }
 
 // Sum of ds over the batch and the pairs of one relative index, one warp per
@@ -44,7 +45,7 @@ __global__ void attn_dbias_kernel(AttnArgs a, AttnPtrs p, const float *bias, con
     if (w >= (int64_t)a.H * a.R) return;
     const int r = (int)(w % a.R), h = (int)(w / a.R);
     const int dy = r / a.P - (a.Hk - 1), dx = r % a.P - (a.Wk - 1);
-    const float b = __ldg(bias + w);
+    const float b = __ldg(bias + (int64_t)h * a.bias_stride + r);
     float sum = 0.0f;
     for (int n = 0; n < a.N && b != -INFINITY; ++n) {
         const int keys = keys_of(a, n);
@@ -111,6 +112,9 @@ __global__ void __launch_bounds__(256) attn_dtable_kernel(AttnArgs a, const floa
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
+// Floats per head of the expanded bias.
+int bias_stride(const AttnArgs &a) { return (a.R + 3) / 4 * 4 + 2 * tc_bias_pad(a); }
+
 // The workspace's parts, in order; offsets in bytes.
 struct Workspace {
     size_t bias, rel, lse2, delta, part, end;
@@ -119,7 +123,7 @@ Workspace workspace_of(const AttnArgs &a, bool backward) {
     Workspace w = {};
     if (!backward && few_takes(a)) return w;
     const size_t per_rel = a.nb ? round256((size_t)a.H * a.R * sizeof(float)) : 0;
-    w.rel = w.end = w.bias + per_rel;
+    w.rel = w.end = a.nb ? round256((size_t)a.H * bias_stride(a) * sizeof(float)) : 0;
     if (!backward) return w;
     const size_t per_row = round256((size_t)a.N * a.H * rows64(a.Lq) * sizeof(float));
     w.lse2 = w.rel + per_rel;
@@ -131,13 +135,16 @@ Workspace workspace_of(const AttnArgs &a, bool backward) {
     return w;
 }
 
+// Fills the expanded bias; returns the entry of relative index 0 of head 0.
 template <typename T>
-const float *expand_bias(const AttnArgs &a, const AttnPtrs &p, char *ws, cudaStream_t s) {
+const float *expand_bias(AttnArgs &a, const AttnPtrs &p, char *ws, cudaStream_t s) {
     if (a.nb == 0) return nullptr;
     float *bias = (float *)(ws + workspace_of(a, false).bias);
-    attn_bias_kernel<T><<<dim3((a.R + 255) / 256, a.H < 65535 ? a.H : 65535), 256, 0, s>>>(
-        (const T *)p.table, a, bias);
-    return bias;
+    const int pad = tc_bias_pad(a);
+    a.bias_stride = bias_stride(a);
+    attn_bias_kernel<T><<<dim3((a.bias_stride + 255) / 256, a.H), 256, 0, s>>>((const T *)p.table, a,
+                                                                              pad, bias);
+    return bias + pad;
 }
 
 // Tensor-core views of the backward pass (16-bit types); false when its kernels
@@ -168,7 +175,8 @@ size_t attn_ws_bytes(const AttnArgs &a, bool backward) {
 }
 
 template <typename T>
-cudaError_t launch_attn(const AttnArgs &a, const AttnPtrs &p, void *ws, cudaStream_t s) {
+cudaError_t launch_attn(const AttnArgs &args, const AttnPtrs &p, void *ws, cudaStream_t s) {
+    AttnArgs a = args;
     if (few_takes(a)) return launch_attn_few<T>(a, p, s);
     const float *bias = expand_bias<T>(a, p, (char *)ws, s);
     if constexpr (sizeof(T) == 2) {
@@ -180,7 +188,8 @@ cudaError_t launch_attn(const AttnArgs &a, const AttnPtrs &p, void *ws, cudaStre
 }
 
 template <typename T>
-cudaError_t launch_attn_backward(const AttnArgs &a, const AttnPtrs &p, void *ws_, cudaStream_t s) {
+cudaError_t launch_attn_backward(const AttnArgs &args, const AttnPtrs &p, void *ws_, cudaStream_t s) {
+    AttnArgs a = args;
     char *ws = (char *)ws_;
     const Workspace w = workspace_of(a, true);
     const float *bias = expand_bias<T>(a, p, ws, s);
@@ -196,7 +205,10 @@ cudaError_t launch_attn_backward(const AttnArgs &a, const AttnPtrs &p, void *ws_
     if constexpr (sizeof(T) == 2) {
         if (tc) {
             kv.a = q.a = a;
-            kv.bias = q.bias = bias;
+            kv.bias = tc_bias_of(a, true);
+            q.bias = tc_bias_of(a, false);
+            kv.bias.base = q.bias.base = bias;
+            kv.bias.stride = q.bias.stride = a.bias_stride;
             kv.lse2 = q.lse2 = lse2;
             kv.delta = q.delta = delta;
             kv.out1 = p.dK;

@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(kSimtThreads)
     const float c2 = a.scale * kLog2e;
     const SimtView<T> Q(p.Q, a.qs, n, h), K(p.K, a.ks, n, h), V(p.V, a.vs, n, h);
     const int keys = keys_of(a, n);
-    if (bias) bias += (int64_t)h * a.R;
+    if (bias) bias += (int64_t)h * a.bias_stride;
 
     simt_load_t(qt, Q, i0, a.Lq - i0, D);
     float2 o[NC][4][2] = {};
@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(kSimtThreads)
     const int cols = i0 < live_rows ? (DKV ? a.Lq : keys) : 0;
     lse2 += (int64_t)nh * rows64(a.Lq);
     delta += (int64_t)nh * rows64(a.Lq);
-    if (bias) bias += (int64_t)h * a.R;
+    if (bias) bias += (int64_t)h * a.bias_stride;
 
     simt_load_t(r1, R1, i0, live_rows - i0, D);
     simt_load_t(r2, R2, i0, live_rows - i0, D);

@@ -10,6 +10,10 @@
 // transposed in memory.
 #pragma once
 
+#include <limits.h>
+
+#include <type_traits>
+
 #include "gs_attn_rel.cuh"
 #include "gs_ptx.cuh"
 #include "gs_tma.cuh"
@@ -192,57 +196,95 @@ __device__ __forceinline__ void tc_clear_rows(unsigned char *tile, int from) {
     __syncwarp();
 }
 
-// The bias of one row of scores against 64 consecutive columns, of which the
-// first `live` count: f(c, bias) for those, dead(c) for the rest.  Column c sits
-// at `row[-rel(c)]` (SIGN = -1: this thread holds a query, columns are keys) or
-// `row[rel(c)]` (SIGN = +1: a key against queries); rel grows by one per token
-// and by `P - W` more at the end of a grid row.  `x` and `rel` belong to the
-// first column, for which x = token % W.
-template <int SIGN, typename F, typename G>
-__device__ __forceinline__ void for_each_bias(const float *row, int x, int rel, int W, int P,
-                                              int live, F &&f, G &&dead) {
+// How a kernel reads the expanded bias: 0 none, 1 a window of it that is copied
+// to shared memory with every column tile, 2 global memory.
+enum { kBiasNone = 0, kBiasWindow = 1, kBiasGlobal = 2 };
+
+// The window of a column tile: the relative indices of 128 rows against 64
+// columns are contiguous, `count` floats from `lowest` (rounded down to 16
+// bytes) on, so one bulk copy brings them.  The columns of a one-row grid, or
+// of one whose rows are multiples of eight tokens, sit at consecutive indices
+// eight at a time (`runs`).
+struct TcBias {
+    const float *base;   // entry of relative index 0 of head 0; `pad` floats before and after
+    int stride;          // floats per head
+    int count;           // floats of a window, a multiple of 4
+    int below;           // relative indices from the first row and column down to the lowest
+    int runs;
+};
+constexpr int kBiasMost = 2560;   // floats of the largest window that is copied (10 KB)
+
+// First float of the window whose first row and column meet at index r.
+__device__ __forceinline__ int bias_start(const TcBias &b, int r) {
+    return (r - b.below) & ~3;   // rounds down below zero too
+}
+
+// Relative offset of 64 consecutive columns from the first one on their grid
+// (rows of W, a new row costs P - W more), into a warp's 64 ints; columns from
+// `live` on repeat the last live one.
+__device__ __forceinline__ void bias_offsets(int *rel, int first, int live, int W, int P) {
+    const int lane = threadIdx.x % 32, y0 = first / W;
+    __syncwarp();
 #pragma unroll
-    for (int c = 0; c < kTcN; c += 8) {
-        if (x + 8 <= W && c + 8 <= live) {   // a run inside one grid row: immediate offsets
-            const float *at = row + SIGN * rel;
+    for (int k = 0; k < kTcN; k += 32) {
+        const int c = min(k + lane, live - 1), y = (first + c) / W;
+        rel[k + lane] = c + (y - y0) * (P - W);
+    }
+    __syncwarp();
+}
+
+// f(c, b) for columns c = C0 .. C0 + 31: b[c] and b[c + 1] of a row of the bias.
+// Column c sits SIGN * (its offset) from `row` (SIGN -1: the thread holds a
+// query, columns are keys; +1: a key against queries).
+template <int SIGN, int C0, typename F>
+__device__ __forceinline__ void bias_by_runs(const float *row, int &x, int &rel, int W, int wrap,
+                                             F &&f) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) f(c + k, at[SIGN * k]);
-            rel += 8;
-            x += 8;
-            if (x == W) {
-                x = 0;
-                rel += P - W;
-            }
-        } else {
+    for (int c = C0; c < C0 + 32; c += 8) {
+        const float *at = row + SIGN * rel;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                if (c + k < live)
-                    f(c + k, row[SIGN * rel]);
-                else
-                    dead(c + k);
-                ++rel;
-                if (++x == W) {
-                    x = 0;
-                    rel += P - W;
-                }
-            }
-        }
+        for (int k = 0; k < 8; k += 2) f(c + k, make_float2(at[SIGN * k], at[SIGN * (k + 1)]));
+        x += 8;
+        rel += 8 + (x == W ? wrap : 0);
+        x = x == W ? 0 : x;
+    }
+}
+template <int SIGN, int C0, typename F>
+__device__ __forceinline__ void bias_by_table(const float *row, const int *rel, F &&f) {
+#pragma unroll
+    for (int c = C0; c < C0 + 32; c += 4) {
+        const int4 o = *reinterpret_cast<const int4 *>(rel + c);
+        f(c, make_float2(row[SIGN * o.x], row[SIGN * o.y]));
+        f(c + 2, make_float2(row[SIGN * o.z], row[SIGN * o.w]));
     }
 }
 
-// Floats of the largest bias window of a CTA: 128 tokens of one grid (queries,
-// or keys with `by_key`) against all of the other.
-inline int64_t tc_bias_window(const AttnArgs &a, bool by_key) {
-    const int64_t q = by_key ? (int64_t)(a.Hq - 1) * a.P + a.Wq - 1
-                             : rel_span(kTcM, a.Lq, a.Hq, a.Wq, a.P);
-    const int64_t k = by_key ? rel_span(kTcM, a.Lk, a.Hk, a.Wk, a.P)
-                             : (int64_t)(a.Hk - 1) * a.P + a.Wk - 1;
-    return std::min<int64_t>(q + k + 1, a.R);
+// Indices that 64 columns of a grid may span when they are counted past its
+// last token as well.
+inline int64_t bias_column_span(int rows, int W, int P) {
+    return kTcN - 1 + (rows == 1 ? 0 : ((kTcN - 2) / W + 1) * (int64_t)(P - W));
 }
 
-// Dynamic shared memory that lets two CTAs share an SM (227 KB, 1 KB of it
-// kept back per CTA, and the kernels' barriers), and the most for one.
-constexpr int kTcSmemTwo = 227 * 1024 / 2 - 1024 - 256;
-constexpr int kTcSmemOne = 227 * 1024 - 256;
+// Window of the kernels whose rows are queries, or keys (`by_key`); count 0
+// when it is larger than kBiasMost.
+inline TcBias tc_bias_of(const AttnArgs &a, bool by_key) {
+    TcBias b = {};
+    const int64_t rows = by_key ? rel_span(kTcM, a.Lk, a.Hk, a.Wk, a.P)
+                                : rel_span(kTcM, a.Lq, a.Hq, a.Wq, a.P);
+    const int64_t cols = by_key ? bias_column_span(a.Hq, a.Wq, a.P) : bias_column_span(a.Hk, a.Wk, a.P);
+    const int64_t count = (rows + cols + 1 + 3 + 3) / 4 * 4;
+    b.below = (int)std::min<int64_t>(by_key ? rows : cols, kBiasMost);
+    b.count = count <= kBiasMost ? (int)count : 0;
+    b.runs = by_key ? a.Hq == 1 || a.Wq % 8 == 0 : a.Hk == 1 || a.Wk % 8 == 0;
+    return b;
+}
+// Floats kept on both sides of a head's bias: windows reach past its ends.
+inline int tc_bias_pad(const AttnArgs &a) {
+    return (std::max(tc_bias_of(a, false).count, tc_bias_of(a, true).count) + 8 + 3) / 4 * 4;
+}
+
+// Dynamic shared memory of one CTA per SM, at most (barriers and offsets take
+// up to 1.25 KB of the 227).
+constexpr int kTcSmemOne = 227 * 1024 - 1280;
 
 }  // namespace gs

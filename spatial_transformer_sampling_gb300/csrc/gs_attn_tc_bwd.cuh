@@ -24,8 +24,7 @@ namespace gs {
 struct TcBwdArgs {
     AttnArgs a;
     TcView r1, r2, c1, c2;
-    const float *bias;        // expanded (H, R), or nullptr
-    int bias_window;          // floats of shared memory for the bias (0: read global memory)
+    TcBias bias;
     const float *lse2;        // (N, H, rows64(Lq)): lse * log2(e), +inf where nothing counts
     const float *delta;       // same shape: dO . O
     void *out1, *out2;        // dK, dV or dQ
@@ -49,7 +48,7 @@ template <int DP, bool DKV> struct TcBwdShape {
 template <typename T> constexpr float kWeightScale = 1.0f;
 template <> constexpr float kWeightScale<__half> = 4096.0f;
 
-template <typename T, int DP, bool BIAS, bool DKV>
+template <typename T, int DP, int BIAS, bool DKV>
 __global__ void __launch_bounds__(kTcThreads, TcBwdShape<DP, DKV>::kCtas)
     attn_tc_bwd_kernel(const __grid_constant__ TcBwdArgs p) {
     using Sh = TcBwdShape<DP, DKV>;
@@ -65,7 +64,8 @@ __global__ void __launch_bounds__(kTcThreads, TcBwdShape<DP, DKV>::kCtas)
                   *sC2 = sC1 + NS * Sh::kTileBytes;
     float *sVec = reinterpret_cast<float *>(tiles + Sh::kTileSmem);
     float *sRel = sVec + NS * Sh::kVecBytes / 4;
-    float *sBias = sRel + rel_smem(p.rel.window, 4) / 4;
+    float *sBias = sRel + rel_smem(p.rel.window, 4) / 4;   // a window per stage
+    __shared__ __align__(16) int s_rel[4][kTcN];
 
     const int rows = DKV ? a.Lk : a.Lq;
     const int row_tiles = (rows + kTcM - 1) / kTcM;
@@ -79,6 +79,12 @@ __global__ void __launch_bounds__(kTcThreads, TcBwdShape<DP, DKV>::kCtas)
     const int steps = (cols + kTcN - 1) / kTcN;
     const float *lse2 = p.lse2 + (int64_t)nh * rows64(a.Lq);
     const float *delta = p.delta + (int64_t)nh * rows64(a.Lq);
+
+    // entry of relative index 0, the first row's part of it, and the index at
+    // which the first row meets column `col`
+    const float *bias = BIAS ? p.bias.base + (int64_t)h * p.bias.stride : nullptr;
+    const int row0 = DKV ? -rel_k(a, i0) : rel_q(a, i0);
+    const auto meet = [&](int col) { return row0 + (DKV ? rel_q(a, col) : -rel_k(a, col)); };
 
     if (warp == 4) {
         if (lane == 0) {
@@ -96,20 +102,6 @@ __global__ void __launch_bounds__(kTcThreads, TcBwdShape<DP, DKV>::kCtas)
         tmem_alloc(&tmem_base, Sh::kTmemCols);
         tcgen05_fence_before_sync();
     }
-    // the window of relative indices that this CTA's pairs fall into
-    const float *bias = nullptr;
-    int rel_base = 0;
-    if (BIAS && steps > 0) {
-        bias = p.bias + (int64_t)h * a.R;
-        if (p.bias_window) {
-            const int last = min(i0 + kTcM, live_rows) - 1;
-            rel_base = DKV ? rel_q(a, 0) - rel_k(a, last) : rel_q(a, i0) - rel_k(a, keys - 1);
-            const int end = DKV ? rel_q(a, a.Lq - 1) - rel_k(a, i0) : rel_q(a, last);
-            for (int r = threadIdx.x; r <= end - rel_base; r += kTcThreads)
-                sBias[r] = __ldg(bias + rel_base + r);
-            bias = sBias;
-        }
-    }
     __syncthreads();
     tcgen05_fence_after_sync();
     const uint32_t tmem = tmem_base;
@@ -124,9 +116,13 @@ __global__ void __launch_bounds__(kTcThreads, TcBwdShape<DP, DKV>::kCtas)
         const uint32_t c1_at = smem_u32(sC1), c2_at = smem_u32(sC2);
         const auto load = [&](int t) {   // one lane
             const int s = t % NS;
-            mbar_arrive_expect_tx(&c_full[s], 2 * Sh::kTileBytes + Sh::kVecBytes);
+            mbar_arrive_expect_tx(&c_full[s], 2 * Sh::kTileBytes + Sh::kVecBytes +
+                                                  (BIAS == kBiasWindow ? p.bias.count * 4 : 0));
             tc_load<DP, kTcN>(sC1 + s * Sh::kTileBytes, p.c1, n, h, t * kTcN, &c_full[s]);
             tc_load<DP, kTcN>(sC2 + s * Sh::kTileBytes, p.c2, n, h, t * kTcN, &c_full[s]);
+            if (BIAS == kBiasWindow)
+                bulk_copy_g2s(sBias + s * p.bias.count, bias + bias_start(p.bias, meet(t * kTcN)),
+                              p.bias.count * 4, &c_full[s]);
             if (DKV) {
                 bulk_copy_g2s(sVec + s * 2 * kTcN, lse2 + t * kTcN, kTcN * 4, &c_full[s]);
                 bulk_copy_g2s(sVec + s * 2 * kTcN + kTcN, delta + t * kTcN, kTcN * 4, &c_full[s]);
@@ -209,8 +205,7 @@ __global__ void __launch_bounds__(kTcThreads, TcBwdShape<DP, DKV>::kCtas)
         const uint32_t my_tmem = (uint32_t)(warp * 32) << 16;   // this warp's TMEM lanes
         const int i = i0 + threadIdx.x, ic = min(i, live_rows - 1);
         const float c2 = a.scale * kLog2e;
-        const float *row = nullptr;
-        if (BIAS && steps > 0) row = DKV ? bias - rel_k(a, ic) - rel_base : bias + rel_q(a, ic) - rel_base;
+        const int my_row = !BIAS || steps == 0 ? 0 : DKV ? -rel_k(a, ic) : rel_q(a, ic);
         const bool counts = i < live_rows && steps > 0;
         const float row_lse = !DKV ? (counts ? lse2[i] : INFINITY) : 0.0f;
         const float row_delta = !DKV && counts ? delta[i] : 0.0f;
@@ -226,34 +221,53 @@ __global__ void __launch_bounds__(kTcThreads, TcBwdShape<DP, DKV>::kCtas)
             ok = mbar_wait_bounded(&s_full, t & 1, a.err);
             if (__any_sync(0xffffffffu, !ok)) break;
             tcgen05_fence_after_sync();
-            tmem_ld_x32<0>(tmem + Sh::kTmemS + my_tmem, r);
-            tmem_ld_x32<32>(tmem + Sh::kTmemS + my_tmem + 32, r);
-            tmem_wait_ld<0>(r);
-            tmem_wait_ld<32>(r);
-            tcgen05_fence_before_sync();
-            mbar_arrive(&s_free);
-            if (DKV) {   // lse2 and delta of the columns came with the tile
+            const uint32_t ts = tmem + Sh::kTmemS + my_tmem;
+            tmem_ld_x32<0>(ts, r);
+            tmem_ld_x32<32>(ts + 32, r);
+            if (DKV || BIAS == kBiasWindow) {   // the vectors and the bias came with the tile
                 ok = mbar_wait_bounded(&c_full[t % NS], (t / NS) & 1, a.err);
                 if (__any_sync(0xffffffffu, !ok)) break;
             }
             const float *vec = sVec + t % NS * 2 * kTcN;
-            const auto score = [&](int c, float b) {
-                r[c] = __float_as_uint(fmaf(__uint_as_float(r[c]), c2, b));
-            };
-            const auto dead = [&](int c) { r[c] = __float_as_uint(-INFINITY); };
+            const float *row = nullptr;   // the bias of this row and the tile's first column
+            int x = 0, rel = 0;
+            const int W = DKV ? a.Wq : a.Wk, grid_rows = DKV ? a.Hq : a.Hk;
             if (BIAS) {
-                const int W = DKV ? a.Wq : a.Wk, y = t * kTcN / W, x = t * kTcN - y * W;
-                if (DKV)
-                    for_each_bias<+1>(row, x, rel_q(a, t * kTcN), W, a.P, live, score, dead);
+                const int at = meet(t * kTcN);
+                x = t * kTcN % W;
+                if (BIAS == kBiasWindow)
+                    row = sBias + t % NS * p.bias.count + (at - row0 + my_row - bias_start(p.bias, at));
                 else
-                    for_each_bias<-1>(row, x, y * a.P + x, W, a.P, live, score, dead);
+                    row = bias + at - row0 + my_row;
+                if (BIAS == kBiasGlobal || !p.bias.runs) bias_offsets(s_rel[warp], t * kTcN, live, W, a.P);
+            }
+            tmem_wait_ld<0>(r);
+            tmem_wait_ld<32>(r);
+            tcgen05_fence_before_sync();
+            mbar_arrive(&s_free);
+            const float2 cc = make_float2(c2, c2);
+            const auto score = [&](int c, float2 b) {
+                const float2 v = fma_f32x2(
+                    make_float2(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), cc, b);
+                r[c] = __float_as_uint(v.x);
+                r[c + 1] = __float_as_uint(v.y);
+            };
+            constexpr int kSign = DKV ? 1 : -1;
+            if (!BIAS) {
+#pragma unroll
+                for (int c = 0; c < kTcN; c += 2) score(c, make_float2(0.0f, 0.0f));
+            } else if (BIAS == kBiasWindow && p.bias.runs) {
+                const int w = grid_rows == 1 ? INT_MAX : W;
+                bias_by_runs<kSign, 0>(row, x, rel, w, a.P - W, score);
+                bias_by_runs<kSign, 32>(row, x, rel, w, a.P - W, score);
             } else {
+                bias_by_table<kSign, 0>(row, s_rel[warp], score);
+                bias_by_table<kSign, 32>(row, s_rel[warp], score);
+            }
+            if (live < kTcN) {   // columns that do not count, whatever they hold
 #pragma unroll
                 for (int c = 0; c < kTcN; ++c)
-                    if (c < live)
-                        score(c, 0.0f);
-                    else
-                        dead(c);
+                    if (c >= live) r[c] = __float_as_uint(-INFINITY);
             }
             if (DKV) {
 #pragma unroll
@@ -346,32 +360,32 @@ __global__ void __launch_bounds__(kTcThreads, TcBwdShape<DP, DKV>::kCtas)
     if (warp == 4) tmem_dealloc(tmem, Sh::kTmemCols);
 }
 
-template <typename T, int DP, bool BIAS, bool DKV>
-cudaError_t launch_attn_tc_bwd_as(TcBwdArgs &p, int heads, cudaStream_t s) {
+template <typename T, int DP, int BIAS, bool DKV>
+cudaError_t launch_attn_tc_bwd_as(const TcBwdArgs &p, int heads, cudaStream_t s) {
     using Sh = TcBwdShape<DP, DKV>;
     auto kernel = attn_tc_bwd_kernel<T, DP, BIAS, DKV>;
     static DeviceFlags ready;
-    cudaError_t e = once_per_device(ready, [&] {
+    const cudaError_t e = once_per_device(ready, [&] {
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmemOne);
     });
     if (e != cudaSuccess) return e;
-    const int base = Sh::kSmem + rel_smem(p.rel.window, 4);
-    const int64_t window = BIAS ? tc_bias_window(p.a, DKV) : 0;
-    const int limit = base <= kTcSmemTwo ? kTcSmemTwo : kTcSmemOne;
-    p.bias_window = base + window * 4 <= limit ? (int)window : 0;
+    const int window = BIAS == kBiasWindow ? Sh::kStages * p.bias.count * 4 : 0;
     const int rows = DKV ? p.a.Lk : p.a.Lq;
     const int64_t blocks = (int64_t)((rows + kTcM - 1) / kTcM) * heads;
-    kernel<<<(unsigned)blocks, kTcThreads, base + p.bias_window * 4, s>>>(p);
+    kernel<<<(unsigned)blocks, kTcThreads, Sh::kSmem + rel_smem(p.rel.window, 4) + window, s>>>(p);
     return cudaGetLastError();
 }
 
 template <typename T, bool DKV>
-cudaError_t launch_attn_tc_bwd_kernel(TcBwdArgs &p, int heads, cudaStream_t s) {
-    if (p.a.D <= 64)
-        return p.bias ? launch_attn_tc_bwd_as<T, 64, true, DKV>(p, heads, s)
-                      : launch_attn_tc_bwd_as<T, 64, false, DKV>(p, heads, s);
-    return p.bias ? launch_attn_tc_bwd_as<T, 128, true, DKV>(p, heads, s)
-                  : launch_attn_tc_bwd_as<T, 128, false, DKV>(p, heads, s);
+cudaError_t launch_attn_tc_bwd_kernel(const TcBwdArgs &p, int heads, cudaStream_t s) {
+    const int mode = !p.bias.base ? kBiasNone : p.bias.count ? kBiasWindow : kBiasGlobal;
+    const auto run = [&](auto dp) {
+        constexpr int DP = decltype(dp)::value;
+        return mode == kBiasNone     ? launch_attn_tc_bwd_as<T, DP, kBiasNone, DKV>(p, heads, s)
+               : mode == kBiasWindow ? launch_attn_tc_bwd_as<T, DP, kBiasWindow, DKV>(p, heads, s)
+                                     : launch_attn_tc_bwd_as<T, DP, kBiasGlobal, DKV>(p, heads, s);
+    };
+    return p.a.D <= 64 ? run(std::integral_constant<int, 64>()) : run(std::integral_constant<int, 128>());
 }
 
 }  // namespace gs

@@ -14,9 +14,7 @@
 // division cancels m; weights stay below 2^8, inside both 16-bit types).  The
 // row sum is kept in fp32 from the unrounded weights.
 //
-// The bias of the CTA's rows is a window of the expanded bias, contiguous in
-// the relative index: it is copied to shared memory once (`bias_window` floats)
-// when it fits beside the tiles of two CTAs per SM, else read through L1.
+// The bias of a tile comes to shared memory with the keys (TcBias).
 #pragma once
 
 #include "gs_attn_tc.cuh"
@@ -26,8 +24,7 @@ namespace gs {
 struct TcFwdArgs {
     AttnArgs a;
     TcView q, k, v;
-    const float *bias;   // expanded (H, R), or nullptr
-    int bias_window;     // floats of shared memory for the bias (0: read global memory)
+    TcBias bias;
     void *O;
     float *lse;
 };
@@ -49,7 +46,7 @@ template <int DP> struct TcFwdShape {
     static constexpr int kTmemO = 2 * kTcN;
 };
 
-template <typename T, int DP, bool BIAS>
+template <typename T, int DP, int BIAS>
 __global__ void __launch_bounds__(kTcThreads, 2)
     attn_tc_fwd_kernel(const __grid_constant__ TcFwdArgs p) {
     using Sh = TcFwdShape<DP>;
@@ -62,12 +59,16 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     const AttnArgs &a = p.a;
     unsigned char *tiles = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     unsigned char *sQ = tiles, *sK = tiles + Sh::kQBytes, *sV = sK + NS * Sh::kTileBytes;
-    float *sBias = reinterpret_cast<float *>(tiles + Sh::kTileSmem);
+    float *sBias = reinterpret_cast<float *>(tiles + Sh::kTileSmem);   // a window per stage
+    __shared__ __align__(16) int s_rel[4][kTcN];
 
     const int q_tiles = (a.Lq + kTcM - 1) / kTcM;
     const int i0 = (int)(blockIdx.x % q_tiles) * kTcM;
     const int h = (int)(blockIdx.x / q_tiles % a.H), n = (int)(blockIdx.x / q_tiles / a.H);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    // entry of relative index 0, and the first query's index
+    const float *bias = BIAS ? p.bias.base + (int64_t)h * p.bias.stride : nullptr;
+    const int rq0 = rel_q(a, i0);
     const int keys = keys_of(a, n), T_tiles = (keys + kTcN - 1) / kTcN;
 
     if (warp == 4) {
@@ -89,19 +90,6 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         tmem_alloc(&tmem_base, Sh::kTmemCols);
         tcgen05_fence_before_sync();
     }
-    // the window of relative indices that this CTA's pairs fall into
-    const int i_last = min(i0 + kTcM, a.Lq) - 1;
-    const float *bias = nullptr;
-    int rel_base = 0;
-    if (BIAS && keys > 0) {
-        bias = p.bias + (int64_t)h * a.R;
-        if (p.bias_window) {
-            rel_base = rel_q(a, i0) - rel_k(a, keys - 1);
-            const int count = rel_q(a, i_last) - rel_base + 1;
-            for (int r = threadIdx.x; r < count; r += kTcThreads) sBias[r] = __ldg(bias + rel_base + r);
-            bias = sBias;
-        }
-    }
     __syncthreads();
     tcgen05_fence_after_sync();
     const uint32_t tmem = tmem_base, tmem_o = tmem + Sh::kTmemO;
@@ -115,8 +103,11 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         const uint32_t q_at = smem_u32(sQ), k_at = smem_u32(sK), v_at = smem_u32(sV);
         const auto load = [&](int t) {   // one lane
             const int s = t % NS;
-            mbar_arrive_expect_tx(&k_full[s], Sh::kTileBytes);
+            mbar_arrive_expect_tx(&k_full[s], Sh::kTileBytes + (BIAS == kBiasWindow ? p.bias.count * 4 : 0));
             tc_load<DP, kTcN>(sK + s * Sh::kTileBytes, p.k, n, h, t * kTcN, &k_full[s]);
+            if (BIAS == kBiasWindow)
+                bulk_copy_g2s(sBias + s * p.bias.count, bias + bias_start(p.bias, rq0 - rel_k(a, t * kTcN)),
+                              p.bias.count * 4, &k_full[s]);
             mbar_arrive_expect_tx(&v_full[s], Sh::kTileBytes);
             tc_load<DP, kTcN>(sV + s * Sh::kTileBytes, p.v, n, h, t * kTcN, &v_full[s]);
         };
@@ -183,7 +174,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         const uint32_t my_tmem = (uint32_t)(warp * 32) << 16;   // this warp's TMEM lanes
         const int i = i0 + threadIdx.x;
         const float c2 = a.scale * kLog2e;
-        const float *row = BIAS && keys > 0 ? bias + (rel_q(a, min(i, a.Lq - 1)) - rel_base) : nullptr;
+        const int rq = BIAS ? rel_q(a, min(i, a.Lq - 1)) : 0;
         float m = -INFINITY, l = 0.0f;
         for (int j = 0; j < T_tiles; ++j) {
             const int live = keys - j * kTcN;
@@ -193,25 +184,55 @@ __global__ void __launch_bounds__(kTcThreads, 2)
             tcgen05_fence_after_sync();
             const uint32_t ts = tmem + my_tmem + (j & 1) * kTcN;
             tmem_ld_x32<0>(ts, r);
-            tmem_ld_x32<32>(ts + 32, r);
-            tmem_wait_ld<0>(r);
-            tmem_wait_ld<32>(r);
+            const float *row = nullptr;   // the bias of this query and the tile's first key
+            int x = 0, rel = 0;
             if (BIAS) {
-                const int y = j * kTcN / a.Wk, x = j * kTcN - y * a.Wk;
-                for_each_bias<-1>(
-                    row, x, y * a.P + x, a.Wk, a.P, live,
-                    [&](int c, float b) {
-                        r[c] = __float_as_uint(fmaf(__uint_as_float(r[c]), c2, b));
-                    },
-                    [&](int c) { r[c] = __float_as_uint(-INFINITY); });
-            } else {
-#pragma unroll
-                for (int c = 0; c < kTcN; ++c)
-                    r[c] = __float_as_uint(c < live ? __uint_as_float(r[c]) * c2 : -INFINITY);
+                const int rk = rel_k(a, j * kTcN);
+                x = j * kTcN % a.Wk;
+                if (BIAS == kBiasWindow) {
+                    ok = mbar_wait_bounded(&k_full[j % NS], (j / NS) & 1, a.err);
+                    if (__any_sync(0xffffffffu, !ok)) break;
+                    row = sBias + j % NS * p.bias.count + (rq - rk - bias_start(p.bias, rq0 - rk));
+                } else {
+                    row = bias + rq - rk;
+                }
+                if (BIAS == kBiasGlobal || !p.bias.runs) bias_offsets(s_rel[warp], j * kTcN, live, a.Wk, a.P);
             }
-            float top = m;
+            const int W = a.Hk == 1 ? INT_MAX : a.Wk;
+            float top4[4] = {m, -INFINITY, -INFINITY, -INFINITY};
+            const float2 cc = make_float2(c2, c2);
+            const auto score = [&](int c, float2 b) {
+                const float2 v = fma_f32x2(
+                    make_float2(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), cc, b);
+                r[c] = __float_as_uint(v.x);
+                r[c + 1] = __float_as_uint(v.y);
+            };
+            const auto half = [&](auto first) {
+                constexpr int C0 = decltype(first)::value;
+                if (!BIAS) {
 #pragma unroll
-            for (int c = 0; c < kTcN; ++c) top = fmaxf(top, __uint_as_float(r[c]));
+                    for (int c = C0; c < C0 + 32; c += 2) score(c, make_float2(0.0f, 0.0f));
+                } else if (BIAS == kBiasWindow && p.bias.runs) {
+                    bias_by_runs<-1, C0>(row, x, rel, W, a.P - a.Wk, score);
+                } else {
+                    bias_by_table<-1, C0>(row, s_rel[warp], score);
+                }
+                if (live < kTcN) {   // masked keys, whatever they hold
+#pragma unroll
+                    for (int c = C0; c < C0 + 32; ++c)
+                        if (c >= live) r[c] = __float_as_uint(-INFINITY);
+                }
+#pragma unroll
+                for (int c = C0; c < C0 + 32; c += 2)
+                    top4[c / 2 % 4] = fmaxf(fmaxf(top4[c / 2 % 4], __uint_as_float(r[c])),
+                                            __uint_as_float(r[c + 1]));
+            };
+            tmem_wait_ld<0>(r);
+            tmem_ld_x32<32>(ts + 32, r);
+            half(std::integral_constant<int, 0>());
+            tmem_wait_ld<32>(r);
+            half(std::integral_constant<int, 32>());
+            const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
             // (top > m + growth) also takes a row out of m = -inf
             if (j == 0) {
                 m = top;
@@ -301,20 +322,19 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     if (warp == 4) tmem_dealloc(tmem, Sh::kTmemCols);
 }
 
-template <typename T, int DP, bool BIAS>
-cudaError_t launch_attn_tc_fwd_as(TcFwdArgs &p, cudaStream_t s) {
+template <typename T, int DP, int BIAS>
+cudaError_t launch_attn_tc_fwd_as(const TcFwdArgs &p, cudaStream_t s) {
     using Sh = TcFwdShape<DP>;
     auto kernel = attn_tc_fwd_kernel<T, DP, BIAS>;
     static DeviceFlags ready;
-    cudaError_t e = once_per_device(ready, [&] {
+    const cudaError_t e = once_per_device(ready, [&] {
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    kTcSmemTwo);
+                                    kTcSmemOne);
     });
     if (e != cudaSuccess) return e;
-    const int64_t window = BIAS ? tc_bias_window(p.a, false) : 0;
-    p.bias_window = Sh::kSmem + window * 4 <= kTcSmemTwo ? (int)window : 0;
+    const int window = BIAS == kBiasWindow ? Sh::kStages * p.bias.count * 4 : 0;
     const int64_t blocks = (int64_t)((p.a.Lq + kTcM - 1) / kTcM) * p.a.H * p.a.N;
-    kernel<<<(unsigned)blocks, kTcThreads, Sh::kSmem + p.bias_window * 4, s>>>(p);
+    kernel<<<(unsigned)blocks, kTcThreads, Sh::kSmem + window, s>>>(p);
     return cudaGetLastError();
 }
 
@@ -333,12 +353,19 @@ cudaError_t launch_attn_tc_fwd(const AttnArgs &a, const AttnPtrs &ptr, const flo
         return cudaSuccess;
     *used = true;
     p.a = a;
-    p.bias = bias;
+    p.bias = tc_bias_of(a, false);
+    p.bias.base = bias;
+    p.bias.stride = a.bias_stride;
     p.O = ptr.O;
     p.lse = ptr.lse;
-    if (a.D <= 64)
-        return bias ? launch_attn_tc_fwd_as<T, 64, true>(p, s) : launch_attn_tc_fwd_as<T, 64, false>(p, s);
-    return bias ? launch_attn_tc_fwd_as<T, 128, true>(p, s) : launch_attn_tc_fwd_as<T, 128, false>(p, s);
+    const int mode = !bias ? kBiasNone : p.bias.count ? kBiasWindow : kBiasGlobal;
+    const auto run = [&](auto dp) {
+        constexpr int DP = decltype(dp)::value;
+        return mode == kBiasNone     ? launch_attn_tc_fwd_as<T, DP, kBiasNone>(p, s)
+               : mode == kBiasWindow ? launch_attn_tc_fwd_as<T, DP, kBiasWindow>(p, s)
+                                     : launch_attn_tc_fwd_as<T, DP, kBiasGlobal>(p, s);
+    };
+    return a.D <= 64 ? run(std::integral_constant<int, 64>()) : run(std::integral_constant<int, 128>());
 }
 
 }  // namespace gs

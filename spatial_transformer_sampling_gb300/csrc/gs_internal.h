@@ -196,6 +196,7 @@ struct AttnArgs {
     int N, H, D;
     int Hq, Wq, Hk, Wk, Lq, Lk, P, R;
     int nb;                             // rows of the bias table (0: no bias)
+    int bias_stride;                    // floats per head of the expanded bias
     int64_t qs[3], ks[3], vs[3];        // strides of batch, token, head in elements
     float scale;                        // of the scores
     const int *buckets;                 // device (R) or nullptr
