@@ -1,11 +1,12 @@
 // gs_attn_rel.cuh -- the gradient of the bias by relative index, and the row
 // sums both backward paths start from.
 //
-// For one column (key) the relative indices of a warp's rows
-// are all different, so each warp adds ds to a private window in shared memory
-// without atomics, four columns at a time in four copies.  Going along the
-// keys the window moves down; indices above it are final and are written once
-// per warp to `part`, which attn_rel_sum_kernel adds up in a fixed order.
+// For one column (key) the relative indices of 32 queries are all different, so
+// a warp adds ds to a window in shared memory without atomics.  Two warps share
+// 32 queries, half of a step's 64 keys each, two columns at a time in a copy
+// of its own each (four copies).  Going along the keys the window moves down;
+// indices above it are final and are written once per 32 queries to `part`,
+// which attn_rel_sum_kernel adds up in a fixed order.
 #pragma once
 
 #include <algorithm>
@@ -14,82 +15,91 @@
 
 namespace gs {
 
-constexpr int kRelCopies = 4;
+constexpr int kRelCopies = 4;     // two for each of the two warps
 constexpr int kRelCols = 64;      // keys of one step
+constexpr int kRelHalf = kRelCols / 2;
 
 // Where a launch of the query kernel leaves its share of the bias gradient.
 struct RelArgs {
-    int window;     // floats of a warp's window, a power of two (0: not computed there)
-    int stride;     // floats a query warp writes
+    int window;     // floats of a window, a power of two (0: not computed there)
+    int stride;     // floats written per 32 queries
     int head0;      // first (batch, head) pair of the launch
-    float *part;    // (pairs of the launch, query warps, stride)
+    float *part;    // (pairs of the launch, groups of 32 queries, stride)
 };
 
 // Rows of lse2 and delta kept per (batch, head): whole column tiles.
 __host__ __device__ inline int rows64(int L) { return (L + 63) / 64 * 64; }
 
-// Shared memory of `warps` bias-gradient windows of `w` floats: per warp four
-// copies, the moving window and the columns' relative indices.
-inline __host__ __device__ int rel_smem(int w, int warps) {
-    return w ? warps * ((kRelCopies + 1) * w + kRelCols) * 4 : 0;
+// Shared memory of `pairs` bias-gradient windows of `w` floats: four copies, the
+// moving window and the columns' relative indices each.
+inline __host__ __device__ int rel_smem(int w, int pairs) {
+    return w ? pairs * ((kRelCopies + 1) * w + kRelCols) * 4 : 0;
 }
 
-// Adds one step's ds (fp32, 64 columns of this thread's query) to the warp's
-// bias-gradient window and writes out the indices that are final.
+// The window of 32 queries, held by a pair of warps (`half` 0 and 1).
 struct RelWindow {
     float *copies, *ring;
     int *rel;
-    int size, rq, rq_min, rq_max, top;
+    int size, rq, rq_min, rq_max, top, pair, half;
     bool mine;
 
-    // Warp `threadIdx.x / 32` of the block takes queries i0 + 32 * warp on, of the
-    // (batch, head) pair nh.  Returns where it writes, indexed by relative index.
+    __device__ __forceinline__ void sync() const {
+        asm volatile("bar.sync %0, 64;" ::"r"(pair + 1) : "memory");
+    }
+
+    // The pair takes queries i0 + 32 * pair on of the (batch, head) pair nh.
+    // Returns where it writes, indexed by relative index.
     __device__ __forceinline__ float *init(const AttnArgs &a, float *smem, const RelArgs &p, int i0,
-                                           int nh) {
-        const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, iw = i0 + warp * 32;
+                                           int nh, int pair_, int half_) {
+        pair = pair_;
+        half = half_;
+        const int lane = threadIdx.x % 32, iw = i0 + pair * 32;
         size = p.window;
-        copies = smem + warp * ((kRelCopies + 1) * size + kRelCols);
+        copies = smem + pair * ((kRelCopies + 1) * size + kRelCols);
         ring = copies + kRelCopies * size;
         rel = reinterpret_cast<int *>(ring + size);
-        for (int k = lane; k < (kRelCopies + 1) * size; k += 32) copies[k] = 0.0f;
+        for (int k = half * 32 + lane; k < (kRelCopies + 1) * size; k += 64) copies[k] = 0.0f;
         mine = iw + lane < a.Lq;
         rq = rel_q(a, min(iw + lane, a.Lq - 1));
         rq_min = rel_q(a, min(iw, a.Lq - 1));
         rq_max = rel_q(a, min(iw + 31, a.Lq - 1));
         top = rq_max;
-        __syncwarp();
         const int64_t slot = (int64_t)(nh - p.head0) * ((a.Lq + 31) / 32) + iw / 32;
         return p.part + slot * p.stride - (rq_min - rel_k(a, a.Lk - 1));
     }
 
-    // keys j0 .. j0 + live - 1 of `keys`; `out` is indexed by relative index
-    __device__ __forceinline__ void add(const AttnArgs &a, const float (&ds)[kRelCols], int j0, int live,
-                                        int keys, float *out) {
-        const int lane = threadIdx.x % 32;
+    // ds (fp32) of this thread's query and its half of the keys j0 .. j0 + 63, of
+    // which `live` count; `keys` in all.  Both warps call it; `out` as from init.
+    __device__ __forceinline__ void add(const AttnArgs &a, const float (&ds)[kRelHalf], int j0,
+                                        int live, int keys, float *out) {
+        const int lane = threadIdx.x % 32, first = half * kRelHalf;
         live = min(live, kRelCols);
-#pragma unroll
-        for (int k = 0; k < kRelCols; k += 32) rel[k + lane] = rel_k(a, min(j0 + k + lane, keys - 1));
-        __syncwarp();
+        rel[first + lane] = rel_k(a, min(j0 + first + lane, keys - 1));
+        sync();   // and the windows are clear
         const int lo = rq_min - rel[live - 1];
         const int span = rq_max - rel[0] - lo + 1;
-        float *at = copies + (rq - lo);
+        float *at = copies + 2 * half * size + (rq - lo);
+        constexpr int kStep = kRelHalf / 2;
 #pragma unroll
-        for (int s = 0; s < kRelCols / kRelCopies; ++s) {
-            float v[kRelCopies];
-            int k[kRelCopies];
+        for (int s = 0; s < kStep; s += 4) {
+            const int4 o0 = *reinterpret_cast<const int4 *>(rel + first + s);
+            const int4 o1 = *reinterpret_cast<const int4 *>(rel + first + kStep + s);
+            const int k0[4] = {o0.x, o0.y, o0.z, o0.w}, k1[4] = {o1.x, o1.y, o1.z, o1.w};
 #pragma unroll
-            for (int g = 0; g < kRelCopies; ++g) {
-                const int c = s + g * (kRelCols / kRelCopies);
-                k[g] = g * size - rel[c];
-                if (c < live && mine) v[g] = at[k[g]] + ds[c];
+            for (int e = 0; e < 4; ++e) {
+                const bool on0 = mine && first + s + e < live;
+                const bool on1 = mine && first + kStep + s + e < live;
+                float v0, v1;
+                if (on0) v0 = at[-k0[e]] + ds[s + e];
+                if (on1) v1 = at[size - k1[e]] + ds[kStep + s + e];
+                if (on0) at[-k0[e]] = v0;
+                if (on1) at[size - k1[e]] = v1;
+                __syncwarp();
             }
-#pragma unroll
-            for (int g = 0; g < kRelCopies; ++g)
-                if (s + g * (kRelCols / kRelCopies) < live && mine) at[k[g]] = v[g];
-            __syncwarp();
         }
+        sync();
         // join the copies into the ring, which is indexed by the relative index
-        for (int k = lane; k < span; k += 32) {
+        for (int k = half * 32 + lane; k < span; k += 64) {
             float v = 0.0f;
 #pragma unroll
             for (int g = 0; g < kRelCopies; ++g) {
@@ -98,14 +108,13 @@ struct RelWindow {
             }
             ring[(lo + k) & (size - 1)] += v;
         }
-        __syncwarp();
+        sync();
         const int final_above = j0 + live < keys ? rq_max - rel_k(a, j0 + live) : lo - 1;
-        for (int r = final_above + 1 + lane; r <= top; r += 32) {
+        for (int r = final_above + 1 + half * 32 + lane; r <= top; r += 64) {
             out[r] = ring[r & (size - 1)];
             ring[r & (size - 1)] = 0.0f;
         }
         top = final_above;
-        __syncwarp();
     }
 };
 

@@ -237,10 +237,11 @@ __global__ void __launch_bounds__(kSimtThreads)
         row_delta[i] = DKV ? 0.0f : delta[row];
         row_rel[i] = !bias ? 0 : DKV ? -rel_k(a, row) : rel_q(a, row);
     }
-    const bool with_rel = !DKV && rel.window > 0 && warp < 2 && i0 + warp * 32 < a.Lq && cols > 0;
+    // four warps, two per 32 queries, see to the bias gradient
+    const bool with_rel = !DKV && rel.window > 0 && warp < 4 && i0 + warp / 2 * 32 < a.Lq && cols > 0;
     RelWindow win;
     float *rel_out = nullptr;
-    if (with_rel) rel_out = win.init(a, win_smem, rel, i0, nh);
+    if (with_rel) rel_out = win.init(a, win_smem, rel, i0, nh, warp / 2, warp % 2);
 
     for (int j0 = 0; j0 < cols; j0 += kSimtTile) {
         const int live = cols - j0;
@@ -274,9 +275,10 @@ __global__ void __launch_bounds__(kSimtThreads)
         simt_store_t(t2, d, ty, tx);
         __syncthreads();
         if (with_rel) {
-            float ds[kSimtTile];
+            float ds[kRelHalf];
 #pragma unroll
-            for (int c = 0; c < kSimtTile; ++c) ds[c] = t2[c * kSimtPitch + warp * 32 + threadIdx.x % 32];
+            for (int c = 0; c < kRelHalf; ++c)
+                ds[c] = t2[(warp % 2 * kRelHalf + c) * kSimtPitch + warp / 2 * 32 + threadIdx.x % 32];
             win.add(a, ds, j0, live, keys, rel_out);
         }
 #pragma unroll

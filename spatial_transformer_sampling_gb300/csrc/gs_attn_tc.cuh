@@ -20,21 +20,47 @@
 
 namespace gs {
 
-constexpr int kTcM = 128;            // rows of a score tile: one per softmax thread
+constexpr int kTcM = 128;            // rows of a score tile, two softmax threads each
 constexpr int kTcN = 64;             // columns of a score tile
-constexpr int kTcThreads = 160;      // four softmax warps and one that issues copies and MMAs
+constexpr int kTcHalf = kTcN / 2;    // columns of one softmax thread
+constexpr int kTcSoft = 2 * kTcM;    // softmax threads: warps w and w + 4 share rows 32 (w % 4) on
+constexpr int kTcThreads = kTcSoft + 64;   // and a warp that issues MMAs, and one that copies
+constexpr int kTcMmaWarp = kTcSoft / 32, kTcCopyWarp = kTcMmaWarp + 1;
 
-// Shared-memory descriptor of an MN-major operand with the 128-byte swizzle:
-// tokens are rows of 128 bytes, eight of them make a 1024-byte atom; `lbo` is
-// the distance between 64-element chunks along the head width.
-__device__ __forceinline__ uint64_t umma_desc_mnmajor_sw128(uint32_t smem_addr, uint32_t lbo) {
-    uint64_t d = 0;
-    d |= (uint64_t)((smem_addr >> 4) & 0x3FFFu);
-    d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
-    d |= (uint64_t)(1024u >> 4) << 32;                    // next eight tokens
-    d |= (uint64_t)1 << 46;
-    d |= (uint64_t)2 << 61;
-    return d;
+// mbar_wait_bounded for waits on the critical path of a pipeline: polls without
+// reading the global timer, which takes longer than the events waited for, but
+// for every 1024th poll.
+__device__ __forceinline__ bool tc_wait(uint64_t *bar, uint32_t parity, unsigned *err) {
+    uint64_t t0 = 0;
+    for (uint32_t n = 1; !mbar_try_wait(bar, parity); ++n) {
+        if (n % 1024 != 0) continue;
+        const uint64_t now = global_timer_ns();
+        if (t0 == 0) t0 = now;
+        if (now - t0 > kWaitLimitNs) {
+            atomicOr(err, kDevErrTimeout);
+            return false;
+        }
+    }
+    return true;
+}
+
+// Barrier of the two warps that share 32 rows.
+__device__ __forceinline__ void pair_sync(int pair) {
+    asm volatile("bar.sync %0, 64;" ::"r"(pair + 1) : "memory");
+}
+
+// Shared-memory descriptors with the 128-byte swizzle (see
+// umma_desc_kmajor_sw128): the upper word is the same for all of a kernel's
+// operands (1024 bytes between groups of eight tokens), the lower one holds the
+// address and moves with it, so that one thread issues an MMA in a few
+// instructions.  MN-major (tokens are the contraction): `lbo` is the distance
+// between 64-element chunks along the head width.
+constexpr uint32_t kUmmaDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t umma_lo_kmajor(uint32_t smem_addr) {
+    return ((smem_addr >> 4) & 0x3FFFu) | (1u << 16);
+}
+__device__ __forceinline__ uint32_t umma_lo_mnmajor(uint32_t smem_addr, uint32_t lbo) {
+    return ((smem_addr >> 4) & 0x3FFFu) | (((lbo >> 4) & 0x3FFFu) << 16);
 }
 
 // umma_idesc_f16 with the second operand MN-major.
@@ -42,15 +68,29 @@ __host__ __device__ constexpr uint32_t umma_idesc_f16_bmn(bool is_bf16, int M, i
     return umma_idesc_f16(is_bf16, M, N) | (1u << 16);
 }
 
-// D[tmem] (+)= A[tmem] * B[smem]: row r of A is lane r, two 16-bit elements of
-// the contraction per 32-bit column.
-__device__ __forceinline__ void umma_f16_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc,
+// D[tmem] (+)= A[smem] * B[smem]^T, lower descriptor words.
+__device__ __forceinline__ void umma_f16_ss(uint32_t tmem_d, uint32_t a_lo, uint32_t b_lo,
                                             uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
-        "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "mov.b64 a, {%1, %3};\n\t"
+        "mov.b64 b, {%2, %3};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(tmem_d),
+        "r"(a_lo), "r"(b_lo), "n"(kUmmaDescHi), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// D[tmem] (+)= A[tmem] * B[smem]: row r of A is lane r, two 16-bit elements of
+// the contraction per 32-bit column.
+__device__ __forceinline__ void umma_f16_ts(uint32_t tmem_d, uint32_t tmem_a, uint32_t b_lo,
+                                            uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "mov.b64 b, {%2, %3};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(tmem_d),
+        "r"(tmem_a), "r"(b_lo), "n"(kUmmaDescHi), "r"(idesc), "r"(accumulate)
         : "memory");
 }
 
@@ -108,6 +148,17 @@ __device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const uint32_t (&r)[
         : "memory");
 }
 
+// Starts storing r[0..15] to 16 consecutive columns of this thread's lane.
+__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+        "%11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+        "r"(r[15])
+        : "memory");
+}
+
 __device__ __forceinline__ void tmem_wait_st() {
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
@@ -161,25 +212,26 @@ __device__ __forceinline__ void tc_load(unsigned char *dst, const TcView &v, int
         tma_load_4d(dst + c * ROWS * 128, &v.map, c * 64, h * v.by_h, row, n * v.by_n, bar);
 }
 
-// Scores: D[128 x N] (+)= A[128 x D] B[N x D]^T over `steps` steps of 16.
-template <int N>
-__device__ __forceinline__ void tc_scores(uint32_t tmem_d, uint32_t a_smem, uint32_t b_smem,
-                                          uint32_t idesc, int steps) {
-    for (int k = 0; k < steps; ++k) {
-        const uint32_t c = k / 4, o = (k % 4) * 32;
-        umma_f16(tmem_d, umma_desc_kmajor_sw128(a_smem + c * kTcM * 128 + o, 1024),
-                 umma_desc_kmajor_sw128(b_smem + c * N * 128 + o, 1024), idesc, k > 0);
-    }
+// Scores: D[128 x 64] = A[128 x D] B[64 x D]^T over `steps` steps of 16, at most
+// DP / 16; a and b are the tiles' lower descriptor words.
+template <int DP>
+__device__ __forceinline__ void tc_scores(uint32_t tmem_d, uint32_t a, uint32_t b, uint32_t idesc,
+                                          int steps) {
+#pragma unroll
+    for (int k = 0; k < DP / 16; ++k)
+        if (k < steps)   // a step is 32 bytes along a row, four fill a chunk
+            umma_f16_ss(tmem_d, a + (k / 4 * kTcM * 128 + k % 4 * 32) / 16,
+                        b + (k / 4 * kTcN * 128 + k % 4 * 32) / 16, idesc, k > 0);
 }
 
-// Weighted sums: D[128 x width] (+)= A[tmem, 128 x TOKENS] B[TOKENS x width].
-template <int TOKENS>
-__device__ __forceinline__ void tc_weighted(uint32_t tmem_d, uint32_t tmem_a, uint32_t b_smem,
+// Weighted sums: D[128 x width] (+)= A[tmem, 128 x 64] B[64 x width].  The
+// 16-bit A lies where the softmax threads read its scores: 16 columns for the
+// first 32 tokens, and 16 from column 32 on for the others.
+__device__ __forceinline__ void tc_weighted(uint32_t tmem_d, uint32_t tmem_a, uint32_t b,
                                             uint32_t idesc, bool accumulate) {
 #pragma unroll
-    for (int k = 0; k < TOKENS / 16; ++k)
-        umma_f16_ts(tmem_d, tmem_a + k * 8,
-                    umma_desc_mnmajor_sw128(b_smem + k * 2048, TOKENS * 128), idesc,
+    for (int k = 0; k < kTcN / 16; ++k)
+        umma_f16_ts(tmem_d, tmem_a + k / 2 * kTcHalf + k % 2 * 8, b + k * 2048 / 16, idesc,
                     accumulate || k > 0);
 }
 
@@ -219,28 +271,68 @@ __device__ __forceinline__ int bias_start(const TcBias &b, int r) {
     return (r - b.below) & ~3;   // rounds down below zero too
 }
 
-// Relative offset of 64 consecutive columns from the first one on their grid
-// (rows of W, a new row costs P - W more), into a warp's 64 ints; columns from
-// `live` on repeat the last live one.
-__device__ __forceinline__ void bias_offsets(int *rel, int first, int live, int W, int P) {
-    const int lane = threadIdx.x % 32, y0 = first / W;
-    __syncwarp();
-#pragma unroll
-    for (int k = 0; k < kTcN; k += 32) {
-        const int c = min(k + lane, live - 1), y = (first + c) / W;
-        rel[k + lane] = c + (y - y0) * (P - W);
+// Walks the columns' grid (rows of W tokens, a new row costs P - W more) a tile
+// of 64 tokens at a time without dividing: x is the first token's place in its
+// row, rel its offset from token 0.  A one-row grid never wraps, also past its
+// last token.
+struct TileWalk {
+    int W, P, x, rel, dy, dx, dy_half, dx_half;
+    __device__ __forceinline__ void init(int rows, int width, int P_) {
+        W = rows == 1 ? INT_MAX : width;
+        P = rows == 1 ? 0 : P_;
+        x = rel = 0;
+        dy = kTcN / W;
+        dx = kTcN - dy * W;
+        dy_half = kTcHalf / W;
+        dx_half = kTcHalf - dy_half * W;
     }
+    __device__ __forceinline__ void next() {
+        x += dx;
+        rel += dy * P + dx;
+        if (x >= W) {
+            x -= W;
+            rel += P - W;
+        }
+    }
+    // Place in its row of the tile's token `part` * 32, and its offset from the
+    // tile's first one.
+    __device__ __forceinline__ void half(int part, int &x_half, int &rel_half) const {
+        x_half = x;
+        rel_half = 0;
+        if (part) {
+            x_half += dx_half;
+            rel_half = dy_half * P + dx_half;
+            if (x_half >= W) {
+                x_half -= W;
+                rel_half += P - W;
+            }
+        }
+    }
+};
+
+// Offsets of 32 consecutive columns from the first of their tile into a warp's
+// 32 ints; columns from `live` of the tile on repeat the last live one.
+// `inverse` is 65536 / W + 1 for W < 64, which divides numbers below 128 by W.
+__device__ __forceinline__ void bias_offsets(int *rel, const TileWalk &walk, int first, int live,
+                                             int inverse) {
+    const int lane = threadIdx.x % 32;
+    const int c = min(first + lane, live - 1), at = walk.x + c;
+    const int rows = walk.W >= kTcN ? at >= walk.W : (at * inverse) >> 16;
+    __syncwarp();
+    rel[lane] = c + rows * (walk.P - walk.W);
     __syncwarp();
 }
 
-// f(c, b) for columns c = C0 .. C0 + 31: b[c] and b[c + 1] of a row of the bias.
+// f(c, b) for columns c = 0, 2, .. 30: the bias of columns c and c + 1 of a row.
 // Column c sits SIGN * (its offset) from `row` (SIGN -1: the thread holds a
-// query, columns are keys; +1: a key against queries).
-template <int SIGN, int C0, typename F>
-__device__ __forceinline__ void bias_by_runs(const float *row, int &x, int &rel, int W, int wrap,
+// query, columns are keys; +1: a key against queries); x and rel as from
+// TileWalk::half.
+template <int SIGN, typename F>
+__device__ __forceinline__ void bias_by_runs(const float *row, int x, int rel, const TileWalk &walk,
                                              F &&f) {
+    const int W = walk.W, wrap = walk.P - walk.W;
 #pragma unroll
-    for (int c = C0; c < C0 + 32; c += 8) {
+    for (int c = 0; c < kTcHalf; c += 8) {
         const float *at = row + SIGN * rel;
 #pragma unroll
         for (int k = 0; k < 8; k += 2) f(c + k, make_float2(at[SIGN * k], at[SIGN * (k + 1)]));
@@ -249,10 +341,10 @@ __device__ __forceinline__ void bias_by_runs(const float *row, int &x, int &rel,
         x = x == W ? 0 : x;
     }
 }
-template <int SIGN, int C0, typename F>
+template <int SIGN, typename F>
 __device__ __forceinline__ void bias_by_table(const float *row, const int *rel, F &&f) {
 #pragma unroll
-    for (int c = C0; c < C0 + 32; c += 4) {
+    for (int c = 0; c < kTcHalf; c += 4) {
         const int4 o = *reinterpret_cast<const int4 *>(rel + c);
         f(c, make_float2(row[SIGN * o.x], row[SIGN * o.y]));
         f(c + 2, make_float2(row[SIGN * o.z], row[SIGN * o.w]));
@@ -283,8 +375,8 @@ inline int tc_bias_pad(const AttnArgs &a) {
     return (std::max(tc_bias_of(a, false).count, tc_bias_of(a, true).count) + 8 + 3) / 4 * 4;
 }
 
-// Dynamic shared memory of one CTA per SM, at most (barriers and offsets take
-// up to 1.25 KB of the 227).
-constexpr int kTcSmemOne = 227 * 1024 - 1280;
+// Dynamic shared memory of one CTA per SM, at most (barriers, offsets and maxima
+// take up to 4 KB of the 227).
+constexpr int kTcSmemOne = 223 * 1024;
 
 }  // namespace gs

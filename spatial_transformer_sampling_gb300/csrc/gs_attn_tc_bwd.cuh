@@ -7,7 +7,7 @@
 // With rows R1, R2 (DKV: K, V; DQ: Q, dO) resident and columns C1, C2 (DKV:
 // Q, dO; DQ: K, V) streamed by TMA, each step computes
 //   S  = R1 C1^T,  dP = R2 C2^T             tcgen05.mma, fp32 in TMEM
-//   p  = 2^(c S + bias - lse),  ds = p (dP - delta)   one thread per row
+//   p  = 2^(c S + bias - lse),  ds = p (dP - delta)   two threads per row
 //   acc1 += ds C1  (dK or dQ),  acc2 += p C2  (dV)    tcgen05.mma
 // p and ds are rounded to the 16-bit type and read back from TMEM, where they
 // overwrite dP; S is free as soon as it is loaded, so the next step's S is
@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(kTcThreads, TcBwdShape<DP, DKV>::kCtas)
     constexpr int NS = Sh::kStages;
     constexpr bool kBf16 = __is_same(T, __nv_bfloat16);
     extern __shared__ unsigned char smem_raw[];
-    __shared__ uint64_t r_full, c_full[NS], s_full, s_free, dp_full, pd_ready, done, finished;
+    __shared__ uint64_t r_full, c_full[NS], s_full, s_free, dp_full, pd_ready, done[NS], finished, cleared;
     __shared__ uint32_t tmem_base;
 
     const AttnArgs &a = p.a;
@@ -65,7 +65,7 @@ __global__ void __launch_bounds__(kTcThreads, TcBwdShape<DP, DKV>::kCtas)
     float *sVec = reinterpret_cast<float *>(tiles + Sh::kTileSmem);
     float *sRel = sVec + NS * Sh::kVecBytes / 4;
     float *sBias = sRel + rel_smem(p.rel.window, 4) / 4;   // a window per stage
-    __shared__ __align__(16) int s_rel[4][kTcN];
+    __shared__ __align__(16) int s_rel[8][kTcHalf];
 
     const int rows = DKV ? a.Lk : a.Lq;
     const int row_tiles = (rows + kTcM - 1) / kTcM;
@@ -86,16 +86,19 @@ __global__ void __launch_bounds__(kTcThreads, TcBwdShape<DP, DKV>::kCtas)
     const int row0 = DKV ? -rel_k(a, i0) : rel_q(a, i0);
     const auto meet = [&](int col) { return row0 + (DKV ? rel_q(a, col) : -rel_k(a, col)); };
 
-    if (warp == 4) {
+    if (warp == kTcMmaWarp) {
         if (lane == 0) {
             mbar_init(&r_full, 1);
-            for (int s = 0; s < NS; ++s) mbar_init(&c_full[s], 1);
+            for (int s = 0; s < NS; ++s) {
+                mbar_init(&c_full[s], 1);
+                mbar_init(&done[s], 1);
+            }
             mbar_init(&s_full, 1);
-            mbar_init(&s_free, kTcM);
+            mbar_init(&s_free, kTcSoft);
             mbar_init(&dp_full, 1);
-            mbar_init(&pd_ready, kTcM);
-            mbar_init(&done, 1);
+            mbar_init(&pd_ready, kTcSoft);
             mbar_init(&finished, 1);
+            mbar_init(&cleared, 1);
             fence_mbar_init();
         }
         __syncwarp();
@@ -107,142 +110,148 @@ __global__ void __launch_bounds__(kTcThreads, TcBwdShape<DP, DKV>::kCtas)
     const uint32_t tmem = tmem_base;
     bool ok = true;
 
-    if (warp == 4) {
-        // ---------------------------------------------------- copies and MMAs
-        const uint32_t idesc_s = umma_idesc_f16(kBf16, kTcM, kTcN);
-        const int width = (a.D + 15) / 16 * 16;
-        const uint32_t idesc_o = umma_idesc_f16_bmn(kBf16, kTcM, width);
-        const uint32_t r1_at = smem_u32(sR1), r2_at = smem_u32(sR2);
-        const uint32_t c1_at = smem_u32(sC1), c2_at = smem_u32(sC2);
-        const auto load = [&](int t) {   // one lane
-            const int s = t % NS;
-            mbar_arrive_expect_tx(&c_full[s], 2 * Sh::kTileBytes + Sh::kVecBytes +
-                                                  (BIAS == kBiasWindow ? p.bias.count * 4 : 0));
-            tc_load<DP, kTcN>(sC1 + s * Sh::kTileBytes, p.c1, n, h, t * kTcN, &c_full[s]);
-            tc_load<DP, kTcN>(sC2 + s * Sh::kTileBytes, p.c2, n, h, t * kTcN, &c_full[s]);
-            if (BIAS == kBiasWindow)
-                bulk_copy_g2s(sBias + s * p.bias.count, bias + bias_start(p.bias, meet(t * kTcN)),
-                              p.bias.count * 4, &c_full[s]);
-            if (DKV) {
-                bulk_copy_g2s(sVec + s * 2 * kTcN, lse2 + t * kTcN, kTcN * 4, &c_full[s]);
-                bulk_copy_g2s(sVec + s * 2 * kTcN + kTcN, delta + t * kTcN, kTcN * 4, &c_full[s]);
+    const bool tail = !DKV && cols % kTcN != 0;   // the last tile holds masked keys
+
+    if (warp == kTcCopyWarp) {
+        // ---------------------------------------------------- copies
+        if (lane == 0 && steps > 0) {
+            mbar_arrive_expect_tx(&r_full, 2 * Sh::kRowBytes);
+            tc_load<DP, kTcM>(sR1, p.r1, n, h, i0, &r_full);
+            tc_load<DP, kTcM>(sR2, p.r2, n, h, i0, &r_full);
+            for (int t = 0; t < steps; ++t) {
+                const int s = t % NS;
+                if (t >= NS) {   // the stage's last tile is consumed
+                    ok = tc_wait(&done[s], (t / NS - 1) & 1, a.err);
+                    if (!ok) break;
+                }
+                mbar_arrive_expect_tx(&c_full[s], 2 * Sh::kTileBytes + Sh::kVecBytes +
+                                                      (BIAS == kBiasWindow ? p.bias.count * 4 : 0));
+                tc_load<DP, kTcN>(sC1 + s * Sh::kTileBytes, p.c1, n, h, t * kTcN, &c_full[s]);
+                tc_load<DP, kTcN>(sC2 + s * Sh::kTileBytes, p.c2, n, h, t * kTcN, &c_full[s]);
+                if (BIAS == kBiasWindow)
+                    bulk_copy_g2s(sBias + s * p.bias.count, bias + bias_start(p.bias, meet(t * kTcN)),
+                                  p.bias.count * 4, &c_full[s]);
+                if (DKV) {
+                    bulk_copy_g2s(sVec + s * 2 * kTcN, lse2 + t * kTcN, kTcN * 4, &c_full[s]);
+                    bulk_copy_g2s(sVec + s * 2 * kTcN + kTcN, delta + t * kTcN, kTcN * 4, &c_full[s]);
+                }
             }
-        };
-        // tile t is in shared memory, masked keys cleared
-        const auto arrived = [&](int t) {
-            bool good = mbar_wait_bounded(&c_full[t % NS], (t / NS) & 1, a.err);
-            if (__any_sync(0xffffffffu, !good)) return false;
-            if (!DKV && keys - t * kTcN < kTcN) {
-                tc_clear_rows<DP, kTcN>(sC1 + t % NS * Sh::kTileBytes, keys - t * kTcN);
-                tc_clear_rows<DP, kTcN>(sC2 + t % NS * Sh::kTileBytes, keys - t * kTcN);
-            }
-            return true;
-        };
-        int loaded = min(NS, steps);
-        if (steps > 0) {
-            if (lane == 0) {
-                mbar_arrive_expect_tx(&r_full, 2 * Sh::kRowBytes);
-                tc_load<DP, kTcM>(sR1, p.r1, n, h, i0, &r_full);
-                tc_load<DP, kTcM>(sR2, p.r2, n, h, i0, &r_full);
-                for (int t = 0; t < loaded; ++t) load(t);
-            }
+        }
+        __syncwarp();
+        if (steps > 0 && tail) {   // what masked keys hold must not reach a product
+            const int t = steps - 1;
+            ok = tc_wait(&c_full[t % NS], (t / NS) & 1, a.err);
             __syncwarp();
-            ok = mbar_wait_bounded(&r_full, 0, a.err);
-            ok = __all_sync(0xffffffffu, ok) && arrived(0);
-            if (ok && lane == 0) {
-                tc_scores<kTcN>(tmem + Sh::kTmemS, r1_at, c1_at, idesc_s, width / 16);
+            tc_clear_rows<DP, kTcN>(sC1 + t % NS * Sh::kTileBytes, cols - t * kTcN);
+            tc_clear_rows<DP, kTcN>(sC2 + t % NS * Sh::kTileBytes, cols - t * kTcN);
+            if (lane == 0) mbar_arrive(&cleared);
+        }
+        // every copy lands before the block may leave (they have, unless a wait gave up)
+        for (int t = max(0, steps - NS); t < steps; ++t)
+            tc_wait(&c_full[t % NS], (t / NS) & 1, a.err);
+    } else if (warp == kTcMmaWarp) {
+        // ---------------------------------------------------- MMAs, one thread
+        if (lane == 0 && steps > 0) {
+            const uint32_t idesc_s = umma_idesc_f16(kBf16, kTcM, kTcN);
+            const int depth = (a.D + 15) / 16;
+            const uint32_t idesc_o = umma_idesc_f16_bmn(kBf16, kTcM, depth * 16);
+            const uint32_t r1_lo = umma_lo_kmajor(smem_u32(sR1)), r2_lo = umma_lo_kmajor(smem_u32(sR2));
+            const uint32_t c1_lo = umma_lo_kmajor(smem_u32(sC1)), c2_lo = umma_lo_kmajor(smem_u32(sC2));
+            const uint32_t c1_mn = umma_lo_mnmajor(smem_u32(sC1), kTcN * 128);
+            const uint32_t c2_mn = umma_lo_mnmajor(smem_u32(sC2), kTcN * 128);
+            constexpr int kTile = Sh::kTileBytes / 16;
+            const auto arrived = [&](int t) {   // tile t is in place, masked keys cleared
+                return tc_wait(&c_full[t % NS], (t / NS) & 1, a.err) &&
+                       (!tail || t + 1 < steps || tc_wait(&cleared, 0, a.err));
+            };
+            ok = tc_wait(&r_full, 0, a.err) && arrived(0);
+            if (ok) {
+                tc_scores<DP>(tmem + Sh::kTmemS, r1_lo, c1_lo, idesc_s, depth);
                 umma_commit(&s_full);
-                tc_scores<kTcN>(tmem + Sh::kTmemP, r2_at, c2_at, idesc_s, width / 16);
+                tc_scores<DP>(tmem + Sh::kTmemP, r2_lo, c2_lo, idesc_s, depth);
                 umma_commit(&dp_full);
             }
-        }
-        for (int t = 0; t < steps && ok; ++t) {
-            const int s = t % NS, s1 = (t + 1) % NS;
-            if (t + 1 < steps) {   // the next scores, once this step's are loaded
-                ok = arrived(t + 1);
-                if (!ok) break;
-                ok = mbar_wait_bounded(&s_free, t & 1, a.err);
-                if (__any_sync(0xffffffffu, !ok)) break;
-                if (lane == 0) {
+            for (int t = 0; t < steps && ok; ++t) {
+                const int s = t % NS, s1 = (t + 1) % NS;
+                if (t + 1 < steps) {   // the next scores, once this step's are loaded
+                    ok = arrived(t + 1) && tc_wait(&s_free, t & 1, a.err);
+                    if (!ok) break;
                     tcgen05_fence_after_sync();
-                    tc_scores<kTcN>(tmem + Sh::kTmemS, r1_at, c1_at + s1 * Sh::kTileBytes, idesc_s,
-                                    width / 16);
+                    tc_scores<DP>(tmem + Sh::kTmemS, r1_lo, c1_lo + s1 * kTile, idesc_s, depth);
                     umma_commit(&s_full);
                 }
-            }
-            ok = mbar_wait_bounded(&pd_ready, t & 1, a.err);
-            if (__any_sync(0xffffffffu, !ok)) break;
-            if (lane == 0) {
+                ok = tc_wait(&pd_ready, t & 1, a.err);
+                if (!ok) break;
                 tcgen05_fence_after_sync();
                 if (DKV)
-                    tc_weighted<kTcN>(tmem + Sh::kTmemAcc2, tmem + Sh::kTmemP,
-                                      c2_at + s * Sh::kTileBytes, idesc_o, t > 0);
-                tc_weighted<kTcN>(tmem + Sh::kTmemAcc1, tmem + Sh::kTmemP + kTcN / 2,
-                                  c1_at + s * Sh::kTileBytes, idesc_o, t > 0);
-                umma_commit(t + 1 < steps ? &done : &finished);
-            }
-            if (t + 1 < steps) {   // p and ds are consumed: dP may be overwritten
-                ok = mbar_wait_bounded(&done, t & 1, a.err);
-                if (__any_sync(0xffffffffu, !ok)) break;
-                if (lane == 0) {
-                    if (loaded < steps) load(loaded);
-                    tc_scores<kTcN>(tmem + Sh::kTmemP, r2_at, c2_at + s1 * Sh::kTileBytes, idesc_s,
-                                    width / 16);
+                    tc_weighted(tmem + Sh::kTmemAcc2, tmem + Sh::kTmemP, c2_mn + s * kTile, idesc_o,
+                                t > 0);
+                tc_weighted(tmem + Sh::kTmemAcc1, tmem + Sh::kTmemP + kTcHalf / 2, c1_mn + s * kTile,
+                            idesc_o, t > 0);
+                umma_commit(t + 1 < steps ? &done[s] : &finished);
+                if (t + 1 < steps) {   // p and ds are consumed: dP may be overwritten
+                    ok = tc_wait(&done[s], (t / NS) & 1, a.err);
+                    if (!ok) break;
+                    tc_scores<DP>(tmem + Sh::kTmemP, r2_lo, c2_lo + s1 * kTile, idesc_s, depth);
                     umma_commit(&dp_full);
                 }
-                if (loaded < steps) ++loaded;
+            }
+            if (!ok) {   // a wait gave up: let the MMAs end before TMEM is released
+                umma_commit(&r_full);
+                tc_wait(&r_full, 1, a.err);
             }
         }
-        if (!__all_sync(0xffffffffu, ok)) {
-            // a wait gave up: let this CTA's copies and MMAs end before it leaves
-            if (lane == 0) umma_commit(&finished);
-            mbar_wait_bounded(&finished, 0, a.err);
-            for (int t = max(0, loaded - NS); t < loaded; ++t)
-                mbar_wait_bounded(&c_full[t % NS], (t / NS) & 1, a.err);
-        }
+        __syncwarp();
     } else {
-        // ---------------------------------------------------- a row per thread
-        const uint32_t my_tmem = (uint32_t)(warp * 32) << 16;   // this warp's TMEM lanes
-        const int i = i0 + threadIdx.x, ic = min(i, live_rows - 1);
+        // ---------------------------------------------------- weights
+        // After a wait that gave up a warp goes on without waiting (and without
+        // storing), so that its partner finds it at every pair_sync.
+        const auto wait = [&](uint64_t *bar, int parity) {
+            if (ok) ok = __all_sync(0xffffffffu, tc_wait(bar, parity, a.err));
+        };
+        const int pair = warp % 4, part = warp / 4;
+        const uint32_t my_tmem = (uint32_t)(pair * 32) << 16;   // this warp's TMEM lanes
+        const int first = part * kTcHalf;                       // this thread's columns of a tile
+        const int i = i0 + pair * 32 + lane, ic = min(i, live_rows - 1);
         const float c2 = a.scale * kLog2e;
         const int my_row = !BIAS || steps == 0 ? 0 : DKV ? -rel_k(a, ic) : rel_q(a, ic);
+        TileWalk walk;
+        if (BIAS) walk.init(DKV ? a.Hq : a.Hk, DKV ? a.Wq : a.Wk, a.P);
+        const int inverse = 65536 / (DKV ? a.Wq : a.Wk) + 1, meet0 = meet(0);
         const bool counts = i < live_rows && steps > 0;
         const float row_lse = !DKV ? (counts ? lse2[i] : INFINITY) : 0.0f;
         const float row_delta = !DKV && counts ? delta[i] : 0.0f;
-        const bool with_rel = !DKV && BIAS && p.rel.window > 0 && i0 + warp * 32 < a.Lq && steps > 0;
+        const bool with_rel = !DKV && BIAS && p.rel.window > 0 && i0 + pair * 32 < a.Lq && steps > 0;
         RelWindow win;
         float *rel_out = nullptr;
         if (!DKV && BIAS) {
-            if (with_rel) rel_out = win.init(a, sRel, p.rel, i0, nh);
+            if (with_rel) rel_out = win.init(a, sRel, p.rel, i0, nh, pair, part);
         }
         for (int t = 0; t < steps; ++t) {
             const int live = cols - t * kTcN;
-            uint32_t r[64], d[64];
-            ok = mbar_wait_bounded(&s_full, t & 1, a.err);
-            if (__any_sync(0xffffffffu, !ok)) break;
-            tcgen05_fence_after_sync();
-            const uint32_t ts = tmem + Sh::kTmemS + my_tmem;
-            tmem_ld_x32<0>(ts, r);
-            tmem_ld_x32<32>(ts + 32, r);
+            uint32_t r[kTcHalf], d[kTcHalf];
             if (DKV || BIAS == kBiasWindow) {   // the vectors and the bias came with the tile
-                ok = mbar_wait_bounded(&c_full[t % NS], (t / NS) & 1, a.err);
-                if (__any_sync(0xffffffffu, !ok)) break;
+                wait(&c_full[t % NS], (t / NS) & 1);
             }
-            const float *vec = sVec + t % NS * 2 * kTcN;
+            const float *vec = sVec + t % NS * 2 * kTcN + first;
             const float *row = nullptr;   // the bias of this row and the tile's first column
             int x = 0, rel = 0;
-            const int W = DKV ? a.Wq : a.Wk, grid_rows = DKV ? a.Hq : a.Hk;
             if (BIAS) {
-                const int at = meet(t * kTcN);
-                x = t * kTcN % W;
+                const int at = meet0 + (DKV ? walk.rel : -walk.rel);
                 if (BIAS == kBiasWindow)
                     row = sBias + t % NS * p.bias.count + (at - row0 + my_row - bias_start(p.bias, at));
                 else
                     row = bias + at - row0 + my_row;
-                if (BIAS == kBiasGlobal || !p.bias.runs) bias_offsets(s_rel[warp], t * kTcN, live, W, a.P);
+                if (BIAS == kBiasGlobal || !p.bias.runs)
+                    bias_offsets(s_rel[warp], walk, first, live, inverse);
+                else
+                    walk.half(part, x, rel);
+                walk.next();
             }
+            wait(&s_full, t & 1);
+            tcgen05_fence_after_sync();
+            tmem_ld_x32<0>(tmem + Sh::kTmemS + my_tmem + first, r);
             tmem_wait_ld<0>(r);
-            tmem_wait_ld<32>(r);
             tcgen05_fence_before_sync();
             mbar_arrive(&s_free);
             const float2 cc = make_float2(c2, c2);
@@ -255,65 +264,66 @@ __global__ void __launch_bounds__(kTcThreads, TcBwdShape<DP, DKV>::kCtas)
             constexpr int kSign = DKV ? 1 : -1;
             if (!BIAS) {
 #pragma unroll
-                for (int c = 0; c < kTcN; c += 2) score(c, make_float2(0.0f, 0.0f));
+                for (int c = 0; c < kTcHalf; c += 2) score(c, make_float2(0.0f, 0.0f));
             } else if (BIAS == kBiasWindow && p.bias.runs) {
-                const int w = grid_rows == 1 ? INT_MAX : W;
-                bias_by_runs<kSign, 0>(row, x, rel, w, a.P - W, score);
-                bias_by_runs<kSign, 32>(row, x, rel, w, a.P - W, score);
+                bias_by_runs<kSign>(row, x, rel, walk, score);
             } else {
-                bias_by_table<kSign, 0>(row, s_rel[warp], score);
-                bias_by_table<kSign, 32>(row, s_rel[warp], score);
+                bias_by_table<kSign>(row, s_rel[warp], score);
             }
             if (live < kTcN) {   // columns that do not count, whatever they hold
+                asm volatile("" ::: "memory");   // a branch: the selects would cost every tile
 #pragma unroll
-                for (int c = 0; c < kTcN; ++c)
-                    if (c >= live) r[c] = __float_as_uint(-INFINITY);
+                for (int c = 0; c < kTcHalf; ++c)
+                    if (first + c >= live) r[c] = __float_as_uint(-INFINITY);
             }
-            if (DKV) {
+            const float2 minus = make_float2(-1.0f, -1.0f);
 #pragma unroll
-                for (int c = 0; c < kTcN; c += 4) {
-                    const float4 l = *reinterpret_cast<const float4 *>(vec + c);
-                    r[c] = __float_as_uint(exp2_approx(__uint_as_float(r[c]) - l.x));
-                    r[c + 1] = __float_as_uint(exp2_approx(__uint_as_float(r[c + 1]) - l.y));
-                    r[c + 2] = __float_as_uint(exp2_approx(__uint_as_float(r[c + 2]) - l.z));
-                    r[c + 3] = __float_as_uint(exp2_approx(__uint_as_float(r[c + 3]) - l.w));
-                }
-            } else {
-#pragma unroll
-                for (int c = 0; c < kTcN; ++c)
-                    r[c] = __float_as_uint(exp2_approx(__uint_as_float(r[c]) - row_lse));
+            for (int c = 0; c < kTcHalf; c += 4) {
+                float4 e = make_float4(row_lse, row_lse, row_lse, row_lse);
+                if (DKV) e = *reinterpret_cast<const float4 *>(vec + c);
+                const float2 u = fma_f32x2(make_float2(e.x, e.y), minus,
+                                           make_float2(__uint_as_float(r[c]), __uint_as_float(r[c + 1])));
+                const float2 v = fma_f32x2(make_float2(e.z, e.w), minus,
+                                           make_float2(__uint_as_float(r[c + 2]), __uint_as_float(r[c + 3])));
+                r[c] = __float_as_uint(exp2_approx(u.x));
+                r[c + 1] = __float_as_uint(exp2_approx(u.y));
+                r[c + 2] = __float_as_uint(exp2_approx(v.x));
+                r[c + 3] = __float_as_uint(exp2_approx(v.y));
             }
-            ok = mbar_wait_bounded(&dp_full, t & 1, a.err);
-            if (__any_sync(0xffffffffu, !ok)) break;
+            wait(&dp_full, t & 1);
             tcgen05_fence_after_sync();
-            tmem_ld_x32<0>(tmem + Sh::kTmemP + my_tmem, d);
-            tmem_ld_x32<32>(tmem + Sh::kTmemP + my_tmem + 32, d);
+            tmem_ld_x32<0>(tmem + Sh::kTmemP + my_tmem + first, d);
             tmem_wait_ld<0>(d);
-            tmem_wait_ld<32>(d);
-            float ds[kTcN];
+            float ds[kTcHalf];
 #pragma unroll
-            for (int c = 0; c < kTcN; c += 4) {
+            for (int c = 0; c < kTcHalf; c += 4) {
                 float4 e = make_float4(row_delta, row_delta, row_delta, row_delta);
                 if (DKV) e = *reinterpret_cast<const float4 *>(vec + kTcN + c);
-                ds[c] = __uint_as_float(r[c]) * (__uint_as_float(d[c]) - e.x);
-                ds[c + 1] = __uint_as_float(r[c + 1]) * (__uint_as_float(d[c + 1]) - e.y);
-                ds[c + 2] = __uint_as_float(r[c + 2]) * (__uint_as_float(d[c + 2]) - e.z);
-                ds[c + 3] = __uint_as_float(r[c + 3]) * (__uint_as_float(d[c + 3]) - e.w);
+                float2 u = fma_f32x2(make_float2(e.x, e.y), minus,
+                                     make_float2(__uint_as_float(d[c]), __uint_as_float(d[c + 1])));
+                float2 v = fma_f32x2(make_float2(e.z, e.w), minus,
+                                     make_float2(__uint_as_float(d[c + 2]), __uint_as_float(d[c + 3])));
+                u = mul_f32x2(u, make_float2(__uint_as_float(r[c]), __uint_as_float(r[c + 1])));
+                v = mul_f32x2(v, make_float2(__uint_as_float(r[c + 2]), __uint_as_float(r[c + 3])));
+                ds[c] = u.x;
+                ds[c + 1] = u.y;
+                ds[c + 2] = v.x;
+                ds[c + 3] = v.y;
             }
-            uint32_t w[32];
+            uint32_t w[kTcHalf / 2];
             if (DKV) {
                 const float2 up = make_float2(kWeightScale<T>, kWeightScale<T>);
 #pragma unroll
-                for (int c = 0; c < 32; ++c) {
+                for (int c = 0; c < kTcHalf / 2; ++c) {
                     const float2 e = mul_f32x2(
                         make_float2(__uint_as_float(r[2 * c]), __uint_as_float(r[2 * c + 1])), up);
                     w[c] = pack2<T>(e.x, e.y);
                 }
-                tmem_st_x32(tmem + Sh::kTmemP + my_tmem, w);
+                tmem_st_x16(tmem + Sh::kTmemP + my_tmem + first, w);
             }
 #pragma unroll
-            for (int c = 0; c < 32; ++c) w[c] = pack2<T>(ds[2 * c], ds[2 * c + 1]);
-            tmem_st_x32(tmem + Sh::kTmemP + my_tmem + kTcN / 2, w);
+            for (int c = 0; c < kTcHalf / 2; ++c) w[c] = pack2<T>(ds[2 * c], ds[2 * c + 1]);
+            tmem_st_x16(tmem + Sh::kTmemP + my_tmem + first + kTcHalf / 2, w);
             tmem_wait_st();
             tcgen05_fence_before_sync();
             mbar_arrive(&pd_ready);
@@ -321,8 +331,8 @@ __global__ void __launch_bounds__(kTcThreads, TcBwdShape<DP, DKV>::kCtas)
                 if (with_rel) win.add(a, ds, t * kTcN, live, keys, rel_out);
             }
         }
-        if (__all_sync(0xffffffffu, ok) && steps > 0) ok = mbar_wait_bounded(&finished, 0, a.err);
-        if (__all_sync(0xffffffffu, ok)) {
+        if (steps > 0) wait(&finished, 0);
+        if (ok) {
             tcgen05_fence_after_sync();
             const int64_t at = (((int64_t)n * rows + i) * a.H + h) * a.D;
             for (int which = 0; which < (DKV ? 2 : 1); ++which) {
@@ -330,7 +340,7 @@ __global__ void __launch_bounds__(kTcThreads, TcBwdShape<DP, DKV>::kCtas)
                 const float f = counts ? (which ? 1.0f / kWeightScale<T> : a.scale) : 0.0f;
                 const uint32_t acc = tmem + (which ? Sh::kTmemAcc2 : Sh::kTmemAcc1) + my_tmem;
 #pragma unroll 1
-                for (int c = 0; c < a.D; c += 32) {
+                for (int c = part * 32; c < a.D; c += 64) {   // every other chunk
                     uint32_t o[32];
                     if (steps > 0) {
                         tmem_ld_x32<0>(acc + c, o);
@@ -357,7 +367,7 @@ __global__ void __launch_bounds__(kTcThreads, TcBwdShape<DP, DKV>::kCtas)
     }
     tcgen05_fence_before_sync();
     __syncthreads();
-    if (warp == 4) tmem_dealloc(tmem, Sh::kTmemCols);
+    if (warp == kTcMmaWarp) tmem_dealloc(tmem, Sh::kTmemCols);
 }
 
 template <typename T, int DP, int BIAS, bool DKV>

@@ -2,12 +2,14 @@
 //
 // One CTA per 128 queries of one head; it walks the keys 64 at a time:
 //   S = Q K^T             tcgen05.mma, fp32 in TMEM, two buffers
-//   p = 2^(c S + bias - m)  one softmax thread per query, m its running reference
+//   p = 2^(c S + bias - m)  two softmax threads per query, m its running reference
 //   O += p V              tcgen05.mma with p (16-bit) read from TMEM, where it
 //                         overwrites the scores it came from
-// so scores and weights never leave the SM.  A fifth warp issues the TMA loads
-// and the MMAs: the scores of tile j + 1 are computed while the softmax warps
-// work on tile j.
+// so scores and weights never leave the SM.  The two threads of a query take 32
+// keys each and exchange their maxima through shared memory.  One thread of a
+// ninth warp issues the MMAs (the scores of tile j + 1 are computed while the
+// softmax warps work on tile j), one of a tenth the TMA loads: issued by one
+// warp with votes between, both took longer than the softmax.
 //
 // The reference m follows the row's maximum lazily: O and the row sum are
 // rescaled only when the maximum has grown by more than 2^8 since (the final
@@ -53,14 +55,15 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     constexpr int NS = Sh::kStages;
     constexpr bool kBf16 = sizeof(T) == 2 && __is_same(T, __nv_bfloat16);
     extern __shared__ unsigned char smem_raw[];
-    __shared__ uint64_t q_full, k_full[NS], v_full[NS], s_full[2], p_ready[2], pv_done, drained;
+    __shared__ uint64_t q_full, k_full[NS], v_full[NS], s_full[2], p_ready[2], pv_done[NS], cleared;
     __shared__ uint32_t tmem_base;
 
     const AttnArgs &a = p.a;
     unsigned char *tiles = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     unsigned char *sQ = tiles, *sK = tiles + Sh::kQBytes, *sV = sK + NS * Sh::kTileBytes;
     float *sBias = reinterpret_cast<float *>(tiles + Sh::kTileSmem);   // a window per stage
-    __shared__ __align__(16) int s_rel[4][kTcN];
+    __shared__ __align__(16) int s_rel[8][kTcHalf];
+    __shared__ float s_top[2][2][kTcM];   // of the two threads of a query, two tiles in turn
 
     const int q_tiles = (a.Lq + kTcM - 1) / kTcM;
     const int i0 = (int)(blockIdx.x % q_tiles) * kTcM;
@@ -71,19 +74,19 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     const int rq0 = rel_q(a, i0);
     const int keys = keys_of(a, n), T_tiles = (keys + kTcN - 1) / kTcN;
 
-    if (warp == 4) {
+    if (warp == kTcMmaWarp) {
         if (lane == 0) {
             mbar_init(&q_full, 1);
             for (int s = 0; s < NS; ++s) {
                 mbar_init(&k_full[s], 1);
                 mbar_init(&v_full[s], 1);
+                mbar_init(&pv_done[s], 1);
             }
             for (int b = 0; b < 2; ++b) {
                 mbar_init(&s_full[b], 1);
-                mbar_init(&p_ready[b], kTcM);
+                mbar_init(&p_ready[b], kTcSoft);
             }
-            mbar_init(&pv_done, 1);
-            mbar_init(&drained, 1);
+            mbar_init(&cleared, 1);
             fence_mbar_init();
         }
         __syncwarp();
@@ -95,111 +98,122 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     const uint32_t tmem = tmem_base, tmem_o = tmem + Sh::kTmemO;
     bool ok = true;
 
-    if (warp == 4) {
-        // ---------------------------------------------------- copies and MMAs
-        const uint32_t idesc_s = umma_idesc_f16(kBf16, kTcM, kTcN);
-        const int width = (a.D + 15) / 16 * 16;
-        const uint32_t idesc_o = umma_idesc_f16_bmn(kBf16, kTcM, width);
-        const uint32_t q_at = smem_u32(sQ), k_at = smem_u32(sK), v_at = smem_u32(sV);
-        const auto load = [&](int t) {   // one lane
-            const int s = t % NS;
-            mbar_arrive_expect_tx(&k_full[s], Sh::kTileBytes + (BIAS == kBiasWindow ? p.bias.count * 4 : 0));
-            tc_load<DP, kTcN>(sK + s * Sh::kTileBytes, p.k, n, h, t * kTcN, &k_full[s]);
-            if (BIAS == kBiasWindow)
-                bulk_copy_g2s(sBias + s * p.bias.count, bias + bias_start(p.bias, rq0 - rel_k(a, t * kTcN)),
-                              p.bias.count * 4, &k_full[s]);
-            mbar_arrive_expect_tx(&v_full[s], Sh::kTileBytes);
-            tc_load<DP, kTcN>(sV + s * Sh::kTileBytes, p.v, n, h, t * kTcN, &v_full[s]);
-        };
-        int loaded = 0;   // tiles whose copies were issued
+    const bool tail = keys % kTcN != 0;   // the last tile holds masked keys
+
+    if (warp == kTcCopyWarp) {
+        // ---------------------------------------------------- copies
         if (lane == 0 && T_tiles > 0) {
             mbar_arrive_expect_tx(&q_full, Sh::kQBytes);
             tc_load<DP, kTcM>(sQ, p.q, n, h, i0, &q_full);
-            for (; loaded < NS && loaded < T_tiles; ++loaded) load(loaded);
+            for (int t = 0; t < T_tiles; ++t) {
+                const int s = t % NS;
+                if (t >= NS) {   // the stage's last tile is consumed
+                    ok = tc_wait(&pv_done[s], (t / NS - 1) & 1, a.err);
+                    if (!ok) break;
+                }
+                mbar_arrive_expect_tx(&k_full[s], Sh::kTileBytes + (BIAS == kBiasWindow ? p.bias.count * 4 : 0));
+                tc_load<DP, kTcN>(sK + s * Sh::kTileBytes, p.k, n, h, t * kTcN, &k_full[s]);
+                if (BIAS == kBiasWindow)
+                    bulk_copy_g2s(sBias + s * p.bias.count,
+                                  bias + bias_start(p.bias, rq0 - rel_k(a, t * kTcN)),
+                                  p.bias.count * 4, &k_full[s]);
+                mbar_arrive_expect_tx(&v_full[s], Sh::kTileBytes);
+                tc_load<DP, kTcN>(sV + s * Sh::kTileBytes, p.v, n, h, t * kTcN, &v_full[s]);
+            }
         }
-        loaded = __shfl_sync(0xffffffffu, loaded, 0);
-        if (T_tiles > 0) {
-            ok = mbar_wait_bounded(&q_full, 0, a.err) && mbar_wait_bounded(&k_full[0], 0, a.err);
-            ok = __all_sync(0xffffffffu, ok);
-            if (ok && lane == 0) {
-                tc_scores<kTcN>(tmem, q_at, k_at, idesc_s, width / 16);
+        __syncwarp();
+        if (T_tiles > 0 && tail) {   // values of masked keys must not reach the product
+            const int t = T_tiles - 1;
+            ok = tc_wait(&v_full[t % NS], (t / NS) & 1, a.err);
+            __syncwarp();
+            tc_clear_rows<DP, kTcN>(sV + t % NS * Sh::kTileBytes, keys - t * kTcN);
+            if (lane == 0) mbar_arrive(&cleared);
+        }
+        // every copy lands before the block may leave (they have, unless a wait gave up)
+        for (int t = max(0, T_tiles - NS); t < T_tiles; ++t) {
+            tc_wait(&k_full[t % NS], (t / NS) & 1, a.err);
+            tc_wait(&v_full[t % NS], (t / NS) & 1, a.err);
+        }
+    } else if (warp == kTcMmaWarp) {
+        // ---------------------------------------------------- MMAs, one thread
+        if (lane == 0 && T_tiles > 0) {
+            const uint32_t idesc_s = umma_idesc_f16(kBf16, kTcM, kTcN);
+            const int steps = (a.D + 15) / 16;
+            const uint32_t idesc_o = umma_idesc_f16_bmn(kBf16, kTcM, steps * 16);
+            const uint32_t q_lo = umma_lo_kmajor(smem_u32(sQ)), k_lo = umma_lo_kmajor(smem_u32(sK));
+            const uint32_t v_lo = umma_lo_mnmajor(smem_u32(sV), kTcN * 128);
+            ok = tc_wait(&q_full, 0, a.err) && tc_wait(&k_full[0], 0, a.err);
+            if (ok) {
+                tc_scores<DP>(tmem, q_lo, k_lo, idesc_s, steps);
                 umma_commit(&s_full[0]);
             }
-        }
-        for (int j = 0; j < T_tiles && ok; ++j) {
-            const int s = j % NS, ph = (j / NS) & 1;
-            if (j > 0) {   // tile j - 1 is consumed: its stage takes the next copy
-                ok = mbar_wait_bounded(&pv_done, (j - 1) & 1, a.err);
-                if (__any_sync(0xffffffffu, !ok)) break;
-                if (loaded < T_tiles) {
-                    if (lane == 0) load(loaded);
-                    ++loaded;
-                }
-            }
-            if (j + 1 < T_tiles) {   // the other score buffer: its weights are consumed
-                const int s1 = (j + 1) % NS;
-                ok = mbar_wait_bounded(&k_full[s1], ((j + 1) / NS) & 1, a.err);
-                if (__any_sync(0xffffffffu, !ok)) break;
-                if (lane == 0) {
+            for (int j = 0; j < T_tiles && ok; ++j) {
+                const int s = j % NS;
+                if (j + 1 < T_tiles) {   // scores into the other buffer: its weights are consumed
+                    const int s1 = (j + 1) % NS;
+                    if (j > 0) ok = tc_wait(&pv_done[(j - 1) % NS], ((j - 1) / NS) & 1, a.err);
+                    ok = ok && tc_wait(&k_full[s1], ((j + 1) / NS) & 1, a.err);
+                    if (!ok) break;
                     tcgen05_fence_after_sync();
-                    tc_scores<kTcN>(tmem + ((j + 1) & 1) * kTcN, q_at, k_at + s1 * Sh::kTileBytes,
-                                    idesc_s, width / 16);
+                    tc_scores<DP>(tmem + ((j + 1) & 1) * kTcN, q_lo, k_lo + s1 * (Sh::kTileBytes / 16),
+                                  idesc_s, steps);
                     umma_commit(&s_full[(j + 1) & 1]);
                 }
-            }
-            ok = mbar_wait_bounded(&v_full[s], ph, a.err);
-            if (__any_sync(0xffffffffu, !ok)) break;
-            if (keys - j * kTcN < kTcN)
-                tc_clear_rows<DP, kTcN>(sV + s * Sh::kTileBytes, keys - j * kTcN);
-            ok = mbar_wait_bounded(&p_ready[j & 1], (j / 2) & 1, a.err);
-            if (__any_sync(0xffffffffu, !ok)) break;
-            if (lane == 0) {
+                ok = tc_wait(&v_full[s], (j / NS) & 1, a.err);
+                if (tail && j == T_tiles - 1) ok = ok && tc_wait(&cleared, 0, a.err);
+                ok = ok && tc_wait(&p_ready[j & 1], (j / 2) & 1, a.err);
+                if (!ok) break;
                 tcgen05_fence_after_sync();
-                tc_weighted<kTcN>(tmem_o, tmem + (j & 1) * kTcN, v_at + s * Sh::kTileBytes, idesc_o,
-                                  j > 0);
-                umma_commit(&pv_done);
+                tc_weighted(tmem_o, tmem + (j & 1) * kTcN, v_lo + s * (Sh::kTileBytes / 16), idesc_o,
+                            j > 0);
+                umma_commit(&pv_done[s]);
+            }
+            if (!ok) {   // a wait gave up: let the MMAs end before TMEM is released
+                umma_commit(&q_full);
+                tc_wait(&q_full, 1, a.err);
             }
         }
-        if (!__all_sync(0xffffffffu, ok)) {
-            // a wait gave up: let this CTA's copies and MMAs end before it leaves
-            if (lane == 0) umma_commit(&drained);
-            mbar_wait_bounded(&drained, 0, a.err);
-            for (int t = max(0, loaded - NS); t < loaded; ++t) {
-                mbar_wait_bounded(&k_full[t % NS], (t / NS) & 1, a.err);
-                mbar_wait_bounded(&v_full[t % NS], (t / NS) & 1, a.err);
-            }
-        }
+        __syncwarp();
     } else {
-        // ---------------------------------------------------- softmax, a row per thread
-        const uint32_t my_tmem = (uint32_t)(warp * 32) << 16;   // this warp's TMEM lanes
-        const int i = i0 + threadIdx.x;
+        // ---------------------------------------------------- softmax
+        // After a wait that gave up a warp goes on without waiting (and without
+        // storing), so that its partner finds it at every pair_sync.
+        const auto wait = [&](uint64_t *bar, int parity) {
+            if (ok) ok = __all_sync(0xffffffffu, tc_wait(bar, parity, a.err));
+        };
+        const int pair = warp % 4, part = warp / 4, lane_row = pair * 32 + lane;
+        const uint32_t my_tmem = (uint32_t)(pair * 32) << 16;   // this warp's TMEM lanes
+        const int first = part * kTcHalf;                       // this thread's columns of a tile
+        const int i = i0 + lane_row;
         const float c2 = a.scale * kLog2e;
         const int rq = BIAS ? rel_q(a, min(i, a.Lq - 1)) : 0;
+        TileWalk walk;
+        if (BIAS) walk.init(a.Hk, a.Wk, a.P);
+        const int inverse = 65536 / a.Wk + 1;
         float m = -INFINITY, l = 0.0f;
         for (int j = 0; j < T_tiles; ++j) {
             const int live = keys - j * kTcN;
-            uint32_t r[64];
-            ok = mbar_wait_bounded(&s_full[j & 1], (j / 2) & 1, a.err);
-            if (__any_sync(0xffffffffu, !ok)) break;
-            tcgen05_fence_after_sync();
-            const uint32_t ts = tmem + my_tmem + (j & 1) * kTcN;
-            tmem_ld_x32<0>(ts, r);
+            uint32_t r[kTcHalf];
             const float *row = nullptr;   // the bias of this query and the tile's first key
             int x = 0, rel = 0;
             if (BIAS) {
-                const int rk = rel_k(a, j * kTcN);
-                x = j * kTcN % a.Wk;
                 if (BIAS == kBiasWindow) {
-                    ok = mbar_wait_bounded(&k_full[j % NS], (j / NS) & 1, a.err);
-                    if (__any_sync(0xffffffffu, !ok)) break;
-                    row = sBias + j % NS * p.bias.count + (rq - rk - bias_start(p.bias, rq0 - rk));
+                    wait(&k_full[j % NS], (j / NS) & 1);
+                    row = sBias + j % NS * p.bias.count +
+                          (rq - walk.rel - bias_start(p.bias, rq0 - walk.rel));
                 } else {
-                    row = bias + rq - rk;
+                    row = bias + rq - walk.rel;
                 }
-                if (BIAS == kBiasGlobal || !p.bias.runs) bias_offsets(s_rel[warp], j * kTcN, live, a.Wk, a.P);
+                if (BIAS == kBiasGlobal || !p.bias.runs)
+                    bias_offsets(s_rel[warp], walk, first, live, inverse);
+                else
+                    walk.half(part, x, rel);
+                walk.next();
             }
-            const int W = a.Hk == 1 ? INT_MAX : a.Wk;
-            float top4[4] = {m, -INFINITY, -INFINITY, -INFINITY};
+            wait(&s_full[j & 1], (j / 2) & 1);
+            tcgen05_fence_after_sync();
+            const uint32_t ts = tmem + my_tmem + (j & 1) * kTcN + first;
+            tmem_ld_x32<0>(ts, r);
             const float2 cc = make_float2(c2, c2);
             const auto score = [&](int c, float2 b) {
                 const float2 v = fma_f32x2(
@@ -207,43 +221,40 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                 r[c] = __float_as_uint(v.x);
                 r[c + 1] = __float_as_uint(v.y);
             };
-            const auto half = [&](auto first) {
-                constexpr int C0 = decltype(first)::value;
-                if (!BIAS) {
-#pragma unroll
-                    for (int c = C0; c < C0 + 32; c += 2) score(c, make_float2(0.0f, 0.0f));
-                } else if (BIAS == kBiasWindow && p.bias.runs) {
-                    bias_by_runs<-1, C0>(row, x, rel, W, a.P - a.Wk, score);
-                } else {
-                    bias_by_table<-1, C0>(row, s_rel[warp], score);
-                }
-                if (live < kTcN) {   // masked keys, whatever they hold
-#pragma unroll
-                    for (int c = C0; c < C0 + 32; ++c)
-                        if (c >= live) r[c] = __float_as_uint(-INFINITY);
-                }
-#pragma unroll
-                for (int c = C0; c < C0 + 32; c += 2)
-                    top4[c / 2 % 4] = fmaxf(fmaxf(top4[c / 2 % 4], __uint_as_float(r[c])),
-                                            __uint_as_float(r[c + 1]));
-            };
             tmem_wait_ld<0>(r);
-            tmem_ld_x32<32>(ts + 32, r);
-            half(std::integral_constant<int, 0>());
-            tmem_wait_ld<32>(r);
-            half(std::integral_constant<int, 32>());
-            const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
+            if (!BIAS) {
+#pragma unroll
+                for (int c = 0; c < kTcHalf; c += 2) score(c, make_float2(0.0f, 0.0f));
+            } else if (BIAS == kBiasWindow && p.bias.runs) {
+                bias_by_runs<-1>(row, x, rel, walk, score);
+            } else {
+                bias_by_table<-1>(row, s_rel[warp], score);
+            }
+            if (live < kTcN) {   // masked keys, whatever they hold
+                asm volatile("" ::: "memory");   // a branch: the selects would cost every tile
+#pragma unroll
+                for (int c = 0; c < kTcHalf; ++c)
+                    if (first + c >= live) r[c] = __float_as_uint(-INFINITY);
+            }
+            float top4[4] = {m, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int c = 0; c < kTcHalf; c += 2)
+                top4[c / 2 % 4] = fmaxf(fmaxf(top4[c / 2 % 4], __uint_as_float(r[c])),
+                                        __uint_as_float(r[c + 1]));
+            float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
+            s_top[j & 1][part][lane_row] = top;
+            pair_sync(pair);
+            top = fmaxf(top, s_top[j & 1][part ^ 1][lane_row]);
             // (top > m + growth) also takes a row out of m = -inf
             if (j == 0) {
                 m = top;
             } else if (__any_sync(0xffffffffu, top > m + kLazyGrowth)) {
                 const float keep = top == -INFINITY ? 1.0f : exp2_approx(m - top);
-                ok = mbar_wait_bounded(&pv_done, (j - 1) & 1, a.err);
-                if (__any_sync(0xffffffffu, !ok)) break;
+                wait(&pv_done[(j - 1) % NS], ((j - 1) / NS) & 1);
                 tcgen05_fence_after_sync();
                 const uint32_t to = tmem_o + my_tmem;
 #pragma unroll 1
-                for (int d = 0; d < DP; d += 32) {
+                for (int d = part * 32; d < DP; d += 64) {   // every other chunk of O
                     uint32_t o[32];
                     tmem_ld_x32<0>(to + d, o);
                     tmem_wait_ld<0>(o);
@@ -258,38 +269,36 @@ __global__ void __launch_bounds__(kTcThreads, 2)
             }
             // a row with no key yet: weights 0
             const float ref = m == -INFINITY ? 0.0f : m - kWeightShift<T>;
-            float2 sum[4] = {};
+            float2 sum[2] = {};
             const float2 one = make_float2(1.0f, 1.0f), shift = make_float2(-ref, -ref);
-            uint32_t w[32];
+            uint32_t w[kTcHalf / 2];
 #pragma unroll
-            for (int c = 0; c < kTcN; c += 2) {
+            for (int c = 0; c < kTcHalf; c += 2) {
                 float2 e = fma_f32x2(
                     make_float2(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), one, shift);
                 e.x = exp2_approx(e.x);
                 e.y = exp2_approx(e.y);
-                sum[c / 2 % 4] = fma_f32x2(e, one, sum[c / 2 % 4]);
+                sum[c / 2 % 2] = fma_f32x2(e, one, sum[c / 2 % 2]);
                 w[c / 2] = pack2<T>(e.x, e.y);
             }
-            tmem_st_x32(ts, w);
-            l += ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y)) +
-                 ((sum[2].x + sum[2].y) + (sum[3].x + sum[3].y));
+            tmem_st_x16(ts, w);
+            l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
             tmem_wait_st();
             tcgen05_fence_before_sync();
             mbar_arrive(&p_ready[j & 1]);
         }
-        // S of the last tile was ready before the product of the one before it
-        // had to be, so this warp may be two phases ahead of pv_done: a parity
-        // wait tells neighbouring phases apart only, hence both in turn
-        if (__all_sync(0xffffffffu, ok) && T_tiles > 1)
-            ok = mbar_wait_bounded(&pv_done, (T_tiles - 2) & 1, a.err);
-        if (__all_sync(0xffffffffu, ok) && T_tiles > 0)
-            ok = mbar_wait_bounded(&pv_done, (T_tiles - 1) & 1, a.err);
-        if (__all_sync(0xffffffffu, ok)) {
+        // the product before the last may be unfinished here, but the one a stage
+        // earlier is done, so the phase's parity tells
+        if (T_tiles > 0) wait(&pv_done[(T_tiles - 1) % NS], ((T_tiles - 1) / NS) & 1);
+        if (ok) {
             tcgen05_fence_after_sync();
+            s_top[T_tiles & 1][part][lane_row] = l;   // the row's other half of the sum
+            pair_sync(pair);
+            l += s_top[T_tiles & 1][part ^ 1][lane_row];
             const float inv = l != 0.0f ? 1.0f / l : 0.0f;
             T *out = (T *)p.O + (((int64_t)n * a.Lq + i) * a.H + h) * a.D;
 #pragma unroll 1
-            for (int d = 0; d < a.D; d += 32) {
+            for (int d = part * 32; d < a.D; d += 64) {
                 uint32_t o[32];
                 if (T_tiles > 0) {
                     tmem_ld_x32<0>(tmem_o + my_tmem + d, o);
@@ -312,14 +321,14 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                         }
                 }
             }
-            if (i < a.Lq && p.lse)
+            if (part == 0 && i < a.Lq && p.lse)
                 p.lse[((int64_t)n * a.H + h) * a.Lq + i] =
                     l != 0.0f ? (m - kWeightShift<T> + log2f(l)) * kLn2 : -INFINITY;
         }
     }
     tcgen05_fence_before_sync();
     __syncthreads();
-    if (warp == 4) tmem_dealloc(tmem, Sh::kTmemCols);
+    if (warp == kTcMmaWarp) tmem_dealloc(tmem, Sh::kTmemCols);
 }
 
 template <typename T, int DP, int BIAS>
