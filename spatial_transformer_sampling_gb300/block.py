@@ -6,18 +6,47 @@ only check and marshal; every step of the computation runs in libgs's kernels.
 import ctypes
 import functools
 
-from . import (AttentionAttrs, _check_tensors, _dtype_code, _i64, _ok, _shape_error, _torch,
-               load_library)
+from . import AttentionAttrs, GsError, _i64, _ok, _shape_error, _torch, load_library
+
+
+class _Host:
+    """torch, the library and the dtype codes, looked up once: a small call is bound by what the
+    host does for it."""
+    torch = lib = stream = codes = None
+
+
+def _host():
+    if _Host.lib is None:
+        torch = _torch()
+        _Host.torch = torch
+        _Host.codes = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+        # the lookup behind torch.cuda.current_stream, without making a Stream object
+        _Host.stream = torch._C._cuda_getCurrentRawStream
+        _Host.lib = load_library()
+    return _Host
 
 
 def _p(t):
     return t.data_ptr() if t is not None else None
 
 
-def _current(t):
-    """Handle of the current stream of t's device.  The lookup behind
-    torch.cuda.current_stream, without making a Stream object (2 us of a call's 15)."""
-    return _torch()._C._cuda_getCurrentRawStream(t.device.index)
+def _check_like(ref, what, t, shape):
+    """t is contiguous, of ref's dtype and device, and of the given shape."""
+    if t.dtype != ref.dtype or t.device != ref.device:
+        raise ValueError("all tensors of one call share dtype and device")
+    if not t.is_contiguous():
+        raise ValueError("libgs takes contiguous tensors")
+    if t.shape != shape:
+        _shape_error(what, t.shape, shape)
+
+
+def _check_input(X):
+    if X.device.type != "cuda":
+        raise ValueError("libgs takes CUDA tensors")
+    if not X.is_contiguous():
+        raise ValueError("libgs takes contiguous tensors")
+    if X.dtype not in _host().codes:
+        raise TypeError(f"unsupported dtype {X.dtype}")
 
 
 def _scratch(workspace, nbytes, like):
@@ -26,7 +55,7 @@ def _scratch(workspace, nbytes, like):
     if isinstance(workspace, str):
         if workspace != "auto":
             raise ValueError(f"workspace must be a tensor, None or 'auto', not {workspace!r}")
-        torch = _torch()
+        torch = _host().torch
         workspace = (torch.empty(nbytes, dtype=torch.uint8, device=like.device) if nbytes
                      else None)
     elif workspace is not None and (workspace.device != like.device
@@ -38,51 +67,51 @@ def _scratch(workspace, nbytes, like):
 
 
 def _check_f32(t, shape, what, like):
-    torch = _torch()
-    if t.dtype != torch.float32 or t.device != like.device or not t.is_contiguous():
+    if t.dtype != _host().torch.float32 or t.device != like.device or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous float32 tensor on the inputs' device")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         _shape_error(what, t.shape, shape)
 
 
 # ------------------------------------------------------------------ layer norm
 
-def _norm_dims(X, axis):
-    if not -X.dim() <= axis < X.dim():
-        raise ValueError(f"axis {axis} out of range for X of shape {tuple(X.shape)}")
-    axis %= X.dim()
+@functools.lru_cache(maxsize=256)
+def _norm_dims(shape, axis):
+    """(rows, D, shape of the normalised axes, shape of the statistics) of a layer norm over the
+    axes of ``shape`` from ``axis`` on."""
+    if not -len(shape) <= axis < len(shape):
+        raise ValueError(f"axis {axis} out of range for X of shape {tuple(shape)}")
+    axis %= len(shape)
     rows = D = 1
-    for n in X.shape[:axis]:
+    for n in shape[:axis]:
         rows *= n
-    for n in X.shape[axis:]:
+    for n in shape[axis:]:
         D *= n
-    return axis, rows, D
-
-
-def _check_norm_vectors(X, axis, **vectors):
-    for what, t in vectors.items():
-        if t is not None and t.shape != X.shape[axis:]:
-            _shape_error(what, t.shape, X.shape[axis:])
+    return rows, D, tuple(shape[axis:]), tuple(shape[:axis]) + (1,) * (len(shape) - axis)
 
 
 def gs_layer_norm(X, Scale, B=None, axis=-1, epsilon=1e-5, out=None):
     """LayerNormalization of X over its axes from ``axis`` on: (Y, Mean, InvStdDev).  Scale and B
     have the shape of the normalised axes; Mean and InvStdDev are float32 with X's leading axes
     and ones in the place of the normalised ones."""
-    torch = _torch()
-    axis, rows, D = _norm_dims(X, axis)
-    _check_tensors(X, Scale, B, out)
-    _check_norm_vectors(X, axis, Scale=Scale, B=B)
+    rows, D, inner, kept = _norm_dims(X.shape, axis)
+    _check_input(X)
+    _check_like(X, "Scale", Scale, inner)
+    if B is not None:
+        _check_like(X, "B", B, inner)
+    h = _host()
+    empty, device = h.torch.empty, X.device
     if out is None:
-        out = torch.empty_like(X)
-    elif out.shape != X.shape:
-        _shape_error("out", out.shape, X.shape)
-    kept = tuple(X.shape[:axis]) + (1,) * (X.dim() - axis)
-    mean = torch.empty(kept, dtype=torch.float32, device=X.device)
-    inv = torch.empty_like(mean)
-    _ok(load_library().gs_layer_norm(X.data_ptr(), Scale.data_ptr(), _p(B), rows, D,
-                                     _dtype_code(X), epsilon, out.data_ptr(), mean.data_ptr(),
-                                     inv.data_ptr(), _current(X)), "gs_layer_norm")
+        out = empty(X.shape, dtype=X.dtype, device=device)
+    else:
+        _check_like(X, "out", out, X.shape)
+    mean = empty(kept, dtype=h.torch.float32, device=device)
+    inv = empty(kept, dtype=h.torch.float32, device=device)
+    status = h.lib.gs_layer_norm(X.data_ptr(), Scale.data_ptr(), _p(B), rows, D, h.codes[X.dtype],
+                                 epsilon, out.data_ptr(), mean.data_ptr(), inv.data_ptr(),
+                                 h.stream(device.index))
+    if status:
+        raise GsError(status, "gs_layer_norm")
     return out, mean, inv
 
 
@@ -98,22 +127,24 @@ def gs_layer_norm_backward_workspace_size(rows, D):
 def gs_layer_norm_backward(dY, X, Scale, Mean, InvStdDev, axis=-1, workspace="auto"):
     """Gradient of gs_layer_norm: (dX, dScale, dB).  ``workspace``: "auto", or a device tensor of
     at least gs_layer_norm_backward_workspace_size bytes."""
-    torch = _torch()
-    axis, rows, D = _norm_dims(X, axis)
-    _check_tensors(X, dY, Scale)
-    if dY.shape != X.shape:
-        _shape_error("dY", dY.shape, X.shape)
-    _check_norm_vectors(X, axis, Scale=Scale)
-    kept = tuple(X.shape[:axis]) + (1,) * (X.dim() - axis)
+    rows, D, inner, kept = _norm_dims(X.shape, axis)
+    _check_input(X)
+    _check_like(X, "dY", dY, X.shape)
+    _check_like(X, "Scale", Scale, inner)
     _check_f32(Mean, kept, "Mean", X)
     _check_f32(InvStdDev, kept, "InvStdDev", X)
-    dX, dScale, dB = torch.empty_like(X), torch.empty_like(Scale), torch.empty_like(Scale)
-    nbytes = gs_layer_norm_backward_workspace_size(rows, D)
-    ws, have, _keep = _scratch(workspace, nbytes, X)
-    _ok(load_library().gs_layer_norm_backward(
+    h = _host()
+    empty, device, dt = h.torch.empty, X.device, X.dtype
+    dX = empty(X.shape, dtype=dt, device=device)
+    dScale = empty(inner, dtype=dt, device=device)
+    dB = empty(inner, dtype=dt, device=device)
+    ws, have, _keep = _scratch(workspace, gs_layer_norm_backward_workspace_size(rows, D), X)
+    status = h.lib.gs_layer_norm_backward(
         dY.data_ptr(), X.data_ptr(), Scale.data_ptr(), Mean.data_ptr(), InvStdDev.data_ptr(), rows,
-        D, _dtype_code(X), ws, have, dX.data_ptr(), dScale.data_ptr(), dB.data_ptr(),
-        _current(X)), "gs_layer_norm_backward")
+        D, h.codes[dt], ws, have, dX.data_ptr(), dScale.data_ptr(), dB.data_ptr(),
+        h.stream(device.index))
+    if status:
+        raise GsError(status, "gs_layer_norm_backward")
     return dX, dScale, dB
 
 
@@ -123,16 +154,20 @@ def gs_dropout(X, ratio=0.5, seed=0, offset=0, residual=None, out=None):
     """residual + dropout(X) with the mask of (seed, offset), which is stored nowhere.  The
     gradient with respect to X is ``gs_dropout(dY, ratio, seed, offset)``.  ``out`` may be X or
     residual itself."""
-    _check_tensors(X, residual, out)
-    for what, t in (("residual", residual), ("out", out)):
-        if t is not None and t.shape != X.shape:
-            _shape_error(what, t.shape, X.shape)
+    _check_input(X)
+    if residual is not None:
+        _check_like(X, "residual", residual, X.shape)
     if not 0 <= seed < 1 << 64 or not 0 <= offset < 1 << 64:
         raise ValueError("seed and offset are unsigned 64-bit numbers")
+    h = _host()
     if out is None:
-        out = _torch().empty_like(X)
-    _ok(load_library().gs_dropout(X.data_ptr(), _p(residual), X.numel(), _dtype_code(X), ratio,
-                                  seed, offset, out.data_ptr(), _current(X)), "gs_dropout")
+        out = h.torch.empty(X.shape, dtype=X.dtype, device=X.device)
+    else:
+        _check_like(X, "out", out, X.shape)
+    status = h.lib.gs_dropout(X.data_ptr(), _p(residual), X.numel(), h.codes[X.dtype], ratio, seed,
+                              offset, out.data_ptr(), h.stream(X.device.index))
+    if status:
+        raise GsError(status, "gs_dropout")
     return out
 
 
@@ -188,7 +223,9 @@ class _Plan:
     def __init__(self, Q, K, V, table, q_extent, k_extent, scale):
         self.attrs = _attention_attrs(Q, K, V, table, q_extent, k_extent, scale)
         self.ref = ctypes.byref(self.attrs)
-        self.code = _dtype_code(Q)
+        if Q.dtype not in _host().codes:
+            raise TypeError(f"unsupported dtype {Q.dtype}")
+        self.code = _host().codes[Q.dtype]
         at = self.attrs
         self.lse_shape = (at.N, at.H, Q.shape[1])
         self.entries = ((at.q_extent[0] + at.k_extent[0] - 1)
@@ -206,7 +243,7 @@ _MOST_PLANS = 256
 
 
 def _plan(Q, K, V, table, buckets, q_extent, k_extent, k_len, scale):
-    torch = _torch()
+    torch = _host().torch
     key = (Q.shape, Q.stride(), K.shape, K.stride(), V.shape, V.stride(), Q.dtype,
            None if table is None else table.shape, q_extent, k_extent, scale)
     try:
@@ -263,18 +300,20 @@ def gs_attention(Q, K, V, table=None, buckets=None, q_extent=None, k_extent=None
     ``q_extent`` / ``k_extent`` are the tokens' grids (default (1, L)); ``k_len`` (N) int32 masks
     the keys from there on; ``scale`` defaults to 1 / sqrt(D).  O is dense (N, Lq, H, D), LSE
     float32 (N, H, Lq)."""
-    torch = _torch()
     plan = _plan(Q, K, V, table, buckets, q_extent, k_extent, k_len, scale)
+    h = _host()
+    empty, device = h.torch.empty, Q.device
     if out is None:
-        out = torch.empty(Q.shape, dtype=Q.dtype, device=Q.device)
-    elif (out.shape != Q.shape or not out.is_contiguous() or out.dtype != Q.dtype
-          or out.device != Q.device):
-        raise ValueError(f"out must be dense {tuple(Q.shape)} of Q's dtype and device")
-    lse = torch.empty(plan.lse_shape, dtype=torch.float32, device=Q.device)
+        out = empty(Q.shape, dtype=Q.dtype, device=device)
+    else:
+        _check_like(Q, "out", out, Q.shape)
+    lse = empty(plan.lse_shape, dtype=h.torch.float32, device=device)
     ws, have, _keep = _scratch(workspace, plan.workspace(False), Q)
-    _ok(load_library().gs_attention(Q.data_ptr(), K.data_ptr(), V.data_ptr(), _p(table),
-                                    _p(buckets), _p(k_len), plan.ref, plan.code, ws, have,
-                                    out.data_ptr(), lse.data_ptr(), _current(Q)), "gs_attention")
+    status = h.lib.gs_attention(Q.data_ptr(), K.data_ptr(), V.data_ptr(), _p(table), _p(buckets),
+                                _p(k_len), plan.ref, plan.code, ws, have, out.data_ptr(),
+                                lse.data_ptr(), h.stream(device.index))
+    if status:
+        raise GsError(status, "gs_attention")
     return out, lse
 
 
@@ -282,20 +321,22 @@ def gs_attention_backward(dO, Q, K, V, O, LSE, table=None, buckets=None, q_exten
                           k_extent=None, k_len=None, scale=None, workspace="auto"):
     """Gradient of gs_attention: [dQ, dK, dV, dTable] (the first three without a table); dQ, dK
     and dV are dense (N, L, H, D)."""
-    torch = _torch()
     plan = _plan(Q, K, V, table, buckets, q_extent, k_extent, k_len, scale)
-    for what, t in (("dO", dO), ("O", O)):
-        if t.shape != Q.shape:
-            _shape_error(what, t.shape, Q.shape)
-        if not t.is_contiguous() or t.dtype != Q.dtype or t.device != Q.device:
-            raise ValueError(f"{what} must be dense, of Q's dtype and device")
+    _check_like(Q, "dO", dO, Q.shape)
+    _check_like(Q, "O", O, Q.shape)
     _check_f32(LSE, plan.lse_shape, "LSE", Q)
-    made = [torch.empty(t.shape, dtype=Q.dtype, device=Q.device)
-            for t in ((Q, K, V) if table is None else (Q, K, V, table))]
+    h = _host()
+    empty, device, dt = h.torch.empty, Q.device, Q.dtype
+    made = [empty(Q.shape, dtype=dt, device=device), empty(K.shape, dtype=dt, device=device),
+            empty(K.shape, dtype=dt, device=device)]
+    if table is not None:
+        made.append(empty(table.shape, dtype=dt, device=device))
     ws, have, _keep = _scratch(workspace, plan.workspace(True), Q)
-    _ok(load_library().gs_attention_backward(
+    status = h.lib.gs_attention_backward(
         dO.data_ptr(), Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(), LSE.data_ptr(),
         _p(table), _p(buckets), _p(k_len), plan.ref, plan.code, ws, have, made[0].data_ptr(),
         made[1].data_ptr(), made[2].data_ptr(), made[3].data_ptr() if table is not None else None,
-        _current(Q)), "gs_attention_backward")
+        h.stream(device.index))
+    if status:
+        raise GsError(status, "gs_attention_backward")
     return made

@@ -199,45 +199,35 @@ cudaError_t launch_attn_backward(const AttnArgs &args, const AttnPtrs &p, void *
     bool tc = false;
     if constexpr (sizeof(T) == 2) tc = tc_backward_views<T>(a, p, kv, q);
     const int pairs = a.N * a.H;
-    RelArgs none = {}, part = {};
     cudaError_t e = launch_attn_delta<T>(a, p, lse2, delta, s);
     if (e != cudaSuccess) return e;
-    if constexpr (sizeof(T) == 2) {
-        if (tc) {
-            kv.a = q.a = a;
-            kv.bias = tc_bias_of(a, true);
-            q.bias = tc_bias_of(a, false);
-            kv.bias.base = q.bias.base = bias;
-            kv.bias.stride = q.bias.stride = a.bias_stride;
-            kv.lse2 = q.lse2 = lse2;
-            kv.delta = q.delta = delta;
-            kv.out1 = p.dK;
-            kv.out2 = p.dV;
-            q.out1 = p.dQ;
-            q.out2 = nullptr;
-            kv.rel = none;
-        }
-    }
-    const auto run = [&](auto dkv, const RelArgs &r, int heads) {
-        constexpr bool DKV = decltype(dkv)::value;
-        if constexpr (sizeof(T) == 2) {
-            if (tc) {
-                TcBwdArgs &args = DKV ? kv : q;
-                args.rel = r;
-                return launch_attn_tc_bwd_kernel<T, DKV>(args, heads, s);
-            }
-        }
-        return launch_attn_simt_bwd<T, DKV>(a, p, bias, lse2, delta, r, heads, s);
-    };
-    e = run(std::true_type(), none, pairs);
-    if (e != cudaSuccess) return e;
+    RelArgs part = {};
     part.window = bias ? rel_window_of(a) : 0;
     part.stride = part.window ? (int)rel_stride_of(a) : 0;
     part.part = (float *)(ws + w.part);
+    if (tc) {
+        kv.a = q.a = a;
+        kv.bias = tc_bias_of(a, true);
+        q.bias = tc_bias_of(a, false);
+        kv.bias.base = q.bias.base = bias;
+        kv.bias.stride = q.bias.stride = a.bias_stride;
+        kv.lse2 = q.lse2 = lse2;
+        kv.delta = q.delta = delta;
+        kv.out1 = p.dK;
+        kv.out2 = p.dV;
+        q.out1 = p.dQ;
+        q.out2 = nullptr;
+        kv.rel = RelArgs();
+    }
     const int heads = part.window ? (int)rel_heads_of(a) : pairs;
     for (part.head0 = 0; part.head0 < pairs; part.head0 += heads) {
         const int now = std::min(heads, pairs - part.head0);
-        e = run(std::false_type(), part, now);
+        const int kv_heads = part.head0 == 0 ? pairs : 0;
+        q.rel = part;
+        e = cudaErrorInvalidValue;
+        if constexpr (sizeof(T) == 2)
+            if (tc) e = launch_attn_tc_bwd<T>(kv, q, kv_heads, now, s);
+        if (!tc) e = launch_attn_simt_bwd<T>(a, p, bias, lse2, delta, part, kv_heads, now, s);
         if (e != cudaSuccess) return e;
         if (part.window)
             attn_rel_sum_kernel<<<dim3((a.R + 31) / 32, a.H), 512, 0, s>>>(a, part, now, rel);

@@ -9,6 +9,8 @@
 // which attn_rel_sum_kernel adds up in a fixed order.
 #pragma once
 
+#include <limits.h>
+
 #include <algorithm>
 
 #include "gs_attn_common.cuh"
@@ -165,36 +167,47 @@ cudaError_t launch_attn_delta(const AttnArgs &a, const AttnPtrs &p, float *lse2,
     return cudaGetLastError();
 }
 
-// rel[h][r] (+)= the warps' sums; `heads` (batch, head) pairs from head0 on are
-// in `part`.  32 indices a block, 16 threads per index that take every 16th
-// query warp of every batch item and are joined in order.
+// rel[h][r] (+)= the sums of groups of 32 queries; `heads` (batch, head) pairs
+// from head0 on are in `part`.  32 indices a block, 16 threads per index that
+// take every 16th (item, group) pair and are joined in order.
 static __global__ void __launch_bounds__(512)
     attn_rel_sum_kernel(AttnArgs a, RelArgs p, int heads, float *rel) {
     constexpr int kSlices = 16, kChunk = 32 * kSlices;
-    __shared__ int s_lo[kChunk], s_hi[kChunk];   // relative indices of a warp's queries
+    __shared__ int s_lo[kChunk], s_hi[kChunk];   // relative indices of a group's queries
+    __shared__ int s_low[kChunk];                // and how far below an item's keys reach
     __shared__ float s_sum[kSlices][32];
     const int lane = threadIdx.x % 32, slice = threadIdx.x / 32;
     const int r0 = blockIdx.x * 32, r = r0 + lane, h = blockIdx.y;
-    const int warps = (a.Lq + 31) / 32, k_end = rel_k(a, a.Lk - 1);
+    const int groups = (a.Lq + 31) / 32, k_end = rel_k(a, a.Lk - 1);
+    const int nh0 = p.head0 + (h - p.head0 % a.H + a.H) % a.H;   // this head's first pair
+    const int items = nh0 < p.head0 + heads ? (p.head0 + heads - 1 - nh0) / a.H + 1 : 0;
     float sum = 0.0f;
-    for (int w0 = 0; w0 < warps; w0 += kChunk) {
-        const int mine = min(w0 + (int)threadIdx.x, warps - 1);
-        __syncthreads();
-        s_lo[threadIdx.x] = rel_q(a, mine * 32);
-        s_hi[threadIdx.x] = rel_q(a, min(mine * 32 + 31, a.Lq - 1));
-        __syncthreads();
-        const int count = min(kChunk, warps - w0);
-        for (int nh = p.head0 + (h - p.head0 % a.H + a.H) % a.H; nh < p.head0 + heads; nh += a.H) {
-            const int keys = keys_of(a, nh / a.H);
-            if (keys == 0) continue;
-            const int low = rel_k(a, keys - 1);   // how far r reaches below the queries' lowest
-            const float *at = p.part + ((int64_t)(nh - p.head0) * warps + w0) * p.stride + r + k_end;
+    for (int n0 = 0; n0 < items; n0 += kChunk)
+        for (int w0 = 0; w0 < groups; w0 += kChunk) {
+            const int mine = min(w0 + (int)threadIdx.x, groups - 1);
+            const int keys = keys_of(a, (nh0 + min(n0 + (int)threadIdx.x, items - 1) * a.H) / a.H);
+            __syncthreads();
+            s_lo[threadIdx.x] = rel_q(a, mine * 32);
+            s_hi[threadIdx.x] = rel_q(a, min(mine * 32 + 31, a.Lq - 1));
+            s_low[threadIdx.x] = keys > 0 ? rel_k(a, keys - 1) : INT_MIN / 2;
+            __syncthreads();
+            const int nw = min(kChunk, groups - w0), nn = min(kChunk, items - n0);
+            int i = slice / nw, w = slice % nw;
+            const int di = kSlices / nw, dw = kSlices % nw;
 #pragma unroll 4
-            for (int w = slice; w < count; w += kSlices)
-                if (r <= s_hi[w] && r >= s_lo[w] - low)
-                    sum += __ldg(at + (int64_t)w * p.stride - s_lo[w]);
+            for (int k = slice; k < nn * nw; k += kSlices) {
+                if (r <= s_hi[w] && r >= s_lo[w] - s_low[i])
+                    sum += __ldg(p.part +
+                                 ((int64_t)(nh0 + (n0 + i) * a.H - p.head0) * groups + w0 + w) * p.stride +
+                                 (r + k_end - s_lo[w]));
+                i += di;
+                w += dw;
+                if (w >= nw) {
+                    w -= nw;
+                    ++i;
+                }
+            }
         }
-    }
     s_sum[slice][lane] = sum;
     __syncthreads();
     if (slice == 0 && r < a.R) {

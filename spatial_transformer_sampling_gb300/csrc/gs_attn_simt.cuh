@@ -14,6 +14,7 @@
 #include "gs_attn_common.cuh"
 #include "gs_attn_rel.cuh"
 #include "gs_ptx.cuh"
+#include "gs_vec.cuh"
 
 namespace gs {
 
@@ -29,25 +30,38 @@ template <typename T> struct SimtView {
         : p((const T *)base + n * s[0] + h * s[2]), by_token(s[1]) {}
 };
 
-// dst[d][64] from 64 tokens, zeros from `live` on; a thread reads along a row.
-template <typename T>
+// dst[d][64] from 64 tokens, zeros from `live` on; a thread reads along a row,
+// V elements at a time (16 bytes, or one where rows are not aligned).
+template <typename T, int V>
 __device__ __forceinline__ void simt_load_t(float *dst, const SimtView<T> &v, int row0, int live,
                                             int D) {
     const int row = threadIdx.x % kSimtTile;
     const T *p = v.p + (int64_t)(row0 + row) * v.by_token;
     const bool on = row < live;
-    for (int d = threadIdx.x / kSimtTile; d < D; d += kSimtThreads / kSimtTile)
-        dst[d * kSimtPitch + row] = on ? IO<T>::ld(p + d) : 0.0f;
+#pragma unroll 4
+    for (int d = threadIdx.x / kSimtTile * V; d < D; d += kSimtThreads / kSimtTile * V) {
+        float x[V] = {};
+        if (on) Run<T, V>::widen(Run<T, V>::load(p + d), x);
+#pragma unroll
+        for (int e = 0; e < V; ++e) dst[(d + e) * kSimtPitch + row] = x[e];
+    }
 }
 
-// dst[64][pitch] (D values a row) from 64 tokens, zeros from `live` on.
-template <typename T>
+// dst[64][pitch] (D values a row) from 64 tokens, zeros from `live` on and
+// behind a row.
+template <typename T, int V>
 __device__ __forceinline__ void simt_load_n(float *dst, int pitch, const SimtView<T> &v, int row0,
                                             int live, int D) {
-    for (int row = threadIdx.x / 32; row < kSimtTile; row += kSimtThreads / 32) {
-        const T *p = v.p + (int64_t)(row0 + row) * v.by_token;
-        for (int d = threadIdx.x % 32; d < pitch; d += 32)
-            dst[row * pitch + d] = row < live && d < D ? IO<T>::ld(p + d) : 0.0f;
+    const int runs = (pitch + V - 1) / V;
+#pragma unroll 4
+    for (int k = threadIdx.x; k < kSimtTile * runs; k += kSimtThreads) {
+        const int row = k / runs, d = (k - row * runs) * V;
+        float x[V] = {};
+        if (row < live && d < D)
+            Run<T, V>::widen(Run<T, V>::load(v.p + (int64_t)(row0 + row) * v.by_token + d), x);
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+            if (d + e < pitch) dst[row * pitch + d + e] = x[e];
     }
 }
 
@@ -105,7 +119,7 @@ inline int simt_bwd_smem(int D, bool dkv, int rel) {
 }
 
 // NC: 64-column chunks of the head width.
-template <typename T, int NC>
+template <typename T, int NC, int E>
 __global__ void __launch_bounds__(kSimtThreads)
     attn_simt_fwd_kernel(AttnArgs a, AttnPtrs p, const float *bias) {
     extern __shared__ float4 simt_smem[];
@@ -121,7 +135,7 @@ __global__ void __launch_bounds__(kSimtThreads)
     const int keys = keys_of(a, n);
     if (bias) bias += (int64_t)h * a.bias_stride;
 
-    simt_load_t(qt, Q, i0, a.Lq - i0, D);
+    simt_load_t<T, E>(qt, Q, i0, a.Lq - i0, D);
     float2 o[NC][4][2] = {};
     float m[4], l[4];
     int rq[4];
@@ -134,8 +148,8 @@ __global__ void __launch_bounds__(kSimtThreads)
     for (int j0 = 0; j0 < keys; j0 += kSimtTile) {
         const int live = keys - j0;
         __syncthreads();
-        simt_load_t(kt, K, j0, live, D);
-        simt_load_n(vn, pitch_n, V, j0, live, D);
+        simt_load_t<T, E>(kt, K, j0, live, D);
+        simt_load_n<T, E>(vn, pitch_n, V, j0, live, D);
         __syncthreads();
         float2 s[4][2] = {};
         simt_product(s, qt + ty * 4, kSimtPitch, kt + tx * 4, kSimtPitch, D);
@@ -199,10 +213,11 @@ __global__ void __launch_bounds__(kSimtThreads)
 
 // DKV: rows are keys, columns queries (dK, dV); else rows are queries, columns
 // keys (dQ, and the bias gradient through `rel`, see RelWindow).
-template <typename T, int NC, bool DKV>
-__global__ void __launch_bounds__(kSimtThreads)
-    attn_simt_bwd_kernel(AttnArgs a, AttnPtrs p, const float *bias, const float *lse2,
-                         const float *delta, RelArgs rel) {
+template <typename T, int NC, int E, bool DKV>
+__device__ __forceinline__ void attn_simt_bwd_block(const AttnArgs &a, const AttnPtrs &p,
+                                                    const float *bias, const float *lse2,
+                                                    const float *delta, const RelArgs &rel,
+                                                    int block) {
     extern __shared__ float4 simt_smem[];
     const int D = a.D, pitch_n = simt_pitch_n(D);
     float *r1 = reinterpret_cast<float *>(simt_smem), *r2 = r1 + simt_floats_t(D, false);
@@ -211,8 +226,8 @@ __global__ void __launch_bounds__(kSimtThreads)
     float *win_smem = DKV ? nullptr : n2;
     const int rows = DKV ? a.Lk : a.Lq;
     const int tiles = (rows + kSimtTile - 1) / kSimtTile;
-    const int i0 = (int)(blockIdx.x % tiles) * kSimtTile;
-    const int nh = rel.head0 + (int)(blockIdx.x / tiles), h = nh % a.H, n = nh / a.H;
+    const int i0 = block % tiles * kSimtTile;
+    const int nh = rel.head0 + block / tiles, h = nh % a.H, n = nh / a.H;
     const int tx = threadIdx.x % 16, ty = threadIdx.x / 16, warp = threadIdx.x / 32;
     const float c2 = a.scale * kLog2e;
     const int64_t dense[3] = {(int64_t)a.Lq * a.H * D, (int64_t)a.H * D, D};
@@ -225,8 +240,8 @@ __global__ void __launch_bounds__(kSimtThreads)
     delta += (int64_t)nh * rows64(a.Lq);
     if (bias) bias += (int64_t)h * a.bias_stride;
 
-    simt_load_t(r1, R1, i0, live_rows - i0, D);
-    simt_load_t(r2, R2, i0, live_rows - i0, D);
+    simt_load_t<T, E>(r1, R1, i0, live_rows - i0, D);
+    simt_load_t<T, E>(r2, R2, i0, live_rows - i0, D);
     float2 acc1[NC][4][2] = {}, acc2[NC][4][2] = {};
     float row_lse[4], row_delta[4];
     int row_rel[4];
@@ -246,10 +261,10 @@ __global__ void __launch_bounds__(kSimtThreads)
     for (int j0 = 0; j0 < cols; j0 += kSimtTile) {
         const int live = cols - j0;
         __syncthreads();
-        simt_load_t(t1, C1, j0, live, D);
-        simt_load_t(t2, C2, j0, live, D);
-        simt_load_n(n1, pitch_n, C1, j0, live, D);
-        if (DKV) simt_load_n(n2, pitch_n, C2, j0, live, D);
+        simt_load_t<T, E>(t1, C1, j0, live, D);
+        simt_load_t<T, E>(t2, C2, j0, live, D);
+        simt_load_n<T, E>(n1, pitch_n, C1, j0, live, D);
+        if (DKV) simt_load_n<T, E>(n2, pitch_n, C2, j0, live, D);
         __syncthreads();
         float2 s[4][2] = {}, d[4][2] = {};
         simt_product(s, r1 + ty * 4, kSimtPitch, t1 + tx * 4, kSimtPitch, D);
@@ -308,14 +323,26 @@ __global__ void __launch_bounds__(kSimtThreads)
     }
 }
 
+// Whether every row of the operands starts at a multiple of 16 bytes.
+template <typename T> bool simt_vec(const AttnArgs &a, const AttnPtrs &p) {
+    constexpr int E = kVec<T>;
+    bool vec = a.D % E == 0;
+    for (const void *x : {p.Q, p.K, p.V, p.dO}) vec = vec && aligned16(x);
+    for (int d = 0; d < 3; ++d)
+        vec = vec && a.qs[d] % E == 0 && a.ks[d] % E == 0 && a.vs[d] % E == 0;
+    return vec;
+}
+
 template <typename T>
 cudaError_t launch_attn_simt_fwd(const AttnArgs &a, const AttnPtrs &p, const float *bias,
                                  cudaStream_t s) {
-    auto kernel = a.D <= 64 ? attn_simt_fwd_kernel<T, 1> : attn_simt_fwd_kernel<T, 2>;
-    static DeviceFlags ready[2];
-    const cudaError_t e = once_per_device(ready[a.D > 64], [&] {
+    const bool wide = a.D > 64, vec = simt_vec<T>(a, p);
+    auto kernel = wide ? (vec ? attn_simt_fwd_kernel<T, 2, kVec<T>> : attn_simt_fwd_kernel<T, 2, 1>)
+                       : (vec ? attn_simt_fwd_kernel<T, 1, kVec<T>> : attn_simt_fwd_kernel<T, 1, 1>);
+    static DeviceFlags ready[2][2];
+    const cudaError_t e = once_per_device(ready[wide][vec], [&] {
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    simt_fwd_smem(a.D <= 64 ? 64 : 128));
+                                    simt_fwd_smem(wide ? 128 : 64));
     });
     if (e != cudaSuccess) return e;
     const int64_t blocks = (int64_t)((a.Lq + kSimtTile - 1) / kSimtTile) * a.H * a.N;
@@ -323,21 +350,38 @@ cudaError_t launch_attn_simt_fwd(const AttnArgs &a, const AttnPtrs &p, const flo
     return cudaGetLastError();
 }
 
-template <typename T, bool DKV>
+// The key blocks, then the query blocks: one launch, so that either fills the
+// SMs that the other leaves.
+template <typename T, int NC, int E>
+__global__ void __launch_bounds__(kSimtThreads)
+    attn_simt_bwd_kernel(AttnArgs a, AttnPtrs p, const float *bias, const float *lse2,
+                         const float *delta, RelArgs rel, int kv_blocks) {
+    if ((int)blockIdx.x < kv_blocks)
+        attn_simt_bwd_block<T, NC, E, true>(a, p, bias, lse2, delta, RelArgs(), blockIdx.x);
+    else
+        attn_simt_bwd_block<T, NC, E, false>(a, p, bias, lse2, delta, rel, blockIdx.x - kv_blocks);
+}
+
+// dK and dV of `kv_heads` (batch, head) pairs and dQ of `q_heads` from
+// rel.head0 on (either may be 0).
+template <typename T>
 cudaError_t launch_attn_simt_bwd(const AttnArgs &a, const AttnPtrs &p, const float *bias,
                                  const float *lse2, const float *delta, const RelArgs &rel,
-                                 int heads, cudaStream_t s) {
-    auto kernel = a.D <= 64 ? attn_simt_bwd_kernel<T, 1, DKV> : attn_simt_bwd_kernel<T, 2, DKV>;
-    static DeviceFlags ready[2];
-    const cudaError_t e = once_per_device(ready[a.D > 64], [&] {
+                                 int kv_heads, int q_heads, cudaStream_t s) {
+    const bool wide = a.D > 64, vec = simt_vec<T>(a, p);
+    auto kernel = wide ? (vec ? attn_simt_bwd_kernel<T, 2, kVec<T>> : attn_simt_bwd_kernel<T, 2, 1>)
+                       : (vec ? attn_simt_bwd_kernel<T, 1, kVec<T>> : attn_simt_bwd_kernel<T, 1, 1>);
+    static DeviceFlags ready[2][2];
+    const cudaError_t e = once_per_device(ready[wide][vec], [&] {
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     227 * 1024 - 256);
     });
     if (e != cudaSuccess) return e;
-    const int rows = DKV ? a.Lk : a.Lq;
-    const int64_t blocks = (int64_t)((rows + kSimtTile - 1) / kSimtTile) * heads;
-    kernel<<<(unsigned)blocks, kSimtThreads, simt_bwd_smem(a.D, DKV, rel.window), s>>>(
-        a, p, bias, lse2, delta, rel);
+    const int kv_blocks = (a.Lk + kSimtTile - 1) / kSimtTile * kv_heads;
+    const int q_blocks = (a.Lq + kSimtTile - 1) / kSimtTile * q_heads;
+    const int smem = std::max(simt_bwd_smem(a.D, true, 0), simt_bwd_smem(a.D, false, rel.window));
+    kernel<<<(unsigned)kv_blocks + (unsigned)q_blocks, kSimtThreads, smem, s>>>(a, p, bias, lse2, delta,
+                                                                               rel, kv_blocks);
     return cudaGetLastError();
 }
 

@@ -31,6 +31,7 @@ constexpr int kTcMmaWarp = kTcSoft / 32, kTcCopyWarp = kTcMmaWarp + 1;
 // reading the global timer, which takes longer than the events waited for, but
 // for every 1024th poll.
 __device__ __forceinline__ bool tc_wait(uint64_t *bar, uint32_t parity, unsigned *err) {
+    if (mbar_try_wait(bar, parity)) return true;
     uint64_t t0 = 0;
     for (uint32_t n = 1; !mbar_try_wait(bar, parity); ++n) {
         if (n % 1024 != 0) continue;
@@ -94,44 +95,28 @@ __device__ __forceinline__ void umma_f16_ts(uint32_t tmem_d, uint32_t tmem_a, ui
         : "memory");
 }
 
-#define GS_R32(r, o)                                                                              \
-    "=r"(r[o + 0]), "=r"(r[o + 1]), "=r"(r[o + 2]), "=r"(r[o + 3]), "=r"(r[o + 4]), "=r"(r[o + 5]), \
-        "=r"(r[o + 6]), "=r"(r[o + 7]), "=r"(r[o + 8]), "=r"(r[o + 9]), "=r"(r[o + 10]),          \
-        "=r"(r[o + 11]), "=r"(r[o + 12]), "=r"(r[o + 13]), "=r"(r[o + 14]), "=r"(r[o + 15]),      \
-        "=r"(r[o + 16]), "=r"(r[o + 17]), "=r"(r[o + 18]), "=r"(r[o + 19]), "=r"(r[o + 20]),      \
-        "=r"(r[o + 21]), "=r"(r[o + 22]), "=r"(r[o + 23]), "=r"(r[o + 24]), "=r"(r[o + 25]),      \
-        "=r"(r[o + 26]), "=r"(r[o + 27]), "=r"(r[o + 28]), "=r"(r[o + 29]), "=r"(r[o + 30]),      \
-        "=r"(r[o + 31])
-
-// Starts loading 32 consecutive columns of this thread's lane into r[O..O+31];
-// the values may be used after tmem_wait_ld on the same registers.
-template <int O, int N>
-__device__ __forceinline__ void tmem_ld_x32(uint32_t taddr, uint32_t (&r)[N]) {
+// 32 consecutive columns of this thread's lane; the wait is part of the load, so
+// that no use of the values can move ahead of it.
+__device__ __forceinline__ void tmem_ld_x32(uint32_t taddr, uint32_t (&r)[32]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
         "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
-        "%28, %29, %30, %31}, [%32];"
-        : GS_R32(r, O)
+        "%28, %29, %30, %31}, [%32];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+          "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+          "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(taddr)
         : "memory");
 }
-#undef GS_R32
 
-// Waits for this thread's TMEM loads.  r[O..O+31] pass through, so that no use
-// of them can be moved ahead of the wait.
-template <int O, int N>
-__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[N]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[O + 0]), "+r"(r[O + 1]), "+r"(r[O + 2]), "+r"(r[O + 3]), "+r"(r[O + 4]),
-                   "+r"(r[O + 5]), "+r"(r[O + 6]), "+r"(r[O + 7]), "+r"(r[O + 8]), "+r"(r[O + 9]),
-                   "+r"(r[O + 10]), "+r"(r[O + 11]), "+r"(r[O + 12]), "+r"(r[O + 13]),
-                   "+r"(r[O + 14]), "+r"(r[O + 15]), "+r"(r[O + 16]), "+r"(r[O + 17]),
-                   "+r"(r[O + 18]), "+r"(r[O + 19]), "+r"(r[O + 20]), "+r"(r[O + 21]),
-                   "+r"(r[O + 22]), "+r"(r[O + 23]), "+r"(r[O + 24]), "+r"(r[O + 25]),
-                   "+r"(r[O + 26]), "+r"(r[O + 27]), "+r"(r[O + 28]), "+r"(r[O + 29]),
-                   "+r"(r[O + 30]), "+r"(r[O + 31])
-                 :
-                 : "memory");
+// The largest of three (a NaN loses to a number, as with fmaxf).
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
 }
 
 // Starts storing r[0..31] to 32 consecutive columns of this thread's lane.

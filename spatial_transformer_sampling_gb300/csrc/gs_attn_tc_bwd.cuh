@@ -49,8 +49,7 @@ template <typename T> constexpr float kWeightScale = 1.0f;
 template <> constexpr float kWeightScale<__half> = 4096.0f;
 
 template <typename T, int DP, int BIAS, bool DKV>
-__global__ void __launch_bounds__(kTcThreads, TcBwdShape<DP, DKV>::kCtas)
-    attn_tc_bwd_kernel(const __grid_constant__ TcBwdArgs p) {
+__device__ __forceinline__ void attn_tc_bwd_block(const TcBwdArgs &p, int block) {
     using Sh = TcBwdShape<DP, DKV>;
     constexpr int NS = Sh::kStages;
     constexpr bool kBf16 = __is_same(T, __nv_bfloat16);
@@ -69,8 +68,8 @@ __global__ void __launch_bounds__(kTcThreads, TcBwdShape<DP, DKV>::kCtas)
 
     const int rows = DKV ? a.Lk : a.Lq;
     const int row_tiles = (rows + kTcM - 1) / kTcM;
-    const int i0 = (int)(blockIdx.x % row_tiles) * kTcM;
-    const int nh = p.rel.head0 + (int)(blockIdx.x / row_tiles);
+    const int i0 = block % row_tiles * kTcM;
+    const int nh = p.rel.head0 + block / row_tiles;
     const int h = nh % a.H, n = nh / a.H;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int keys = keys_of(a, n);
@@ -204,10 +203,11 @@ __global__ void __launch_bounds__(kTcThreads, TcBwdShape<DP, DKV>::kCtas)
         __syncwarp();
     } else {
         // ---------------------------------------------------- weights
-        // After a wait that gave up a warp goes on without waiting (and without
-        // storing), so that its partner finds it at every pair_sync.
+        // After a wait that gave up a thread goes on without waiting (and its warp
+        // without storing), so that its partner finds it at every pair_sync.
         const auto wait = [&](uint64_t *bar, int parity) {
-            if (ok) ok = __all_sync(0xffffffffu, tc_wait(bar, parity, a.err));
+            if (ok) ok = tc_wait(bar, parity, a.err);
+            __syncwarp();
         };
         const int pair = warp % 4, part = warp / 4;
         const uint32_t my_tmem = (uint32_t)(pair * 32) << 16;   // this warp's TMEM lanes
@@ -250,8 +250,7 @@ __global__ void __launch_bounds__(kTcThreads, TcBwdShape<DP, DKV>::kCtas)
             }
             wait(&s_full, t & 1);
             tcgen05_fence_after_sync();
-            tmem_ld_x32<0>(tmem + Sh::kTmemS + my_tmem + first, r);
-            tmem_wait_ld<0>(r);
+            tmem_ld_x32(tmem + Sh::kTmemS + my_tmem + first, r);
             tcgen05_fence_before_sync();
             mbar_arrive(&s_free);
             const float2 cc = make_float2(c2, c2);
@@ -292,8 +291,7 @@ __global__ void __launch_bounds__(kTcThreads, TcBwdShape<DP, DKV>::kCtas)
             }
             wait(&dp_full, t & 1);
             tcgen05_fence_after_sync();
-            tmem_ld_x32<0>(tmem + Sh::kTmemP + my_tmem + first, d);
-            tmem_wait_ld<0>(d);
+            tmem_ld_x32(tmem + Sh::kTmemP + my_tmem + first, d);
             float ds[kTcHalf];
 #pragma unroll
             for (int c = 0; c < kTcHalf; c += 4) {
@@ -332,7 +330,7 @@ __global__ void __launch_bounds__(kTcThreads, TcBwdShape<DP, DKV>::kCtas)
             }
         }
         if (steps > 0) wait(&finished, 0);
-        if (ok) {
+        if (__all_sync(0xffffffffu, ok)) {
             tcgen05_fence_after_sync();
             const int64_t at = (((int64_t)n * rows + i) * a.H + h) * a.D;
             for (int which = 0; which < (DKV ? 2 : 1); ++which) {
@@ -343,8 +341,7 @@ __global__ void __launch_bounds__(kTcThreads, TcBwdShape<DP, DKV>::kCtas)
                 for (int c = part * 32; c < a.D; c += 64) {   // every other chunk
                     uint32_t o[32];
                     if (steps > 0) {
-                        tmem_ld_x32<0>(acc + c, o);
-                        tmem_wait_ld<0>(o);
+                        tmem_ld_x32(acc + c, o);
                     }
                     if (i < rows) {
 #pragma unroll
@@ -370,32 +367,55 @@ __global__ void __launch_bounds__(kTcThreads, TcBwdShape<DP, DKV>::kCtas)
     if (warp == kTcMmaWarp) tmem_dealloc(tmem, Sh::kTmemCols);
 }
 
-template <typename T, int DP, int BIAS, bool DKV>
-cudaError_t launch_attn_tc_bwd_as(const TcBwdArgs &p, int heads, cudaStream_t s) {
-    using Sh = TcBwdShape<DP, DKV>;
-    auto kernel = attn_tc_bwd_kernel<T, DP, BIAS, DKV>;
+// The key blocks, then the query blocks: one launch, so that either fills the
+// SMs that the other leaves.
+template <typename T, int DP, int BIAS>
+__global__ void __launch_bounds__(kTcThreads, TcBwdShape<DP, true>::kCtas)
+    attn_tc_bwd_kernel(const __grid_constant__ TcBwdArgs kv, const __grid_constant__ TcBwdArgs q,
+                       int kv_blocks) {
+    if ((int)blockIdx.x < kv_blocks)
+        attn_tc_bwd_block<T, DP, BIAS, true>(kv, blockIdx.x);
+    else
+        attn_tc_bwd_block<T, DP, BIAS, false>(q, blockIdx.x - kv_blocks);
+}
+
+template <typename T, int DP, int BIAS>
+cudaError_t launch_attn_tc_bwd_as(const TcBwdArgs &kv, const TcBwdArgs &q, int kv_heads, int q_heads,
+                                  cudaStream_t s) {
+    auto kernel = attn_tc_bwd_kernel<T, DP, BIAS>;
     static DeviceFlags ready;
     const cudaError_t e = once_per_device(ready, [&] {
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmemOne);
     });
     if (e != cudaSuccess) return e;
-    const int window = BIAS == kBiasWindow ? Sh::kStages * p.bias.count * 4 : 0;
-    const int rows = DKV ? p.a.Lk : p.a.Lq;
-    const int64_t blocks = (int64_t)((rows + kTcM - 1) / kTcM) * heads;
-    kernel<<<(unsigned)blocks, kTcThreads, Sh::kSmem + rel_smem(p.rel.window, 4) + window, s>>>(p);
+    const auto window = [](const TcBwdArgs &p, int stages) {
+        return BIAS == kBiasWindow ? stages * p.bias.count * 4 : 0;
+    };
+    using Kv = TcBwdShape<DP, true>;
+    using Qs = TcBwdShape<DP, false>;
+    const int smem = std::max(Kv::kSmem + window(kv, Kv::kStages),
+                              Qs::kSmem + rel_smem(q.rel.window, 4) + window(q, Qs::kStages));
+    const int kv_blocks = (kv.a.Lk + kTcM - 1) / kTcM * kv_heads;
+    const int q_blocks = (q.a.Lq + kTcM - 1) / kTcM * q_heads;
+    kernel<<<(unsigned)kv_blocks + (unsigned)q_blocks, kTcThreads, smem, s>>>(kv, q, kv_blocks);
     return cudaGetLastError();
 }
 
-template <typename T, bool DKV>
-cudaError_t launch_attn_tc_bwd_kernel(const TcBwdArgs &p, int heads, cudaStream_t s) {
-    const int mode = !p.bias.base ? kBiasNone : p.bias.count ? kBiasWindow : kBiasGlobal;
+// dK and dV of `kv_heads` (batch, head) pairs and dQ of `q_heads` (either may be 0).
+template <typename T>
+cudaError_t launch_attn_tc_bwd(const TcBwdArgs &kv, const TcBwdArgs &q, int kv_heads, int q_heads,
+                               cudaStream_t s) {
+    // one mode for both: a window that is too large for one is read through L1 by both
+    const int mode = !q.bias.base                          ? kBiasNone
+                     : q.bias.count && kv.bias.count ? kBiasWindow
+                                                     : kBiasGlobal;
     const auto run = [&](auto dp) {
         constexpr int DP = decltype(dp)::value;
-        return mode == kBiasNone     ? launch_attn_tc_bwd_as<T, DP, kBiasNone, DKV>(p, heads, s)
-               : mode == kBiasWindow ? launch_attn_tc_bwd_as<T, DP, kBiasWindow, DKV>(p, heads, s)
-                                     : launch_attn_tc_bwd_as<T, DP, kBiasGlobal, DKV>(p, heads, s);
+        return mode == kBiasNone     ? launch_attn_tc_bwd_as<T, DP, kBiasNone>(kv, q, kv_heads, q_heads, s)
+               : mode == kBiasWindow ? launch_attn_tc_bwd_as<T, DP, kBiasWindow>(kv, q, kv_heads, q_heads, s)
+                                     : launch_attn_tc_bwd_as<T, DP, kBiasGlobal>(kv, q, kv_heads, q_heads, s);
     };
-    return p.a.D <= 64 ? run(std::integral_constant<int, 64>()) : run(std::integral_constant<int, 128>());
+    return q.a.D <= 64 ? run(std::integral_constant<int, 64>()) : run(std::integral_constant<int, 128>());
 }
 
 }  // namespace gs

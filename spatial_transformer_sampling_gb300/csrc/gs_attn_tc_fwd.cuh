@@ -176,10 +176,11 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         __syncwarp();
     } else {
         // ---------------------------------------------------- softmax
-        // After a wait that gave up a warp goes on without waiting (and without
-        // storing), so that its partner finds it at every pair_sync.
+        // After a wait that gave up a thread goes on without waiting (and its warp
+        // without storing), so that its partner finds it at every pair_sync.
         const auto wait = [&](uint64_t *bar, int parity) {
-            if (ok) ok = __all_sync(0xffffffffu, tc_wait(bar, parity, a.err));
+            if (ok) ok = tc_wait(bar, parity, a.err);
+            __syncwarp();
         };
         const int pair = warp % 4, part = warp / 4, lane_row = pair * 32 + lane;
         const uint32_t my_tmem = (uint32_t)(pair * 32) << 16;   // this warp's TMEM lanes
@@ -191,6 +192,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         if (BIAS) walk.init(a.Hk, a.Wk, a.P);
         const int inverse = 65536 / a.Wk + 1;
         float m = -INFINITY, l = 0.0f;
+        int stage = 0, phase = 0;   // of the copies of tile j
         for (int j = 0; j < T_tiles; ++j) {
             const int live = keys - j * kTcN;
             uint32_t r[kTcHalf];
@@ -198,8 +200,8 @@ __global__ void __launch_bounds__(kTcThreads, 2)
             int x = 0, rel = 0;
             if (BIAS) {
                 if (BIAS == kBiasWindow) {
-                    wait(&k_full[j % NS], (j / NS) & 1);
-                    row = sBias + j % NS * p.bias.count +
+                    wait(&k_full[stage], phase);
+                    row = sBias + stage * p.bias.count +
                           (rq - walk.rel - bias_start(p.bias, rq0 - walk.rel));
                 } else {
                     row = bias + rq - walk.rel;
@@ -213,7 +215,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
             wait(&s_full[j & 1], (j / 2) & 1);
             tcgen05_fence_after_sync();
             const uint32_t ts = tmem + my_tmem + (j & 1) * kTcN + first;
-            tmem_ld_x32<0>(ts, r);
+            tmem_ld_x32(ts, r);
             const float2 cc = make_float2(c2, c2);
             const auto score = [&](int c, float2 b) {
                 const float2 v = fma_f32x2(
@@ -221,7 +223,6 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                 r[c] = __float_as_uint(v.x);
                 r[c + 1] = __float_as_uint(v.y);
             };
-            tmem_wait_ld<0>(r);
             if (!BIAS) {
 #pragma unroll
                 for (int c = 0; c < kTcHalf; c += 2) score(c, make_float2(0.0f, 0.0f));
@@ -239,8 +240,8 @@ __global__ void __launch_bounds__(kTcThreads, 2)
             float top4[4] = {m, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
             for (int c = 0; c < kTcHalf; c += 2)
-                top4[c / 2 % 4] = fmaxf(fmaxf(top4[c / 2 % 4], __uint_as_float(r[c])),
-                                        __uint_as_float(r[c + 1]));
+                top4[c / 2 % 4] =
+                    max3(top4[c / 2 % 4], __uint_as_float(r[c]), __uint_as_float(r[c + 1]));
             float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
             s_top[j & 1][part][lane_row] = top;
             pair_sync(pair);
@@ -256,8 +257,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
 #pragma unroll 1
                 for (int d = part * 32; d < DP; d += 64) {   // every other chunk of O
                     uint32_t o[32];
-                    tmem_ld_x32<0>(to + d, o);
-                    tmem_wait_ld<0>(o);
+                    tmem_ld_x32(to + d, o);
 #pragma unroll
                     for (int k = 0; k < 32; ++k)
                         o[k] = __float_as_uint(__uint_as_float(o[k]) * keep);
@@ -286,23 +286,26 @@ __global__ void __launch_bounds__(kTcThreads, 2)
             tmem_wait_st();
             tcgen05_fence_before_sync();
             mbar_arrive(&p_ready[j & 1]);
+            if (++stage == NS) {
+                stage = 0;
+                phase ^= 1;
+            }
         }
         // the product before the last may be unfinished here, but the one a stage
         // earlier is done, so the phase's parity tells
         if (T_tiles > 0) wait(&pv_done[(T_tiles - 1) % NS], ((T_tiles - 1) / NS) & 1);
-        if (ok) {
+        s_top[T_tiles & 1][part][lane_row] = l;   // the row's other half of the sum
+        pair_sync(pair);
+        l += s_top[T_tiles & 1][part ^ 1][lane_row];
+        if (__all_sync(0xffffffffu, ok)) {
             tcgen05_fence_after_sync();
-            s_top[T_tiles & 1][part][lane_row] = l;   // the row's other half of the sum
-            pair_sync(pair);
-            l += s_top[T_tiles & 1][part ^ 1][lane_row];
             const float inv = l != 0.0f ? 1.0f / l : 0.0f;
             T *out = (T *)p.O + (((int64_t)n * a.Lq + i) * a.H + h) * a.D;
 #pragma unroll 1
             for (int d = part * 32; d < a.D; d += 64) {
                 uint32_t o[32];
                 if (T_tiles > 0) {
-                    tmem_ld_x32<0>(tmem_o + my_tmem + d, o);
-                    tmem_wait_ld<0>(o);
+                    tmem_ld_x32(tmem_o + my_tmem + d, o);
                 } else {
 #pragma unroll
                     for (int k = 0; k < 32; ++k) o[k] = 0;
