@@ -36,12 +36,14 @@ __device__ __forceinline__ int keys_of(const AttnArgs &a, int n) {
 // lies outside the table (the pair is masked).  A finite entry stays finite:
 // the lowest value of a type times log2(e) would leave fp32's range, and a row
 // of such entries is a uniform softmax, not an empty one.
+__device__ __forceinline__ float bias2(float b) {
+    const float f = b * kLog2e;
+    return isinf(f) && !isinf(b) ? copysignf(3.4028234e38f, b) : f;
+}
 template <typename T>
 __device__ __forceinline__ float bias2_of(const T *table, int bucket, int nb, int H, int h) {
     if ((unsigned)bucket >= (unsigned)nb) return -INFINITY;
-    const float b = IO<T>::ld(table + (int64_t)bucket * H + h);
-    if (isinf(b) || isnan(b)) return b;
-    return fminf(fmaxf(b * kLog2e, -3.4028234e38f), 3.4028234e38f);
+    return bias2(IO<T>::ld(table + (int64_t)bucket * H + h));
 }
 
 }  // namespace gs

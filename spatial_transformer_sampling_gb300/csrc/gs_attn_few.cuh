@@ -3,8 +3,8 @@
 //
 // The work is reading K and V once, so it is laid out for the loads: a key's
 // row is read by a group of G lanes, 16 bytes each (or, where rows are not
-// 16-byte aligned, by a whole warp, element by element), four keys per group
-// in flight.  Each group keeps its own running maximum, sum and output for up
+// 16-byte aligned, by a whole warp, element by element), a batch of
+// keys at a time with the next one in flight.  Each group keeps its own running maximum, sum and output for up
 // to NQ queries; groups, warps and the blocks of a cluster, which share the
 // keys of one head, are joined at the end (distributed shared memory: no
 // second launch and no workspace).  The bias is looked up per key.
@@ -17,7 +17,6 @@
 namespace gs {
 
 constexpr int kFewThreads = 256;
-constexpr int kFewBatch = 4;      // keys per group in flight
 constexpr int kFewMaxSplits = 8;  // blocks of a cluster
 constexpr int kFewQueries = 8;    // queries up to which this kernel is taken
 
@@ -54,9 +53,10 @@ template <typename T, bool VEC> struct FewRow {
 };
 
 template <typename T, bool VEC, int NQ>
-__global__ void __launch_bounds__(kFewThreads)
+__global__ void __launch_bounds__(kFewThreads, 2)
     attn_few_kernel(AttnArgs a, AttnPtrs p, int G, int splits) {
-    constexpr int E = FewRow<T, VEC>::E, W = kFewThreads / 32, U = kFewBatch;
+    constexpr int E = FewRow<T, VEC>::E, W = kFewThreads / 32;
+    constexpr int U = NQ == 1 ? 4 : 2;   // keys of a batch per group: what the registers hold
     __shared__ float s_o[W][NQ][128], s_m[W][NQ], s_l[W][NQ];   // per warp, then [0] per block
     const int groups = (a.Lq + NQ - 1) / NQ;
     const int64_t job = blockIdx.x / splits;
@@ -89,34 +89,64 @@ __global__ void __launch_bounds__(kFewThreads)
     const int keys = keys_of(a, n);
     const int chunk = (keys + splits - 1) / splits;
     const int lo = min(rank * chunk, keys), hi = min(lo + chunk, keys);
-    for (int base = lo + warp * per_warp * U; base < hi; base += W * per_warp * U) {
-        FewRow<T, VEC> k[U], v[U];
-        float s[U][NQ];
+    // The loads run ahead of their use: K, V and the bias by one batch of keys, the
+    // buckets that name the bias by two.
+    FewRow<T, VEC> k[U], v[U];
+    T entry[U][NQ];           // table entries of the next batch
+    int bucket[U][NQ];        // and the buckets of the batch after it, then of the next
+    const auto key_of = [&](int base, int u) { return base + u * per_warp + group; };
+    const auto load_buckets = [&](int base) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int j = base + u * per_warp + group;
-            const bool live = j < hi;
-            k[u].load(K + (int64_t)j * a.ks[1], part, a.D, live);
-            v[u].load(V + (int64_t)j * a.vs[1], part, a.D, live);
+            const int j = key_of(base, u);
+            const int rk = a.Hk == 1 ? j : j < hi ? rel_k(a, j) : 0;
+#pragma unroll
+            for (int x = 0; x < NQ; ++x)
+                bucket[u][x] = a.nb && j < hi ? __ldg(a.buckets + rq[x] - rk) : -1;
         }
-        float b[U][NQ];
+    };
+    // whether the pair has an entry goes with it as one bit per key and query
+    uint32_t has = 0;
+    const auto load = [&](int base) {
+        has = 0;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int j = base + u * per_warp + group;
-            const int rk = a.Hk == 1 ? j : rel_k(a, j);
+            const int j = key_of(base, u);
+            k[u].load(K + (int64_t)j * a.ks[1], part, a.D, j < hi);
+            v[u].load(V + (int64_t)j * a.vs[1], part, a.D, j < hi);
 #pragma unroll
             for (int x = 0; x < NQ; ++x) {
-                b[u][x] = j < hi ? 0.0f : -INFINITY;
-                if (a.nb && j < hi) b[u][x] = bias2_of(table, __ldg(a.buckets + rq[x] - rk), a.nb, a.H, h);
+                const bool in = (unsigned)bucket[u][x] < (unsigned)a.nb;
+                entry[u][x] = in ? table[(int64_t)bucket[u][x] * a.H + h] : IO<T>::st(0.0f);
+                if (a.nb ? in : j < hi) has |= 1u << (u * NQ + x);
             }
         }
+    };
+    const int stride = W * per_warp * U;
+    int base = lo + warp * per_warp * U;
+    load_buckets(base);
+    load(base);
+    load_buckets(base + stride);
+    for (; base < hi; base += stride) {
+        float s[U][NQ], b[U][NQ];
+        FewRow<T, VEC> keys_now[U], values[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            keys_now[u] = k[u];
+            values[u] = v[u];
+#pragma unroll
+            for (int x = 0; x < NQ; ++x)
+                b[u][x] = has >> (u * NQ + x) & 1 ? bias2(IO<T>::to_f(entry[u][x])) : -INFINITY;
+        }
+        load(base + stride);
+        load_buckets(base + 2 * stride);
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int x = 0; x < NQ; ++x) {
                 s[u][x] = 0.0f;
 #pragma unroll
-                for (int e = 0; e < E; ++e) s[u][x] = fmaf(q[x][e], k[u].at(e), s[u][x]);
+                for (int e = 0; e < E; ++e) s[u][x] = fmaf(q[x][e], keys_now[u].at(e), s[u][x]);
             }
         for (int w = G / 2; w > 0; w /= 2)
 #pragma unroll
@@ -140,12 +170,16 @@ __global__ void __launch_bounds__(kFewThreads)
             for (int e = 0; e < E; ++e) o[x][e] *= keep;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const float w = exp2_approx(s[u][x] - ref);
-                l[x] += w;
-#pragma unroll
-                for (int e = 0; e < E; ++e) o[x][e] = fmaf(w, v[u].at(e), o[x][e]);
+                s[u][x] = exp2_approx(s[u][x] - ref);
+                l[x] += s[u][x];
             }
         }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int x = 0; x < NQ; ++x)
+#pragma unroll
+                for (int e = 0; e < E; ++e) o[x][e] = fmaf(s[u][x], values[u].at(e), o[x][e]);
     }
     // join the groups of a warp
     for (int w = G; w < 32; w *= 2)
@@ -230,13 +264,13 @@ __global__ void __launch_bounds__(kFewThreads)
 
 inline bool few_takes(const AttnArgs &a) { return a.Lq <= kFewQueries; }
 
-// splits: as many blocks per head as fill the GPU about four times over, of at
-// least 128 keys each.
+// splits: blocks per head, as many as the SMs hold at once with two each (a
+// second wave would leave most of them idle), of at least 128 keys.
 template <typename T, bool VEC, int NQ>
 cudaError_t launch_attn_few_as(const AttnArgs &a, const AttnPtrs &p, int G, cudaStream_t s) {
     const int64_t jobs = (int64_t)((a.Lq + NQ - 1) / NQ) * a.H * a.N;
     int splits = 1;
-    while (splits < kFewMaxSplits && jobs * splits < 152 * 4 && a.Lk > 128 * splits) splits *= 2;
+    while (splits < kFewMaxSplits && jobs * splits * 2 <= 152 * 2 && a.Lk > 128 * splits) splits *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(jobs * splits));
     cfg.blockDim = dim3(kFewThreads);

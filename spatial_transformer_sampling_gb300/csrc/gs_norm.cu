@@ -130,8 +130,31 @@ __global__ void __launch_bounds__(kNormThreads)
     }
 }
 
+// Sums of two values over the L threads of a row; slots alternate between calls,
+// so that one barrier per call suffices.
+template <int L> __device__ __forceinline__ void row_sum2(float &a, float &b, int slot) {
+#pragma unroll
+    for (int o = (L < 32 ? L : 32) / 2; o > 0; o >>= 1) {
+        a += __shfl_xor_sync(0xffffffffu, a, o);
+        b += __shfl_xor_sync(0xffffffffu, b, o);
+    }
+    if (L > 32) {
+        __shared__ float2 s[2][kNormThreads / 32];
+        if (threadIdx.x % 32 == 0) s[slot][threadIdx.x / 32] = make_float2(a, b);
+        __syncthreads();
+        a = b = 0.0f;
+        const int first = threadIdx.x / L * (L / 32);
+#pragma unroll
+        for (int w = 0; w < L / 32; ++w) {
+            a += s[slot][first + w].x;
+            b += s[slot][first + w].y;
+        }
+    }
+}
+
 // dX of the block's rows and, into partials[block], its column sums (the sums
-// for dScale, then those for dB).
+// for dScale, then those for dB).  The next row's loads are issued before this
+// one is worked on.
 template <typename T, int V, int L, int NV>
 __global__ void __launch_bounds__(kNormThreads)
     layer_norm_backward_kernel(const T *dY, const T *X, const T *scale, const float *mean,
@@ -140,11 +163,10 @@ __global__ void __launch_bounds__(kNormThreads)
     constexpr int kGroups = kNormThreads / L;
     const int part = threadIdx.x % L, group = threadIdx.x / L;
     float ds[NV][V] = {}, db[NV][V] = {};
-    for (int64_t row0 = (int64_t)blockIdx.x * kGroups; row0 < a.rows;
-         row0 += (int64_t)gridDim.x * kGroups) {
-        const int64_t row = row0 + group;
+    typename IOV::Raw rx[NV], rg[NV];
+    float m = 0.0f, iv = 0.0f;
+    const auto load = [&](int64_t row) {
         const bool here = row < a.rows;
-        typename IOV::Raw rx[NV], rg[NV];
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int d = (k * L + part) * V;
@@ -152,38 +174,46 @@ __global__ void __launch_bounds__(kNormThreads)
             rx[k] = on ? IOV::load(X + row * a.D + d) : IOV::zero();
             rg[k] = on ? IOV::load(dY + row * a.D + d) : IOV::zero();
         }
-        const float m = here ? __ldg(mean + row) : 0.0f, iv = here ? __ldg(inv + row) : 0.0f;
-        float s0 = 0.0f, s1 = 0.0f;
+        m = here ? __ldg(mean + row) : 0.0f;
+        iv = here ? __ldg(inv + row) : 0.0f;
+    };
+    const int64_t step = (int64_t)gridDim.x * kGroups;
+    int64_t row = (int64_t)blockIdx.x * kGroups + group;
+    load(row);
+    int slot = 0;
+    for (int64_t row0 = (int64_t)blockIdx.x * kGroups; row0 < a.rows; row0 += step, row += step) {
+        float xh[NV][V], gw[NV][V], s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int d = (k * L + part) * V;
-            if (d >= a.D) continue;
-            float x[V], g[V], w[V];
+            float x[V], g[V], w[V] = {};
             IOV::widen(rx[k], x);
             IOV::widen(rg[k], g);
-            IOV::widen(IOV::load(scale + d), w);
+            if (d < a.D) IOV::widen(IOV::load(scale + d), w);
 #pragma unroll
             for (int e = 0; e < V; ++e) {
-                const float xh = (x[e] - m) * iv;
-                ds[k][e] = fmaf(g[e], xh, ds[k][e]);
+                xh[k][e] = d < a.D ? (x[e] - m) * iv : 0.0f;
+                ds[k][e] = fmaf(g[e], xh[k][e], ds[k][e]);
                 db[k][e] += g[e];
-                s0 = fmaf(g[e], w[e], s0);
-                s1 = fmaf(g[e] * w[e], xh, s1);
+                gw[k][e] = g[e] * w[e];
+                s0 += gw[k][e];
+                s1 = fmaf(gw[k][e], xh[k][e], s1);
             }
         }
-        s0 = row_sum<L>(s0, 0) / (float)a.D;
-        s1 = row_sum<L>(s1, 1) / (float)a.D;
-        if (!here) continue;
+        const float row_iv = iv;
+        load(row + step);
+        row_sum2<L>(s0, s1, slot);
+        slot ^= 1;
+        s0 /= (float)a.D;
+        s1 /= (float)a.D;
+        if (row >= a.rows) continue;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int d = (k * L + part) * V;
             if (d >= a.D) continue;
-            float x[V], g[V], w[V], out[V];
-            IOV::widen(rx[k], x);
-            IOV::widen(rg[k], g);
-            IOV::widen(IOV::load(scale + d), w);
+            float out[V];
 #pragma unroll
-            for (int e = 0; e < V; ++e) out[e] = iv * (g[e] * w[e] - s0 - (x[e] - m) * iv * s1);
+            for (int e = 0; e < V; ++e) out[e] = row_iv * (gw[k][e] - s0 - xh[k][e] * s1);
             IOV::store(dX + row * a.D + d, out);
         }
     }
@@ -306,18 +336,38 @@ template <int V, typename F> cudaError_t norm_shape(int runs, F &&f) {
     return cudaErrorInvalidValue;   // not reached: D <= kNormOnChip
 }
 
-// Row blocks of the backward pass: eight per SM while a thread holds one run
-// per row (few bytes in flight each), down to two with its registers full.
+// Calls f(L, NV) for the backward pass: as many threads per row as keep a
+// thread's share, and with it the sums it holds, to one run (a block of 256 at
+// most), so that many warps share an SM: 16384 x 1024 bf16 takes @@ us, against
+// 37.5 with a warp per row and four runs per thread.
+template <int V, typename F> cudaError_t norm_backward_shape(int runs, F &&f) {
+    using std::integral_constant;
+    if (runs <= 8) return f(integral_constant<int, 8>(), integral_constant<int, 1>());
+    if (runs <= 16) return f(integral_constant<int, 16>(), integral_constant<int, 1>());
+    if (runs <= 32) return f(integral_constant<int, 32>(), integral_constant<int, 1>());
+    if (runs <= 64) return f(integral_constant<int, 64>(), integral_constant<int, 1>());
+    if (runs <= 128) return f(integral_constant<int, 128>(), integral_constant<int, 1>());
+    if (runs <= 256) return f(integral_constant<int, 256>(), integral_constant<int, 1>());
+    if (runs <= 512) return f(integral_constant<int, 256>(), integral_constant<int, 2>());
+    if (runs <= 1024) return f(integral_constant<int, 256>(), integral_constant<int, 4>());
+    if constexpr (V <= 4)
+        if (runs <= 2048) return f(integral_constant<int, 256>(), integral_constant<int, 8>());
+    if constexpr (V == 1) return f(integral_constant<int, 256>(), integral_constant<int, 32>());
+    return cudaErrorInvalidValue;   // not reached: D <= kNormOnChip
+}
+
+// Row blocks of the backward pass: what an SM holds of them at once, and no
+// more, since each leaves 2 D sums behind.
 int row_blocks(int64_t rows, int L, int NV) {
     const int64_t b = (rows + kNormThreads / L - 1) / (kNormThreads / L);
-    const int most = kNormSms * (NV == 1 ? 8 : NV == 2 ? 4 : 2);
+    const int most = kNormSms * (NV == 1 ? 4 : 2);
     return (int)(b < most ? b : most);
 }
 constexpr int kWideNV = 32;   // rows wider than kNormOnChip: as the fullest
 template <int V> int row_blocks_of(int64_t rows, int64_t D) {
     int blocks = row_blocks(rows, kNormThreads, kWideNV);
     if (D <= kNormOnChip)
-        norm_shape<V>((int)((D + V - 1) / V), [&](auto l, auto nv) {
+        norm_backward_shape<V>((int)((D + V - 1) / V), [&](auto l, auto nv) {
             blocks = row_blocks(rows, decltype(l)::value, decltype(nv)::value);
             return cudaSuccess;
         });
@@ -342,7 +392,7 @@ template <typename T, int V>
 cudaError_t run_backward(const T *dY, const T *X, const T *scale, const float *mean,
                          const float *inv, T *dX, float *partials, int *blocks, const NormArgs &a,
                          cudaStream_t s) {
-    return norm_shape<V>((a.D + V - 1) / V, [&](auto l, auto nv) {
+    return norm_backward_shape<V>((a.D + V - 1) / V, [&](auto l, auto nv) {
         constexpr int L = decltype(l)::value, NV = decltype(nv)::value;
         *blocks = row_blocks(a.rows, L, NV);
         layer_norm_backward_kernel<T, V, L, NV>
