@@ -3,11 +3,13 @@
 //
 // The work is reading K and V once, so it is laid out for the loads: a key's
 // row is read by a group of G lanes, 16 bytes each (or, where rows are not
-// 16-byte aligned, by a whole warp, element by element), a batch of
-// keys at a time with the next one in flight.  Each group keeps its own running maximum, sum and output for up
-// to NQ queries; groups, warps and the blocks of a cluster, which share the
-// keys of one head, are joined at the end (distributed shared memory: no
-// second launch and no workspace).  The bias is looked up per key.
+// 16-byte aligned, by a whole warp, element by element), a batch of keys at a
+// time with the next one in flight.  Each group keeps its own running maximum,
+// sum and output for up to NQ queries; groups, warps and the blocks of a
+// cluster, which share the keys of one head, are joined at the end (distributed
+// shared memory: no second launch and no workspace).  The bias is looked up per
+// key, its bucket two batches ahead and its entry one: looked up in place it
+// took 130 us instead of 98 (8 x 8 heads, 32771 keys, D 64, bf16).
 #pragma once
 
 #include <cooperative_groups.h>

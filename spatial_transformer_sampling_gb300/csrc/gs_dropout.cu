@@ -2,10 +2,8 @@
 // residual sum: Y = residual + (kept ? X / (1 - ratio) : 0).
 //
 // The mask is a function of (seed, offset, element index) and is never stored:
-// the backward pass calls the same kernel on the gradient.  Bound by memory:
-// ten Philox rounds cost about 45 instructions per four elements, a third of
-// the issue slots that moving them leaves.  A thread moves 16-byte runs, kRuns
-// of them a block apart, all loads first.
+// the backward pass calls the same kernel on the gradient.  A thread moves
+// 16-byte runs, kRuns of them a block apart, all loads first.
 #include "gs_internal.h"
 #include "gs_philox.cuh"
 #include "gs_vec.cuh"
@@ -16,15 +14,15 @@ namespace {
 constexpr int kDropThreads = 256;
 constexpr int kRuns = 4;
 
-// The kept and scaled value of E consecutive elements from element i0 on (a
-// multiple of four), plus r.
+// The kept and scaled value of E consecutive elements from element 4 * quad on
+// (`high`: bits 32 and up of quad), plus r.
 template <int E>
-__device__ __forceinline__ void drop(float (&x)[E], const float (&r)[E], int64_t i0, bool residual,
-                                     const DropoutArgs &a) {
+__device__ __forceinline__ void drop(float (&x)[E], const float (&r)[E], uint32_t quad, uint32_t high,
+                                     bool residual, const DropoutArgs &a, const PhiloxKeys &keys) {
 #pragma unroll
     for (int e = 0; e < E; e += 4) {
         uint32_t w[4];
-        philox4x32_10((uint64_t)(i0 + e) / 4, a.offset, a.seed, w);
+        philox4x32_10(quad + e / 4, high, a.offset, keys, w);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             const float y = w[q] >= a.threshold ? x[e + q] * a.scale : 0.0f;
@@ -39,9 +37,14 @@ __device__ __forceinline__ void drop(float (&x)[E], const float (&r)[E], int64_t
 // no other does.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kDropThreads)
-    dropout_kernel(const T *X, const T *residual, T *Y, DropoutArgs a) {
+    dropout_kernel(const T *X, const T *residual, T *Y, DropoutArgs a,
+                   const __grid_constant__ PhiloxKeys keys) {
     constexpr int E = VEC ? kVec<T> : 4;
     const int64_t run0 = (int64_t)blockIdx.x * (kDropThreads * kRuns) + threadIdx.x;
+    // a block's generator calls share their upper 32 bits: it makes a power of
+    // two of them, aligned to that
+    const uint64_t first = (uint64_t)blockIdx.x * (kDropThreads * kRuns * (E / 4));
+    const uint32_t high = (uint32_t)(first >> 32);
     if constexpr (VEC) {
         if ((run0 + (kRuns - 1) * kDropThreads + 1) * E <= a.n) {
             using IOV = Run<T, E>;
@@ -58,7 +61,7 @@ __global__ void __launch_bounds__(kDropThreads)
                 float x[E], r[E];
                 IOV::widen(rx[k], x);
                 IOV::widen(rr[k], r);
-                drop(x, r, i, residual != nullptr, a);
+                drop(x, r, (uint32_t)(i / 4), high, residual != nullptr, a, keys);
                 IOV::store(Y + i, x);
             }
             return;
@@ -76,7 +79,7 @@ __global__ void __launch_bounds__(kDropThreads)
                 r[e] = i + e < a.n && residual ? IO<T>::to_f(residual[i + e]) : 0.0f;
             }
             if (i >= a.n) return;
-            drop(x, r, i, residual != nullptr, a);
+            drop(x, r, (uint32_t)(i / 4), high, residual != nullptr, a, keys);
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 if (i + e < a.n) Y[i + e] = IO<T>::st(x[e]);
@@ -92,7 +95,7 @@ cudaError_t launch_dropout(const void *X, const void *residual, void *Y, const D
     const int64_t per_block = (int64_t)kDropThreads * kRuns * (vec ? kVec<T> : 4);
     auto kernel = vec ? dropout_kernel<T, true> : dropout_kernel<T, false>;
     kernel<<<(unsigned)((a.n + per_block - 1) / per_block), kDropThreads, 0, s>>>(
-        (const T *)X, (const T *)residual, (T *)Y, a);
+        (const T *)X, (const T *)residual, (T *)Y, a, philox_keys(a.seed));
     return cudaGetLastError();
 }
 
