@@ -50,6 +50,20 @@ __device__ __forceinline__ void pair_sync(int pair) {
     asm volatile("bar.sync %0, 64;" ::"r"(pair + 1) : "memory");
 }
 
+// The same barrier; true for all of its 64 threads when `p` is for any.
+__device__ __forceinline__ bool pair_any(int pair, bool p) {
+    uint32_t any;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %2, 0;\n\t"
+        "barrier.cta.red.or.pred q, %1, 64, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(any)
+        : "r"(pair + 1), "r"((uint32_t)p)
+        : "memory");
+    return any != 0;
+}
+
 // Shared-memory descriptors with the 128-byte swizzle (see
 // umma_desc_kmajor_sw128): the upper word is the same for all of a kernel's
 // operands (1024 bytes between groups of eight tokens), the lower one holds the
@@ -95,14 +109,13 @@ __device__ __forceinline__ void umma_f16_ts(uint32_t tmem_d, uint32_t tmem_a, ui
         : "memory");
 }
 
-// 32 consecutive columns of this thread's lane; the wait is part of the load, so
-// that no use of the values can move ahead of it.
-__device__ __forceinline__ void tmem_ld_x32(uint32_t taddr, uint32_t (&r)[32]) {
+// Starts loading 32 consecutive columns of this thread's lane; the values may be
+// used after tmem_wait_ld on them.
+__device__ __forceinline__ void tmem_start_ld_x32(uint32_t taddr, uint32_t (&r)[32]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
         "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
-        "%28, %29, %30, %31}, [%32];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
+        "%28, %29, %30, %31}, [%32];"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
           "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
           "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
@@ -110,6 +123,25 @@ __device__ __forceinline__ void tmem_ld_x32(uint32_t taddr, uint32_t (&r)[32]) {
           "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(taddr)
         : "memory");
+}
+
+// Waits for this thread's TMEM loads.  The values pass through, so that no use
+// of them can be moved ahead of the wait.
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                   "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                   "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
+                   "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                   "+r"(r[30]), "+r"(r[31])
+                 :
+                 : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld_x32(uint32_t taddr, uint32_t (&r)[32]) {
+    tmem_start_ld_x32(taddr, r);
+    tmem_wait_ld(r);
 }
 
 // The largest of three (a NaN loses to a number, as with fmaxf).
@@ -308,31 +340,46 @@ __device__ __forceinline__ void bias_offsets(int *rel, const TileWalk &walk, int
     __syncwarp();
 }
 
-// f(c, b) for columns c = 0, 2, .. 30: the bias of columns c and c + 1 of a row.
-// Column c sits SIGN * (its offset) from `row` (SIGN -1: the thread holds a
-// query, columns are keys; +1: a key against queries); x and rel as from
-// TileWalk::half.
-template <int SIGN, typename F>
+// The bias of 32 columns of a row.  Column c sits SIGN * (its offset) from `row`
+// (SIGN -1: the thread holds a query, columns are keys; +1: a key against
+// queries); x and rel as from TileWalk::half.
+template <int SIGN>
 __device__ __forceinline__ void bias_by_runs(const float *row, int x, int rel, const TileWalk &walk,
-                                             F &&f) {
+                                             float (&b)[kTcHalf]) {
     const int W = walk.W, wrap = walk.P - walk.W;
 #pragma unroll
     for (int c = 0; c < kTcHalf; c += 8) {
         const float *at = row + SIGN * rel;
 #pragma unroll
-        for (int k = 0; k < 8; k += 2) f(c + k, make_float2(at[SIGN * k], at[SIGN * (k + 1)]));
+        for (int k = 0; k < 8; ++k) b[c + k] = at[SIGN * k];
         x += 8;
         rel += 8 + (x == W ? wrap : 0);
         x = x == W ? 0 : x;
     }
 }
-template <int SIGN, typename F>
-__device__ __forceinline__ void bias_by_table(const float *row, const int *rel, F &&f) {
+template <int SIGN>
+__device__ __forceinline__ void bias_by_table(const float *row, const int *rel,
+                                              float (&b)[kTcHalf]) {
 #pragma unroll
     for (int c = 0; c < kTcHalf; c += 4) {
         const int4 o = *reinterpret_cast<const int4 *>(rel + c);
-        f(c, make_float2(row[SIGN * o.x], row[SIGN * o.y]));
-        f(c + 2, make_float2(row[SIGN * o.z], row[SIGN * o.w]));
+        b[c] = row[SIGN * o.x];
+        b[c + 1] = row[SIGN * o.y];
+        b[c + 2] = row[SIGN * o.z];
+        b[c + 3] = row[SIGN * o.w];
+    }
+}
+
+// r = r * scale + b, on pairs.
+__device__ __forceinline__ void scale_and_bias(uint32_t (&r)[kTcHalf], float scale,
+                                               const float (&b)[kTcHalf]) {
+    const float2 s = make_float2(scale, scale);
+#pragma unroll
+    for (int c = 0; c < kTcHalf; c += 2) {
+        const float2 v = fma_f32x2(make_float2(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), s,
+                                   make_float2(b[c], b[c + 1]));
+        r[c] = __float_as_uint(v.x);
+        r[c + 1] = __float_as_uint(v.y);
     }
 }
 

@@ -92,7 +92,7 @@ __device__ __forceinline__ void attn_tc_bwd_block(const TcBwdArgs &p, int block)
                 mbar_init(&c_full[s], 1);
                 mbar_init(&done[s], 1);
             }
-            mbar_init(&s_full, 1);
+            mbar_init(&s_full, 2);   // the MMA thread, which saw the copies land, and its MMAs
             mbar_init(&s_free, kTcSoft);
             mbar_init(&dp_full, 1);
             mbar_init(&pd_ready, kTcSoft);
@@ -166,6 +166,7 @@ __device__ __forceinline__ void attn_tc_bwd_block(const TcBwdArgs &p, int block)
             ok = tc_wait(&r_full, 0, a.err) && arrived(0);
             if (ok) {
                 tc_scores<DP>(tmem + Sh::kTmemS, r1_lo, c1_lo, idesc_s, depth);
+                mbar_arrive(&s_full);
                 umma_commit(&s_full);
                 tc_scores<DP>(tmem + Sh::kTmemP, r2_lo, c2_lo, idesc_s, depth);
                 umma_commit(&dp_full);
@@ -177,6 +178,7 @@ __device__ __forceinline__ void attn_tc_bwd_block(const TcBwdArgs &p, int block)
                     if (!ok) break;
                     tcgen05_fence_after_sync();
                     tc_scores<DP>(tmem + Sh::kTmemS, r1_lo, c1_lo + s1 * kTile, idesc_s, depth);
+                    mbar_arrive(&s_full);
                     umma_commit(&s_full);
                 }
                 ok = tc_wait(&pd_ready, t & 1, a.err);
@@ -227,48 +229,42 @@ __device__ __forceinline__ void attn_tc_bwd_block(const TcBwdArgs &p, int block)
         if (!DKV && BIAS) {
             if (with_rel) rel_out = win.init(a, sRel, p.rel, i0, nh, pair, part);
         }
+        int stage = 0;
+        // the bias of this row and the next step's first column, and where the
+        // thread's columns start in their grid
+        const float *row = nullptr;
+        int x = 0, rel = 0;
+        const auto aim = [&] {
+            const int at = meet0 + (DKV ? walk.rel : -walk.rel);
+            if (BIAS == kBiasWindow)
+                row = sBias + stage * p.bias.count + (at - row0 + my_row - bias_start(p.bias, at));
+            else if (BIAS)
+                row = bias + at - row0 + my_row;
+            if (BIAS) walk.half(part, x, rel);
+        };
+        aim();
         for (int t = 0; t < steps; ++t) {
             const int live = cols - t * kTcN;
             uint32_t r[kTcHalf], d[kTcHalf];
-            if (DKV || BIAS == kBiasWindow) {   // the vectors and the bias came with the tile
-                wait(&c_full[t % NS], (t / NS) & 1);
-            }
-            const float *vec = sVec + t % NS * 2 * kTcN + first;
-            const float *row = nullptr;   // the bias of this row and the tile's first column
-            int x = 0, rel = 0;
-            if (BIAS) {
-                const int at = meet0 + (DKV ? walk.rel : -walk.rel);
-                if (BIAS == kBiasWindow)
-                    row = sBias + t % NS * p.bias.count + (at - row0 + my_row - bias_start(p.bias, at));
-                else
-                    row = bias + at - row0 + my_row;
-                if (BIAS == kBiasGlobal || !p.bias.runs)
-                    bias_offsets(s_rel[warp], walk, first, live, inverse);
-                else
-                    walk.half(part, x, rel);
-                walk.next();
-            }
+            float b[kTcHalf];
             wait(&s_full, t & 1);
             tcgen05_fence_after_sync();
-            tmem_ld_x32(tmem + Sh::kTmemS + my_tmem + first, r);
-            tcgen05_fence_before_sync();
-            mbar_arrive(&s_free);
-            const float2 cc = make_float2(c2, c2);
-            const auto score = [&](int c, float2 b) {
-                const float2 v = fma_f32x2(
-                    make_float2(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), cc, b);
-                r[c] = __float_as_uint(v.x);
-                r[c + 1] = __float_as_uint(v.y);
-            };
+            tmem_start_ld_x32(tmem + Sh::kTmemS + my_tmem + first, r);
             constexpr int kSign = DKV ? 1 : -1;
             if (!BIAS) {
 #pragma unroll
-                for (int c = 0; c < kTcHalf; c += 2) score(c, make_float2(0.0f, 0.0f));
+                for (int c = 0; c < kTcHalf; ++c) b[c] = 0.0f;
             } else if (BIAS == kBiasWindow && p.bias.runs) {
-                bias_by_runs<kSign>(row, x, rel, walk, score);
+                bias_by_runs<kSign>(row, x, rel, walk, b);
             } else {
-                bias_by_table<kSign>(row, s_rel[warp], score);
+                bias_offsets(s_rel[warp], walk, first, live, inverse);
+                bias_by_table<kSign>(row, s_rel[warp], b);
             }
+            const float *vec = sVec + stage * 2 * kTcN + first;   // lse2 and delta of the columns
+            tmem_wait_ld(r);
+            tcgen05_fence_before_sync();
+            mbar_arrive(&s_free);
+            scale_and_bias(r, c2, b);
             if (live < kTcN) {   // columns that do not count, whatever they hold
                 asm volatile("" ::: "memory");   // a branch: the selects would cost every tile
 #pragma unroll
@@ -289,6 +285,10 @@ __device__ __forceinline__ void attn_tc_bwd_block(const TcBwdArgs &p, int block)
                 r[c + 2] = __float_as_uint(exp2_approx(v.x));
                 r[c + 3] = __float_as_uint(exp2_approx(v.y));
             }
+            // the next step's place, among the exponentials
+            if (BIAS) walk.next();
+            if (++stage == NS) stage = 0;
+            aim();
             wait(&dp_full, t & 1);
             tcgen05_fence_after_sync();
             tmem_ld_x32(tmem + Sh::kTmemP + my_tmem + first, d);

@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     unsigned char *sQ = tiles, *sK = tiles + Sh::kQBytes, *sV = sK + NS * Sh::kTileBytes;
     float *sBias = reinterpret_cast<float *>(tiles + Sh::kTileSmem);   // a window per stage
     __shared__ __align__(16) int s_rel[8][kTcHalf];
-    __shared__ float s_top[2][2][kTcM];   // of the two threads of a query, two tiles in turn
+    __shared__ float s_top[2][2][kTcM];   // of the two threads of a query, in turn
 
     const int q_tiles = (a.Lq + kTcM - 1) / kTcM;
     const int i0 = (int)(blockIdx.x % q_tiles) * kTcM;
@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                 mbar_init(&pv_done[s], 1);
             }
             for (int b = 0; b < 2; ++b) {
-                mbar_init(&s_full[b], 1);
+                mbar_init(&s_full[b], 2);   // the MMA thread, which saw the copies land, and its MMAs
                 mbar_init(&p_ready[b], kTcSoft);
             }
             mbar_init(&cleared, 1);
@@ -145,6 +145,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
             ok = tc_wait(&q_full, 0, a.err) && tc_wait(&k_full[0], 0, a.err);
             if (ok) {
                 tc_scores<DP>(tmem, q_lo, k_lo, idesc_s, steps);
+                mbar_arrive(&s_full[0]);
                 umma_commit(&s_full[0]);
             }
             for (int j = 0; j < T_tiles && ok; ++j) {
@@ -157,6 +158,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                     tcgen05_fence_after_sync();
                     tc_scores<DP>(tmem + ((j + 1) & 1) * kTcN, q_lo, k_lo + s1 * (Sh::kTileBytes / 16),
                                   idesc_s, steps);
+                    mbar_arrive(&s_full[(j + 1) & 1]);
                     umma_commit(&s_full[(j + 1) & 1]);
                 }
                 ok = tc_wait(&v_full[s], (j / NS) & 1, a.err);
@@ -192,45 +194,39 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         if (BIAS) walk.init(a.Hk, a.Wk, a.P);
         const int inverse = 65536 / a.Wk + 1;
         float m = -INFINITY, l = 0.0f;
-        int stage = 0, phase = 0;   // of the copies of tile j
+        int stage = 0, turn = 0;
+        // the bias of this query and the next tile's first key, and where the
+        // thread's columns start in the keys' grid
+        const float *row = nullptr;
+        int x = 0, rel = 0;
+        const auto aim = [&] {
+            if (BIAS == kBiasWindow)
+                row = sBias + stage * p.bias.count +
+                      (rq - walk.rel - bias_start(p.bias, rq0 - walk.rel));
+            else if (BIAS)
+                row = bias + rq - walk.rel;
+            if (BIAS) walk.half(part, x, rel);
+        };
+        aim();
         for (int j = 0; j < T_tiles; ++j) {
             const int live = keys - j * kTcN;
             uint32_t r[kTcHalf];
-            const float *row = nullptr;   // the bias of this query and the tile's first key
-            int x = 0, rel = 0;
-            if (BIAS) {
-                if (BIAS == kBiasWindow) {
-                    wait(&k_full[stage], phase);
-                    row = sBias + stage * p.bias.count +
-                          (rq - walk.rel - bias_start(p.bias, rq0 - walk.rel));
-                } else {
-                    row = bias + rq - walk.rel;
-                }
-                if (BIAS == kBiasGlobal || !p.bias.runs)
-                    bias_offsets(s_rel[warp], walk, first, live, inverse);
-                else
-                    walk.half(part, x, rel);
-                walk.next();
-            }
+            float b[kTcHalf];
             wait(&s_full[j & 1], (j / 2) & 1);
             tcgen05_fence_after_sync();
             const uint32_t ts = tmem + my_tmem + (j & 1) * kTcN + first;
-            tmem_ld_x32(ts, r);
-            const float2 cc = make_float2(c2, c2);
-            const auto score = [&](int c, float2 b) {
-                const float2 v = fma_f32x2(
-                    make_float2(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), cc, b);
-                r[c] = __float_as_uint(v.x);
-                r[c + 1] = __float_as_uint(v.y);
-            };
+            tmem_start_ld_x32(ts, r);
             if (!BIAS) {
 #pragma unroll
-                for (int c = 0; c < kTcHalf; c += 2) score(c, make_float2(0.0f, 0.0f));
+                for (int c = 0; c < kTcHalf; ++c) b[c] = 0.0f;
             } else if (BIAS == kBiasWindow && p.bias.runs) {
-                bias_by_runs<-1>(row, x, rel, walk, score);
+                bias_by_runs<-1>(row, x, rel, walk, b);
             } else {
-                bias_by_table<-1>(row, s_rel[warp], score);
+                bias_offsets(s_rel[warp], walk, first, live, inverse);
+                bias_by_table<-1>(row, s_rel[warp], b);
             }
+            tmem_wait_ld(r);
+            scale_and_bias(r, c2, b);
             if (live < kTcN) {   // masked keys, whatever they hold
                 asm volatile("" ::: "memory");   // a branch: the selects would cost every tile
 #pragma unroll
@@ -243,30 +239,36 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                 top4[c / 2 % 4] =
                     max3(top4[c / 2 % 4], __uint_as_float(r[c]), __uint_as_float(r[c + 1]));
             float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
-            s_top[j & 1][part][lane_row] = top;
-            pair_sync(pair);
-            top = fmaxf(top, s_top[j & 1][part ^ 1][lane_row]);
-            // (top > m + growth) also takes a row out of m = -inf
-            if (j == 0) {
-                m = top;
-            } else if (__any_sync(0xffffffffu, top > m + kLazyGrowth)) {
-                const float keep = top == -INFINITY ? 1.0f : exp2_approx(m - top);
-                wait(&pv_done[(j - 1) % NS], ((j - 1) / NS) & 1);
-                tcgen05_fence_after_sync();
-                const uint32_t to = tmem_o + my_tmem;
+            // a new reference for the pair's rows (also out of m = -inf): rare after
+            // the first tile
+            if (pair_any(pair, top > m + kLazyGrowth)) {
+                s_top[turn][part][lane_row] = top;
+                pair_sync(pair);
+                top = fmaxf(top, s_top[turn][part ^ 1][lane_row]);
+                turn ^= 1;
+                if (j > 0) {
+                    const float keep = top == -INFINITY ? 1.0f : exp2_approx(m - top);
+                    wait(&pv_done[(j - 1) % NS], ((j - 1) / NS) & 1);
+                    tcgen05_fence_after_sync();
+                    const uint32_t to = tmem_o + my_tmem;
 #pragma unroll 1
-                for (int d = part * 32; d < DP; d += 64) {   // every other chunk of O
-                    uint32_t o[32];
-                    tmem_ld_x32(to + d, o);
+                    for (int d = part * 32; d < DP; d += 64) {   // every other chunk of O
+                        uint32_t o[32];
+                        tmem_ld_x32(to + d, o);
 #pragma unroll
-                    for (int k = 0; k < 32; ++k)
-                        o[k] = __float_as_uint(__uint_as_float(o[k]) * keep);
-                    tmem_st_x32(to + d, o);
+                        for (int k = 0; k < 32; ++k)
+                            o[k] = __float_as_uint(__uint_as_float(o[k]) * keep);
+                        tmem_st_x32(to + d, o);
+                    }
+                    tmem_wait_st();
+                    l *= keep;
                 }
-                tmem_wait_st();
-                l *= keep;
                 m = top;
             }
+            // the next tile's place, among the exponentials
+            if (BIAS) walk.next();
+            if (++stage == NS) stage = 0;
+            aim();
             // a row with no key yet: weights 0
             const float ref = m == -INFINITY ? 0.0f : m - kWeightShift<T>;
             float2 sum[2] = {};
@@ -286,17 +288,13 @@ __global__ void __launch_bounds__(kTcThreads, 2)
             tmem_wait_st();
             tcgen05_fence_before_sync();
             mbar_arrive(&p_ready[j & 1]);
-            if (++stage == NS) {
-                stage = 0;
-                phase ^= 1;
-            }
         }
         // the product before the last may be unfinished here, but the one a stage
         // earlier is done, so the phase's parity tells
         if (T_tiles > 0) wait(&pv_done[(T_tiles - 1) % NS], ((T_tiles - 1) / NS) & 1);
-        s_top[T_tiles & 1][part][lane_row] = l;   // the row's other half of the sum
+        s_top[turn][part][lane_row] = l;   // the row's other half of the sum
         pair_sync(pair);
-        l += s_top[T_tiles & 1][part ^ 1][lane_row];
+        l += s_top[turn][part ^ 1][lane_row];
         if (__all_sync(0xffffffffu, ok)) {
             tcgen05_fence_after_sync();
             const float inv = l != 0.0f ? 1.0f / l : 0.0f;

@@ -3,7 +3,10 @@
 //
 // The mask is a function of (seed, offset, element index) and is never stored:
 // the backward pass calls the same kernel on the gradient.  A thread moves
-// 16-byte runs, kRuns of them a block apart, all loads first.
+// 16-byte runs, kRuns of them a block apart, all loads first.  For 16-bit types
+// the generator weighs as much as the memory traffic (18 wide products and 20
+// exclusive-ors per four elements): 67 M bf16 take 65.5 us with a residual (6.1
+// TB/s) and 60 us without; two runs per thread in 32 registers take 77.5 and 61.5.
 #include "gs_internal.h"
 #include "gs_philox.cuh"
 #include "gs_vec.cuh"
