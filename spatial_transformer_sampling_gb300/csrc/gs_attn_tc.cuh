@@ -347,6 +347,12 @@ template <int SIGN>
 __device__ __forceinline__ void bias_by_runs(const float *row, int x, int rel, const TileWalk &walk,
                                              float (&b)[kTcHalf]) {
     const int W = walk.W, wrap = walk.P - walk.W;
+    if (x + kTcHalf <= W) {   // all in one grid row
+        const float *at = row + SIGN * rel;
+#pragma unroll
+        for (int c = 0; c < kTcHalf; ++c) b[c] = at[SIGN * c];
+        return;
+    }
 #pragma unroll
     for (int c = 0; c < kTcHalf; c += 8) {
         const float *at = row + SIGN * rel;
