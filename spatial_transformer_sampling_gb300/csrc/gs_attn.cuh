@@ -230,7 +230,8 @@ cudaError_t launch_attn_backward(const AttnArgs &args, const AttnPtrs &p, void *
         if (!tc) e = launch_attn_simt_bwd<T>(a, p, bias, lse2, delta, part, kv_heads, now, s);
         if (e != cudaSuccess) return e;
         if (part.window)
-            attn_rel_sum_kernel<<<dim3((a.R + 31) / 32, a.H), 512, 0, s>>>(a, part, now, rel);
+            attn_rel_sum_kernel<<<dim3((a.R + kRelSumIndices - 1) / kRelSumIndices, a.H),
+                                  kRelSumThreads, 0, s>>>(a, part, now, rel);
     }
     if (bias) {
         if (!part.window)

@@ -70,33 +70,48 @@ struct RelWindow {
         return p.part + slot * p.stride - (rq_min - rel_k(a, a.Lk - 1));
     }
 
-    // ds (fp32) of this thread's query and its half of the keys j0 .. j0 + 63, of
-    // which `live` count; `keys` in all.  Both warps call it; `out` as from init.
-    __device__ __forceinline__ void add(const AttnArgs &a, const float (&ds)[kRelHalf], int j0,
-                                        int live, int keys, float *out) {
+    // ds (fp32) of this thread's query and its half of a step's 64 keys, of which
+    // `live` count.  my_rel: rel_k of key half * 32 + lane of the step (of the last
+    // live one from there on); next_rel: of the next step's first key (`last`:
+    // there is none).  Both warps call it; `out` as from init.
+    __device__ __forceinline__ void add(const float (&ds)[kRelHalf], int live, int my_rel,
+                                        int next_rel, bool last, float *out) {
         const int lane = threadIdx.x % 32, first = half * kRelHalf;
         live = min(live, kRelCols);
-        rel[first + lane] = rel_k(a, min(j0 + first + lane, keys - 1));
+        rel[first + lane] = my_rel;
+        const bool all = __all_sync(0xffffffffu, mine);
         sync();   // and the windows are clear
         const int lo = rq_min - rel[live - 1];
         const int span = rq_max - rel[0] - lo + 1;
         float *at = copies + 2 * half * size + (rq - lo);
         constexpr int kStep = kRelHalf / 2;
+        if (all && live == kRelCols && rel[first + kRelHalf - 1] - rel[first] == kRelHalf - 1) {
+            // all rows and columns count and the columns are neighbours in a grid row
+            float *p0 = at - rel[first], *p1 = p0 + size - kStep;
 #pragma unroll
-        for (int s = 0; s < kStep; s += 4) {
-            const int4 o0 = *reinterpret_cast<const int4 *>(rel + first + s);
-            const int4 o1 = *reinterpret_cast<const int4 *>(rel + first + kStep + s);
-            const int k0[4] = {o0.x, o0.y, o0.z, o0.w}, k1[4] = {o1.x, o1.y, o1.z, o1.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const bool on0 = mine && first + s + e < live;
-                const bool on1 = mine && first + kStep + s + e < live;
-                float v0, v1;
-                if (on0) v0 = at[-k0[e]] + ds[s + e];
-                if (on1) v1 = at[size - k1[e]] + ds[kStep + s + e];
-                if (on0) at[-k0[e]] = v0;
-                if (on1) at[size - k1[e]] = v1;
+            for (int s = 0; s < kStep; ++s) {
+                const float v0 = p0[-s] + ds[s], v1 = p1[-s] + ds[kStep + s];
+                p0[-s] = v0;
+                p1[-s] = v1;
                 __syncwarp();
+            }
+        } else {
+#pragma unroll
+            for (int s = 0; s < kStep; s += 4) {
+                const int4 o0 = *reinterpret_cast<const int4 *>(rel + first + s);
+                const int4 o1 = *reinterpret_cast<const int4 *>(rel + first + kStep + s);
+                const int k0[4] = {o0.x, o0.y, o0.z, o0.w}, k1[4] = {o1.x, o1.y, o1.z, o1.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const bool on0 = mine && first + s + e < live;
+                    const bool on1 = mine && first + kStep + s + e < live;
+                    float v0, v1;
+                    if (on0) v0 = at[-k0[e]] + ds[s + e];
+                    if (on1) v1 = at[size - k1[e]] + ds[kStep + s + e];
+                    if (on0) at[-k0[e]] = v0;
+                    if (on1) at[size - k1[e]] = v1;
+                    __syncwarp();
+                }
             }
         }
         sync();
@@ -111,7 +126,7 @@ struct RelWindow {
             ring[(lo + k) & (size - 1)] += v;
         }
         sync();
-        const int final_above = j0 + live < keys ? rq_max - rel_k(a, j0 + live) : lo - 1;
+        const int final_above = last ? lo - 1 : rq_max - next_rel;
         for (int r = final_above + 1 + half * 32 + lane; r <= top; r += 64) {
             out[r] = ring[r & (size - 1)];
             ring[r & (size - 1)] = 0.0f;
@@ -168,27 +183,34 @@ cudaError_t launch_attn_delta(const AttnArgs &a, const AttnPtrs &p, float *lse2,
 }
 
 // rel[h][r] (+)= the sums of groups of 32 queries; `heads` (batch, head) pairs
-// from head0 on are in `part`.  32 indices a block, 16 threads per index that
-// take every 16th (item, group) pair and are joined in order.
-static __global__ void __launch_bounds__(512)
+// from head0 on are in `part`.  128 indices a block, four per thread; eight
+// warps take every eighth (item, group) pair and are joined in order.
+constexpr int kRelSumIndices = 128, kRelSumThreads = 256;
+static __global__ void __launch_bounds__(kRelSumThreads)
     attn_rel_sum_kernel(AttnArgs a, RelArgs p, int heads, float *rel) {
-    constexpr int kSlices = 16, kChunk = 32 * kSlices;
-    __shared__ int s_lo[kChunk], s_hi[kChunk];   // relative indices of a group's queries
-    __shared__ int s_low[kChunk];                // and how far below an item's keys reach
-    __shared__ float s_sum[kSlices][32];
+    constexpr int kSlices = kRelSumThreads / 32, kChunk = kRelSumThreads, kEach = kRelSumIndices / 32;
+    // per group of queries: its lowest and highest relative index, and where its
+    // entry 0 lies from the start of an item's sums; per item: that start, and how
+    // far the relative indices reach below a group's lowest one
+    __shared__ int s_lo[kChunk], s_hi[kChunk], s_at[kChunk], s_low[kChunk];
+    __shared__ const float *s_item[kChunk];
+    __shared__ float s_sum[kSlices][kRelSumIndices];
     const int lane = threadIdx.x % 32, slice = threadIdx.x / 32;
-    const int r0 = blockIdx.x * 32, r = r0 + lane, h = blockIdx.y;
+    const int r = blockIdx.x * kRelSumIndices + lane, h = blockIdx.y;
     const int groups = (a.Lq + 31) / 32, k_end = rel_k(a, a.Lk - 1);
     const int nh0 = p.head0 + (h - p.head0 % a.H + a.H) % a.H;   // this head's first pair
     const int items = nh0 < p.head0 + heads ? (p.head0 + heads - 1 - nh0) / a.H + 1 : 0;
-    float sum = 0.0f;
+    float sum[kEach] = {};
     for (int n0 = 0; n0 < items; n0 += kChunk)
         for (int w0 = 0; w0 < groups; w0 += kChunk) {
-            const int mine = min(w0 + (int)threadIdx.x, groups - 1);
-            const int keys = keys_of(a, (nh0 + min(n0 + (int)threadIdx.x, items - 1) * a.H) / a.H);
+            const int w_mine = min(w0 + (int)threadIdx.x, groups - 1);
+            const int nh = nh0 + min(n0 + (int)threadIdx.x, items - 1) * a.H;
+            const int keys = keys_of(a, nh / a.H);
             __syncthreads();
-            s_lo[threadIdx.x] = rel_q(a, mine * 32);
-            s_hi[threadIdx.x] = rel_q(a, min(mine * 32 + 31, a.Lq - 1));
+            s_lo[threadIdx.x] = rel_q(a, w_mine * 32);
+            s_hi[threadIdx.x] = rel_q(a, min(w_mine * 32 + 31, a.Lq - 1));
+            s_at[threadIdx.x] = (w_mine - w0) * p.stride + k_end - s_lo[threadIdx.x];
+            s_item[threadIdx.x] = p.part + ((int64_t)(nh - p.head0) * groups + w0) * p.stride;
             s_low[threadIdx.x] = keys > 0 ? rel_k(a, keys - 1) : INT_MIN / 2;
             __syncthreads();
             const int nw = min(kChunk, groups - w0), nn = min(kChunk, items - n0);
@@ -196,10 +218,11 @@ static __global__ void __launch_bounds__(512)
             const int di = kSlices / nw, dw = kSlices % nw;
 #pragma unroll 4
             for (int k = slice; k < nn * nw; k += kSlices) {
-                if (r <= s_hi[w] && r >= s_lo[w] - s_low[i])
-                    sum += __ldg(p.part +
-                                 ((int64_t)(nh0 + (n0 + i) * a.H - p.head0) * groups + w0 + w) * p.stride +
-                                 (r + k_end - s_lo[w]));
+                const int hi = s_hi[w], lo = s_lo[w] - s_low[i];
+                const float *at = s_item[i] + s_at[w] + r;
+#pragma unroll
+                for (int q = 0; q < kEach; ++q)
+                    if (r + 32 * q <= hi && r + 32 * q >= lo) sum[q] += __ldg(at + 32 * q);
                 i += di;
                 w += dw;
                 if (w >= nw) {
@@ -208,12 +231,17 @@ static __global__ void __launch_bounds__(512)
                 }
             }
         }
-    s_sum[slice][lane] = sum;
+#pragma unroll
+    for (int q = 0; q < kEach; ++q) s_sum[slice][lane + 32 * q] = sum[q];
     __syncthreads();
-    if (slice == 0 && r < a.R) {
-        for (int k = 1; k < kSlices; ++k) sum += s_sum[k][lane];
-        float *out = rel + (int64_t)h * a.R + r;
-        *out = p.head0 > 0 ? *out + sum : sum;
+    for (int k = threadIdx.x; k < kRelSumIndices; k += kRelSumThreads) {
+        const int at = blockIdx.x * kRelSumIndices + k;
+        float all = 0.0f;
+        for (int w = 0; w < kSlices; ++w) all += s_sum[w][k];
+        if (at < a.R) {
+            float *out = rel + (int64_t)h * a.R + at;
+            *out = p.head0 > 0 ? *out + all : all;
+        }
     }
 }
 

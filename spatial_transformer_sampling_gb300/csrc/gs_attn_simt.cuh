@@ -294,7 +294,9 @@ __device__ __forceinline__ void attn_simt_bwd_block(const AttnArgs &a, const Att
 #pragma unroll
             for (int c = 0; c < kRelHalf; ++c)
                 ds[c] = t2[(warp % 2 * kRelHalf + c) * kSimtPitch + warp / 2 * 32 + threadIdx.x % 32];
-            win.add(a, ds, j0, live, keys, rel_out);
+            const int col = min(j0 + warp % 2 * kRelHalf + (int)threadIdx.x % 32, keys - 1);
+            const bool last = live <= kSimtTile;
+            win.add(ds, live, rel_k(a, col), last ? 0 : rel_k(a, j0 + kSimtTile), last, rel_out);
         }
 #pragma unroll
         for (int c = 0; c < NC; ++c)

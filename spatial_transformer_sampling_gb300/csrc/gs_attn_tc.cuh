@@ -311,6 +311,12 @@ struct TileWalk {
             rel += P - W;
         }
     }
+    // Offset of the tile's token c < 64 from its first one.  `inverse` is
+    // 65536 / W + 1, which divides numbers below 128 by W < 64.
+    __device__ __forceinline__ int offset(int c, int inverse) const {
+        const int at = x + c, rows = W >= kTcN ? at >= W : (at * inverse) >> 16;
+        return c + rows * (P - W);
+    }
     // Place in its row of the tile's token `part` * 32, and its offset from the
     // tile's first one.
     __device__ __forceinline__ void half(int part, int &x_half, int &rel_half) const {
@@ -329,14 +335,11 @@ struct TileWalk {
 
 // Offsets of 32 consecutive columns from the first of their tile into a warp's
 // 32 ints; columns from `live` of the tile on repeat the last live one.
-// `inverse` is 65536 / W + 1 for W < 64, which divides numbers below 128 by W.
 __device__ __forceinline__ void bias_offsets(int *rel, const TileWalk &walk, int first, int live,
                                              int inverse) {
     const int lane = threadIdx.x % 32;
-    const int c = min(first + lane, live - 1), at = walk.x + c;
-    const int rows = walk.W >= kTcN ? at >= walk.W : (at * inverse) >> 16;
     __syncwarp();
-    rel[lane] = c + rows * (walk.P - walk.W);
+    rel[lane] = walk.offset(min(first + lane, live - 1), inverse);
     __syncwarp();
 }
 

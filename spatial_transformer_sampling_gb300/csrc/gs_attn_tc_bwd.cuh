@@ -286,6 +286,7 @@ __device__ __forceinline__ void attn_tc_bwd_block(const TcBwdArgs &p, int block)
                 r[c + 3] = __float_as_uint(exp2_approx(v.y));
             }
             // the next step's place, among the exponentials
+            const int my_rel = with_rel ? walk.rel + walk.offset(min(first + lane, live - 1), inverse) : 0;
             if (BIAS) walk.next();
             if (++stage == NS) stage = 0;
             aim();
@@ -326,7 +327,7 @@ __device__ __forceinline__ void attn_tc_bwd_block(const TcBwdArgs &p, int block)
             tcgen05_fence_before_sync();
             mbar_arrive(&pd_ready);
             if (!DKV && BIAS) {
-                if (with_rel) win.add(a, ds, t * kTcN, live, keys, rel_out);
+                if (with_rel) win.add(ds, live, my_rel, walk.rel, t + 1 == steps, rel_out);
             }
         }
         if (steps > 0) wait(&finished, 0);
