@@ -1,6 +1,6 @@
 // gs_attn_tc_fwd.cuh -- attention forward on the tensor cores (fp16 / bf16).
 //
-// One CTA per 128 queries of one head; it walks the keys 64 at a time:
+// One CTA per 128 queries of one head, two to an SM; it walks the keys 64 at a time:
 //   S = Q K^T             tcgen05.mma, fp32 in TMEM, two buffers
 //   p = 2^(c S + bias - m)  two softmax threads per query, m its running reference
 //   O += p V              tcgen05.mma with p (16-bit) read from TMEM, where it
@@ -9,7 +9,10 @@
 // keys each and exchange their maxima through shared memory.  One thread of a
 // ninth warp issues the MMAs (the scores of tile j + 1 are computed while the
 // softmax warps work on tile j), one of a tenth the TMA loads: issued by one
-// warp with votes between, both took longer than the softmax.
+// warp with votes between, both took longer than the softmax.  Where heads are
+// short a CTA goes through several items of 128 queries (MANY): the copies and
+// the scores of the next one run ahead of the end of the current one, whose
+// output is stored after the next one's first tile.
 //
 // The reference m follows the row's maximum lazily: O and the row sum are
 // rescaled only when the maximum has grown by more than 2^8 since (the final
@@ -31,6 +34,7 @@ struct TcFwdArgs {
     float *lse;
 };
 
+constexpr int kTcSms = 152;
 constexpr float kLazyGrowth = 8.0f;   // log2 of how far the maximum may outgrow the reference
 
 // log2 of the weight at the reference: fp16 weights are kept 2^6 up, so that
@@ -38,45 +42,94 @@ constexpr float kLazyGrowth = 8.0f;   // log2 of how far the maximum may outgrow
 template <typename T> constexpr float kWeightShift = 0.0f;
 template <> constexpr float kWeightShift<__half> = 6.0f;
 
-template <int DP> struct TcFwdShape {
+template <int DP, bool MANY> struct TcFwdShape {
     static constexpr int kStages = DP == 64 ? 3 : 2;
+    // queries and outputs of two items at a time, where both fit
+    static constexpr int kItems = MANY && DP == 64 ? 2 : 1;
     static constexpr int kQBytes = kTcM * DP * 2;
     static constexpr int kTileBytes = kTcN * DP * 2;
-    static constexpr int kTileSmem = kQBytes + 2 * kStages * kTileBytes;
+    static constexpr int kTileSmem = kItems * kQBytes + 2 * kStages * kTileBytes;
     static constexpr int kSmem = kTileSmem + 1024;   // 1024-byte alignment of the tiles
     static constexpr int kTmemCols = 256;            // two score buffers, O; two CTAs per SM
     static constexpr int kTmemO = 2 * kTcN;
 };
 
-template <typename T, int DP, int BIAS>
+// An item of work: 128 queries of one head.  A CTA takes one, or with MANY every
+// gridDim.x-th one; its key tiles are numbered through (`tile`), which gives a tile its score
+// buffer, its stage of NS and the parity of their barriers' phases, and so are
+// the items that have keys (`count`).
+template <int NS, bool MANY> struct TcItem {
+    int index, n, h, i0, keys, tiles, j, tile, stage, parity, count;
+    __device__ __forceinline__ void decode(const AttnArgs &a, int q_tiles) {
+        i0 = index % q_tiles * kTcM;
+        h = index / q_tiles % a.H;
+        n = index / q_tiles / a.H;
+        keys = keys_of(a, n);
+        tiles = (keys + kTcN - 1) / kTcN;
+    }
+    // The first item with keys from `index` on; false when there is none.
+    __device__ __forceinline__ bool seek(const AttnArgs &a, int q_tiles, int items) {
+        for (; index < items; index += gridDim.x) {
+            decode(a, q_tiles);
+            if (tiles > 0) return true;
+            if (!MANY) break;
+        }
+        return false;
+    }
+    // The next tile, of the next item after the last; false when there is none.
+    __device__ __forceinline__ bool next(const AttnArgs &a, int q_tiles, int items) {
+        step();
+        if (++j < tiles) return true;
+        if (!MANY) return false;
+        j = 0;
+        ++count;
+        index += gridDim.x;
+        return seek(a, q_tiles, items);
+    }
+    __device__ __forceinline__ void step() {
+        ++tile;
+        if (++stage == NS) {
+            stage = 0;
+            parity ^= 1;
+        }
+    }
+    // Stage of the tile `back` < NS + 1 tiles ago, and its barriers' parity.
+    __device__ __forceinline__ int stage_of(int back, int &its_parity) const {
+        const int s = stage - back;
+        its_parity = s < 0 ? parity ^ 1 : parity;
+        return s < 0 ? s + NS : s;
+    }
+    __device__ __forceinline__ bool last() const { return j + 1 == tiles; }
+    __device__ __forceinline__ bool tail() const { return last() && keys % kTcN != 0; }
+};
+
+template <typename T, int DP, int BIAS, bool MANY>
 __global__ void __launch_bounds__(kTcThreads, 2)
     attn_tc_fwd_kernel(const __grid_constant__ TcFwdArgs p) {
-    using Sh = TcFwdShape<DP>;
-    constexpr int NS = Sh::kStages;
-    constexpr bool kBf16 = sizeof(T) == 2 && __is_same(T, __nv_bfloat16);
+    using Sh = TcFwdShape<DP, MANY>;
+    constexpr int NS = Sh::kStages, NI = Sh::kItems;
+    constexpr bool kBf16 = __is_same(T, __nv_bfloat16);
     extern __shared__ unsigned char smem_raw[];
-    __shared__ uint64_t q_full, k_full[NS], v_full[NS], s_full[2], p_ready[2], pv_done[NS], cleared;
+    __shared__ uint64_t q_full[NI], q_free[NI], o_free[NI], k_full[NS], v_full[NS], pv_done[NS],
+        s_full[2], p_ready[2], landed, drained;
     __shared__ uint32_t tmem_base;
-
-    const AttnArgs &a = p.a;
-    unsigned char *tiles = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-    unsigned char *sQ = tiles, *sK = tiles + Sh::kQBytes, *sV = sK + NS * Sh::kTileBytes;
-    float *sBias = reinterpret_cast<float *>(tiles + Sh::kTileSmem);   // a window per stage
     __shared__ __align__(16) int s_rel[8][kTcHalf];
     __shared__ float s_top[2][2][kTcM];   // of the two threads of a query, in turn
 
-    const int q_tiles = (a.Lq + kTcM - 1) / kTcM;
-    const int i0 = (int)(blockIdx.x % q_tiles) * kTcM;
-    const int h = (int)(blockIdx.x / q_tiles % a.H), n = (int)(blockIdx.x / q_tiles / a.H);
+    const AttnArgs &a = p.a;
+    unsigned char *tiles = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+    unsigned char *sQ = tiles, *sK = tiles + NI * Sh::kQBytes, *sV = sK + NS * Sh::kTileBytes;
+    float *sBias = reinterpret_cast<float *>(tiles + Sh::kTileSmem);   // a window per stage
+    const int q_tiles = (a.Lq + kTcM - 1) / kTcM, items = q_tiles * a.H * a.N;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    // entry of relative index 0, and the first query's index
-    const float *bias = BIAS ? p.bias.base + (int64_t)h * p.bias.stride : nullptr;
-    const int rq0 = rel_q(a, i0);
-    const int keys = keys_of(a, n), T_tiles = (keys + kTcN - 1) / kTcN;
 
     if (warp == kTcMmaWarp) {
         if (lane == 0) {
-            mbar_init(&q_full, 1);
+            for (int b = 0; b < NI; ++b) {
+                mbar_init(&q_full[b], 1);
+                mbar_init(&q_free[b], 1);
+                mbar_init(&o_free[b], kTcSoft);
+            }
             for (int s = 0; s < NS; ++s) {
                 mbar_init(&k_full[s], 1);
                 mbar_init(&v_full[s], 1);
@@ -86,7 +139,8 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                 mbar_init(&s_full[b], 2);   // the MMA thread, which saw the copies land, and its MMAs
                 mbar_init(&p_ready[b], kTcSoft);
             }
-            mbar_init(&cleared, 1);
+            mbar_init(&landed, 1);
+            mbar_init(&drained, 1);
             fence_mbar_init();
         }
         __syncwarp();
@@ -95,84 +149,105 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     }
     __syncthreads();
     tcgen05_fence_after_sync();
-    const uint32_t tmem = tmem_base, tmem_o = tmem + Sh::kTmemO;
+    const uint32_t tmem = tmem_base;
     bool ok = true;
-
-    const bool tail = keys % kTcN != 0;   // the last tile holds masked keys
+    TcItem<NS, MANY> w = {};
+    w.index = blockIdx.x;
 
     if (warp == kTcCopyWarp) {
         // ---------------------------------------------------- copies
-        if (lane == 0 && T_tiles > 0) {
-            mbar_arrive_expect_tx(&q_full, Sh::kQBytes);
-            tc_load<DP, kTcM>(sQ, p.q, n, h, i0, &q_full);
-            for (int t = 0; t < T_tiles; ++t) {
-                const int s = t % NS;
-                if (t >= NS) {   // the stage's last tile is consumed
-                    ok = tc_wait(&pv_done[s], (t / NS - 1) & 1, a.err);
-                    if (!ok) break;
+        const float *bias = nullptr;
+        int rq0 = 0, tails = 0;
+        for (bool more = w.seek(a, q_tiles, items); more; more = w.next(a, q_tiles, items)) {
+            const int s = w.stage;
+            if (lane == 0) {
+                if (w.j == 0) {
+                    const int b = w.count % NI;
+                    if (w.count >= NI) ok = tc_wait(&q_free[b], (w.count / NI - 1) & 1, a.err);
+                    if (ok) {
+                        mbar_arrive_expect_tx(&q_full[b], Sh::kQBytes);
+                        tc_load<DP, kTcM>(sQ + b * Sh::kQBytes, p.q, w.n, w.h, w.i0, &q_full[b]);
+                    }
+                    if (BIAS) {
+                        bias = p.bias.base + (int64_t)w.h * p.bias.stride;
+                        rq0 = rel_q(a, w.i0);
+                    }
                 }
-                mbar_arrive_expect_tx(&k_full[s], Sh::kTileBytes + (BIAS == kBiasWindow ? p.bias.count * 4 : 0));
-                tc_load<DP, kTcN>(sK + s * Sh::kTileBytes, p.k, n, h, t * kTcN, &k_full[s]);
-                if (BIAS == kBiasWindow)
-                    bulk_copy_g2s(sBias + s * p.bias.count,
-                                  bias + bias_start(p.bias, rq0 - rel_k(a, t * kTcN)),
-                                  p.bias.count * 4, &k_full[s]);
-                mbar_arrive_expect_tx(&v_full[s], Sh::kTileBytes);
-                tc_load<DP, kTcN>(sV + s * Sh::kTileBytes, p.v, n, h, t * kTcN, &v_full[s]);
+                if (ok && w.tile >= NS) ok = tc_wait(&pv_done[s], w.parity ^ 1, a.err);   // consumed
+                if (ok) {
+                    mbar_arrive_expect_tx(&k_full[s], Sh::kTileBytes + (BIAS == kBiasWindow ? p.bias.count * 4 : 0));
+                    tc_load<DP, kTcN>(sK + s * Sh::kTileBytes, p.k, w.n, w.h, w.j * kTcN, &k_full[s]);
+                    if (BIAS == kBiasWindow)
+                        bulk_copy_g2s(sBias + s * p.bias.count,
+                                      bias + bias_start(p.bias, rq0 - rel_k(a, w.j * kTcN)),
+                                      p.bias.count * 4, &k_full[s]);
+                    // a tile with masked keys is cleared before it counts as loaded
+                    uint64_t *bar = w.tail() ? &landed : &v_full[s];
+                    mbar_arrive_expect_tx(bar, Sh::kTileBytes);
+                    tc_load<DP, kTcN>(sV + s * Sh::kTileBytes, p.v, w.n, w.h, w.j * kTcN, bar);
+                }
+            }
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (!ok) break;
+            if (w.tail()) {   // values of masked keys must not reach the product
+                ok = __all_sync(0xffffffffu, tc_wait(&landed, tails++ & 1, a.err));
+                if (!ok) break;
+                tc_clear_rows<DP, kTcN>(sV + s * Sh::kTileBytes, w.keys - w.j * kTcN);
+                if (lane == 0) mbar_arrive(&v_full[s]);
             }
         }
-        __syncwarp();
-        if (T_tiles > 0 && tail) {   // values of masked keys must not reach the product
-            const int t = T_tiles - 1;
-            ok = tc_wait(&v_full[t % NS], (t / NS) & 1, a.err);
-            __syncwarp();
-            tc_clear_rows<DP, kTcN>(sV + t % NS * Sh::kTileBytes, keys - t * kTcN);
-            if (lane == 0) mbar_arrive(&cleared);
-        }
         // every copy lands before the block may leave (they have, unless a wait gave up)
-        for (int t = max(0, T_tiles - NS); t < T_tiles; ++t) {
+        for (int t = max(0, w.tile - NS); t < w.tile; ++t) {
             tc_wait(&k_full[t % NS], (t / NS) & 1, a.err);
             tc_wait(&v_full[t % NS], (t / NS) & 1, a.err);
         }
+        if (!ok && w.count > 0) tc_wait(&q_full[(w.count - 1) % NI], ((w.count - 1) / NI) & 1, a.err);
     } else if (warp == kTcMmaWarp) {
         // ---------------------------------------------------- MMAs, one thread
-        if (lane == 0 && T_tiles > 0) {
+        if (lane == 0) {
             const uint32_t idesc_s = umma_idesc_f16(kBf16, kTcM, kTcN);
             const int steps = (a.D + 15) / 16;
             const uint32_t idesc_o = umma_idesc_f16_bmn(kBf16, kTcM, steps * 16);
             const uint32_t q_lo = umma_lo_kmajor(smem_u32(sQ)), k_lo = umma_lo_kmajor(smem_u32(sK));
             const uint32_t v_lo = umma_lo_mnmajor(smem_u32(sV), kTcN * 128);
-            ok = tc_wait(&q_full, 0, a.err) && tc_wait(&k_full[0], 0, a.err);
-            if (ok) {
-                tc_scores<DP>(tmem, q_lo, k_lo, idesc_s, steps);
-                mbar_arrive(&s_full[0]);
-                umma_commit(&s_full[0]);
-            }
-            for (int j = 0; j < T_tiles && ok; ++j) {
-                const int s = j % NS;
-                if (j + 1 < T_tiles) {   // scores into the other buffer: its weights are consumed
-                    const int s1 = (j + 1) % NS;
-                    if (j > 0) ok = tc_wait(&pv_done[(j - 1) % NS], ((j - 1) / NS) & 1, a.err);
-                    ok = ok && tc_wait(&k_full[s1], ((j + 1) / NS) & 1, a.err);
-                    if (!ok) break;
-                    tcgen05_fence_after_sync();
-                    tc_scores<DP>(tmem + ((j + 1) & 1) * kTcN, q_lo, k_lo + s1 * (Sh::kTileBytes / 16),
-                                  idesc_s, steps);
-                    mbar_arrive(&s_full[(j + 1) & 1]);
-                    umma_commit(&s_full[(j + 1) & 1]);
+            TcItem<NS, MANY> c = w;   // one tile ahead: its scores are issued before w's product
+            bool c_more = c.seek(a, q_tiles, items), w_more = w.seek(a, q_tiles, items);
+            const auto scores = [&] {
+                const int s = c.stage, b = c.count % NI;
+                if (c.j == 0) ok = tc_wait(&q_full[b], (c.count / NI) & 1, a.err);
+                if (ok && c.tile >= 2) {   // the weights of two tiles ago are consumed
+                    int parity;
+                    const int s2 = c.stage_of(2, parity);
+                    ok = tc_wait(&pv_done[s2], parity, a.err);
                 }
-                ok = tc_wait(&v_full[s], (j / NS) & 1, a.err);
-                if (tail && j == T_tiles - 1) ok = ok && tc_wait(&cleared, 0, a.err);
-                ok = ok && tc_wait(&p_ready[j & 1], (j / 2) & 1, a.err);
+                ok = ok && tc_wait(&k_full[s], c.parity, a.err);
+                if (!ok) return;
+                tcgen05_fence_after_sync();
+                tc_scores<DP>(tmem + (c.tile & 1) * kTcN, q_lo + b * (Sh::kQBytes / 16),
+                              k_lo + s * (Sh::kTileBytes / 16), idesc_s, steps);
+                mbar_arrive(&s_full[c.tile & 1]);
+                umma_commit(&s_full[c.tile & 1]);
+                if (c.last()) umma_commit(&q_free[b]);
+                c_more = c.next(a, q_tiles, items);
+            };
+            if (c_more) scores();
+            while (w_more && ok) {
+                if (c_more) scores();
+                const int s = w.stage, b = w.count % NI;
+                ok = ok && tc_wait(&v_full[s], w.parity, a.err);
+                if (w.j == 0 && w.count >= NI)   // the output that was there is stored
+                    ok = ok && tc_wait(&o_free[b], (w.count / NI - 1) & 1, a.err);
+                ok = ok && tc_wait(&p_ready[w.tile & 1], (w.tile / 2) & 1, a.err);
                 if (!ok) break;
                 tcgen05_fence_after_sync();
-                tc_weighted(tmem_o, tmem + (j & 1) * kTcN, v_lo + s * (Sh::kTileBytes / 16), idesc_o,
-                            j > 0);
+                tc_weighted(tmem + Sh::kTmemO + b * DP, tmem + (w.tile & 1) * kTcN,
+                            v_lo + s * (Sh::kTileBytes / 16), idesc_o, w.j > 0);
                 umma_commit(&pv_done[s]);
+                w_more = w.next(a, q_tiles, items);
             }
             if (!ok) {   // a wait gave up: let the MMAs end before TMEM is released
-                umma_commit(&q_full);
-                tc_wait(&q_full, 1, a.err);
+                umma_commit(&drained);
+                tc_wait(&drained, 0, a.err);
             }
         }
         __syncwarp();
@@ -187,123 +262,19 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         const int pair = warp % 4, part = warp / 4, lane_row = pair * 32 + lane;
         const uint32_t my_tmem = (uint32_t)(pair * 32) << 16;   // this warp's TMEM lanes
         const int first = part * kTcHalf;                       // this thread's columns of a tile
-        const int i = i0 + lane_row;
         const float c2 = a.scale * kLog2e;
-        const int rq = BIAS ? rel_q(a, min(i, a.Lq - 1)) : 0;
-        TileWalk walk;
-        if (BIAS) walk.init(a.Hk, a.Wk, a.P);
         const int inverse = 65536 / a.Wk + 1;
-        float m = -INFINITY, l = 0.0f;
-        int stage = 0, turn = 0;
-        // the bias of this query and the next tile's first key, and where the
-        // thread's columns start in the keys' grid
-        const float *row = nullptr;
-        int x = 0, rel = 0;
-        const auto aim = [&] {
-            if (BIAS == kBiasWindow)
-                row = sBias + stage * p.bias.count +
-                      (rq - walk.rel - bias_start(p.bias, rq0 - walk.rel));
-            else if (BIAS)
-                row = bias + rq - walk.rel;
-            if (BIAS) walk.half(part, x, rel);
-        };
-        aim();
-        for (int j = 0; j < T_tiles; ++j) {
-            const int live = keys - j * kTcN;
-            uint32_t r[kTcHalf];
-            float b[kTcHalf];
-            wait(&s_full[j & 1], (j / 2) & 1);
-            tcgen05_fence_after_sync();
-            const uint32_t ts = tmem + my_tmem + (j & 1) * kTcN + first;
-            tmem_start_ld_x32(ts, r);
-            if (!BIAS) {
-#pragma unroll
-                for (int c = 0; c < kTcHalf; ++c) b[c] = 0.0f;
-            } else if (BIAS == kBiasWindow && p.bias.runs) {
-                bias_by_runs<-1>(row, x, rel, walk, b);
-            } else {
-                bias_offsets(s_rel[warp], walk, first, live, inverse);
-                bias_by_table<-1>(row, s_rel[warp], b);
-            }
-            tmem_wait_ld(r);
-            scale_and_bias(r, c2, b);
-            if (live < kTcN) {   // masked keys, whatever they hold
-                asm volatile("" ::: "memory");   // a branch: the selects would cost every tile
-#pragma unroll
-                for (int c = 0; c < kTcHalf; ++c)
-                    if (first + c >= live) r[c] = __float_as_uint(-INFINITY);
-            }
-            float top4[4] = {m, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-            for (int c = 0; c < kTcHalf; c += 2)
-                top4[c / 2 % 4] =
-                    max3(top4[c / 2 % 4], __uint_as_float(r[c]), __uint_as_float(r[c + 1]));
-            float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
-            // a new reference for the pair's rows (also out of m = -inf): rare after
-            // the first tile
-            if (pair_any(pair, top > m + kLazyGrowth)) {
-                s_top[turn][part][lane_row] = top;
-                pair_sync(pair);
-                top = fmaxf(top, s_top[turn][part ^ 1][lane_row]);
-                turn ^= 1;
-                if (j > 0) {
-                    const float keep = top == -INFINITY ? 1.0f : exp2_approx(m - top);
-                    wait(&pv_done[(j - 1) % NS], ((j - 1) / NS) & 1);
-                    tcgen05_fence_after_sync();
-                    const uint32_t to = tmem_o + my_tmem;
-#pragma unroll 1
-                    for (int d = part * 32; d < DP; d += 64) {   // every other chunk of O
-                        uint32_t o[32];
-                        tmem_ld_x32(to + d, o);
-#pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            o[k] = __float_as_uint(__uint_as_float(o[k]) * keep);
-                        tmem_st_x32(to + d, o);
-                    }
-                    tmem_wait_st();
-                    l *= keep;
-                }
-                m = top;
-            }
-            // the next tile's place, among the exponentials
-            if (BIAS) walk.next();
-            if (++stage == NS) stage = 0;
-            aim();
-            // a row with no key yet: weights 0
-            const float ref = m == -INFINITY ? 0.0f : m - kWeightShift<T>;
-            float2 sum[2] = {};
-            const float2 one = make_float2(1.0f, 1.0f), shift = make_float2(-ref, -ref);
-            uint32_t w[kTcHalf / 2];
-#pragma unroll
-            for (int c = 0; c < kTcHalf; c += 2) {
-                float2 e = fma_f32x2(
-                    make_float2(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), one, shift);
-                e.x = exp2_approx(e.x);
-                e.y = exp2_approx(e.y);
-                sum[c / 2 % 2] = fma_f32x2(e, one, sum[c / 2 % 2]);
-                w[c / 2] = pack2<T>(e.x, e.y);
-            }
-            tmem_st_x16(ts, w);
-            l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-            tmem_wait_st();
-            tcgen05_fence_before_sync();
-            mbar_arrive(&p_ready[j & 1]);
-        }
-        // the product before the last may be unfinished here, but the one a stage
-        // earlier is done, so the phase's parity tells
-        if (T_tiles > 0) wait(&pv_done[(T_tiles - 1) % NS], ((T_tiles - 1) / NS) & 1);
-        s_top[turn][part][lane_row] = l;   // the row's other half of the sum
-        pair_sync(pair);
-        l += s_top[turn][part ^ 1][lane_row];
-        if (__all_sync(0xffffffffu, ok)) {
-            tcgen05_fence_after_sync();
+        int turn = 0;
+
+        // Stores the output of a finished item: rows of `o_at` in TMEM times 1 / l.
+        const auto store = [&](int n, int h, int i, uint32_t o_at, bool any, float m, float l) {
             const float inv = l != 0.0f ? 1.0f / l : 0.0f;
             T *out = (T *)p.O + (((int64_t)n * a.Lq + i) * a.H + h) * a.D;
 #pragma unroll 1
             for (int d = part * 32; d < a.D; d += 64) {
                 uint32_t o[32];
-                if (T_tiles > 0) {
-                    tmem_ld_x32(tmem_o + my_tmem + d, o);
+                if (any) {
+                    tmem_ld_x32(o_at + d, o);
                 } else {
 #pragma unroll
                     for (int k = 0; k < 32; ++k) o[k] = 0;
@@ -312,30 +283,171 @@ __global__ void __launch_bounds__(kTcThreads, 2)
 #pragma unroll
                     for (int k = 0; k < 32; k += 8)
                         if (d + k < a.D) {   // D is a multiple of 8
-                            uint4 w;
-                            uint32_t *u = &w.x;
+                            uint4 v;
+                            uint32_t *u = &v.x;
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
                                 u[e] = pack2<T>(__uint_as_float(o[k + 2 * e]) * inv,
                                                 __uint_as_float(o[k + 2 * e + 1]) * inv);
-                            *reinterpret_cast<uint4 *>(out + d + k) = w;
+                            *reinterpret_cast<uint4 *>(out + d + k) = v;
                         }
                 }
             }
             if (part == 0 && i < a.Lq && p.lse)
                 p.lse[((int64_t)n * a.H + h) * a.Lq + i] =
                     l != 0.0f ? (m - kWeightShift<T> + log2f(l)) * kLn2 : -INFINITY;
+        };
+        // The item before the current one, whose product ends while the first tile
+        // of the current one is worked on.
+        struct {
+            int n, h, i, stage, parity, count;
+            float m, l;
+        } past = {};
+        const auto finish = [&] {
+            s_top[turn][part][lane_row] = past.l;   // the row's other half of the sum
+            pair_sync(pair);
+            const float l = past.l + s_top[turn][part ^ 1][lane_row];
+            turn ^= 1;
+            wait(&pv_done[past.stage], past.parity);
+            const int b = past.count % NI;
+            if (__all_sync(0xffffffffu, ok)) {
+                tcgen05_fence_after_sync();
+                store(past.n, past.h, past.i, tmem + Sh::kTmemO + b * DP + my_tmem, true, past.m, l);
+                tcgen05_fence_before_sync();
+            }
+            mbar_arrive(&o_free[b]);
+        };
+
+        for (; w.index < items; w.index += gridDim.x) {
+            w.decode(a, q_tiles);
+            const int i = w.i0 + lane_row;
+            if (w.tiles == 0) {   // no key: nothing comes from the other warps
+                if (__all_sync(0xffffffffu, ok)) store(w.n, w.h, i, 0, false, 0.0f, 0.0f);
+                if (!MANY) break;
+                continue;
+            }
+            const float *bias = BIAS ? p.bias.base + (int64_t)w.h * p.bias.stride : nullptr;
+            const int rq0 = BIAS ? rel_q(a, w.i0) : 0, rq = BIAS ? rel_q(a, min(i, a.Lq - 1)) : 0;
+            const uint32_t to = tmem + Sh::kTmemO + w.count % NI * DP + my_tmem;
+            TileWalk walk;
+            if (BIAS) walk.init(a.Hk, a.Wk, a.P);
+            // the bias of this query and the next tile's first key, and where the
+            // thread's columns start in the keys' grid
+            const float *row = nullptr;
+            int x = 0, rel = 0;
+            const auto aim = [&] {
+                if (BIAS == kBiasWindow)
+                    row = sBias + w.stage * p.bias.count +
+                          (rq - walk.rel - bias_start(p.bias, rq0 - walk.rel));
+                else if (BIAS)
+                    row = bias + rq - walk.rel;
+                if (BIAS) walk.half(part, x, rel);
+            };
+            aim();
+            float m = -INFINITY, l = 0.0f;
+            for (w.j = 0; w.j < w.tiles; ++w.j) {
+                const int live = w.keys - w.j * kTcN, buffer = w.tile & 1, phase = (w.tile >> 1) & 1;
+                uint32_t r[kTcHalf];
+                float b[kTcHalf];
+                wait(&s_full[buffer], phase);
+                tcgen05_fence_after_sync();
+                const uint32_t ts = tmem + my_tmem + buffer * kTcN + first;
+                tmem_start_ld_x32(ts, r);
+                if (!BIAS) {
+#pragma unroll
+                    for (int c = 0; c < kTcHalf; ++c) b[c] = 0.0f;
+                } else if (BIAS == kBiasWindow && p.bias.runs) {
+                    bias_by_runs<-1>(row, x, rel, walk, b);
+                } else {
+                    bias_offsets(s_rel[warp], walk, first, live, inverse);
+                    bias_by_table<-1>(row, s_rel[warp], b);
+                }
+                tmem_wait_ld(r);
+                scale_and_bias(r, c2, b);
+                if (live < kTcN) {   // masked keys, whatever they hold
+                    asm volatile("" ::: "memory");   // a branch: the selects would cost every tile
+#pragma unroll
+                    for (int c = 0; c < kTcHalf; ++c)
+                        if (first + c >= live) r[c] = __float_as_uint(-INFINITY);
+                }
+                float top4[4] = {m, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int c = 0; c < kTcHalf; c += 2)
+                    top4[c / 2 % 4] =
+                        max3(top4[c / 2 % 4], __uint_as_float(r[c]), __uint_as_float(r[c + 1]));
+                float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
+                // a new reference for the pair's rows (also out of m = -inf): rare after
+                // the first tile
+                if (pair_any(pair, top > m + kLazyGrowth)) {
+                    s_top[turn][part][lane_row] = top;
+                    pair_sync(pair);
+                    top = fmaxf(top, s_top[turn][part ^ 1][lane_row]);
+                    turn ^= 1;
+                    if (w.j > 0) {
+                        const float keep = top == -INFINITY ? 1.0f : exp2_approx(m - top);
+                        int parity;
+                        const int s1 = w.stage_of(1, parity);
+                        wait(&pv_done[s1], parity);
+                        tcgen05_fence_after_sync();
+#pragma unroll 1
+                        for (int d = part * 32; d < DP; d += 64) {   // every other chunk of O
+                            uint32_t o[32];
+                            tmem_ld_x32(to + d, o);
+#pragma unroll
+                            for (int k = 0; k < 32; ++k)
+                                o[k] = __float_as_uint(__uint_as_float(o[k]) * keep);
+                            tmem_st_x32(to + d, o);
+                        }
+                        tmem_wait_st();
+                        l *= keep;
+                    }
+                    m = top;
+                }
+                // the next tile's place, among the exponentials
+                if (BIAS) walk.next();
+                w.step();
+                aim();
+                // a row with no key yet: weights 0
+                const float ref = m == -INFINITY ? 0.0f : m - kWeightShift<T>;
+                float2 sum[2] = {};
+                const float2 one = make_float2(1.0f, 1.0f), shift = make_float2(-ref, -ref);
+                uint32_t u[kTcHalf / 2];
+#pragma unroll
+                for (int c = 0; c < kTcHalf; c += 2) {
+                    float2 e = fma_f32x2(
+                        make_float2(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), one, shift);
+                    e.x = exp2_approx(e.x);
+                    e.y = exp2_approx(e.y);
+                    sum[c / 2 % 2] = fma_f32x2(e, one, sum[c / 2 % 2]);
+                    u[c / 2] = pack2<T>(e.x, e.y);
+                }
+                tmem_st_x16(ts, u);
+                l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                tmem_wait_st();
+                tcgen05_fence_before_sync();
+                mbar_arrive(&p_ready[buffer]);
+                if (MANY && w.j == 0 && w.count > 0) finish();
+            }
+            past.n = w.n;
+            past.h = w.h;
+            past.i = i;
+            past.stage = w.stage_of(1, past.parity);
+            past.count = w.count++;
+            past.m = m;
+            past.l = l;
+            if (!MANY) break;
         }
+        if (w.count > 0) finish();
     }
     tcgen05_fence_before_sync();
     __syncthreads();
     if (warp == kTcMmaWarp) tmem_dealloc(tmem, Sh::kTmemCols);
 }
 
-template <typename T, int DP, int BIAS>
+template <typename T, int DP, int BIAS, bool MANY>
 cudaError_t launch_attn_tc_fwd_as(const TcFwdArgs &p, cudaStream_t s) {
-    using Sh = TcFwdShape<DP>;
-    auto kernel = attn_tc_fwd_kernel<T, DP, BIAS>;
+    using Sh = TcFwdShape<DP, MANY>;
+    auto kernel = attn_tc_fwd_kernel<T, DP, BIAS, MANY>;
     static DeviceFlags ready;
     const cudaError_t e = once_per_device(ready, [&] {
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -343,9 +455,23 @@ cudaError_t launch_attn_tc_fwd_as(const TcFwdArgs &p, cudaStream_t s) {
     });
     if (e != cudaSuccess) return e;
     const int window = BIAS == kBiasWindow ? Sh::kStages * p.bias.count * 4 : 0;
-    const int64_t blocks = (int64_t)((p.a.Lq + kTcM - 1) / kTcM) * p.a.H * p.a.N;
+    const int64_t items = (int64_t)((p.a.Lq + kTcM - 1) / kTcM) * p.a.H * p.a.N;
+    const int64_t blocks = MANY ? std::min<int64_t>(items, 2 * kTcSms) : items;
     kernel<<<(unsigned)blocks, kTcThreads, Sh::kSmem + window, s>>>(p);
     return cudaGetLastError();
+}
+
+// MANY: blocks that go through items pay off where an item is so short that
+// setting up a block for it weighs (8 x 8 windows, 4096 items of one key tile:
+// 44.7 us, 59.6 with a block each); keeping count of the items costs a fifth of
+// a long one (64 x 64 tokens, 2048 items of 64 tiles: 557 us and 466).
+constexpr int kTcManyTiles = 4;
+template <typename T, int DP, int BIAS>
+cudaError_t launch_attn_tc_fwd_by_length(const TcFwdArgs &p, cudaStream_t s) {
+    const int64_t items = (int64_t)((p.a.Lq + kTcM - 1) / kTcM) * p.a.H * p.a.N;
+    return items > 2 * kTcSms && p.a.Lk <= kTcManyTiles * kTcN
+               ? launch_attn_tc_fwd_as<T, DP, BIAS, true>(p, s)
+               : launch_attn_tc_fwd_as<T, DP, BIAS, false>(p, s);
 }
 
 // Runs the tensor-core forward pass when it takes the pointers and strides;
@@ -371,9 +497,9 @@ cudaError_t launch_attn_tc_fwd(const AttnArgs &a, const AttnPtrs &ptr, const flo
     const int mode = !bias ? kBiasNone : p.bias.count ? kBiasWindow : kBiasGlobal;
     const auto run = [&](auto dp) {
         constexpr int DP = decltype(dp)::value;
-        return mode == kBiasNone     ? launch_attn_tc_fwd_as<T, DP, kBiasNone>(p, s)
-               : mode == kBiasWindow ? launch_attn_tc_fwd_as<T, DP, kBiasWindow>(p, s)
-                                     : launch_attn_tc_fwd_as<T, DP, kBiasGlobal>(p, s);
+        return mode == kBiasNone     ? launch_attn_tc_fwd_by_length<T, DP, kBiasNone>(p, s)
+               : mode == kBiasWindow ? launch_attn_tc_fwd_by_length<T, DP, kBiasWindow>(p, s)
+                                     : launch_attn_tc_fwd_by_length<T, DP, kBiasGlobal>(p, s);
     };
     return a.D <= 64 ? run(std::integral_constant<int, 64>()) : run(std::integral_constant<int, 128>());
 }

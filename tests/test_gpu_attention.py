@@ -410,3 +410,16 @@ def test_bias_gradient_summed_over_several_launches(gs_cuda):
     # pairs beside it, far below the smallest of those
     lim = ref.U["float16"] / 2 * (dT.abs() + sum(p.abs() for p in parts)) * 1.1 + 1e-2
     assert ((dT - sum(parts)).abs() <= lim).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("D", [32, 96])
+@pytest.mark.parametrize("q", [(6, 11), (8, 8), (1, 150)])
+def test_many_small_heads_of_ragged_length(gs_cuda, q, D, dtype):
+    # several items of work per block, of one to three key tiles, some with no key at all
+    L, N = q[0] * q[1], 260
+    g = wl.rng(340)
+    lens = g.integers(0, L + 1, size=N)
+    lens[:4] = [0, L, 1, 0]
+    lens[-1] = 0
+    Problem(gs_cuda, 341, dtype, N, 3, D, q, q, 8, k_len=[int(x) for x in lens]).both()
