@@ -18,6 +18,10 @@
 namespace gs {
 namespace {
 
+// Bound by memory.  16 x 256 x 256 rows of 64 fp32 forward: 91.4 us, 5.96 TB/s
+// (0.88 of a copy's rate); 16384 x 1024 bf16 backward: 32.7 us and 5.2 us for the
+// sum over blocks, 2.7 TB/s (the sums each block leaves behind are a tenth of its
+// traffic, and a row's two reductions stand between its loads and its store).
 constexpr int kNormThreads = 256;
 constexpr int kNormOnChip = 8192;      // widest row held in registers
 constexpr int kNormSms = 152;
@@ -338,8 +342,8 @@ template <int V, typename F> cudaError_t norm_shape(int runs, F &&f) {
 
 // Calls f(L, NV) for the backward pass: as many threads per row as keep a
 // thread's share, and with it the sums it holds, to one run (a block of 256 at
-// most), so that many warps share an SM: 16384 x 1024 bf16 takes @@ us, against
-// 37.5 with a warp per row and four runs per thread.
+// most), so that many warps share an SM: 16384 x 1024 bf16 takes 32.7 us, 37.5
+// with a warp per row and four runs per thread.
 template <int V, typename F> cudaError_t norm_backward_shape(int runs, F &&f) {
     using std::integral_constant;
     if (runs <= 8) return f(integral_constant<int, 8>(), integral_constant<int, 1>());
