@@ -2,10 +2,17 @@
 // fp32 tensors and for 16-bit ones whose rows the tensor-core kernels cannot
 // take (head widths or strides that are not multiples of 16 bytes).
 //
-// 64 x 64 score tiles, 256 threads, 4 x 4 values each, every product as a
-// register-tiled outer product over operands in shared memory laid out
-// contraction-major ([k][64 + 4]): per step two 16-byte shared loads feed
-// eight packed FMAs.  Rows (queries; keys in the dK / dV kernel) stay resident,
+// 64 x 64 score tiles, four warps of 32 x 32, a thread 8 x 4 values, every
+// product as a register-tiled outer product over operands in shared memory laid
+// out contraction-major ([k][64 + 4]): per step three 16-byte shared loads feed
+// sixteen packed FMAs.  A half-warp's lanes ask for 32 or 128 distinct bytes, one
+// pass through shared memory each; with 4 x 4 values in rows of 16 lanes the
+// loads took two thirds of its time and bound the kernels.  A tile's operands are
+// fetched into registers in one batch, since with two or three blocks per SM
+// the latency of loads in several batches showed.  Both together (4 images,
+// 8 heads, 48 x 48 tokens, D 64, fp32): forward 1504 -> 1319 us (33 TFLOP/s of about 75 that the FMA units
+// have), backward 4872 -> 4104 us (26 TFLOP/s).  Rows (queries; keys in the
+// dK / dV blocks) stay resident,
 // columns are walked tile by tile; weights and their gradients go back through
 // shared memory, over the columns' transposed copy, as the first operand of the
 // next product.  One block sums each gradient in one order.
@@ -19,7 +26,7 @@
 namespace gs {
 
 constexpr int kSimtTile = 64;
-constexpr int kSimtThreads = 256;
+constexpr int kSimtThreads = 128;
 constexpr int kSimtPitch = kSimtTile + 4;   // keeps 16-byte alignment, spreads banks
 
 // Element offsets of one operand: base + n, h, token strides.
@@ -30,78 +37,114 @@ template <typename T> struct SimtView {
         : p((const T *)base + n * s[0] + h * s[2]), by_token(s[1]) {}
 };
 
-// dst[d][64] from 64 tokens, zeros from `live` on; a thread reads along a row,
-// V elements at a time (16 bytes, or one where rows are not aligned).
-template <typename T, int V>
-__device__ __forceinline__ void simt_load_t(float *dst, const SimtView<T> &v, int row0, int live,
-                                            int D) {
-    const int row = threadIdx.x % kSimtTile;
-    const T *p = v.p + (int64_t)(row0 + row) * v.by_token;
-    const bool on = row < live;
-#pragma unroll 4
-    for (int d = threadIdx.x / kSimtTile * V; d < D; d += kSimtThreads / kSimtTile * V) {
-        float x[V] = {};
-        if (on) Run<T, V>::widen(Run<T, V>::load(p + d), x);
-#pragma unroll
-        for (int e = 0; e < V; ++e) dst[(d + e) * kSimtPitch + row] = x[e];
-    }
-}
+// 64 tokens of an operand on their way from device memory: fetched into
+// registers (by the backward kernel while the products of the tile before run),
+// then put into shared memory token-major or contraction-major, or both.  A warp takes 16 tokens, two
+// runs of V elements side by side: a 32-byte sector each, and no two lanes of a
+// store in one bank.  Tokens from `live` on are zeros.
+template <typename T, int NC, int V> struct SimtTokens {
+    static constexpr int kRuns = 64 * NC / (2 * V);
+    typename Run<T, V>::Raw r[kRuns];
 
-// dst[64][pitch] (D values a row) from 64 tokens, zeros from `live` on and
-// behind a row.
-template <typename T, int V>
-__device__ __forceinline__ void simt_load_n(float *dst, int pitch, const SimtView<T> &v, int row0,
-                                            int live, int D) {
-    const int runs = (pitch + V - 1) / V;
-#pragma unroll 4
-    for (int k = threadIdx.x; k < kSimtTile * runs; k += kSimtThreads) {
-        const int row = k / runs, d = (k - row * runs) * V;
-        float x[V] = {};
-        if (row < live && d < D)
-            Run<T, V>::widen(Run<T, V>::load(v.p + (int64_t)(row0 + row) * v.by_token + d), x);
-#pragma unroll
-        for (int e = 0; e < V; ++e)
-            if (d + e < pitch) dst[row * pitch + d + e] = x[e];
+    static __device__ __forceinline__ int token() {
+        return threadIdx.x / 32 * 16 + threadIdx.x % 16;
     }
-}
+    static __device__ __forceinline__ int first(int k) { return (threadIdx.x / 16 % 2 + 2 * k) * V; }
 
-// c[4][4] += sum_k a[k][4 rows] b[k][4 columns]
-__device__ __forceinline__ void simt_product(float2 (&c)[4][2], const float *a, int pitch_a,
+    __device__ __forceinline__ void fetch(const SimtView<T> &v, int row0, int live, int D) {
+        const T *p = v.p + (int64_t)(row0 + token()) * v.by_token;
+        const bool on = token() < live;
+#pragma unroll
+        for (int k = 0; k < kRuns; ++k) {
+            r[k] = Run<T, V>::zero();
+            if (on && first(k) < D) r[k] = Run<T, V>::load(p + first(k));
+        }
+    }
+    // dst[d][64]
+    __device__ __forceinline__ void put_t(float *dst, int D) const {
+#pragma unroll
+        for (int k = 0; k < kRuns; ++k) {
+            float x[V];
+            Run<T, V>::widen(r[k], x);
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                if (first(k) < D) dst[(first(k) + e) * kSimtPitch + token()] = x[e];
+        }
+    }
+    // dst[64][pitch]
+    __device__ __forceinline__ void put_n(float *dst, int pitch, int D) const {
+#pragma unroll
+        for (int k = 0; k < kRuns; ++k) {
+            float x[V];
+            Run<T, V>::widen(r[k], x);
+            float *at = dst + token() * pitch + first(k);
+            if (first(k) >= D) continue;
+            if constexpr (V == 1) {
+                at[0] = x[0];
+            } else {
+#pragma unroll
+                for (int e = 0; e < V; e += 4)
+                    *reinterpret_cast<float4 *>(at + e) =
+                        make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+            }
+        }
+    }
+};
+
+// A thread's place in the block's tile: eight rows from `row` on, four columns
+// from `col` on.
+struct SimtPlace {
+    int row, col;
+    __device__ __forceinline__ SimtPlace() {
+        const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+        row = warp / 2 * 32 + lane / 8 * 8;
+        col = warp % 2 * 32 + lane % 8 * 4;
+    }
+};
+
+// c[8 rows][4] += sum_k a[k][8 rows] b[k][4 columns].  Pairs of rows share a
+// packed FMA: the operand to be doubled is then the one of four values.
+__device__ __forceinline__ void simt_product(float2 (&c)[4][4], const float *a, int pitch_a,
                                              const float *b, int pitch_b, int K) {
 #pragma unroll 4
     for (int k = 0; k < K; ++k) {
         const float4 x = *reinterpret_cast<const float4 *>(a + k * pitch_a);
+        const float4 z = *reinterpret_cast<const float4 *>(a + k * pitch_a + 4);
         const float4 y = *reinterpret_cast<const float4 *>(b + k * pitch_b);
-        const float2 y0 = make_float2(y.x, y.y), y1 = make_float2(y.z, y.w);
-        const float r[4] = {x.x, x.y, x.z, x.w};
+        const float2 r[4] = {make_float2(x.x, x.y), make_float2(x.z, x.w), make_float2(z.x, z.y),
+                             make_float2(z.z, z.w)};
+        const float w[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            c[i][0] = fma_f32x2(make_float2(r[i], r[i]), y0, c[i][0]);
-            c[i][1] = fma_f32x2(make_float2(r[i], r[i]), y1, c[i][1]);
-        }
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                c[i][j] = fma_f32x2(r[i], make_float2(w[j], w[j]), c[i][j]);
     }
 }
 
-__device__ __forceinline__ float &at(float2 (&c)[4][2], int i, int j) {
-    return j % 2 ? c[i][j / 2].y : c[i][j / 2].x;
+__device__ __forceinline__ float &at(float2 (&c)[4][4], int i, int j) {
+    return i % 2 ? c[i / 2][j].y : c[i / 2][j].x;
 }
 
 // Stores the transpose of the block's 64 x 64 tile: dst[column][row].
-__device__ __forceinline__ void simt_store_t(float *dst, float2 (&c)[4][2], int ty, int tx) {
+__device__ __forceinline__ void simt_store_t(float *dst, float2 (&c)[4][4], const SimtPlace &me) {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-        *reinterpret_cast<float4 *>(dst + (tx * 4 + j) * kSimtPitch + ty * 4) =
-            make_float4(at(c, 0, j), at(c, 1, j), at(c, 2, j), at(c, 3, j));
+#pragma unroll
+        for (int i = 0; i < 8; i += 4)
+            *reinterpret_cast<float4 *>(dst + (me.col + j) * kSimtPitch + me.row + i) =
+                make_float4(at(c, i, j), at(c, i + 1, j), at(c, i + 2, j), at(c, i + 3, j));
 }
 
-__device__ __forceinline__ float half_warp_max(float v) {
+// Over the eight lanes that share a thread's rows.
+__device__ __forceinline__ float row_lanes_max(float v) {
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    for (int o = 4; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
     return v;
 }
-__device__ __forceinline__ float half_warp_sum(float v) {
+__device__ __forceinline__ float row_lanes_sum(float v) {
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
 
@@ -118,9 +161,10 @@ inline int simt_bwd_smem(int D, bool dkv, int rel) {
             (dkv ? 2 : 1) * kSimtTile * simt_pitch_n(D)) * 4 + rel_smem(rel, 2);
 }
 
-// NC: 64-column chunks of the head width.
+// NC: 64-column chunks of the head width.  Three blocks per SM without fetching
+// ahead beat two that do, 1319 to 1413 us at the size above.
 template <typename T, int NC, int E>
-__global__ void __launch_bounds__(kSimtThreads)
+__global__ void __launch_bounds__(kSimtThreads, NC == 1 ? 3 : 2)
     attn_simt_fwd_kernel(AttnArgs a, AttnPtrs p, const float *bias) {
     extern __shared__ float4 simt_smem[];
     const int D = a.D, pitch_n = simt_pitch_n(D);
@@ -129,48 +173,63 @@ __global__ void __launch_bounds__(kSimtThreads)
     const int tiles = (a.Lq + kSimtTile - 1) / kSimtTile;
     const int i0 = (int)(blockIdx.x % tiles) * kSimtTile;
     const int h = (int)(blockIdx.x / tiles % a.H), n = (int)(blockIdx.x / tiles / a.H);
-    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
+    const SimtPlace me;
+    // of the columns' two halves, for a row's maximum and its sum
+    __shared__ float s_half[2][kSimtTile];
+    const int side = me.col / 32;
+    const bool speaks = threadIdx.x % 8 == 0;   // for the eight lanes of its rows
     const float c2 = a.scale * kLog2e;
     const SimtView<T> Q(p.Q, a.qs, n, h), K(p.K, a.ks, n, h), V(p.V, a.vs, n, h);
     const int keys = keys_of(a, n);
     if (bias) bias += (int64_t)h * a.bias_stride;
 
-    simt_load_t<T, E>(qt, Q, i0, a.Lq - i0, D);
-    float2 o[NC][4][2] = {};
-    float m[4], l[4];
-    int rq[4];
+    SimtTokens<T, NC, E> next_k, next_v;
+    next_k.fetch(Q, i0, a.Lq - i0, D);
+    next_k.put_t(qt, D);
+    float2 o[NC][4][4] = {};
+    float m[8], l[8];
+    int rq[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 8; ++i) {
         m[i] = -INFINITY;
         l[i] = 0.0f;
-        rq[i] = bias ? rel_q(a, min(i0 + ty * 4 + i, a.Lq - 1)) : 0;
+        rq[i] = bias ? rel_q(a, min(i0 + me.row + i, a.Lq - 1)) : 0;
     }
     for (int j0 = 0; j0 < keys; j0 += kSimtTile) {
         const int live = keys - j0;
         __syncthreads();
-        simt_load_t<T, E>(kt, K, j0, live, D);
-        simt_load_n<T, E>(vn, pitch_n, V, j0, live, D);
+        next_k.fetch(K, j0, live, D);
+        if (NC == 1) next_v.fetch(V, j0, live, D);
+        next_k.put_t(kt, D);
+        if (NC == 2) next_v.fetch(V, j0, live, D);
+        next_v.put_n(vn, pitch_n, D);
         __syncthreads();
-        float2 s[4][2] = {};
-        simt_product(s, qt + ty * 4, kSimtPitch, kt + tx * 4, kSimtPitch, D);
+        float2 s[4][4] = {};
+        simt_product(s, qt + me.row, kSimtPitch, kt + me.col, kSimtPitch, D);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const bool on = tx * 4 + j < live;
-            const int rk = bias && on ? rel_k(a, j0 + tx * 4 + j) : 0;
+            const bool on = me.col + j < live;
+            const int rk = bias && on ? rel_k(a, j0 + me.col + j) : 0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < 8; ++i) {
                 const float b = bias && on ? __ldg(bias + rq[i] - rk) : 0.0f;
                 at(s, i, j) = on ? fmaf(at(s, i, j), c2, b) : -INFINITY;
             }
         }
-        float keep[4];
+        float top[8], keep[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float top = half_warp_max(fmaxf(
-                m[i], fmaxf(fmaxf(at(s, i, 0), at(s, i, 1)), fmaxf(at(s, i, 2), at(s, i, 3)))));
-            const float ref = top == -INFINITY ? 0.0f : top;   // no key yet: weights 0
+        for (int i = 0; i < 8; ++i) {
+            top[i] = row_lanes_max(
+                fmaxf(fmaxf(at(s, i, 0), at(s, i, 1)), fmaxf(at(s, i, 2), at(s, i, 3))));
+            if (speaks) s_half[side][me.row + i] = top[i];
+        }
+        __syncthreads();   // and kt is read
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float next = fmaxf(m[i], fmaxf(top[i], s_half[side ^ 1][me.row + i]));
+            const float ref = next == -INFINITY ? 0.0f : next;   // no key yet: weights 0
             keep[i] = exp2_approx(m[i] - ref);
-            m[i] = top;
+            m[i] = next;
             l[i] *= keep[i];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -178,34 +237,42 @@ __global__ void __launch_bounds__(kSimtThreads)
                 l[i] += at(s, i, j);
             }
         }
-        __syncthreads();
-        simt_store_t(kt, s, ty, tx);
+        simt_store_t(kt, s, me);
         __syncthreads();
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                o[c][i][0] = mul_f32x2(o[c][i][0], make_float2(keep[i], keep[i]));
-                o[c][i][1] = mul_f32x2(o[c][i][1], make_float2(keep[i], keep[i]));
-            }
-            if (c * 64 + tx * 4 < D)
-                simt_product(o[c], kt + ty * 4, kSimtPitch, vn + c * 64 + tx * 4, pitch_n,
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    o[c][i][j] = mul_f32x2(o[c][i][j], make_float2(keep[2 * i], keep[2 * i + 1]));
+            if (c * 64 + me.col < D)
+                simt_product(o[c], kt + me.row, kSimtPitch, vn + c * 64 + me.col, pitch_n,
                              min(live, kSimtTile));
         }
     }
+    __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float sum = half_warp_sum(l[i]), f = sum != 0.0f ? 1.0f / sum : 0.0f;
-        const int row = i0 + ty * 4 + i;
+    for (int i = 0; i < 8; ++i) {
+        l[i] = row_lanes_sum(l[i]);
+        if (speaks) s_half[side][me.row + i] = l[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        // both halves add in the same order
+        const float sum = s_half[0][me.row + i] + s_half[1][me.row + i];
+        const float f = sum != 0.0f ? 1.0f / sum : 0.0f;
+        const int row = i0 + me.row + i;
         if (row >= a.Lq) continue;
         T *out = (T *)p.O + (((int64_t)n * a.Lq + row) * a.H + h) * D;
 #pragma unroll
         for (int c = 0; c < NC; ++c)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                if (c * 64 + tx * 4 + j < D)
-                    out[c * 64 + tx * 4 + j] = IO<T>::st(at(o[c], i, j) * f);
-        if (tx == 0 && p.lse)
+                if (c * 64 + me.col + j < D)
+                    out[c * 64 + me.col + j] = IO<T>::st(at(o[c], i, j) * f);
+        if (me.col == 0 && p.lse)
             p.lse[((int64_t)n * a.H + h) * a.Lq + row] =
                 sum != 0.0f ? (m[i] + log2f(sum)) * kLn2 : -INFINITY;
     }
@@ -228,7 +295,8 @@ __device__ __forceinline__ void attn_simt_bwd_block(const AttnArgs &a, const Att
     const int tiles = (rows + kSimtTile - 1) / kSimtTile;
     const int i0 = block % tiles * kSimtTile;
     const int nh = rel.head0 + block / tiles, h = nh % a.H, n = nh / a.H;
-    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16, warp = threadIdx.x / 32;
+    const SimtPlace me;
+    const int warp = threadIdx.x / 32;
     const float c2 = a.scale * kLog2e;
     const int64_t dense[3] = {(int64_t)a.Lq * a.H * D, (int64_t)a.H * D, D};
     const SimtView<T> Q(p.Q, a.qs, n, h), K(p.K, a.ks, n, h), V(p.V, a.vs, n, h), G(p.dO, dense, n, h);
@@ -240,20 +308,29 @@ __device__ __forceinline__ void attn_simt_bwd_block(const AttnArgs &a, const Att
     delta += (int64_t)nh * rows64(a.Lq);
     if (bias) bias += (int64_t)h * a.bias_stride;
 
-    simt_load_t<T, E>(r1, R1, i0, live_rows - i0, D);
-    simt_load_t<T, E>(r2, R2, i0, live_rows - i0, D);
-    float2 acc1[NC][4][2] = {}, acc2[NC][4][2] = {};
-    float row_lse[4], row_delta[4];
-    int row_rel[4];
+    // One head-width chunk leaves the registers to fetch the next tile early.
+    constexpr bool kAhead = NC == 1;
+    SimtTokens<T, NC, E> next1, next2;
+    next1.fetch(R1, i0, live_rows - i0, D);
+    next2.fetch(R2, i0, live_rows - i0, D);
+    next1.put_t(r1, D);
+    next2.put_t(r2, D);
+    if (kAhead) {
+        next1.fetch(C1, 0, cols, D);
+        next2.fetch(C2, 0, cols, D);
+    }
+    float2 acc1[NC][4][4] = {}, acc2[NC][4][4] = {};
+    float row_lse[8], row_delta[8];
+    int row_rel[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int row = min(i0 + ty * 4 + i, max(live_rows - 1, 0));
+    for (int i = 0; i < 8; ++i) {
+        const int row = min(i0 + me.row + i, max(live_rows - 1, 0));
         row_lse[i] = DKV ? 0.0f : lse2[row];
         row_delta[i] = DKV ? 0.0f : delta[row];
         row_rel[i] = !bias ? 0 : DKV ? -rel_k(a, row) : rel_q(a, row);
     }
-    // four warps, two per 32 queries, see to the bias gradient
-    const bool with_rel = !DKV && rel.window > 0 && warp < 4 && i0 + warp / 2 * 32 < a.Lq && cols > 0;
+    // two warps per 32 queries see to the bias gradient
+    const bool with_rel = !DKV && rel.window > 0 && i0 + warp / 2 * 32 < a.Lq && cols > 0;
     RelWindow win;
     float *rel_out = nullptr;
     if (with_rel) rel_out = win.init(a, win_smem, rel, i0, nh, warp / 2, warp % 2);
@@ -261,23 +338,25 @@ __device__ __forceinline__ void attn_simt_bwd_block(const AttnArgs &a, const Att
     for (int j0 = 0; j0 < cols; j0 += kSimtTile) {
         const int live = cols - j0;
         __syncthreads();
-        simt_load_t<T, E>(t1, C1, j0, live, D);
-        simt_load_t<T, E>(t2, C2, j0, live, D);
-        simt_load_n<T, E>(n1, pitch_n, C1, j0, live, D);
-        if (DKV) simt_load_n<T, E>(n2, pitch_n, C2, j0, live, D);
+        if (!kAhead) next1.fetch(C1, j0, live, D);
+        next1.put_t(t1, D);
+        next1.put_n(n1, pitch_n, D);
+        if (!kAhead) next2.fetch(C2, j0, live, D);
+        next2.put_t(t2, D);
+        if (DKV) next2.put_n(n2, pitch_n, D);
         __syncthreads();
-        float2 s[4][2] = {}, d[4][2] = {};
-        simt_product(s, r1 + ty * 4, kSimtPitch, t1 + tx * 4, kSimtPitch, D);
-        simt_product(d, r2 + ty * 4, kSimtPitch, t2 + tx * 4, kSimtPitch, D);
+        float2 s[4][4] = {}, d[4][4] = {};
+        simt_product(s, r1 + me.row, kSimtPitch, t1 + me.col, kSimtPitch, D);
+        simt_product(d, r2 + me.row, kSimtPitch, t2 + me.col, kSimtPitch, D);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int col = j0 + tx * 4 + j;
-            const bool on = tx * 4 + j < live;
+            const int col = j0 + me.col + j;
+            const bool on = me.col + j < live;
             const int col_rel = !bias || !on ? 0 : DKV ? rel_q(a, col) : -rel_k(a, col);
             const float col_lse = DKV && on ? __ldg(lse2 + col) : 0.0f;
             const float col_delta = DKV && on ? __ldg(delta + col) : 0.0f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < 8; ++i) {
                 const float b = bias && on ? __ldg(bias + row_rel[i] + col_rel) : 0.0f;
                 const float lse = DKV ? col_lse : row_lse[i], del = DKV ? col_delta : row_delta[i];
                 const float w = on ? exp2_approx(fmaf(at(s, i, j), c2, b) - lse) : 0.0f;
@@ -286,9 +365,13 @@ __device__ __forceinline__ void attn_simt_bwd_block(const AttnArgs &a, const Att
             }
         }
         __syncthreads();
-        if (DKV) simt_store_t(t1, s, ty, tx);
-        simt_store_t(t2, d, ty, tx);
+        if (DKV) simt_store_t(t1, s, me);
+        simt_store_t(t2, d, me);
         __syncthreads();
+        if (kAhead) {
+            next1.fetch(C1, j0 + kSimtTile, live - kSimtTile, D);
+            next2.fetch(C2, j0 + kSimtTile, live - kSimtTile, D);
+        }
         if (with_rel) {
             float ds[kRelHalf];
 #pragma unroll
@@ -300,16 +383,16 @@ __device__ __forceinline__ void attn_simt_bwd_block(const AttnArgs &a, const Att
         }
 #pragma unroll
         for (int c = 0; c < NC; ++c)
-            if (c * 64 + tx * 4 < D) {
+            if (c * 64 + me.col < D) {
                 const int K_ = min(live, kSimtTile);
-                simt_product(acc1[c], t2 + ty * 4, kSimtPitch, n1 + c * 64 + tx * 4, pitch_n, K_);
+                simt_product(acc1[c], t2 + me.row, kSimtPitch, n1 + c * 64 + me.col, pitch_n, K_);
                 if (DKV)
-                    simt_product(acc2[c], t1 + ty * 4, kSimtPitch, n2 + c * 64 + tx * 4, pitch_n, K_);
+                    simt_product(acc2[c], t1 + me.row, kSimtPitch, n2 + c * 64 + me.col, pitch_n, K_);
             }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int row = i0 + ty * 4 + i;
+    for (int i = 0; i < 8; ++i) {
+        const int row = i0 + me.row + i;
         if (row >= rows) continue;
         const bool on = row < live_rows;   // rows of masked keys get zeros
         const int64_t at_row = (((int64_t)n * rows + row) * a.H + h) * D;
@@ -317,7 +400,7 @@ __device__ __forceinline__ void attn_simt_bwd_block(const AttnArgs &a, const Att
         for (int c = 0; c < NC; ++c)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int d = c * 64 + tx * 4 + j;
+                const int d = c * 64 + me.col + j;
                 if (d >= D) continue;
                 ((T *)(DKV ? p.dK : p.dQ))[at_row + d] = IO<T>::st(on ? at(acc1[c], i, j) * a.scale : 0.0f);
                 if (DKV) ((T *)p.dV)[at_row + d] = IO<T>::st(on ? at(acc2[c], i, j) : 0.0f);
