@@ -77,18 +77,20 @@ __global__ void attn_dbias_kernel(AttnArgs a, AttnPtrs p, const float *bias, con
 }
 
 // dtable[b][h]: a lane per bucket goes through the relative indices in order,
-// eight warps a share each of what shared memory holds at a time.
+// sixteen warps a share each of what shared memory holds at a time.  4.7 us for
+// 3969 indices, 225 buckets, 8 heads (eight warps: 6.6): two passes' latency.
+constexpr int kTableThreads = 512;
 template <typename T>
-__global__ void __launch_bounds__(256) attn_dtable_kernel(AttnArgs a, const float *rel, T *dTable) {
-    constexpr int kHeld = 2048, kShare = kHeld / 8;
+__global__ void __launch_bounds__(kTableThreads) attn_dtable_kernel(AttnArgs a, const float *rel, T *dTable) {
+    constexpr int kWarps = kTableThreads / 32, kHeld = 4096, kShare = kHeld / kWarps;
     __shared__ __align__(16) int2 s_pair[kHeld];   // bucket, bits of the sum
-    __shared__ float s_sum[8][32];
+    __shared__ float s_sum[kWarps][32];
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, h = blockIdx.y;
     const int b = blockIdx.x * 32 + lane;
     float sum = 0.0f;
     for (int r0 = 0; r0 < a.R; r0 += kHeld) {
         __syncthreads();
-        for (int k = threadIdx.x; k < kHeld; k += 256)
+        for (int k = threadIdx.x; k < kHeld; k += kTableThreads)
             s_pair[k] = r0 + k < a.R ? make_int2(__ldg(a.buckets + r0 + k),
                                                  __float_as_int(rel[(int64_t)h * a.R + r0 + k]))
                                      : make_int2(-1, 0);
@@ -105,7 +107,7 @@ __global__ void __launch_bounds__(256) attn_dtable_kernel(AttnArgs a, const floa
     s_sum[warp][lane] = sum;
     __syncthreads();
     if (warp == 0 && b < a.nb) {
-        for (int w = 1; w < 8; ++w) sum += s_sum[w][lane];
+        for (int w = 1; w < kWarps; ++w) sum += s_sum[w][lane];
         dTable[(int64_t)b * a.H + h] = IO<T>::st(sum);
     }
 }
@@ -237,7 +239,8 @@ cudaError_t launch_attn_backward(const AttnArgs &args, const AttnPtrs &p, void *
         if (!part.window)
             attn_dbias_kernel<T><<<(unsigned)(((int64_t)a.H * a.R + 7) / 8), 256, 0, s>>>(
                 a, p, bias, lse2, delta, rel);
-        attn_dtable_kernel<T><<<dim3((a.nb + 31) / 32, a.H), 256, 0, s>>>(a, rel, (T *)p.dTable);
+        attn_dtable_kernel<T><<<dim3((a.nb + 31) / 32, a.H), kTableThreads, 0, s>>>(a, rel,
+                                                                              (T *)p.dTable);
     }
     return cudaGetLastError();
 }
