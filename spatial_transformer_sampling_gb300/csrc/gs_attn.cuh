@@ -28,6 +28,7 @@ namespace {
 template <typename T>
 __global__ void attn_bias_kernel(const T *table, AttnArgs a, int pad, float *bias) {
     const int at = blockIdx.x * blockDim.x + threadIdx.x, r = at - pad;
+    let_next_kernel_start();
     if (at >= a.bias_stride) return;
     const int b = r >= 0 && r < a.R ? __ldg(a.buckets + r) : 0;
     for (int h = blockIdx.y; h < a.H; h += gridDim.y)
@@ -40,6 +41,7 @@ __global__ void attn_bias_kernel(const T *table, AttnArgs a, int pad, float *bia
 template <typename T>
 __global__ void attn_dbias_kernel(AttnArgs a, AttnPtrs p, const float *bias, const float *lse2,
                                   const float *delta, float *rel) {
+    wait_for_previous_kernel(bias, lse2, delta);
     const int64_t w = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / 32;
     const int lane = threadIdx.x % 32;
     if (w >= (int64_t)a.H * a.R) return;
@@ -88,6 +90,7 @@ __global__ void __launch_bounds__(kTableThreads) attn_dtable_kernel(AttnArgs a, 
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, h = blockIdx.y;
     const int b = blockIdx.x * 32 + lane;
     float sum = 0.0f;
+    wait_for_previous_kernel(rel);
     for (int r0 = 0; r0 < a.R; r0 += kHeld) {
         __syncthreads();
         for (int k = threadIdx.x; k < kHeld; k += kTableThreads)
@@ -232,17 +235,19 @@ cudaError_t launch_attn_backward(const AttnArgs &args, const AttnPtrs &p, void *
         if (!tc) e = launch_attn_simt_bwd<T>(a, p, bias, lse2, delta, part, kv_heads, now, s);
         if (e != cudaSuccess) return e;
         if (part.window)
-            attn_rel_sum_kernel<<<dim3((a.R + kRelSumIndices - 1) / kRelSumIndices, a.H),
-                                  kRelSumThreads, 0, s>>>(a, part, now, rel);
+            e = launch_next(true, attn_rel_sum_kernel, dim3((a.R + kRelSumIndices - 1) / kRelSumIndices, a.H),
+                            kRelSumThreads, 0, s, a, part, now, rel);
+        if (e != cudaSuccess) return e;
     }
     if (bias) {
         if (!part.window)
-            attn_dbias_kernel<T><<<(unsigned)(((int64_t)a.H * a.R + 7) / 8), 256, 0, s>>>(
-                a, p, bias, lse2, delta, rel);
-        attn_dtable_kernel<T><<<dim3((a.nb + 31) / 32, a.H), kTableThreads, 0, s>>>(a, rel,
-                                                                              (T *)p.dTable);
+            e = launch_next(true, attn_dbias_kernel<T>, (unsigned)(((int64_t)a.H * a.R + 7) / 8), 256, 0, s,
+                            a, p, bias, lse2, delta, rel);
+        if (e != cudaSuccess) return e;
+        e = launch_next(true, attn_dtable_kernel<T>, dim3((a.nb + 31) / 32, a.H), kTableThreads, 0, s, a,
+                        rel, (T *)p.dTable);
     }
-    return cudaGetLastError();
+    return e;
 }
 
 }  // namespace gs

@@ -14,6 +14,7 @@
 #include <algorithm>
 
 #include "gs_attn_common.cuh"
+#include "gs_ptx.cuh"
 
 namespace gs {
 
@@ -166,6 +167,9 @@ __global__ void attn_delta_kernel(AttnArgs a, const T *dO, const T *O, const flo
         lse2[nh * L64 + i] = v == -INFINITY ? INFINITY : v * kLog2e;   // no key: weights of 0
         delta[nh * L64 + i] = s;
     }
+    // nothing here reads the expanded bias, but the kernels that wait for this
+    // one's end do
+    wait_for_previous_kernel();
 }
 
 template <typename T>
@@ -177,9 +181,8 @@ cudaError_t launch_attn_delta(const AttnArgs &a, const AttnPtrs &p, float *lse2,
     while (vec && G * E < a.D) G *= 2;
     const int64_t per_item = ((int64_t)rows64(a.Lq) * a.H * G + 255) / 256;
     auto kernel = vec ? attn_delta_kernel<T, true> : attn_delta_kernel<T, false>;
-    kernel<<<(unsigned)(per_item * a.N), 256, 0, s>>>(a, (const T *)p.dO, (const T *)p.O, p.lse, G,
-                                                     (int)per_item, lse2, delta);
-    return cudaGetLastError();
+    return launch_next(a.nb > 0, kernel, (unsigned)(per_item * a.N), 256, 0, s, a, (const T *)p.dO,
+                       (const T *)p.O, p.lse, G, (int)per_item, lse2, delta);
 }
 
 // rel[h][r] (+)= the sums of groups of 32 queries; `heads` (batch, head) pairs
@@ -203,6 +206,8 @@ static __global__ void __launch_bounds__(kRelSumThreads)
     const int nh0 = p.head0 + (h - p.head0 % a.H + a.H) % a.H;   // this head's first pair
     const int items = nh0 < p.head0 + heads ? (p.head0 + heads - 1 - nh0) / a.H + 1 : 0;
     float sum[kEach] = {};
+    let_next_kernel_start();
+    wait_for_previous_kernel(p.part, rel);
     for (int n0 = 0; n0 < items; n0 += kChunk)
         for (int w0 = 0; w0 < groups; w0 += kChunk) {
             const int w_mine = min(w0 + (int)threadIdx.x, groups - 1);

@@ -181,6 +181,7 @@ __global__ void __launch_bounds__(kSimtThreads, NC == 1 ? 3 : 2)
     const float c2 = a.scale * kLog2e;
     const SimtView<T> Q(p.Q, a.qs, n, h), K(p.K, a.ks, n, h), V(p.V, a.vs, n, h);
     const int keys = keys_of(a, n);
+    wait_for_previous_kernel(bias);
     if (bias) bias += (int64_t)h * a.bias_stride;
 
     SimtTokens<T, NC, E> next_k, next_v;
@@ -304,6 +305,7 @@ __device__ __forceinline__ void attn_simt_bwd_block(const AttnArgs &a, const Att
     const int keys = keys_of(a, n);
     const int live_rows = DKV ? keys : a.Lq;
     const int cols = i0 < live_rows ? (DKV ? a.Lq : keys) : 0;
+    wait_for_previous_kernel(lse2, delta, bias);
     lse2 += (int64_t)nh * rows64(a.Lq);
     delta += (int64_t)nh * rows64(a.Lq);
     if (bias) bias += (int64_t)h * a.bias_stride;
@@ -431,8 +433,8 @@ cudaError_t launch_attn_simt_fwd(const AttnArgs &a, const AttnPtrs &p, const flo
     });
     if (e != cudaSuccess) return e;
     const int64_t blocks = (int64_t)((a.Lq + kSimtTile - 1) / kSimtTile) * a.H * a.N;
-    kernel<<<(unsigned)blocks, kSimtThreads, simt_fwd_smem(a.D), s>>>(a, p, bias);
-    return cudaGetLastError();
+    return launch_next(bias != nullptr, kernel, (unsigned)blocks, kSimtThreads, simt_fwd_smem(a.D), s,
+                       a, p, bias);
 }
 
 // The key blocks, then the query blocks: one launch, so that either fills the
@@ -465,9 +467,8 @@ cudaError_t launch_attn_simt_bwd(const AttnArgs &a, const AttnPtrs &p, const flo
     const int kv_blocks = (a.Lk + kSimtTile - 1) / kSimtTile * kv_heads;
     const int q_blocks = (a.Lq + kSimtTile - 1) / kSimtTile * q_heads;
     const int smem = std::max(simt_bwd_smem(a.D, true, 0), simt_bwd_smem(a.D, false, rel.window));
-    kernel<<<(unsigned)kv_blocks + (unsigned)q_blocks, kSimtThreads, smem, s>>>(a, p, bias, lse2, delta,
-                                                                               rel, kv_blocks);
-    return cudaGetLastError();
+    return launch_next(true, kernel, (unsigned)kv_blocks + (unsigned)q_blocks, kSimtThreads, smem, s, a,
+                       p, bias, lse2, delta, rel, kv_blocks);
 }
 
 }  // namespace gs

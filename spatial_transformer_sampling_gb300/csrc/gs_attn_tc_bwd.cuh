@@ -107,6 +107,7 @@ __device__ __forceinline__ void attn_tc_bwd_block(const TcBwdArgs &p, int block)
     __syncthreads();
     tcgen05_fence_after_sync();
     const uint32_t tmem = tmem_base;
+    wait_for_previous_kernel(lse2, delta, bias);
     bool ok = true;
 
     const bool tail = !DKV && cols % kTcN != 0;   // the last tile holds masked keys
@@ -398,8 +399,8 @@ cudaError_t launch_attn_tc_bwd_as(const TcBwdArgs &kv, const TcBwdArgs &q, int k
                               Qs::kSmem + rel_smem(q.rel.window, 4) + window(q, Qs::kStages));
     const int kv_blocks = (kv.a.Lk + kTcM - 1) / kTcM * kv_heads;
     const int q_blocks = (q.a.Lq + kTcM - 1) / kTcM * q_heads;
-    kernel<<<(unsigned)kv_blocks + (unsigned)q_blocks, kTcThreads, smem, s>>>(kv, q, kv_blocks);
-    return cudaGetLastError();
+    return launch_next(true, kernel, (unsigned)kv_blocks + (unsigned)q_blocks, kTcThreads, smem, s, kv, q,
+                       kv_blocks);
 }
 
 // dK and dV of `kv_heads` (batch, head) pairs and dQ of `q_heads` (either may be 0).

@@ -150,6 +150,8 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     __syncthreads();
     tcgen05_fence_after_sync();
     const uint32_t tmem = tmem_base;
+    const float *bias0 = p.bias.base;
+    wait_for_previous_kernel(bias0);
     bool ok = true;
     TcItem<NS, MANY> w = {};
     w.index = blockIdx.x;
@@ -169,7 +171,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                         tc_load<DP, kTcM>(sQ + b * Sh::kQBytes, p.q, w.n, w.h, w.i0, &q_full[b]);
                     }
                     if (BIAS) {
-                        bias = p.bias.base + (int64_t)w.h * p.bias.stride;
+                        bias = bias0 + (int64_t)w.h * p.bias.stride;
                         rq0 = rel_q(a, w.i0);
                     }
                 }
@@ -326,7 +328,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                 if (!MANY) break;
                 continue;
             }
-            const float *bias = BIAS ? p.bias.base + (int64_t)w.h * p.bias.stride : nullptr;
+            const float *bias = BIAS ? bias0 + (int64_t)w.h * p.bias.stride : nullptr;
             const int rq0 = BIAS ? rel_q(a, w.i0) : 0, rq = BIAS ? rel_q(a, min(i, a.Lq - 1)) : 0;
             const uint32_t to = tmem + Sh::kTmemO + w.count % NI * DP + my_tmem;
             TileWalk walk;
@@ -457,8 +459,8 @@ cudaError_t launch_attn_tc_fwd_as(const TcFwdArgs &p, cudaStream_t s) {
     const int window = BIAS == kBiasWindow ? Sh::kStages * p.bias.count * 4 : 0;
     const int64_t items = (int64_t)((p.a.Lq + kTcM - 1) / kTcM) * p.a.H * p.a.N;
     const int64_t blocks = MANY ? std::min<int64_t>(items, 2 * kTcSms) : items;
-    kernel<<<(unsigned)blocks, kTcThreads, Sh::kSmem + window, s>>>(p);
-    return cudaGetLastError();
+    return launch_next(BIAS != kBiasNone, kernel, (unsigned)blocks, kTcThreads, Sh::kSmem + window, s,
+                       p);
 }
 
 // MANY: blocks that go through items pay off where an item is so short that

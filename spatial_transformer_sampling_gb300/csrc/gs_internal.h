@@ -34,6 +34,28 @@ cudaError_t once_per_device(DeviceFlags &flags, F &&setup) {
     return e;
 }
 
+// Launches a kernel of a call whose kernels follow one another.  With `follows` it
+// comes after one of the same call: its blocks are set up while that one ends, and
+// it waits by itself (wait_for_previous_kernel) before it reads or writes what that
+// one has to do with.  Every kernel in between waits too, so that the end of one
+// means the end of all before it; a call's first kernel is launched without, so
+// that nothing of the call runs before the stream's earlier work has ended.
+template <typename... P, typename... A>
+cudaError_t launch_next(bool follows, void (*kernel)(P...), dim3 grid, int threads, int smem,
+                        cudaStream_t s, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = follows ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 constexpr int kSampleThreads = 256;
 
 struct Axis;   // gs_common.cuh

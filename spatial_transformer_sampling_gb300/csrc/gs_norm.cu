@@ -13,6 +13,7 @@
 // walks rows with a fixed set of blocks, so that a thread keeps the sums of its
 // columns over all its rows; a second kernel adds the blocks in order.
 #include "gs_internal.h"
+#include "gs_ptx.cuh"
 #include "gs_vec.cuh"
 
 namespace gs {
@@ -222,6 +223,7 @@ __global__ void __launch_bounds__(kNormThreads)
         }
     }
     if (!partials) return;
+    let_next_kernel_start();
     // the groups of the block in order; one column run of every thread at a time
     float *out = partials + (int64_t)blockIdx.x * 2 * a.D;
     __shared__ float s_ds[kNormThreads * V], s_db[kNormThreads * V];
@@ -308,6 +310,7 @@ __global__ void __launch_bounds__(1024)
     T *out = blockIdx.y ? dB : dScale;
     if (!out) return;
     float sum = 0.0f;
+    wait_for_previous_kernel(partials);
 #pragma unroll 4
     for (int b = slice; b < blocks; b += 32)
         if (d < D) sum += __ldg(partials + ((int64_t)b * 2 + blockIdx.y) * D + d);
@@ -451,9 +454,8 @@ cudaError_t launch_layer_norm_backward(const void *dY, const void *X, const void
             e = run_backward<T, 1>(dy, x, g, mean, inv, (T *)dX, sums, &blocks, a, s);
     }
     if (e != cudaSuccess || !(dScale || dB)) return e;
-    layer_norm_finish_kernel<T>
-        <<<dim3((a.D + 31) / 32, 2), 1024, 0, s>>>(partials, blocks, (T *)dScale, (T *)dB, a.D);
-    return cudaGetLastError();
+    return launch_next(blocks > 0, layer_norm_finish_kernel<T>, dim3((a.D + 31) / 32, 2), 1024, 0, s,
+                       partials, blocks, (T *)dScale, (T *)dB, a.D);
 }
 
 #define GS_NORM_INST(T)                                                                           \

@@ -26,6 +26,21 @@ __device__ __forceinline__ uint64_t global_timer_ns() {
     return t;
 }
 
+// A kernel launched by launch_next waits here until the kernel before it has
+// ended and its writes are visible; the others pass.  The pointers go through, so
+// that no load from them moves ahead of the wait, one that the compiler takes for
+// a load of constant data least of all.
+template <typename... P> __device__ __forceinline__ void wait_for_previous_kernel(P *&...pointers) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    (..., [](auto *&p) { asm volatile("" : "+l"(p)::"memory"); }(pointers));
+}
+
+// Lets the blocks of the kernel after this one be set up once every block of this
+// one has come here or ended.
+__device__ __forceinline__ void let_next_kernel_start() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 __device__ __forceinline__ void mbar_init(uint64_t *bar, uint32_t count) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count)
                  : "memory");
