@@ -28,7 +28,6 @@ namespace {
 template <typename T>
 __global__ void attn_bias_kernel(const T *table, AttnArgs a, int pad, float *bias) {
     const int at = blockIdx.x * blockDim.x + threadIdx.x, r = at - pad;
-    let_next_kernel_start();
     if (at >= a.bias_stride) return;
     const int b = r >= 0 && r < a.R ? __ldg(a.buckets + r) : 0;
     for (int h = blockIdx.y; h < a.H; h += gridDim.y)

@@ -206,7 +206,6 @@ static __global__ void __launch_bounds__(kRelSumThreads)
     const int nh0 = p.head0 + (h - p.head0 % a.H + a.H) % a.H;   // this head's first pair
     const int items = nh0 < p.head0 + heads ? (p.head0 + heads - 1 - nh0) / a.H + 1 : 0;
     float sum[kEach] = {};
-    let_next_kernel_start();
     wait_for_previous_kernel(p.part, rel);
     for (int n0 = 0; n0 < items; n0 += kChunk)
         for (int w0 = 0; w0 < groups; w0 += kChunk) {

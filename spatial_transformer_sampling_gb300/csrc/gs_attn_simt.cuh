@@ -438,7 +438,8 @@ cudaError_t launch_attn_simt_fwd(const AttnArgs &a, const AttnPtrs &p, const flo
 }
 
 // The key blocks, then the query blocks: one launch, so that either fills the
-// SMs that the other leaves.
+// SMs that the other leaves, the longer ones (four products of 64 x 64 x D a step,
+// not three) first.
 template <typename T, int NC, int E>
 __global__ void __launch_bounds__(kSimtThreads)
     attn_simt_bwd_kernel(AttnArgs a, AttnPtrs p, const float *bias, const float *lse2,

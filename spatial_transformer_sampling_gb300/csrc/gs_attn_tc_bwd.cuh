@@ -369,16 +369,19 @@ __device__ __forceinline__ void attn_tc_bwd_block(const TcBwdArgs &p, int block)
     if (warp == kTcMmaWarp) tmem_dealloc(tmem, Sh::kTmemCols);
 }
 
-// The key blocks, then the query blocks: one launch, so that either fills the
-// SMs that the other leaves.
+// The query blocks, then the key blocks: one launch, so that either fills the
+// SMs that the other leaves.  The longer ones (the bias gradient) come first: the
+// other order takes 126 us instead of 121 at 8 x 8 heads of 32 x 32 tokens; one of
+// each in turn takes 155.
 template <typename T, int DP, int BIAS>
 __global__ void __launch_bounds__(kTcThreads, TcBwdShape<DP, true>::kCtas)
     attn_tc_bwd_kernel(const __grid_constant__ TcBwdArgs kv, const __grid_constant__ TcBwdArgs q,
                        int kv_blocks) {
-    if ((int)blockIdx.x < kv_blocks)
-        attn_tc_bwd_block<T, DP, BIAS, true>(kv, blockIdx.x);
+    const int q_blocks = gridDim.x - kv_blocks;
+    if ((int)blockIdx.x < q_blocks)
+        attn_tc_bwd_block<T, DP, BIAS, false>(q, blockIdx.x);
     else
-        attn_tc_bwd_block<T, DP, BIAS, false>(q, blockIdx.x - kv_blocks);
+        attn_tc_bwd_block<T, DP, BIAS, true>(kv, blockIdx.x - q_blocks);
 }
 
 template <typename T, int DP, int BIAS>

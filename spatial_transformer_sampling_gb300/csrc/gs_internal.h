@@ -35,11 +35,14 @@ cudaError_t once_per_device(DeviceFlags &flags, F &&setup) {
 }
 
 // Launches a kernel of a call whose kernels follow one another.  With `follows` it
-// comes after one of the same call: its blocks are set up while that one ends, and
-// it waits by itself (wait_for_previous_kernel) before it reads or writes what that
-// one has to do with.  Every kernel in between waits too, so that the end of one
-// means the end of all before it; a call's first kernel is launched without, so
-// that nothing of the call runs before the stream's earlier work has ended.
+// comes after one of the same call: its blocks are set up once that one's blocks
+// have ended, and it waits by itself (wait_for_previous_kernel) for what that one
+// wrote before it reads or writes anything that the two share: 3 us less per pair
+// of kernels.  (Set up while the earlier kernel's blocks still run, they spread
+// unevenly over the SMs: attention over 1500 tokens, 6 heads, fp32, 242 us and not
+// 160.)  Every kernel in between waits too, so that the end of one means the end
+// of all before it; a call's first kernel is launched without, so that nothing of
+// the call runs before the stream's earlier work has ended.
 template <typename... P, typename... A>
 cudaError_t launch_next(bool follows, void (*kernel)(P...), dim3 grid, int threads, int smem,
                         cudaStream_t s, A... args) {

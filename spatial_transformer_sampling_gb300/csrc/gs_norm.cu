@@ -223,7 +223,6 @@ __global__ void __launch_bounds__(kNormThreads)
         }
     }
     if (!partials) return;
-    let_next_kernel_start();
     // the groups of the block in order; one column run of every thread at a time
     float *out = partials + (int64_t)blockIdx.x * 2 * a.D;
     __shared__ float s_ds[kNormThreads * V], s_db[kNormThreads * V];

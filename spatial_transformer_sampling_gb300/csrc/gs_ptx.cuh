@@ -35,12 +35,6 @@ template <typename... P> __device__ __forceinline__ void wait_for_previous_kerne
     (..., [](auto *&p) { asm volatile("" : "+l"(p)::"memory"); }(pointers));
 }
 
-// Lets the blocks of the kernel after this one be set up once every block of this
-// one has come here or ended.
-__device__ __forceinline__ void let_next_kernel_start() {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-
 __device__ __forceinline__ void mbar_init(uint64_t *bar, uint32_t count) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count)
                  : "memory");
