@@ -7,19 +7,26 @@
 // time with the next one in flight.  Each group keeps its own running maximum,
 // sum and output for up to NQ queries; groups, warps and the blocks of a
 // cluster, which share the keys of one head, are joined at the end (distributed
-// shared memory: no second launch and no workspace).  The bias is looked up per
-// key, its bucket two batches ahead and its entry one: looked up in place it
-// took 130 us instead of 98 (8 x 8 heads, 32771 keys, D 64, bf16).
+// shared memory: no second launch and no workspace).  The bias is looked up by
+// one lane per key, the bucket two batches ahead and the entry one: looked up in
+// place, the latency of both showed (130 us instead of 98).
+//
+// 8 x 8 heads, 32771 keys, D 64, bf16 (537 MB): 96.9 us, 5.5 TB/s, 0.82 of a copy's
+// rate; 84.6 us where the lengths are between half and all of that (403 MB, 0.70),
+// since the longest head sets the time.  One batch item: 24.4 us with clusters of
+// up to sixteen blocks, 33.8 with eight.
 #pragma once
 
 #include <cooperative_groups.h>
 
 #include "gs_attn_common.cuh"
+#include "gs_ptx.cuh"
 
 namespace gs {
 
 constexpr int kFewThreads = 256;
-constexpr int kFewMaxSplits = 8;  // blocks of a cluster
+constexpr int kFewMaxSplits = 16; // blocks of a cluster (more than 8: opted into)
+constexpr int kFewLanes = 4;      // lanes of a key at least: a batch has no more keys than the warp lanes
 constexpr int kFewQueries = 8;    // queries up to which this kernel is taken
 
 // E consecutive (VEC: one 16-byte load) or 32-strided elements of a row.
@@ -37,6 +44,7 @@ template <typename T, bool VEC> struct FewRow {
                 v[k] = live && part + 32 * k < D ? IO<T>::ld(row + part + 32 * k) : 0.0f;
         }
     }
+    __device__ __forceinline__ float2 pair(int k) const { return make_float2(at(2 * k), at(2 * k + 1)); }
     __device__ __forceinline__ float at(int k) const {
         if constexpr (VEC) {
             const uint32_t *u = &raw.x;
@@ -72,7 +80,8 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     const T *V = (const T *)p.V + n * a.vs[0] + h * a.vs[2];
     const T *table = (const T *)p.table;
 
-    float q[NQ][E], o[NQ][E], m[NQ], l[NQ];
+    float2 q[NQ][E / 2], o[NQ][E / 2];
+    float m[NQ], l[NQ];
     int rq[NQ];
 #pragma unroll
     for (int x = 0; x < NQ; ++x) {
@@ -80,9 +89,9 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         FewRow<T, VEC> r;
         r.load((const T *)p.Q + n * a.qs[0] + i * a.qs[1] + h * a.qs[2], part, a.D, true);
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            q[x][e] = r.at(e) * c2;
-            o[x][e] = 0.0f;
+        for (int e = 0; e < E / 2; ++e) {
+            q[x][e] = make_float2(r.at(2 * e) * c2, r.at(2 * e + 1) * c2);
+            o[x][e] = make_float2(0.0f, 0.0f);
         }
         m[x] = -INFINITY;
         l[x] = 0.0f;
@@ -92,63 +101,61 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     const int chunk = (keys + splits - 1) / splits;
     const int lo = min(rank * chunk, keys), hi = min(lo + chunk, keys);
     // The loads run ahead of their use: K, V and the bias by one batch of keys, the
-    // buckets that name the bias by two.
+    // buckets that name the bias by two.  A lane looks up the bias of one key of
+    // the warp's batch, the groups get it from there.
     FewRow<T, VEC> k[U], v[U];
-    T entry[U][NQ];           // table entries of the next batch
-    int bucket[U][NQ];        // and the buckets of the batch after it, then of the next
-    const auto key_of = [&](int base, int u) { return base + u * per_warp + group; };
+    T entry[NQ];              // table entries of the next batch
+    int bucket[NQ];           // and the buckets of the batch after it, then of the next
+    uint32_t has = 0;         // which of the entries there are, one bit per query
+    const int batch = per_warp * U;   // 32 keys at most
     const auto load_buckets = [&](int base) {
+        const int j = base + lane;
+        const bool on = lane < batch && j < hi;
+        const int rk = a.Hk == 1 ? j : on ? rel_k(a, j) : 0;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int j = key_of(base, u);
-            const int rk = a.Hk == 1 ? j : j < hi ? rel_k(a, j) : 0;
-#pragma unroll
-            for (int x = 0; x < NQ; ++x)
-                bucket[u][x] = a.nb && j < hi ? __ldg(a.buckets + rq[x] - rk) : -1;
-        }
+        for (int x = 0; x < NQ; ++x) bucket[x] = a.nb && on ? __ldg(a.buckets + rq[x] - rk) : -1;
     };
-    // whether the pair has an entry goes with it as one bit per key and query
-    uint32_t has = 0;
     const auto load = [&](int base) {
-        has = 0;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int j = key_of(base, u);
+            const int j = base + u * per_warp + group;
             k[u].load(K + (int64_t)j * a.ks[1], part, a.D, j < hi);
             v[u].load(V + (int64_t)j * a.vs[1], part, a.D, j < hi);
+        }
+        has = 0;
 #pragma unroll
-            for (int x = 0; x < NQ; ++x) {
-                const bool in = (unsigned)bucket[u][x] < (unsigned)a.nb;
-                entry[u][x] = in ? table[(int64_t)bucket[u][x] * a.H + h] : IO<T>::st(0.0f);
-                if (a.nb ? in : j < hi) has |= 1u << (u * NQ + x);
-            }
+        for (int x = 0; x < NQ; ++x) {
+            const bool in = (unsigned)bucket[x] < (unsigned)a.nb;
+            entry[x] = in ? table[(int64_t)bucket[x] * a.H + h] : IO<T>::st(0.0f);
+            if (a.nb ? in : base + lane < hi) has |= 1u << x;
         }
     };
-    const int stride = W * per_warp * U;
-    int base = lo + warp * per_warp * U;
+    const int stride = W * batch;
+    int base = lo + warp * batch;
     load_buckets(base);
     load(base);
     load_buckets(base + stride);
     for (; base < hi; base += stride) {
-        float s[U][NQ], b[U][NQ];
+        float s[U][NQ], b[NQ];
         FewRow<T, VEC> keys_now[U], values[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             keys_now[u] = k[u];
             values[u] = v[u];
-#pragma unroll
-            for (int x = 0; x < NQ; ++x)
-                b[u][x] = has >> (u * NQ + x) & 1 ? bias2(IO<T>::to_f(entry[u][x])) : -INFINITY;
         }
+#pragma unroll
+        for (int x = 0; x < NQ; ++x)
+            b[x] = has >> x & 1 ? bias2(IO<T>::to_f(entry[x])) : -INFINITY;
         load(base + stride);
         load_buckets(base + 2 * stride);
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int x = 0; x < NQ; ++x) {
-                s[u][x] = 0.0f;
+                float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
-                for (int e = 0; e < E; ++e) s[u][x] = fmaf(q[x][e], keys_now[u].at(e), s[u][x]);
+                for (int e = 0; e < E / 2; ++e) sum = fma_f32x2(q[x][e], keys_now[u].pair(e), sum);
+                s[u][x] = sum.x + sum.y;
             }
         for (int w = G / 2; w > 0; w /= 2)
 #pragma unroll
@@ -161,7 +168,8 @@ __global__ void __launch_bounds__(kFewThreads, 2)
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 // a key that is not there stays masked whatever its score
-                s[u][x] = b[u][x] == -INFINITY ? -INFINITY : s[u][x] + b[u][x];
+                const float its = __shfl_sync(0xffffffffu, b[x], u * per_warp + group);
+                s[u][x] = its == -INFINITY ? -INFINITY : s[u][x] + its;
                 top = fmaxf(top, s[u][x]);
             }
             const float ref = top == -INFINITY ? 0.0f : top;
@@ -169,7 +177,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
             m[x] = top;
             l[x] *= keep;
 #pragma unroll
-            for (int e = 0; e < E; ++e) o[x][e] *= keep;
+            for (int e = 0; e < E / 2; ++e) o[x][e] = mul_f32x2(o[x][e], make_float2(keep, keep));
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 s[u][x] = exp2_approx(s[u][x] - ref);
@@ -181,7 +189,8 @@ __global__ void __launch_bounds__(kFewThreads, 2)
 #pragma unroll
             for (int x = 0; x < NQ; ++x)
 #pragma unroll
-                for (int e = 0; e < E; ++e) o[x][e] = fmaf(s[u][x], values[u].at(e), o[x][e]);
+                for (int e = 0; e < E / 2; ++e)
+                    o[x][e] = fma_f32x2(make_float2(s[u][x], s[u][x]), values[u].pair(e), o[x][e]);
     }
     // join the groups of a warp
     for (int w = G; w < 32; w *= 2)
@@ -194,8 +203,11 @@ __global__ void __launch_bounds__(kFewThreads, 2)
             l[x] = l[x] * f + l2 * f2;
             m[x] = top;
 #pragma unroll
-            for (int e = 0; e < E; ++e)
-                o[x][e] = o[x][e] * f + __shfl_xor_sync(0xffffffffu, o[x][e], w) * f2;
+            for (int e = 0; e < E / 2; ++e) {
+                const float x2 = __shfl_xor_sync(0xffffffffu, o[x][e].x, w);
+                const float y2 = __shfl_xor_sync(0xffffffffu, o[x][e].y, w);
+                o[x][e] = make_float2(o[x][e].x * f + x2 * f2, o[x][e].y * f + y2 * f2);
+            }
         }
     if (group == 0) {
 #pragma unroll
@@ -203,7 +215,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
 #pragma unroll
             for (int e = 0; e < E; ++e) {
                 const int d = VEC ? part * E + e : part + 32 * e;
-                if (d < a.D) s_o[warp][x][d] = o[x][e];
+                if (d < a.D) s_o[warp][x][d] = e % 2 ? o[x][e / 2].y : o[x][e / 2].x;
             }
             if (part == 0) {
                 s_m[warp][x] = m[x];
@@ -273,6 +285,12 @@ cudaError_t launch_attn_few_as(const AttnArgs &a, const AttnPtrs &p, int G, cuda
     const int64_t jobs = (int64_t)((a.Lq + NQ - 1) / NQ) * a.H * a.N;
     int splits = 1;
     while (splits < kFewMaxSplits && jobs * splits * 2 <= 152 * 2 && a.Lk > 128 * splits) splits *= 2;
+    static DeviceFlags ready;
+    const cudaError_t e = once_per_device(ready, [&] {
+        return cudaFuncSetAttribute(attn_few_kernel<T, VEC, NQ>,
+                                    cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    });
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(jobs * splits));
     cfg.blockDim = dim3(kFewThreads);
@@ -293,9 +311,9 @@ cudaError_t launch_attn_few(const AttnArgs &a, const AttnPtrs &p, cudaStream_t s
     for (const void *x : {p.Q, p.K, p.V}) vec = vec && ((uintptr_t)x & 15u) == 0;
     for (int d = 0; d < 3; ++d)
         vec = vec && a.qs[d] % E == 0 && a.ks[d] % E == 0 && a.vs[d] % E == 0;
-    int G = 32;   // lanes per key: a power of two that covers the row
+    int G = 32;   // lanes per key: a power of two that covers the row, kFewLanes at least
     if (vec)
-        while (G / 2 * E >= a.D) G /= 2;
+        while (G > kFewLanes && G / 2 * E >= a.D) G /= 2;
     if (vec)
         return a.Lq == 1 ? launch_attn_few_as<T, true, 1>(a, p, G, s)
                          : launch_attn_few_as<T, true, 4>(a, p, G, s);

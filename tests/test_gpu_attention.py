@@ -423,3 +423,12 @@ def test_many_small_heads_of_ragged_length(gs_cuda, q, D, dtype):
     lens[:4] = [0, L, 1, 0]
     lens[-1] = 0
     Problem(gs_cuda, 341, dtype, N, 3, D, q, q, 8, k_len=[int(x) for x in lens]).both()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("Lq", [1, 5, 8])
+@pytest.mark.parametrize("D", [4, 8, 16, 128])
+def test_few_queries_at_every_width_of_a_key(gs_cuda, D, Lq, dtype):
+    # from one lane per key to a whole warp, keys shared by up to sixteen blocks
+    Problem(gs_cuda, 440, dtype, 1, 3, D, (1, Lq), (3, 811), 16, k_len=[2200]).forward()
+    Problem(gs_cuda, 441, dtype, 2, 2, D, (1, Lq), (1, 131)).forward()
