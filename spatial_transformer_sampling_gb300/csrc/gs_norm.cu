@@ -20,9 +20,11 @@ namespace gs {
 namespace {
 
 // Bound by memory.  16 x 256 x 256 rows of 64 fp32 forward: 91.4 us, 5.96 TB/s
-// (0.88 of a copy's rate); 16384 x 1024 bf16 backward: 32.7 us and 5.2 us for the
-// sum over blocks, 2.7 TB/s (the sums each block leaves behind are a tenth of its
-// traffic, and a row's two reductions stand between its loads and its store).
+// (0.88 of a copy's rate); 16384 x 1024 bf16 backward: 28.9 us with the sum over
+// blocks, 3.5 TB/s (a row's two reductions stand between its loads and its store,
+// and the sums that each block leaves behind are a tenth of the traffic).  Before
+// the arithmetic was packed, a thread's scale kept and the blocks cut to what the
+// registers hold at once, it took 41.9 us.
 constexpr int kNormThreads = 256;
 constexpr int kNormOnChip = 8192;      // widest row held in registers
 constexpr int kNormSms = 152;
@@ -138,88 +140,140 @@ __global__ void __launch_bounds__(kNormThreads)
 // Sums of two values over the L threads of a row; slots alternate between calls,
 // so that one barrier per call suffices.
 template <int L> __device__ __forceinline__ void row_sum2(float &a, float &b, int slot) {
+    if (L < 32) {
 #pragma unroll
-    for (int o = (L < 32 ? L : 32) / 2; o > 0; o >>= 1) {
-        a += __shfl_xor_sync(0xffffffffu, a, o);
-        b += __shfl_xor_sync(0xffffffffu, b, o);
+        for (int o = L / 2; o > 0; o >>= 1) {
+            a += __shfl_xor_sync(0xffffffffu, a, o);
+            b += __shfl_xor_sync(0xffffffffu, b, o);
+        }
+        return;
     }
-    if (L > 32) {
-        __shared__ float2 s[2][kNormThreads / 32];
-        if (threadIdx.x % 32 == 0) s[slot][threadIdx.x / 32] = make_float2(a, b);
+    // the lower half of a warp goes on with a, the upper half with b
+    const int lane = threadIdx.x % 32;
+    float v = lane < 16 ? a : b;
+    v += __shfl_xor_sync(0xffffffffu, lane < 16 ? b : a, 16);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (L == 32) {
+        a = __shfl_sync(0xffffffffu, v, 0);
+        b = __shfl_sync(0xffffffffu, v, 16);
+    } else {
+        constexpr int W = L > 32 ? L / 32 : 1;
+        __shared__ float s[2][2][kNormThreads / 32];
+        if (lane % 16 == 0) s[slot][lane / 16][threadIdx.x / 32] = v;
         __syncthreads();
         a = b = 0.0f;
-        const int first = threadIdx.x / L * (L / 32);
+        const int first = threadIdx.x / L * W;
 #pragma unroll
-        for (int w = 0; w < L / 32; ++w) {
-            a += s[slot][first + w].x;
-            b += s[slot][first + w].y;
+        for (int w = 0; w < W; ++w) {
+            a += s[slot][0][first + w];
+            b += s[slot][1][first + w];
         }
     }
 }
+
+// Blocks per SM of the backward pass, by the elements of a row that a thread holds.
+constexpr int norm_backward_blocks(int N) { return N <= 4 ? 4 : N <= 8 ? 3 : N <= 16 ? 2 : 1; }
 
 // dX of the block's rows and, into partials[block], its column sums (the sums
 // for dScale, then those for dB).  The next row's loads are issued before this
 // one is worked on.
 template <typename T, int V, int L, int NV>
-__global__ void __launch_bounds__(kNormThreads)
+__global__ void __launch_bounds__(kNormThreads, norm_backward_blocks(NV * V))
     layer_norm_backward_kernel(const T *dY, const T *X, const T *scale, const float *mean,
                                const float *inv, T *dX, float *partials, NormArgs a) {
     using IOV = Run<T, V>;
     constexpr int kGroups = kNormThreads / L;
+    constexpr int N = NV * V, P = (N + 1) / 2;   // a thread's elements, in pairs
     const int part = threadIdx.x % L, group = threadIdx.x / L;
-    float ds[NV][V] = {}, db[NV][V] = {};
-    typename IOV::Raw rx[NV], rg[NV];
+    const float per_d = 1.0f / (float)a.D;
+    float2 ds[P] = {}, db[P] = {};
+    typename IOV::Raw rx[NV], rg[NV], rw[NV];
     float m = 0.0f, iv = 0.0f;
+    // zeros behind a row's end, whose products and sums are zeros
     const auto load = [&](int64_t row) {
         const bool here = row < a.rows;
+        const int64_t at = row * a.D;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int d = (k * L + part) * V;
             const bool on = here && d < a.D;
-            rx[k] = on ? IOV::load(X + row * a.D + d) : IOV::zero();
-            rg[k] = on ? IOV::load(dY + row * a.D + d) : IOV::zero();
+            rx[k] = on ? IOV::load(X + at + d) : IOV::zero();
+            rg[k] = on ? IOV::load(dY + at + d) : IOV::zero();
         }
         m = here ? __ldg(mean + row) : 0.0f;
         iv = here ? __ldg(inv + row) : 0.0f;
     };
+    const auto load_scale = [&] {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int d = (k * L + part) * V;
+            rw[k] = d < a.D ? IOV::load(scale + d) : IOV::zero();
+        }
+    };
+    const auto pairs_of = [](const typename IOV::Raw (&r)[NV], float2 (&v)[P]) {
+        float f[2 * P] = {};
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            float e[V];
+            IOV::widen(r[k], e);
+#pragma unroll
+            for (int i = 0; i < V; ++i) f[k * V + i] = e[i];
+        }
+#pragma unroll
+        for (int p = 0; p < P; ++p) v[p] = make_float2(f[2 * p], f[2 * p + 1]);
+    };
+    const auto element = [](const float2 (&v)[P], int i) { return i % 2 ? v[i / 2].y : v[i / 2].x; };
     const int64_t step = (int64_t)gridDim.x * kGroups;
     int64_t row = (int64_t)blockIdx.x * kGroups + group;
     load(row);
+    if (NV == 1) load_scale();   // stays in registers
     int slot = 0;
     for (int64_t row0 = (int64_t)blockIdx.x * kGroups; row0 < a.rows; row0 += step, row += step) {
-        float xh[NV][V], gw[NV][V], s0 = 0.0f, s1 = 0.0f;
+        float2 xh[P], gw[P], w[P], t0 = {}, t1 = {};
+        if (NV > 1) load_scale();
+        pairs_of(rx, xh);
+        pairs_of(rg, gw);
+        pairs_of(rw, w);
+        const float2 minus_m = make_float2(-m, -m), iv2 = make_float2(iv, iv);
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int d = (k * L + part) * V;
-            float x[V], g[V], w[V] = {};
-            IOV::widen(rx[k], x);
-            IOV::widen(rg[k], g);
-            if (d < a.D) IOV::widen(IOV::load(scale + d), w);
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                xh[k][e] = d < a.D ? (x[e] - m) * iv : 0.0f;
-                ds[k][e] = fmaf(g[e], xh[k][e], ds[k][e]);
-                db[k][e] += g[e];
-                gw[k][e] = g[e] * w[e];
-                s0 += gw[k][e];
-                s1 = fmaf(gw[k][e], xh[k][e], s1);
-            }
+        for (int p = 0; p < P; ++p) {
+            xh[p] = mul_f32x2(add_f32x2(xh[p], minus_m), iv2);
+            ds[p] = fma_f32x2(gw[p], xh[p], ds[p]);
+            db[p] = add_f32x2(db[p], gw[p]);
+            gw[p] = mul_f32x2(gw[p], w[p]);
+            t0 = add_f32x2(t0, gw[p]);
+            t1 = fma_f32x2(gw[p], xh[p], t1);
         }
-        const float row_iv = iv;
+        float s0 = t0.x + t0.y, s1 = t1.x + t1.y;
+        if (isinf(m * iv)) {   // behind the row's end, 0 * ((0 - m) * iv) is no zero then
+            s1 = 0.0f;
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if ((i / V * L + part) * V < a.D)
+                    s1 = fmaf(element(gw, i), element(xh, i), s1);
+        }
         load(row + step);
         row_sum2<L>(s0, s1, slot);
         slot ^= 1;
-        s0 /= (float)a.D;
-        s1 /= (float)a.D;
         if (row >= a.rows) continue;
+        s0 *= -per_d;
+        s1 *= -per_d;
+        float out[2 * P];
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            const float2 g0 = add_f32x2(gw[p], make_float2(s0, s0));
+            const float2 v = mul_f32x2(fma_f32x2(xh[p], make_float2(s1, s1), g0), iv2);
+            out[2 * p] = v.x;
+            out[2 * p + 1] = v.y;
+        }
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int d = (k * L + part) * V;
-            if (d >= a.D) continue;
-            float out[V];
+            float e[V];
 #pragma unroll
-            for (int e = 0; e < V; ++e) out[e] = row_iv * (gw[k][e] - s0 - xh[k][e] * s1);
-            IOV::store(dX + row * a.D + d, out);
+            for (int i = 0; i < V; ++i) e[i] = out[k * V + i];
+            if (d < a.D) IOV::store(dX + row * a.D + d, e);
         }
     }
     if (!partials) return;
@@ -232,8 +286,8 @@ __global__ void __launch_bounds__(kNormThreads)
             __syncthreads();
 #pragma unroll
             for (int e = 0; e < V; ++e) {
-                s_ds[threadIdx.x * V + e] = ds[k][e];
-                s_db[threadIdx.x * V + e] = db[k][e];
+                s_ds[threadIdx.x * V + e] = element(ds, k * V + e);
+                s_db[threadIdx.x * V + e] = element(db, k * V + e);
             }
             __syncthreads();
             for (int c = threadIdx.x; c < L * V; c += kNormThreads) {
@@ -254,8 +308,8 @@ __global__ void __launch_bounds__(kNormThreads)
             for (int e = 0; e < V; ++e) {
                 const int d = (k * L + part) * V + e;
                 if (d < a.D) {
-                    out[d] = ds[k][e];
-                    out[a.D + d] = db[k][e];
+                    out[d] = element(ds, k * V + e);
+                    out[a.D + d] = element(db, k * V + e);
                 }
             }
         }
@@ -310,7 +364,7 @@ __global__ void __launch_bounds__(1024)
     if (!out) return;
     float sum = 0.0f;
     wait_for_previous_kernel(partials);
-#pragma unroll 4
+#pragma unroll 8
     for (int b = slice; b < blocks; b += 32)
         if (d < D) sum += __ldg(partials + ((int64_t)b * 2 + blockIdx.y) * D + d);
     s[slice][lane] = sum;
@@ -338,14 +392,16 @@ template <int V, typename F> cudaError_t norm_shape(int runs, F &&f) {
     if (runs <= 1024) return f(integral_constant<int, 256>(), integral_constant<int, 4>());
     if constexpr (V <= 4)
         if (runs <= 2048) return f(integral_constant<int, 256>(), integral_constant<int, 8>());
-    if constexpr (V == 1) return f(integral_constant<int, 256>(), integral_constant<int, 32>());
+    if constexpr (V == 1)
+        return runs <= 4096 ? f(integral_constant<int, 256>(), integral_constant<int, 16>())
+                            : f(integral_constant<int, 256>(), integral_constant<int, 32>());
     return cudaErrorInvalidValue;   // not reached: D <= kNormOnChip
 }
 
 // Calls f(L, NV) for the backward pass: as many threads per row as keep a
 // thread's share, and with it the sums it holds, to one run (a block of 256 at
-// most), so that many warps share an SM: 16384 x 1024 bf16 takes 32.7 us, 37.5
-// with a warp per row and four runs per thread.
+// most: of 1024, with fewer blocks per SM to wait for each other's barriers, 8192
+// x 4096 fp32 takes 78.8 us instead of 68.2), so that many warps share an SM.
 template <int V, typename F> cudaError_t norm_backward_shape(int runs, F &&f) {
     using std::integral_constant;
     if (runs <= 8) return f(integral_constant<int, 8>(), integral_constant<int, 1>());
@@ -358,23 +414,25 @@ template <int V, typename F> cudaError_t norm_backward_shape(int runs, F &&f) {
     if (runs <= 1024) return f(integral_constant<int, 256>(), integral_constant<int, 4>());
     if constexpr (V <= 4)
         if (runs <= 2048) return f(integral_constant<int, 256>(), integral_constant<int, 8>());
-    if constexpr (V == 1) return f(integral_constant<int, 256>(), integral_constant<int, 32>());
+    if constexpr (V == 1)
+        return runs <= 4096 ? f(integral_constant<int, 256>(), integral_constant<int, 16>())
+                            : f(integral_constant<int, 256>(), integral_constant<int, 32>());
     return cudaErrorInvalidValue;   // not reached: D <= kNormOnChip
 }
 
 // Row blocks of the backward pass: what an SM holds of them at once, and no
 // more, since each leaves 2 D sums behind.
-int row_blocks(int64_t rows, int L, int NV) {
+int row_blocks(int64_t rows, int L, int per_sm) {
     const int64_t b = (rows + kNormThreads / L - 1) / (kNormThreads / L);
-    const int most = kNormSms * (NV == 1 ? 4 : 2);
+    const int most = kNormSms * per_sm;
     return (int)(b < most ? b : most);
 }
-constexpr int kWideNV = 32;   // rows wider than kNormOnChip: as the fullest
+constexpr int kWideBlocks = 2;   // of rows, per SM, for rows wider than kNormOnChip
 template <int V> int row_blocks_of(int64_t rows, int64_t D) {
-    int blocks = row_blocks(rows, kNormThreads, kWideNV);
+    int blocks = row_blocks(rows, kNormThreads, kWideBlocks);
     if (D <= kNormOnChip)
         norm_backward_shape<V>((int)((D + V - 1) / V), [&](auto l, auto nv) {
-            blocks = row_blocks(rows, decltype(l)::value, decltype(nv)::value);
+            blocks = row_blocks(rows, decltype(l)::value, norm_backward_blocks(V * decltype(nv)::value));
             return cudaSuccess;
         });
     return blocks;
@@ -400,7 +458,7 @@ cudaError_t run_backward(const T *dY, const T *X, const T *scale, const float *m
                          cudaStream_t s) {
     return norm_backward_shape<V>((a.D + V - 1) / V, [&](auto l, auto nv) {
         constexpr int L = decltype(l)::value, NV = decltype(nv)::value;
-        *blocks = row_blocks(a.rows, L, NV);
+        *blocks = row_blocks(a.rows, L, norm_backward_blocks(NV * V));
         layer_norm_backward_kernel<T, V, L, NV>
             <<<*blocks, kNormThreads, 0, s>>>(dY, X, scale, mean, inv, dX, partials, a);
         return cudaGetLastError();
@@ -441,7 +499,7 @@ cudaError_t launch_layer_norm_backward(const void *dY, const void *X, const void
     if (a.rows > 0 && a.D > kNormOnChip) {
         layer_norm_wide_dx_kernel<T>
             <<<(unsigned)a.rows, kNormThreads, 0, s>>>(dy, x, g, mean, inv, (T *)dX, a);
-        blocks = row_blocks(a.rows, kNormThreads, kWideNV);
+        blocks = row_blocks(a.rows, kNormThreads, kWideBlocks);
         if (sums)
             layer_norm_wide_partial_kernel<T>
                 <<<dim3((a.D + 255) / 256, blocks), 256, 0, s>>>(dy, x, mean, inv, sums, a);

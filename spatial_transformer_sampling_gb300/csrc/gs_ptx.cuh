@@ -142,6 +142,7 @@ __device__ __forceinline__ void cp_async_wait_pending(int pending) {
 // compiler allocates the register pairs itself): lane-wise a*b and a*b+c, each
 // rounded to nearest exactly as fmulf / fmaf would round it.
 __device__ __forceinline__ float2 mul_f32x2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 add_f32x2(float2 a, float2 b) { return __fadd2_rn(a, b); }
 
 __device__ __forceinline__ float2 fma_f32x2(float2 a, float2 b, float2 c) {
     return __ffma2_rn(a, b, c);

@@ -138,6 +138,27 @@ def test_layer_norm_constant_rows_infinities_and_nan(gs_cuda):
     assert torch.isnan(Y[1]).all() and torch.isnan(Y[2]).all()  # other rows are untouched
 
 
+@pytest.mark.parametrize("dtype,D", [("float32", 37), ("float32", 132), ("bfloat16", 264),
+                                     ("bfloat16", 2100)])
+def test_layer_norm_gradient_of_constant_rows_whose_level_overflows(gs_cuda, dtype, D):
+    # mean * inv is beyond fp32, x - mean is zero: only lanes behind a row's end see it
+    level, inv = 2.0 ** 112, 2.0 ** 20
+    g = wl.rng(31)
+    dY = wl.as_dtype(g.normal(size=(3, D)), dtype)
+    scale = wl.as_dtype(g.normal(size=D), dtype)
+    X = torch.full((3, D), level, dtype=dY.dtype)
+    stat = lambda v: torch.full((3, 1), v).cuda()
+    dX, dScale, dB = gs_cuda.gs_layer_norm_backward(dY.cuda(), X.cuda(), scale.cuda(), stat(level),
+                                                    stat(inv))
+    gw = dY.double() * scale.double()
+    want = inv * (gw - gw.mean(1, keepdim=True))
+    # a rounding of the output and fp32 roundings of a sum of D terms
+    unit = 2.0 ** -23 if dtype == "float32" else 2.0 ** -8
+    bound = unit * want.abs() + 2.0 ** -23 * inv * (gw.abs() + gw.abs().sum(1, keepdim=True))
+    assert ((dX.cpu().double() - want).abs() <= bound).all()
+    assert (dScale == 0).all() and torch.isfinite(dB.float()).all()
+
+
 def test_layer_norm_large_level_keeps_its_variance(gs_cuda):
     # mean 4096 with deviations of 1: a one-pass sum of squares would lose the variance
     g = wl.rng(3)
