@@ -10,12 +10,13 @@
 // loads took two thirds of its time and bound the kernels.  A tile's operands are
 // fetched into registers in one batch, since with two or three blocks per SM
 // the latency of loads in several batches showed.  Both together (4 images,
-// 8 heads, 48 x 48 tokens, D 64, fp32): forward 1504 -> 1319 us (33 TFLOP/s of about 75 that the FMA units
-// have), backward 4872 -> 4104 us (26 TFLOP/s).  Rows (queries; keys in the
-// dK / dV blocks) stay resident,
-// columns are walked tile by tile; weights and their gradients go back through
-// shared memory, over the columns' transposed copy, as the first operand of the
-// next product.  One block sums each gradient in one order.
+// 8 heads, 48 x 48 tokens, D 64, fp32): forward 1504 -> 1319 us, backward 4872 ->
+// 4081 us; with the operands of a step read from shared memory one step ahead
+// 1244 us (35 TFLOP/s of about 75 that the FMA units have) and 3906 us (28).  Rows
+// (queries; keys in the dK / dV blocks) stay resident, columns are walked tile by
+// tile; weights and their gradients go back through shared memory, over the
+// columns' transposed copy, as the first operand of the next product.  One block
+// sums each gradient in one order.
 #pragma once
 
 #include "gs_attn_common.cuh"
@@ -103,17 +104,23 @@ struct SimtPlace {
 };
 
 // c[8 rows][4] += sum_k a[k][8 rows] b[k][4 columns].  Pairs of rows share a
-// packed FMA: the operand to be doubled is then the one of four values.
+// packed FMA: the operand to be doubled is then the one of four values.  The next
+// step's operands are read ahead, after the last one those of the row behind
+// (kSimtBehind).
 __device__ __forceinline__ void simt_product(float2 (&c)[4][4], const float *a, int pitch_a,
                                              const float *b, int pitch_b, int K) {
-#pragma unroll 4
+    float4 x = *reinterpret_cast<const float4 *>(a), z = *reinterpret_cast<const float4 *>(a + 4),
+           y = *reinterpret_cast<const float4 *>(b);
+#pragma unroll 8
     for (int k = 0; k < K; ++k) {
-        const float4 x = *reinterpret_cast<const float4 *>(a + k * pitch_a);
-        const float4 z = *reinterpret_cast<const float4 *>(a + k * pitch_a + 4);
-        const float4 y = *reinterpret_cast<const float4 *>(b + k * pitch_b);
         const float2 r[4] = {make_float2(x.x, x.y), make_float2(x.z, x.w), make_float2(z.x, z.y),
                              make_float2(z.z, z.w)};
         const float w[4] = {y.x, y.y, y.z, y.w};
+        a += pitch_a;
+        b += pitch_b;
+        x = *reinterpret_cast<const float4 *>(a);
+        z = *reinterpret_cast<const float4 *>(a + 4);
+        y = *reinterpret_cast<const float4 *>(b);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -148,17 +155,22 @@ __device__ __forceinline__ float row_lanes_sum(float v) {
     return v;
 }
 
+// Floats behind the last operand that are read but not used.
+constexpr int kSimtBehind = 192;
+static_assert(kSimtBehind >= kSimtPitch && kSimtBehind >= 128 + 8, "one row of either layout");
+
 __host__ __device__ inline int simt_pitch_n(int D) { return (D + 3) / 4 * 4 + 4; }
 // A transposed operand; one that weights are written over holds 64 rows at least.
 __host__ __device__ inline int simt_floats_t(int D, bool reused) {
     return (reused && D < kSimtTile ? kSimtTile : D) * kSimtPitch;
 }
 inline int simt_fwd_smem(int D) {
-    return (simt_floats_t(D, false) + simt_floats_t(D, true) + kSimtTile * simt_pitch_n(D)) * 4;
+    return (simt_floats_t(D, false) + simt_floats_t(D, true) + kSimtTile * simt_pitch_n(D) +
+            kSimtBehind) * 4;
 }
 inline int simt_bwd_smem(int D, bool dkv, int rel) {
     return (2 * simt_floats_t(D, false) + 2 * simt_floats_t(D, true) +
-            (dkv ? 2 : 1) * kSimtTile * simt_pitch_n(D)) * 4 + rel_smem(rel, 2);
+            (dkv ? 2 : 1) * kSimtTile * simt_pitch_n(D) + kSimtBehind) * 4 + rel_smem(rel, 2);
 }
 
 // NC: 64-column chunks of the head width.  Three blocks per SM without fetching
