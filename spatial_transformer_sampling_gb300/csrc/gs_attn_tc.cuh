@@ -294,10 +294,12 @@ __device__ __forceinline__ int bias_start(const TcBias &b, int r) {
 // last token.
 struct TileWalk {
     int W, P, x, rel, dy, dx, dy_half, dx_half;
-    __device__ __forceinline__ void init(int rows, int width, int P_) {
+    // Starts at the tile of token `token`.
+    __device__ __forceinline__ void init(int rows, int width, int P_, int token = 0) {
         W = rows == 1 ? INT_MAX : width;
         P = rows == 1 ? 0 : P_;
-        x = rel = 0;
+        x = token % W;
+        rel = token / W * P + x;
         dy = kTcN / W;
         dx = kTcN - dy * W;
         dy_half = kTcHalf / W;

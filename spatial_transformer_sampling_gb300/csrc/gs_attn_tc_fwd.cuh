@@ -22,6 +22,8 @@
 // The bias of a tile comes to shared memory with the keys (TcBias).
 #pragma once
 
+#include <cooperative_groups.h>
+
 #include "gs_attn_tc.cuh"
 
 namespace gs {
@@ -42,7 +44,12 @@ constexpr float kLazyGrowth = 8.0f;   // log2 of how far the maximum may outgrow
 template <typename T> constexpr float kWeightShift = 0.0f;
 template <> constexpr float kWeightShift<__half> = 6.0f;
 
-template <int DP, bool MANY> struct TcFwdShape {
+// How blocks and items of 128 queries go together: a block each, a block for
+// several items (short heads), a cluster for one (few items of long heads).
+enum { kFwdOne = 0, kFwdMany = 1, kFwdSplit = 2 };
+
+template <int DP, int MODE> struct TcFwdShape {
+    static constexpr bool MANY = MODE == kFwdMany;
     static constexpr int kStages = DP == 64 ? 3 : 2;
     // queries and outputs of two items at a time, where both fit
     static constexpr int kItems = MANY && DP == 64 ? 2 : 1;
@@ -52,20 +59,33 @@ template <int DP, bool MANY> struct TcFwdShape {
     static constexpr int kSmem = kTileSmem + 1024;   // 1024-byte alignment of the tiles
     static constexpr int kTmemCols = 256;            // two score buffers, O; two CTAs per SM
     static constexpr int kTmemO = 2 * kTcN;
+    // a block's share of the output, over the tiles, for the other blocks of the cluster
+    static constexpr int kSharePitch = DP + 4;
+    static_assert(MODE != kFwdSplit || kTcM * kSharePitch * 4 <= kTileSmem, "fits the tiles");
 };
 
-// An item of work: 128 queries of one head.  A CTA takes one, or with MANY every
-// gridDim.x-th one; its key tiles are numbered through (`tile`), which gives a tile its score
+// An item of work: 128 queries of one head.  A CTA takes one, or with kFwdMany every
+// gridDim.x-th one, or with kFwdSplit its part of one's keys; its key tiles are numbered through (`tile`), which gives a tile its score
 // buffer, its stage of NS and the parity of their barriers' phases, and so are
 // the items that have keys (`count`).
-template <int NS, bool MANY> struct TcItem {
-    int index, n, h, i0, keys, tiles, j, tile, stage, parity, count;
+template <int NS, int MODE> struct TcItem {
+    static constexpr bool MANY = MODE == kFwdMany;
+    // key0: the first key that is taken, `keys` how many from there on
+    int index, n, h, i0, key0, keys, tiles, j, tile, stage, parity, count;
     __device__ __forceinline__ void decode(const AttnArgs &a, int q_tiles) {
         i0 = index % q_tiles * kTcM;
         h = index / q_tiles % a.H;
         n = index / q_tiles / a.H;
         keys = keys_of(a, n);
         tiles = (keys + kTcN - 1) / kTcN;
+        key0 = 0;
+        if (MODE == kFwdSplit) {   // whole tiles each, the last ones fewer or none
+            const int share = (tiles + cluster_size() - 1) / cluster_size();
+            const int first = min(cluster_rank() * share, tiles);
+            tiles = min(share, tiles - first);
+            key0 = first * kTcN;
+            keys = min(keys - key0, tiles * kTcN);
+        }
     }
     // The first item with keys from `index` on; false when there is none.
     __device__ __forceinline__ bool seek(const AttnArgs &a, int q_tiles, int items) {
@@ -103,10 +123,11 @@ template <int NS, bool MANY> struct TcItem {
     __device__ __forceinline__ bool tail() const { return last() && keys % kTcN != 0; }
 };
 
-template <typename T, int DP, int BIAS, bool MANY>
+template <typename T, int DP, int BIAS, int MODE>
 __global__ void __launch_bounds__(kTcThreads, 2)
     attn_tc_fwd_kernel(const __grid_constant__ TcFwdArgs p) {
-    using Sh = TcFwdShape<DP, MANY>;
+    using Sh = TcFwdShape<DP, MODE>;
+    constexpr bool MANY = MODE == kFwdMany, SPLIT = MODE == kFwdSplit;
     constexpr int NS = Sh::kStages, NI = Sh::kItems;
     constexpr bool kBf16 = __is_same(T, __nv_bfloat16);
     extern __shared__ unsigned char smem_raw[];
@@ -115,6 +136,8 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     __shared__ uint32_t tmem_base;
     __shared__ __align__(16) int s_rel[8][kTcHalf];
     __shared__ float s_top[2][2][kTcM];   // of the two threads of a query, in turn
+    // at the end, with SPLIT: reference and the two halves of the sum
+    float *s_m = s_top[0][0], *s_l = s_top[1][0];
 
     const AttnArgs &a = p.a;
     unsigned char *tiles = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -153,8 +176,8 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     const float *bias0 = p.bias.base;
     wait_for_previous_kernel(bias0);
     bool ok = true;
-    TcItem<NS, MANY> w = {};
-    w.index = blockIdx.x;
+    TcItem<NS, MODE> w = {};
+    w.index = SPLIT ? blockIdx.x / cluster_size() : blockIdx.x;
 
     if (warp == kTcCopyWarp) {
         // ---------------------------------------------------- copies
@@ -178,15 +201,16 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                 if (ok && w.tile >= NS) ok = tc_wait(&pv_done[s], w.parity ^ 1, a.err);   // consumed
                 if (ok) {
                     mbar_arrive_expect_tx(&k_full[s], Sh::kTileBytes + (BIAS == kBiasWindow ? p.bias.count * 4 : 0));
-                    tc_load<DP, kTcN>(sK + s * Sh::kTileBytes, p.k, w.n, w.h, w.j * kTcN, &k_full[s]);
+                    tc_load<DP, kTcN>(sK + s * Sh::kTileBytes, p.k, w.n, w.h, w.key0 + w.j * kTcN,
+                                      &k_full[s]);
                     if (BIAS == kBiasWindow)
                         bulk_copy_g2s(sBias + s * p.bias.count,
-                                      bias + bias_start(p.bias, rq0 - rel_k(a, w.j * kTcN)),
+                                      bias + bias_start(p.bias, rq0 - rel_k(a, w.key0 + w.j * kTcN)),
                                       p.bias.count * 4, &k_full[s]);
                     // a tile with masked keys is cleared before it counts as loaded
                     uint64_t *bar = w.tail() ? &landed : &v_full[s];
                     mbar_arrive_expect_tx(bar, Sh::kTileBytes);
-                    tc_load<DP, kTcN>(sV + s * Sh::kTileBytes, p.v, w.n, w.h, w.j * kTcN, bar);
+                    tc_load<DP, kTcN>(sV + s * Sh::kTileBytes, p.v, w.n, w.h, w.key0 + w.j * kTcN, bar);
                 }
             }
             ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -212,7 +236,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
             const uint32_t idesc_o = umma_idesc_f16_bmn(kBf16, kTcM, steps * 16);
             const uint32_t q_lo = umma_lo_kmajor(smem_u32(sQ)), k_lo = umma_lo_kmajor(smem_u32(sK));
             const uint32_t v_lo = umma_lo_mnmajor(smem_u32(sV), kTcN * 128);
-            TcItem<NS, MANY> c = w;   // one tile ahead: its scores are issued before w's product
+            TcItem<NS, MODE> c = w;   // one tile ahead: its scores are issued before w's product
             bool c_more = c.seek(a, q_tiles, items), w_more = w.seek(a, q_tiles, items);
             const auto scores = [&] {
                 const int s = c.stage, b = c.count % NI;
@@ -324,6 +348,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
             w.decode(a, q_tiles);
             const int i = w.i0 + lane_row;
             if (w.tiles == 0) {   // no key: nothing comes from the other warps
+                if (SPLIT) break;
                 if (__all_sync(0xffffffffu, ok)) store(w.n, w.h, i, 0, false, 0.0f, 0.0f);
                 if (!MANY) break;
                 continue;
@@ -332,7 +357,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
             const int rq0 = BIAS ? rel_q(a, w.i0) : 0, rq = BIAS ? rel_q(a, min(i, a.Lq - 1)) : 0;
             const uint32_t to = tmem + Sh::kTmemO + w.count % NI * DP + my_tmem;
             TileWalk walk;
-            if (BIAS) walk.init(a.Hk, a.Wk, a.P);
+            if (BIAS) walk.init(a.Hk, a.Wk, a.P, w.key0);
             // the bias of this query and the next tile's first key, and where the
             // thread's columns start in the keys' grid
             const float *row = nullptr;
@@ -439,17 +464,76 @@ __global__ void __launch_bounds__(kTcThreads, 2)
             past.l = l;
             if (!MANY) break;
         }
-        if (w.count > 0) finish();
+        if (SPLIT) {
+            if (w.count > 0)   // after that nothing reads the tiles any more
+                wait(&pv_done[past.stage], past.parity);
+            const bool any = __all_sync(0xffffffffu, ok) && w.count > 0;
+            pair_sync(pair);   // the other warp has read s_top
+            if (part == 0) s_m[lane_row] = any ? past.m : -INFINITY;
+            s_l[part * kTcM + lane_row] = any ? past.l : 0.0f;
+            if (any) {
+                tcgen05_fence_after_sync();
+                float *mine = reinterpret_cast<float *>(tiles) + lane_row * Sh::kSharePitch;
+#pragma unroll 1
+                for (int d = part * 32; d < a.D; d += 64) {
+                    uint32_t o[32];
+                    tmem_ld_x32(tmem + Sh::kTmemO + my_tmem + d, o);
+#pragma unroll
+                    for (int k = 0; k < 32; k += 4)
+                        *reinterpret_cast<uint4 *>(mine + d + k) =
+                            make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+                }
+            }
+        } else if (w.count > 0) {
+            finish();
+        }
     }
     tcgen05_fence_before_sync();
     __syncthreads();
     if (warp == kTcMmaWarp) tmem_dealloc(tmem, Sh::kTmemCols);
+    if constexpr (SPLIT) {
+        // join: each block takes its part of the rows, the blocks' shares in order
+        const auto cluster = cooperative_groups::this_cluster();
+        cluster.sync();
+        const int ranks = cluster_size(), rows = kTcM / ranks, runs = a.D / 8;
+        w.decode(a, q_tiles);
+        for (int k = threadIdx.x; k < rows * runs; k += kTcThreads) {
+            const int row = cluster_rank() * rows + k / runs, d = k % runs * 8, i = w.i0 + row;
+            if (i >= a.Lq) break;   // and so are the rows of later k
+            float m = -INFINITY, l = 0.0f, o[8] = {};
+            for (int r = 0; r < ranks; ++r) m = fmaxf(m, *cluster.map_shared_rank(&s_m[row], r));
+            for (int r = 0; r < ranks; ++r) {
+                const float its = *cluster.map_shared_rank(&s_m[row], r);
+                const float lr = *cluster.map_shared_rank(&s_l[row], r) +
+                                 *cluster.map_shared_rank(&s_l[kTcM + row], r);
+                if (its == -INFINITY && lr == 0.0f) continue;   // no key: its output may be anything
+                const float f = exp2_approx(its - m);
+                const float4 *from = reinterpret_cast<const float4 *>(cluster.map_shared_rank(
+                    reinterpret_cast<float *>(tiles) + row * Sh::kSharePitch + d, r));
+                const float4 u = from[0], v = from[1];
+                const float x[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[e] = fmaf(x[e], f, o[e]);
+                l = fmaf(lr, f, l);
+            }
+            const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+            uint4 v;
+            uint32_t *u = &v.x;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) u[e] = pack2<T>(o[2 * e] * inv, o[2 * e + 1] * inv);
+            *reinterpret_cast<uint4 *>((T *)p.O + (((int64_t)w.n * a.Lq + i) * a.H + w.h) * a.D + d) = v;
+            if (d == 0 && p.lse)
+                p.lse[((int64_t)w.n * a.H + w.h) * a.Lq + i] =
+                    l != 0.0f ? (m - kWeightShift<T> + log2f(l)) * kLn2 : -INFINITY;
+        }
+        cluster.sync();   // shared memory stays until the others have read it
+    }
 }
 
-template <typename T, int DP, int BIAS, bool MANY>
-cudaError_t launch_attn_tc_fwd_as(const TcFwdArgs &p, cudaStream_t s) {
-    using Sh = TcFwdShape<DP, MANY>;
-    auto kernel = attn_tc_fwd_kernel<T, DP, BIAS, MANY>;
+template <typename T, int DP, int BIAS, int MODE>
+cudaError_t launch_attn_tc_fwd_as(const TcFwdArgs &p, int64_t blocks, int cluster, cudaStream_t s) {
+    using Sh = TcFwdShape<DP, MODE>;
+    auto kernel = attn_tc_fwd_kernel<T, DP, BIAS, MODE>;
     static DeviceFlags ready;
     const cudaError_t e = once_per_device(ready, [&] {
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -457,23 +541,28 @@ cudaError_t launch_attn_tc_fwd_as(const TcFwdArgs &p, cudaStream_t s) {
     });
     if (e != cudaSuccess) return e;
     const int window = BIAS == kBiasWindow ? Sh::kStages * p.bias.count * 4 : 0;
-    const int64_t items = (int64_t)((p.a.Lq + kTcM - 1) / kTcM) * p.a.H * p.a.N;
-    const int64_t blocks = MANY ? std::min<int64_t>(items, 2 * kTcSms) : items;
-    return launch_next(BIAS != kBiasNone, kernel, (unsigned)blocks, kTcThreads, Sh::kSmem + window, s,
-                       p);
+    return launch_next(LaunchAs(BIAS != kBiasNone, cluster), kernel, (unsigned)blocks, kTcThreads,
+                       Sh::kSmem + window, s, p);
 }
 
-// MANY: blocks that go through items pay off where an item is so short that
-// setting up a block for it weighs (8 x 8 windows, 4096 items of one key tile:
-// 44.7 us, 59.6 with a block each); keeping count of the items costs a fifth of
-// a long one (64 x 64 tokens, 2048 items of 64 tiles: 557 us and 466).
-constexpr int kTcManyTiles = 4;
+// kFwdMany pays off where an item is so short that setting up a block for it
+// weighs (8 x 8 windows, 4096 items of one key tile: 44.7 us, 59.6 with a block
+// each); keeping count of the items costs a fifth of a long one (64 x 64 tokens,
+// 2048 items of 64 tiles: 557 us and 466).
+// kFwdSplit where items leave SMs free: as many blocks for one as the SMs hold at
+// two each, of two key tiles at least (16 queries, 8 heads, 32768 keys, D 64: 45
+// us, 277 with a block each; 3000 tokens, 2 heads, D 128: 30 and 49).
+constexpr int kTcManyTiles = 4, kTcMaxSplit = 8;
 template <typename T, int DP, int BIAS>
 cudaError_t launch_attn_tc_fwd_by_length(const TcFwdArgs &p, cudaStream_t s) {
     const int64_t items = (int64_t)((p.a.Lq + kTcM - 1) / kTcM) * p.a.H * p.a.N;
-    return items > 2 * kTcSms && p.a.Lk <= kTcManyTiles * kTcN
-               ? launch_attn_tc_fwd_as<T, DP, BIAS, true>(p, s)
-               : launch_attn_tc_fwd_as<T, DP, BIAS, false>(p, s);
+    const int tiles = (p.a.Lk + kTcN - 1) / kTcN;
+    int split = 1;
+    while (split < kTcMaxSplit && items * split * 2 <= 2 * kTcSms && tiles >= split * 4) split *= 2;
+    if (split > 1) return launch_attn_tc_fwd_as<T, DP, BIAS, kFwdSplit>(p, items * split, split, s);
+    return items > 2 * kTcSms && tiles <= kTcManyTiles
+               ? launch_attn_tc_fwd_as<T, DP, BIAS, kFwdMany>(p, 2 * kTcSms, 1, s)
+               : launch_attn_tc_fwd_as<T, DP, BIAS, kFwdOne>(p, items, 1, s);
 }
 
 // Runs the tensor-core forward pass when it takes the pointers and strides;

@@ -43,19 +43,31 @@ cudaError_t once_per_device(DeviceFlags &flags, F &&setup) {
 // 160.)  Every kernel in between waits too, so that the end of one means the end
 // of all before it; a call's first kernel is launched without, so that nothing of
 // the call runs before the stream's earlier work has ended.
+struct LaunchAs {
+    bool follows;
+    int cluster;   // blocks of a cluster, along x
+    LaunchAs(bool follows_, int cluster_ = 1) : follows(follows_), cluster(cluster_) {}
+};
 template <typename... P, typename... A>
-cudaError_t launch_next(bool follows, void (*kernel)(P...), dim3 grid, int threads, int smem,
+cudaError_t launch_next(LaunchAs as, void (*kernel)(P...), dim3 grid, int threads, int smem,
                         cudaStream_t s, A... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = follows ? 1 : 0;
+    cudaLaunchAttribute attrs[2];
+    cfg.attrs = attrs;
+    if (as.follows) {
+        attrs[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attrs[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    if (as.cluster > 1) {
+        attrs[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+        attrs[cfg.numAttrs].val.clusterDim.x = (unsigned)as.cluster;
+        attrs[cfg.numAttrs].val.clusterDim.y = attrs[cfg.numAttrs].val.clusterDim.z = 1;
+        ++cfg.numAttrs;
+    }
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
 }
 

@@ -35,6 +35,18 @@ template <typename... P> __device__ __forceinline__ void wait_for_previous_kerne
     (..., [](auto *&p) { asm volatile("" : "+l"(p)::"memory"); }(pointers));
 }
 
+// Blocks of this block's cluster, and its place among them.
+__device__ __forceinline__ int cluster_size() {
+    int n;
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(n));
+    return n;
+}
+__device__ __forceinline__ int cluster_rank() {
+    int r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
 __device__ __forceinline__ void mbar_init(uint64_t *bar, uint32_t count) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count)
                  : "memory");

@@ -432,3 +432,19 @@ def test_few_queries_at_every_width_of_a_key(gs_cuda, D, Lq, dtype):
     # from one lane per key to a whole warp, keys shared by up to sixteen blocks
     Problem(gs_cuda, 440, dtype, 1, 3, D, (1, Lq), (3, 811), 16, k_len=[2200]).forward()
     Problem(gs_cuda, 441, dtype, 2, 2, D, (1, Lq), (1, 131)).forward()
+
+
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+@pytest.mark.parametrize("D", [40, 64, 128])
+@pytest.mark.parametrize("q,k", [((1, 9), (1, 2050)), ((1, 130), (1, 1023)), ((3, 20), (4, 211))])
+def test_long_keys_shared_by_the_blocks_of_a_cluster(gs_cuda, q, k, D, dtype):
+    # lengths that leave some blocks a part of a tile, one key or nothing
+    Lk = k[0] * k[1]
+    p = Problem(gs_cuda, 450, dtype, 6, 2, D, q, k, 16, k_len=[Lk, 0, 1, 65, 513, Lk - 63])
+    O, LSE = p.forward()
+    O2, LSE2 = gs_cuda.gs_attention(*p.qkv(), **p.args())
+    assert torch.equal(O, O2) and torch.equal(LSE, LSE2)
+    Problem(gs_cuda, 451, dtype, 1, 1, D, q, k, bias=False, layout="packed").forward()
+    # masked by the map: whole tiles, and with them whole blocks, that hold no key
+    Problem(gs_cuda, 452, dtype, 1, 2, D, (1, 140), (1, Lk), 16, causal=True).forward()
+    assert gs_cuda.gs_device_status() == 0
