@@ -19,6 +19,8 @@
 // sums each gradient in one order.
 #pragma once
 
+#include <cooperative_groups.h>
+
 #include "gs_attn_common.cuh"
 #include "gs_attn_rel.cuh"
 #include "gs_ptx.cuh"
@@ -28,6 +30,7 @@ namespace gs {
 
 constexpr int kSimtTile = 64;
 constexpr int kSimtThreads = 128;
+constexpr int kSimtMaxSplit = 8;   // blocks that share the keys of 64 queries (forward)
 constexpr int kSimtPitch = kSimtTile + 4;   // keeps 16-byte alignment, spreads banks
 
 // Element offsets of one operand: base + n, h, token strides.
@@ -175,7 +178,7 @@ inline int simt_bwd_smem(int D, bool dkv, int rel) {
 
 // NC: 64-column chunks of the head width.  Three blocks per SM without fetching
 // ahead beat two that do, 1319 to 1413 us at the size above.
-template <typename T, int NC, int E>
+template <typename T, int NC, int E, bool SPLIT>
 __global__ void __launch_bounds__(kSimtThreads, NC == 1 ? 3 : 2)
     attn_simt_fwd_kernel(AttnArgs a, AttnPtrs p, const float *bias) {
     extern __shared__ float4 simt_smem[];
@@ -183,8 +186,9 @@ __global__ void __launch_bounds__(kSimtThreads, NC == 1 ? 3 : 2)
     float *qt = reinterpret_cast<float *>(simt_smem), *kt = qt + simt_floats_t(D, false);
     float *vn = kt + simt_floats_t(D, true);
     const int tiles = (a.Lq + kSimtTile - 1) / kSimtTile;
-    const int i0 = (int)(blockIdx.x % tiles) * kSimtTile;
-    const int h = (int)(blockIdx.x / tiles % a.H), n = (int)(blockIdx.x / tiles / a.H);
+    // SPLIT: a cluster shares the keys of 64 queries, whole tiles each
+    const int splits = SPLIT ? cluster_size() : 1, block = blockIdx.x / splits;
+    const int i0 = block % tiles * kSimtTile, h = block / tiles % a.H, n = block / tiles / a.H;
     const SimtPlace me;
     // of the columns' two halves, for a row's maximum and its sum
     __shared__ float s_half[2][kSimtTile];
@@ -192,7 +196,10 @@ __global__ void __launch_bounds__(kSimtThreads, NC == 1 ? 3 : 2)
     const bool speaks = threadIdx.x % 8 == 0;   // for the eight lanes of its rows
     const float c2 = a.scale * kLog2e;
     const SimtView<T> Q(p.Q, a.qs, n, h), K(p.K, a.ks, n, h), V(p.V, a.vs, n, h);
-    const int keys = keys_of(a, n);
+    const int all_keys = keys_of(a, n);
+    const int share = ((all_keys + kSimtTile - 1) / kSimtTile + splits - 1) / splits * kSimtTile;
+    const int first = SPLIT ? cluster_rank() * share : 0;
+    const int keys = SPLIT ? min(all_keys, first + share) : all_keys;
     wait_for_previous_kernel(bias);
     if (bias) bias += (int64_t)h * a.bias_stride;
 
@@ -208,7 +215,7 @@ __global__ void __launch_bounds__(kSimtThreads, NC == 1 ? 3 : 2)
         l[i] = 0.0f;
         rq[i] = bias ? rel_q(a, min(i0 + me.row + i, a.Lq - 1)) : 0;
     }
-    for (int j0 = 0; j0 < keys; j0 += kSimtTile) {
+    for (int j0 = first; j0 < keys; j0 += kSimtTile) {
         const int live = keys - j0;
         __syncthreads();
         next_k.fetch(K, j0, live, D);
@@ -271,6 +278,52 @@ __global__ void __launch_bounds__(kSimtThreads, NC == 1 ? 3 : 2)
         if (speaks) s_half[side][me.row + i] = l[i];
     }
     __syncthreads();
+    if constexpr (SPLIT) {
+        // the block's share: the output over V, the maximum and the sum over the halves
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            l[i] = s_half[0][me.row + i] + s_half[1][me.row + i];
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (c * 64 + me.col + j < D)
+                        vn[(me.row + i) * pitch_n + c * 64 + me.col + j] = at(o[c], i, j);
+        }
+        __syncthreads();
+        if (me.col == 0)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                s_half[0][me.row + i] = m[i];
+                s_half[1][me.row + i] = l[i];
+            }
+        // each block joins its part of the rows, the shares in order
+        const auto cluster = cooperative_groups::this_cluster();
+        cluster.sync();
+        const int rows = kSimtTile / splits;
+        for (int k = threadIdx.x; k < rows * D; k += kSimtThreads) {
+            const int row = cluster_rank() * rows + k / D, d = k % D;
+            if (i0 + row >= a.Lq) break;
+            float top = -INFINITY, sum = 0.0f, v = 0.0f;
+            for (int r = 0; r < splits; ++r)
+                top = fmaxf(top, *cluster.map_shared_rank(&s_half[0][row], r));
+            for (int r = 0; r < splits; ++r) {
+                const float its = *cluster.map_shared_rank(&s_half[0][row], r);
+                const float of = *cluster.map_shared_rank(&s_half[1][row], r);
+                if (its == -INFINITY && of == 0.0f) continue;   // no key (a row of NaN has some)
+                const float f = exp2_approx(its - top);
+                sum = fmaf(of, f, sum);
+                v = fmaf(*cluster.map_shared_rank(&vn[row * pitch_n + d], r), f, v);
+            }
+            const int64_t at_row = (int64_t)n * a.Lq + i0 + row;
+            ((T *)p.O)[(at_row * a.H + h) * D + d] = IO<T>::st(sum != 0.0f ? v / sum : 0.0f);
+            if (d == 0 && p.lse)
+                p.lse[((int64_t)n * a.H + h) * a.Lq + i0 + row] =
+                    sum != 0.0f ? (top + log2f(sum)) * kLn2 : -INFINITY;
+        }
+        cluster.sync();   // shared memory stays until the others have read it
+        return;
+    }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         // both halves add in the same order
@@ -435,18 +488,30 @@ template <typename T> bool simt_vec(const AttnArgs &a, const AttnPtrs &p) {
 template <typename T>
 cudaError_t launch_attn_simt_fwd(const AttnArgs &a, const AttnPtrs &p, const float *bias,
                                  cudaStream_t s) {
+    constexpr int E = kVec<T>;
     const bool wide = a.D > 64, vec = simt_vec<T>(a, p);
-    auto kernel = wide ? (vec ? attn_simt_fwd_kernel<T, 2, kVec<T>> : attn_simt_fwd_kernel<T, 2, 1>)
-                       : (vec ? attn_simt_fwd_kernel<T, 1, kVec<T>> : attn_simt_fwd_kernel<T, 1, 1>);
-    static DeviceFlags ready[2][2];
-    const cudaError_t e = once_per_device(ready[wide][vec], [&] {
+    // Few blocks of long heads: several for one, of two key tiles at least, up to a
+    // quarter more blocks than SMs (3000 tokens, one head, D 64, fp32: 107 us, 209
+    // with one each; 17 x 23 tokens, 4 x 4 heads, from 112 blocks to 224: 41 to 51).
+    const int64_t blocks = (int64_t)((a.Lq + kSimtTile - 1) / kSimtTile) * a.H * a.N;
+    const int tiles = (a.Lk + kSimtTile - 1) / kSimtTile;
+    int splits = 1;
+    while (splits < kSimtMaxSplit && blocks * splits * 2 <= 152 + 152 / 4 && tiles >= splits * 4)
+        splits *= 2;
+    const bool split = splits > 1;
+    auto kernel =
+        split ? (wide ? (vec ? attn_simt_fwd_kernel<T, 2, E, true> : attn_simt_fwd_kernel<T, 2, 1, true>)
+                      : (vec ? attn_simt_fwd_kernel<T, 1, E, true> : attn_simt_fwd_kernel<T, 1, 1, true>))
+              : (wide ? (vec ? attn_simt_fwd_kernel<T, 2, E, false> : attn_simt_fwd_kernel<T, 2, 1, false>)
+                      : (vec ? attn_simt_fwd_kernel<T, 1, E, false> : attn_simt_fwd_kernel<T, 1, 1, false>));
+    static DeviceFlags ready[2][2][2];
+    const cudaError_t e = once_per_device(ready[split][wide][vec], [&] {
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     simt_fwd_smem(wide ? 128 : 64));
     });
     if (e != cudaSuccess) return e;
-    const int64_t blocks = (int64_t)((a.Lq + kSimtTile - 1) / kSimtTile) * a.H * a.N;
-    return launch_next(bias != nullptr, kernel, (unsigned)blocks, kSimtThreads, simt_fwd_smem(a.D), s,
-                       a, p, bias);
+    return launch_next(LaunchAs(bias != nullptr, splits), kernel, (unsigned)(blocks * splits),
+                       kSimtThreads, simt_fwd_smem(a.D), s, a, p, bias);
 }
 
 // The key blocks, then the query blocks: one launch, so that either fills the

@@ -434,8 +434,8 @@ def test_few_queries_at_every_width_of_a_key(gs_cuda, D, Lq, dtype):
     Problem(gs_cuda, 441, dtype, 2, 2, D, (1, Lq), (1, 131)).forward()
 
 
-@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
-@pytest.mark.parametrize("D", [40, 64, 128])
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("D", [40, 64, 77, 128])
 @pytest.mark.parametrize("q,k", [((1, 9), (1, 2050)), ((1, 130), (1, 1023)), ((3, 20), (4, 211))])
 def test_long_keys_shared_by_the_blocks_of_a_cluster(gs_cuda, q, k, D, dtype):
     # lengths that leave some blocks a part of a tile, one key or nothing
