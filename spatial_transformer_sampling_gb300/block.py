@@ -5,6 +5,7 @@ only check and marshal; every step of the computation runs in libgs's kernels.
 """
 import ctypes
 import functools
+import operator
 
 from . import AttentionAttrs, GsError, _i64, _ok, _shape_error, _torch, load_library
 
@@ -94,7 +95,7 @@ def gs_layer_norm(X, Scale, B=None, axis=-1, epsilon=1e-5, out=None):
     """LayerNormalization of X over its axes from ``axis`` on: (Y, Mean, InvStdDev).  Scale and B
     have the shape of the normalised axes; Mean and InvStdDev are float32 with X's leading axes
     and ones in the place of the normalised ones."""
-    rows, D, inner, kept = _norm_dims(X.shape, axis)
+    rows, D, inner, kept = _norm_dims(X.shape, operator.index(axis))
     _check_input(X)
     _check_like(X, "Scale", Scale, inner)
     if B is not None:
@@ -127,7 +128,7 @@ def gs_layer_norm_backward_workspace_size(rows, D):
 def gs_layer_norm_backward(dY, X, Scale, Mean, InvStdDev, axis=-1, workspace="auto"):
     """Gradient of gs_layer_norm: (dX, dScale, dB).  ``workspace``: "auto", or a device tensor of
     at least gs_layer_norm_backward_workspace_size bytes."""
-    rows, D, inner, kept = _norm_dims(X.shape, axis)
+    rows, D, inner, kept = _norm_dims(X.shape, operator.index(axis))
     _check_input(X)
     _check_like(X, "dY", dY, X.shape)
     _check_like(X, "Scale", Scale, inner)
@@ -244,6 +245,8 @@ _MOST_PLANS = 256
 
 def _plan(Q, K, V, table, buckets, q_extent, k_extent, k_len, scale):
     torch = _host().torch
+    if scale is not None:
+        scale = float(scale)   # a plan holds numbers: a tensor would be known by its identity
     key = (Q.shape, Q.stride(), K.shape, K.stride(), V.shape, V.stride(), Q.dtype,
            None if table is None else table.shape, q_extent, k_extent, scale)
     try:
@@ -298,7 +301,8 @@ def gs_attention(Q, K, V, table=None, buckets=None, q_extent=None, k_extent=None
     Q (N, Lq, H, D), K and V (N, Lk, H, D), any strides with a contiguous last axis; ``table``
     (buckets, H) and ``buckets`` (int32, see gs_relative_buckets) name each pair's bias;
     ``q_extent`` / ``k_extent`` are the tokens' grids (default (1, L)); ``k_len`` (N) int32 masks
-    the keys from there on; ``scale`` defaults to 1 / sqrt(D).  O is dense (N, Lq, H, D), LSE
+    the keys from there on; ``scale`` is a number, read at every call (a one-element
+    tensor's value as well), and defaults to 1 / sqrt(D).  O is dense (N, Lq, H, D), LSE
     float32 (N, H, Lq)."""
     plan = _plan(Q, K, V, table, buckets, q_extent, k_extent, k_len, scale)
     h = _host()
