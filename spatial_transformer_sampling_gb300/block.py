@@ -202,8 +202,10 @@ def _attention_attrs(Q, K, V, table, q_extent, k_extent, scale):
         _shape_error("K", K.shape, (N, Lk, H, D))
     if V.shape != K.shape:
         _shape_error("V", V.shape, K.shape)
-    q_extent = (1, Lq) if q_extent is None else tuple(q_extent)
-    k_extent = (1, Lk) if k_extent is None else tuple(k_extent)
+    q_extent = (1, Lq) if q_extent is None else q_extent
+    k_extent = (1, Lk) if k_extent is None else k_extent
+    if len(q_extent) != 2 or len(k_extent) != 2:
+        raise ValueError(f"an extent is (rows, columns), got {q_extent} and {k_extent}")
     if q_extent[0] * q_extent[1] != Lq or k_extent[0] * k_extent[1] != Lk:
         raise ValueError(f"extents {q_extent} and {k_extent} do not hold {Lq} and {Lk} tokens")
     nb = 0
@@ -243,16 +245,19 @@ _PLANS = {}
 _MOST_PLANS = 256
 
 
+def _extent(e):
+    """A grid's extent as a tuple of whole numbers; None stays None."""
+    return None if e is None else tuple(map(operator.index, e))
+
+
 def _plan(Q, K, V, table, buckets, q_extent, k_extent, k_len, scale):
     torch = _host().torch
     if scale is not None:
         scale = float(scale)   # a plan holds numbers: a tensor would be known by its identity
+    q_extent, k_extent = _extent(q_extent), _extent(k_extent)
     key = (Q.shape, Q.stride(), K.shape, K.stride(), V.shape, V.stride(), Q.dtype,
            None if table is None else table.shape, q_extent, k_extent, scale)
-    try:
-        plan = _PLANS.get(key)
-    except TypeError:        # extents given as lists
-        return _plan(Q, K, V, table, buckets, tuple(q_extent), tuple(k_extent), k_len, scale)
+    plan = _PLANS.get(key)
     if plan is None:
         plan = _Plan(Q, K, V, table, q_extent, k_extent, scale)
         if len(_PLANS) >= _MOST_PLANS:

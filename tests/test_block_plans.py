@@ -59,3 +59,17 @@ def test_results_follow_a_scale_that_changes_in_place(gs_cuda):
     for a, b in zip(gs_cuda.gs_attention_backward(dO, Q, K, V, *want, scale=scale),
                     gs_cuda.gs_attention_backward(dO, Q, K, V, *want, scale=0.125)):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("q,k", [([2, 3], None), (None, [3, 2]), ([2, 3], (3, 2)), (None, None),
+                                 (torch.Size((2, 3)), [1, 6])])
+def test_extents_in_any_sequence_or_left_out(q, k):
+    at = _plan_of(q_extent=q, k_extent=k).attrs
+    assert tuple(at.q_extent) == tuple(q or (1, 6)) and tuple(at.k_extent) == tuple(k or (1, 6))
+
+
+@pytest.mark.parametrize("q", [(), (6,), (1, 2, 3), (2, 2)])
+def test_extents_of_another_shape_are_refused(q):
+    t = torch.zeros((2, 6, 3, 8))
+    with pytest.raises(ValueError, match="extent"):
+        gs.gs_attention(t, t, t, q_extent=q)
