@@ -186,6 +186,14 @@ cudaError_t launch_attn_delta(const AttnArgs &a, const AttnPtrs &p, float *lse2,
                        (const T *)p.O, p.lse, G, (int)per_item, lse2, delta);
 }
 
+// Where group `w` of 32 queries, whose lowest relative index on its side is `lo`,
+// keeps relative index 0, in floats from the start of its (batch, head) pair's
+// sums: 64 bits, since 512 groups of a stride of 2^22 (16384 queries over 4 M
+// keys) are 2^31.  k_end: rel_k of the last key.
+__host__ __device__ inline int64_t rel_entry_0(int w, int stride, int k_end, int lo) {
+    return (int64_t)w * stride + k_end - lo;
+}
+
 // rel[h][r] (+)= the sums of groups of 32 queries; `heads` (batch, head) pairs
 // from head0 on are in `part`.  128 indices a block, four per thread; sixteen
 // warps take every sixteenth (item, group) pair and are joined in order.  Bound by
@@ -196,9 +204,10 @@ static __global__ void __launch_bounds__(kRelSumThreads)
     attn_rel_sum_kernel(AttnArgs a, RelArgs p, int heads, float *rel) {
     constexpr int kSlices = kRelSumThreads / 32, kChunk = kRelSumThreads, kEach = kRelSumIndices / 32;
     // per group of queries: its lowest and highest relative index, and where its
-    // entry 0 lies from the start of an item's sums; per item: that start, and how
-    // far the relative indices reach below a group's lowest one
-    __shared__ int s_lo[kChunk], s_hi[kChunk], s_at[kChunk], s_low[kChunk];
+    // entry 0 lies; per item: the start of its sums, and how far the relative indices
+    // reach below a group's lowest one
+    __shared__ int s_lo[kChunk], s_hi[kChunk], s_low[kChunk];
+    __shared__ int64_t s_at[kChunk];
     __shared__ const float *s_item[kChunk];
     __shared__ float s_sum[kSlices][kRelSumIndices];
     const int lane = threadIdx.x % 32, slice = threadIdx.x / 32;
@@ -216,8 +225,8 @@ static __global__ void __launch_bounds__(kRelSumThreads)
             __syncthreads();
             s_lo[threadIdx.x] = rel_q(a, w_mine * 32);
             s_hi[threadIdx.x] = rel_q(a, min(w_mine * 32 + 31, a.Lq - 1));
-            s_at[threadIdx.x] = (w_mine - w0) * p.stride + k_end - s_lo[threadIdx.x];
-            s_item[threadIdx.x] = p.part + ((int64_t)(nh - p.head0) * groups + w0) * p.stride;
+            s_at[threadIdx.x] = rel_entry_0(w_mine, p.stride, k_end, s_lo[threadIdx.x]);
+            s_item[threadIdx.x] = p.part + (int64_t)(nh - p.head0) * groups * p.stride;
             s_low[threadIdx.x] = keys > 0 ? rel_k(a, keys - 1) : INT_MIN / 2;
             __syncthreads();
             const int nw = min(kChunk, groups - w0), nn = min(kChunk, items - n0);

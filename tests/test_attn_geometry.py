@@ -1,0 +1,71 @@
+"""Host arithmetic of the attention kernels' geometry over the extents that the entry points
+allow: a small program includes the kernels' headers, evaluates their formulas and prints them."""
+import os
+import subprocess
+
+import pytest
+
+from spatial_transformer_sampling_gb300 import build as gsbuild
+
+PROGRAM = r"""
+#include <cstdio>
+#include <cstdlib>
+#include <cstring>
+#include "gs_attn.cuh"
+using namespace gs;
+
+static AttnArgs args(int N, int H, int D, int Hq, int Wq, int Hk, int Wk) {
+    AttnArgs a = {};
+    a.N = N; a.H = H; a.D = D;
+    a.Hq = Hq; a.Wq = Wq; a.Hk = Hk; a.Wk = Wk;
+    a.Lq = Hq * Wq; a.Lk = Hk * Wk;
+    a.P = Wq + Wk - 1;
+    a.R = (Hq + Hk - 1) * a.P;
+    a.nb = 1;
+    return a;
+}
+
+// Lines of "what D Hq Wq Hk Wk" on the input, a number for each on the output.
+int main() {
+    char what[32];
+    int D, g[4];
+    while (scanf("%31s %d %d %d %d %d", what, &D, g, g + 1, g + 2, g + 3) == 6) {
+        const AttnArgs a = args(1, 1, D, g[0], g[1], g[2], g[3]);
+        const int k_end = (a.Hk - 1) * a.P + a.Wk - 1;
+        long long v = -1;
+        if (!strcmp(what, "stride")) v = rel_stride_of(a);
+        if (!strcmp(what, "last_entry")) {   // of the 512th group of queries
+            v = rel_entry_0(511, (int)rel_stride_of(a), k_end, (a.Hk - 1) * a.P + a.Wk - 1);
+        }
+        printf("%lld\n", v);
+    }
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def geometry(tmp_path_factory):
+    d = tmp_path_factory.mktemp("geometry")
+    src, exe = d / "geometry.cu", d / "geometry"
+    src.write_text(PROGRAM)
+    r = subprocess.run([gsbuild.nvcc(), *gsbuild.ARCH, "-std=c++17", "--expt-relaxed-constexpr",
+                        "-I", gsbuild.CSRC, "-I", gsbuild.INCLUDE, "-o", str(exe), str(src)],
+                       capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    assert os.path.exists(exe)
+
+    def ask(what, cases):
+        text = "".join(f"{what} {D} {q[0]} {q[1]} {k[0]} {k[1]}\n" for D, q, k in cases)
+        out = subprocess.run([str(exe)], input=text, capture_output=True, text=True, check=True)
+        return [int(x) for x in out.stdout.split()]
+
+    return ask
+
+
+def test_offsets_of_the_bias_gradients_sums_keep_64_bits(geometry):
+    # 512 groups of 32 queries over as many keys as the relative indices allow (2^24)
+    cases = [(64, (1, 16384), (1, 4_300_000)), (64, (1, 16384), (1, (1 << 24) - 16383)),
+             (64, (2, 8192), (1, 4_190_000))]
+    strides = geometry("stride", cases)
+    assert max(511 * s for s in strides) > 1 << 31
+    assert geometry("last_entry", cases) == [511 * s for s in strides]
