@@ -271,10 +271,13 @@ inline int64_t rel_span(int tokens, int L, int rows, int W, int P) {
 }
 
 // Power of two that holds the relative indices of a warp's 32 queries against
-// 64 keys; 0 when that is more than 1024 (rows of hundreds of tokens that end
-// inside a tile): 20 KB of windows per 256 floats.
+// 64 keys, and those that become final before the next 64: the distance to the
+// next step's first key may cross one grid row more than a step's keys do (rows of
+// 63 tokens, from the last of one on).  0 when that is more than 1024 (rows of
+// hundreds of tokens that end inside a tile): 20 KB of windows per 256 floats.
 inline int rel_window_of(const AttnArgs &a) {
-    const int64_t span = rel_span(32, a.Lq, a.Hq, a.Wq, a.P) + rel_span(kRelCols, a.Lk, a.Hk, a.Wk, a.P) + 1;
+    const int64_t span = rel_span(32, a.Lq, a.Hq, a.Wq, a.P) +
+                         rel_span(kRelCols + 1, a.Lk, a.Hk, a.Wk, a.P) + 1;
     int w = 128;
     while (w < span) w *= 2;
     return w <= 1024 ? w : 0;

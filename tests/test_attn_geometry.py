@@ -34,6 +34,7 @@ int main() {
         const int k_end = (a.Hk - 1) * a.P + a.Wk - 1;
         long long v = -1;
         if (!strcmp(what, "stride")) v = rel_stride_of(a);
+        if (!strcmp(what, "window")) v = rel_window_of(a);
         if (!strcmp(what, "last_entry")) {   // of the 512th group of queries
             v = rel_entry_0(511, (int)rel_stride_of(a), k_end, (a.Hk - 1) * a.P + a.Wk - 1);
         }
@@ -69,3 +70,36 @@ def test_offsets_of_the_bias_gradients_sums_keep_64_bits(geometry):
     strides = geometry("stride", cases)
     assert max(511 * s for s in strides) > 1 << 31
     assert geometry("last_entry", cases) == [511 * s for s in strides]
+
+
+def _widest_use_of_the_window(q, k):
+    """Largest number of relative indices that one step of 64 keys adds to, or makes final, for
+    any 32 queries."""
+    (hq, wq), (hk, wk) = q, k
+    P, Lq, Lk = wq + wk - 1, hq * wq, hk * wk
+    rel_q = lambda i: (i // wq + hk - 1) * P + i % wq + wk - 1
+    rel_k = lambda j: j // wk * P + j % wk
+    widest = 0
+    for i in range(0, Lq, 32):
+        low, high = rel_q(i), rel_q(min(i + 31, Lq - 1))
+        top = high
+        for j in range(0, Lk, 64):
+            bottom = low - rel_k(min(j + 63, Lk - 1))
+            final_above = bottom - 1 if j + 64 >= Lk else high - rel_k(j + 64)
+            widest = max(widest, high - rel_k(j) - bottom + 1, top - final_above)
+            top = final_above
+    return widest
+
+
+WINDOW_GRIDS = [((1, 226), (70, 63)), ((1, 130), (70, 63)), ((1, 34), (64, 63)), ((1, 400), (90, 63)),
+                ((1, 500), (9, 21)), ((4, 33), (70, 21)), ((8, 8), (8, 8)), ((32, 32), (32, 32)),
+                ((1, 300), (1, 257)), ((3, 100), (5, 70)), ((20, 1), (31, 1)), ((2, 65), (2, 65)),
+                ((17, 23), (17, 23)), ((64, 3), (64, 3)), ((20, 8), (4, 130)), ((12, 200), (9, 7)),
+                ((7, 9), (65, 9)), ((1, 77), (70, 7))]
+
+
+def test_window_of_the_bias_gradient_holds_what_a_step_adds_to_and_what_it_leaves(geometry):
+    windows = geometry("window", [(64, q, k) for q, k in WINDOW_GRIDS])
+    assert any(windows)
+    for (q, k), w in zip(WINDOW_GRIDS, windows):
+        assert w == 0 or w >= _widest_use_of_the_window(q, k), (q, k, w)
