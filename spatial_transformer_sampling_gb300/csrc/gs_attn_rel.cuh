@@ -21,6 +21,7 @@ namespace gs {
 constexpr int kRelCopies = 4;     // two for each of the two warps
 constexpr int kRelCols = 64;      // keys of one step
 constexpr int kRelHalf = kRelCols / 2;
+constexpr int kRelMost = 1024;    // floats of the largest window
 
 // Where a launch of the query kernel leaves its share of the bias gradient.
 struct RelArgs {
@@ -35,7 +36,7 @@ __host__ __device__ inline int rows64(int L) { return (L + 63) / 64 * 64; }
 
 // Shared memory of `pairs` bias-gradient windows of `w` floats: four copies, the
 // moving window and the columns' relative indices each.
-inline __host__ __device__ int rel_smem(int w, int pairs) {
+inline __host__ __device__ constexpr int rel_smem(int w, int pairs) {
     return w ? pairs * ((kRelCopies + 1) * w + kRelCols) * 4 : 0;
 }
 
@@ -273,14 +274,14 @@ inline int64_t rel_span(int tokens, int L, int rows, int W, int P) {
 // Power of two that holds the relative indices of a warp's 32 queries against
 // 64 keys, and those that become final before the next 64: the distance to the
 // next step's first key may cross one grid row more than a step's keys do (rows of
-// 63 tokens, from the last of one on).  0 when that is more than 1024 (rows of
+// 63 tokens, from the last of one on).  0 when that is more than kRelMost (rows of
 // hundreds of tokens that end inside a tile): 20 KB of windows per 256 floats.
 inline int rel_window_of(const AttnArgs &a) {
     const int64_t span = rel_span(32, a.Lq, a.Hq, a.Wq, a.P) +
                          rel_span(kRelCols + 1, a.Lk, a.Hk, a.Wk, a.P) + 1;
     int w = 128;
     while (w < span) w *= 2;
-    return w <= 1024 ? w : 0;
+    return w <= kRelMost ? w : 0;
 }
 // Floats a query warp writes to `part`.
 inline int64_t rel_stride_of(const AttnArgs &a) {

@@ -389,22 +389,37 @@ __global__ void __launch_bounds__(kTcThreads, TcBwdShape<DP, true>::kCtas)
         attn_tc_bwd_block<T, DP, BIAS, true>(kv, blockIdx.x - q_blocks);
 }
 
+// How a launch reads the bias, and its dynamic shared memory: what the larger of
+// the two kinds of blocks needs.
+struct TcBwdLaunch {
+    int mode, smem;
+};
+template <int DP> constexpr int tc_bwd_smem(int kv_count, int q_count, int rel_window) {
+    using Kv = TcBwdShape<DP, true>;
+    using Qs = TcBwdShape<DP, false>;
+    return std::max(Kv::kSmem + Kv::kStages * kv_count * 4,
+                    Qs::kSmem + rel_smem(rel_window, 4) + Qs::kStages * q_count * 4);
+}
+static_assert(tc_bwd_smem<128>(0, 0, kRelMost) <= kTcSmemOne, "the bias gradient always fits");
+// One mode for both kinds: with a window that is too large for one, or where the
+// windows do not fit beside those of the bias gradient (wide heads, a narrow grid of
+// queries against a wide one of keys), both read the bias through L1.
+template <int DP>
+TcBwdLaunch tc_bwd_launch_of(const TcBias &kv, const TcBias &q, bool bias, int rel_window) {
+    const int with = tc_bwd_smem<DP>(kv.count, q.count, rel_window);
+    if (bias && q.count && kv.count && with <= kTcSmemOne) return {kBiasWindow, with};
+    return {bias ? kBiasGlobal : kBiasNone, tc_bwd_smem<DP>(0, 0, rel_window)};
+}
+
 template <typename T, int DP, int BIAS>
 cudaError_t launch_attn_tc_bwd_as(const TcBwdArgs &kv, const TcBwdArgs &q, int kv_heads, int q_heads,
-                                  cudaStream_t s) {
+                                  int smem, cudaStream_t s) {
     auto kernel = attn_tc_bwd_kernel<T, DP, BIAS>;
     static DeviceFlags ready;
     const cudaError_t e = once_per_device(ready, [&] {
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmemOne);
     });
     if (e != cudaSuccess) return e;
-    const auto window = [](const TcBwdArgs &p, int stages) {
-        return BIAS == kBiasWindow ? stages * p.bias.count * 4 : 0;
-    };
-    using Kv = TcBwdShape<DP, true>;
-    using Qs = TcBwdShape<DP, false>;
-    const int smem = std::max(Kv::kSmem + window(kv, Kv::kStages),
-                              Qs::kSmem + rel_smem(q.rel.window, 4) + window(q, Qs::kStages));
     const int kv_blocks = (kv.a.Lk + kTcM - 1) / kTcM * kv_heads;
     const int q_blocks = (q.a.Lq + kTcM - 1) / kTcM * q_heads;
     return launch_next(true, kernel, (unsigned)kv_blocks + (unsigned)q_blocks, kTcThreads, smem, s, kv, q,
@@ -415,15 +430,13 @@ cudaError_t launch_attn_tc_bwd_as(const TcBwdArgs &kv, const TcBwdArgs &q, int k
 template <typename T>
 cudaError_t launch_attn_tc_bwd(const TcBwdArgs &kv, const TcBwdArgs &q, int kv_heads, int q_heads,
                                cudaStream_t s) {
-    // one mode for both: a window that is too large for one is read through L1 by both
-    const int mode = !q.bias.base                          ? kBiasNone
-                     : q.bias.count && kv.bias.count ? kBiasWindow
-                                                     : kBiasGlobal;
     const auto run = [&](auto dp) {
         constexpr int DP = decltype(dp)::value;
-        return mode == kBiasNone     ? launch_attn_tc_bwd_as<T, DP, kBiasNone>(kv, q, kv_heads, q_heads, s)
-               : mode == kBiasWindow ? launch_attn_tc_bwd_as<T, DP, kBiasWindow>(kv, q, kv_heads, q_heads, s)
-                                     : launch_attn_tc_bwd_as<T, DP, kBiasGlobal>(kv, q, kv_heads, q_heads, s);
+        const TcBwdLaunch as = tc_bwd_launch_of<DP>(kv.bias, q.bias, q.bias.base, q.rel.window);
+        return as.mode == kBiasNone ? launch_attn_tc_bwd_as<T, DP, kBiasNone>(kv, q, kv_heads, q_heads, as.smem, s)
+               : as.mode == kBiasWindow
+                   ? launch_attn_tc_bwd_as<T, DP, kBiasWindow>(kv, q, kv_heads, q_heads, as.smem, s)
+                   : launch_attn_tc_bwd_as<T, DP, kBiasGlobal>(kv, q, kv_heads, q_heads, as.smem, s);
     };
     return q.a.D <= 64 ? run(std::integral_constant<int, 64>()) : run(std::integral_constant<int, 128>());
 }

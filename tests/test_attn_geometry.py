@@ -35,6 +35,20 @@ int main() {
         long long v = -1;
         if (!strcmp(what, "stride")) v = rel_stride_of(a);
         if (!strcmp(what, "window")) v = rel_window_of(a);
+        const TcBias q = tc_bias_of(a, false), k = tc_bias_of(a, true);
+        if (!strcmp(what, "bwd_smem"))
+            v = D <= 64 ? tc_bwd_launch_of<64>(k, q, true, rel_window_of(a)).smem
+                        : tc_bwd_launch_of<128>(k, q, true, rel_window_of(a)).smem;
+        if (!strcmp(what, "bwd_mode"))
+            v = D <= 64 ? tc_bwd_launch_of<64>(k, q, true, rel_window_of(a)).mode
+                        : tc_bwd_launch_of<128>(k, q, true, rel_window_of(a)).mode;
+        if (!strcmp(what, "fwd_smem"))
+            v = D <= 64 ? std::max(TcFwdShape<64, kFwdMany>::kSmem, TcFwdShape<64, kFwdSplit>::kSmem) +
+                              TcFwdShape<64, kFwdMany>::kStages * q.count * 4
+                        : std::max(TcFwdShape<128, kFwdMany>::kSmem, TcFwdShape<128, kFwdSplit>::kSmem) +
+                              TcFwdShape<128, kFwdMany>::kStages * q.count * 4;
+        if (!strcmp(what, "simt_smem"))
+            v = std::max({simt_fwd_smem(D), simt_bwd_smem(D, true, 0), simt_bwd_smem(D, false, rel_window_of(a))});
         if (!strcmp(what, "last_entry")) {   // of the 512th group of queries
             v = rel_entry_0(511, (int)rel_stride_of(a), k_end, (a.Hk - 1) * a.P + a.Wk - 1);
         }
@@ -103,3 +117,26 @@ def test_window_of_the_bias_gradient_holds_what_a_step_adds_to_and_what_it_leave
     assert any(windows)
     for (q, k), w in zip(WINDOW_GRIDS, windows):
         assert w == 0 or w >= _widest_use_of_the_window(q, k), (q, k, w)
+
+
+def test_every_launch_fits_into_a_blocks_shared_memory(geometry):
+    # grids of one to forty rows, narrow against wide: their windows are the largest
+    widths = (1, 2, 4, 8, 12, 16, 20, 31, 32, 48, 64, 96, 128, 130, 200, 208, 224, 256, 300, 466)
+    grids = [((hq, wq), (hk, wk)) for hq in (1, 3, 8, 20, 40) for hk in (1, 3, 4, 32, 40)
+             for wq in widths for wk in widths]
+    for D in (64, 128):
+        cases = [(D, q, k) for q, k in grids]
+        for what, limit in (("bwd_smem", 223 * 1024), ("fwd_smem", 223 * 1024),
+                            ("simt_smem", 227 * 1024 - 256)):
+            worst = max(zip(geometry(what, cases), cases))
+            assert worst[0] <= limit, (what, worst)
+
+
+def test_windows_of_the_bias_are_copied_wherever_they_fit(geometry):
+    window, through_l1 = 1, 2
+    cases = [(64, (32, 32), (32, 32)), (128, (48, 48), (48, 48)), (128, (1, 3000), (1, 3000)),
+             (128, (64, 64), (64, 64)), (64, (20, 8), (4, 130))]
+    assert geometry("bwd_mode", cases) == [window] * len(cases)
+    cases = [(128, (20, 8), (4, 130)), (128, (16, 8), (3, 128)), (128, (40, 16), (40, 208)),
+             (128, (1, 32), (32, 1)), (128, (16, 16), (1, 256))]
+    assert geometry("bwd_mode", cases) == [through_l1] * len(cases)
