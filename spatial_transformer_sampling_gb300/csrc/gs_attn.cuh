@@ -140,16 +140,17 @@ Workspace workspace_of(const AttnArgs &a, bool backward) {
     return w;
 }
 
-// Fills the expanded bias; returns the entry of relative index 0 of head 0.
+// Fills the expanded bias; *entry_0: the entry of relative index 0 of head 0.
 template <typename T>
-const float *expand_bias(AttnArgs &a, const AttnPtrs &p, char *ws, cudaStream_t s) {
-    if (a.nb == 0) return nullptr;
+cudaError_t expand_bias(AttnArgs &a, const AttnPtrs &p, char *ws, const float **entry_0, cudaStream_t s) {
+    *entry_0 = nullptr;
+    if (a.nb == 0) return cudaSuccess;
     float *bias = (float *)(ws + workspace_of(a, false).bias);
     const int pad = tc_bias_pad(a);
     a.bias_stride = bias_stride(a);
-    attn_bias_kernel<T><<<dim3((a.bias_stride + 255) / 256, a.H), 256, 0, s>>>((const T *)p.table, a,
-                                                                              pad, bias);
-    return bias + pad;
+    *entry_0 = bias + pad;
+    return launch_next(false, attn_bias_kernel<T>, dim3((a.bias_stride + 255) / 256, a.H), 256, 0, s,
+                       (const T *)p.table, a, pad, bias);
 }
 
 // Tensor-core views of the backward pass (16-bit types); false when its kernels
@@ -183,10 +184,12 @@ template <typename T>
 cudaError_t launch_attn(const AttnArgs &args, const AttnPtrs &p, void *ws, cudaStream_t s) {
     AttnArgs a = args;
     if (few_takes(a)) return launch_attn_few<T>(a, p, s);
-    const float *bias = expand_bias<T>(a, p, (char *)ws, s);
+    const float *bias;
+    cudaError_t e = expand_bias<T>(a, p, (char *)ws, &bias, s);
+    if (e != cudaSuccess) return e;
     if constexpr (sizeof(T) == 2) {
         bool used = false;
-        const cudaError_t e = launch_attn_tc_fwd<T>(a, p, bias, s, &used);
+        e = launch_attn_tc_fwd<T>(a, p, bias, s, &used);
         if (used || e != cudaSuccess) return e;
     }
     return launch_attn_simt_fwd<T>(a, p, bias, s);
@@ -197,14 +200,16 @@ cudaError_t launch_attn_backward(const AttnArgs &args, const AttnPtrs &p, void *
     AttnArgs a = args;
     char *ws = (char *)ws_;
     const Workspace w = workspace_of(a, true);
-    const float *bias = expand_bias<T>(a, p, ws, s);
+    const float *bias;
+    cudaError_t e = expand_bias<T>(a, p, ws, &bias, s);
+    if (e != cudaSuccess) return e;
     float *rel = (float *)(ws + w.rel), *lse2 = (float *)(ws + w.lse2);
     float *delta = (float *)(ws + w.delta);
     TcBwdArgs kv, q;
     bool tc = false;
     if constexpr (sizeof(T) == 2) tc = tc_backward_views<T>(a, p, kv, q);
     const int pairs = a.N * a.H;
-    cudaError_t e = launch_attn_delta<T>(a, p, lse2, delta, s);
+    e = launch_attn_delta<T>(a, p, lse2, delta, s);
     if (e != cudaSuccess) return e;
     RelArgs part = {};
     part.window = bias ? rel_window_of(a) : 0;

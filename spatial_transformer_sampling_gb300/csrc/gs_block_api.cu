@@ -21,6 +21,14 @@ size_t elem_size(gs_dtype dt) { return dt == GS_F32 ? 4 : 2; }
 bool dtype_ok(int dt) { return dt == GS_F32 || dt == GS_F16 || dt == GS_BF16; }
 bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
+// A call's error is its own: the runtime keeps the last one until it is asked for,
+// and a later call that asks would take it for its own.
+gs_status status_of(cudaError_t e) {
+    if (e == cudaSuccess) return GS_OK;
+    (void)cudaGetLastError();
+    return GS_ERR_CUDA;
+}
+
 template <typename F>
 gs_status dispatch(gs_dtype dt, F &&f) {
     cudaError_t e;
@@ -29,7 +37,7 @@ gs_status dispatch(gs_dtype dt, F &&f) {
         case GS_F16: e = f(__half()); break;
         default: e = f(__nv_bfloat16()); break;
     }
-    return e == cudaSuccess ? GS_OK : GS_ERR_CUDA;
+    return status_of(e);
 }
 
 // a * b <= limit for a, b >= 0 (no overflow).
@@ -115,8 +123,6 @@ size_t attention_ws(const gs::AttnArgs &a, gs_dtype dt, bool backward) {
 
 // Nothing to attend with: no query, no key or no head.
 bool no_pairs(const gs::AttnArgs &a) { return a.N == 0 || a.H == 0 || a.Lq == 0 || a.Lk == 0; }
-
-bool on_device_error(cudaError_t e) { return e != cudaSuccess; }
 
 // Distance from which bucket e + k of one axis side starts.
 int64_t bucket_start(int e, int m, int64_t far, int k) {
@@ -322,16 +328,16 @@ gs_status gs_attention_backward(const void *dO, const void *Q, const void *K, co
         !aligned(k_len, 4))
         return GS_ERR_ALIGN;
     if (no_pairs(a)) {   // every gradient there is is zero
+        cudaError_t e = cudaSuccess;
         const auto clear = [&](void *p, int64_t n) {
-            return n == 0 ? cudaSuccess : cudaMemsetAsync(p, 0, (size_t)n * es, stream);
+            if (n > 0 && e == cudaSuccess) e = cudaMemsetAsync(p, 0, (size_t)n * es, stream);
         };
         const int64_t row = (int64_t)a.H * a.D;
-        if (on_device_error(clear(dQ, (int64_t)a.N * a.Lq * row)) ||
-            on_device_error(clear(dK, (int64_t)a.N * a.Lk * row)) ||
-            on_device_error(clear(dV, (int64_t)a.N * a.Lk * row)) ||
-            on_device_error(clear(dTable, (int64_t)a.nb * a.H)))
-            return GS_ERR_CUDA;
-        return GS_OK;
+        clear(dQ, (int64_t)a.N * a.Lq * row);
+        clear(dK, (int64_t)a.N * a.Lk * row);
+        clear(dV, (int64_t)a.N * a.Lk * row);
+        clear(dTable, (int64_t)a.nb * a.H);
+        return status_of(e);
     }
     st = check_workspace(workspace, workspace_bytes, attention_ws(a, dt, true), 256);
     if (st != GS_OK) return st;
