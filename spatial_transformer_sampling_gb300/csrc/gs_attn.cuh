@@ -122,9 +122,9 @@ int bias_stride(const AttnArgs &a) { return (a.R + 3) / 4 * 4 + 2 * tc_bias_pad(
 
 // The workspace's parts, in order; offsets in bytes.
 struct Workspace {
-    size_t bias, rel, lse2, delta, part, end;
+    size_t bias, rel, lse2, delta, range, part, end;
 };
-Workspace workspace_of(const AttnArgs &a, bool backward) {
+template <typename T> Workspace workspace_of(const AttnArgs &a, bool backward) {
     Workspace w = {};
     if (!backward && few_takes(a)) return w;
     const size_t per_rel = a.nb ? round256((size_t)a.H * a.R * sizeof(float)) : 0;
@@ -133,7 +133,10 @@ Workspace workspace_of(const AttnArgs &a, bool backward) {
     const size_t per_row = round256((size_t)a.N * a.H * rows64(a.Lq) * sizeof(float));
     w.lse2 = w.rel + per_rel;
     w.delta = w.lse2 + per_row;
-    w.part = w.end = w.delta + per_row;
+    w.range = w.delta + per_row;
+    w.part = w.end = w.range + (kScaledGradient<T> ? round256((size_t)a.N * a.H * range_parts(a) * 2 *
+                                                              sizeof(float))
+                                                   : 0);
     if (a.nb && rel_window_of(a) > 0)
         w.end += round256((size_t)rel_heads_of(a) * ((a.Lq + 31) / 32) * rel_stride_of(a) *
                           sizeof(float));
@@ -145,7 +148,7 @@ template <typename T>
 cudaError_t expand_bias(AttnArgs &a, const AttnPtrs &p, char *ws, const float **entry_0, cudaStream_t s) {
     *entry_0 = nullptr;
     if (a.nb == 0) return cudaSuccess;
-    float *bias = (float *)(ws + workspace_of(a, false).bias);
+    float *bias = (float *)(ws + workspace_of<T>(a, false).bias);
     const int pad = tc_bias_pad(a);
     a.bias_stride = bias_stride(a);
     *entry_0 = bias + pad;
@@ -177,7 +180,7 @@ bool tc_backward_views(const AttnArgs &a, const AttnPtrs &ptr, TcBwdArgs &kv, Tc
 
 template <typename T>
 size_t attn_ws_bytes(const AttnArgs &a, bool backward) {
-    return workspace_of(a, backward).end;
+    return workspace_of<T>(a, backward).end;
 }
 
 template <typename T>
@@ -199,7 +202,7 @@ template <typename T>
 cudaError_t launch_attn_backward(const AttnArgs &args, const AttnPtrs &p, void *ws_, cudaStream_t s) {
     AttnArgs a = args;
     char *ws = (char *)ws_;
-    const Workspace w = workspace_of(a, true);
+    const Workspace w = workspace_of<T>(a, true);
     const float *bias;
     cudaError_t e = expand_bias<T>(a, p, ws, &bias, s);
     if (e != cudaSuccess) return e;
@@ -209,7 +212,9 @@ cudaError_t launch_attn_backward(const AttnArgs &args, const AttnPtrs &p, void *
     bool tc = false;
     if constexpr (sizeof(T) == 2) tc = tc_backward_views<T>(a, p, kv, q);
     const int pairs = a.N * a.H;
-    e = launch_attn_delta<T>(a, p, lse2, delta, s);
+    RangeArgs range = {};
+    if (kScaledGradient<T> && tc) range = {range_parts(a), (float *)(ws + w.range)};
+    e = launch_attn_delta<T>(a, p, lse2, delta, range, s);
     if (e != cudaSuccess) return e;
     RelArgs part = {};
     part.window = bias ? rel_window_of(a) : 0;
@@ -223,6 +228,7 @@ cudaError_t launch_attn_backward(const AttnArgs &args, const AttnPtrs &p, void *
         kv.bias.stride = q.bias.stride = a.bias_stride;
         kv.lse2 = q.lse2 = lse2;
         kv.delta = q.delta = delta;
+        kv.range = q.range = range;
         kv.out1 = p.dK;
         kv.out2 = p.dV;
         q.out1 = p.dQ;

@@ -137,14 +137,78 @@ struct RelWindow {
     }
 };
 
+// How far dS may be scaled up on its way to a 16-bit type: the largest sums of
+// squares of a dO row and of a live V row, in `parts` shares per (batch, head)
+// pair.  By Cauchy and Schwarz their product bounds dP, and delta, in which V is
+// averaged, as well.  Rows that are not finite do not count: what they reach is
+// not finite either way.
+struct RangeArgs {
+    int parts;      // 0: not wanted
+    float *most;    // (pairs, parts, 2): dO, V
+};
+constexpr int kRangeMost = 16;     // shares at most
+constexpr int kRangeRows = 256;    // rows of a share at least
+inline int range_parts(const AttnArgs &a) {
+    return std::min((std::max(a.Lq, a.Lk) + kRangeRows - 1) / kRangeRows, kRangeMost);
+}
+
+// One share: `part` of dO's and V's rows, which are runs of 16 bytes.
+template <typename T>
+__device__ __forceinline__ void attn_range_block(const AttnArgs &a, const T *dO, const T *V,
+                                                 const RangeArgs &range, int block) {
+    constexpr int E = 16 / (int)sizeof(T);
+    __shared__ float s_most[8];
+    const int nh = block / range.parts, part = block % range.parts, n = nh / a.H, h = nh % a.H;
+    int G = 1;   // lanes of a row
+    while (G * E < a.D) G *= 2;
+    const int lane = threadIdx.x % G;
+    for (int which = 0; which < 2; ++which) {
+        const int rows = which ? keys_of(a, n) : a.Lq;
+        const int64_t step = which ? a.vs[1] : (int64_t)a.H * a.D;
+        const T *base = which ? V + n * a.vs[0] + h * a.vs[2] : dO + ((int64_t)n * a.Lq * a.H + h) * a.D;
+        const int chunk = (rows + range.parts - 1) / range.parts;
+        const int end = min((part + 1) * chunk, rows);
+        float most = 0.0f;
+        for (int r0 = part * chunk; r0 < end; r0 += 256 / G) {   // the same for all threads
+            const int r = r0 + threadIdx.x / G;
+            float sum = 0.0f;
+            if (r < end && lane * E < a.D) {
+                const uint4 u = __ldg(reinterpret_cast<const uint4 *>(base + r * step + lane * E));
+                const T *x = reinterpret_cast<const T *>(&u);
+#pragma unroll
+                for (int k = 0; k < E; ++k) sum = fmaf(IO<T>::to_f(x[k]), IO<T>::to_f(x[k]), sum);
+            }
+            for (int o = G / 2; o > 0; o /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            if (sum < INFINITY) most = fmaxf(most, sum);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+        __syncthreads();
+        if (threadIdx.x % 32 == 0) s_most[threadIdx.x / 32] = most;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            for (int w = 1; w < 8; ++w) most = fmaxf(most, s_most[w]);
+            range.most[((int64_t)nh * range.parts + part) * 2 + which] = most;
+        }
+    }
+}
+
 // lse2 and delta of every query (6.6 us for the 17 MB of 8 x 8 heads of 32 x 32
 // tokens, D 64, bf16: latency and memory), G lanes per row (a power of two; VEC: rows of
 // 16-byte runs, one per lane).  A block takes 256 / G rows of one batch item, in
-// memory order (token, head).
-template <typename T, bool VEC>
-__global__ void attn_delta_kernel(AttnArgs a, const T *dO, const T *O, const float *lse, int G,
-                                  int blocks_per_item, float *lse2, float *delta) {
+// memory order (token, head).  RANGE: the blocks from `rows` on take a share of
+// RangeArgs each.
+template <typename T, bool VEC, bool RANGE>
+__global__ void attn_delta_kernel(AttnArgs a, const T *dO, const T *O, const T *V, const float *lse,
+                                  int G, int blocks_per_item, float *lse2, float *delta,
+                                  RangeArgs range) {
     constexpr int E = 16 / (int)sizeof(T);
+    const int row_blocks = blocks_per_item * a.N;
+    if (RANGE && (int)blockIdx.x >= row_blocks) {
+        attn_range_block(a, dO, V, range, blockIdx.x - row_blocks);
+        wait_for_previous_kernel();
+        return;
+    }
     const int L64 = rows64(a.Lq), part = threadIdx.x % G;
     const int n = blockIdx.x / blocks_per_item;
     const int64_t row = (int64_t)(blockIdx.x % blocks_per_item) * (256 / G) + threadIdx.x / G;
@@ -176,15 +240,18 @@ __global__ void attn_delta_kernel(AttnArgs a, const T *dO, const T *O, const flo
 
 template <typename T>
 cudaError_t launch_attn_delta(const AttnArgs &a, const AttnPtrs &p, float *lse2, float *delta,
-                              cudaStream_t s) {
+                              const RangeArgs &range, cudaStream_t s) {
     constexpr int E = 16 / (int)sizeof(T);
     const bool vec = a.D % E == 0 && (((uintptr_t)p.dO | (uintptr_t)p.O) & 15u) == 0;
     int G = vec ? 1 : 16;
     while (vec && G * E < a.D) G *= 2;
     const int64_t per_item = ((int64_t)rows64(a.Lq) * a.H * G + 255) / 256;
-    auto kernel = vec ? attn_delta_kernel<T, true> : attn_delta_kernel<T, false>;
-    return launch_next(a.nb > 0, kernel, (unsigned)(per_item * a.N), 256, 0, s, a, (const T *)p.dO,
-                       (const T *)p.O, p.lse, G, (int)per_item, lse2, delta);
+    auto kernel = vec ? attn_delta_kernel<T, true, false> : attn_delta_kernel<T, false, false>;
+    if constexpr (__is_same(T, __half))   // its rows are then runs of 16 bytes
+        if (range.parts) kernel = attn_delta_kernel<T, true, true>;
+    return launch_next(a.nb > 0, kernel, (unsigned)(per_item * a.N + (int64_t)a.N * a.H * range.parts), 256,
+                       0, s, a, (const T *)p.dO, (const T *)p.O, (const T *)p.V, p.lse, G, (int)per_item,
+                       lse2, delta, range);
 }
 
 // Where group `w` of 32 queries, whose lowest relative index on its side is `lo`,

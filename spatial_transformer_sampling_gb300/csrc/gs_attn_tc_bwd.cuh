@@ -32,6 +32,7 @@ struct TcBwdArgs {
     TcBias bias;
     const float *lse2;        // (N, H, rows64(Lq)): lse * log2(e), +inf where nothing counts
     const float *delta;       // same shape: dO . O
+    RangeArgs range;          // fp16: what bounds ds
     void *out1, *out2;        // dK, dV or dQ
     RelArgs rel;              // DQ: the bias gradient
 };
@@ -52,6 +53,35 @@ template <int DP, bool DKV> struct TcBwdShape {
 // tensor cores (and dV back), so that those below 2^-14 keep their precision.
 template <typename T> constexpr float kWeightScale = 1.0f;
 template <> constexpr float kWeightScale<__half> = 4096.0f;
+
+// Their gradients ds go with dO, which may be anything between a mean's over all
+// tokens and a scaled loss's: fp16 ones are multiplied by the power of two that
+// takes the bound of a (batch, head) pair to 2^15 at most (dK and dQ are divided
+// by it again).  Unscaled, a dO of 1e-4 over 4096 keys left ds below 2^-14, with 5 %
+// of dK lost, and one of 2e4 over 64 keys took it beyond the type's range.
+template <typename T> constexpr bool kScaledGradient = __is_same(T, __half);
+
+// That power of two; a whole warp calls it.
+__device__ __forceinline__ float gradient_scale(const float *most, int parts, int nh) {
+    const int lane = threadIdx.x % 32;
+    float g = 0.0f, v = 0.0f;
+    if (lane < parts) {
+        const float2 both = *reinterpret_cast<const float2 *>(most + ((int64_t)nh * parts + lane) * 2);
+        g = both.x;
+        v = both.y;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
+        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    }
+    // |ds| <= 2 sqrt(g v) < 2^(1 + e / 2) with e the exponent above g v: both are sums
+    // of 128 squares of fp16 values, 2^-48 to 2^39, so that the scale is 2^-26 to 2^62
+    const float square = g * v;
+    if (!(square > 0.0f)) return 1.0f;
+    const int e = (int)(__float_as_uint(square) >> 23) - 126;
+    return __uint_as_float((uint32_t)(127 + 14 - ((e + 1) >> 1)) << 23);
+}
 
 template <typename T, int DP, int BIAS, bool DKV>
 __device__ __forceinline__ void attn_tc_bwd_block(const TcBwdArgs &p, int block) {
@@ -112,7 +142,11 @@ __device__ __forceinline__ void attn_tc_bwd_block(const TcBwdArgs &p, int block)
     __syncthreads();
     tcgen05_fence_after_sync();
     const uint32_t tmem = tmem_base;
-    wait_for_previous_kernel(lse2, delta, bias);
+    const float *most = p.range.most;
+    if (kScaledGradient<T>)
+        wait_for_previous_kernel(lse2, delta, bias, most);
+    else
+        wait_for_previous_kernel(lse2, delta, bias);
     bool ok = true;
 
     const bool tail = !DKV && cols % kTcN != 0;   // the last tile holds masked keys
@@ -229,6 +263,7 @@ __device__ __forceinline__ void attn_tc_bwd_block(const TcBwdArgs &p, int block)
         const bool counts = i < live_rows && steps > 0;
         const float row_lse = !DKV ? (counts ? lse2[i] : INFINITY) : 0.0f;
         const float row_delta = !DKV && counts ? delta[i] : 0.0f;
+        const float up = kScaledGradient<T> ? gradient_scale(most, p.range.parts, nh) : 1.0f;
         const bool with_rel = !DKV && BIAS && p.rel.window > 0 && i0 + pair * 32 < a.Lq && steps > 0;
         RelWindow win;
         float *rel_out = nullptr;
@@ -327,7 +362,11 @@ __device__ __forceinline__ void attn_tc_bwd_block(const TcBwdArgs &p, int block)
                 tmem_st_x16(tmem + Sh::kTmemP + my_tmem + first, w);
             }
 #pragma unroll
-            for (int c = 0; c < kTcHalf / 2; ++c) w[c] = pack2<T>(ds[2 * c], ds[2 * c + 1]);
+            for (int c = 0; c < kTcHalf / 2; ++c) {
+                float2 e = make_float2(ds[2 * c], ds[2 * c + 1]);
+                if (kScaledGradient<T>) e = mul_f32x2(e, make_float2(up, up));
+                w[c] = pack2<T>(e.x, e.y);
+            }
             tmem_st_x16(tmem + Sh::kTmemP + my_tmem + first + kTcHalf / 2, w);
             tmem_wait_st();
             tcgen05_fence_before_sync();
@@ -342,7 +381,7 @@ __device__ __forceinline__ void attn_tc_bwd_block(const TcBwdArgs &p, int block)
             const int64_t at = (((int64_t)n * rows + i) * a.H + h) * a.D;
             for (int which = 0; which < (DKV ? 2 : 1); ++which) {
                 T *out = (T *)(which ? p.out2 : p.out1) + at;
-                const float f = counts ? (which ? 1.0f / kWeightScale<T> : a.scale) : 0.0f;
+                const float f = !counts ? 0.0f : which ? 1.0f / kWeightScale<T> : a.scale / up;
                 const uint32_t acc = tmem + (which ? Sh::kTmemAcc2 : Sh::kTmemAcc1) + my_tmem;
 #pragma unroll 1
                 for (int c = part * 32; c < a.D; c += 64) {   // every other chunk
