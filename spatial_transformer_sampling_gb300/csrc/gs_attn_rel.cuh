@@ -271,11 +271,9 @@ constexpr int kRelSumIndices = 128, kRelSumThreads = 512;
 static __global__ void __launch_bounds__(kRelSumThreads)
     attn_rel_sum_kernel(AttnArgs a, RelArgs p, int heads, float *rel) {
     constexpr int kSlices = kRelSumThreads / 32, kChunk = kRelSumThreads, kEach = kRelSumIndices / 32;
-    // per group of queries: its lowest and highest relative index, and where its
-    // entry 0 lies; per item: the start of its sums, and how far the relative indices
-    // reach below a group's lowest one
+    // per group of queries: its lowest and highest relative index; per item: the start
+    // of its sums, and how far the relative indices reach below a group's lowest one
     __shared__ int s_lo[kChunk], s_hi[kChunk], s_low[kChunk];
-    __shared__ int64_t s_at[kChunk];
     __shared__ const float *s_item[kChunk];
     __shared__ float s_sum[kSlices][kRelSumIndices];
     const int lane = threadIdx.x % 32, slice = threadIdx.x / 32;
@@ -293,7 +291,6 @@ static __global__ void __launch_bounds__(kRelSumThreads)
             __syncthreads();
             s_lo[threadIdx.x] = rel_q(a, w_mine * 32);
             s_hi[threadIdx.x] = rel_q(a, min(w_mine * 32 + 31, a.Lq - 1));
-            s_at[threadIdx.x] = rel_entry_0(w_mine, p.stride, k_end, s_lo[threadIdx.x]);
             s_item[threadIdx.x] = p.part + (int64_t)(nh - p.head0) * groups * p.stride;
             s_low[threadIdx.x] = keys > 0 ? rel_k(a, keys - 1) : INT_MIN / 2;
             __syncthreads();
@@ -303,7 +300,7 @@ static __global__ void __launch_bounds__(kRelSumThreads)
 #pragma unroll 4
             for (int k = slice; k < nn * nw; k += kSlices) {
                 const int hi = s_hi[w], lo = s_lo[w] - s_low[i];
-                const float *at = s_item[i] + s_at[w] + r;
+                const float *at = s_item[i] + rel_entry_0(w0 + w, p.stride, k_end, s_lo[w]) + r;
 #pragma unroll
                 for (int q = 0; q < kEach; ++q)
                     if (r + 32 * q <= hi && r + 32 * q >= lo) sum[q] += __ldg(at + 32 * q);
