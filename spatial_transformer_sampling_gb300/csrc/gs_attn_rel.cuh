@@ -146,8 +146,8 @@ struct RangeArgs {
     int parts;      // 0: not wanted
     float *most;    // (pairs, parts, 2): dO, V
 };
-constexpr int kRangeMost = 16;     // shares at most
-constexpr int kRangeRows = 256;    // rows of a share at least
+constexpr int kRangeMost = 32;     // shares at most, one per lane of the warps that read them
+constexpr int kRangeRows = 64;     // rows of a share at least: two batches of loads at D = 64
 inline int range_parts(const AttnArgs &a) {
     return std::min((std::max(a.Lq, a.Lk) + kRangeRows - 1) / kRangeRows, kRangeMost);
 }
@@ -169,6 +169,7 @@ __device__ __forceinline__ void attn_range_block(const AttnArgs &a, const T *dO,
         const int chunk = (rows + range.parts - 1) / range.parts;
         const int end = min((part + 1) * chunk, rows);
         float most = 0.0f;
+#pragma unroll 4
         for (int r0 = part * chunk; r0 < end; r0 += 256 / G) {   // the same for all threads
             const int r = r0 + threadIdx.x / G;
             float sum = 0.0f;
