@@ -560,7 +560,15 @@ gs_status gs_attention_backward_workspace_size(const gs_attention_attrs *attrs, 
  *
  * s = scale * q . k + table[bucket][h];  O = softmax(s) V.  A row whose mask
  * leaves no key gives O = 0 and LSE = -inf.  A row of finite entries as low as
- * the type allows is an ordinary softmax.
+ * the type allows is an ordinary softmax.  Scores are held in base 2 in fp32: a
+ * finite table entry beyond +-2.35e38 counts as that, in O and in LSE.
+ *
+ * LSE is one fp32 number, and the weights that the backward pass forms from it
+ * are as good as its spacing: to 2^-9 where it is near -1e4, to one half near
+ * -1e6.  In a row whose scores are all of the size of -1e9 and below, where it
+ * holds nothing of their number, the largest scores have the weight 1 each, not
+ * 1 / count.  Where the gradients of such rows matter, mask the pairs by an entry
+ * of -inf or a bucket outside the table, whose rows have none.
  */
 gs_status gs_attention(const void *Q, const void *K, const void *V, const void *table,
                        const int32_t *buckets, const int32_t *k_len,

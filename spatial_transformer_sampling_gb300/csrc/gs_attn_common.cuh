@@ -40,6 +40,26 @@ __device__ __forceinline__ float bias2(float b) {
     const float f = b * kLog2e;
     return isinf(f) && !isinf(b) ? copysignf(3.4028234e38f, b) : f;
 }
+
+// A row's LSE in base 2, from which the backward pass subtracts its scores; a row
+// with no key: weights of 0.  The same steps as a table entry's: in a row of one
+// common entry, however large, the two cancel.
+__device__ __forceinline__ float lse2_of(float lse) { return lse == -INFINITY ? INFINITY : bias2(lse); }
+
+// A row's LSE from the reference `m` of its scores and the sum `l` of 2^(s - m),
+// 0 where there is no key.  From 2^20 on, where the spacing of t = m + log2 l is no
+// longer small beside 1, it is the lowest number with lse2_of(LSE) >= t: one step
+// lower, and the weights of the backward pass would be 2^128 for scores of -1e9.
+__device__ __forceinline__ float lse_of(float m, float l) {
+    if (l == 0.0f) return -INFINITY;
+    const float t = m + log2f(l);
+    float v = t * kLn2;
+    if (!(fabsf(t) >= 1048576.0f)) return v;
+    for (int k = 0; k < 2 && lse2_of(v) >= t; ++k) v = nextafterf(v, -INFINITY);
+    for (int k = 0; k < 4 && lse2_of(v) < t; ++k) v = nextafterf(v, INFINITY);
+    return v;
+}
+
 template <typename T>
 __device__ __forceinline__ float bias2_of(const T *table, int bucket, int nb, int H, int h) {
     if ((unsigned)bucket >= (unsigned)nb) return -INFINITY;

@@ -269,8 +269,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
             ((T *)p.O)[(((int64_t)n * a.Lq + i0 + x) * a.H + h) * a.D + d] =
                 IO<T>::st(l_all != 0.0f ? sum / l_all : 0.0f);
             if (d == 0 && p.lse)
-                p.lse[((int64_t)n * a.H + h) * a.Lq + i0 + x] =
-                    l_all != 0.0f ? (top + log2f(l_all)) * kLn2 : -INFINITY;
+                p.lse[((int64_t)n * a.H + h) * a.Lq + i0 + x] = lse_of(top, l_all);
         }
     }
     if (splits > 1) cluster.sync();   // shared memory stays until rank 0 has read it

@@ -231,7 +231,7 @@ __global__ void attn_delta_kernel(AttnArgs a, const T *dO, const T *O, const T *
     if (part == 0 && i < L64) {
         const int64_t nh = (int64_t)n * a.H + h;
         const float v = i < a.Lq ? lse[nh * a.Lq + i] : -INFINITY;
-        lse2[nh * L64 + i] = v == -INFINITY ? INFINITY : v * kLog2e;   // no key: weights of 0
+        lse2[nh * L64 + i] = lse2_of(v);
         delta[nh * L64 + i] = s;
     }
     // nothing here reads the expanded bias, but the kernels that wait for this

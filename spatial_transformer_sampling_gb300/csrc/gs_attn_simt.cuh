@@ -318,8 +318,7 @@ __global__ void __launch_bounds__(kSimtThreads, NC == 1 ? 3 : 2)
             const int64_t at_row = (int64_t)n * a.Lq + i0 + row;
             ((T *)p.O)[(at_row * a.H + h) * D + d] = IO<T>::st(sum != 0.0f ? v / sum : 0.0f);
             if (d == 0 && p.lse)
-                p.lse[((int64_t)n * a.H + h) * a.Lq + i0 + row] =
-                    sum != 0.0f ? (top + log2f(sum)) * kLn2 : -INFINITY;
+                p.lse[((int64_t)n * a.H + h) * a.Lq + i0 + row] = lse_of(top, sum);
         }
         cluster.sync();   // shared memory stays until the others have read it
         return;
@@ -339,8 +338,7 @@ __global__ void __launch_bounds__(kSimtThreads, NC == 1 ? 3 : 2)
                 if (c * 64 + me.col + j < D)
                     out[c * 64 + me.col + j] = IO<T>::st(at(o[c], i, j) * f);
         if (me.col == 0 && p.lse)
-            p.lse[((int64_t)n * a.H + h) * a.Lq + row] =
-                sum != 0.0f ? (m[i] + log2f(sum)) * kLn2 : -INFINITY;
+            p.lse[((int64_t)n * a.H + h) * a.Lq + row] = lse_of(m[i], sum);
     }
 }
 

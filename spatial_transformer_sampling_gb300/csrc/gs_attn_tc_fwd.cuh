@@ -325,8 +325,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                 }
             }
             if (part == 0 && i < a.Lq && p.lse)
-                p.lse[((int64_t)n * a.H + h) * a.Lq + i] =
-                    l != 0.0f ? (m - kWeightShift<T> + log2f(l)) * kLn2 : -INFINITY;
+                p.lse[((int64_t)n * a.H + h) * a.Lq + i] = lse_of(m - kWeightShift<T>, l);
         };
         // The item before the current one, whose product ends while the first tile
         // of the current one is worked on.
@@ -528,8 +527,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
             for (int e = 0; e < 4; ++e) u[e] = pack2<T>(o[2 * e] * inv, o[2 * e + 1] * inv);
             *reinterpret_cast<uint4 *>((T *)p.O + (((int64_t)w.n * a.Lq + i) * a.H + w.h) * a.D + d) = v;
             if (d == 0 && p.lse)
-                p.lse[((int64_t)w.n * a.H + w.h) * a.Lq + i] =
-                    l != 0.0f ? (m - kWeightShift<T> + log2f(l)) * kLn2 : -INFINITY;
+                p.lse[((int64_t)w.n * a.H + w.h) * a.Lq + i] = lse_of(m - kWeightShift<T>, l);
         }
         cluster.sync();   // shared memory stays until the others have read it
     }
