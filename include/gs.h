@@ -432,7 +432,7 @@ gs_status gs_resize(const void *X, int rank, const int64_t *x_shape, const int64
  *
  * mean = sum x / D, var = sum (x - mean)^2 / D (two passes over the row, held
  * on chip up to D = 8192), InvStdDev = 1 / sqrt(var + epsilon),
- * Y = (x - mean) * InvStdDev * Scale + B.
+ * Y = (x - mean) * InvStdDev * Scale + B.  With D = 0 nothing is written.
  */
 gs_status gs_layer_norm(const void *X, const void *Scale, const void *B, int64_t rows, int64_t D,
                         gs_dtype dt, float epsilon, void *Y, float *Mean, float *InvStdDev,

@@ -94,7 +94,7 @@ def _norm_dims(shape, axis):
 def gs_layer_norm(X, Scale, B=None, axis=-1, epsilon=1e-5, out=None):
     """LayerNormalization of X over its axes from ``axis`` on: (Y, Mean, InvStdDev).  Scale and B
     have the shape of the normalised axes; Mean and InvStdDev are float32 with X's leading axes
-    and ones in the place of the normalised ones."""
+    and ones in the place of the normalised ones (NaN where those hold no element)."""
     rows, D, inner, kept = _norm_dims(X.shape, operator.index(axis))
     _check_input(X)
     _check_like(X, "Scale", Scale, inner)
@@ -113,6 +113,9 @@ def gs_layer_norm(X, Scale, B=None, axis=-1, epsilon=1e-5, out=None):
                                  h.stream(device.index))
     if status:
         raise GsError(status, "gs_layer_norm")
+    if D == 0:   # the call writes nothing; the mean of no element
+        mean.fill_(float("nan"))
+        inv.fill_(float("nan"))
     return out, mean, inv
 
 
