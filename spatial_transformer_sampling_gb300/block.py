@@ -200,6 +200,8 @@ def _attention_attrs(Q, K, V, table, q_extent, k_extent, scale):
         if t.stride(3) != 1 and t.shape[3] != 1:
             raise ValueError(f"the last axis of {what} must be contiguous")
     N, Lq, H, D = Q.shape
+    if D == 0:
+        raise ValueError(f"heads of width 0: Q is {tuple(Q.shape)}")
     Lk = K.shape[1]
     if K.shape != (N, Lk, H, D):
         _shape_error("K", K.shape, (N, Lk, H, D))

@@ -42,6 +42,12 @@ def test_axis_given_as_a_tensor_is_read_at_every_call():
     assert block._norm_dims.cache_info().currsize == before
 
 
+def test_heads_of_width_zero_are_refused():
+    t = torch.zeros((2, 6, 3, 0))
+    with pytest.raises(ValueError, match="width 0"):
+        gs.gs_attention(t, t, t)
+
+
 @pytest.mark.gpu
 def test_results_follow_a_scale_that_changes_in_place(gs_cuda):
     g = torch.Generator(device="cuda")
