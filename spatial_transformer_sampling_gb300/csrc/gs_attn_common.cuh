@@ -46,18 +46,21 @@ __device__ __forceinline__ float bias2(float b) {
 // common entry, however large, the two cancel.
 __device__ __forceinline__ float lse2_of(float lse) { return lse == -INFINITY ? INFINITY : bias2(lse); }
 
+// A row's LSE from t = m + log2 l where the spacing of t is no longer small beside
+// 1: the lowest number with lse2_of(LSE) >= t, one step from t / log2 e at most.  One
+// lower, and the weights of the backward pass would be 2^128 and more for scores of
+// -1e9.  Out of the kernels' way: in place it took 2 us more over 1024 windows of
+// 8 x 8 (47 us).
+static __device__ __noinline__ float lse_of_far(float t) {
+    const float v = t * kLn2, lower = nextafterf(v, -INFINITY);
+    return lse2_of(lower) >= t ? lower : lse2_of(v) < t ? nextafterf(v, INFINITY) : v;
+}
+
 // A row's LSE from the reference `m` of its scores and the sum `l` of 2^(s - m),
-// 0 where there is no key.  From 2^20 on, where the spacing of t = m + log2 l is no
-// longer small beside 1, it is the lowest number with lse2_of(LSE) >= t: one step
-// lower, and the weights of the backward pass would be 2^128 for scores of -1e9.
+// 0 where there is no key.
 __device__ __forceinline__ float lse_of(float m, float l) {
-    if (l == 0.0f) return -INFINITY;
-    const float t = m + log2f(l);
-    float v = t * kLn2;
-    if (!(fabsf(t) >= 1048576.0f)) return v;
-    for (int k = 0; k < 2 && lse2_of(v) >= t; ++k) v = nextafterf(v, -INFINITY);
-    for (int k = 0; k < 4 && lse2_of(v) < t; ++k) v = nextafterf(v, INFINITY);
-    return v;
+    const float t = l != 0.0f ? m + log2f(l) : -INFINITY;
+    return fabsf(t) >= 1048576.0f && !isinf(t) ? lse_of_far(t) : t * kLn2;
 }
 
 template <typename T>
