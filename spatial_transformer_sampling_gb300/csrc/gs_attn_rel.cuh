@@ -255,12 +255,14 @@ cudaError_t launch_attn_delta(const AttnArgs &a, const AttnPtrs &p, float *lse2,
                        lse2, delta, range);
 }
 
-// Where group `w` of 32 queries, whose lowest relative index on its side is `lo`,
-// keeps relative index 0, in floats from the start of its (batch, head) pair's
-// sums: 64 bits, since 512 groups of a stride of 2^22 (16384 queries over 4 M
-// keys) are 2^31.  k_end: rel_k of the last key.
-__host__ __device__ inline int64_t rel_entry_0(int w, int stride, int k_end, int lo) {
-    return (int64_t)w * stride + k_end - lo;
+// Groups of 32 queries whose sums attn_rel_sum_kernel goes through at a time: as
+// many as threads, fewer where their offsets from the first one, `stride` floats a
+// group, would not fit 32 bits beside two relative indices (which stay below 2^25).
+// 512 groups of 16384 queries over 4 M keys would be 2^31.
+constexpr int kRelSumThreads = 512;
+__host__ __device__ inline int rel_groups_at_once(int stride) {
+    const int most = (1 << 30) / stride;
+    return most < kRelSumThreads ? most : kRelSumThreads;
 }
 
 // rel[h][r] (+)= the sums of groups of 32 queries; `heads` (batch, head) pairs
@@ -268,13 +270,14 @@ __host__ __device__ inline int64_t rel_entry_0(int w, int stride, int k_end, int
 // warps take every sixteenth (item, group) pair and are joined in order.  Bound by
 // the latency of the loads: 8 x 8 heads of 32 x 32 tokens (16 MB, in L2) take 8.9 us,
 // 16.5 with eight warps and 11.3 with 32, which fewer SMs hold at a time.
-constexpr int kRelSumIndices = 128, kRelSumThreads = 512;
+constexpr int kRelSumIndices = 128;
 static __global__ void __launch_bounds__(kRelSumThreads)
     attn_rel_sum_kernel(AttnArgs a, RelArgs p, int heads, float *rel) {
     constexpr int kSlices = kRelSumThreads / 32, kChunk = kRelSumThreads, kEach = kRelSumIndices / 32;
-    // per group of queries: its lowest and highest relative index; per item: the start
-    // of its sums, and how far the relative indices reach below a group's lowest one
-    __shared__ int s_lo[kChunk], s_hi[kChunk], s_low[kChunk];
+    // per group of queries: its lowest and highest relative index, and where its
+    // entry 0 lies from the first group's sums; per item: those of the first group, and
+    // how far the relative indices reach below a group's lowest one
+    __shared__ int s_lo[kChunk], s_hi[kChunk], s_at[kChunk], s_low[kChunk];
     __shared__ const float *s_item[kChunk];
     __shared__ float s_sum[kSlices][kRelSumIndices];
     const int lane = threadIdx.x % 32, slice = threadIdx.x / 32;
@@ -282,26 +285,28 @@ static __global__ void __launch_bounds__(kRelSumThreads)
     const int groups = (a.Lq + 31) / 32, k_end = rel_k(a, a.Lk - 1);
     const int nh0 = p.head0 + (h - p.head0 % a.H + a.H) % a.H;   // this head's first pair
     const int items = nh0 < p.head0 + heads ? (p.head0 + heads - 1 - nh0) / a.H + 1 : 0;
+    const int at_once = rel_groups_at_once(p.stride);
     float sum[kEach] = {};
     wait_for_previous_kernel(p.part, rel);
     for (int n0 = 0; n0 < items; n0 += kChunk)
-        for (int w0 = 0; w0 < groups; w0 += kChunk) {
-            const int w_mine = min(w0 + (int)threadIdx.x, groups - 1);
+        for (int w0 = 0; w0 < groups; w0 += at_once) {
+            const int w_mine = min(w0 + min((int)threadIdx.x, at_once - 1), groups - 1);
             const int nh = nh0 + min(n0 + (int)threadIdx.x, items - 1) * a.H;
             const int keys = keys_of(a, nh / a.H);
             __syncthreads();
             s_lo[threadIdx.x] = rel_q(a, w_mine * 32);
             s_hi[threadIdx.x] = rel_q(a, min(w_mine * 32 + 31, a.Lq - 1));
-            s_item[threadIdx.x] = p.part + (int64_t)(nh - p.head0) * groups * p.stride;
+            s_at[threadIdx.x] = (w_mine - w0) * p.stride + k_end - s_lo[threadIdx.x];
+            s_item[threadIdx.x] = p.part + ((int64_t)(nh - p.head0) * groups + w0) * p.stride;
             s_low[threadIdx.x] = keys > 0 ? rel_k(a, keys - 1) : INT_MIN / 2;
             __syncthreads();
-            const int nw = min(kChunk, groups - w0), nn = min(kChunk, items - n0);
+            const int nw = min(at_once, groups - w0), nn = min(kChunk, items - n0);
             int i = slice / nw, w = slice % nw;
             const int di = kSlices / nw, dw = kSlices % nw;
 #pragma unroll 4
             for (int k = slice; k < nn * nw; k += kSlices) {
                 const int hi = s_hi[w], lo = s_lo[w] - s_low[i];
-                const float *at = s_item[i] + rel_entry_0(w0 + w, p.stride, k_end, s_lo[w]) + r;
+                const float *at = s_item[i] + s_at[w] + r;
 #pragma unroll
                 for (int q = 0; q < kEach; ++q)
                     if (r + 32 * q <= hi && r + 32 * q >= lo) sum[q] += __ldg(at + 32 * q);

@@ -31,7 +31,6 @@ int main() {
     int D, g[4];
     while (scanf("%31s %d %d %d %d %d", what, &D, g, g + 1, g + 2, g + 3) == 6) {
         const AttnArgs a = args(1, 1, D, g[0], g[1], g[2], g[3]);
-        const int k_end = (a.Hk - 1) * a.P + a.Wk - 1;
         long long v = -1;
         if (!strcmp(what, "stride")) v = rel_stride_of(a);
         if (!strcmp(what, "window")) v = rel_window_of(a);
@@ -49,9 +48,7 @@ int main() {
                               TcFwdShape<128, kFwdMany>::kStages * q.count * 4;
         if (!strcmp(what, "simt_smem"))
             v = std::max({simt_fwd_smem(D), simt_bwd_smem(D, true, 0), simt_bwd_smem(D, false, rel_window_of(a))});
-        if (!strcmp(what, "last_entry")) {   // of the 512th group of queries
-            v = rel_entry_0(511, (int)rel_stride_of(a), k_end, (a.Hk - 1) * a.P + a.Wk - 1);
-        }
+        if (!strcmp(what, "groups")) v = rel_groups_at_once((int)rel_stride_of(a));
         printf("%lld\n", v);
     }
 }
@@ -77,13 +74,18 @@ def geometry(tmp_path_factory):
     return ask
 
 
-def test_offsets_of_the_bias_gradients_sums_keep_64_bits(geometry):
-    # 512 groups of 32 queries over as many keys as the relative indices allow (2^24)
+def test_offsets_of_the_bias_gradients_sums_fit_32_bits(geometry):
+    # 512 groups of 32 queries over as many keys as the relative indices allow (2^24): the offset
+    # of a group, with the last key's relative index and the entry's own beside it
     cases = [(64, (1, 16384), (1, 4_300_000)), (64, (1, 16384), (1, (1 << 24) - 16383)),
-             (64, (2, 8192), (1, 4_190_000))]
-    strides = geometry("stride", cases)
-    assert max(511 * s for s in strides) > 1 << 31
-    assert geometry("last_entry", cases) == [511 * s for s in strides]
+             (64, (2, 8192), (1, 4_190_000)), (64, (1, 9), (4000, 4000)), (64, (32, 32), (32, 32)),
+             (64, (1, 1), (1, 1)), (64, (4000, 4000), (1, 1))]
+    strides, groups = geometry("stride", cases), geometry("groups", cases)
+    assert max(511 * s for s in strides) > 1 << 31 and groups[0] < 512
+    for (_, q, k), s, n in zip(cases, strides, groups):
+        entries = (q[0] + k[0] - 1) * (q[1] + k[1] - 1)
+        assert 1 <= n <= 512 and (n - 1) * s + 2 * entries < 1 << 31
+    assert groups[4] == 512
 
 
 def _widest_use_of_the_window(q, k):
