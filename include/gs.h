@@ -412,9 +412,20 @@ gs_status gs_resize(const void *X, int rank, const int64_t *x_shape, const int64
  * Operators of a transformer block over sampled tokens.  A sampled map or
  * glimpse is a grid of tokens; these calls normalise them, let them attend to
  * one another with a learned bias by relative grid position, and drop and sum
- * the branch, each with its gradient.  Sums, statistics and softmax run in
- * fp32 and are rounded once, at the store.  No sum depends on the order in
- * which threads finish: a call repeated on the same inputs gives the same bits.
+ * the branch, each with its gradient.  Sums, statistics, running maxima and
+ * accumulators are fp32.  No sum depends on the order in which threads finish: a
+ * call repeated on the same inputs gives the same bits.
+ *
+ * Layer norm and dropout round once, at the store, and so does attention in fp32,
+ * in 16-bit types whose rows are not multiples of 16 bytes, and forward for up to
+ * eight queries.  Elsewhere the tensor cores take fp16 and bf16, and the factors
+ * of the second products are rounded to the type as well: the softmax weights
+ * (forward, and for dV) and their gradients dS (for dQ and dK), half a step of the
+ * type on every term.  Results are then off by 2.0e-3 to 2.4e-3 of their size in
+ * bf16 and by 3e-4 in fp16, where the store alone is 1.7e-3 and 2e-4.  In fp16 the
+ * weights are scaled by a power of two, and dS by one that the largest rows of dO
+ * and V allow, so that neither leaves the type's range.  Attention's exponential
+ * is the hardware's (ex2.approx.ftz), in fp32 too.
  * ---------------------------------------------------------------------------
  */
 
@@ -474,7 +485,7 @@ gs_status gs_layer_norm_backward(const void *dY, const void *X, const void *Scal
  *
  * Element i draws word i % 4 of Philox4x32-10 (Salmon et al., SC 2011) with
  * key `seed` and counter (i / 4, offset), low words first, and is kept when
- * word >= round(ratio * 2^32).  The mask is a function of these numbers alone
+ * word >= round(ratio * 2^32), 2^32 - 1 at most.  The mask is a function of these numbers alone
  * and is stored nowhere.  The gradient with respect to X is the same call on
  * dY (no residual) with the same ratio, seed and offset; the gradient with
  * respect to the residual is dY.
@@ -517,9 +528,12 @@ typedef struct {
  *              first half): per axis, half of the buckets belong to keys at or
  *              before the query (offset query - key >= 0) and half to keys
  *              after it; in each, the first half hold one distance each and
- *              the rest grow by a constant ratio up to max_distance, from which
- *              on the last one is taken: with m = num_buckets / 2 and e = m / 2,
- *              bucket e + k starts at distance ceil(e * (max_distance / e)^(k / (m - e))).
+ *              the rest grow by a constant ratio: with m = num_buckets / 2 and
+ *              e = m / 2, bucket e + k starts at distance
+ *              ceil(e * (max_distance / e)^(k / (m - e))).  The last of them,
+ *              k = m - e - 1, takes every distance from its start on;
+ *              max_distance is where one more would start (16 buckets and a
+ *              max_distance of 64: the last holds 32 and up).
  *              An axis on which both grids have extent 1 takes no part; with
  *              two axes the bucket is by * num_buckets + bx.
  *   max_distance  > num_buckets / 4.
@@ -548,9 +562,13 @@ gs_status gs_attention_backward_workspace_size(const gs_attention_attrs *attrs, 
  *             (yq - yk + Hk-1, xq - xk + Wk-1) names the pair's row of the
  *             table.  A value outside [0, num_buckets) masks the pair, and so
  *             does a table entry of -inf (causal and local attention are
- *             bucket maps).
+ *             bucket maps).  A masked pair has the weight 0, but its K and V
+ *             are read: what is not finite there may make the row NaN.
  *   k_len     device, (N) int32, or NULL: keys from k_len[n] on are masked
  *             (clamped to [0, Lk]); what K and V hold there is never used.
+ *             The items share the map, and with it the queries' place among
+ *             the keys: a new token that stands at the end of its own item's
+ *             keys takes a call per item where items end at different lengths.
  *   workspace device, 256-byte aligned (GS_ERR_ALIGN), at least the size
  *             gs_attention_workspace_size reports (GS_ERR_NULL for none,
  *             GS_ERR_SHAPE for less).

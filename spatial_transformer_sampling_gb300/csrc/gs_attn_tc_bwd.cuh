@@ -9,8 +9,9 @@
 //   S  = R1 C1^T,  dP = R2 C2^T             tcgen05.mma, fp32 in TMEM
 //   p  = 2^(c S + bias - lse),  ds = p (dP - delta)   two threads per row
 //   acc1 += ds C1  (dK or dQ),  acc2 += p C2  (dV)    tcgen05.mma
-// p and ds are rounded to the 16-bit type and read back from TMEM, where they
-// overwrite dP; S is free as soon as it is loaded, so the next step's S is
+// p and ds are rounded to the 16-bit type (both operands of the matrix instruction
+// have one; 2.4e-3 of a gradient in bf16 with the store's 1.7e-3) and read back from
+// TMEM, where they overwrite dP; S is free as soon as it is loaded, so the next step's S is
 // computed while the softmax warps work.  The scores are computed in both
 // kinds (7 products instead of 5): the alternative, dQ summed across CTAs,
 // needs fp32 atomics, whose order would change the result.
