@@ -598,7 +598,8 @@ gs_status gs_attention(const void *Q, const void *K, const void *V, const void *
  *
  *   dO, O     device, (N, Lq, H, D).       LSE  device, (N, H, Lq) fp32.
  *   dQ, dK, dV  device outputs, dense (N, Lq | Lk, H, D).  Rows of masked keys
- *             and of queries with no key are zero.
+ *             and of queries with no key are zero.  dO is read in every row: one
+ *             that is not finite reaches dK and dV, and dQ's row, with no key too.
  *   dTable    device output, (num_buckets, H) of `dt`; NULL without a table.
  *   Other arguments as gs_attention; the workspace's size is
  *   gs_attention_backward_workspace_size.
