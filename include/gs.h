@@ -1,8 +1,9 @@
 /*
  * gs.h -- C ABI of libgs, GB300 (sm_103a) kernels for spatial-transformer
  * sampling: AffineGrid, GridSample, the two fused, and DeformConv; and for the
- * transformer block over the sampled tokens: layer norm, dropout and attention
- * with a relative position bias, with their gradients.
+ * transformer block over the sampled tokens: layer norm, dropout, attention with a
+ * relative position bias, the gated projections of a feed-forward half and the
+ * norms around a gated branch, with their gradients.
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -614,6 +615,144 @@ gs_status gs_attention_backward(const void *dO, const void *Q, const void *K, co
                                 const gs_attention_attrs *attrs, gs_dtype dt, void *workspace,
                                 size_t workspace_bytes, void *dQ, void *dK, void *dV,
                                 void *dTable, cudaStream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * The feed-forward half of the block: its gated projections, and the norms on both
+ * sides of a branch with the branch's gate and the scaled residual sum.
+ * ---------------------------------------------------------------------------
+ */
+
+/* Activation of the gated projections: g / (1 + e^-g); g Phi(g) with the normal
+ * distribution's Phi; its tanh form 0.5 g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3)));
+ * max(g, 0); 1 / (1 + e^-g); g. */
+typedef enum {
+    GS_ACT_SILU = 0, GS_ACT_GELU = 1, GS_ACT_GELU_TANH = 2, GS_ACT_RELU = 3, GS_ACT_SIGMOID = 4,
+    GS_ACT_IDENTITY = 5
+} gs_activation;
+
+/* Device workspace gs_gated_linear and gs_gated_linear_backward need (host output
+ * `bytes`; 0: none), with or without biases. */
+gs_status gs_gated_linear_workspace_size(int64_t rows, int64_t D, int64_t F, gs_dtype dt,
+                                         size_t *bytes);
+gs_status gs_gated_linear_backward_workspace_size(int64_t rows, int64_t D, int64_t F, gs_dtype dt,
+                                                  size_t *bytes);
+
+/*
+ * gs_gated_linear -- both projections of a gated feed-forward block, the activation
+ * and the product: G = X Wg^T + bg, U = X Wu^T + bu, H = act(G) * U.
+ *
+ *   X         device, (rows, D).
+ *   Wg, Wu    device, (F, D): an output's weights are contiguous.
+ *   bg, bu    device, (F), or both NULL.
+ *   rows      < 2^31.      D, F  1 <= D <= 2^20, F <= 2^20; rows * D and rows * F
+ *             <= 2^40.
+ *   workspace device, 256-byte aligned (GS_ERR_ALIGN), at least the size
+ *             gs_gated_linear_workspace_size reports (GS_ERR_NULL for none,
+ *             GS_ERR_SHAPE for less).
+ *   H         device output, (rows, F).
+ *   G, U      device outputs, (rows, F), both or neither: what the backward pass
+ *             takes.
+ *
+ * The sums over D are fp32; G, U and H are each rounded once, at the store, and H
+ * is formed of the unrounded G and U.
+ */
+gs_status gs_gated_linear(const void *X, const void *Wg, const void *Wu, const void *bg,
+                          const void *bu, int64_t rows, int64_t D, int64_t F, gs_activation act,
+                          gs_dtype dt, void *workspace, size_t workspace_bytes, void *H, void *G,
+                          void *U, cudaStream_t stream);
+
+/*
+ * gs_gated_linear_backward -- the gradient of gs_gated_linear.
+ *
+ *   dH, G, U  device, (rows, F).
+ *   dX        device output, (rows, D).      dWg, dWu  device outputs, (F, D).
+ *   dbg, dbu  device outputs, (F), or both NULL.
+ *   Other arguments as gs_gated_linear; the workspace's size is
+ *   gs_gated_linear_backward_workspace_size.
+ *
+ * dG = dH * U * act'(G), dU = dH * act(G); dX = dG Wg + dU Wu; dWg = dG^T X,
+ * dWu = dU^T X; dbg and dbu are the sums of dG and dU over the rows.  relu's slope
+ * at 0 is 0.  In 16-bit types dG and dU are rounded to the type as factors of the
+ * products (half a step on every term); the biases' sums take them unrounded.  With
+ * rows = 0 the gradients of the weights and biases are zeros.
+ */
+gs_status gs_gated_linear_backward(const void *dH, const void *X, const void *Wg, const void *Wu,
+                                   const void *G, const void *U, int64_t rows, int64_t D,
+                                   int64_t F, gs_activation act, gs_dtype dt, void *workspace,
+                                   size_t workspace_bytes, void *dX, void *dWg, void *dWu,
+                                   void *dbg, void *dbu, cudaStream_t stream);
+
+/* The norms of gs_residual_norm: (x - mean) / sqrt(var + epsilon), or
+ * x / sqrt(mean(x^2) + epsilon). */
+typedef enum { GS_NORM_LAYER = 0, GS_NORM_RMS = 1 } gs_norm_kind;
+
+/*
+ * Shapes of gs_residual_norm.
+ *   rows    < 2^31.      D  <= 2^20.
+ *   groups  rows of the gate, or 0 without one; it divides `rows`.  rows / groups
+ *           consecutive rows share one: 1 is a gate per channel, the batch's items a
+ *           gate for each, `rows` one for every row.
+ *   kind    of both norms.
+ *   alpha   factor of the residual, finite.     epsilon  >= 0.
+ */
+typedef struct {
+    int64_t rows, D, groups;
+    gs_norm_kind kind;
+    float alpha, epsilon;
+} gs_residual_norm_attrs;
+
+/*
+ * gs_residual_norm -- the norm after a branch, its gate, the scaled residual sum and
+ * the norm before the next branch, in one pass:
+ *   z' = norm(Z) * z_scale + z_B, or Z without z_scale,
+ *   S = alpha * X + gate * z',   Y = norm(S) * Scale + B.
+ *
+ *   X, Z      device, (rows, D): the residual and the branch's output.
+ *   gate      device, (groups, D), or NULL with groups = 0 (a factor of 1).
+ *   z_scale   device, (D), or NULL for no norm of Z.
+ *   z_B, B    device, (D), or NULL for zeros; z_B needs z_scale (GS_ERR_NULL).
+ *   Scale     device, (D).
+ *   S, Y      device outputs, (rows, D).  Y is formed of the unrounded S.
+ *   Stats     device output, (rows, 4) fp32, 16-byte aligned, or NULL: the mean and
+ *             the reciprocal deviation of Z (0 and 1 without z_scale) and those of S
+ *             (means are 0 for GS_NORM_RMS).  The backward pass takes them.
+ */
+gs_status gs_residual_norm(const void *X, const void *Z, const void *gate, const void *z_scale,
+                           const void *z_B, const void *Scale, const void *B,
+                           const gs_residual_norm_attrs *attrs, gs_dtype dt, void *S, void *Y,
+                           float *Stats, cudaStream_t stream);
+
+/* Device workspace gs_residual_norm_backward needs (host output `bytes`). */
+gs_status gs_residual_norm_backward_workspace_size(const gs_residual_norm_attrs *attrs,
+                                                   gs_dtype dt, size_t *bytes);
+
+/*
+ * gs_residual_norm_backward -- the gradient of gs_residual_norm.
+ *
+ *   dS        device, (rows, D), or NULL for zeros: what reaches S otherwise.
+ *   dY        device, (rows, D).
+ *   S, Stats  the forward pass's.
+ *   dX, dZ    device outputs, (rows, D).
+ *   dgate     device output, (groups, D); NULL without a gate.
+ *   dz_scale, dz_B, dScale, dB  device outputs, (D), each or all NULL; dz_scale and
+ *             dz_B need z_scale.  With rows = 0 they are written as zeros.
+ *   workspace device, 256-byte aligned, at least the size
+ *             gs_residual_norm_backward_workspace_size reports.
+ *
+ * With N(w, x^, inv) = inv * (w - mean(w) - x^ * mean(w * x^)) (no mean(w) for
+ * GS_NORM_RMS), s^ and z^ the normalised S and Z:
+ * ds = dS + N(dY * Scale, s^, inv_s);  dX = alpha * ds;  dScale = sum dY * s^,
+ * dB = sum dY;  dgate = sum of ds * z' over the rows that share it;  e = gate * ds;
+ * dz_scale = sum e * z^, dz_B = sum e;  dZ = N(e * z_scale, z^, inv_z), or e.
+ */
+gs_status gs_residual_norm_backward(const void *dS, const void *dY, const void *S, const void *Z,
+                                    const float *Stats, const void *gate, const void *z_scale,
+                                    const void *z_B, const void *Scale,
+                                    const gs_residual_norm_attrs *attrs, gs_dtype dt,
+                                    void *workspace, size_t workspace_bytes, void *dX, void *dZ,
+                                    void *dgate, void *dz_scale, void *dz_B, void *dScale,
+                                    void *dB, cudaStream_t stream);
 
 /* Human-readable name of a status code (static storage). */
 const char *gs_status_str(gs_status s);

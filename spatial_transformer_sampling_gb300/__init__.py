@@ -15,6 +15,9 @@ Operators (see the docstrings and include/gs.h):
   gs_deform_conv   DeformConv 2-D
   gs_layer_norm, gs_dropout, gs_attention (and their gradients)
                    a transformer block over the sampled tokens (block.py)
+  gs_gated_linear, gs_residual_norm (and their gradients)
+                   its feed-forward half: gated projections, and the norms around
+                   a gated branch (feed_forward.py)
 
 Host-memory variants (gs_affine_sample_from_host, gs_grid_sample_from_host)
 stream a batch from pinned host memory in chunks, overlapping the copies in
@@ -27,7 +30,8 @@ __all__ = ["gs_affine_grid", "gs_grid_sample", "gs_affine_sample", "gs_deform_co
            "gs_status_str", "gs_device_status", "GsError", "library_path", "load_library",
            "EXPORTED_SYMBOLS", "HostStreamer", "gs_affine_sample_from_host",
            "gs_grid_sample_from_host", "gs_layer_norm", "gs_layer_norm_backward", "gs_dropout",
-           "gs_attention", "gs_attention_backward", "gs_relative_buckets"]
+           "gs_attention", "gs_attention_backward", "gs_relative_buckets", "gs_gated_linear",
+           "gs_gated_linear_backward", "gs_residual_norm", "gs_residual_norm_backward"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "_build", "libgs.so")
@@ -37,7 +41,8 @@ EXPORTED_SYMBOLS = ("gs_affine_grid", "gs_grid_sample", "gs_affine_sample",
                     "gs_resize", "gs_resize_output_shape", "gs_grid_sample_int", "gs_status_str",
                     "gs_device_status", "gs_layer_norm", "gs_layer_norm_backward", "gs_dropout",
                     "gs_relative_buckets", "gs_attention", "gs_attention_backward",
-                    "gs_version")
+                    "gs_gated_linear", "gs_gated_linear_backward", "gs_residual_norm",
+                    "gs_residual_norm_backward", "gs_version")
 
 MODES = {"linear": 0, "bilinear": 0, "nearest": 1, "cubic": 2, "bicubic": 2}
 PADS = {"zeros": 0, "border": 1, "reflection": 2}
@@ -81,6 +86,12 @@ class AttentionAttrs(ctypes.Structure):
                 ("q_strides", ctypes.c_int64 * 3), ("k_strides", ctypes.c_int64 * 3),
                 ("v_strides", ctypes.c_int64 * 3), ("num_buckets", ctypes.c_int64),
                 ("scale", ctypes.c_float)]
+
+
+class ResidualNormAttrs(ctypes.Structure):
+    """gs_residual_norm_attrs (include/gs.h)."""
+    _fields_ = [("rows", ctypes.c_int64), ("D", ctypes.c_int64), ("groups", ctypes.c_int64),
+                ("kind", ctypes.c_int), ("alpha", ctypes.c_float), ("epsilon", ctypes.c_float)]
 
 
 def library_path():
@@ -132,6 +143,14 @@ def load_library(path=None):
     L.gs_attention.argtypes = [vp, vp, vp, vp, vp, vp, atp, ci, vp, sz, vp, vp, vp]
     L.gs_attention_backward.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, atp, ci, vp, sz, vp, vp,
                                         vp, vp, vp]
+    rtp = ctypes.POINTER(ResidualNormAttrs)
+    L.gs_gated_linear_workspace_size.argtypes = [i64, i64, i64, ci, szp]
+    L.gs_gated_linear_backward_workspace_size.argtypes = [i64, i64, i64, ci, szp]
+    L.gs_gated_linear.argtypes = [vp] * 5 + [i64, i64, i64, ci, ci, vp, sz] + [vp] * 4
+    L.gs_gated_linear_backward.argtypes = [vp] * 6 + [i64, i64, i64, ci, ci, vp, sz] + [vp] * 6
+    L.gs_residual_norm.argtypes = [vp] * 7 + [rtp, ci] + [vp] * 4
+    L.gs_residual_norm_backward_workspace_size.argtypes = [rtp, ci, szp]
+    L.gs_residual_norm_backward.argtypes = [vp] * 9 + [rtp, ci, vp, sz] + [vp] * 8
     L.gs_status_str.argtypes = [ci]
     L.gs_status_str.restype = ctypes.c_char_p
     L.gs_device_status.argtypes = [vp]
@@ -145,7 +164,10 @@ def load_library(path=None):
               "gs_test_bounded_wait_expires", "gs_layer_norm",
               "gs_layer_norm_backward_workspace_size", "gs_layer_norm_backward", "gs_dropout",
               "gs_relative_buckets", "gs_attention_workspace_size",
-              "gs_attention_backward_workspace_size", "gs_attention", "gs_attention_backward"):
+              "gs_attention_backward_workspace_size", "gs_attention", "gs_attention_backward",
+              "gs_gated_linear_workspace_size", "gs_gated_linear_backward_workspace_size",
+              "gs_gated_linear", "gs_gated_linear_backward", "gs_residual_norm",
+              "gs_residual_norm_backward_workspace_size", "gs_residual_norm_backward"):
         getattr(L, f).restype = ci
     if path is None:
         _lib = L
@@ -676,3 +698,7 @@ from .block import (gs_attention, gs_attention_backward,  # noqa: E402
                     gs_attention_backward_workspace_size, gs_attention_workspace_size, gs_dropout,
                     gs_layer_norm, gs_layer_norm_backward,
                     gs_layer_norm_backward_workspace_size, gs_relative_buckets)
+from .feed_forward import (gs_gated_linear, gs_gated_linear_backward,  # noqa: E402
+                           gs_gated_linear_backward_workspace_size,
+                           gs_gated_linear_workspace_size, gs_residual_norm,
+                           gs_residual_norm_backward, gs_residual_norm_backward_workspace_size)

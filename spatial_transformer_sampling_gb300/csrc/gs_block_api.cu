@@ -5,6 +5,8 @@
 #include <cuda_fp16.h>
 #include <math.h>
 
+#include <initializer_list>
+
 #include "../../include/gs.h"
 #include "gs_internal.h"
 
@@ -146,6 +148,48 @@ int axis_bucket(int64_t offset, int num, int64_t far) {
         }
     }
     return b + (offset < 0 ? m : 0);
+}
+
+constexpr int64_t kMaxGatedWidth = int64_t(1) << 20;
+constexpr int64_t kMaxGatedElements = int64_t(1) << 40;
+
+gs_status check_gated(int64_t rows, int64_t D, int64_t F, int act, gs_dtype dt, gs::GatedArgs *a) {
+    if (!dtype_ok(dt)) return GS_ERR_DTYPE;
+    if (act < GS_ACT_SILU || act > GS_ACT_IDENTITY) return GS_ERR_ATTR;
+    if (rows < 0 || rows > kMax31 || D < 1 || D > kMaxGatedWidth || F < 0 || F > kMaxGatedWidth ||
+        !product_fits(rows, D, kMaxGatedElements) || !product_fits(rows, F, kMaxGatedElements))
+        return GS_ERR_SHAPE;
+    *a = {rows, (int)D, (int)F, act, nullptr};
+    return GS_OK;
+}
+
+size_t gated_ws(const gs::GatedArgs &a, gs_dtype dt, bool backward) {
+    return by_dtype(dt, [&](auto tag) { return gs::gated_ws_bytes<decltype(tag)>(a, backward); });
+}
+
+gs_status check_residual_norm(const gs_residual_norm_attrs *at, gs_dtype dt, gs::ResNormArgs *a) {
+    if (!at) return GS_ERR_NULL;
+    if (!dtype_ok(dt)) return GS_ERR_DTYPE;
+    if (at->kind != GS_NORM_LAYER && at->kind != GS_NORM_RMS) return GS_ERR_ATTR;
+    if (!isfinite(at->alpha) || !(at->epsilon >= 0.0f) || isinf(at->epsilon)) return GS_ERR_ATTR;
+    const gs_status st = check_norm(at->rows, at->D);
+    if (st != GS_OK) return st;
+    if (at->groups < 0 || (at->groups > 0 && at->rows % at->groups != 0) ||
+        at->groups > (at->rows > 0 ? at->rows : kMax31))
+        return GS_ERR_SHAPE;
+    a->rows = at->rows;
+    a->D = (int)at->D;
+    a->groups = (int)at->groups;
+    a->group_rows = at->groups > 0 ? at->rows / at->groups : at->rows;
+    a->layer = at->kind == GS_NORM_LAYER;
+    a->alpha = at->alpha;
+    a->eps = at->epsilon;
+    return GS_OK;
+}
+
+size_t residual_norm_ws(const gs::ResNormArgs &a, gs_dtype dt) {
+    if (a.rows == 0 || a.D == 0) return 0;
+    return by_dtype(dt, [&](auto tag) { return gs::resnorm_ws_bytes<decltype(tag)>(a); });
 }
 
 }  // namespace
@@ -349,6 +393,177 @@ gs_status gs_attention_backward(const void *dO, const void *Q, const void *K, co
                             dO, dQ, dK, dV,    dTable};
     return dispatch(dt, [&](auto tag) {
         return gs::launch_attn_backward<decltype(tag)>(a, p, workspace, stream);
+    });
+}
+
+gs_status gs_gated_linear_workspace_size(int64_t rows, int64_t D, int64_t F, gs_dtype dt,
+                                         size_t *bytes) {
+    if (!bytes) return GS_ERR_NULL;
+    *bytes = 0;
+    gs::GatedArgs a;
+    const gs_status st = check_gated(rows, D, F, GS_ACT_SILU, dt, &a);
+    if (st == GS_OK) *bytes = gated_ws(a, dt, false);
+    return st;
+}
+
+gs_status gs_gated_linear_backward_workspace_size(int64_t rows, int64_t D, int64_t F, gs_dtype dt,
+                                                  size_t *bytes) {
+    if (!bytes) return GS_ERR_NULL;
+    *bytes = 0;
+    gs::GatedArgs a;
+    const gs_status st = check_gated(rows, D, F, GS_ACT_SILU, dt, &a);
+    if (st == GS_OK) *bytes = gated_ws(a, dt, true);
+    return st;
+}
+
+gs_status gs_gated_linear(const void *X, const void *Wg, const void *Wu, const void *bg,
+                          const void *bu, int64_t rows, int64_t D, int64_t F, gs_activation act,
+                          gs_dtype dt, void *workspace, size_t workspace_bytes, void *H, void *G,
+                          void *U, cudaStream_t stream) {
+    gs::GatedArgs a;
+    gs_status st = check_gated(rows, D, F, act, dt, &a);
+    if (st != GS_OK) return st;
+    if (rows == 0 || F == 0) return GS_OK;
+    if (!X || !Wg || !Wu || !H || !bg != !bu || !G != !U) return GS_ERR_NULL;
+    const size_t es = elem_size(dt);
+    if (!aligned(X, es) || !aligned(Wg, es) || !aligned(Wu, es) || !aligned(bg, es) ||
+        !aligned(bu, es) || !aligned(H, es) || !aligned(G, es) || !aligned(U, es))
+        return GS_ERR_ALIGN;
+    st = check_workspace(workspace, workspace_bytes, gated_ws(a, dt, false), 256);
+    if (st != GS_OK) return st;
+    a.err = gs::device_error_word();
+    if (!a.err) return GS_ERR_CUDA;
+    gs::GatedPtrs p = {X, Wg, Wu, bg, bu, H, G, U};
+    return dispatch(dt, [&](auto tag) {
+        return gs::launch_gated<decltype(tag)>(a, p, workspace, stream);
+    });
+}
+
+gs_status gs_gated_linear_backward(const void *dH, const void *X, const void *Wg, const void *Wu,
+                                   const void *G, const void *U, int64_t rows, int64_t D,
+                                   int64_t F, gs_activation act, gs_dtype dt, void *workspace,
+                                   size_t workspace_bytes, void *dX, void *dWg, void *dWu,
+                                   void *dbg, void *dbu, cudaStream_t stream) {
+    gs::GatedArgs a;
+    gs_status st = check_gated(rows, D, F, act, dt, &a);
+    if (st != GS_OK) return st;
+    if (rows > 0 && (!X || !dX)) return GS_ERR_NULL;
+    if (F > 0 && (!Wg || !Wu || !dWg || !dWu)) return GS_ERR_NULL;
+    if (rows > 0 && F > 0 && (!dH || !G || !U)) return GS_ERR_NULL;
+    if (!dbg != !dbu) return GS_ERR_NULL;
+    const size_t es = elem_size(dt);
+    for (const void *q : {dH, X, Wg, Wu, G, U, (const void *)dX, (const void *)dWg,
+                          (const void *)dWu, (const void *)dbg, (const void *)dbu})
+        if (!aligned(q, es)) return GS_ERR_ALIGN;
+    if (rows == 0 || F == 0) {   // every gradient there is is zero
+        cudaError_t e = cudaSuccess;
+        const auto clear = [&](void *q, int64_t n) {
+            if (q && n > 0 && e == cudaSuccess) e = cudaMemsetAsync(q, 0, (size_t)n * es, stream);
+        };
+        clear(dX, rows * D);
+        clear(dWg, F * D);
+        clear(dWu, F * D);
+        clear(dbg, F);
+        clear(dbu, F);
+        return status_of(e);
+    }
+    st = check_workspace(workspace, workspace_bytes, gated_ws(a, dt, true), 256);
+    if (st != GS_OK) return st;
+    a.err = gs::device_error_word();
+    if (!a.err) return GS_ERR_CUDA;
+    gs::GatedPtrs p = {X,  Wg, Wu, nullptr, nullptr, nullptr, const_cast<void *>(G),
+                       const_cast<void *>(U), dH, dX, dWg, dWu, dbg, dbu};
+    return dispatch(dt, [&](auto tag) {
+        return gs::launch_gated_backward<decltype(tag)>(a, p, workspace, stream);
+    });
+}
+
+gs_status gs_residual_norm(const void *X, const void *Z, const void *gate, const void *z_scale,
+                           const void *z_B, const void *Scale, const void *B,
+                           const gs_residual_norm_attrs *attrs, gs_dtype dt, void *S, void *Y,
+                           float *Stats, cudaStream_t stream) {
+    gs::ResNormArgs a;
+    const gs_status st = check_residual_norm(attrs, dt, &a);
+    if (st != GS_OK) return st;
+    if (a.rows == 0 || a.D == 0) return GS_OK;
+    if (!X || !Z || !Scale || !S || !Y || (a.groups > 0 && !gate) || (z_B && !z_scale))
+        return GS_ERR_NULL;
+    if (a.groups == 0 && gate) return GS_ERR_SHAPE;
+    const size_t es = elem_size(dt);
+    for (const void *q : {X, Z, gate, z_scale, z_B, Scale, B, (const void *)S, (const void *)Y})
+        if (!aligned(q, es)) return GS_ERR_ALIGN;
+    if (!aligned(Stats, 16)) return GS_ERR_ALIGN;
+    gs::ResNormPtrs p = {};
+    p.gate = gate;
+    p.z_scale = z_scale;
+    p.z_B = z_B;
+    p.scale = Scale;
+    p.B = B;
+    p.X = X;
+    p.Z = Z;
+    p.S = S;
+    p.Y = Y;
+    p.stats = Stats;
+    return dispatch(dt, [&](auto tag) { return gs::launch_resnorm<decltype(tag)>(a, p, stream); });
+}
+
+gs_status gs_residual_norm_backward_workspace_size(const gs_residual_norm_attrs *attrs,
+                                                   gs_dtype dt, size_t *bytes) {
+    if (!bytes) return GS_ERR_NULL;
+    *bytes = 0;
+    gs::ResNormArgs a;
+    const gs_status st = check_residual_norm(attrs, dt, &a);
+    if (st == GS_OK) *bytes = residual_norm_ws(a, dt);
+    return st;
+}
+
+gs_status gs_residual_norm_backward(const void *dS, const void *dY, const void *S, const void *Z,
+                                    const float *Stats, const void *gate, const void *z_scale,
+                                    const void *z_B, const void *Scale,
+                                    const gs_residual_norm_attrs *attrs, gs_dtype dt,
+                                    void *workspace, size_t workspace_bytes, void *dX, void *dZ,
+                                    void *dgate, void *dz_scale, void *dz_B, void *dScale,
+                                    void *dB, cudaStream_t stream) {
+    gs::ResNormArgs a;
+    gs_status st = check_residual_norm(attrs, dt, &a);
+    if (st != GS_OK) return st;
+    if (a.D == 0) return GS_OK;
+    if (a.rows > 0 && (!dY || !S || !Z || !Stats || !Scale || !dX || !dZ)) return GS_ERR_NULL;
+    if (a.groups > 0 && ((a.rows > 0 && !gate) || !dgate)) return GS_ERR_NULL;
+    if (!z_scale && (z_B || dz_scale || dz_B)) return GS_ERR_NULL;
+    if (a.groups == 0 && (gate || dgate)) return GS_ERR_SHAPE;
+    const size_t es = elem_size(dt);
+    for (const void *q : {dS, dY, S, Z, gate, z_scale, z_B, Scale, (const void *)dX,
+                          (const void *)dZ, (const void *)dgate, (const void *)dz_scale,
+                          (const void *)dz_B, (const void *)dScale, (const void *)dB})
+        if (!aligned(q, es)) return GS_ERR_ALIGN;
+    if (!aligned(Stats, 16)) return GS_ERR_ALIGN;
+    st = check_workspace(workspace, workspace_bytes, residual_norm_ws(a, dt), 256);
+    if (st != GS_OK) return st;
+    if (a.rows == 0 && a.groups > 0) {   // gates of no row
+        const gs_status done = status_of(
+            cudaMemsetAsync(dgate, 0, (size_t)a.groups * a.D * es, stream));
+        if (done != GS_OK) return done;
+    }
+    gs::ResNormPtrs p = {};
+    p.gate = gate;
+    p.z_scale = z_scale;
+    p.z_B = z_B;
+    p.scale = Scale;
+    p.Z = Z;
+    p.S = const_cast<void *>(S);
+    p.stats = const_cast<float *>(Stats);
+    p.dS = dS;
+    p.dY = dY;
+    p.dX = dX;
+    p.dZ = dZ;
+    p.dgate = dgate;
+    p.dz_scale = dz_scale;
+    p.dz_B = dz_B;
+    p.dScale = dScale;
+    p.dB = dB;
+    return dispatch(dt, [&](auto tag) {
+        return gs::launch_resnorm_backward<decltype(tag)>(a, p, workspace, stream);
     });
 }
 

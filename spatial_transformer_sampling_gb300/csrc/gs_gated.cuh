@@ -1,0 +1,74 @@
+// gs_gated.cuh -- the gated projections of a feed-forward block:
+//   G = X Wg^T + bg, U = X Wu^T + bu, H = act(G) * U,
+// and their gradient from dH, G and U:
+//   dG = dH U act'(G), dU = dH act(G), dX = dG Wg + dU Wu, dWg = dG^T X, dWu = dU^T X.
+#pragma once
+
+#include "../../include/gs.h"
+#include "gs_attn_common.cuh"
+#include "gs_sums.cuh"
+
+namespace gs {
+
+// 1 / (1 + e^-x): two hardware approximations of 2 ulps each.
+__device__ __forceinline__ float sigmoid_of(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(1.0f + exp2_approx(-kLog2e * x)));
+    return y;
+}
+
+// The tanh form's argument, doubled: 0.5 (1 + tanh a) = sigmoid(2 a).
+constexpr float kGeluTanh2 = 1.5957691216057308f;   // 2 sqrt(2 / pi)
+constexpr float kGeluCubic = 0.044715f;
+
+template <int ACT> __device__ __forceinline__ float act_of(float g) {
+    if (ACT == GS_ACT_SILU) return g * sigmoid_of(g);
+    if (ACT == GS_ACT_GELU) return 0.5f * g * (1.0f + erff(g * 0.70710678118654752f));
+    if (ACT == GS_ACT_GELU_TANH) return g * sigmoid_of(kGeluTanh2 * g * fmaf(kGeluCubic * g, g, 1.0f));
+    if (ACT == GS_ACT_RELU) return g < 0.0f ? 0.0f : g;   // NaN stays
+    if (ACT == GS_ACT_SIGMOID) return sigmoid_of(g);
+    return g;
+}
+
+// act(g) and its slope.
+template <int ACT> __device__ __forceinline__ void act_and_slope(float g, float &a, float &da) {
+    if (ACT == GS_ACT_SILU) {
+        const float r = sigmoid_of(g);
+        a = g * r;
+        da = fmaf(a, 1.0f - r, r);
+    } else if (ACT == GS_ACT_GELU) {
+        const float phi = 0.5f * (1.0f + erff(g * 0.70710678118654752f));
+        a = g * phi;
+        da = fmaf(g * 0.3989422804014327f, exp2_approx(-0.5f * kLog2e * g * g), phi);
+    } else if (ACT == GS_ACT_GELU_TANH) {
+        const float r = sigmoid_of(kGeluTanh2 * g * fmaf(kGeluCubic * g, g, 1.0f));
+        a = g * r;
+        da = fmaf(a * (1.0f - r), kGeluTanh2 * fmaf(3.0f * kGeluCubic * g, g, 1.0f), r);
+    } else if (ACT == GS_ACT_RELU) {
+        a = g < 0.0f ? 0.0f : g;
+        da = g > 0.0f ? 1.0f : 0.0f;
+    } else if (ACT == GS_ACT_SIGMOID) {
+        a = sigmoid_of(g);
+        da = a * (1.0f - a);
+    } else {
+        a = g;
+        da = 1.0f;
+    }
+}
+
+// Calls f with the activation as a compile-time number.
+template <typename F> __device__ __forceinline__ void with_act(int act, F &&f) {
+    using std::integral_constant;
+    switch (act) {
+        case GS_ACT_SILU: f(integral_constant<int, GS_ACT_SILU>()); break;
+        case GS_ACT_GELU: f(integral_constant<int, GS_ACT_GELU>()); break;
+        case GS_ACT_GELU_TANH: f(integral_constant<int, GS_ACT_GELU_TANH>()); break;
+        case GS_ACT_RELU: f(integral_constant<int, GS_ACT_RELU>()); break;
+        case GS_ACT_SIGMOID: f(integral_constant<int, GS_ACT_SIGMOID>()); break;
+        default: f(integral_constant<int, GS_ACT_IDENTITY>()); break;
+    }
+}
+
+constexpr int kGatedSms = 152;
+
+}  // namespace gs

@@ -255,4 +255,48 @@ template <typename T>
 cudaError_t launch_attn_backward(const AttnArgs &args, const AttnPtrs &p, void *ws,
                                  cudaStream_t s);
 
+// Gated projections of a feed-forward block (gs_gated*.cu).
+struct GatedArgs {
+    int64_t rows;
+    int D, F;
+    int act;                            // gs_activation
+    unsigned *err;
+};
+struct GatedPtrs {                      // device pointers; forward: G and U are outputs
+    const void *X, *Wg, *Wu, *bg, *bu;
+    void *H, *G, *U;
+    const void *dH;
+    void *dX, *dWg, *dWu, *dbg, *dbu;
+};
+template <typename T> size_t gated_ws_bytes(const GatedArgs &args, bool backward);
+template <typename T>
+cudaError_t launch_gated(const GatedArgs &args, const GatedPtrs &p, void *ws, cudaStream_t s);
+template <typename T>
+cudaError_t launch_gated_backward(const GatedArgs &args, const GatedPtrs &p, void *ws,
+                                  cudaStream_t s);
+
+// Norms around a gated branch (gs_residual_norm.cuh).
+struct ResNormArgs {
+    int64_t rows;
+    int D;
+    int groups;                         // rows of the gate, 0 without one
+    int64_t group_rows;                 // rows that share one
+    int layer;                          // layer norms: means are subtracted
+    float alpha, eps;
+};
+struct ResNormPtrs {                    // device pointers
+    const void *gate, *z_scale, *z_B, *scale, *B;
+    const void *X, *Z;
+    void *S, *Y;
+    float *stats;
+    const void *dS, *dY;                // backward: S is an input, B unused
+    void *dX, *dZ, *dgate, *dz_scale, *dz_B, *dScale, *dB;
+};
+template <typename T> size_t resnorm_ws_bytes(const ResNormArgs &args);
+template <typename T>
+cudaError_t launch_resnorm(const ResNormArgs &args, const ResNormPtrs &p, cudaStream_t s);
+template <typename T>
+cudaError_t launch_resnorm_backward(const ResNormArgs &args, const ResNormPtrs &p, void *ws,
+                                    cudaStream_t s);
+
 }  // namespace gs
