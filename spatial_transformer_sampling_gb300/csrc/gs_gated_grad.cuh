@@ -11,6 +11,37 @@ namespace gs {
 // in registers until the end.
 constexpr int kGradThreads = 256, kGradWarps = kGradThreads / 32;
 
+// fp32 as three bf16 numbers, each the nearest to what the ones before leave: their
+// sum is x to 2^-24 of it or better.  What is not finite stays in the first.
+__device__ __forceinline__ void split3(float x, __nv_bfloat16 (&v)[3]) {
+    v[0] = __float2bfloat16_rn(x);
+    if (__hisinf(v[0])) v[0] = __float2bfloat16_rz(x);   // the largest numbers round to infinity
+    const float r = isfinite(x) ? x - __bfloat162float(v[0]) : 0.0f;
+    v[1] = __float2bfloat16_rn(r);
+    v[2] = __float2bfloat16_rn(r - __bfloat162float(v[1]));
+}
+
+// Stores a run where the products read it: rounded to the type, or, of fp32, in three
+// planes `plane` elements apart.
+template <typename T> using Factor = std::conditional_t<sizeof(T) == 4, __nv_bfloat16, T>;
+template <typename T, int V>
+__device__ __forceinline__ void store_factor(Factor<T> *to, int64_t plane, const float (&v)[V]) {
+    if constexpr (sizeof(T) == 4) {
+        struct alignas(V * 2) Part { __nv_bfloat16 e[V]; } part[3];
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            __nv_bfloat16 x[3];
+            split3(v[e], x);
+#pragma unroll
+            for (int i = 0; i < 3; ++i) part[i].e[e] = x[i];
+        }
+#pragma unroll
+        for (int i = 0; i < 3; ++i) *reinterpret_cast<Part *>(to + i * plane) = part[i];
+    } else {
+        Run<T, V>::store(to, v);
+    }
+}
+
 inline int gated_grad_col_blocks(int F, int V) { return (F + 32 * V - 1) / (32 * V); }
 // Row blocks: about four blocks of 256 threads per SM.
 inline int gated_grad_row_blocks(int64_t rows, int F, int V) {
@@ -19,11 +50,12 @@ inline int gated_grad_row_blocks(int64_t rows, int F, int V) {
     return (int)(need < most ? need : most);
 }
 
-// Into dG and dU (rows, pitch) and, with SUMS, partials[row block][2][F].
+// Into dG and dU (rows, pitch), planes of fp32 rows * pitch apart, and, with SUMS,
+// partials[row block][2][F].
 template <typename T, int V, bool SUMS, int ACT>
 __device__ __forceinline__ void gated_grad_rows(const GatedArgs &a, const T *dH, const T *G,
-                                                const T *U, T *dG, T *dU, int64_t pitch,
-                                                float *partials) {
+                                                const T *U, Factor<T> *dG, Factor<T> *dU,
+                                                int64_t pitch, float *partials) {
     using IOV = Run<T, V>;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int f = (blockIdx.x * 32 + lane) * V;
@@ -48,8 +80,8 @@ __device__ __forceinline__ void gated_grad_rows(const GatedArgs &a, const T *dH,
                     su[e] += u[e];
                 }
             }
-            IOV::store(dG + r * pitch + f, g);
-            IOV::store(dU + r * pitch + f, u);
+            store_factor<T, V>(dG + r * pitch + f, a.rows * pitch, g);
+            store_factor<T, V>(dU + r * pitch + f, a.rows * pitch, u);
         }
     }
     if (!SUMS) return;
@@ -78,16 +110,16 @@ __device__ __forceinline__ void gated_grad_rows(const GatedArgs &a, const T *dH,
 
 template <typename T, int V, bool SUMS>
 __global__ void __launch_bounds__(kGradThreads)
-    gated_grad_kernel(GatedArgs a, const T *dH, const T *G, const T *U, T *dG, T *dU, int64_t pitch,
-                      float *partials) {
+    gated_grad_kernel(GatedArgs a, const T *dH, const T *G, const T *U, Factor<T> *dG, Factor<T> *dU,
+                      int64_t pitch, float *partials) {
     with_act(a.act, [&](auto act) {
         gated_grad_rows<T, V, SUMS, decltype(act)::value>(a, dH, G, U, dG, dU, pitch, partials);
     });
 }
 
 template <typename T, int V>
-cudaError_t launch_gated_grad(const GatedArgs &a, const GatedPtrs &p, T *dG, T *dU, int64_t pitch,
-                              float *partials, cudaStream_t s) {
+cudaError_t launch_gated_grad(const GatedArgs &a, const GatedPtrs &p, Factor<T> *dG, Factor<T> *dU,
+                              int64_t pitch, float *partials, cudaStream_t s) {
     const dim3 grid(gated_grad_col_blocks(a.F, V), gated_grad_row_blocks(a.rows, a.F, V));
     const auto kernel = p.dbg ? gated_grad_kernel<T, V, true> : gated_grad_kernel<T, V, false>;
     kernel<<<grid, kGradThreads, 0, s>>>(a, (const T *)p.dH, (const T *)p.G, (const T *)p.U, dG, dU,

@@ -7,43 +7,55 @@
 
 namespace gs {
 
-// Rows of a matrix copied to a pitch of whole 16-byte runs; what lies behind a row's
-// end is not written (and not read: the tensor maps end with the row).
-template <typename T>
-__global__ void __launch_bounds__(256) gated_pad_kernel(const T *from, T *to, int64_t n, int width,
-                                                        int64_t pitch) {
+// Rows of up to three matrices copied to a pitch of whole 16-byte runs, fp32 as planes
+// rows * pitch elements apart; what lies behind a row's end is not written (and not
+// read: the tensor maps end with the row).
+template <typename T> struct PadArgs {
+    const T *from[3];
+    Factor<T> *to[3];
+    int64_t rows[3];
+    int width;
+    int64_t pitch;
+};
+template <typename T, int V> __global__ void __launch_bounds__(256) gated_pad_kernel(PadArgs<T> p) {
+    const int m = blockIdx.y, runs = p.width / V;
+    const int64_t n = p.rows[m] * runs;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-        const int64_t r = i / width;
-        to[r * pitch + (i - r * width)] = from[i];
+        const int64_t r = i / runs;
+        const int d = (int)(i - r * runs) * V;
+        float v[V];
+        Run<T, V>::widen(Run<T, V>::load(p.from[m] + r * p.width + d), v);
+        store_factor<T, V>(p.to[m] + r * p.pitch + d, p.rows[m] * p.pitch, v);
     }
 }
 
-// Workspace: copies of X, Wg and Wu where rows are no multiple of 16 bytes; backward,
-// dG and dU and the biases' partial sums.
+// Workspace: copies of X, Wg and Wu where rows are no multiple of 16 bytes, or their
+// planes; backward, dG and dU and the biases' partial sums.
 template <typename T> struct GatedLayout {
     int64_t pitch_d, pitch_f;
-    bool pad;
+    bool copy;
     size_t X, Wg, Wu, dG, dU, partials, bytes;
     GatedLayout(const GatedArgs &a, bool backward) {
         bytes = 0;
-        const auto take = [&](size_t n) {
+        const auto take = [&](int64_t n) {
             const size_t at = bytes;
-            bytes += (n + 255) & ~(size_t)255;
+            bytes += ((size_t)n + 255) & ~(size_t)255;
             return at;
         };
+        const int each = sizeof(T) == 4 ? 6 : 2;   // bytes of an element in its planes
         pitch_d = (a.D + 7) / 8 * 8;
         pitch_f = (a.F + 7) / 8 * 8;
-        pad = sizeof(T) == 2 && pitch_d != a.D;
-        X = take(pad ? a.rows * pitch_d * sizeof(T) : 0);
-        Wg = take(pad ? a.F * pitch_d * sizeof(T) : 0);
-        Wu = take(pad ? a.F * pitch_d * sizeof(T) : 0);
+        copy = sizeof(T) == 4 || pitch_d != a.D;
+        X = take(copy ? a.rows * pitch_d * each : 0);
+        Wg = take(copy ? a.F * pitch_d * each : 0);
+        Wu = take(copy ? a.F * pitch_d * each : 0);
         if (!backward) return;
-        dG = take(a.rows * pitch_f * sizeof(T));
-        dU = take(a.rows * pitch_f * sizeof(T));
+        dG = take(a.rows * pitch_f * each);
+        dU = take(a.rows * pitch_f * each);
         // whatever the alignment will be
         const int b1 = gated_grad_row_blocks(a.rows, a.F, 1);
         const int bv = gated_grad_row_blocks(a.rows, a.F, kVec<T>);
-        partials = take((size_t)(b1 > bv ? b1 : bv) * 2 * a.F * sizeof(float));
+        partials = take((int64_t)(b1 > bv ? b1 : bv) * 2 * a.F * sizeof(float));
     }
 };
 
@@ -54,36 +66,42 @@ template <typename T> size_t gated_ws_bytes(const GatedArgs &a, bool backward) {
 // X, Wg and Wu as TMA reads them: where they lie, or copied.
 template <typename T>
 cudaError_t gated_operands(const GatedArgs &a, const GatedPtrs &p, const GatedLayout<T> &at,
-                           char *ws, GtMatrix (&m)[3], bool *launched, cudaStream_t s) {
+                           char *ws, GtMatrix (&m)[3], cudaStream_t s) {
     const void *from[3] = {p.X, p.Wg, p.Wu};
     const size_t to[3] = {at.X, at.Wg, at.Wu};
+    PadArgs<T> q;
+    q.width = a.D;
+    q.pitch = at.pitch_d;
+    bool runs = a.D % kVec<T> == 0;
     for (int i = 0; i < 3; ++i) {
-        const int64_t rows = i == 0 ? a.rows : a.F;
-        m[i] = {from[i], rows, a.D, at.pitch_d};
-        if (!at.pad) continue;
-        m[i].at = ws + to[i];
-        const int64_t n = rows * a.D, blocks = (n + 1023) / 1024;
-        gated_pad_kernel<T><<<(unsigned)(blocks < 8 * kGatedSms ? blocks : 8 * kGatedSms), 256, 0, s>>>(
-            (const T *)from[i], (T *)(ws + to[i]), n, a.D, at.pitch_d);
-        const cudaError_t e = cudaGetLastError();
-        if (e != cudaSuccess) return e;
-        *launched = true;
+        q.rows[i] = i == 0 ? a.rows : a.F;
+        q.from[i] = (const T *)from[i];
+        q.to[i] = (Factor<T> *)(ws + to[i]);
+        runs = runs && aligned16(from[i]);
+        m[i] = {at.copy ? (const void *)q.to[i] : from[i], q.rows[i], a.D, at.pitch_d};
     }
-    return cudaSuccess;
+    if (!at.copy) return cudaSuccess;
+    const int64_t most = (a.rows > a.F ? a.rows : a.F) * (int64_t)(a.D / (runs ? kVec<T> : 1));
+    const int64_t need = (most + 255) / 256;
+    const dim3 grid((unsigned)(need < 4 * kGatedSms ? need : 4 * kGatedSms), 3);
+    const auto kernel = runs ? gated_pad_kernel<T, kVec<T>> : gated_pad_kernel<T, 1>;
+    kernel<<<grid, 256, 0, s>>>(q);
+    return cudaGetLastError();
 }
 
 template <typename T>
 cudaError_t launch_gated(const GatedArgs &a, const GatedPtrs &p, void *ws, cudaStream_t s) {
+    GtMatrix m[3];
+    const GatedLayout<T> at(a, false);
+    bool used = false;
+    cudaError_t e = gated_operands(a, p, at, (char *)ws, m, s);
+    if (e == cudaSuccess) e = launch_gt_forward<T>(a, p, m[0], m[1], m[2], at.copy, s, &used);
+    if (e != cudaSuccess || used) return e;
     if constexpr (sizeof(T) == 2) {
-        GtMatrix m[3];
-        bool used = false, launched = false;
-        cudaError_t e = gated_operands(a, p, GatedLayout<T>(a, false), (char *)ws, m, &launched, s);
-        if (e == cudaSuccess)
-            e = launch_gt_forward<T>(a, p, m[0], m[1], m[2], launched, s, &used);
-        if (e != cudaSuccess || used) return e;
+        gated_simt_kernel<T><<<(unsigned)simt_blocks(a.rows, a.F), kSimtThreads, 0, s>>>(a, p);
+        return cudaGetLastError();
     }
-    gated_simt_kernel<T><<<(unsigned)simt_blocks(a.rows, a.F), kSimtThreads, 0, s>>>(a, p);
-    return cudaGetLastError();
+    return cudaErrorInvalidValue;   // not reached: planes are 16-byte aligned
 }
 
 template <typename T>
@@ -91,13 +109,11 @@ cudaError_t launch_gated_backward(const GatedArgs &a, const GatedPtrs &p, void *
                                   cudaStream_t s) {
     const GatedLayout<T> at(a, true);
     char *base = (char *)ws;
-    T *dG = (T *)(base + at.dG), *dU = (T *)(base + at.dU);
+    Factor<T> *dG = (Factor<T> *)(base + at.dG), *dU = (Factor<T> *)(base + at.dU);
     float *partials = (float *)(base + at.partials);
     const bool wide = a.F % kVec<T> == 0 && aligned16(p.dH) && aligned16(p.G) && aligned16(p.U);
     GtMatrix m[3];
-    bool launched = false;
-    cudaError_t e = cudaSuccess;
-    if (sizeof(T) == 2) e = gated_operands(a, p, at, base, m, &launched, s);
+    cudaError_t e = gated_operands(a, p, at, base, m, s);
     if (e != cudaSuccess) return e;
     e = wide ? launch_gated_grad<T, kVec<T>>(a, p, dG, dU, at.pitch_f, partials, s)
              : launch_gated_grad<T, 1>(a, p, dG, dU, at.pitch_f, partials, s);
@@ -107,21 +123,22 @@ cudaError_t launch_gated_backward(const GatedArgs &a, const GatedPtrs &p, void *
         e = launch_gated_bias_sums<T>(a, p, partials, blocks, true, s);
         if (e != cudaSuccess) return e;
     }
+    bool used = false;
+    e = launch_gt_backward<T>(a, p, m[0], m[1], m[2], {dG, a.rows, a.F, at.pitch_f},
+                              {dU, a.rows, a.F, at.pitch_f}, true, s, &used);
+    if (e != cudaSuccess || used) return e;
     if constexpr (sizeof(T) == 2) {
-        bool used = false;
-        e = launch_gt_backward<T>(a, p, m[0], m[1], m[2], {dG, a.rows, a.F, at.pitch_f},
-                                  {dU, a.rows, a.F, at.pitch_f}, true, s, &used);
-        if (e != cudaSuccess || used) return e;
+        const auto product = [&](SimtProduct q, void *out) {
+            return launch_next(true, gated_simt_product_kernel<T>,
+                               dim3((unsigned)simt_blocks(q.M, q.N)), kSimtThreads, 0, s, q, (T *)out);
+        };
+        e = product({{dG, dU}, {p.Wg, p.Wu}, at.pitch_f, 1, 1, a.D, a.rows, a.D, a.F, 2}, p.dX);
+        if (e != cudaSuccess) return e;
+        e = product({{dG, dG}, {p.X, p.X}, 1, at.pitch_f, 1, a.D, a.F, a.D, a.rows, 1}, p.dWg);
+        if (e != cudaSuccess) return e;
+        return product({{dU, dU}, {p.X, p.X}, 1, at.pitch_f, 1, a.D, a.F, a.D, a.rows, 1}, p.dWu);
     }
-    const auto product = [&](SimtProduct q, void *out) {
-        return launch_next(true, gated_simt_product_kernel<T>, dim3((unsigned)simt_blocks(q.M, q.N)),
-                           kSimtThreads, 0, s, q, (T *)out);
-    };
-    e = product({{dG, dU}, {p.Wg, p.Wu}, at.pitch_f, 1, 1, a.D, a.rows, a.D, a.F, 2}, p.dX);
-    if (e != cudaSuccess) return e;
-    e = product({{dG, dG}, {p.X, p.X}, 1, at.pitch_f, 1, a.D, a.F, a.D, a.rows, 1}, p.dWg);
-    if (e != cudaSuccess) return e;
-    return product({{dU, dU}, {p.X, p.X}, 1, at.pitch_f, 1, a.D, a.F, a.D, a.rows, 1}, p.dWu);
+    return cudaErrorInvalidValue;   // not reached: planes are 16-byte aligned
 }
 
 #define GS_GATED_INST(T)                                                                         \

@@ -1,20 +1,27 @@
 // gs_gated_tc.cuh -- the products of the gated projections on the fifth-generation
 // tensor cores: one persistent kernel for the forward pass, for dX and for dWg, dWu.
 //
-// A pair of CTAs (a cluster of two, cta_group::2) works on tiles of 256 rows x 256
-// columns.  Each CTA stages its 128 rows of A and 128 rows of B, 64 steps of the
+// A pair of CTAs (a cluster of two, cta_group::2) works on tiles of 256 rows x NT
+// columns.  Each CTA stages its 128 rows of A and NT / 2 rows of B, 64 steps of the
 // contraction at a time, by TMA with the 128-byte swizzle; one thread of the pair
 // issues tcgen05.mma over both halves, and each CTA's tensor memory receives its 128
-// rows.  TMEM holds two tiles, so that eight epilogue warps store one while the next
-// is multiplied.
+// rows.  TMEM holds two tiles, so that the epilogue warps store one while the next is
+// multiplied.
 //
-//   forward  A = X, B = 128 rows of Wg (first CTA) and the same 128 of Wu (second):
-//            a tile's columns are G and U of the same 128 outputs, side by side.
+//   forward  A = X, B = NT / 2 rows of Wg (first CTA) and the same of Wu (second): a
+//            tile's columns are G and U of the same NT / 2 outputs, side by side.
 //   dX       A = dG, then dU; B = Wg, then Wu, N-major (their rows are contraction).
 //   dW       A = dG or dU, M-major; B = X, N-major; the contraction runs over rows.
 //
 // Both operands are read where they lie: K-major or MN-major is a bit of the
 // instruction, nothing is transposed in memory.
+//
+// fp32 operands come as three bf16 planes, x = x0 + x1 + x2 to 2^-24 of x or better,
+// and a product is the sum of six of theirs, the small ones first: x2 y0, x0 y2, x1 y1,
+// x1 y0, x0 y1, x0 y0 (the other three are below 2^-26 of it).  The tensor cores cut
+// each sum off at the accumulator's last bit, so the contraction is cut into runs of
+// kGtRun steps: each is accumulated in TMEM by itself and added up in the epilogue's
+// registers, rounded to nearest.
 #pragma once
 
 #include "gs_attn_tc.cuh"
@@ -22,24 +29,31 @@
 
 namespace gs {
 
-constexpr int kGtEpilogueWarps = 8;
-constexpr int kGtMmaWarp = kGtEpilogueWarps, kGtCopyWarp = kGtMmaWarp + 1;
-constexpr int kGtThreads = (kGtEpilogueWarps + 2) * 32;
-constexpr int kGtTile = 256;          // rows and columns of a pair's tile
-constexpr int kGtHalf = 128;          // rows of A, and of B, of one CTA
+constexpr int kGtTile = 256;          // rows of a pair's tile
+constexpr int kGtHalf = 128;          // rows of A of one CTA
 constexpr int kGtK = 64;              // contraction steps per stage: 128 bytes
-constexpr int kGtOperand = kGtHalf * kGtK * 2;          // bytes of one operand's stage
-constexpr int kGtStage = 2 * kGtOperand;
-constexpr int kGtBox = 32 * 64 * 2;   // bytes of a warp's staged output box, 32 rows x 64 columns
+constexpr int kGtA = kGtHalf * kGtK * 2;   // bytes of A's stage
+constexpr int kGtChunk = 64 * kGtK * 2;    // bytes of 64 rows of an MN-major operand
+constexpr int kGtBox = 32 * 128;      // bytes of a warp's staged output box: 32 rows of 128 bytes
 constexpr int kGtSmem = 224 * 1024;
+constexpr int kGtRun = 4;             // stages of a plane's run (fp32)
 
 enum { kGtForward = 0, kGtForwardKeep = 1, kGtDx = 2, kGtDw = 3 };
 
-template <int MODE> struct GtShape {
+// T: type of the outputs.
+template <typename T, int MODE, int NT> struct GtShape {
+    static constexpr int kParts = NT / 128;          // epilogue warps that share 32 rows
+    static constexpr int kEpilogueWarps = 4 * kParts;
+    static constexpr int kMmaWarp = kEpilogueWarps, kCopyWarp = kMmaWarp + 1;
+    static constexpr int kThreads = (kEpilogueWarps + 2) * 32;
+    static constexpr int kB = NT / 2 * kGtK * 2;     // bytes of B's stage
+    static constexpr int kStage = kGtA + kB;
     static constexpr int kBoxes = MODE == kGtForwardKeep ? 3 : MODE == kGtForward ? 1 : 2;
-    static constexpr int kBoxBytes = kBoxes * kGtEpilogueWarps * kGtBox;
-    static constexpr int kStages = (kGtSmem - kBoxBytes) / kGtStage;
-    static constexpr int kSmem = kStages * kGtStage + kBoxBytes + 1024;
+    static constexpr int kBoxBytes = kBoxes * kEpilogueWarps * kGtBox;
+    static constexpr int kStages = (kGtSmem - kBoxBytes) / kStage < 8 ? (kGtSmem - kBoxBytes) / kStage : 8;
+    static constexpr int kSmem = kStages * kStage + kBoxBytes + 1024;
+    static constexpr int kPlanes = sizeof(T) == 4 ? 3 : 1;
+    static constexpr int kBoxCols = 128 / (int)sizeof(T);
 };
 
 // ------------------------------------------------------------------ pairs of CTAs
@@ -144,13 +158,15 @@ __device__ __forceinline__ void umma_commit_pair(uint64_t *bar) {
 
 // ------------------------------------------------------------------ arguments
 
-// A 16-bit matrix (rows, width) with rows `pitch` elements apart.
+// A 16-bit matrix (rows, width) with rows `pitch` elements apart; planes of fp32 follow
+// one another, rows * pitch elements apart.
 struct GtMatrix {
     const void *at;
     int64_t rows;
     int width;
     int64_t pitch;
 };
+constexpr int kGtMostPlanes = 3;
 
 // An output (rows, width): TMA boxes where its rows are multiples of 16 bytes, plain
 // stores elsewhere.
@@ -162,11 +178,12 @@ struct GtOutput {
 };
 
 struct GtArgs {
-    CUtensorMap a[2], b[2];       // forward: a[0], b = Wg and Wu; dX: dG, Wg and dU, Wu; dW: b[0]
+    // planes of each operand; forward: a[0], b = Wg and Wu; dX: dG, Wg and dU, Wu; dW: b[0]
+    CUtensorMap a[2][kGtMostPlanes], b[2][kGtMostPlanes];
     GtOutput out[3];              // forward: H, G, U; dX: dX; dW: dWg, dWu
     const void *bg, *bu;
     int F, act, bias_runs;        // bias_runs: the biases are 16-byte aligned
-    int tiles_m, tiles_n;         // of 256 rows, and 256 columns (forward: 128 outputs)
+    int tiles_m, tiles_n;         // of 256 rows, and NT columns (forward: NT / 2 outputs)
     int k_steps;                  // of one pair of operands
     unsigned *err;
 };
@@ -177,11 +194,23 @@ inline bool gt_map(CUtensorMap *map, const GtMatrix &m, bool bf16, int box_rows)
     const uint32_t box[2] = {64, (uint32_t)box_rows};
     return tmap_encode(map, 2, bf16, 2, m.at, dims, stride, box, true);
 }
-inline void gt_output(GtOutput *o, void *at, int64_t rows, int width, bool bf16) {
+template <typename T>
+bool gt_maps(CUtensorMap (&map)[kGtMostPlanes], const GtMatrix &m, int box_rows) {
+    constexpr int planes = sizeof(T) == 4 ? 3 : 1;
+    for (int i = 0; i < planes; ++i)
+        if (!gt_map(&map[i], {(const char *)m.at + i * m.rows * m.pitch * 2, m.rows, m.width, m.pitch},
+                    !__is_same(T, __half), box_rows))
+            return false;
+    return true;
+}
+template <typename T> void gt_output(GtOutput *o, void *at, int64_t rows, int width) {
     o->at = at;
     o->rows = rows;
     o->width = width;
-    o->boxes = width % 8 == 0 && gt_map(&o->map, {at, rows, width, width}, bf16, 32);
+    const uint64_t dims[2] = {(uint64_t)width, (uint64_t)rows}, stride[1] = {width * sizeof(T)};
+    const uint32_t box[2] = {128 / sizeof(T), 32};
+    o->boxes = width * sizeof(T) % 16 == 0 &&
+               tmap_encode(&o->map, sizeof(T), __is_same(T, __nv_bfloat16), 2, at, dims, stride, box, true);
 }
 
 // Tile t of tiles_m x tiles_n: eight rows of tiles at a time, so that the tiles in
@@ -218,20 +247,48 @@ template <int NS> struct GtRing {
     }
 };
 
-// 64 staged columns of 32 rows from shared memory to where TMA cannot store.
+// The products of planes that make up one of fp32 operands, the small ones first.
+__device__ __forceinline__ int gt_plane_a(int product) { return (0x201100 >> (20 - 4 * product)) & 3; }
+__device__ __forceinline__ int gt_plane_b(int product) { return (0x021010 >> (20 - 4 * product)) & 3; }
+
+// The parts of a tile that TMEM accumulates by themselves, and their steps in order:
+// f(pair of operands, planes of A and B, stage of the contraction) until it is false.
+template <int MODE, int PLANES> __device__ __forceinline__ int gt_units(const GtArgs &p) {
+    if (PLANES == 1) return 1;
+    return (p.k_steps + kGtRun - 1) / kGtRun * (MODE == kGtDx ? 2 : 1);
+}
+template <int MODE, int PLANES, typename F>
+__device__ __forceinline__ void gt_steps(const GtArgs &p, int unit, F &&f) {
+    if (PLANES == 1) {
+        for (int which = 0; which < (MODE == kGtDx ? 2 : 1); ++which)
+            for (int k = 0; k < p.k_steps; ++k)
+                if (!f(which, 0, 0, k)) return;
+        return;
+    }
+    const int runs = (p.k_steps + kGtRun - 1) / kGtRun, which = unit >= runs;
+    const int k0 = (unit - which * runs) * kGtRun, k1 = min(k0 + kGtRun, p.k_steps);
+    for (int product = 0; product < 6; ++product)
+        for (int k = k0; k < k1; ++k)
+            if (!f(which, gt_plane_a(product), gt_plane_b(product), k)) return;
+}
+
+// A box's staged columns of 32 rows from shared memory to where TMA cannot store.
 template <typename T>
 __device__ __forceinline__ void gt_store_plain(const GtOutput &o, const unsigned char *box,
                                                int64_t row0, int col0) {
-    const int lane = threadIdx.x % 32, c = lane * 2;
+    constexpr int N = 4 / (int)sizeof(T);   // columns of a lane
+    const int lane = threadIdx.x % 32;
     for (int r = 0; r < 32 && row0 + r < o.rows; ++r) {
-        const T *from = reinterpret_cast<const T *>(box + r * 128 + (((c / 8) ^ (r % 8)) * 16)) + c % 8;
-        T *to = (T *)o.at + (row0 + r) * o.width + col0 + c;
-        if (col0 + c < o.width) to[0] = from[0];
-        if (col0 + c + 1 < o.width) to[1] = from[1];
+        const T *from = reinterpret_cast<const T *>(box + r * 128 + (((lane / 4) ^ (r % 8)) * 16) +
+                                                    lane % 4 * 4);
+        T *to = (T *)o.at + (row0 + r) * o.width + col0 + lane * N;
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+            if (col0 + lane * N + e < o.width) to[e] = from[e];
     }
 }
 
-// A warp's box of 32 rows x 64 columns, written by all its lanes, to the output.
+// A warp's box of 32 rows, written by all its lanes, to the output.
 template <typename T>
 __device__ __forceinline__ void gt_store_box(const GtOutput &o, const unsigned char *box, int64_t row0,
                                              int col0) {
@@ -244,59 +301,73 @@ __device__ __forceinline__ void gt_store_box(const GtOutput &o, const unsigned c
         gt_store_plain<T>(o, box, row0, col0);
     }
 }
+// Until a warp's boxes may be written again.
+__device__ __forceinline__ void gt_boxes_free() {
+    if (threadIdx.x % 32 == 0) {
+        bulk_commit();
+        bulk_wait_read();
+    }
+    __syncwarp();
+}
 
-// 32 packed columns (16 words) of this lane's row into its box, chunks from `chunk` on.
-__device__ __forceinline__ void gt_stage(unsigned char *box, int chunk, const uint32_t (&w)[16]) {
+// 32 columns of this lane's row into its box, rounded: the second half of the box's
+// columns with `half` (16-bit types).
+template <typename T>
+__device__ __forceinline__ void gt_stage(unsigned char *box, int half, const uint32_t (&v)[32]) {
     const int lane = threadIdx.x % 32;
     unsigned char *row = box + lane * 128;
+    if constexpr (sizeof(T) == 4) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        *reinterpret_cast<uint4 *>(row + (((chunk + i) ^ (lane % 8)) * 16)) =
-            make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<uint4 *>(row + ((i ^ (lane % 8)) * 16)) =
+                make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    } else {
+        uint32_t w[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            w[i] = pack2<T>(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<uint4 *>(row + (((4 * half + i) ^ (lane % 8)) * 16)) =
+                make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    }
 }
 
 // v += 32 biases from column f on; the same for all lanes.
 template <typename T>
 __device__ __forceinline__ void gt_add_bias(uint32_t (&v)[32], const T *bias, int f, int F, bool runs) {
 #pragma unroll
-    for (int c = 0; c < 32; c += 8) {
-        float b[8] = {};
-        if (runs && f + c + 8 <= F) {
-            Run<T, 8>::widen(__ldg(reinterpret_cast<const uint4 *>(bias + f + c)), b);
+    for (int c = 0; c < 32; c += kVec<T>) {
+        float b[kVec<T>] = {};
+        if (runs && f + c + kVec<T> <= F) {
+            Run<T, kVec<T>>::widen(__ldg(reinterpret_cast<const uint4 *>(bias + f + c)), b);
         } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
+            for (int e = 0; e < kVec<T>; ++e)
                 if (f + c + e < F) b[e] = IO<T>::ld(bias + f + c + e);
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[c + e] = __float_as_uint(__uint_as_float(v[c + e]) + b[e]);
+        for (int e = 0; e < kVec<T>; ++e) v[c + e] = __float_as_uint(__uint_as_float(v[c + e]) + b[e]);
     }
 }
 
-template <typename T> __device__ __forceinline__ void gt_pack(const uint32_t (&v)[32], uint32_t (&w)[16]) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-        w[i] = pack2<T>(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-}
-
-template <typename T, int MODE>
-__global__ void __launch_bounds__(kGtThreads, 1) gated_tc_kernel(const __grid_constant__ GtArgs p) {
-    using Sh = GtShape<MODE>;
+template <typename T, int MODE, int NT>
+__global__ void __launch_bounds__(GtShape<T, MODE, NT>::kThreads, 1)
+    gated_tc_kernel(const __grid_constant__ GtArgs p) {
+    using Sh = GtShape<T, MODE, NT>;
     constexpr bool kForward = MODE == kGtForward || MODE == kGtForwardKeep;
-    constexpr bool kBf16 = __is_same(T, __nv_bfloat16);
-    constexpr int NS = Sh::kStages;
+    constexpr int NS = Sh::kStages, kPlanes = Sh::kPlanes, kBoxCols = Sh::kBoxCols;
     extern __shared__ unsigned char smem_raw[];
     __shared__ __align__(8) uint64_t full[NS], empty[NS], tile_full[2], tile_empty[2], drained;
     __shared__ uint32_t tmem_base;
     unsigned char *stages = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-    unsigned char *boxes = stages + NS * kGtStage;
+    unsigned char *boxes = stages + NS * Sh::kStage;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t rank = cluster_rank();
     const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
-    const int tiles = p.tiles_m * p.tiles_n;
-    const int steps = MODE == kGtDx ? 2 * p.k_steps : p.k_steps;
+    const int tiles = p.tiles_m * p.tiles_n, units = gt_units<MODE, kPlanes>(p);
 
-    if (warp == kGtMmaWarp) {
+    if (warp == Sh::kMmaWarp) {
         if (lane == 0) {
             for (int s = 0; s < NS; ++s) {
                 mbar_init(&full[s], 1);
@@ -304,7 +375,7 @@ __global__ void __launch_bounds__(kGtThreads, 1) gated_tc_kernel(const __grid_co
             }
             for (int b = 0; b < 2; ++b) {
                 mbar_init(&tile_full[b], 1);
-                mbar_init(&tile_empty[b], 2 * kGtEpilogueWarps);
+                mbar_init(&tile_empty[b], 2 * Sh::kEpilogueWarps);
             }
             mbar_init(&drained, 1);
             fence_mbar_init();
@@ -321,42 +392,47 @@ __global__ void __launch_bounds__(kGtThreads, 1) gated_tc_kernel(const __grid_co
     wait_for_previous_kernel(bg, bu);
     bool ok = true;
 
-    if (warp == kGtCopyWarp) {
+    if (warp == Sh::kCopyWarp) {
         // ---------------------------------------------------- copies, one thread of each CTA
         if (lane == 0) {
             GtRing<NS> r;
             for (int t = pair; t < tiles && ok; t += pairs) {
                 const GtTile w = gt_tile(p, t);
-                for (int k = 0; k < steps; ++k, r.next()) {
-                    const int s = r.stage;
-                    ok = tc_wait(&empty[s], r.parity ^ 1, p.err);
-                    if (!ok) break;
-                    if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kGtStage);
-                    const uint32_t bar = smem_of_rank(smem_u32(&full[s]), 0);
-                    const uint32_t a = smem_u32(stages + s * kGtStage), b = a + kGtOperand;
-                    if (kForward) {
-                        tma_load_2d_pair(a, &p.a[0], k * kGtK, w.m * kGtTile + rank * kGtHalf, bar);
-                        tma_load_2d_pair(b, &p.b[rank], k * kGtK, w.n * kGtHalf, bar);
-                    } else if (MODE == kGtDx) {
-                        const int which = k >= p.k_steps, kk = (k - which * p.k_steps) * kGtK;
-                        const int col = w.n * kGtTile + rank * kGtHalf;
-                        tma_load_2d_pair(a, &p.a[which], kk, w.m * kGtTile + rank * kGtHalf, bar);
-                        tma_load_2d_pair(b, &p.b[which], col, kk, bar);
-                        tma_load_2d_pair(b + kGtOperand / 2, &p.b[which], col + 64, kk, bar);
-                    } else {
-                        const int half = p.tiles_m / 2, which = w.m >= half;
-                        const int row = (w.m - which * half) * kGtTile + rank * kGtHalf;
-                        const int col = w.n * kGtTile + rank * kGtHalf;
-                        tma_load_2d_pair(a, &p.a[which], row, k * kGtK, bar);
-                        tma_load_2d_pair(a + kGtOperand / 2, &p.a[which], row + 64, k * kGtK, bar);
-                        tma_load_2d_pair(b, &p.b[0], col, k * kGtK, bar);
-                        tma_load_2d_pair(b + kGtOperand / 2, &p.b[0], col + 64, k * kGtK, bar);
-                    }
-                }
+                for (int u = 0; u < units && ok; ++u)
+                    gt_steps<MODE, kPlanes>(p, u, [&](int which, int pa, int pb, int k) {
+                        const int s = r.stage;
+                        ok = tc_wait(&empty[s], r.parity ^ 1, p.err);
+                        if (!ok) return false;
+                        if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * Sh::kStage);
+                        const uint32_t bar = smem_of_rank(smem_u32(&full[s]), 0);
+                        const uint32_t a = smem_u32(stages + s * Sh::kStage), b = a + kGtA;
+                        const int kk = k * kGtK;
+                        if (kForward) {
+                            tma_load_2d_pair(a, &p.a[0][pa], kk, w.m * kGtTile + rank * kGtHalf, bar);
+                            tma_load_2d_pair(b, &p.b[rank][pb], kk, w.n * (NT / 2), bar);
+                        } else {
+                            const int col = w.n * NT + rank * (NT / 2);
+                            if (MODE == kGtDx) {
+                                tma_load_2d_pair(a, &p.a[which][pa], kk,
+                                                 w.m * kGtTile + rank * kGtHalf, bar);
+                            } else {
+                                const int half = p.tiles_m / 2, of = w.m >= half;
+                                const int row = (w.m - of * half) * kGtTile + rank * kGtHalf;
+                                tma_load_2d_pair(a, &p.a[of][pa], row, kk, bar);
+                                tma_load_2d_pair(a + kGtChunk, &p.a[of][pa], row + 64, kk, bar);
+                            }
+#pragma unroll
+                            for (int c = 0; c < NT / 128; ++c)
+                                tma_load_2d_pair(b + c * kGtChunk, &p.b[which][pb], col + c * 64, kk,
+                                                 bar);
+                        }
+                        r.next();
+                        return true;
+                    });
             }
             // every copy lands, and every stage is handed back, before either CTA may
             // leave; where a wait gave up, the copies (counted in the first CTA) land
-            const int fills = r.filled < NS ? r.filled : NS;
+            const int fills = r.filled;
             for (int i = 0; i < fills; ++i) {
                 r.back();
                 if (ok)
@@ -366,35 +442,42 @@ __global__ void __launch_bounds__(kGtThreads, 1) gated_tc_kernel(const __grid_co
             }
         }
         __syncwarp();
-    } else if (warp == kGtMmaWarp) {
+    } else if (warp == Sh::kMmaWarp) {
         // ---------------------------------------------------- MMAs, one thread of the pair
         if (lane == 0 && rank == 0) {
-            constexpr uint32_t idesc = umma_idesc_f16(kBf16, kGtTile, kGtTile) |
+            constexpr uint32_t idesc = umma_idesc_f16(!__is_same(T, __half), kGtTile, NT) |
                                        (MODE == kGtDw ? 1u << 15 : 0u) | (kForward ? 0u : 1u << 16);
             constexpr bool kAmn = MODE == kGtDw, kBmn = !kForward;
             const uint32_t base = smem_u32(stages);
-            const uint32_t a0 = kAmn ? umma_lo_mnmajor(base, kGtOperand / 2) : umma_lo_kmajor(base);
-            const uint32_t b0 = kBmn ? umma_lo_mnmajor(base + kGtOperand, kGtOperand / 2)
-                                     : umma_lo_kmajor(base + kGtOperand);
+            const uint32_t a0 = kAmn ? umma_lo_mnmajor(base, kGtChunk) : umma_lo_kmajor(base);
+            const uint32_t b0 =
+                kBmn ? umma_lo_mnmajor(base + kGtA, kGtChunk) : umma_lo_kmajor(base + kGtA);
             GtRing<NS> r;
             int count = 0;
-            for (int t = pair; t < tiles && ok; t += pairs, ++count) {
-                const int b = count & 1;
-                if (count >= 2) ok = tc_wait_cluster(&tile_empty[b], (count / 2 - 1) & 1, p.err);
-                for (int k = 0; k < steps && ok; ++k, r.next()) {
-                    const int s = r.stage;
-                    ok = tc_wait(&full[s], r.parity, p.err);
+            for (int t = pair; t < tiles && ok; t += pairs)
+                for (int u = 0; u < units && ok; ++u, ++count) {
+                    const int b = count & 1;
+                    if (count >= 2) ok = tc_wait_cluster(&tile_empty[b], (count / 2 - 1) & 1, p.err);
+                    uint32_t more = 0;
                     if (!ok) break;
-                    tcgen05_fence_after_sync();
-                    const uint32_t a = a0 + s * (kGtStage / 16), bb = b0 + s * (kGtStage / 16);
+                    gt_steps<MODE, kPlanes>(p, u, [&](int, int, int, int) {
+                        const int s = r.stage;
+                        ok = tc_wait(&full[s], r.parity, p.err);
+                        if (!ok) return false;
+                        tcgen05_fence_after_sync();
+                        const uint32_t a = a0 + s * (Sh::kStage / 16), bb = b0 + s * (Sh::kStage / 16);
 #pragma unroll
-                    for (int i = 0; i < kGtK / 16; ++i)   // 16 steps: 32 bytes of a row, or 16 rows
-                        umma_f16_pair(tmem + b * kGtTile, a + i * (kAmn ? 2048 : 32) / 16,
-                                      bb + i * (kBmn ? 2048 : 32) / 16, idesc, k > 0 || i > 0);
-                    umma_commit_pair(&empty[s]);
+                        for (int i = 0; i < kGtK / 16; ++i) {   // 16 steps: 32 bytes of a row, or 16 rows
+                            umma_f16_pair(tmem + b * NT, a + i * (kAmn ? 2048 : 32) / 16,
+                                          bb + i * (kBmn ? 2048 : 32) / 16, idesc, more);
+                            more = 1;
+                        }
+                        umma_commit_pair(&empty[s]);
+                        r.next();
+                        return true;
+                    });
+                    if (ok) umma_commit_pair(&tile_full[b]);
                 }
-                if (ok) umma_commit_pair(&tile_full[b]);
-            }
             if (!ok) {   // a wait gave up: let the MMAs end before TMEM is released
                 umma_commit_pair(&drained);
                 tc_wait(&drained, 0, p.err);
@@ -403,104 +486,141 @@ __global__ void __launch_bounds__(kGtThreads, 1) gated_tc_kernel(const __grid_co
         __syncwarp();
     } else {
         // ---------------------------------------------------- epilogue
+        // A warp has 32 rows and 128 columns of the tile: G and U of 64 outputs, or 128
+        // columns of a gradient; `column(i)` is where the i-th 32 of them start.
         const int quarter = warp % 4, part = warp / 4;
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
         unsigned char *box = boxes + warp * Sh::kBoxes * kGtBox;
+        const auto column = [&](int i) {
+            return kForward ? i / 2 * (NT / 2) + part * 64 + i % 2 * 32 : part * 128 + i * 32;
+        };
         int count = 0;
-        for (int t = pair; t < tiles && ok; t += pairs, ++count) {
+        for (int t = pair; t < tiles && ok; t += pairs) {
             const GtTile w = gt_tile(p, t);
-            const int b = count & 1;
-            ok = __all_sync(0xffffffffu, tc_wait(&tile_full[b], (count / 2) & 1, p.err));
-            if (!ok) break;
-            tcgen05_fence_after_sync();
-            const uint32_t at = tmem + b * kGtTile + lanes;
-            const auto release = [&] {   // TMEM is read: the tile after next may be multiplied
+            const int64_t row0 = (int64_t)w.m * kGtTile + rank * kGtHalf + quarter * 32;
+            uint32_t at = 0;
+            const auto arrive = [&] {   // waits for a part of the tile
+                const int b = count & 1;
+                ok = __all_sync(0xffffffffu, tc_wait(&tile_full[b], (count / 2) & 1, p.err));
+                tcgen05_fence_after_sync();
+                at = tmem + b * NT + lanes;
+            };
+            const auto release = [&] {   // TMEM is read: the part after next may be multiplied
                 tcgen05_fence_before_sync();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_remote(smem_of_rank(smem_u32(&tile_empty[b]), 0));
+                if (lane == 0) mbar_arrive_remote(smem_of_rank(smem_u32(&tile_empty[count & 1]), 0));
+                ++count;
             };
-            if (lane == 0) bulk_wait_read();
-            __syncwarp();
-            const int64_t row0 = (int64_t)w.m * kGtTile + rank * kGtHalf + quarter * 32;
+            // the four runs of 32 columns: of one part in TMEM, or the sums of them all
+            uint32_t v[4][32];
+            if constexpr (kPlanes > 1) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) v[i][c] = 0;
+                for (int u = 0; u < units; ++u) {
+                    arrive();
+                    if (!ok) break;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t x[32];
+                        tmem_ld_x32(at + column(i), x);
+#pragma unroll
+                        for (int c = 0; c < 32; ++c)
+                            v[i][c] = __float_as_uint(__uint_as_float(v[i][c]) + __uint_as_float(x[c]));
+                    }
+                    release();
+                }
+            } else {
+                arrive();
+            }
+            if (!ok) break;
+            // runs i and j, read from TMEM now where there is one part; `last`: no more of them
+            const auto read = [&](int i, int j, bool last) {
+                if constexpr (kPlanes == 1) {
+                    tmem_start_ld_x32(at + column(i), v[i]);
+                    tmem_start_ld_x32(at + column(j), v[j]);
+                    tmem_wait_ld(v[i]);
+                    tmem_wait_ld(v[j]);
+                    if (last) release();
+                }
+            };
+            gt_boxes_free();
             if constexpr (kForward) {
-                const int f0 = w.n * kGtHalf + part * 64;
-#pragma unroll 1
-                for (int c = 0; c < 64; c += 32) {
-                    uint32_t g[32], u[32], h[32], packed[16];
-                    tmem_start_ld_x32(at + part * 64 + c, g);
-                    tmem_start_ld_x32(at + kGtHalf + part * 64 + c, u);
-                    tmem_wait_ld(g);
-                    tmem_wait_ld(u);
-                    if (c == 32) release();
+                const int f0 = w.n * (NT / 2) + part * 64;
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    read(c, 2 + c, c == 1);
+                    uint32_t(&g)[32] = v[c], (&u)[32] = v[2 + c];
+                    const int f = f0 + c * 32, half = kBoxCols == 64 ? c : 0;
                     if (bg) {
-                        gt_add_bias(g, (const T *)bg, f0 + c, p.F, p.bias_runs);
-                        gt_add_bias(u, (const T *)bu, f0 + c, p.F, p.bias_runs);
+                        gt_add_bias(g, (const T *)bg, f, p.F, p.bias_runs);
+                        gt_add_bias(u, (const T *)bu, f, p.F, p.bias_runs);
+                    }
+                    if (MODE == kGtForwardKeep) {
+                        gt_stage<T>(box + kGtBox, half, g);
+                        gt_stage<T>(box + 2 * kGtBox, half, u);
                     }
                     with_act(p.act, [&](auto act) {
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
-                            h[i] = __float_as_uint(act_of<decltype(act)::value>(__uint_as_float(g[i])) *
+                            g[i] = __float_as_uint(act_of<decltype(act)::value>(__uint_as_float(g[i])) *
                                                    __uint_as_float(u[i]));
                     });
-                    gt_pack<T>(h, packed);
-                    gt_stage(box, c / 8, packed);
-                    if (MODE == kGtForwardKeep) {
-                        gt_pack<T>(g, packed);
-                        gt_stage(box + kGtBox, c / 8, packed);
-                        gt_pack<T>(u, packed);
-                        gt_stage(box + 2 * kGtBox, c / 8, packed);
-                    }
-                }
+                    gt_stage<T>(box, half, g);
+                    if (kBoxCols == 64 && c == 0) continue;   // half a box
 #pragma unroll
-                for (int o = 0; o < Sh::kBoxes; ++o)
-                    gt_store_box<T>(p.out[o], box + o * kGtBox, row0, f0);
+                    for (int o = 0; o < Sh::kBoxes; ++o)
+                        gt_store_box<T>(p.out[o], box + o * kGtBox, row0, kBoxCols == 64 ? f0 : f);
+                    if (c == 0) gt_boxes_free();
+                }
             } else {
                 const int half = p.tiles_m / 2, which = MODE == kGtDw && w.m >= half;
                 const GtOutput &out = p.out[which];
                 const int64_t out_row = row0 - (int64_t)which * half * kGtTile;
-#pragma unroll 1
-                for (int c = 0; c < 128; c += 64) {
-                    uint32_t x[32], y[32], packed[16];
-                    tmem_start_ld_x32(at + part * 128 + c, x);
-                    tmem_start_ld_x32(at + part * 128 + c + 32, y);
-                    tmem_wait_ld(x);
-                    tmem_wait_ld(y);
-                    if (c == 64) release();
-                    unsigned char *to = box + c / 64 * kGtBox;
-                    gt_pack<T>(x, packed);
-                    gt_stage(to, 0, packed);
-                    gt_pack<T>(y, packed);
-                    gt_stage(to, 4, packed);
-                    gt_store_box<T>(out, to, out_row, w.n * kGtTile + part * 128 + c);
+                const int col0 = w.n * NT + part * 128;
+#pragma unroll
+                for (int c = 0; c < 4; c += 2) {
+                    read(c, c + 1, c == 2);
+                    if constexpr (kBoxCols == 64) {
+                        unsigned char *to = box + c / 2 * kGtBox;
+                        gt_stage<T>(to, 0, v[c]);
+                        gt_stage<T>(to, 1, v[c + 1]);
+                        gt_store_box<T>(out, to, out_row, col0 + c * 32);
+                    } else {
+                        gt_stage<T>(box, 0, v[c]);
+                        gt_stage<T>(box + kGtBox, 0, v[c + 1]);
+                        gt_store_box<T>(out, box, out_row, col0 + c * 32);
+                        gt_store_box<T>(out, box + kGtBox, out_row, col0 + c * 32 + 32);
+                        if (c == 0) gt_boxes_free();
+                    }
                 }
             }
-            if (lane == 0) bulk_commit();
-            __syncwarp();
         }
-        if (lane == 0) bulk_wait_read();
-        __syncwarp();
+        gt_boxes_free();
     }
     tcgen05_fence_before_sync();
     __syncthreads();
     cluster_barrier();   // the other CTA neither reads this one's memory nor arrives here any more
-    if (warp == kGtMmaWarp) tmem_dealloc_pair(tmem);
+    if (warp == Sh::kMmaWarp) tmem_dealloc_pair(tmem);
 }
 
 // Pairs of CTAs that the device holds at once.
-template <typename T, int MODE> cudaError_t gt_most_pairs(int *pairs) {
+template <typename T, int MODE, int NT> cudaError_t gt_most_pairs(int *pairs) {
+    using Sh = GtShape<T, MODE, NT>;
     static std::atomic<int> known[kMaxDevices];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     const bool cached = dev >= 0 && dev < kMaxDevices;
     if (cached && (*pairs = known[dev].load(std::memory_order_acquire)) > 0) return cudaSuccess;
-    const auto kernel = gated_tc_kernel<T, MODE>;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, GtShape<MODE>::kSmem);
+    const auto kernel = gated_tc_kernel<T, MODE, NT>;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(kGatedSms);
-    cfg.blockDim = dim3(kGtThreads);
-    cfg.dynamicSmemBytes = GtShape<MODE>::kSmem;
+    cfg.blockDim = dim3(Sh::kThreads);
+    cfg.dynamicSmemBytes = Sh::kSmem;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
     attr.val.clusterDim.x = 2;
@@ -514,69 +634,82 @@ template <typename T, int MODE> cudaError_t gt_most_pairs(int *pairs) {
     return cudaSuccess;
 }
 
-template <typename T, int MODE>
-cudaError_t launch_gt(const GtArgs &p, bool follows, cudaStream_t s) {
+template <typename T, int MODE, int NT>
+cudaError_t launch_gt_as(GtArgs &p, bool follows, cudaStream_t s) {
+    using Sh = GtShape<T, MODE, NT>;
     int pairs = 0;
-    const cudaError_t e = gt_most_pairs<T, MODE>(&pairs);
+    const cudaError_t e = gt_most_pairs<T, MODE, NT>(&pairs);
     if (e != cudaSuccess) return e;
     const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
     const unsigned blocks = 2 * (unsigned)(tiles < pairs ? tiles : pairs);
-    return launch_next(LaunchAs(follows, 2), gated_tc_kernel<T, MODE>, dim3(blocks), kGtThreads,
-                       GtShape<MODE>::kSmem, s, p);
+    return launch_next(LaunchAs(follows, 2), gated_tc_kernel<T, MODE, NT>, dim3(blocks), Sh::kThreads,
+                       Sh::kSmem, s, p);
 }
 
-// Forward pass from 16-bit operands; *used: TMA takes them.
+// Columns of B per tile: 256, or 128 where tiles that wide leave SMs without one.
+inline int gt_columns(int64_t tiles_m, int columns) {
+    return tiles_m * ((columns + 255) / 256) * 2 < kGatedSms ? 128 : 256;
+}
+
+// Forward pass from 16-bit operands (T float: planes); *used: TMA takes them.
 template <typename T>
 cudaError_t launch_gt_forward(const GatedArgs &a, const GatedPtrs &q, const GtMatrix &X,
                               const GtMatrix &Wg, const GtMatrix &Wu, bool follows, cudaStream_t s,
                               bool *used) {
-    constexpr bool bf16 = __is_same(T, __nv_bfloat16);
     GtArgs p = {};
-    *used = gt_map(&p.a[0], X, bf16, kGtHalf) && gt_map(&p.b[0], Wg, bf16, kGtHalf) &&
-            gt_map(&p.b[1], Wu, bf16, kGtHalf);
+    p.tiles_m = (int)((a.rows + kGtTile - 1) / kGtTile);
+    const int nt = gt_columns(p.tiles_m, 2 * a.F);
+    *used = gt_maps<T>(p.a[0], X, kGtHalf) && gt_maps<T>(p.b[0], Wg, nt / 2) &&
+            gt_maps<T>(p.b[1], Wu, nt / 2);
     if (!*used) return cudaSuccess;
-    gt_output(&p.out[0], q.H, a.rows, a.F, bf16);
+    gt_output<T>(&p.out[0], q.H, a.rows, a.F);
     if (q.G) {
-        gt_output(&p.out[1], q.G, a.rows, a.F, bf16);
-        gt_output(&p.out[2], q.U, a.rows, a.F, bf16);
+        gt_output<T>(&p.out[1], q.G, a.rows, a.F);
+        gt_output<T>(&p.out[2], q.U, a.rows, a.F);
     }
     p.bg = q.bg;
     p.bu = q.bu;
     p.bias_runs = aligned16(q.bg) && aligned16(q.bu);
     p.F = a.F;
     p.act = a.act;
-    p.tiles_m = (int)((a.rows + kGtTile - 1) / kGtTile);
-    p.tiles_n = (a.F + kGtHalf - 1) / kGtHalf;
+    p.tiles_n = (a.F + nt / 2 - 1) / (nt / 2);
     p.k_steps = (a.D + kGtK - 1) / kGtK;
     p.err = a.err;
-    return q.G ? launch_gt<T, kGtForwardKeep>(p, follows, s) : launch_gt<T, kGtForward>(p, follows, s);
+    if (nt == 128)
+        return q.G ? launch_gt_as<T, kGtForwardKeep, 128>(p, follows, s)
+                   : launch_gt_as<T, kGtForward, 128>(p, follows, s);
+    return q.G ? launch_gt_as<T, kGtForwardKeep, 256>(p, follows, s)
+               : launch_gt_as<T, kGtForward, 256>(p, follows, s);
 }
 
-// dX, dWg and dWu from 16-bit operands; *used: TMA takes them.
+// dX, dWg and dWu from 16-bit operands (T float: planes); *used: TMA takes them.
 template <typename T>
 cudaError_t launch_gt_backward(const GatedArgs &a, const GatedPtrs &q, const GtMatrix &X,
                                const GtMatrix &Wg, const GtMatrix &Wu, const GtMatrix &dG,
                                const GtMatrix &dU, bool follows, cudaStream_t s, bool *used) {
-    constexpr bool bf16 = __is_same(T, __nv_bfloat16);
     GtArgs x = {}, w = {};
-    *used = gt_map(&x.a[0], dG, bf16, kGtHalf) && gt_map(&x.a[1], dU, bf16, kGtHalf) &&
-            gt_map(&x.b[0], Wg, bf16, kGtK) && gt_map(&x.b[1], Wu, bf16, kGtK) &&
-            gt_map(&w.a[0], dG, bf16, kGtK) && gt_map(&w.a[1], dU, bf16, kGtK) &&
-            gt_map(&w.b[0], X, bf16, kGtK);
+    *used = gt_maps<T>(x.a[0], dG, kGtHalf) && gt_maps<T>(x.a[1], dU, kGtHalf) &&
+            gt_maps<T>(x.b[0], Wg, kGtK) && gt_maps<T>(x.b[1], Wu, kGtK) &&
+            gt_maps<T>(w.a[0], dG, kGtK) && gt_maps<T>(w.a[1], dU, kGtK) &&
+            gt_maps<T>(w.b[0], X, kGtK);
     if (!*used) return cudaSuccess;
-    gt_output(&x.out[0], q.dX, a.rows, a.D, bf16);
+    gt_output<T>(&x.out[0], q.dX, a.rows, a.D);
     x.tiles_m = (int)((a.rows + kGtTile - 1) / kGtTile);
-    x.tiles_n = (a.D + kGtTile - 1) / kGtTile;
     x.k_steps = (a.F + kGtK - 1) / kGtK;
     x.err = a.err;
-    gt_output(&w.out[0], q.dWg, a.F, a.D, bf16);
-    gt_output(&w.out[1], q.dWu, a.F, a.D, bf16);
+    gt_output<T>(&w.out[0], q.dWg, a.F, a.D);
+    gt_output<T>(&w.out[1], q.dWu, a.F, a.D);
     w.tiles_m = 2 * ((a.F + kGtTile - 1) / kGtTile);
-    w.tiles_n = (a.D + kGtTile - 1) / kGtTile;
     w.k_steps = (int)((a.rows + kGtK - 1) / kGtK);
     w.err = a.err;
-    const cudaError_t e = launch_gt<T, kGtDx>(x, follows, s);
-    return e != cudaSuccess ? e : launch_gt<T, kGtDw>(w, true, s);
+    const auto run = [&](GtArgs &p, auto mode, bool after) {
+        constexpr int MODE = decltype(mode)::value;
+        const int nt = gt_columns(p.tiles_m, a.D);
+        p.tiles_n = (a.D + nt - 1) / nt;
+        return nt == 128 ? launch_gt_as<T, MODE, 128>(p, after, s) : launch_gt_as<T, MODE, 256>(p, after, s);
+    };
+    const cudaError_t e = run(x, std::integral_constant<int, kGtDx>(), follows);
+    return e != cudaSuccess ? e : run(w, std::integral_constant<int, kGtDw>(), true);
 }
 
 }  // namespace gs
