@@ -30,6 +30,42 @@ template <int ACT> __device__ __forceinline__ float act_of(float g) {
     return g;
 }
 
+// act(g) for a whole kernel, chosen by numbers where one formula serves: the sigmoid
+// family is sigmoid(g (c1 + c2 g^2)), times g or not; relu and identity are the larger
+// of g and a bound.  Six copies of an unrolled epilogue did not stay in the instruction
+// cache.
+struct ActNumbers {
+    int form;          // 0 sigmoid family, 1 gelu, 2 bounded
+    bool times_g;
+    float c1, c2, low;
+};
+inline ActNumbers act_numbers(int act) {
+    if (act == GS_ACT_GELU) return {1, true, 0.0f, 0.0f, 0.0f};
+    if (act == GS_ACT_RELU) return {2, true, 0.0f, 0.0f, 0.0f};
+    if (act == GS_ACT_IDENTITY) return {2, true, 0.0f, 0.0f, -__builtin_inff()};
+    const bool cubic = act == GS_ACT_GELU_TANH;
+    return {0, act != GS_ACT_SIGMOID, cubic ? kGeluTanh2 : 1.0f, cubic ? kGeluTanh2 * kGeluCubic : 0.0f,
+            0.0f};
+}
+// g[i] = act(g[i]) u[i].
+template <int N>
+__device__ __forceinline__ void act_product(const ActNumbers &a, float (&g)[N], const float (&u)[N]) {
+    if (a.form == 0) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            // the square is bounded: it may not make 0 * infinity of c2 = 0
+            const float r = sigmoid_of(g[i] * fmaf(a.c2, fminf(g[i] * g[i], 1e30f), a.c1));
+            g[i] = (a.times_g ? g[i] * r : r) * u[i];
+        }
+    } else if (a.form == 1) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) g[i] = act_of<GS_ACT_GELU>(g[i]) * u[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) g[i] = (g[i] < a.low ? a.low : g[i]) * u[i];   // NaN stays
+    }
+}
+
 // act(g) and its slope.
 template <int ACT> __device__ __forceinline__ void act_and_slope(float g, float &a, float &da) {
     if (ACT == GS_ACT_SILU) {

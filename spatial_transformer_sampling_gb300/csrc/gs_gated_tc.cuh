@@ -34,26 +34,33 @@ constexpr int kGtHalf = 128;          // rows of A of one CTA
 constexpr int kGtK = 64;              // contraction steps per stage: 128 bytes
 constexpr int kGtA = kGtHalf * kGtK * 2;   // bytes of A's stage
 constexpr int kGtChunk = 64 * kGtK * 2;    // bytes of 64 rows of an MN-major operand
-constexpr int kGtBox = 32 * 128;      // bytes of a warp's staged output box: 32 rows of 128 bytes
 constexpr int kGtSmem = 224 * 1024;
 constexpr int kGtRun = 4;             // stages of a plane's run (fp32)
 
 enum { kGtForward = 0, kGtForwardKeep = 1, kGtDx = 2, kGtDw = 3 };
 
-// T: type of the outputs.
+// T: type of the outputs.  An epilogue warp has 32 rows and kCols columns of a tile
+// (forward: as many of G as of U), which it stages for its stores in boxes of 32 rows:
+// sixteen warps of 64 columns in 16-bit types, where what waits for TMEM, the staging
+// and the stores is hidden by the other warps (eight warps of 128: 157 us and not TBD for
+// 262144 x 64 x 256, kept); eight warps of 128 in fp32, whose sums stay in registers.
 template <typename T, int MODE, int NT> struct GtShape {
-    static constexpr int kParts = NT / 128;          // epilogue warps that share 32 rows
+    static constexpr bool kForward = MODE == kGtForward || MODE == kGtForwardKeep;
+    static constexpr int kPlanes = sizeof(T) == 4 ? 3 : 1;
+    static constexpr int kCols = sizeof(T) == 4 ? 128 : 64;
+    static constexpr int kParts = NT / kCols;        // epilogue warps that share 32 rows
     static constexpr int kEpilogueWarps = 4 * kParts;
     static constexpr int kMmaWarp = kEpilogueWarps, kCopyWarp = kMmaWarp + 1;
     static constexpr int kThreads = (kEpilogueWarps + 2) * 32;
     static constexpr int kB = NT / 2 * kGtK * 2;     // bytes of B's stage
     static constexpr int kStage = kGtA + kB;
-    static constexpr int kBoxes = MODE == kGtForwardKeep ? 3 : MODE == kGtForward ? 1 : 2;
-    static constexpr int kBoxBytes = kBoxes * kEpilogueWarps * kGtBox;
+    static constexpr int kBoxRow = sizeof(T) == 2 && kForward ? 64 : 128;   // bytes
+    static constexpr int kBox = 32 * kBoxRow;
+    static constexpr int kBoxCols = kBoxRow / (int)sizeof(T);
+    static constexpr int kBoxes = MODE == kGtForwardKeep ? 3 : kForward ? 1 : sizeof(T) == 4 ? 2 : 1;
+    static constexpr int kBoxBytes = kBoxes * kEpilogueWarps * kBox;
     static constexpr int kStages = (kGtSmem - kBoxBytes) / kStage < 8 ? (kGtSmem - kBoxBytes) / kStage : 8;
     static constexpr int kSmem = kStages * kStage + kBoxBytes + 1024;
-    static constexpr int kPlanes = sizeof(T) == 4 ? 3 : 1;
-    static constexpr int kBoxCols = 128 / (int)sizeof(T);
 };
 
 // ------------------------------------------------------------------ pairs of CTAs
@@ -182,7 +189,8 @@ struct GtArgs {
     CUtensorMap a[2][kGtMostPlanes], b[2][kGtMostPlanes];
     GtOutput out[3];              // forward: H, G, U; dX: dX; dW: dWg, dWu
     const void *bg, *bu;
-    int F, act, bias_runs;        // bias_runs: the biases are 16-byte aligned
+    int F;
+    ActNumbers act;
     int tiles_m, tiles_n;         // of 256 rows, and NT columns (forward: NT / 2 outputs)
     int k_steps;                  // of one pair of operands
     unsigned *err;
@@ -203,14 +211,16 @@ bool gt_maps(CUtensorMap (&map)[kGtMostPlanes], const GtMatrix &m, int box_rows)
             return false;
     return true;
 }
-template <typename T> void gt_output(GtOutput *o, void *at, int64_t rows, int width) {
+template <typename T>
+void gt_output(GtOutput *o, void *at, int64_t rows, int width, int box_row) {
     o->at = at;
     o->rows = rows;
     o->width = width;
     const uint64_t dims[2] = {(uint64_t)width, (uint64_t)rows}, stride[1] = {width * sizeof(T)};
-    const uint32_t box[2] = {128 / sizeof(T), 32};
+    const uint32_t box[2] = {box_row / (uint32_t)sizeof(T), 32};
     o->boxes = width * sizeof(T) % 16 == 0 &&
-               tmap_encode(&o->map, sizeof(T), __is_same(T, __nv_bfloat16), 2, at, dims, stride, box, true);
+               tmap_encode(&o->map, sizeof(T), __is_same(T, __nv_bfloat16), 2, at, dims, stride, box,
+                           box_row == 128, box_row == 64);
 }
 
 // Tile t of tiles_m x tiles_n: eight rows of tiles at a time, so that the tiles in
@@ -272,33 +282,39 @@ __device__ __forceinline__ void gt_steps(const GtArgs &p, int unit, F &&f) {
             if (!f(which, gt_plane_a(product), gt_plane_b(product), k)) return;
 }
 
+// Where 16-byte chunk c of a box's row lies: swizzled as TMA reads it.
+template <int ROW> __device__ __forceinline__ int gt_chunk(int row, int c) {
+    return row * ROW + (c ^ (ROW == 128 ? row % 8 : row / 2 % 4)) * 16;
+}
+
 // A box's staged columns of 32 rows from shared memory to where TMA cannot store.
-template <typename T>
+template <typename T, int ROW>
 __device__ __forceinline__ void gt_store_plain(const GtOutput &o, const unsigned char *box,
                                                int64_t row0, int col0) {
-    constexpr int N = 4 / (int)sizeof(T);   // columns of a lane
-    const int lane = threadIdx.x % 32;
-    for (int r = 0; r < 32 && row0 + r < o.rows; ++r) {
-        const T *from = reinterpret_cast<const T *>(box + r * 128 + (((lane / 4) ^ (r % 8)) * 16) +
-                                                    lane % 4 * 4);
-        T *to = (T *)o.at + (row0 + r) * o.width + col0 + lane * N;
+    constexpr int N = 4 / (int)sizeof(T), kLanes = ROW / 4;   // columns of a lane, lanes of a row
+    const int lane = threadIdx.x % 32, at = lane % kLanes, col = col0 + at * N;
+    for (int r = lane / kLanes; r < 32 && row0 + r < o.rows; r += 32 / kLanes) {
+        const T *from = reinterpret_cast<const T *>(box + gt_chunk<ROW>(r, at / 4) + at % 4 * 4);
+        T *to = (T *)o.at + (row0 + r) * o.width + col;
 #pragma unroll
         for (int e = 0; e < N; ++e)
-            if (col0 + lane * N + e < o.width) to[e] = from[e];
+            if (col + e < o.width) to[e] = from[e];
     }
 }
 
-// A warp's box of 32 rows, written by all its lanes, to the output.
-template <typename T>
-__device__ __forceinline__ void gt_store_box(const GtOutput &o, const unsigned char *box, int64_t row0,
-                                             int col0) {
-    if (o.boxes) fence_proxy_async_smem();
+// N boxes of a warp, one for each output, all of them at row0 and col0.
+template <typename T, int ROW, int N>
+__device__ __forceinline__ void gt_store_boxes(const GtOutput *out, const unsigned char *box,
+                                               int64_t row0, int col0) {
+    fence_proxy_async_smem();   // all lanes' writes, before the TMA reads them
     __syncwarp();
-    if (row0 >= o.rows || col0 >= o.width) return;
-    if (o.boxes) {
-        if (threadIdx.x % 32 == 0) tma_store_2d(&o.map, col0, (int)row0, smem_u32(box));
-    } else {
-        gt_store_plain<T>(o, box, row0, col0);
+    if (row0 >= out->rows || col0 >= out->width) return;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        if (!out[i].boxes)
+            gt_store_plain<T, ROW>(out[i], box + i * 32 * ROW, row0, col0);
+        else if (threadIdx.x % 32 == 0)
+            tma_store_2d(&out[i].map, col0, (int)row0, smem_u32(box + i * 32 * ROW));
     }
 }
 // Until a warp's boxes may be written again.
@@ -310,44 +326,61 @@ __device__ __forceinline__ void gt_boxes_free() {
     __syncwarp();
 }
 
-// 32 columns of this lane's row into its box, rounded: the second half of the box's
-// columns with `half` (16-bit types).
-template <typename T>
-__device__ __forceinline__ void gt_stage(unsigned char *box, int half, const uint32_t (&v)[32]) {
+// N columns of this lane's row into its box from column `col` on, rounded.
+template <typename T, int ROW, int N>
+__device__ __forceinline__ void gt_stage(unsigned char *box, int col, const float (&v)[N]) {
     const int lane = threadIdx.x % 32;
-    unsigned char *row = box + lane * 128;
-    if constexpr (sizeof(T) == 4) {
+    constexpr int V = kVec<T>;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            *reinterpret_cast<uint4 *>(row + ((i ^ (lane % 8)) * 16)) =
-                make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-    } else {
-        uint32_t w[16];
+    for (int i = 0; i < N / V; ++i) {
+        uint4 w;
+        uint32_t *u = &w.x;
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-            w[i] = pack2<T>(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<uint4 *>(row + (((4 * half + i) ^ (lane % 8)) * 16)) =
-                make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        for (int e = 0; e < 4; ++e) {
+            if constexpr (sizeof(T) == 4)
+                u[e] = __float_as_uint(v[i * V + e]);
+            else
+                u[e] = pack2<T>(v[i * V + 2 * e], v[i * V + 2 * e + 1]);
+        }
+        *reinterpret_cast<uint4 *>(box + gt_chunk<ROW>(lane, col / V + i)) = w;
     }
 }
 
-// v += 32 biases from column f on; the same for all lanes.
-template <typename T>
-__device__ __forceinline__ void gt_add_bias(uint32_t (&v)[32], const T *bias, int f, int F, bool runs) {
+// Loads 32 columns of this lane's row from TMEM.
+__device__ __forceinline__ void gt_columns_of(uint32_t at, float (&v)[32]) {
+    tmem_ld_x32(at, reinterpret_cast<uint32_t (&)[32]>(v));
+}
+
+// v += 16 columns of this lane's row in TMEM.
+__device__ __forceinline__ void gt_add_columns(uint32_t at, float *v) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+        "%11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(at)
+        : "memory");
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                   "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                   "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :
+                 : "memory");
 #pragma unroll
-    for (int c = 0; c < 32; c += kVec<T>) {
-        float b[kVec<T>] = {};
-        if (runs && f + c + kVec<T> <= F) {
-            Run<T, kVec<T>>::widen(__ldg(reinterpret_cast<const uint4 *>(bias + f + c)), b);
-        } else {
+    for (int c = 0; c < 16; ++c) v[c] += __uint_as_float(r[c]);
+}
+
+// v += 32 values that lane i holds the i-th of, by way of 128 bytes of the warp's own.
+__device__ __forceinline__ void gt_add_lanes(float (&v)[32], const float *shared) {
 #pragma unroll
-            for (int e = 0; e < kVec<T>; ++e)
-                if (f + c + e < F) b[e] = IO<T>::ld(bias + f + c + e);
-        }
-#pragma unroll
-        for (int e = 0; e < kVec<T>; ++e) v[c + e] = __float_as_uint(__uint_as_float(v[c + e]) + b[e]);
+    for (int c = 0; c < 32; c += 4) {
+        const float4 b = *reinterpret_cast<const float4 *>(shared + c);
+        v[c] += b.x;
+        v[c + 1] += b.y;
+        v[c + 2] += b.z;
+        v[c + 3] += b.w;
     }
 }
 
@@ -355,8 +388,8 @@ template <typename T, int MODE, int NT>
 __global__ void __launch_bounds__(GtShape<T, MODE, NT>::kThreads, 1)
     gated_tc_kernel(const __grid_constant__ GtArgs p) {
     using Sh = GtShape<T, MODE, NT>;
-    constexpr bool kForward = MODE == kGtForward || MODE == kGtForwardKeep;
-    constexpr int NS = Sh::kStages, kPlanes = Sh::kPlanes, kBoxCols = Sh::kBoxCols;
+    constexpr bool kForward = Sh::kForward;
+    constexpr int NS = Sh::kStages, kPlanes = Sh::kPlanes, kRow = Sh::kBoxRow;
     extern __shared__ unsigned char smem_raw[];
     __shared__ __align__(8) uint64_t full[NS], empty[NS], tile_full[2], tile_empty[2], drained;
     __shared__ uint32_t tmem_base;
@@ -486,113 +519,94 @@ __global__ void __launch_bounds__(GtShape<T, MODE, NT>::kThreads, 1)
         __syncwarp();
     } else {
         // ---------------------------------------------------- epilogue
-        // A warp has 32 rows and 128 columns of the tile: G and U of 64 outputs, or 128
-        // columns of a gradient; `column(i)` is where the i-th 32 of them start.
         const int quarter = warp % 4, part = warp / 4;
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-        unsigned char *box = boxes + warp * Sh::kBoxes * kGtBox;
-        const auto column = [&](int i) {
-            return kForward ? i / 2 * (NT / 2) + part * 64 + i % 2 * 32 : part * 128 + i * 32;
-        };
+        unsigned char *box = boxes + warp * Sh::kBoxes * Sh::kBox;
+        // where the warp's i-th 32 columns start in TMEM; forward, U's follow G's
+        constexpr int kRuns = Sh::kCols / 32, kHalf = kForward ? kRuns / 2 : kRuns;
+        const auto column = [&](int i) { return i / kHalf * (NT / 2) + (part * kHalf + i % kHalf) * 32; };
         int count = 0;
         for (int t = pair; t < tiles && ok; t += pairs) {
             const GtTile w = gt_tile(p, t);
             const int64_t row0 = (int64_t)w.m * kGtTile + rank * kGtHalf + quarter * 32;
-            uint32_t at = 0;
-            const auto arrive = [&] {   // waits for a part of the tile
+            const int f0 = w.n * (NT / 2) + part * kHalf * 32;   // forward: the first output
+            float bias[kHalf][2] = {};                           // of outputs f0 + 32 i + lane
+            if (kForward && bg)
+#pragma unroll
+                for (int i = 0; i < kHalf; ++i)
+                    if (f0 + i * 32 + lane < p.F) {
+                        bias[i][0] = IO<T>::ld((const T *)bg + f0 + i * 32 + lane);
+                        bias[i][1] = IO<T>::ld((const T *)bu + f0 + i * 32 + lane);
+                    }
+            // the warp's columns: of one part in TMEM, or the sums of them all
+            float v[kRuns][32];
+            if (kPlanes > 1)
+#pragma unroll
+                for (int i = 0; i < kRuns; ++i)
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) v[i][c] = 0.0f;
+            for (int u = 0; u < units; ++u, ++count) {
                 const int b = count & 1;
                 ok = __all_sync(0xffffffffu, tc_wait(&tile_full[b], (count / 2) & 1, p.err));
+                if (!ok) break;
                 tcgen05_fence_after_sync();
-                at = tmem + b * NT + lanes;
-            };
-            const auto release = [&] {   // TMEM is read: the part after next may be multiplied
+                const uint32_t at = tmem + b * NT + lanes;
+                if constexpr (kPlanes > 1) {
+#pragma unroll
+                    for (int i = 0; i < kRuns; ++i) {
+                        gt_add_columns(at + column(i), v[i]);
+                        gt_add_columns(at + column(i) + 16, v[i] + 16);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < kRuns; ++i) gt_columns_of(at + column(i), v[i]);
+                }
+                // TMEM is read: the part after next may be multiplied
                 tcgen05_fence_before_sync();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_remote(smem_of_rank(smem_u32(&tile_empty[count & 1]), 0));
-                ++count;
-            };
-            // the four runs of 32 columns: of one part in TMEM, or the sums of them all
-            uint32_t v[4][32];
-            if constexpr (kPlanes > 1) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int c = 0; c < 32; ++c) v[i][c] = 0;
-                for (int u = 0; u < units; ++u) {
-                    arrive();
-                    if (!ok) break;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint32_t x[32];
-                        tmem_ld_x32(at + column(i), x);
-#pragma unroll
-                        for (int c = 0; c < 32; ++c)
-                            v[i][c] = __float_as_uint(__uint_as_float(v[i][c]) + __uint_as_float(x[c]));
-                    }
-                    release();
-                }
-            } else {
-                arrive();
+                if (lane == 0) mbar_arrive_remote(smem_of_rank(smem_u32(&tile_empty[b]), 0));
             }
             if (!ok) break;
-            // runs i and j, read from TMEM now where there is one part; `last`: no more of them
-            const auto read = [&](int i, int j, bool last) {
-                if constexpr (kPlanes == 1) {
-                    tmem_start_ld_x32(at + column(i), v[i]);
-                    tmem_start_ld_x32(at + column(j), v[j]);
-                    tmem_wait_ld(v[i]);
-                    tmem_wait_ld(v[j]);
-                    if (last) release();
-                }
-            };
-            gt_boxes_free();
             if constexpr (kForward) {
-                const int f0 = w.n * (NT / 2) + part * 64;
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    read(c, 2 + c, c == 1);
-                    uint32_t(&g)[32] = v[c], (&u)[32] = v[2 + c];
-                    const int f = f0 + c * 32, half = kBoxCols == 64 ? c : 0;
+                for (int i = 0; i < kHalf; ++i) {
+                    float(&g)[32] = v[i], (&u)[32] = v[kHalf + i];
+                    gt_boxes_free();
                     if (bg) {
-                        gt_add_bias(g, (const T *)bg, f, p.F, p.bias_runs);
-                        gt_add_bias(u, (const T *)bu, f, p.F, p.bias_runs);
+                        float *shared = reinterpret_cast<float *>(box);
+                        shared[lane] = bias[i][0];
+                        shared[32 + lane] = bias[i][1];
+                        __syncwarp();
+                        gt_add_lanes(g, shared);
+                        gt_add_lanes(u, shared + 32);
+                        __syncwarp();
                     }
                     if (MODE == kGtForwardKeep) {
-                        gt_stage<T>(box + kGtBox, half, g);
-                        gt_stage<T>(box + 2 * kGtBox, half, u);
+                        gt_stage<T, kRow>(box + Sh::kBox, 0, g);
+                        gt_stage<T, kRow>(box + 2 * Sh::kBox, 0, u);
                     }
-                    with_act(p.act, [&](auto act) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            g[i] = __float_as_uint(act_of<decltype(act)::value>(__uint_as_float(g[i])) *
-                                                   __uint_as_float(u[i]));
-                    });
-                    gt_stage<T>(box, half, g);
-                    if (kBoxCols == 64 && c == 0) continue;   // half a box
-#pragma unroll
-                    for (int o = 0; o < Sh::kBoxes; ++o)
-                        gt_store_box<T>(p.out[o], box + o * kGtBox, row0, kBoxCols == 64 ? f0 : f);
-                    if (c == 0) gt_boxes_free();
+                    act_product(p.act, g, u);
+                    gt_stage<T, kRow>(box, 0, g);
+                    gt_store_boxes<T, kRow, Sh::kBoxes>(p.out, box, row0, f0 + i * 32);
                 }
             } else {
                 const int half = p.tiles_m / 2, which = MODE == kGtDw && w.m >= half;
-                const GtOutput &out = p.out[which];
+                const GtOutput *out = &p.out[which];
                 const int64_t out_row = row0 - (int64_t)which * half * kGtTile;
-                const int col0 = w.n * NT + part * 128;
+                const int col0 = w.n * NT + part * Sh::kCols;
+                // two runs at a time: a box of both, or one each
 #pragma unroll
-                for (int c = 0; c < 4; c += 2) {
-                    read(c, c + 1, c == 2);
-                    if constexpr (kBoxCols == 64) {
-                        unsigned char *to = box + c / 2 * kGtBox;
-                        gt_stage<T>(to, 0, v[c]);
-                        gt_stage<T>(to, 1, v[c + 1]);
-                        gt_store_box<T>(out, to, out_row, col0 + c * 32);
+                for (int i = 0; i < kRuns; i += 2) {
+                    gt_boxes_free();
+                    if constexpr (Sh::kBoxCols == 64) {
+                        gt_stage<T, kRow>(box, 0, v[i]);
+                        gt_stage<T, kRow>(box, 32, v[i + 1]);
+                        gt_store_boxes<T, kRow, 1>(out, box, out_row, col0 + i * 32);
                     } else {
-                        gt_stage<T>(box, 0, v[c]);
-                        gt_stage<T>(box + kGtBox, 0, v[c + 1]);
-                        gt_store_box<T>(out, box, out_row, col0 + c * 32);
-                        gt_store_box<T>(out, box + kGtBox, out_row, col0 + c * 32 + 32);
-                        if (c == 0) gt_boxes_free();
+                        gt_stage<T, kRow>(box, 0, v[i]);
+                        gt_stage<T, kRow>(box + Sh::kBox, 0, v[i + 1]);
+                        gt_store_boxes<T, kRow, 1>(out, box, out_row, col0 + i * 32);
+                        gt_store_boxes<T, kRow, 1>(out, box + Sh::kBox, out_row, col0 + i * 32 + 32);
                     }
                 }
             }
@@ -662,16 +676,16 @@ cudaError_t launch_gt_forward(const GatedArgs &a, const GatedPtrs &q, const GtMa
     *used = gt_maps<T>(p.a[0], X, kGtHalf) && gt_maps<T>(p.b[0], Wg, nt / 2) &&
             gt_maps<T>(p.b[1], Wu, nt / 2);
     if (!*used) return cudaSuccess;
-    gt_output<T>(&p.out[0], q.H, a.rows, a.F);
+    const int box_row = GtShape<T, kGtForward, 256>::kBoxRow;
+    gt_output<T>(&p.out[0], q.H, a.rows, a.F, box_row);
     if (q.G) {
-        gt_output<T>(&p.out[1], q.G, a.rows, a.F);
-        gt_output<T>(&p.out[2], q.U, a.rows, a.F);
+        gt_output<T>(&p.out[1], q.G, a.rows, a.F, box_row);
+        gt_output<T>(&p.out[2], q.U, a.rows, a.F, box_row);
     }
     p.bg = q.bg;
     p.bu = q.bu;
-    p.bias_runs = aligned16(q.bg) && aligned16(q.bu);
     p.F = a.F;
-    p.act = a.act;
+    p.act = act_numbers(a.act);
     p.tiles_n = (a.F + nt / 2 - 1) / (nt / 2);
     p.k_steps = (a.D + kGtK - 1) / kGtK;
     p.err = a.err;
@@ -693,12 +707,12 @@ cudaError_t launch_gt_backward(const GatedArgs &a, const GatedPtrs &q, const GtM
             gt_maps<T>(w.a[0], dG, kGtK) && gt_maps<T>(w.a[1], dU, kGtK) &&
             gt_maps<T>(w.b[0], X, kGtK);
     if (!*used) return cudaSuccess;
-    gt_output<T>(&x.out[0], q.dX, a.rows, a.D);
+    gt_output<T>(&x.out[0], q.dX, a.rows, a.D, 128);
     x.tiles_m = (int)((a.rows + kGtTile - 1) / kGtTile);
     x.k_steps = (a.F + kGtK - 1) / kGtK;
     x.err = a.err;
-    gt_output<T>(&w.out[0], q.dWg, a.F, a.D);
-    gt_output<T>(&w.out[1], q.dWu, a.F, a.D);
+    gt_output<T>(&w.out[0], q.dWg, a.F, a.D, 128);
+    gt_output<T>(&w.out[1], q.dWu, a.F, a.D, 128);
     w.tiles_m = 2 * ((a.F + kGtTile - 1) / kGtTile);
     w.k_steps = (int)((a.rows + kGtK - 1) / kGtK);
     w.err = a.err;
