@@ -1,6 +1,7 @@
 // gs_gated_launch.cuh -- workspace layout and launches of the gated projections.
 #pragma once
 
+#include "gs_gated_few.cuh"
 #include "gs_gated_grad.cuh"
 #include "gs_gated_simt.cuh"
 #include "gs_gated_tc.cuh"
@@ -91,6 +92,9 @@ cudaError_t gated_operands(const GatedArgs &a, const GatedPtrs &p, const GatedLa
 
 template <typename T>
 cudaError_t launch_gated(const GatedArgs &a, const GatedPtrs &p, void *ws, cudaStream_t s) {
+#ifndef GS_NO_FEW
+    if (a.rows <= kFewMost) return launch_gated_few<T>(a, p, s);
+#endif
     GtMatrix m[3];
     const GatedLayout<T> at(a, false);
     bool used = false;
