@@ -184,6 +184,7 @@ gs_status check_residual_norm(const gs_residual_norm_attrs *at, gs_dtype dt, gs:
     a->layer = at->kind == GS_NORM_LAYER;
     a->alpha = at->alpha;
     a->eps = at->epsilon;
+    a->err = nullptr;
     return GS_OK;
 }
 
@@ -540,6 +541,8 @@ gs_status gs_residual_norm_backward(const void *dS, const void *dY, const void *
     if (!aligned(Stats, 16)) return GS_ERR_ALIGN;
     st = check_workspace(workspace, workspace_bytes, residual_norm_ws(a, dt), 256);
     if (st != GS_OK) return st;
+    a.err = gs::device_error_word();
+    if (!a.err) return GS_ERR_CUDA;
     if (a.rows == 0 && a.groups > 0) {   // gates of no row
         const gs_status done = status_of(
             cudaMemsetAsync(dgate, 0, (size_t)a.groups * a.D * es, stream));

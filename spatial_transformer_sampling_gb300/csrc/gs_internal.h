@@ -283,6 +283,7 @@ struct ResNormArgs {
     int64_t group_rows;                 // rows that share one
     int layer;                          // layer norms: means are subtracted
     float alpha, eps;
+    unsigned *err;
 };
 struct ResNormPtrs {                    // device pointers
     const void *gate, *z_scale, *z_B, *scale, *B;

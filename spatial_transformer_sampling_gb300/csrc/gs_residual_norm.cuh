@@ -17,6 +17,8 @@
 // sums in order.
 #pragma once
 
+#include <algorithm>
+
 #include "gs_sums.cuh"
 
 namespace gs {
@@ -239,20 +241,21 @@ inline ResNormPlan resnorm_plan(const ResNormArgs &a, int teams_per_block, int m
 
 // A walker's place: segment, step in it, the row there (-1: none) and its gate.
 struct ResNormWalk {
-    int64_t segment, row, end, gate;
-    int step;
-    __device__ __forceinline__ void start(const ResNormPlan &q, int64_t s) {
+    uint32_t segment, gate;
+    int row, step;
+    __device__ __forceinline__ void start(const ResNormPlan &q, uint32_t s, int i = 0) {
         segment = s;
-        step = 0;
-        gate = s / q.chunks;
-        const int64_t within = s - gate * q.chunks;
-        row = gate < q.groups && within < q.group_rows ? gate * q.group_rows + within : -1;
-        end = (gate + 1) * q.group_rows;
+        step = i;
+        gate = s / (uint32_t)q.chunks;
+        const int64_t within = s - gate * (uint32_t)q.chunks + (int64_t)i * q.chunks;
+        row = gate < (uint32_t)q.groups && within < q.group_rows ? (int)(gate * q.group_rows + within) : -1;
     }
     __device__ __forceinline__ void next(const ResNormPlan &q) {
         if (++step < q.steps) {
-            if (row >= 0) row += q.chunks;
-            if (row >= end) row = -1;
+            if (row >= 0) {
+                const int64_t to = (int64_t)row + q.chunks;
+                row = to < (gate + (int64_t)1) * q.group_rows ? (int)to : -1;
+            }
         } else {
             start(q, segment + q.teams);
         }
@@ -279,7 +282,7 @@ __global__ void __launch_bounds__(res_block(L), resnorm_backward_blocks(L, NV * 
     typename IOV::Raw rd[NV], ry[NV], rs[NV], rz[NV], rg[NV];
     float4 st;
     const auto load = [&](const ResNormWalk &w) {
-        const int64_t row = w.row, at = row * a.D, gate = w.gate * a.D;
+        const int64_t row = w.row, at = row * a.D, gate = (int64_t)w.gate * a.D;
         const bool here = row >= 0;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
@@ -295,7 +298,7 @@ __global__ void __launch_bounds__(res_block(L), resnorm_backward_blocks(L, NV * 
                   : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     };
     ResNormWalk w;
-    w.start(q, (int64_t)blockIdx.x * kTeams + team);
+    w.start(q, blockIdx.x * kTeams + team);
     load(w);
     int slot = 0;
     for (int64_t n = (int64_t)q.rounds * q.steps; n > 0; --n) {
@@ -429,6 +432,334 @@ __global__ void __launch_bounds__(res_block(L), resnorm_backward_blocks(L, NV * 
         }
 }
 
+// ------------------------------------------------------------------ backward, staged
+
+// Rows wider than a warp's run: each team's rows come to shared memory by bulk copies
+// that its first threads issue, one array each, as many rows ahead as there is room
+// for, so that the registers hold sums and not loads in flight.  A block of 512 threads
+// per SM.
+constexpr int kStagedThreads = 512;
+constexpr int kStagedRing = 200 * 1024;   // bytes of all teams' rows
+constexpr int kStagedMost = 4;            // rows of a team, being worked on and ahead
+
+// Bytes of one array's row: it starts on a 16-byte boundary of memory, up to 15 bytes
+// ahead of its first element.
+__host__ __device__ inline int staged_pitch(int D, int size) { return (D * size + 15 + 15) / 16 * 16; }
+
+// Arrays of a stage, and behind them the row's statistics.
+constexpr int kStagedStats = 16;
+struct StagedShape {
+    int stages, pitch, arrays;
+};
+inline StagedShape staged_shape(int D, int size, int L, bool gate, bool dS) {
+    StagedShape q;
+    q.pitch = staged_pitch(D, size);
+    q.arrays = 3 + dS + gate;
+    const int per = kStagedThreads / L * (q.arrays * q.pitch + kStagedStats);
+    q.stages = kStagedRing / per < kStagedMost ? kStagedRing / per : kStagedMost;
+    return q;
+}
+
+// Barrier of a team of whole warps.
+template <int L> __device__ __forceinline__ void team_barrier() {
+    if (L == 32)
+        __syncwarp();
+    else
+        asm volatile("bar.sync %0, %1;" ::"r"(threadIdx.x / L + 1), "n"(L) : "memory");
+}
+template <int L>
+__device__ __forceinline__ void staged_sum2(float &a, float &b, float (*shared)[2][L / 32], int &slot) {
+    const int lane = threadIdx.x % 32;
+    float v = lane < 16 ? a : b;
+    v += __shfl_xor_sync(0xffffffffu, lane < 16 ? b : a, 16);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (L == 32) {
+        a = __shfl_sync(0xffffffffu, v, 0);
+        b = __shfl_sync(0xffffffffu, v, 16);
+        return;
+    }
+    if (lane % 16 == 0) shared[slot][lane / 16][threadIdx.x % L / 32] = v;
+    team_barrier<L>();
+    a = b = 0.0f;
+#pragma unroll
+    for (int w = 0; w < L / 32; ++w) {
+        a += shared[slot][0][w];
+        b += shared[slot][1][w];
+    }
+    slot ^= 1;
+}
+
+// A row of D elements at `from` to `to`, from the 16-byte boundary at or before its
+// start to the one at or after its end, and this thread's arrival on `bar`.  With EDGES,
+// `first` and `last` bound the tensor, whose outermost elements are copied one at a time
+// where a boundary lies outside.
+template <typename T, bool EDGES>
+__device__ __forceinline__ void staged_fetch(unsigned char *to, const T *from, int D, const T *first,
+                                             const T *last, uint64_t *bar) {
+    const uintptr_t start = (uintptr_t)from & ~(uintptr_t)15;
+    uintptr_t a = start, b = ((uintptr_t)(from + D) + 15) & ~(uintptr_t)15;
+    if (EDGES && (a < (uintptr_t)first || b > (uintptr_t)last)) {
+        if (a < (uintptr_t)first) a += 16;
+        if (b > (uintptr_t)last) b -= 16;
+        if (b < a) b = a;
+        T *row = reinterpret_cast<T *>(to + ((uintptr_t)from & 15));
+        for (int d = 0; d < D && (uintptr_t)(from + d) < a; ++d) row[d] = from[d];
+        for (int d = D - 1; d >= 0 && (uintptr_t)(from + d) >= b; --d) row[d] = from[d];
+    }
+    const uint32_t bytes = (uint32_t)(b - a);
+    mbar_arrive_expect_tx(bar, bytes);
+    if (bytes) bulk_copy_g2s(to + (a - start), reinterpret_cast<const void *>(a), bytes, bar);
+}
+
+template <typename T, int V, int L, int NV, bool POST, bool GATE>
+__global__ void __launch_bounds__(kStagedThreads, 1)
+    resnorm_staged_kernel(ResNormArgs a, ResNormPtrs p, ResNormPlan q, StagedShape sh_, float *partials,
+                          float *gate_partials) {
+    constexpr int kTeams = kStagedThreads / L, N = NV * V, P = N / 2, kVectors = POST ? 4 : 2;
+    using IOV = Run<T, V>;
+    extern __shared__ __align__(16) unsigned char ring[];
+    __shared__ __align__(8) uint64_t full[kTeams][kStagedMost];
+    __shared__ float shared_sums[kTeams][2][2][L / 32];
+    const int part = threadIdx.x % L, team = threadIdx.x / L;
+    const int stages = sh_.stages, row_bytes = sh_.pitch, stats_at = sh_.arrays * row_bytes;
+    const int stage_bytes = stats_at + kStagedStats;
+    unsigned char *mine = ring + (size_t)team * stages * stage_bytes;
+    float(*sums)[2][L / 32] = shared_sums[team];
+    const float per_d = 1.0f / (float)a.D;
+    const int zs_at = 2, gate_at = 3, ds_at = GATE ? 4 : 3;   // dY and S are the first two
+
+    if (part == 0) {
+        for (int s = 0; s < stages; ++s) mbar_init(&full[team][s], sh_.arrays + 1);
+        fence_mbar_init();
+    }
+    team_barrier<L>();
+
+    // the team's rows: `w` is worked on, `ahead` is fetched next, an array by each of the
+    // first threads
+    ResNormWalk w, ahead;
+    w.start(q, blockIdx.x * kTeams + team);
+    ahead = w;
+    const int steps = q.rounds * q.steps;
+    const bool fetches = part < sh_.arrays, of_gate = GATE && part == gate_at;
+    const T *array = (const T *)(part == 0 ? p.dY : part == 1 ? p.S : part == zs_at ? p.Z : of_gate ? p.gate : p.dS);
+    const T *array_end = array + (of_gate ? q.groups : a.rows) * (int64_t)a.D;
+    const auto fetch = [&](int s) {   // into stage s
+        uint64_t *bar = &full[team][s];
+        if (part == sh_.arrays && ahead.row >= 0) {
+            mbar_arrive_expect_tx(bar, kStagedStats);
+            bulk_copy_g2s(mine + s * stage_bytes + stats_at, p.stats + (int64_t)ahead.row * 4, kStagedStats,
+                          bar);
+        } else if (fetches && ahead.row >= 0)
+            staged_fetch<T, V == 1>(mine + s * stage_bytes + part * row_bytes,
+                                    array + (of_gate ? (int64_t)ahead.gate : (int64_t)ahead.row) * a.D, a.D,
+                                    array, array_end, bar);
+        else if (part <= sh_.arrays)   // no row: the phase is over at once
+            mbar_arrive(bar);
+        ahead.next(q);
+    };
+    for (int n = 0; n < stages && n < steps; ++n) fetch(n);
+
+    float2 sum[kVectors][P] = {}, gate_sum[P] = {};
+    // a thread's elements of a staged row, in pairs; zeros behind the row's end
+    const auto take = [&](const unsigned char *row, const void *base, int64_t offset, float2 (&v)[P]) {
+        const T *e = reinterpret_cast<const T *>(row + ((uintptr_t)((const T *)base + offset) & 15));
+        float f[N];
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int d = (k * L + part) * V;
+            float x[V];
+            IOV::widen(d < a.D ? IOV::load(e + d) : IOV::zero(), x);
+#pragma unroll
+            for (int i = 0; i < V; ++i) f[k * V + i] = x[i];
+        }
+#pragma unroll
+        for (int i = 0; i < P; ++i) v[i] = make_float2(f[2 * i], f[2 * i + 1]);
+    };
+    const auto param = [&](const void *base, float2 (&v)[P]) {   // of the row's columns
+        float f[N];
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int d = (k * L + part) * V;
+            float x[V];
+            IOV::widen(d < a.D ? IOV::load((const T *)base + d) : IOV::zero(), x);
+#pragma unroll
+            for (int i = 0; i < V; ++i) f[k * V + i] = x[i];
+        }
+#pragma unroll
+        for (int i = 0; i < P; ++i) v[i] = make_float2(f[2 * i], f[2 * i + 1]);
+    };
+    const auto element = [](const float2 (&v)[P], int i) { return i % 2 ? v[i / 2].y : v[i / 2].x; };
+    const auto put = [&](void *base, int64_t at, const float2 (&v)[P]) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int d = (k * L + part) * V;
+            float x[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) x[i] = element(v, k * V + i);
+            if (d < a.D) IOV::store((T *)base + at + d, x);
+        }
+    };
+    const auto both = [](float x) { return make_float2(x, x); };
+    // (v - mean) * inv; behind the row's end 0, whatever the statistics
+    const auto normal = [&](float2 (&v)[P], float mean, float inv) {
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            if constexpr (V > 1) {   // a run is inside or outside as a whole
+                const bool in = (2 * i / V * L + part) * V < a.D;
+                v[i] = mul_f32x2(add_f32x2(v[i], both(in ? -mean : 0.0f)), both(in ? inv : 0.0f));
+            } else {
+                v[i] = mul_f32x2(add_f32x2(v[i], both(-mean)), both(inv));
+                if (2 * i * L + part >= a.D) v[i].x = 0.0f;
+                if ((2 * i + 1) * L + part >= a.D) v[i].y = 0.0f;
+            }
+        }
+    };
+
+    bool ok = true;
+    int slot = 0, s = 0;
+    uint32_t parity = 0;
+    for (int n = 0; n < steps; ++n) {
+        const int row = w.row;
+        const int64_t at = (int64_t)(row >= 0 ? row : 0) * a.D;
+        const unsigned char *here = mine + s * stage_bytes;
+        float2 sh[P], wy[P], ds[P], zh[P], c[P];
+        param(p.scale, c);
+        if (ok) ok = mbar_wait_bounded(&full[team][s], parity, a.err);
+        float4 st = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        float2 t0 = both(0.0f), t1 = both(0.0f);
+        if (row >= 0) {
+            st = *reinterpret_cast<const float4 *>(here + stats_at);
+            take(here + row_bytes, p.S, at, sh);
+            take(here, p.dY, at, wy);
+            normal(sh, st.z, st.w);
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                sum[0][i] = fma_f32x2(wy[i], sh[i], sum[0][i]);
+                sum[1][i] = add_f32x2(sum[1][i], wy[i]);
+                wy[i] = mul_f32x2(wy[i], c[i]);
+                t0 = add_f32x2(t0, wy[i]);
+                t1 = fma_f32x2(wy[i], sh[i], t1);
+            }
+        }
+        float s0 = t0.x + t0.y, s1 = t1.x + t1.y;
+        if (POST) param(p.z_scale, c);
+        staged_sum2<L>(s0, s1, sums, slot);
+        if (L == 32) __syncwarp();
+        // the team is past its reads of the row before: that stage is filled again
+        if (n > 0 && n - 1 + stages < steps) fetch(s == 0 ? stages - 1 : s - 1);
+        s0 = a.layer ? s0 * -per_d : 0.0f;
+        s1 *= -per_d;
+        float2 u0 = both(0.0f), u1 = both(0.0f);
+        if (row >= 0) {
+            if (p.dS) {
+                take(here + ds_at * row_bytes, p.dS, at, ds);
+            } else {
+#pragma unroll
+                for (int i = 0; i < P; ++i) ds[i] = both(0.0f);
+            }
+            take(here + zs_at * row_bytes, p.Z, at, zh);
+            if (POST) normal(zh, st.x, st.y);
+            float2 out[P];
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                ds[i] = fma_f32x2(fma_f32x2(sh[i], both(s1), add_f32x2(wy[i], both(s0))), both(st.w), ds[i]);
+                out[i] = mul_f32x2(ds[i], both(a.alpha));
+            }
+            put(p.dX, at, out);
+            if (GATE) {
+                float2 g[P], b[P];
+                take(here + gate_at * row_bytes, p.gate, (int64_t)w.gate * a.D, g);
+                if (POST && p.z_B) param(p.z_B, b);
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    const float2 z = !POST    ? zh[i]
+                                     : p.z_B ? fma_f32x2(zh[i], c[i], b[i])
+                                             : mul_f32x2(zh[i], c[i]);
+                    gate_sum[i] = fma_f32x2(ds[i], z, gate_sum[i]);
+                    ds[i] = mul_f32x2(ds[i], g[i]);
+                }
+            }
+            if (POST) {
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    sum[kVectors - 2][i] = fma_f32x2(ds[i], zh[i], sum[kVectors - 2][i]);
+                    sum[kVectors - 1][i] = add_f32x2(sum[kVectors - 1][i], ds[i]);
+                    ds[i] = mul_f32x2(ds[i], c[i]);
+                    u0 = add_f32x2(u0, ds[i]);
+                    u1 = fma_f32x2(ds[i], zh[i], u1);
+                }
+            } else {
+                put(p.dZ, at, ds);
+            }
+        }
+        if (POST) {
+            s0 = u0.x + u0.y;
+            s1 = u1.x + u1.y;
+            staged_sum2<L>(s0, s1, sums, slot);
+            s0 = a.layer ? s0 * -per_d : 0.0f;
+            s1 *= -per_d;
+            if (row >= 0) {
+                float2 out[P];
+#pragma unroll
+                for (int i = 0; i < P; ++i)
+                    out[i] = mul_f32x2(fma_f32x2(zh[i], both(s1), add_f32x2(ds[i], both(s0))), both(st.y));
+                put(p.dZ, at, out);
+            }
+        }
+        if (GATE && w.step + 1 == q.steps) {
+            if (w.segment < (int64_t)q.groups * q.chunks) {
+                if (q.chunks == 1) {
+                    put(p.dgate, (int64_t)w.segment * a.D, gate_sum);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < N; ++i) {
+                        const int d = (i / V * L + part) * V + i % V;
+                        if (d < a.D) gate_partials[(int64_t)w.segment * a.D + d] = element(gate_sum, i);
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < P; ++i) gate_sum[i] = both(0.0f);
+        }
+        w.next(q);
+        if (++s == stages) {
+            s = 0;
+            parity ^= 1;
+        }
+    }
+    // copies that a wait gave up on land before the block may leave
+    if (!ok && part == 0)
+        for (int n = steps > stages ? steps - stages : 0; n < steps; ++n)
+            mbar_wait_bounded(&full[team][n % stages], (n / stages) & 1, a.err);
+    if (!partials) return;
+    // the teams of the block in order, one vector at a time, by way of the ring
+    float *out = partials + (int64_t)blockIdx.x * kVectors * a.D;
+    float *join = reinterpret_cast<float *>(ring);
+#pragma unroll
+    for (int j = 0; j < kVectors; ++j) {
+        if (kTeams == 1) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int d = (i / V * L + part) * V + i % V;
+                if (d < a.D) out[(int64_t)j * a.D + d] = element(sum[j], i);
+            }
+            continue;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < N; ++i) join[(team * N + i) * L + part] = element(sum[j], i);
+        __syncthreads();
+        for (int c = threadIdx.x; c < N * L; c += kStagedThreads) {
+            const int i = c / L, d = (i / V * L + c % L) * V + i % V;
+            float t = 0.0f;
+#pragma unroll
+            for (int g = 0; g < kTeams; ++g) t += join[g * N * L + c];
+            if (d < a.D) out[(int64_t)j * a.D + d] = t;
+        }
+    }
+}
+
 // Rows wider than kResOnChip: a block per row for dX and dZ, which leaves the row's
 // two means in `means`; then a thread per column for the sums.
 template <typename T>
@@ -495,7 +826,7 @@ __global__ void __launch_bounds__(kResThreads)
     w.start(q, blockIdx.y);
     for (int64_t n = (int64_t)q.rounds * q.steps; n > 0; --n, w.next(q)) {
         if (w.row >= 0) {
-            const int64_t at = w.row * a.D + d;
+            const int64_t at = (int64_t)w.row * a.D + d;
             const float4 st = __ldg(reinterpret_cast<const float4 *>(p.stats) + w.row);
             const float2 t = __ldg(means + w.row);
             const float y = IO<T>::ld((const T *)p.dY + at);
@@ -507,7 +838,7 @@ __global__ void __launch_bounds__(kResThreads)
             sum[1] += y;
             if (a.groups > 0) {
                 gate_sum = fmaf(ds, fmaf(zh, zs, zb), gate_sum);
-                ds *= IO<T>::ld((const T *)p.gate + w.gate * a.D + d);
+                ds *= IO<T>::ld((const T *)p.gate + (int64_t)w.gate * a.D + d);
             }
             sum[2] = fmaf(ds, zh, sum[2]);
             sum[3] += ds;
@@ -515,9 +846,9 @@ __global__ void __launch_bounds__(kResThreads)
         if (a.groups > 0 && w.step + 1 == q.steps) {
             if (w.segment < (int64_t)q.groups * q.chunks) {
                 if (q.chunks == 1)
-                    ((T *)p.dgate)[w.segment * a.D + d] = IO<T>::st(gate_sum);
+                    ((T *)p.dgate)[(int64_t)w.segment * a.D + d] = IO<T>::st(gate_sum);
                 else
-                    gate_partials[w.segment * a.D + d] = gate_sum;
+                    gate_partials[(int64_t)w.segment * a.D + d] = gate_sum;
             }
             gate_sum = 0.0f;
         }
@@ -548,32 +879,41 @@ template <int V, typename F> cudaError_t resnorm_shape(int runs, F &&f) {
     return cudaErrorInvalidValue;   // not reached: D <= kResOnChip
 }
 
-// The same for the backward pass: as many threads per row as keep a thread's share,
-// and with it the five sums it holds per element, to one run.
-template <int V, typename F> cudaError_t resnorm_backward_shape(int runs, F &&f) {
+// The same for the backward pass.  f(staged, L, NV): a team's sums, five per element,
+// stay in registers, eight elements of a thread where rows are staged.  Rows of a
+// warp's run or less keep their loads in registers: a bulk copy of 128 bytes costs as
+// much to issue as one of a few KB; so do rows too wide for two of them in the ring.
+template <typename T, int V, typename F>
+cudaError_t resnorm_backward_shape(int D, bool gate, bool dS, F &&f) {
     using std::integral_constant;
-    if (runs <= 8) return f(integral_constant<int, 8>(), integral_constant<int, 1>());
-    if (runs <= 16) return f(integral_constant<int, 16>(), integral_constant<int, 1>());
-    if (runs <= 32) return f(integral_constant<int, 32>(), integral_constant<int, 1>());
-    if (runs <= 64) return f(integral_constant<int, 64>(), integral_constant<int, 1>());
-    if (runs <= 128) return f(integral_constant<int, 128>(), integral_constant<int, 1>());
-    if (runs <= 256) return f(integral_constant<int, 256>(), integral_constant<int, 1>());
-    if (runs <= 512) return f(integral_constant<int, 512>(), integral_constant<int, 1>());
-    if (runs <= 1024) return f(integral_constant<int, 512>(), integral_constant<int, 2>());
-    if constexpr (V <= 4)
-        if (runs <= 2048) return f(integral_constant<int, 512>(), integral_constant<int, 4>());
-    if constexpr (V == 1)
-        return runs <= 4096 ? f(integral_constant<int, 512>(), integral_constant<int, 8>())
-                            : f(integral_constant<int, 512>(), integral_constant<int, 16>());
-    return cudaErrorInvalidValue;   // not reached: D <= kResOnChip
+    using std::false_type;
+    using std::true_type;
+    const int runs = (D + V - 1) / V;
+    const auto pick = [&](auto l, auto nv) {
+        constexpr int L = decltype(l)::value, NV = decltype(nv)::value;
+        if (staged_shape(D, sizeof(T), L, gate, dS).stages >= 2) return f(true_type(), l, nv);
+        return f(false_type(), integral_constant<int, 512>(), integral_constant<int, kResOnChip / V / 512>());
+    };
+    if (runs <= 8) return f(false_type(), integral_constant<int, 8>(), integral_constant<int, 1>());
+    if (runs <= 16) return f(false_type(), integral_constant<int, 16>(), integral_constant<int, 1>());
+    if (runs <= 32) return f(false_type(), integral_constant<int, 32>(), integral_constant<int, 1>());
+    constexpr int NV = 8 / V;
+    if (D <= 256) return pick(integral_constant<int, 32>(), integral_constant<int, NV>());
+    if (D <= 512) return pick(integral_constant<int, 64>(), integral_constant<int, NV>());
+    if (D <= 1024) return pick(integral_constant<int, 128>(), integral_constant<int, NV>());
+    if (D <= 2048) return pick(integral_constant<int, 256>(), integral_constant<int, NV>());
+    if (D <= 4096) return pick(integral_constant<int, 512>(), integral_constant<int, NV>());
+    return pick(integral_constant<int, 512>(), integral_constant<int, 2 * NV>());
 }
 
-template <int V> ResNormPlan resnorm_plan_of(const ResNormArgs &a) {
+template <typename T, int V> ResNormPlan resnorm_plan_of(const ResNormArgs &a, bool dS) {
     ResNormPlan q = {};
     if (a.D > kResOnChip) return resnorm_plan(a, 1, kResWideBlocks * kResSms);
-    resnorm_backward_shape<V>((a.D + V - 1) / V, [&](auto l, auto nv) {
+    resnorm_backward_shape<T, V>(a.D, a.groups > 0, dS, [&](auto staged, auto l, auto nv) {
         constexpr int L = decltype(l)::value, NV = decltype(nv)::value;
-        q = resnorm_plan(a, res_block(L) / L, kResSms * resnorm_backward_blocks(L, NV * V));
+        q = decltype(staged)::value
+                ? resnorm_plan(a, kStagedThreads / L, kResSms)
+                : resnorm_plan(a, res_block(L) / L, kResSms * resnorm_backward_blocks(L, NV * V));
         return cudaSuccess;
     });
     return q;
@@ -594,10 +934,13 @@ struct ResNormLayout {
 };
 
 template <typename T> size_t resnorm_ws_bytes(const ResNormArgs &a) {
-    // whatever the alignment will be
-    const size_t b1 = ResNormLayout(a, resnorm_plan_of<1>(a)).bytes;
-    const size_t bv = ResNormLayout(a, resnorm_plan_of<kVec<T>>(a)).bytes;
-    return b1 > bv ? b1 : bv;
+    size_t most = 0;   // whatever the alignment will be, and with dS or without
+    for (const bool dS : {false, true}) {
+        const size_t b1 = ResNormLayout(a, resnorm_plan_of<T, 1>(a, dS)).bytes;
+        const size_t bv = ResNormLayout(a, resnorm_plan_of<T, kVec<T>>(a, dS)).bytes;
+        most = std::max(most, std::max(b1, bv));
+    }
+    return most;
 }
 
 template <typename T, int V>
@@ -626,19 +969,43 @@ cudaError_t launch_resnorm(const ResNormArgs &a, const ResNormPtrs &p, cudaStrea
     return run_resnorm<T, 1>(a, p, s);
 }
 
+template <typename T, int V, int L, int NV, bool POST, bool GATE>
+cudaError_t run_resnorm_staged(const ResNormArgs &a, const ResNormPtrs &p, const ResNormPlan &q,
+                               float *partials, float *gate_partials, cudaStream_t s) {
+    const auto kernel = resnorm_staged_kernel<T, V, L, NV, POST, GATE>;
+    const StagedShape shape = staged_shape(a.D, sizeof(T), L, GATE, p.dS);
+    int smem = kStagedThreads / L * shape.stages * (shape.arrays * shape.pitch + kStagedStats);
+    const int join = kStagedThreads > L ? kStagedThreads * NV * V * (int)sizeof(float) : 0;
+    if (smem < join) smem = join;
+    static DeviceFlags ready;
+    const cudaError_t e = once_per_device(ready, [&] {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kStagedRing);
+    });
+    if (e != cudaSuccess) return e;
+    kernel<<<q.blocks, kStagedThreads, smem, s>>>(a, p, q, shape, partials, gate_partials);
+    return cudaGetLastError();
+}
+
 template <typename T, int V>
 cudaError_t run_resnorm_backward(const ResNormArgs &a, const ResNormPtrs &p, const ResNormPlan &q,
                                  float *partials, float *gate_partials, cudaStream_t s) {
-    return resnorm_backward_shape<V>((a.D + V - 1) / V, [&](auto l, auto nv) {
-        constexpr int L = decltype(l)::value, NV = decltype(nv)::value;
-        const bool post = p.z_scale, gate = a.groups > 0;
-        const auto kernel = post ? (gate ? resnorm_backward_kernel<T, V, L, NV, true, true>
-                                         : resnorm_backward_kernel<T, V, L, NV, true, false>)
-                                 : (gate ? resnorm_backward_kernel<T, V, L, NV, false, true>
-                                         : resnorm_backward_kernel<T, V, L, NV, false, false>);
-        kernel<<<q.blocks, res_block(L), 0, s>>>(a, p, q, partials, gate_partials);
-        return cudaGetLastError();
-    });
+    const auto form = [&](auto post, auto gate) {
+        constexpr bool POST = decltype(post)::value, GATE = decltype(gate)::value;
+        return resnorm_backward_shape<T, V>(a.D, GATE, p.dS, [&](auto staged, auto l, auto nv) {
+            constexpr int L = decltype(l)::value, NV = decltype(nv)::value;
+            if constexpr (decltype(staged)::value) {
+                return run_resnorm_staged<T, V, L, NV, POST, GATE>(a, p, q, partials, gate_partials, s);
+            } else {
+                resnorm_backward_kernel<T, V, L, NV, POST, GATE>
+                    <<<q.blocks, res_block(L), 0, s>>>(a, p, q, partials, gate_partials);
+                return cudaGetLastError();
+            }
+        });
+    };
+    using std::false_type;
+    using std::true_type;
+    if (p.z_scale) return a.groups > 0 ? form(true_type(), true_type()) : form(true_type(), false_type());
+    return a.groups > 0 ? form(false_type(), true_type()) : form(false_type(), false_type());
 }
 
 template <typename T>
@@ -653,7 +1020,7 @@ cudaError_t launch_resnorm_backward(const ResNormArgs &a, const ResNormPtrs &p, 
     ResNormPlan q = {};
     SumArgs sum = {};
     if (a.rows > 0) {
-        q = runs ? resnorm_plan_of<kVec<T>>(a) : resnorm_plan_of<1>(a);
+        q = runs ? resnorm_plan_of<T, kVec<T>>(a, p.dS) : resnorm_plan_of<T, 1>(a, p.dS);
         const ResNormLayout at(a, q);
         char *base = (char *)ws;
         float *partials = sums ? (float *)base : nullptr, *gates = (float *)(base + at.gate);
