@@ -439,24 +439,29 @@ __global__ void __launch_bounds__(res_block(L), resnorm_backward_blocks(L, NV * 
 // for, so that the registers hold sums and not loads in flight.  A block of 512 threads
 // per SM.
 constexpr int kStagedThreads = 512;
-constexpr int kStagedRing = 200 * 1024;   // bytes of all teams' rows
+constexpr int kStagedRing = 200 * 1024;   // bytes of all teams' rows, and of their totals
+constexpr int kStagedN = 8;               // elements of a thread
 constexpr int kStagedMost = 4;            // rows of a team, being worked on and ahead
 
 // Bytes of one array's row: it starts on a 16-byte boundary of memory, up to 15 bytes
 // ahead of its first element.
 __host__ __device__ inline int staged_pitch(int D, int size) { return (D * size + 15 + 15) / 16 * 16; }
 
-// Arrays of a stage, and behind them the row's statistics.
-constexpr int kStagedStats = 16;
+// Arrays of a stage, and behind them the row's statistics and its place: row (-1: none),
+// gate, segment (-1: none), whether the segment ends with it.
+constexpr int kStagedStats = 32;
 struct StagedShape {
     int stages, pitch, arrays;
 };
-inline StagedShape staged_shape(int D, int size, int L, bool gate, bool dS) {
+// Floats of the totals that a team keeps over its gates (dz_scale's and dz_B's).
+inline int staged_totals(bool post, bool gate) { return post && gate ? 2 * kStagedN * kStagedThreads : 0; }
+inline StagedShape staged_shape(int D, int size, int L, bool post, bool gate, bool dS) {
     StagedShape q;
     q.pitch = staged_pitch(D, size);
     q.arrays = 3 + dS + gate;
     const int per = kStagedThreads / L * (q.arrays * q.pitch + kStagedStats);
-    q.stages = kStagedRing / per < kStagedMost ? kStagedRing / per : kStagedMost;
+    const int room = (kStagedRing - 4 * staged_totals(post, gate)) / per;
+    q.stages = room < kStagedMost ? room : kStagedMost;
     return q;
 }
 
@@ -481,12 +486,16 @@ __device__ __forceinline__ void staged_sum2(float &a, float &b, float (*shared)[
     }
     if (lane % 16 == 0) shared[slot][lane / 16][threadIdx.x % L / 32] = v;
     team_barrier<L>();
-    a = b = 0.0f;
+    const float2 *sa = reinterpret_cast<const float2 *>(shared[slot][0]);
+    const float2 *sb = reinterpret_cast<const float2 *>(shared[slot][1]);
+    float2 ta = sa[0], tb = sb[0];
 #pragma unroll
-    for (int w = 0; w < L / 32; ++w) {
-        a += shared[slot][0][w];
-        b += shared[slot][1][w];
+    for (int w = 1; w < L / 64; ++w) {
+        ta = add_f32x2(ta, sa[w]);
+        tb = add_f32x2(tb, sb[w]);
     }
+    a = ta.x + ta.y;
+    b = tb.x + tb.y;
     slot ^= 1;
 }
 
@@ -512,6 +521,9 @@ __device__ __forceinline__ void staged_fetch(unsigned char *to, const T *from, i
     if (bytes) bulk_copy_g2s(to + (a - start), reinterpret_cast<const void *>(a), bytes, bar);
 }
 
+// The sums of ds and of ds * z^ over the rows that share a gate give the gradients of all
+// that stands between z^ and S: dgate = zs * sum ds z^ + zb * sum ds, and with the gate
+// as a factor they add up to dzs and dzb over the gates.
 template <typename T, int V, int L, int NV, bool POST, bool GATE>
 __global__ void __launch_bounds__(kStagedThreads, 1)
     resnorm_staged_kernel(ResNormArgs a, ResNormPtrs p, ResNormPlan q, StagedShape sh_, float *partials,
@@ -520,11 +532,15 @@ __global__ void __launch_bounds__(kStagedThreads, 1)
     using IOV = Run<T, V>;
     extern __shared__ __align__(16) unsigned char ring[];
     __shared__ __align__(8) uint64_t full[kTeams][kStagedMost];
-    __shared__ float shared_sums[kTeams][2][2][L / 32];
+    __shared__ __align__(16) float shared_sums[kTeams][2][2][L / 32];
     const int part = threadIdx.x % L, team = threadIdx.x / L;
     const int stages = sh_.stages, row_bytes = sh_.pitch, stats_at = sh_.arrays * row_bytes;
-    const int stage_bytes = stats_at + kStagedStats;
-    unsigned char *mine = ring + (size_t)team * stages * stage_bytes;
+    const int stage_bytes = stats_at + kStagedStats;   // a multiple of 16
+    static_assert(N == kStagedN, "elements of a thread");
+    constexpr int kTotals = POST && GATE ? 2 * N * kStagedThreads : 0;
+    // this thread's totals, kStagedThreads floats apart
+    float *totals = reinterpret_cast<float *>(ring) + threadIdx.x;
+    unsigned char *mine = ring + kTotals * 4 + (size_t)team * stages * stage_bytes;
     float(*sums)[2][L / 32] = shared_sums[team];
     const float per_d = 1.0f / (float)a.D;
     const int zs_at = 2, gate_at = 3, ds_at = GATE ? 4 : 3;   // dY and S are the first two
@@ -535,35 +551,48 @@ __global__ void __launch_bounds__(kStagedThreads, 1)
     }
     team_barrier<L>();
 
-    // the team's rows: `w` is worked on, `ahead` is fetched next, an array by each of the
-    // first threads
-    ResNormWalk w, ahead;
-    w.start(q, blockIdx.x * kTeams + team);
-    ahead = w;
+    // the row that is fetched next; the arrays, and the statistics after them, go round
+    // the warps, so that none of them holds up the others
+    ResNormWalk ahead;
+    ahead.start(q, blockIdx.x * kTeams + team);
     const int steps = q.rounds * q.steps;
-    const bool fetches = part < sh_.arrays, of_gate = GATE && part == gate_at;
-    const T *array = (const T *)(part == 0 ? p.dY : part == 1 ? p.S : part == zs_at ? p.Z : of_gate ? p.gate : p.dS);
+    const int mine_of = part % 32 * (L / 32) + part / 32;
+    const bool fetches = mine_of < sh_.arrays, of_gate = GATE && mine_of == gate_at;
+    const T *array = (const T *)(mine_of == 0       ? p.dY
+                                 : mine_of == 1     ? p.S
+                                 : mine_of == zs_at ? p.Z
+                                 : of_gate          ? p.gate
+                                                    : p.dS);
     const T *array_end = array + (of_gate ? q.groups : a.rows) * (int64_t)a.D;
     const auto fetch = [&](int s) {   // into stage s
         uint64_t *bar = &full[team][s];
-        if (part == sh_.arrays && ahead.row >= 0) {
-            mbar_arrive_expect_tx(bar, kStagedStats);
-            bulk_copy_g2s(mine + s * stage_bytes + stats_at, p.stats + (int64_t)ahead.row * 4, kStagedStats,
-                          bar);
+        if (mine_of == sh_.arrays) {
+            unsigned char *to = mine + s * stage_bytes + stats_at;
+            *reinterpret_cast<int4 *>(to + 16) = make_int4(
+                ahead.row, (int)ahead.gate,
+                ahead.segment < (uint32_t)q.groups * q.chunks ? (int)ahead.segment : -1,
+                ahead.step + 1 == q.steps);
+            mbar_arrive_expect_tx(bar, ahead.row >= 0 ? 16 : 0);
+            if (ahead.row >= 0) bulk_copy_g2s(to, p.stats + (int64_t)ahead.row * 4, 16, bar);
         } else if (fetches && ahead.row >= 0)
-            staged_fetch<T, V == 1>(mine + s * stage_bytes + part * row_bytes,
+            staged_fetch<T, V == 1>(mine + s * stage_bytes + mine_of * row_bytes,
                                     array + (of_gate ? (int64_t)ahead.gate : (int64_t)ahead.row) * a.D, a.D,
                                     array, array_end, bar);
-        else if (part <= sh_.arrays)   // no row: the phase is over at once
+        else if (fetches)   // no row: the phase is over at once
             mbar_arrive(bar);
         ahead.next(q);
     };
     for (int n = 0; n < stages && n < steps; ++n) fetch(n);
 
-    float2 sum[kVectors][P] = {}, gate_sum[P] = {};
+    // over all rows, for dScale and dB; over a segment's, of ds * z^ and of ds
+    float2 sum[2][P] = {}, seg[2][P] = {};
+    if (kTotals)
+#pragma unroll
+        for (int i = 0; i < 2 * N; ++i) totals[i * kStagedThreads] = 0.0f;
     // a thread's elements of a staged row, in pairs; zeros behind the row's end
     const auto take = [&](const unsigned char *row, const void *base, int64_t offset, float2 (&v)[P]) {
-        const T *e = reinterpret_cast<const T *>(row + ((uintptr_t)((const T *)base + offset) & 15));
+        const T *e = reinterpret_cast<const T *>(
+            V > 1 ? row : row + ((uintptr_t)((const T *)base + offset) & 15));
         float f[N];
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
@@ -576,13 +605,13 @@ __global__ void __launch_bounds__(kStagedThreads, 1)
 #pragma unroll
         for (int i = 0; i < P; ++i) v[i] = make_float2(f[2 * i], f[2 * i + 1]);
     };
-    const auto param = [&](const void *base, float2 (&v)[P]) {   // of the row's columns
+    const auto param = [&](const void *base, float2 (&v)[P], int64_t at = 0) {   // of the row's columns
         float f[N];
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int d = (k * L + part) * V;
             float x[V];
-            IOV::widen(d < a.D ? IOV::load((const T *)base + d) : IOV::zero(), x);
+            IOV::widen(d < a.D ? IOV::load((const T *)base + at + d) : IOV::zero(), x);
 #pragma unroll
             for (int i = 0; i < V; ++i) f[k * V + i] = x[i];
         }
@@ -620,12 +649,14 @@ __global__ void __launch_bounds__(kStagedThreads, 1)
     int slot = 0, s = 0;
     uint32_t parity = 0;
     for (int n = 0; n < steps; ++n) {
-        const int row = w.row;
-        const int64_t at = (int64_t)(row >= 0 ? row : 0) * a.D;
         const unsigned char *here = mine + s * stage_bytes;
-        float2 sh[P], wy[P], ds[P], zh[P], c[P];
+        float2 sh[P], wy[P], ds[P], zh[P], g[P], c[P];
         param(p.scale, c);
         if (ok) ok = mbar_wait_bounded(&full[team][s], parity, a.err);
+        int4 place = *reinterpret_cast<const int4 *>(here + stats_at + 16);
+        if (!ok) place = make_int4(-1, 0, -1, 0);
+        const int row = place.x;
+        const int64_t at = (int64_t)row * a.D;
         float4 st = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         float2 t0 = both(0.0f), t1 = both(0.0f);
         if (row >= 0) {
@@ -667,31 +698,19 @@ __global__ void __launch_bounds__(kStagedThreads, 1)
                 out[i] = mul_f32x2(ds[i], both(a.alpha));
             }
             put(p.dX, at, out);
-            if (GATE) {
-                float2 g[P], b[P];
-                take(here + gate_at * row_bytes, p.gate, (int64_t)w.gate * a.D, g);
-                if (POST && p.z_B) param(p.z_B, b);
+            if (GATE) take(here + gate_at * row_bytes, p.gate, (int64_t)place.y * a.D, g);
 #pragma unroll
-                for (int i = 0; i < P; ++i) {
-                    const float2 z = !POST    ? zh[i]
-                                     : p.z_B ? fma_f32x2(zh[i], c[i], b[i])
-                                             : mul_f32x2(zh[i], c[i]);
-                    gate_sum[i] = fma_f32x2(ds[i], z, gate_sum[i]);
-                    ds[i] = mul_f32x2(ds[i], g[i]);
-                }
-            }
-            if (POST) {
-#pragma unroll
-                for (int i = 0; i < P; ++i) {
-                    sum[kVectors - 2][i] = fma_f32x2(ds[i], zh[i], sum[kVectors - 2][i]);
-                    sum[kVectors - 1][i] = add_f32x2(sum[kVectors - 1][i], ds[i]);
+            for (int i = 0; i < P; ++i) {
+                if (POST || GATE) seg[0][i] = fma_f32x2(ds[i], zh[i], seg[0][i]);
+                if (POST) seg[1][i] = add_f32x2(seg[1][i], ds[i]);
+                if (GATE) ds[i] = mul_f32x2(ds[i], g[i]);
+                if (POST) {
                     ds[i] = mul_f32x2(ds[i], c[i]);
                     u0 = add_f32x2(u0, ds[i]);
                     u1 = fma_f32x2(ds[i], zh[i], u1);
                 }
-            } else {
-                put(p.dZ, at, ds);
             }
+            if (!POST) put(p.dZ, at, ds);
         }
         if (POST) {
             s0 = u0.x + u0.y;
@@ -707,22 +726,41 @@ __global__ void __launch_bounds__(kStagedThreads, 1)
                 put(p.dZ, at, out);
             }
         }
-        if (GATE && w.step + 1 == q.steps) {
-            if (w.segment < (int64_t)q.groups * q.chunks) {
+        if (GATE && place.w) {
+            if (place.z >= 0) {
+                float2 d[P];
+#pragma unroll
+                for (int i = 0; i < P; ++i) d[i] = seg[0][i];
+                if (POST) {
+                    float2 b[P];
+                    param(p.gate, g, (int64_t)place.y * a.D);
+                    param(p.z_scale, c);
+                    if (p.z_B) param(p.z_B, b);
+#pragma unroll
+                    for (int i = 0; i < P; ++i) {
+                        d[i] = mul_f32x2(seg[0][i], c[i]);
+                        if (p.z_B) d[i] = fma_f32x2(seg[1][i], b[i], d[i]);
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            float *t = totals + (j * N + 2 * i) * kStagedThreads;
+                            t[0] = fmaf(seg[j][i].x, g[i].x, t[0]);
+                            t[kStagedThreads] = fmaf(seg[j][i].y, g[i].y, t[kStagedThreads]);
+                        }
+                    }
+                }
                 if (q.chunks == 1) {
-                    put(p.dgate, (int64_t)w.segment * a.D, gate_sum);
+                    put(p.dgate, (int64_t)place.z * a.D, d);
                 } else {
 #pragma unroll
                     for (int i = 0; i < N; ++i) {
-                        const int d = (i / V * L + part) * V + i % V;
-                        if (d < a.D) gate_partials[(int64_t)w.segment * a.D + d] = element(gate_sum, i);
+                        const int e = (i / V * L + part) * V + i % V;
+                        if (e < a.D) gate_partials[(int64_t)place.z * a.D + e] = element(d, i);
                     }
                 }
             }
 #pragma unroll
-            for (int i = 0; i < P; ++i) gate_sum[i] = both(0.0f);
+            for (int i = 0; i < P; ++i) seg[0][i] = seg[1][i] = both(0.0f);
         }
-        w.next(q);
         if (++s == stages) {
             s = 0;
             parity ^= 1;
@@ -735,20 +773,26 @@ __global__ void __launch_bounds__(kStagedThreads, 1)
     if (!partials) return;
     // the teams of the block in order, one vector at a time, by way of the ring
     float *out = partials + (int64_t)blockIdx.x * kVectors * a.D;
-    float *join = reinterpret_cast<float *>(ring);
+    float *join = reinterpret_cast<float *>(ring) + kTotals;
 #pragma unroll
     for (int j = 0; j < kVectors; ++j) {
+        float x[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            x[i] = j < 2 ? element(sum[j % 2], i)
+                   : kTotals ? totals[((j % 2) * N + i) * kStagedThreads]
+                             : element(seg[j % 2], i);
         if (kTeams == 1) {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 const int d = (i / V * L + part) * V + i % V;
-                if (d < a.D) out[(int64_t)j * a.D + d] = element(sum[j], i);
+                if (d < a.D) out[(int64_t)j * a.D + d] = x[i];
             }
             continue;
         }
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < N; ++i) join[(team * N + i) * L + part] = element(sum[j], i);
+        for (int i = 0; i < N; ++i) join[(team * N + i) * L + part] = x[i];
         __syncthreads();
         for (int c = threadIdx.x; c < N * L; c += kStagedThreads) {
             const int i = c / L, d = (i / V * L + c % L) * V + i % V;
@@ -879,37 +923,38 @@ template <int V, typename F> cudaError_t resnorm_shape(int runs, F &&f) {
     return cudaErrorInvalidValue;   // not reached: D <= kResOnChip
 }
 
-// The same for the backward pass.  f(staged, L, NV): a team's sums, five per element,
+// The same for the backward pass (`post`, `gate`, `dS`: what the call has).  f(staged, L, NV): a team's sums, five per element,
 // stay in registers, eight elements of a thread where rows are staged.  Rows of a
 // warp's run or less keep their loads in registers: a bulk copy of 128 bytes costs as
-// much to issue as one of a few KB; so do rows too wide for two of them in the ring.
+// much to issue as one of a few KB; so do rows too wide for two of them in the ring, or
+// for eight elements of 512 threads.
 template <typename T, int V, typename F>
-cudaError_t resnorm_backward_shape(int D, bool gate, bool dS, F &&f) {
+cudaError_t resnorm_backward_shape(int D, bool post, bool gate, bool dS, F &&f) {
     using std::integral_constant;
     using std::false_type;
     using std::true_type;
     const int runs = (D + V - 1) / V;
     const auto pick = [&](auto l, auto nv) {
         constexpr int L = decltype(l)::value, NV = decltype(nv)::value;
-        if (staged_shape(D, sizeof(T), L, gate, dS).stages >= 2) return f(true_type(), l, nv);
+        if (staged_shape(D, sizeof(T), L, post, gate, dS).stages >= 2) return f(true_type(), l, nv);
         return f(false_type(), integral_constant<int, 512>(), integral_constant<int, kResOnChip / V / 512>());
     };
     if (runs <= 8) return f(false_type(), integral_constant<int, 8>(), integral_constant<int, 1>());
     if (runs <= 16) return f(false_type(), integral_constant<int, 16>(), integral_constant<int, 1>());
     if (runs <= 32) return f(false_type(), integral_constant<int, 32>(), integral_constant<int, 1>());
-    constexpr int NV = 8 / V;
+    constexpr int NV = kStagedN / V;
     if (D <= 256) return pick(integral_constant<int, 32>(), integral_constant<int, NV>());
     if (D <= 512) return pick(integral_constant<int, 64>(), integral_constant<int, NV>());
     if (D <= 1024) return pick(integral_constant<int, 128>(), integral_constant<int, NV>());
     if (D <= 2048) return pick(integral_constant<int, 256>(), integral_constant<int, NV>());
     if (D <= 4096) return pick(integral_constant<int, 512>(), integral_constant<int, NV>());
-    return pick(integral_constant<int, 512>(), integral_constant<int, 2 * NV>());
+    return f(false_type(), integral_constant<int, 512>(), integral_constant<int, kResOnChip / V / 512>());
 }
 
-template <typename T, int V> ResNormPlan resnorm_plan_of(const ResNormArgs &a, bool dS) {
+template <typename T, int V> ResNormPlan resnorm_plan_of(const ResNormArgs &a, bool post, bool dS) {
     ResNormPlan q = {};
     if (a.D > kResOnChip) return resnorm_plan(a, 1, kResWideBlocks * kResSms);
-    resnorm_backward_shape<T, V>(a.D, a.groups > 0, dS, [&](auto staged, auto l, auto nv) {
+    resnorm_backward_shape<T, V>(a.D, post, a.groups > 0, dS, [&](auto staged, auto l, auto nv) {
         constexpr int L = decltype(l)::value, NV = decltype(nv)::value;
         q = decltype(staged)::value
                 ? resnorm_plan(a, kStagedThreads / L, kResSms)
@@ -934,10 +979,11 @@ struct ResNormLayout {
 };
 
 template <typename T> size_t resnorm_ws_bytes(const ResNormArgs &a) {
-    size_t most = 0;   // whatever the alignment will be, and with dS or without
-    for (const bool dS : {false, true}) {
-        const size_t b1 = ResNormLayout(a, resnorm_plan_of<T, 1>(a, dS)).bytes;
-        const size_t bv = ResNormLayout(a, resnorm_plan_of<T, kVec<T>>(a, dS)).bytes;
+    size_t most = 0;   // whatever the alignment will be, with dS and z_scale or without
+    for (int form = 0; form < 4; ++form) {
+        const bool post = form & 1, dS = form & 2;
+        const size_t b1 = ResNormLayout(a, resnorm_plan_of<T, 1>(a, post, dS)).bytes;
+        const size_t bv = ResNormLayout(a, resnorm_plan_of<T, kVec<T>>(a, post, dS)).bytes;
         most = std::max(most, std::max(b1, bv));
     }
     return most;
@@ -973,10 +1019,10 @@ template <typename T, int V, int L, int NV, bool POST, bool GATE>
 cudaError_t run_resnorm_staged(const ResNormArgs &a, const ResNormPtrs &p, const ResNormPlan &q,
                                float *partials, float *gate_partials, cudaStream_t s) {
     const auto kernel = resnorm_staged_kernel<T, V, L, NV, POST, GATE>;
-    const StagedShape shape = staged_shape(a.D, sizeof(T), L, GATE, p.dS);
-    int smem = kStagedThreads / L * shape.stages * (shape.arrays * shape.pitch + kStagedStats);
-    const int join = kStagedThreads > L ? kStagedThreads * NV * V * (int)sizeof(float) : 0;
-    if (smem < join) smem = join;
+    const StagedShape shape = staged_shape(a.D, sizeof(T), L, POST, GATE, p.dS);
+    const int rows = kStagedThreads / L * shape.stages * (shape.arrays * shape.pitch + kStagedStats);
+    const int join = kStagedThreads > L ? kStagedThreads * kStagedN * (int)sizeof(float) : 0;
+    const int smem = 4 * staged_totals(POST, GATE) + std::max(rows, join);
     static DeviceFlags ready;
     const cudaError_t e = once_per_device(ready, [&] {
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kStagedRing);
@@ -991,7 +1037,7 @@ cudaError_t run_resnorm_backward(const ResNormArgs &a, const ResNormPtrs &p, con
                                  float *partials, float *gate_partials, cudaStream_t s) {
     const auto form = [&](auto post, auto gate) {
         constexpr bool POST = decltype(post)::value, GATE = decltype(gate)::value;
-        return resnorm_backward_shape<T, V>(a.D, GATE, p.dS, [&](auto staged, auto l, auto nv) {
+        return resnorm_backward_shape<T, V>(a.D, POST, GATE, p.dS, [&](auto staged, auto l, auto nv) {
             constexpr int L = decltype(l)::value, NV = decltype(nv)::value;
             if constexpr (decltype(staged)::value) {
                 return run_resnorm_staged<T, V, L, NV, POST, GATE>(a, p, q, partials, gate_partials, s);
@@ -1020,7 +1066,7 @@ cudaError_t launch_resnorm_backward(const ResNormArgs &a, const ResNormPtrs &p, 
     ResNormPlan q = {};
     SumArgs sum = {};
     if (a.rows > 0) {
-        q = runs ? resnorm_plan_of<T, kVec<T>>(a, p.dS) : resnorm_plan_of<T, 1>(a, p.dS);
+        q = runs ? resnorm_plan_of<T, kVec<T>>(a, p.z_scale, p.dS) : resnorm_plan_of<T, 1>(a, p.z_scale, p.dS);
         const ResNormLayout at(a, q);
         char *base = (char *)ws;
         float *partials = sums ? (float *)base : nullptr, *gates = (float *)(base + at.gate);
