@@ -107,6 +107,21 @@ __device__ __forceinline__ bool tc_wait_cluster(uint64_t *bar, uint32_t parity, 
     return true;
 }
 
+// One thread of the warp, always the same.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, e;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+// tc_wait by a whole warp.
+__device__ __forceinline__ bool gt_wait(uint64_t *bar, uint32_t parity, unsigned *err) {
+    return __all_sync(0xffffffffu, tc_wait(bar, parity, err));
+}
+
 // Loads a box of a 2-D map into this CTA; its bytes are counted on a barrier of the
 // pair (a shared::cluster address).
 __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap *map, int c0, int c1,
@@ -400,7 +415,10 @@ __global__ void __launch_bounds__(GtShape<T, MODE, NT>::kThreads, 1)
     __shared__ uint32_t tmem_base;
     unsigned char *stages = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     unsigned char *boxes = stages + NS * Sh::kStage;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    // the same for a whole warp, and known to be: the loops that copy and multiply are run
+    // by whole warps, with their numbers in uniform registers, and one thread issues (by a
+    // lane's own loop a stage took 640 cycles to issue, which its MMAs need 512 of)
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
     const uint32_t rank = cluster_rank();
     const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
     const int tiles = p.tiles_m * p.tiles_n, units = gt_units<MODE, kPlanes>(p);
@@ -432,15 +450,18 @@ __global__ void __launch_bounds__(GtShape<T, MODE, NT>::kThreads, 1)
 
     if (warp == Sh::kCopyWarp) {
         // ---------------------------------------------------- copies, one thread of each CTA
-        if (lane == 0) {
+        {
+            const bool issues = elect_one();
             GtRing<NS> r;
             for (int t = pair; t < tiles && ok; t += pairs) {
                 const GtTile w = gt_tile(p, t);
                 for (int u = 0; u < units && ok; ++u)
                     gt_steps<MODE, kPlanes>(p, u, [&](int which, int pa, int pb, int k) {
                         const int s = r.stage;
-                        ok = tc_wait(&empty[s], r.parity ^ 1, p.err);
+                        ok = gt_wait(&empty[s], r.parity ^ 1, p.err);
                         if (!ok) return false;
+                        r.next();
+                        if (!issues) return true;
                         if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * Sh::kStage);
                         const uint32_t bar = smem_of_rank(smem_u32(&full[s]), 0);
                         const uint32_t a = smem_u32(stages + s * Sh::kStage), b = a + kGtA;
@@ -464,7 +485,6 @@ __global__ void __launch_bounds__(GtShape<T, MODE, NT>::kThreads, 1)
                                 tma_load_2d_pair(b + c * kGtChunk, &p.b[which][pb], col + c * 64, kk,
                                                  bar);
                         }
-                        r.next();
                         return true;
                     });
             }
@@ -474,15 +494,16 @@ __global__ void __launch_bounds__(GtShape<T, MODE, NT>::kThreads, 1)
             for (int i = 0; i < fills; ++i) {
                 r.back();
                 if (ok)
-                    ok = tc_wait(&empty[r.stage], r.parity, p.err);
+                    ok = gt_wait(&empty[r.stage], r.parity, p.err);
                 else if (rank == 0)
-                    tc_wait(&full[r.stage], r.parity, p.err);
+                    gt_wait(&full[r.stage], r.parity, p.err);
             }
         }
         __syncwarp();
     } else if (warp == Sh::kMmaWarp) {
         // ---------------------------------------------------- MMAs, one thread of the pair
-        if (lane == 0 && rank == 0) {
+        if (rank == 0) {
+            const bool issues = elect_one();
             constexpr uint32_t idesc = umma_idesc_f16(!__is_same(T, __half), kGtTile, NT) |
                                        (MODE == kGtDw ? 1u << 15 : 0u) | (kForward ? 0u : 1u << 16);
             constexpr bool kAmn = MODE == kGtDw, kBmn = !kForward;
@@ -495,30 +516,33 @@ __global__ void __launch_bounds__(GtShape<T, MODE, NT>::kThreads, 1)
             for (int t = pair; t < tiles && ok; t += pairs)
                 for (int u = 0; u < units && ok; ++u, ++count) {
                     const int b = count & 1;
-                    if (count >= 2) ok = tc_wait_cluster(&tile_empty[b], (count / 2 - 1) & 1, p.err);
+                    if (count >= 2)
+                        ok = __all_sync(0xffffffffu,
+                                        tc_wait_cluster(&tile_empty[b], (count / 2 - 1) & 1, p.err));
                     uint32_t more = 0;
                     if (!ok) break;
                     gt_steps<MODE, kPlanes>(p, u, [&](int, int, int, int) {
                         const int s = r.stage;
-                        ok = tc_wait(&full[s], r.parity, p.err);
+                        ok = gt_wait(&full[s], r.parity, p.err);
                         if (!ok) return false;
+                        r.next();
                         tcgen05_fence_after_sync();
                         const uint32_t a = a0 + s * (Sh::kStage / 16), bb = b0 + s * (Sh::kStage / 16);
+                        if (issues) {
 #pragma unroll
-                        for (int i = 0; i < kGtK / 16; ++i) {   // 16 steps: 32 bytes of a row, or 16 rows
-                            umma_f16_pair(tmem + b * NT, a + i * (kAmn ? 2048 : 32) / 16,
-                                          bb + i * (kBmn ? 2048 : 32) / 16, idesc, more);
-                            more = 1;
+                            for (int i = 0; i < kGtK / 16; ++i)   // 16 steps: 32 bytes of a row, or 16 rows
+                                umma_f16_pair(tmem + b * NT, a + i * (kAmn ? 2048 : 32) / 16,
+                                              bb + i * (kBmn ? 2048 : 32) / 16, idesc, i > 0 ? 1u : more);
+                            umma_commit_pair(&empty[s]);
                         }
-                        umma_commit_pair(&empty[s]);
-                        r.next();
+                        more = 1;
                         return true;
                     });
-                    if (ok) umma_commit_pair(&tile_full[b]);
+                    if (ok && issues) umma_commit_pair(&tile_full[b]);
                 }
             if (!ok) {   // a wait gave up: let the MMAs end before TMEM is released
-                umma_commit_pair(&drained);
-                tc_wait(&drained, 0, p.err);
+                if (issues) umma_commit_pair(&drained);
+                gt_wait(&drained, 0, p.err);
             }
         }
         __syncwarp();
