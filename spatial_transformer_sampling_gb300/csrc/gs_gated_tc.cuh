@@ -1,5 +1,5 @@
 // gs_gated_tc.cuh -- the products of the gated projections on the fifth-generation
-// tensor cores: one persistent kernel for the forward pass, for dX and for dWg, dWu.
+// tensor cores: a persistent kernel for the forward pass and one for dX, dWg and dWu.
 //
 // A pair of CTAs (a cluster of two, cta_group::2) works on tiles of 256 rows x NT
 // columns.  Each CTA stages its 128 rows of A and NT / 2 rows of B, 64 steps of the
@@ -12,6 +12,10 @@
 //            tile's columns are G and U of the same NT / 2 outputs, side by side.
 //   dX       A = dG, then dU; B = Wg, then Wu, N-major (their rows are contraction).
 //   dW       A = dG or dU, M-major; B = X, N-major; the contraction runs over rows.
+//
+// The tiles of dX and of dWg, dWu are worked on in one launch, the longer contraction
+// first and the others where a pair is free: 16384 x 1024 x 4096 needs 3.4 and 1.7 tiles
+// per pair, 6 of one length in turn and 5.1 together.
 //
 // Both operands are read where they lie: K-major or MN-major is a bit of the
 // instruction, nothing is transposed in memory.
@@ -37,7 +41,8 @@ constexpr int kGtChunk = 64 * kGtK * 2;    // bytes of 64 rows of an MN-major op
 constexpr int kGtSmem = 224 * 1024;
 constexpr int kGtRun = 4;             // stages of a plane's run (fp32)
 
-enum { kGtForward = 0, kGtForwardKeep = 1, kGtDx = 2, kGtDw = 3 };
+enum { kGtForward = 0, kGtForwardKeep = 1, kGtBackward = 2 };
+enum { kGtDx = 0, kGtDw = 1 };   // kinds of a backward tile
 
 // T: type of the outputs.  An epilogue warp has 32 rows and kCols columns of a tile
 // (forward: as many of G as of U), which it stages for its stores in boxes of 32 rows:
@@ -204,15 +209,28 @@ struct GtOutput {
     int width, boxes;
 };
 
-struct GtArgs {
-    // planes of each operand; forward: a[0], b = Wg and Wu; dX: dG, Wg and dU, Wu; dW: b[0]
+// Tiles of one kind: planes of each operand (forward: a[0], b = Wg and Wu; dX: dG, Wg and
+// dU, Wu; dW: dG and dU, b[0]), tiles of 256 rows and NT columns (forward: NT / 2
+// outputs), stages of one pair of operands' contraction.
+struct GtKind {
     CUtensorMap a[2][kGtMostPlanes], b[2][kGtMostPlanes];
-    GtOutput out[3];              // forward: H, G, U; dX: dX; dW: dWg, dWu
+    int tiles_m, tiles_n, k_steps;
+};
+
+// Which tiles a pair works on: those of kind `first` go round, `turns` and one more for
+// the first `extra` pairs; then these take `long_turns` of the other kind's tiles each,
+// and the others `short_turns`.
+struct GtSchedule {
+    int first, turns, extra, long_turns, short_turns, others;
+};
+
+struct GtArgs {
+    GtKind kind[2];               // forward: the first alone
+    GtSchedule plan;
+    GtOutput out[3];              // forward: H, G, U; backward: dX, dWg, dWu
     const void *bg, *bu;
     int F;
     ActNumbers act;
-    int tiles_m, tiles_n;         // of 256 rows, and NT columns (forward: NT / 2 outputs)
-    int k_steps;                  // of one pair of operands
     unsigned *err;
 };
 
@@ -243,16 +261,35 @@ void gt_output(GtOutput *o, void *at, int64_t rows, int width, int box_row) {
                            box_row == 128, box_row == 64);
 }
 
-// Tile t of tiles_m x tiles_n: eight rows of tiles at a time, so that the tiles in
-// flight share their operands in L2.
+// The i-th tile of pair `pair` of `pairs`; false when there are no more.  Tiles of a kind
+// are numbered eight rows of them at a time, so that those in flight share their operands
+// in L2.
 struct GtTile {
-    int m, n;
+    int kind, m, n;
 };
-__device__ __forceinline__ GtTile gt_tile(const GtArgs &p, int t) {
+__device__ __forceinline__ bool gt_tile(const GtArgs &p, int pair, int pairs, int i, GtTile &w) {
     constexpr int kGroup = 8;
-    const int per = kGroup * p.tiles_n, g = t / per, r = t - g * per;
-    const int rows = min(kGroup, p.tiles_m - g * kGroup);
-    return {g * kGroup + r % rows, r / rows};
+    const GtSchedule &s = p.plan;
+    const bool extra = pair < s.extra;
+    const int turns = s.turns + extra;
+    int t;
+    if (i < turns) {
+        w.kind = s.first;
+        t = pair + i * pairs;
+    } else {
+        i -= turns;
+        if (i >= (extra ? s.long_turns : s.short_turns)) return false;
+        w.kind = 1 - s.first;
+        t = extra ? pair + i * s.extra
+                  : s.extra * s.long_turns + pair - s.extra + i * (pairs - s.extra);
+        if (t >= s.others) return false;
+    }
+    const GtKind &k = p.kind[w.kind];
+    const int per = kGroup * k.tiles_n, g = t / per, r = t - g * per;
+    const int rows = min(kGroup, k.tiles_m - g * kGroup);
+    w.m = g * kGroup + r % rows;
+    w.n = r / rows;
+    return true;
 }
 
 // ------------------------------------------------------------------ kernel
@@ -283,20 +320,21 @@ __device__ __forceinline__ int gt_plane_b(int product) { return (0x021010 >> (20
 
 // The parts of a tile that TMEM accumulates by themselves, and their steps in order:
 // f(pair of operands, planes of A and B, stage of the contraction) until it is false.
-template <int MODE, int PLANES> __device__ __forceinline__ int gt_units(const GtArgs &p) {
+template <int MODE, int PLANES> __device__ __forceinline__ int gt_units(const GtKind &k, int kind) {
     if (PLANES == 1) return 1;
-    return (p.k_steps + kGtRun - 1) / kGtRun * (MODE == kGtDx ? 2 : 1);
+    return (k.k_steps + kGtRun - 1) / kGtRun * (MODE == kGtBackward && kind == kGtDx ? 2 : 1);
 }
 template <int MODE, int PLANES, typename F>
-__device__ __forceinline__ void gt_steps(const GtArgs &p, int unit, F &&f) {
+__device__ __forceinline__ void gt_steps(const GtKind &kind, int which_kind, int unit, F &&f) {
     if (PLANES == 1) {
-        for (int which = 0; which < (MODE == kGtDx ? 2 : 1); ++which)
-            for (int k = 0; k < p.k_steps; ++k)
+        const int operands = MODE == kGtBackward && which_kind == kGtDx ? 2 : 1;
+        for (int which = 0; which < operands; ++which)
+            for (int k = 0; k < kind.k_steps; ++k)
                 if (!f(which, 0, 0, k)) return;
         return;
     }
-    const int runs = (p.k_steps + kGtRun - 1) / kGtRun, which = unit >= runs;
-    const int k0 = (unit - which * runs) * kGtRun, k1 = min(k0 + kGtRun, p.k_steps);
+    const int runs = (kind.k_steps + kGtRun - 1) / kGtRun, which = unit >= runs;
+    const int k0 = (unit - which * runs) * kGtRun, k1 = min(k0 + kGtRun, kind.k_steps);
     for (int product = 0; product < 6; ++product)
         for (int k = k0; k < k1; ++k)
             if (!f(which, gt_plane_a(product), gt_plane_b(product), k)) return;
@@ -421,7 +459,7 @@ __global__ void __launch_bounds__(GtShape<T, MODE, NT>::kThreads, 1)
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
     const uint32_t rank = cluster_rank();
     const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
-    const int tiles = p.tiles_m * p.tiles_n, units = gt_units<MODE, kPlanes>(p);
+    GtTile w;
 
     if (warp == Sh::kMmaWarp) {
         if (lane == 0) {
@@ -453,10 +491,11 @@ __global__ void __launch_bounds__(GtShape<T, MODE, NT>::kThreads, 1)
         {
             const bool issues = elect_one();
             GtRing<NS> r;
-            for (int t = pair; t < tiles && ok; t += pairs) {
-                const GtTile w = gt_tile(p, t);
+            for (int i = 0; ok && gt_tile(p, pair, pairs, i, w); ++i) {
+                const GtKind &kind = p.kind[w.kind];
+                const int units = gt_units<MODE, kPlanes>(kind, w.kind);
                 for (int u = 0; u < units && ok; ++u)
-                    gt_steps<MODE, kPlanes>(p, u, [&](int which, int pa, int pb, int k) {
+                    gt_steps<MODE, kPlanes>(kind, w.kind, u, [&](int which, int pa, int pb, int k) {
                         const int s = r.stage;
                         ok = gt_wait(&empty[s], r.parity ^ 1, p.err);
                         if (!ok) return false;
@@ -467,22 +506,22 @@ __global__ void __launch_bounds__(GtShape<T, MODE, NT>::kThreads, 1)
                         const uint32_t a = smem_u32(stages + s * Sh::kStage), b = a + kGtA;
                         const int kk = k * kGtK;
                         if (kForward) {
-                            tma_load_2d_pair(a, &p.a[0][pa], kk, w.m * kGtTile + rank * kGtHalf, bar);
-                            tma_load_2d_pair(b, &p.b[rank][pb], kk, w.n * (NT / 2), bar);
+                            tma_load_2d_pair(a, &kind.a[0][pa], kk, w.m * kGtTile + rank * kGtHalf, bar);
+                            tma_load_2d_pair(b, &kind.b[rank][pb], kk, w.n * (NT / 2), bar);
                         } else {
                             const int col = w.n * NT + rank * (NT / 2);
-                            if (MODE == kGtDx) {
-                                tma_load_2d_pair(a, &p.a[which][pa], kk,
+                            if (w.kind == kGtDx) {
+                                tma_load_2d_pair(a, &kind.a[which][pa], kk,
                                                  w.m * kGtTile + rank * kGtHalf, bar);
                             } else {
-                                const int half = p.tiles_m / 2, of = w.m >= half;
+                                const int half = kind.tiles_m / 2, of = w.m >= half;
                                 const int row = (w.m - of * half) * kGtTile + rank * kGtHalf;
-                                tma_load_2d_pair(a, &p.a[of][pa], row, kk, bar);
-                                tma_load_2d_pair(a + kGtChunk, &p.a[of][pa], row + 64, kk, bar);
+                                tma_load_2d_pair(a, &kind.a[of][pa], row, kk, bar);
+                                tma_load_2d_pair(a + kGtChunk, &kind.a[of][pa], row + 64, kk, bar);
                             }
 #pragma unroll
                             for (int c = 0; c < NT / 128; ++c)
-                                tma_load_2d_pair(b + c * kGtChunk, &p.b[which][pb], col + c * 64, kk,
+                                tma_load_2d_pair(b + c * kGtChunk, &kind.b[which][pb], col + c * 64, kk,
                                                  bar);
                         }
                         return true;
@@ -504,16 +543,22 @@ __global__ void __launch_bounds__(GtShape<T, MODE, NT>::kThreads, 1)
         // ---------------------------------------------------- MMAs, one thread of the pair
         if (rank == 0) {
             const bool issues = elect_one();
-            constexpr uint32_t idesc = umma_idesc_f16(!__is_same(T, __half), kGtTile, NT) |
-                                       (MODE == kGtDw ? 1u << 15 : 0u) | (kForward ? 0u : 1u << 16);
-            constexpr bool kAmn = MODE == kGtDw, kBmn = !kForward;
+            constexpr uint32_t idesc_k = umma_idesc_f16(!__is_same(T, __half), kGtTile, NT) |
+                                         (kForward ? 0u : 1u << 16);
+            constexpr bool kBmn = !kForward;
             const uint32_t base = smem_u32(stages);
-            const uint32_t a0 = kAmn ? umma_lo_mnmajor(base, kGtChunk) : umma_lo_kmajor(base);
             const uint32_t b0 =
                 kBmn ? umma_lo_mnmajor(base + kGtA, kGtChunk) : umma_lo_kmajor(base + kGtA);
             GtRing<NS> r;
             int count = 0;
-            for (int t = pair; t < tiles && ok; t += pairs)
+            for (int t = 0; ok && gt_tile(p, pair, pairs, t, w); ++t) {
+                const GtKind &kind = p.kind[w.kind];
+                const int units = gt_units<MODE, kPlanes>(kind, w.kind);
+                // A is M-major for dW: 16 steps of the contraction are 16 rows, not 32 bytes of one
+                const bool amn = !kForward && w.kind == kGtDw;
+                const uint32_t idesc = idesc_k | (amn ? 1u << 15 : 0u);
+                const uint32_t a0 = amn ? umma_lo_mnmajor(base, kGtChunk) : umma_lo_kmajor(base);
+                const uint32_t a_step = (amn ? 2048 : 32) / 16;
                 for (int u = 0; u < units && ok; ++u, ++count) {
                     const int b = count & 1;
                     if (count >= 2)
@@ -521,7 +566,7 @@ __global__ void __launch_bounds__(GtShape<T, MODE, NT>::kThreads, 1)
                                         tc_wait_cluster(&tile_empty[b], (count / 2 - 1) & 1, p.err));
                     uint32_t more = 0;
                     if (!ok) break;
-                    gt_steps<MODE, kPlanes>(p, u, [&](int, int, int, int) {
+                    gt_steps<MODE, kPlanes>(kind, w.kind, u, [&](int, int, int, int) {
                         const int s = r.stage;
                         ok = gt_wait(&full[s], r.parity, p.err);
                         if (!ok) return false;
@@ -530,8 +575,8 @@ __global__ void __launch_bounds__(GtShape<T, MODE, NT>::kThreads, 1)
                         const uint32_t a = a0 + s * (Sh::kStage / 16), bb = b0 + s * (Sh::kStage / 16);
                         if (issues) {
 #pragma unroll
-                            for (int i = 0; i < kGtK / 16; ++i)   // 16 steps: 32 bytes of a row, or 16 rows
-                                umma_f16_pair(tmem + b * NT, a + i * (kAmn ? 2048 : 32) / 16,
+                            for (int i = 0; i < kGtK / 16; ++i)
+                                umma_f16_pair(tmem + b * NT, a + i * a_step,
                                               bb + i * (kBmn ? 2048 : 32) / 16, idesc, i > 0 ? 1u : more);
                             umma_commit_pair(&empty[s]);
                         }
@@ -540,6 +585,7 @@ __global__ void __launch_bounds__(GtShape<T, MODE, NT>::kThreads, 1)
                     });
                     if (ok && issues) umma_commit_pair(&tile_full[b]);
                 }
+            }
             if (!ok) {   // a wait gave up: let the MMAs end before TMEM is released
                 if (issues) umma_commit_pair(&drained);
                 gt_wait(&drained, 0, p.err);
@@ -555,8 +601,9 @@ __global__ void __launch_bounds__(GtShape<T, MODE, NT>::kThreads, 1)
         constexpr int kRuns = Sh::kCols / 32, kHalf = kForward ? kRuns / 2 : kRuns;
         const auto column = [&](int i) { return i / kHalf * (NT / 2) + (part * kHalf + i % kHalf) * 32; };
         int count = 0;
-        for (int t = pair; t < tiles && ok; t += pairs) {
-            const GtTile w = gt_tile(p, t);
+        for (int t = 0; ok && gt_tile(p, pair, pairs, t, w); ++t) {
+            const GtKind &kind = p.kind[w.kind];
+            const int units = gt_units<MODE, kPlanes>(kind, w.kind);
             const int64_t row0 = (int64_t)w.m * kGtTile + rank * kGtHalf + quarter * 32;
             const int f0 = w.n * (NT / 2) + part * kHalf * 32;   // forward: the first output
             float bias[kHalf][2] = {};                           // of outputs f0 + 32 i + lane
@@ -619,8 +666,8 @@ __global__ void __launch_bounds__(GtShape<T, MODE, NT>::kThreads, 1)
                     gt_store_boxes<T, kRow, Sh::kBoxes>(p.out, box, row0, f0 + i * 32);
                 }
             } else {
-                const int half = p.tiles_m / 2, which = MODE == kGtDw && w.m >= half;
-                const GtOutput *out = &p.out[which];
+                const int half = kind.tiles_m / 2, which = w.kind == kGtDw && w.m >= half;
+                const GtOutput *out = &p.out[w.kind == kGtDw ? 1 + which : 0];
                 const int64_t out_row = row0 - (int64_t)which * half * kGtTile;
                 const int col0 = w.n * NT + part * Sh::kCols;
                 // two runs at a time: a box of both, or one each
@@ -677,21 +724,57 @@ template <typename T, int MODE, int NT> cudaError_t gt_most_pairs(int *pairs) {
     return cudaSuccess;
 }
 
+// The schedule of n1 tiles of `steps1` stages each and n2 shorter ones of `steps2` over
+// `pairs`, and the stages that the longest of them has (`*length`).
+inline GtSchedule gt_schedule(int first, int64_t n1, int64_t steps1, int64_t n2, int64_t steps2,
+                              int64_t pairs, int64_t *length) {
+    GtSchedule s = {first, (int)(n1 / pairs), (int)(n1 % pairs), 0, 0, (int)n2};
+    const int64_t many = s.extra, few = pairs - s.extra;   // pairs with one tile more, and the others
+    int64_t by_many = (s.turns + 1) * steps1, by_few = s.turns * steps1, left = n2;
+    // whole rounds of all pairs first, then whichever group is done earlier
+    const int64_t ahead = steps2 > 0 ? (steps1 + steps2 - 1) / steps2 + 1 : 0;
+    const int64_t rounds = n2 / pairs > ahead ? n2 / pairs - ahead : 0;
+    s.long_turns = s.short_turns = (int)rounds;
+    by_many += rounds * steps2;
+    by_few += rounds * steps2;
+    left -= rounds * pairs;
+    while (left > 0) {
+        if (many > 0 && by_many + steps2 < by_few + steps2) {
+            ++s.long_turns;
+            by_many += steps2;
+            left -= many;
+        } else {
+            ++s.short_turns;
+            by_few += steps2;
+            left -= few;
+        }
+    }
+    *length = many > 0 && by_many > by_few ? by_many : by_few;
+    return s;
+}
+
 template <typename T, int MODE, int NT>
 cudaError_t launch_gt_as(GtArgs &p, bool follows, cudaStream_t s) {
     using Sh = GtShape<T, MODE, NT>;
     int pairs = 0;
     const cudaError_t e = gt_most_pairs<T, MODE, NT>(&pairs);
     if (e != cudaSuccess) return e;
-    const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
-    const unsigned blocks = 2 * (unsigned)(tiles < pairs ? tiles : pairs);
-    return launch_next(LaunchAs(follows, 2), gated_tc_kernel<T, MODE, NT>, dim3(blocks), Sh::kThreads,
-                       Sh::kSmem, s, p);
+    const int64_t n0 = (int64_t)p.kind[0].tiles_m * p.kind[0].tiles_n;
+    const int64_t n1 = (int64_t)p.kind[1].tiles_m * p.kind[1].tiles_n;
+    if (n0 + n1 < pairs) pairs = (int)(n0 + n1);
+    const int64_t k0 = p.kind[0].k_steps * (MODE == kGtBackward ? 2 : 1), k1 = p.kind[1].k_steps;
+    int64_t length;
+    p.plan = k0 >= k1 ? gt_schedule(0, n0, k0, n1, k1, pairs, &length)
+                      : gt_schedule(1, n1, k1, n0, k0, pairs, &length);
+    return launch_next(LaunchAs(follows, 2), gated_tc_kernel<T, MODE, NT>, dim3(2 * pairs),
+                       Sh::kThreads, Sh::kSmem, s, p);
 }
 
-// Columns of B per tile: 256, or 128 where tiles that wide leave SMs without one.
-inline int gt_columns(int64_t tiles_m, int columns) {
-    return tiles_m * ((columns + 255) / 256) * 2 < kGatedSms ? 128 : 256;
+// Whether tiles of 128 columns are done sooner than tiles of 256: `length(NT)` are the
+// stages of the pair that has most.  A stage takes 0.216 us with 128 columns (its copies
+// bound it) and 0.302 with 256 (its MMAs).
+template <typename F> bool gt_narrow(F &&length) {
+    return (double)length(128) * 0.216 < (double)length(256) * 0.302;
 }
 
 // Forward pass from 16-bit operands (T float: planes); *used: TMA takes them.
@@ -700,10 +783,18 @@ cudaError_t launch_gt_forward(const GatedArgs &a, const GatedPtrs &q, const GtMa
                               const GtMatrix &Wg, const GtMatrix &Wu, bool follows, cudaStream_t s,
                               bool *used) {
     GtArgs p = {};
-    p.tiles_m = (int)((a.rows + kGtTile - 1) / kGtTile);
-    const int nt = gt_columns(p.tiles_m, 2 * a.F);
-    *used = gt_maps<T>(p.a[0], X, kGtHalf) && gt_maps<T>(p.b[0], Wg, nt / 2) &&
-            gt_maps<T>(p.b[1], Wu, nt / 2);
+    GtKind &k = p.kind[0];
+    k.tiles_m = (int)((a.rows + kGtTile - 1) / kGtTile);
+    k.k_steps = (a.D + kGtK - 1) / kGtK;
+    const auto tiles_n = [&](int nt) { return (a.F + nt / 2 - 1) / (nt / 2); };
+    const bool narrow = gt_narrow([&](int nt) {
+        const int64_t pairs = kGatedSms / 2;
+        return ((int64_t)k.tiles_m * tiles_n(nt) + pairs - 1) / pairs;
+    });
+    const int nt = narrow ? 128 : 256;
+    k.tiles_n = tiles_n(nt);
+    *used = gt_maps<T>(k.a[0], X, kGtHalf) && gt_maps<T>(k.b[0], Wg, nt / 2) &&
+            gt_maps<T>(k.b[1], Wu, nt / 2);
     if (!*used) return cudaSuccess;
     const int box_row = GtShape<T, kGtForward, 256>::kBoxRow;
     gt_output<T>(&p.out[0], q.H, a.rows, a.F, box_row);
@@ -715,10 +806,8 @@ cudaError_t launch_gt_forward(const GatedArgs &a, const GatedPtrs &q, const GtMa
     p.bu = q.bu;
     p.F = a.F;
     p.act = act_numbers(a.act);
-    p.tiles_n = (a.F + nt / 2 - 1) / (nt / 2);
-    p.k_steps = (a.D + kGtK - 1) / kGtK;
     p.err = a.err;
-    if (nt == 128)
+    if (narrow)
         return q.G ? launch_gt_as<T, kGtForwardKeep, 128>(p, follows, s)
                    : launch_gt_as<T, kGtForward, 128>(p, follows, s);
     return q.G ? launch_gt_as<T, kGtForwardKeep, 256>(p, follows, s)
@@ -730,29 +819,35 @@ template <typename T>
 cudaError_t launch_gt_backward(const GatedArgs &a, const GatedPtrs &q, const GtMatrix &X,
                                const GtMatrix &Wg, const GtMatrix &Wu, const GtMatrix &dG,
                                const GtMatrix &dU, bool follows, cudaStream_t s, bool *used) {
-    GtArgs x = {}, w = {};
+    GtArgs p = {};
+    GtKind &x = p.kind[kGtDx], &w = p.kind[kGtDw];
     *used = gt_maps<T>(x.a[0], dG, kGtHalf) && gt_maps<T>(x.a[1], dU, kGtHalf) &&
             gt_maps<T>(x.b[0], Wg, kGtK) && gt_maps<T>(x.b[1], Wu, kGtK) &&
             gt_maps<T>(w.a[0], dG, kGtK) && gt_maps<T>(w.a[1], dU, kGtK) &&
             gt_maps<T>(w.b[0], X, kGtK);
     if (!*used) return cudaSuccess;
-    gt_output<T>(&x.out[0], q.dX, a.rows, a.D, 128);
+    gt_output<T>(&p.out[0], q.dX, a.rows, a.D, 128);
+    gt_output<T>(&p.out[1], q.dWg, a.F, a.D, 128);
+    gt_output<T>(&p.out[2], q.dWu, a.F, a.D, 128);
+    p.err = a.err;
     x.tiles_m = (int)((a.rows + kGtTile - 1) / kGtTile);
     x.k_steps = (a.F + kGtK - 1) / kGtK;
-    x.err = a.err;
-    gt_output<T>(&w.out[0], q.dWg, a.F, a.D, 128);
-    gt_output<T>(&w.out[1], q.dWu, a.F, a.D, 128);
     w.tiles_m = 2 * ((a.F + kGtTile - 1) / kGtTile);
     w.k_steps = (int)((a.rows + kGtK - 1) / kGtK);
-    w.err = a.err;
-    const auto run = [&](GtArgs &p, auto mode, bool after) {
-        constexpr int MODE = decltype(mode)::value;
-        const int nt = gt_columns(p.tiles_m, a.D);
-        p.tiles_n = (a.D + nt - 1) / nt;
-        return nt == 128 ? launch_gt_as<T, MODE, 128>(p, after, s) : launch_gt_as<T, MODE, 256>(p, after, s);
-    };
-    const cudaError_t e = run(x, std::integral_constant<int, kGtDx>(), follows);
-    return e != cudaSuccess ? e : run(w, std::integral_constant<int, kGtDw>(), true);
+    const bool narrow = gt_narrow([&](int nt) {
+        const int64_t n = (a.D + nt - 1) / nt, nx = x.tiles_m * n, nw = w.tiles_m * n;
+        const int64_t kx = 2 * (int64_t)x.k_steps, kw = w.k_steps;
+        int64_t length;
+        if (kx >= kw)
+            gt_schedule(kGtDx, nx, kx, nw, kw, kGatedSms / 2, &length);
+        else
+            gt_schedule(kGtDw, nw, kw, nx, kx, kGatedSms / 2, &length);
+        return length;
+    });
+    const int nt = narrow ? 128 : 256;
+    x.tiles_n = w.tiles_n = (a.D + nt - 1) / nt;
+    return narrow ? launch_gt_as<T, kGtBackward, 128>(p, follows, s)
+                  : launch_gt_as<T, kGtBackward, 256>(p, follows, s);
 }
 
 }  // namespace gs
