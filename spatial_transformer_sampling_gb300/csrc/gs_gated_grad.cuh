@@ -2,6 +2,8 @@
 // and dU = dH act(G), and the column sums that are the biases' gradients.
 #pragma once
 
+#include <initializer_list>
+
 #include "gs_gated.cuh"
 
 namespace gs {
@@ -12,13 +14,81 @@ namespace gs {
 constexpr int kGradThreads = 256, kGradWarps = kGradThreads / 32;
 
 // fp32 as three bf16 numbers, each the nearest to what the ones before leave: their
-// sum is x to 2^-24 of it or better.  What is not finite stays in the first.
-__device__ __forceinline__ void split3(float x, __nv_bfloat16 (&v)[3]) {
-    v[0] = __float2bfloat16_rn(x);
-    if (__hisinf(v[0])) v[0] = __float2bfloat16_rz(x);   // the largest numbers round to infinity
-    const float r = isfinite(x) ? x - __bfloat162float(v[0]) : 0.0f;
-    v[1] = __float2bfloat16_rn(r);
-    v[2] = __float2bfloat16_rn(r - __bfloat162float(v[1]));
+// sum is x to 2^-24 of it or better.  What is not finite stays in the first.  Two at a
+// time, packed.
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ void split3(float lo, float hi, uint32_t (&v)[3]) {
+    v[0] = bf16_pair(lo, hi);
+    float a = __uint_as_float(v[0] << 16), b = __uint_as_float(v[0] & 0xffff0000u);
+    if (!(fabsf(a) < INFINITY) || !(fabsf(b) < INFINITY)) {
+        // NaN and infinities leave nothing; the largest numbers do not round to infinity
+        if (isinf(a) && !isinf(lo)) a = copysignf(3.3895314e38f, lo);
+        if (isinf(b) && !isinf(hi)) b = copysignf(3.3895314e38f, hi);
+        v[0] = bf16_pair(a, b);
+        if (!isfinite(lo)) lo = a = 0.0f;
+        if (!isfinite(hi)) hi = b = 0.0f;
+    }
+    lo -= a;
+    hi -= b;
+    v[1] = bf16_pair(lo, hi);
+    v[2] = bf16_pair(lo - __uint_as_float(v[1] << 16), hi - __uint_as_float(v[1] & 0xffff0000u));
+}
+
+// kVec<T> elements from element e of a tensor of `total`, whatever e: the two 16-byte
+// runs that hold them, shifted together.  The tensor starts on a 16-byte boundary; what
+// lies behind its end reads as 0.
+template <typename T>
+__device__ __forceinline__ uint4 load_shifted(const T *base, int64_t e, int64_t total) {
+    constexpr int V = kVec<T>;
+    const int64_t run = e / V * V;
+    const int by = (int)(e - run);
+    if (run + 2 * V <= total || (by == 0 && run + V <= total)) {
+        const uint4 a = __ldg(reinterpret_cast<const uint4 *>(base + run));
+        if (by == 0) return a;
+        const uint4 b = __ldg(reinterpret_cast<const uint4 *>(base + run + V));
+        uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        const int words = by * (int)sizeof(T) / 4;
+        if (words & 2) {
+#pragma unroll
+            for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+        }
+        if (words & 1) {
+#pragma unroll
+            for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+        }
+        if (sizeof(T) == 2 && (by & 1)) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    uint4 v;
+    T *x = reinterpret_cast<T *>(&v);
+#pragma unroll
+    for (int i = 0; i < V; ++i) x[i] = e + i < total ? base[e + i] : IO<T>::st(0.0f);
+    return v;
+}
+
+// How rows are read: one element at a time, in 16-byte runs, or in runs that start
+// anywhere (rows that are no multiple of 16 bytes in a tensor that starts on one).
+enum { kRowsSingle = 0, kRowsRuns = 1, kRowsShifted = 2 };
+template <typename T, int READ> constexpr int kRowsV = READ == kRowsSingle ? 1 : kVec<T>;
+template <typename T, int READ>
+__device__ __forceinline__ typename Run<T, kRowsV<T, READ>>::Raw row_load(const T *base, int64_t e,
+                                                                          int64_t total) {
+    if constexpr (READ == kRowsShifted)
+        return load_shifted(base, e, total);
+    else
+        return Run<T, kRowsV<T, READ>>::load(base + e);
+}
+template <typename T> int rows_read(int width, std::initializer_list<const void *> tensors) {
+    for (const void *t : tensors)
+        if (!aligned16(t)) return kRowsSingle;
+    return width % kVec<T> == 0 ? kRowsRuns : kRowsShifted;
 }
 
 // Stores a run where the products read it: rounded to the type, or, of fp32, in three
@@ -26,17 +96,18 @@ __device__ __forceinline__ void split3(float x, __nv_bfloat16 (&v)[3]) {
 template <typename T> using Factor = std::conditional_t<sizeof(T) == 4, __nv_bfloat16, T>;
 template <typename T, int V>
 __device__ __forceinline__ void store_factor(Factor<T> *to, int64_t plane, const float (&v)[V]) {
+    static_assert(sizeof(T) == 2 || V == 1 || V == 4, "a run of fp32");
     if constexpr (sizeof(T) == 4) {
-        struct alignas(V * 2) Part { __nv_bfloat16 e[V]; } part[3];
+        uint32_t x[3], y[3] = {};
+        split3(v[0], V > 1 ? v[V > 1 ? 1 : 0] : 0.0f, x);
+        if constexpr (V == 4) split3(v[2], v[3], y);
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-            __nv_bfloat16 x[3];
-            split3(v[e], x);
-#pragma unroll
-            for (int i = 0; i < 3; ++i) part[i].e[e] = x[i];
+        for (int i = 0; i < 3; ++i) {
+            if constexpr (V == 4)
+                *reinterpret_cast<uint2 *>(to + i * plane) = make_uint2(x[i], y[i]);
+            else
+                to[i * plane] = __ushort_as_bfloat16((unsigned short)x[i]);
         }
-#pragma unroll
-        for (int i = 0; i < 3; ++i) *reinterpret_cast<Part *>(to + i * plane) = part[i];
     } else {
         Run<T, V>::store(to, v);
     }
@@ -52,12 +123,15 @@ inline int gated_grad_row_blocks(int64_t rows, int F, int V) {
 
 // Into dG and dU (rows, pitch), planes of fp32 rows * pitch apart, and, with SUMS,
 // partials[row block][2][F].
-template <typename T, int V, bool SUMS, int ACT>
+template <typename T, int READ, bool SUMS, int ACT>
 __device__ __forceinline__ void gated_grad_rows(const GatedArgs &a, const T *dH, const T *G,
                                                 const T *U, Factor<T> *dG, Factor<T> *dU,
-                                                int64_t pitch, float *partials) {
+                                                int64_t pitch, float *partials,
+                                                float (*s)[kGradWarps][32 * kRowsV<T, READ>]) {
+    constexpr int V = kRowsV<T, READ>;
     using IOV = Run<T, V>;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int64_t total = a.rows * a.F;
     const int f = (blockIdx.x * 32 + lane) * V;
     float sg[V] = {}, su[V] = {};
     if (f < a.F) {
@@ -66,9 +140,9 @@ __device__ __forceinline__ void gated_grad_rows(const GatedArgs &a, const T *dH,
              r += (int64_t)gridDim.y * kGradWarps) {
             const int64_t at = r * a.F + f;
             float h[V], g[V], u[V];
-            IOV::widen(IOV::load(dH + at), h);
-            IOV::widen(IOV::load(G + at), g);
-            IOV::widen(IOV::load(U + at), u);
+            IOV::widen(row_load<T, READ>(dH, at, total), h);
+            IOV::widen(row_load<T, READ>(G, at, total), g);
+            IOV::widen(row_load<T, READ>(U, at, total), u);
 #pragma unroll
             for (int e = 0; e < V; ++e) {
                 float y, slope;
@@ -85,7 +159,6 @@ __device__ __forceinline__ void gated_grad_rows(const GatedArgs &a, const T *dH,
         }
     }
     if (!SUMS) return;
-    __shared__ float s[2][kGradWarps][32 * V];
 #pragma unroll
     for (int e = 0; e < V; ++e) {
         s[0][warp][lane * V + e] = sg[e];
@@ -108,20 +181,24 @@ __device__ __forceinline__ void gated_grad_rows(const GatedArgs &a, const T *dH,
     }
 }
 
-template <typename T, int V, bool SUMS>
-__global__ void __launch_bounds__(kGradThreads)
+template <typename T, int READ, bool SUMS>
+__global__ void __launch_bounds__(kGradThreads, 3)
     gated_grad_kernel(GatedArgs a, const T *dH, const T *G, const T *U, Factor<T> *dG, Factor<T> *dU,
                       int64_t pitch, float *partials) {
+    __shared__ float sums[SUMS ? 2 : 1][SUMS ? kGradWarps : 1][32 * kRowsV<T, READ>];
     with_act(a.act, [&](auto act) {
-        gated_grad_rows<T, V, SUMS, decltype(act)::value>(a, dH, G, U, dG, dU, pitch, partials);
+        gated_grad_rows<T, READ, SUMS, decltype(act)::value>(
+            a, dH, G, U, dG, dU, pitch, partials,
+            reinterpret_cast<float(*)[kGradWarps][32 * kRowsV<T, READ>]>(sums));
     });
 }
 
-template <typename T, int V>
+template <typename T, int READ>
 cudaError_t launch_gated_grad(const GatedArgs &a, const GatedPtrs &p, Factor<T> *dG, Factor<T> *dU,
                               int64_t pitch, float *partials, cudaStream_t s) {
+    constexpr int V = kRowsV<T, READ>;
     const dim3 grid(gated_grad_col_blocks(a.F, V), gated_grad_row_blocks(a.rows, a.F, V));
-    const auto kernel = p.dbg ? gated_grad_kernel<T, V, true> : gated_grad_kernel<T, V, false>;
+    const auto kernel = p.dbg ? gated_grad_kernel<T, READ, true> : gated_grad_kernel<T, READ, false>;
     kernel<<<grid, kGradThreads, 0, s>>>(a, (const T *)p.dH, (const T *)p.G, (const T *)p.U, dG, dU,
                                          pitch, partials);
     return cudaGetLastError();

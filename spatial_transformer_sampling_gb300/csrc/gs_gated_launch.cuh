@@ -18,15 +18,30 @@ template <typename T> struct PadArgs {
     int width;
     int64_t pitch;
 };
-template <typename T, int V> __global__ void __launch_bounds__(256) gated_pad_kernel(PadArgs<T> p) {
-    const int m = blockIdx.y, runs = p.width / V;
-    const int64_t n = p.rows[m] * runs;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-        const int64_t r = i / runs;
-        const int d = (int)(i - r * runs) * V;
-        float v[V];
-        Run<T, V>::widen(Run<T, V>::load(p.from[m] + r * p.width + d), v);
-        store_factor<T, V>(p.to[m] + r * p.pitch + d, p.rows[m] * p.pitch, v);
+// A row is copied by `team` lanes, 8, 16 or 32; a run behind its end is copied too (the
+// pitch is a multiple of one).
+template <typename T, int READ>
+__global__ void __launch_bounds__(256) gated_pad_kernel(PadArgs<T> p, int team) {
+    constexpr int V = kRowsV<T, READ>;
+    const int m = blockIdx.y, lane = threadIdx.x % team, per = 256 / team;
+    // chosen here: an index into the arguments would copy them to the stack
+    const int64_t rows = m == 0 ? p.rows[0] : m == 1 ? p.rows[1] : p.rows[2], total = rows * p.width;
+    const T *from = m == 0 ? p.from[0] : m == 1 ? p.from[1] : p.from[2];
+    Factor<T> *all = m == 0 ? p.to[0] : m == 1 ? p.to[1] : p.to[2];
+    for (int64_t r = (int64_t)blockIdx.x * per + threadIdx.x / team; r < rows; r += (int64_t)gridDim.x * per) {
+        const int64_t at = r * p.width;
+        Factor<T> *to = all + r * p.pitch;
+#pragma unroll 4
+        for (int d = lane * V; d < p.width; d += team * V) {
+            const auto run = row_load<T, READ>(from, at + d, total);
+            if constexpr (sizeof(T) == 2) {
+                *reinterpret_cast<std::remove_const_t<decltype(run)> *>(to + d) = run;
+            } else {
+                float v[V];
+                Run<T, V>::widen(run, v);
+                store_factor<T, V>(to + d, rows * p.pitch, v);
+            }
+        }
     }
 }
 
@@ -73,20 +88,21 @@ cudaError_t gated_operands(const GatedArgs &a, const GatedPtrs &p, const GatedLa
     PadArgs<T> q;
     q.width = a.D;
     q.pitch = at.pitch_d;
-    bool runs = a.D % kVec<T> == 0;
+    const int read = rows_read<T>(a.D, {p.X, p.Wg, p.Wu});
     for (int i = 0; i < 3; ++i) {
         q.rows[i] = i == 0 ? a.rows : a.F;
         q.from[i] = (const T *)from[i];
         q.to[i] = (Factor<T> *)(ws + to[i]);
-        runs = runs && aligned16(from[i]);
         m[i] = {at.copy ? (const void *)q.to[i] : from[i], q.rows[i], a.D, at.pitch_d};
     }
     if (!at.copy) return cudaSuccess;
-    const int64_t most = (a.rows > a.F ? a.rows : a.F) * (int64_t)(a.D / (runs ? kVec<T> : 1));
-    const int64_t need = (most + 255) / 256;
-    const dim3 grid((unsigned)(need < 4 * kGatedSms ? need : 4 * kGatedSms), 3);
-    const auto kernel = runs ? gated_pad_kernel<T, kVec<T>> : gated_pad_kernel<T, 1>;
-    kernel<<<grid, 256, 0, s>>>(q);
+    const int runs = (a.D + kVec<T> - 1) / kVec<T>, team = runs <= 8 ? 8 : runs <= 16 ? 16 : 32;
+    const int64_t need = ((a.rows > a.F ? a.rows : a.F) * team + 255) / 256;
+    const dim3 grid((unsigned)(need < 8 * kGatedSms ? need : 8 * kGatedSms), 3);
+    const auto kernel = read == kRowsSingle ? gated_pad_kernel<T, kRowsSingle>
+                        : read == kRowsRuns ? gated_pad_kernel<T, kRowsRuns>
+                                            : gated_pad_kernel<T, kRowsShifted>;
+    kernel<<<grid, 256, 0, s>>>(q, team);
     return cudaGetLastError();
 }
 
@@ -115,15 +131,16 @@ cudaError_t launch_gated_backward(const GatedArgs &a, const GatedPtrs &p, void *
     char *base = (char *)ws;
     Factor<T> *dG = (Factor<T> *)(base + at.dG), *dU = (Factor<T> *)(base + at.dU);
     float *partials = (float *)(base + at.partials);
-    const bool wide = a.F % kVec<T> == 0 && aligned16(p.dH) && aligned16(p.G) && aligned16(p.U);
+    const int read = rows_read<T>(a.F, {p.dH, p.G, p.U});
     GtMatrix m[3];
     cudaError_t e = gated_operands(a, p, at, base, m, s);
     if (e != cudaSuccess) return e;
-    e = wide ? launch_gated_grad<T, kVec<T>>(a, p, dG, dU, at.pitch_f, partials, s)
-             : launch_gated_grad<T, 1>(a, p, dG, dU, at.pitch_f, partials, s);
+    e = read == kRowsSingle ? launch_gated_grad<T, kRowsSingle>(a, p, dG, dU, at.pitch_f, partials, s)
+        : read == kRowsRuns ? launch_gated_grad<T, kRowsRuns>(a, p, dG, dU, at.pitch_f, partials, s)
+                            : launch_gated_grad<T, kRowsShifted>(a, p, dG, dU, at.pitch_f, partials, s);
     if (e != cudaSuccess) return e;
     if (p.dbg) {
-        const int blocks = gated_grad_row_blocks(a.rows, a.F, wide ? kVec<T> : 1);
+        const int blocks = gated_grad_row_blocks(a.rows, a.F, read == kRowsSingle ? 1 : kVec<T>);
         e = launch_gated_bias_sums<T>(a, p, partials, blocks, true, s);
         if (e != cudaSuccess) return e;
     }

@@ -461,6 +461,15 @@ __global__ void __launch_bounds__(GtShape<T, MODE, NT>::kThreads, 1)
     const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
     GtTile w;
 
+    if (warp == Sh::kCopyWarp) {   // the maps are there when the first copies want them
+        // a plane's maps by four lanes: a[0], a[1], b[0], b[1] of a kind, but for those that
+        // it does not have
+        const int plane = lane / 4 % 3, of = lane % 4, k = lane / 12;
+        const bool has = lane < (kForward ? 12 : 24) && plane < kPlanes &&
+                         !(kForward && of == 1) && !(k == kGtDw && of == 3);
+        if (has) tma_prefetch_map(of < 2 ? &p.kind[k].a[of][plane] : &p.kind[k].b[of - 2][plane]);
+        __syncwarp();
+    }
     if (warp == Sh::kMmaWarp) {
         if (lane == 0) {
             for (int s = 0; s < NS; ++s) {
