@@ -21,9 +21,30 @@ __device__ __forceinline__ float sigmoid_of(float x) {
 constexpr float kGeluTanh2 = 1.5957691216057308f;   // 2 sqrt(2 / pi)
 constexpr float kGeluCubic = 0.044715f;
 
-template <int ACT> __device__ __forceinline__ float act_of(float g) {
+// The normal distribution's Phi(g), and *density = e^(-g^2 / 2).  For 16-bit types by
+// Abramowitz and Stegun's formula 7.1.26, erfc(x) = (a1 t + .. + a5 t^5) e^(-x^2) with
+// t = 1 / (1 + p x), off by 1.5e-7 at most: the exponential serves the slope as well, and
+// the two took 23 us less of 123 in the gradient of 16384 x 4096 (TBD).
+template <typename T> __device__ __forceinline__ float normal_phi(float g, float *density) {
+    *density = exp2_approx(-0.5f * kLog2e * g * g);
+    if (sizeof(T) == 4) return 0.5f * (1.0f + erff(g * 0.70710678118654752f));
+    float t;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(fmaf(0.3275911f * 0.70710678118654752f, fabsf(g), 1.0f)));
+    float q = fmaf(1.061405429f, t, -1.453152027f);
+    q = fmaf(q, t, 1.421413741f);
+    q = fmaf(q, t, -0.284496736f);
+    q = fmaf(q, t, 0.254829592f);
+    const float half_erfc = 0.5f * q * t * *density;   // of |g| / sqrt 2
+    return g < 0.0f ? half_erfc : 1.0f - half_erfc;
+}
+
+// T: the type of the result.
+template <typename T, int ACT> __device__ __forceinline__ float act_of(float g) {
     if (ACT == GS_ACT_SILU) return g * sigmoid_of(g);
-    if (ACT == GS_ACT_GELU) return 0.5f * g * (1.0f + erff(g * 0.70710678118654752f));
+    if (ACT == GS_ACT_GELU) {
+        float density;
+        return g * normal_phi<T>(g, &density);
+    }
     if (ACT == GS_ACT_GELU_TANH) return g * sigmoid_of(kGeluTanh2 * g * fmaf(kGeluCubic * g, g, 1.0f));
     if (ACT == GS_ACT_RELU) return g < 0.0f ? 0.0f : g;   // NaN stays
     if (ACT == GS_ACT_SIGMOID) return sigmoid_of(g);
@@ -48,7 +69,7 @@ inline ActNumbers act_numbers(int act) {
             0.0f};
 }
 // g[i] = act(g[i]) u[i].
-template <int N>
+template <typename T, int N>
 __device__ __forceinline__ void act_product(const ActNumbers &a, float (&g)[N], const float (&u)[N]) {
     if (a.form == 0) {
 #pragma unroll
@@ -59,7 +80,7 @@ __device__ __forceinline__ void act_product(const ActNumbers &a, float (&g)[N], 
         }
     } else if (a.form == 1) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) g[i] = act_of<GS_ACT_GELU>(g[i]) * u[i];
+        for (int i = 0; i < N; ++i) g[i] = act_of<T, GS_ACT_GELU>(g[i]) * u[i];
     } else {
 #pragma unroll
         for (int i = 0; i < N; ++i) g[i] = (g[i] < a.low ? a.low : g[i]) * u[i];   // NaN stays
@@ -67,15 +88,16 @@ __device__ __forceinline__ void act_product(const ActNumbers &a, float (&g)[N], 
 }
 
 // act(g) and its slope.
-template <int ACT> __device__ __forceinline__ void act_and_slope(float g, float &a, float &da) {
+template <typename T, int ACT> __device__ __forceinline__ void act_and_slope(float g, float &a, float &da) {
     if (ACT == GS_ACT_SILU) {
         const float r = sigmoid_of(g);
         a = g * r;
         da = fmaf(a, 1.0f - r, r);
     } else if (ACT == GS_ACT_GELU) {
-        const float phi = 0.5f * (1.0f + erff(g * 0.70710678118654752f));
+        float density;
+        const float phi = normal_phi<T>(g, &density);
         a = g * phi;
-        da = fmaf(g * 0.3989422804014327f, exp2_approx(-0.5f * kLog2e * g * g), phi);
+        da = fmaf(g * 0.3989422804014327f, density, phi);
     } else if (ACT == GS_ACT_GELU_TANH) {
         const float r = sigmoid_of(kGeluTanh2 * g * fmaf(kGeluCubic * g, g, 1.0f));
         a = g * r;

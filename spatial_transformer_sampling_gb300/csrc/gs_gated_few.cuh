@@ -56,7 +56,7 @@ __device__ __forceinline__ void few_store(const GatedArgs &a, const GatedPtrs &p
         ((T *)p.G)[at] = IO<T>::st(g);
         ((T *)p.U)[at] = IO<T>::st(u);
     }
-    with_act(a.act, [&](auto act) { g = act_of<decltype(act)::value>(g) * u; });
+    with_act(a.act, [&](auto act) { g = act_of<T, decltype(act)::value>(g) * u; });
     ((T *)p.H)[at] = IO<T>::st(g);
 }
 

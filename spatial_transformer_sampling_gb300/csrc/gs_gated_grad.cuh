@@ -146,7 +146,7 @@ __device__ __forceinline__ void gated_grad_rows(const GatedArgs &a, const T *dH,
 #pragma unroll
             for (int e = 0; e < V; ++e) {
                 float y, slope;
-                act_and_slope<ACT>(g[e], y, slope);
+                act_and_slope<T, ACT>(g[e], y, slope);
                 g[e] = h[e] * u[e] * slope;
                 u[e] = h[e] * y;
                 if (SUMS) {

@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(kSimtThreads) gated_simt_kernel(GatedArgs a, G
                 gv += IO<T>::ld((const T *)p.bg + n + j);
                 uv += IO<T>::ld((const T *)p.bu + n + j);
             }
-            with_act(a.act, [&](auto act) { h = act_of<decltype(act)::value>(gv) * uv; });
+            with_act(a.act, [&](auto act) { h = act_of<T, decltype(act)::value>(gv) * uv; });
             ((T *)p.H)[at] = IO<T>::st(h);
             if (p.G) {
                 ((T *)p.G)[at] = IO<T>::st(gv);

@@ -670,7 +670,7 @@ __global__ void __launch_bounds__(GtShape<T, MODE, NT>::kThreads, 1)
                         gt_stage<T, kRow>(box + Sh::kBox, 0, g);
                         gt_stage<T, kRow>(box + 2 * Sh::kBox, 0, u);
                     }
-                    act_product(p.act, g, u);
+                    act_product<T>(p.act, g, u);
                     gt_stage<T, kRow>(box, 0, g);
                     gt_store_boxes<T, kRow, Sh::kBoxes>(p.out, box, row0, f0 + i * 32);
                 }
