@@ -15,6 +15,9 @@ namespace gs {
 // without any.)
 constexpr int kFewThreads = 256, kFewWarps = kFewThreads / 32, kFewOutputs = 8;
 constexpr int kFewMost = 32;   // rows of a block
+// Widest rows in 16-bit types: the matrix instruction cuts its sums off as the larger
+// tensor cores do, and a warp's run of them is not broken up.
+constexpr int kFewWidth = 262144;
 
 template <typename T>
 __device__ __forceinline__ void few_mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,

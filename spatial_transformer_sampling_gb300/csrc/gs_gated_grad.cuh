@@ -8,10 +8,22 @@
 
 namespace gs {
 
-// Bound by memory: three reads and two writes of rows x F.  A warp covers 32 V
-// columns of a row; the block's eight warps walk rows, and its sums over them stay
-// in registers until the end.
+// Bound by memory: three reads and two writes of rows x F.  A team of 8, 16 or 32 lanes
+// covers as many runs of a row; the block's teams walk rows, and a lane's sums over them
+// stay in registers until the end.
 constexpr int kGradThreads = 256, kGradWarps = kGradThreads / 32;
+
+// How the rows are gone over: lanes of a team, blocks along F and along the rows (about
+// four blocks of 256 threads per SM).
+struct GradPlan {
+    int team, cols, rows;
+};
+inline GradPlan grad_plan(int64_t rows, int F, int V) {
+    const int runs = (F + V - 1) / V, team = runs <= 8 ? 8 : runs <= 16 ? 16 : 32;
+    const int cols = (runs + team - 1) / team, each = kGradThreads / team;
+    const int64_t most = (4 * kGatedSms + cols - 1) / cols, need = (rows + each - 1) / each;
+    return {team, cols, (int)(need < most ? need : most)};
+}
 
 // fp32 as three bf16 numbers, each the nearest to what the ones before leave: their
 // sum is x to 2^-24 of it or better.  What is not finite stays in the first.  Two at a
@@ -126,18 +138,18 @@ inline int gated_grad_row_blocks(int64_t rows, int F, int V) {
 template <typename T, int READ, bool SUMS, int ACT>
 __device__ __forceinline__ void gated_grad_rows(const GatedArgs &a, const T *dH, const T *G,
                                                 const T *U, Factor<T> *dG, Factor<T> *dU,
-                                                int64_t pitch, float *partials,
+                                                int64_t pitch, float *partials, int team,
                                                 float (*s)[kGradWarps][32 * kRowsV<T, READ>]) {
     constexpr int V = kRowsV<T, READ>;
     using IOV = Run<T, V>;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, teams = kGradThreads / team;
     const int64_t total = a.rows * a.F;
-    const int f = (blockIdx.x * 32 + lane) * V;
+    const int f = (blockIdx.x * team + threadIdx.x % team) * V;
     float sg[V] = {}, su[V] = {};
     if (f < a.F) {
 #pragma unroll 2
-        for (int64_t r = (int64_t)blockIdx.y * kGradWarps + warp; r < a.rows;
-             r += (int64_t)gridDim.y * kGradWarps) {
+        for (int64_t r = (int64_t)blockIdx.y * teams + threadIdx.x / team; r < a.rows;
+             r += (int64_t)gridDim.y * teams) {
             const int64_t at = r * a.F + f;
             float h[V], g[V], u[V];
             IOV::widen(row_load<T, READ>(dH, at, total), h);
@@ -166,13 +178,14 @@ __device__ __forceinline__ void gated_grad_rows(const GatedArgs &a, const T *dH,
     }
     __syncthreads();
     float *out = partials + (int64_t)blockIdx.y * 2 * a.F;
-    for (int c = threadIdx.x; c < 32 * V; c += kGradThreads) {
-        const int d = blockIdx.x * 32 * V + c;
+    // the teams in order
+    const float *all_g = &s[0][0][0], *all_u = &s[1][0][0];
+    for (int c = threadIdx.x; c < team * V; c += kGradThreads) {
+        const int d = blockIdx.x * team * V + c;
         float t0 = 0.0f, t1 = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kGradWarps; ++w) {
-            t0 += s[0][w][c];
-            t1 += s[1][w][c];
+        for (int w = 0; w < teams; ++w) {
+            t0 += all_g[w * team * V + c];
+            t1 += all_u[w * team * V + c];
         }
         if (d < a.F) {
             out[d] = t0;
@@ -184,11 +197,11 @@ __device__ __forceinline__ void gated_grad_rows(const GatedArgs &a, const T *dH,
 template <typename T, int READ, bool SUMS>
 __global__ void __launch_bounds__(kGradThreads, 3)
     gated_grad_kernel(GatedArgs a, const T *dH, const T *G, const T *U, Factor<T> *dG, Factor<T> *dU,
-                      int64_t pitch, float *partials) {
+                      int64_t pitch, float *partials, int team) {
     __shared__ float sums[SUMS ? 2 : 1][SUMS ? kGradWarps : 1][32 * kRowsV<T, READ>];
     with_act(a.act, [&](auto act) {
         gated_grad_rows<T, READ, SUMS, decltype(act)::value>(
-            a, dH, G, U, dG, dU, pitch, partials,
+            a, dH, G, U, dG, dU, pitch, partials, team,
             reinterpret_cast<float(*)[kGradWarps][32 * kRowsV<T, READ>]>(sums));
     });
 }
@@ -197,10 +210,10 @@ template <typename T, int READ>
 cudaError_t launch_gated_grad(const GatedArgs &a, const GatedPtrs &p, Factor<T> *dG, Factor<T> *dU,
                               int64_t pitch, float *partials, cudaStream_t s) {
     constexpr int V = kRowsV<T, READ>;
-    const dim3 grid(gated_grad_col_blocks(a.F, V), gated_grad_row_blocks(a.rows, a.F, V));
+    const GradPlan plan = grad_plan(a.rows, a.F, V);
     const auto kernel = p.dbg ? gated_grad_kernel<T, READ, true> : gated_grad_kernel<T, READ, false>;
-    kernel<<<grid, kGradThreads, 0, s>>>(a, (const T *)p.dH, (const T *)p.G, (const T *)p.U, dG, dU,
-                                         pitch, partials);
+    kernel<<<dim3(plan.cols, plan.rows), kGradThreads, 0, s>>>(
+        a, (const T *)p.dH, (const T *)p.G, (const T *)p.U, dG, dU, pitch, partials, plan.team);
     return cudaGetLastError();
 }
 

@@ -46,11 +46,11 @@ __global__ void __launch_bounds__(256) gated_pad_kernel(PadArgs<T> p, int team) 
 }
 
 // Workspace: copies of X, Wg and Wu where rows are no multiple of 16 bytes, or their
-// planes; backward, dG and dU and the biases' partial sums.
+// planes; backward, dG and dU, the biases' partial sums and those of shared products.
 template <typename T> struct GatedLayout {
     int64_t pitch_d, pitch_f;
     bool copy;
-    size_t X, Wg, Wu, dG, dU, partials, bytes;
+    size_t X, Wg, Wu, dG, dU, partials, sums, bytes;
     GatedLayout(const GatedArgs &a, bool backward) {
         bytes = 0;
         const auto take = [&](int64_t n) {
@@ -69,9 +69,10 @@ template <typename T> struct GatedLayout {
         dG = take(a.rows * pitch_f * each);
         dU = take(a.rows * pitch_f * each);
         // whatever the alignment will be
-        const int b1 = gated_grad_row_blocks(a.rows, a.F, 1);
-        const int bv = gated_grad_row_blocks(a.rows, a.F, kVec<T>);
+        const int b1 = grad_plan(a.rows, a.F, 1).rows;
+        const int bv = grad_plan(a.rows, a.F, kVec<T>).rows;
         partials = take((int64_t)(b1 > bv ? b1 : bv) * 2 * a.F * sizeof(float));
+        sums = take(gt_backward_plan<T>(a).bytes());
     }
 };
 
@@ -108,9 +109,7 @@ cudaError_t gated_operands(const GatedArgs &a, const GatedPtrs &p, const GatedLa
 
 template <typename T>
 cudaError_t launch_gated(const GatedArgs &a, const GatedPtrs &p, void *ws, cudaStream_t s) {
-#ifndef GS_NO_FEW
-    if (a.rows <= kFewMost) return launch_gated_few<T>(a, p, s);
-#endif
+    if (a.rows <= kFewMost && (sizeof(T) == 4 || a.D <= kFewWidth)) return launch_gated_few<T>(a, p, s);
     GtMatrix m[3];
     const GatedLayout<T> at(a, false);
     bool used = false;
@@ -140,13 +139,14 @@ cudaError_t launch_gated_backward(const GatedArgs &a, const GatedPtrs &p, void *
                             : launch_gated_grad<T, kRowsShifted>(a, p, dG, dU, at.pitch_f, partials, s);
     if (e != cudaSuccess) return e;
     if (p.dbg) {
-        const int blocks = gated_grad_row_blocks(a.rows, a.F, read == kRowsSingle ? 1 : kVec<T>);
+        const int blocks = grad_plan(a.rows, a.F, read == kRowsSingle ? 1 : kVec<T>).rows;
         e = launch_gated_bias_sums<T>(a, p, partials, blocks, true, s);
         if (e != cudaSuccess) return e;
     }
     bool used = false;
     e = launch_gt_backward<T>(a, p, m[0], m[1], m[2], {dG, a.rows, a.F, at.pitch_f},
-                              {dU, a.rows, a.F, at.pitch_f}, true, s, &used);
+                              {dU, a.rows, a.F, at.pitch_f}, (float *)(base + at.sums), true, s,
+                              &used);
     if (e != cudaSuccess || used) return e;
     if constexpr (sizeof(T) == 2) {
         const auto product = [&](SimtProduct q, void *out) {

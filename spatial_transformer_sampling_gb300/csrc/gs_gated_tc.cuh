@@ -20,12 +20,20 @@
 // Both operands are read where they lie: K-major or MN-major is a bit of the
 // instruction, nothing is transposed in memory.
 //
+// Where there are few tiles, a long contraction is shared out: each part's fp32 sums go
+// to the workspace and a second kernel adds them in order (262144 rows, D = F = 64:
+// TBD us and TBD).
+//
 // fp32 operands come as three bf16 planes, x = x0 + x1 + x2 to 2^-24 of x or better,
 // and a product is the sum of six of theirs, the small ones first: x2 y0, x0 y2, x1 y1,
-// x1 y0, x0 y1, x0 y0 (the other three are below 2^-26 of it).  The tensor cores cut
-// each sum off at the accumulator's last bit, so the contraction is cut into runs of
-// kGtRun steps: each is accumulated in TMEM by itself and added up in the epilogue's
-// registers, rounded to nearest.
+// x1 y0, x0 y1, x0 y0 (the other three are below 2^-26 of it).
+//
+// The tensor cores cut each sum off at the accumulator's last bit: over n steps of
+// sixteen products a result is off by up to n 2^-24 of its size, always towards 0.  In
+// fp32 the contraction is cut into runs of 4 stages of six products, each accumulated in
+// TMEM by itself and added up in the epilogue's registers, rounded to nearest (2.4e-7 of
+// the result at D = 2048); in 16-bit types no sum in TMEM is longer than 512 stages,
+// 1.2e-4 of the result, a quarter of fp16's half step.
 #pragma once
 
 #include "gs_attn_tc.cuh"
@@ -39,7 +47,8 @@ constexpr int kGtK = 64;              // contraction steps per stage: 128 bytes
 constexpr int kGtA = kGtHalf * kGtK * 2;   // bytes of A's stage
 constexpr int kGtChunk = 64 * kGtK * 2;    // bytes of 64 rows of an MN-major operand
 constexpr int kGtSmem = 224 * 1024;
-constexpr int kGtRun = 4;             // stages of a plane's run (fp32)
+constexpr int kGtRun = 4;             // stages of each product in a run (fp32)
+constexpr int kGtLongest = 512;       // stages of a sum in TMEM (16-bit types)
 
 enum { kGtForward = 0, kGtForwardKeep = 1, kGtBackward = 2 };
 enum { kGtDx = 0, kGtDw = 1 };   // kinds of a backward tile
@@ -215,6 +224,11 @@ struct GtOutput {
 struct GtKind {
     CUtensorMap a[2][kGtMostPlanes], b[2][kGtMostPlanes];
     int tiles_m, tiles_n, k_steps;
+    // parts of the contraction, and where their sums go: rows of `pitch` floats, a part
+    // every `part_stride` floats (backward)
+    int parts, pitch;
+    float *sums;
+    int64_t part_stride;
 };
 
 // Which tiles a pair works on: those of kind `first` go round, `turns` and one more for
@@ -265,7 +279,7 @@ void gt_output(GtOutput *o, void *at, int64_t rows, int width, int box_row) {
 // are numbered eight rows of them at a time, so that those in flight share their operands
 // in L2.
 struct GtTile {
-    int kind, m, n;
+    int kind, m, n, part;
 };
 __device__ __forceinline__ bool gt_tile(const GtArgs &p, int pair, int pairs, int i, GtTile &w) {
     constexpr int kGroup = 8;
@@ -285,6 +299,10 @@ __device__ __forceinline__ bool gt_tile(const GtArgs &p, int pair, int pairs, in
         if (t >= s.others) return false;
     }
     const GtKind &k = p.kind[w.kind];
+    // the parts of all tiles in turn: those in flight read the same rows
+    const int tiles = k.tiles_m * k.tiles_n;
+    w.part = t / tiles;
+    t -= w.part * tiles;
     const int per = kGroup * k.tiles_n, g = t / per, r = t - g * per;
     const int rows = min(kGroup, k.tiles_m - g * kGroup);
     w.m = g * kGroup + r % rows;
@@ -318,23 +336,35 @@ template <int NS> struct GtRing {
 __device__ __forceinline__ int gt_plane_a(int product) { return (0x201100 >> (20 - 4 * product)) & 3; }
 __device__ __forceinline__ int gt_plane_b(int product) { return (0x021010 >> (20 - 4 * product)) & 3; }
 
-// The parts of a tile that TMEM accumulates by themselves, and their steps in order:
-// f(pair of operands, planes of A and B, stage of the contraction) until it is false.
-template <int MODE, int PLANES> __device__ __forceinline__ int gt_units(const GtKind &k, int kind) {
-    if (PLANES == 1) return 1;
-    return (k.k_steps + kGtRun - 1) / kGtRun * (MODE == kGtBackward && kind == kGtDx ? 2 : 1);
+// The runs of a tile's contraction (of its part of it) that TMEM accumulates by
+// themselves, and a run's stages in order: f(pair of operands, planes of A and B, stage of
+// the contraction) until it is false.
+struct GtRuns {
+    int k_steps, from, to;   // the contraction's stages (fp32: runs) from..to - 1
+    template <int PLANES> __device__ __forceinline__ int count() const { return PLANES == 1 ? 1 : to - from; }
+};
+template <int MODE, int PLANES>
+__device__ __forceinline__ GtRuns gt_runs(const GtKind &k, const GtTile &w) {
+    const int operands = MODE == kGtBackward && w.kind == kGtDx ? 2 : 1;
+    const int all = operands * (PLANES == 1 ? k.k_steps : (k.k_steps + kGtRun - 1) / kGtRun);
+    GtRuns r = {k.k_steps, 0, all};
+    if (MODE == kGtBackward && k.parts > 1) {
+        r.from = (int)((int64_t)all * w.part / k.parts);
+        r.to = (int)((int64_t)all * (w.part + 1) / k.parts);
+    }
+    return r;
 }
-template <int MODE, int PLANES, typename F>
-__device__ __forceinline__ void gt_steps(const GtKind &kind, int which_kind, int unit, F &&f) {
+template <int PLANES, typename F>
+__device__ __forceinline__ void gt_steps(const GtRuns &r, int run, F &&f) {
     if (PLANES == 1) {
-        const int operands = MODE == kGtBackward && which_kind == kGtDx ? 2 : 1;
-        for (int which = 0; which < operands; ++which)
-            for (int k = 0; k < kind.k_steps; ++k)
-                if (!f(which, 0, 0, k)) return;
+        for (int k = r.from; k < r.to; ++k) {
+            const int which = k >= r.k_steps;
+            if (!f(which, 0, 0, k - which * r.k_steps)) return;
+        }
         return;
     }
-    const int runs = (kind.k_steps + kGtRun - 1) / kGtRun, which = unit >= runs;
-    const int k0 = (unit - which * runs) * kGtRun, k1 = min(k0 + kGtRun, kind.k_steps);
+    const int runs = (r.k_steps + kGtRun - 1) / kGtRun, at = r.from + run, which = at >= runs;
+    const int k0 = (at - which * runs) * kGtRun, k1 = min(k0 + kGtRun, r.k_steps);
     for (int product = 0; product < 6; ++product)
         for (int k = k0; k < k1; ++k)
             if (!f(which, gt_plane_a(product), gt_plane_b(product), k)) return;
@@ -502,9 +532,9 @@ __global__ void __launch_bounds__(GtShape<T, MODE, NT>::kThreads, 1)
             GtRing<NS> r;
             for (int i = 0; ok && gt_tile(p, pair, pairs, i, w); ++i) {
                 const GtKind &kind = p.kind[w.kind];
-                const int units = gt_units<MODE, kPlanes>(kind, w.kind);
-                for (int u = 0; u < units && ok; ++u)
-                    gt_steps<MODE, kPlanes>(kind, w.kind, u, [&](int which, int pa, int pb, int k) {
+                const GtRuns runs = gt_runs<MODE, kPlanes>(kind, w);
+                for (int u = 0, units = runs.count<kPlanes>(); u < units && ok; ++u)
+                    gt_steps<kPlanes>(runs, u, [&](int which, int pa, int pb, int k) {
                         const int s = r.stage;
                         ok = gt_wait(&empty[s], r.parity ^ 1, p.err);
                         if (!ok) return false;
@@ -562,20 +592,20 @@ __global__ void __launch_bounds__(GtShape<T, MODE, NT>::kThreads, 1)
             int count = 0;
             for (int t = 0; ok && gt_tile(p, pair, pairs, t, w); ++t) {
                 const GtKind &kind = p.kind[w.kind];
-                const int units = gt_units<MODE, kPlanes>(kind, w.kind);
+                const GtRuns runs = gt_runs<MODE, kPlanes>(kind, w);
                 // A is M-major for dW: 16 steps of the contraction are 16 rows, not 32 bytes of one
                 const bool amn = !kForward && w.kind == kGtDw;
                 const uint32_t idesc = idesc_k | (amn ? 1u << 15 : 0u);
                 const uint32_t a0 = amn ? umma_lo_mnmajor(base, kGtChunk) : umma_lo_kmajor(base);
                 const uint32_t a_step = (amn ? 2048 : 32) / 16;
-                for (int u = 0; u < units && ok; ++u, ++count) {
+                for (int u = 0, units = runs.count<kPlanes>(); u < units && ok; ++u, ++count) {
                     const int b = count & 1;
                     if (count >= 2)
                         ok = __all_sync(0xffffffffu,
                                         tc_wait_cluster(&tile_empty[b], (count / 2 - 1) & 1, p.err));
                     uint32_t more = 0;
                     if (!ok) break;
-                    gt_steps<MODE, kPlanes>(kind, w.kind, u, [&](int, int, int, int) {
+                    gt_steps<kPlanes>(runs, u, [&](int, int, int, int) {
                         const int s = r.stage;
                         ok = gt_wait(&full[s], r.parity, p.err);
                         if (!ok) return false;
@@ -612,7 +642,7 @@ __global__ void __launch_bounds__(GtShape<T, MODE, NT>::kThreads, 1)
         int count = 0;
         for (int t = 0; ok && gt_tile(p, pair, pairs, t, w); ++t) {
             const GtKind &kind = p.kind[w.kind];
-            const int units = gt_units<MODE, kPlanes>(kind, w.kind);
+            const int units = gt_runs<MODE, kPlanes>(kind, w).template count<kPlanes>();
             const int64_t row0 = (int64_t)w.m * kGtTile + rank * kGtHalf + quarter * 32;
             const int f0 = w.n * (NT / 2) + part * kHalf * 32;   // forward: the first output
             float bias[kHalf][2] = {};                           // of outputs f0 + 32 i + lane
@@ -623,7 +653,7 @@ __global__ void __launch_bounds__(GtShape<T, MODE, NT>::kThreads, 1)
                         bias[i][0] = IO<T>::ld((const T *)bg + f0 + i * 32 + lane);
                         bias[i][1] = IO<T>::ld((const T *)bu + f0 + i * 32 + lane);
                     }
-            // the warp's columns: of one part in TMEM, or the sums of them all
+            // the warp's columns: of one run in TMEM, or the sums of them all
             float v[kRuns][32];
             if (kPlanes > 1)
 #pragma unroll
@@ -646,7 +676,7 @@ __global__ void __launch_bounds__(GtShape<T, MODE, NT>::kThreads, 1)
 #pragma unroll
                     for (int i = 0; i < kRuns; ++i) gt_columns_of(at + column(i), v[i]);
                 }
-                // TMEM is read: the part after next may be multiplied
+                // TMEM is read: the run after next may be multiplied
                 tcgen05_fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_remote(smem_of_rank(smem_u32(&tile_empty[b]), 0));
@@ -679,6 +709,19 @@ __global__ void __launch_bounds__(GtShape<T, MODE, NT>::kThreads, 1)
                 const GtOutput *out = &p.out[w.kind == kGtDw ? 1 + which : 0];
                 const int64_t out_row = row0 - (int64_t)which * half * kGtTile;
                 const int col0 = w.n * NT + part * Sh::kCols;
+                if (kind.parts > 1) {   // this part's sums, for the kernel that adds them
+                    if (out_row + lane >= out->rows) continue;
+                    float *to = kind.sums + w.part * kind.part_stride +
+                                (which * out->rows + out_row + lane) * kind.pitch + col0;
+#pragma unroll
+                    for (int i = 0; i < kRuns; ++i)
+                        if (col0 + i * 32 < kind.pitch)   // a multiple of 32
+#pragma unroll
+                            for (int c = 0; c < 32; c += 4)
+                                *reinterpret_cast<float4 *>(to + i * 32 + c) =
+                                    make_float4(v[i][c], v[i][c + 1], v[i][c + 2], v[i][c + 3]);
+                    continue;
+                }
                 // two runs at a time: a box of both, or one each
 #pragma unroll
                 for (int i = 0; i < kRuns; i += 2) {
@@ -768,10 +811,13 @@ cudaError_t launch_gt_as(GtArgs &p, bool follows, cudaStream_t s) {
     int pairs = 0;
     const cudaError_t e = gt_most_pairs<T, MODE, NT>(&pairs);
     if (e != cudaSuccess) return e;
-    const int64_t n0 = (int64_t)p.kind[0].tiles_m * p.kind[0].tiles_n;
-    const int64_t n1 = (int64_t)p.kind[1].tiles_m * p.kind[1].tiles_n;
+    const auto tiles = [&](int k) { return (int64_t)p.kind[k].tiles_m * p.kind[k].tiles_n * p.kind[k].parts; };
+    const auto stages = [&](int k) {   // of a tile's part
+        const int64_t all = (int64_t)p.kind[k].k_steps * (MODE == kGtBackward && k == kGtDx ? 2 : 1);
+        return p.kind[k].parts ? (all + p.kind[k].parts - 1) / p.kind[k].parts : 0;
+    };
+    const int64_t n0 = tiles(0), n1 = tiles(1), k0 = stages(0), k1 = stages(1);
     if (n0 + n1 < pairs) pairs = (int)(n0 + n1);
-    const int64_t k0 = p.kind[0].k_steps * (MODE == kGtBackward ? 2 : 1), k1 = p.kind[1].k_steps;
     int64_t length;
     p.plan = k0 >= k1 ? gt_schedule(0, n0, k0, n1, k1, pairs, &length)
                       : gt_schedule(1, n1, k1, n0, k0, pairs, &length);
@@ -779,11 +825,92 @@ cudaError_t launch_gt_as(GtArgs &p, bool follows, cudaStream_t s) {
                        Sh::kThreads, Sh::kSmem, s, p);
 }
 
-// Whether tiles of 128 columns are done sooner than tiles of 256: `length(NT)` are the
-// stages of the pair that has most.  A stage takes 0.216 us with 128 columns (its copies
-// bound it) and 0.302 with 256 (its MMAs).
-template <typename F> bool gt_narrow(F &&length) {
-    return (double)length(128) * 0.216 < (double)length(256) * 0.302;
+// What a stage takes in us with tiles of 128 columns (its copies bound it) and of 256
+// (its MMAs), as measured.
+constexpr double gt_stage_us(int nt) { return nt == 128 ? 0.216 : 0.302; }
+constexpr int kGtPairs = kGatedSms / 2;
+
+// How the backward products are laid out: columns of a tile, parts of each kind's
+// contraction, and the workspace of the parts' sums.
+struct GtBackwardPlan {
+    int columns, parts[2], pitch;
+    int64_t sums[2];   // floats
+    int64_t bytes() const { return (sums[0] + sums[1]) * 4; }
+};
+template <typename T> GtBackwardPlan gt_backward_plan(const GatedArgs &a) {
+    const int products = sizeof(T) == 4 ? 6 : 1;
+    const int64_t rows_of[2] = {a.rows, 2 * (int64_t)a.F};
+    const int64_t tiles_m[2] = {(a.rows + kGtTile - 1) / kGtTile,
+                                2 * (((int64_t)a.F + kGtTile - 1) / kGtTile)};
+    const int64_t k[2] = {2 * (((int64_t)a.F + kGtK - 1) / kGtK), (a.rows + kGtK - 1) / kGtK};
+    GtBackwardPlan best = {};
+    double least = 0.0;
+    for (const int nt : {256, 128})
+        for (const bool share : {false, true}) {
+            GtBackwardPlan q = {nt, {1, 1}, (a.D + 31) / 32 * 32, {0, 0}};
+            const int64_t n = (a.D + nt - 1) / nt;
+            const int64_t even = (n * (tiles_m[0] * k[0] + tiles_m[1] * k[1]) + kGtPairs - 1) / kGtPairs;
+            double us = 0.0;
+            // shared out: parts of what a pair has, of eight stages at least
+            int64_t most = share ? (even > 8 ? even : 8) : INT64_MAX;
+            if (sizeof(T) == 2 && most > kGtLongest) most = kGtLongest;
+            for (int i = 0; i < 2; ++i) {
+                q.parts[i] = (int)((k[i] - 1) / most) + 1;
+                if (q.parts[i] > 1) q.sums[i] = q.parts[i] * rows_of[i] * q.pitch;
+            }
+            if (q.bytes() > 0) us = 5.0 + 2.0 * (double)q.bytes() / 4e6;   // a kernel more, at 4 TB/s
+            const int64_t n0 = n * tiles_m[0] * q.parts[0], n1 = n * tiles_m[1] * q.parts[1];
+            const int64_t k0 = (k[0] + q.parts[0] - 1) / q.parts[0], k1 = (k[1] + q.parts[1] - 1) / q.parts[1];
+            int64_t length;
+            if (k0 >= k1)
+                gt_schedule(kGtDx, n0, k0, n1, k1, kGtPairs, &length);
+            else
+                gt_schedule(kGtDw, n1, k1, n0, k0, kGtPairs, &length);
+            us += (double)length * products * gt_stage_us(nt);
+            if (best.columns == 0 || us < least) {
+                best = q;
+                least = us;
+            }
+        }
+    return best;
+}
+
+// The sums of the parts, added in order and rounded: four columns a thread.
+struct GtJoin {
+    const float *from[2];
+    int parts[2], pitch, D;
+    int64_t rows[2], part_stride[2];   // dX's rows; dWg's and then dWu's
+    void *dX, *dWg, *dWu;
+};
+template <typename T> __global__ void __launch_bounds__(256) gated_join_kernel(GtJoin j) {
+    const int kind = blockIdx.y, quads = j.pitch / 4;
+    const int parts = kind ? j.parts[1] : j.parts[0];
+    const float *from = kind ? j.from[1] : j.from[0];
+    const int64_t rows = kind ? j.rows[1] : j.rows[0], stride = kind ? j.part_stride[1] : j.part_stride[0];
+    wait_for_previous_kernel(from);
+    if (parts < 2) return;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < rows * quads; i += (int64_t)gridDim.x * 256) {
+        const int64_t r = i / quads;
+        const int d = (int)(i - r * quads) * 4;
+        if (d >= j.D) continue;
+        float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+        for (int s = 0; s < parts; ++s) {
+            const float4 x = *reinterpret_cast<const float4 *>(from + s * stride + r * j.pitch + d);
+            t.x += x.x;
+            t.y += x.y;
+            t.z += x.z;
+            t.w += x.w;
+        }
+        const int64_t half = rows / 2;
+        T *out = kind == kGtDx ? (T *)j.dX + r * j.D
+                 : r < half    ? (T *)j.dWg + r * j.D
+                               : (T *)j.dWu + (r - half) * j.D;
+        const float v[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (d + e < j.D) out[d + e] = IO<T>::st(v[e]);
+    }
 }
 
 // Forward pass from 16-bit operands (T float: planes); *used: TMA takes them.
@@ -792,16 +919,19 @@ cudaError_t launch_gt_forward(const GatedArgs &a, const GatedPtrs &q, const GtMa
                               const GtMatrix &Wg, const GtMatrix &Wu, bool follows, cudaStream_t s,
                               bool *used) {
     GtArgs p = {};
+    *used = false;
+    if (sizeof(T) == 2 && a.D > kGtLongest * kGtK) return cudaSuccess;
     GtKind &k = p.kind[0];
     k.tiles_m = (int)((a.rows + kGtTile - 1) / kGtTile);
     k.k_steps = (a.D + kGtK - 1) / kGtK;
     const auto tiles_n = [&](int nt) { return (a.F + nt / 2 - 1) / (nt / 2); };
-    const bool narrow = gt_narrow([&](int nt) {
-        const int64_t pairs = kGatedSms / 2;
-        return ((int64_t)k.tiles_m * tiles_n(nt) + pairs - 1) / pairs;
-    });
+    const auto us = [&](int nt) {
+        return (double)(((int64_t)k.tiles_m * tiles_n(nt) + kGtPairs - 1) / kGtPairs) * gt_stage_us(nt);
+    };
+    const bool narrow = us(128) < us(256);
     const int nt = narrow ? 128 : 256;
     k.tiles_n = tiles_n(nt);
+    k.parts = 1;
     *used = gt_maps<T>(k.a[0], X, kGtHalf) && gt_maps<T>(k.b[0], Wg, nt / 2) &&
             gt_maps<T>(k.b[1], Wu, nt / 2);
     if (!*used) return cudaSuccess;
@@ -827,7 +957,8 @@ cudaError_t launch_gt_forward(const GatedArgs &a, const GatedPtrs &q, const GtMa
 template <typename T>
 cudaError_t launch_gt_backward(const GatedArgs &a, const GatedPtrs &q, const GtMatrix &X,
                                const GtMatrix &Wg, const GtMatrix &Wu, const GtMatrix &dG,
-                               const GtMatrix &dU, bool follows, cudaStream_t s, bool *used) {
+                               const GtMatrix &dU, float *sums, bool follows, cudaStream_t s,
+                               bool *used) {
     GtArgs p = {};
     GtKind &x = p.kind[kGtDx], &w = p.kind[kGtDw];
     *used = gt_maps<T>(x.a[0], dG, kGtHalf) && gt_maps<T>(x.a[1], dU, kGtHalf) &&
@@ -843,20 +974,29 @@ cudaError_t launch_gt_backward(const GatedArgs &a, const GatedPtrs &q, const GtM
     x.k_steps = (a.F + kGtK - 1) / kGtK;
     w.tiles_m = 2 * ((a.F + kGtTile - 1) / kGtTile);
     w.k_steps = (int)((a.rows + kGtK - 1) / kGtK);
-    const bool narrow = gt_narrow([&](int nt) {
-        const int64_t n = (a.D + nt - 1) / nt, nx = x.tiles_m * n, nw = w.tiles_m * n;
-        const int64_t kx = 2 * (int64_t)x.k_steps, kw = w.k_steps;
-        int64_t length;
-        if (kx >= kw)
-            gt_schedule(kGtDx, nx, kx, nw, kw, kGatedSms / 2, &length);
-        else
-            gt_schedule(kGtDw, nw, kw, nx, kx, kGatedSms / 2, &length);
-        return length;
-    });
-    const int nt = narrow ? 128 : 256;
+    const GtBackwardPlan plan = gt_backward_plan<T>(a);
+    const int nt = plan.columns;
     x.tiles_n = w.tiles_n = (a.D + nt - 1) / nt;
-    return narrow ? launch_gt_as<T, kGtBackward, 128>(p, follows, s)
-                  : launch_gt_as<T, kGtBackward, 256>(p, follows, s);
+    const int64_t rows_of[2] = {a.rows, 2 * (int64_t)a.F};
+    for (int i = 0; i < 2; ++i) {
+        p.kind[i].parts = plan.parts[i];
+        p.kind[i].pitch = plan.pitch;
+        p.kind[i].sums = sums + (i ? plan.sums[0] : 0);
+        p.kind[i].part_stride = rows_of[i] * plan.pitch;
+    }
+    const cudaError_t e = nt == 128 ? launch_gt_as<T, kGtBackward, 128>(p, follows, s)
+                                    : launch_gt_as<T, kGtBackward, 256>(p, follows, s);
+    if (e != cudaSuccess || plan.bytes() == 0) return e;
+    const GtJoin j = {{x.sums, w.sums},     {x.parts, w.parts},
+                      plan.pitch,           a.D,
+                      {rows_of[0], rows_of[1]}, {x.part_stride, w.part_stride},
+                      q.dX,                 q.dWg,
+                      q.dWu};
+    const int64_t most = (x.parts > 1 && (w.parts < 2 || rows_of[0] > rows_of[1]) ? rows_of[0] : rows_of[1]) *
+                         (plan.pitch / 4);
+    const int64_t need = (most + 255) / 256;
+    return launch_next(true, gated_join_kernel<T>,
+                       dim3((unsigned)(need < 8 * kGatedSms ? need : 8 * kGatedSms), 2), 256, 0, s, j);
 }
 
 }  // namespace gs

@@ -46,7 +46,8 @@ def test_activations(gs_cuda, rows, act, dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("rows,D,F", [(3000, 192, 520), (2049, 1024, 1160)])
+@pytest.mark.parametrize("rows,D,F", [(3000, 192, 520), (2049, 1024, 1160), (40000, 16, 24),
+                                      (70001, 9, 8), (100, 64, 3000), (33, 8, 40000)])
 def test_larger(gs_cuda, rows, D, F, dtype):
     _both(gs_cuda, rows, D, F, dtype, "gelu_tanh", True, 3)
 
