@@ -149,9 +149,13 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap
 // Stores a box from shared memory; what lies outside the tensor is not written.  The
 // outputs are the first to leave L2, where the operands are read again: 191 us instead
 // of 197 for 16384 x 1024 x 4096, kept.
-__device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, int c0, int c1, uint32_t src) {
+__device__ __forceinline__ uint64_t first_to_leave() {
     uint64_t policy;
     asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+    return policy;
+}
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, int c0, int c1, uint32_t src,
+                                             uint64_t policy) {
     asm volatile(
         "cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group.L2::cache_hint [%0, {%1, %2}], "
         "[%3], %4;" ::"l"(reinterpret_cast<uint64_t>(map)),
@@ -224,6 +228,7 @@ struct GtOutput {
 struct GtKind {
     CUtensorMap a[2][kGtMostPlanes], b[2][kGtMostPlanes];
     int tiles_m, tiles_n, k_steps;
+    uint32_t per_tiles, per_group;   // 2^32 over the kind's tiles, and over a group's
     // parts of the contraction, and where their sums go: rows of `pitch` floats, a part
     // every `part_stride` floats (backward)
     int parts, pitch;
@@ -275,6 +280,23 @@ void gt_output(GtOutput *o, void *at, int64_t rows, int width, int box_row) {
                            box_row == 128, box_row == 64);
 }
 
+// n / d and its remainder by 2^32 / d, rounded down: the estimate is 1 too small at most.
+// (Every warp asks for its next tile: by the compiler's division that took 800 cycles, a
+// seventh of a tile of 64 channels.)
+constexpr uint32_t gt_per(int64_t d) { return d > 1 ? (uint32_t)((int64_t(1) << 32) / d) : 0xFFFFFFFFu; }
+__device__ __forceinline__ int gt_divide(int n, int d, uint32_t per, int &rest) {
+    int q = (int)__umulhi((uint32_t)n, per);
+    rest = n - q * d;
+    if (rest >= d) {
+        ++q;
+        rest -= d;
+    }
+    return q;
+}
+
+// Rows of tiles that are numbered together.
+constexpr int kGtGroup = 8;
+
 // The i-th tile of pair `pair` of `pairs`; false when there are no more.  Tiles of a kind
 // are numbered eight rows of them at a time, so that those in flight share their operands
 // in L2.
@@ -282,7 +304,6 @@ struct GtTile {
     int kind, m, n, part;
 };
 __device__ __forceinline__ bool gt_tile(const GtArgs &p, int pair, int pairs, int i, GtTile &w) {
-    constexpr int kGroup = 8;
     const GtSchedule &s = p.plan;
     const bool extra = pair < s.extra;
     const int turns = s.turns + extra;
@@ -300,13 +321,18 @@ __device__ __forceinline__ bool gt_tile(const GtArgs &p, int pair, int pairs, in
     }
     const GtKind &k = p.kind[w.kind];
     // the parts of all tiles in turn: those in flight read the same rows
-    const int tiles = k.tiles_m * k.tiles_n;
-    w.part = t / tiles;
-    t -= w.part * tiles;
-    const int per = kGroup * k.tiles_n, g = t / per, r = t - g * per;
-    const int rows = min(kGroup, k.tiles_m - g * kGroup);
-    w.m = g * kGroup + r % rows;
-    w.n = r / rows;
+    w.part = 0;
+    if (k.parts > 1) w.part = gt_divide(t, k.tiles_m * k.tiles_n, k.per_tiles, t);
+    int r;
+    const int g = gt_divide(t, kGtGroup * k.tiles_n, k.per_group, r);
+    const int rows = k.tiles_m - g * kGtGroup;
+    if (rows >= kGtGroup) {
+        w.m = g * kGtGroup + r % kGtGroup;
+        w.n = r / kGtGroup;
+    } else {   // the last group, lower than the others
+        w.m = g * kGtGroup + r % rows;
+        w.n = r / rows;
+    }
     return true;
 }
 
@@ -390,24 +416,23 @@ __device__ __forceinline__ void gt_store_plain(const GtOutput &o, const unsigned
     }
 }
 
-// N boxes of a warp, one for each output, all of them at row0 and col0.
+// N boxes of a warp, one for each output, all of them at row0 and col0: a lane each.
 template <typename T, int ROW, int N>
 __device__ __forceinline__ void gt_store_boxes(const GtOutput *out, const unsigned char *box,
-                                               int64_t row0, int col0) {
+                                               int64_t row0, int col0, uint64_t policy) {
+    const int lane = threadIdx.x % 32;
     fence_proxy_async_smem();   // all lanes' writes, before the TMA reads them
     __syncwarp();
     if (row0 >= out->rows || col0 >= out->width) return;
+    if (lane < N && out[lane].boxes)
+        tma_store_2d(&out[lane].map, col0, (int)row0, smem_u32(box + lane * 32 * ROW), policy);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        if (!out[i].boxes)
-            gt_store_plain<T, ROW>(out[i], box + i * 32 * ROW, row0, col0);
-        else if (threadIdx.x % 32 == 0)
-            tma_store_2d(&out[i].map, col0, (int)row0, smem_u32(box + i * 32 * ROW));
-    }
+    for (int i = 0; i < N; ++i)
+        if (!out[i].boxes) gt_store_plain<T, ROW>(out[i], box + i * 32 * ROW, row0, col0);
 }
 // Until a warp's boxes may be written again.
 __device__ __forceinline__ void gt_boxes_free() {
-    if (threadIdx.x % 32 == 0) {
+    if (threadIdx.x % 32 < 3) {   // the lanes that store
         bulk_commit();
         bulk_wait_read();
     }
@@ -434,9 +459,12 @@ __device__ __forceinline__ void gt_stage(unsigned char *box, int col, const floa
     }
 }
 
-// Loads 32 columns of this lane's row from TMEM.
-__device__ __forceinline__ void gt_columns_of(uint32_t at, float (&v)[32]) {
-    tmem_ld_x32(at, reinterpret_cast<uint32_t (&)[32]>(v));
+// Loads twice 32 columns of this lane's row from TMEM.
+__device__ __forceinline__ void gt_columns_of(uint32_t a, uint32_t b, float (&v)[32], float (&w)[32]) {
+    tmem_start_ld_x32(a, reinterpret_cast<uint32_t (&)[32]>(v));
+    tmem_start_ld_x32(b, reinterpret_cast<uint32_t (&)[32]>(w));
+    tmem_wait_ld(reinterpret_cast<uint32_t (&)[32]>(v));
+    tmem_wait_ld(reinterpret_cast<uint32_t (&)[32]>(w));
 }
 
 // v += 16 columns of this lane's row in TMEM.
@@ -639,6 +667,7 @@ __global__ void __launch_bounds__(GtShape<T, MODE, NT>::kThreads, 1)
         // where the warp's i-th 32 columns start in TMEM; forward, U's follow G's
         constexpr int kRuns = Sh::kCols / 32, kHalf = kForward ? kRuns / 2 : kRuns;
         const auto column = [&](int i) { return i / kHalf * (NT / 2) + (part * kHalf + i % kHalf) * 32; };
+        const uint64_t policy = first_to_leave();
         int count = 0;
         for (int t = 0; ok && gt_tile(p, pair, pairs, t, w); ++t) {
             const GtKind &kind = p.kind[w.kind];
@@ -673,8 +702,8 @@ __global__ void __launch_bounds__(GtShape<T, MODE, NT>::kThreads, 1)
                         gt_add_columns(at + column(i) + 16, v[i] + 16);
                     }
                 } else {
-#pragma unroll
-                    for (int i = 0; i < kRuns; ++i) gt_columns_of(at + column(i), v[i]);
+                    static_assert(kRuns == 2, "both loads before one wait");
+                    gt_columns_of(at + column(0), at + column(1), v[0], v[kRuns - 1]);
                 }
                 // TMEM is read: the run after next may be multiplied
                 tcgen05_fence_before_sync();
@@ -702,7 +731,7 @@ __global__ void __launch_bounds__(GtShape<T, MODE, NT>::kThreads, 1)
                     }
                     act_product<T>(p.act, g, u);
                     gt_stage<T, kRow>(box, 0, g);
-                    gt_store_boxes<T, kRow, Sh::kBoxes>(p.out, box, row0, f0 + i * 32);
+                    gt_store_boxes<T, kRow, Sh::kBoxes>(p.out, box, row0, f0 + i * 32, policy);
                 }
             } else {
                 const int half = kind.tiles_m / 2, which = w.kind == kGtDw && w.m >= half;
@@ -729,12 +758,13 @@ __global__ void __launch_bounds__(GtShape<T, MODE, NT>::kThreads, 1)
                     if constexpr (Sh::kBoxCols == 64) {
                         gt_stage<T, kRow>(box, 0, v[i]);
                         gt_stage<T, kRow>(box, 32, v[i + 1]);
-                        gt_store_boxes<T, kRow, 1>(out, box, out_row, col0 + i * 32);
+                        gt_store_boxes<T, kRow, 1>(out, box, out_row, col0 + i * 32, policy);
                     } else {
                         gt_stage<T, kRow>(box, 0, v[i]);
                         gt_stage<T, kRow>(box + Sh::kBox, 0, v[i + 1]);
-                        gt_store_boxes<T, kRow, 1>(out, box, out_row, col0 + i * 32);
-                        gt_store_boxes<T, kRow, 1>(out, box + Sh::kBox, out_row, col0 + i * 32 + 32);
+                        gt_store_boxes<T, kRow, 1>(out, box, out_row, col0 + i * 32, policy);
+                        gt_store_boxes<T, kRow, 1>(out, box + Sh::kBox, out_row, col0 + i * 32 + 32,
+                                                      policy);
                     }
                 }
             }
@@ -818,6 +848,10 @@ cudaError_t launch_gt_as(GtArgs &p, bool follows, cudaStream_t s) {
     };
     const int64_t n0 = tiles(0), n1 = tiles(1), k0 = stages(0), k1 = stages(1);
     if (n0 + n1 < pairs) pairs = (int)(n0 + n1);
+    for (GtKind &k : p.kind) {
+        k.per_tiles = gt_per((int64_t)k.tiles_m * k.tiles_n);
+        k.per_group = gt_per((int64_t)kGtGroup * k.tiles_n);
+    }
     int64_t length;
     p.plan = k0 >= k1 ? gt_schedule(0, n0, k0, n1, k1, pairs, &length)
                       : gt_schedule(1, n1, k1, n0, k0, pairs, &length);
