@@ -133,12 +133,76 @@ inline int gated_grad_row_blocks(int64_t rows, int F, int V) {
     return (int)(need < most ? need : most);
 }
 
+// In fp16 dG and dU are scaled by a power of two, so that as factors of the products they
+// neither leave the type's range nor fall among its subnormal numbers: 2^14 over the
+// power of two below `bound`, the largest |dH| max(1.13 |U|, |G|) of the call (no
+// activation's slope is above 1.13, and no activation above |G|, sigmoid's above 1).
+// Finding it takes one more pass over the inputs; the second one finds up to 100 MB of
+// them in L2.
+constexpr float kMostSlope = 1.13f;
+__device__ __forceinline__ float gated_scale(uint32_t bound, bool inverse) {
+    const int e = (int)(bound >> 23) - 127;            // of a number that is not negative
+    if (bound == 0 || e == 128) return 1.0f;           // nothing, or infinity
+    const int s = max(-100, min(100, inverse ? e - 14 : 14 - e));
+    return __int_as_float((s + 127) << 23);
+}
+template <typename T, int READ>
+__global__ void __launch_bounds__(kGradThreads)
+    gated_bound_kernel(GatedArgs a, const T *dH, const T *G, const T *U, uint32_t *bound) {
+    constexpr int V = kRowsV<T, READ == kRowsSingle ? kRowsSingle : kRowsRuns>;
+    using IOV = Run<T, V>;
+    const int64_t total = a.rows * a.F, runs = total / V;
+    const float low = a.act == GS_ACT_SIGMOID ? 1.0f : 0.0f;
+    float most = 0.0f;
+    const auto take = [&](float h, float g, float u) {
+        most = fmaxf(most, fabsf(h) * fmaxf(kMostSlope * fabsf(u), fmaxf(fabsf(g), low)));
+    };
+    // the rows are one array here
+#pragma unroll 2
+    for (int64_t i = (int64_t)blockIdx.x * kGradThreads + threadIdx.x; i < runs;
+         i += (int64_t)gridDim.x * kGradThreads) {
+        float h[V], g[V], u[V];
+        IOV::widen(IOV::load(dH + i * V), h);
+        IOV::widen(IOV::load(G + i * V), g);
+        IOV::widen(IOV::load(U + i * V), u);
+#pragma unroll
+        for (int e = 0; e < V; ++e) take(h[e], g[e], u[e]);
+    }
+    if (blockIdx.x == 0 && runs * V + threadIdx.x < total) {
+        const int64_t e = runs * V + threadIdx.x;
+        take(IO<T>::ld(dH + e), IO<T>::ld(G + e), IO<T>::ld(U + e));
+    }
+    // a maximum does not depend on the order, and numbers that are not negative compare
+    // as their bits do
+    __shared__ float warps[kGradWarps];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+    if (threadIdx.x % 32 == 0) warps[threadIdx.x / 32] = most;
+    __syncthreads();
+    if (threadIdx.x > 0) return;
+#pragma unroll
+    for (int w = 1; w < kGradWarps; ++w) most = fmaxf(most, warps[w]);
+    atomicMax(bound, __float_as_uint(most));
+}
+template <typename T>
+cudaError_t launch_gated_bound(const GatedArgs &a, const GatedPtrs &p, bool runs, uint32_t *bound,
+                               cudaStream_t s) {
+    const cudaError_t e = cudaMemsetAsync(bound, 0, sizeof(uint32_t), s);
+    if (e != cudaSuccess) return e;
+    const int V = runs ? kVec<T> : 1;
+    const int64_t need = (a.rows * a.F / V + kGradThreads - 1) / kGradThreads;
+    const unsigned blocks = (unsigned)(need < 8 * kGatedSms ? (need > 0 ? need : 1) : 8 * kGatedSms);
+    const auto kernel = runs ? gated_bound_kernel<T, kRowsRuns> : gated_bound_kernel<T, kRowsSingle>;
+    kernel<<<blocks, kGradThreads, 0, s>>>(a, (const T *)p.dH, (const T *)p.G, (const T *)p.U, bound);
+    return cudaGetLastError();
+}
+
 // Into dG and dU (rows, pitch), planes of fp32 rows * pitch apart, and, with SUMS,
 // partials[row block][2][F].
 template <typename T, int READ, bool SUMS, int ACT>
 __device__ __forceinline__ void gated_grad_rows(const GatedArgs &a, const T *dH, const T *G,
                                                 const T *U, Factor<T> *dG, Factor<T> *dU,
-                                                int64_t pitch, float *partials, int team,
+                                                int64_t pitch, float *partials, int team, float scale,
                                                 float (*s)[kGradWarps][32 * kRowsV<T, READ>]) {
     constexpr int V = kRowsV<T, READ>;
     using IOV = Run<T, V>;
@@ -164,6 +228,13 @@ __device__ __forceinline__ void gated_grad_rows(const GatedArgs &a, const T *dH,
                 if (SUMS) {
                     sg[e] += g[e];
                     su[e] += u[e];
+                }
+            }
+            if (__is_same(T, __half)) {
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    g[e] *= scale;
+                    u[e] *= scale;
                 }
             }
             store_factor<T, V>(dG + r * pitch + f, a.rows * pitch, g);
@@ -197,23 +268,25 @@ __device__ __forceinline__ void gated_grad_rows(const GatedArgs &a, const T *dH,
 template <typename T, int READ, bool SUMS>
 __global__ void __launch_bounds__(kGradThreads, 3)
     gated_grad_kernel(GatedArgs a, const T *dH, const T *G, const T *U, Factor<T> *dG, Factor<T> *dU,
-                      int64_t pitch, float *partials, int team) {
+                      int64_t pitch, float *partials, int team, const uint32_t *bound) {
+    const float scale = __is_same(T, __half) ? gated_scale(__ldg(bound), false) : 1.0f;
     __shared__ float sums[SUMS ? 2 : 1][SUMS ? kGradWarps : 1][32 * kRowsV<T, READ>];
     with_act(a.act, [&](auto act) {
         gated_grad_rows<T, READ, SUMS, decltype(act)::value>(
-            a, dH, G, U, dG, dU, pitch, partials, team,
+            a, dH, G, U, dG, dU, pitch, partials, team, scale,
             reinterpret_cast<float(*)[kGradWarps][32 * kRowsV<T, READ>]>(sums));
     });
 }
 
 template <typename T, int READ>
 cudaError_t launch_gated_grad(const GatedArgs &a, const GatedPtrs &p, Factor<T> *dG, Factor<T> *dU,
-                              int64_t pitch, float *partials, cudaStream_t s) {
+                              int64_t pitch, float *partials, const uint32_t *bound,
+                              cudaStream_t s) {
     constexpr int V = kRowsV<T, READ>;
     const GradPlan plan = grad_plan(a.rows, a.F, V);
     const auto kernel = p.dbg ? gated_grad_kernel<T, READ, true> : gated_grad_kernel<T, READ, false>;
     kernel<<<dim3(plan.cols, plan.rows), kGradThreads, 0, s>>>(
-        a, (const T *)p.dH, (const T *)p.G, (const T *)p.U, dG, dU, pitch, partials, plan.team);
+        a, (const T *)p.dH, (const T *)p.G, (const T *)p.U, dG, dU, pitch, partials, plan.team, bound);
     return cudaGetLastError();
 }
 

@@ -50,7 +50,7 @@ __global__ void __launch_bounds__(256) gated_pad_kernel(PadArgs<T> p, int team) 
 template <typename T> struct GatedLayout {
     int64_t pitch_d, pitch_f;
     bool copy;
-    size_t X, Wg, Wu, dG, dU, partials, sums, bytes;
+    size_t X, Wg, Wu, dG, dU, partials, sums, bound, bytes;
     GatedLayout(const GatedArgs &a, bool backward) {
         bytes = 0;
         const auto take = [&](int64_t n) {
@@ -73,6 +73,7 @@ template <typename T> struct GatedLayout {
         const int bv = grad_plan(a.rows, a.F, kVec<T>).rows;
         partials = take((int64_t)(b1 > bv ? b1 : bv) * 2 * a.F * sizeof(float));
         sums = take(gt_backward_plan<T>(a).bytes());
+        bound = take(__is_same(T, __half) ? sizeof(uint32_t) : 0);
     }
 };
 
@@ -134,9 +135,14 @@ cudaError_t launch_gated_backward(const GatedArgs &a, const GatedPtrs &p, void *
     GtMatrix m[3];
     cudaError_t e = gated_operands(a, p, at, base, m, s);
     if (e != cudaSuccess) return e;
-    e = read == kRowsSingle ? launch_gated_grad<T, kRowsSingle>(a, p, dG, dU, at.pitch_f, partials, s)
-        : read == kRowsRuns ? launch_gated_grad<T, kRowsRuns>(a, p, dG, dU, at.pitch_f, partials, s)
-                            : launch_gated_grad<T, kRowsShifted>(a, p, dG, dU, at.pitch_f, partials, s);
+    uint32_t *bound = (uint32_t *)(base + at.bound);
+    if (__is_same(T, __half)) {
+        e = launch_gated_bound<T>(a, p, read != kRowsSingle, bound, s);
+        if (e != cudaSuccess) return e;
+    }
+    e = read == kRowsSingle ? launch_gated_grad<T, kRowsSingle>(a, p, dG, dU, at.pitch_f, partials, bound, s)
+        : read == kRowsRuns ? launch_gated_grad<T, kRowsRuns>(a, p, dG, dU, at.pitch_f, partials, bound, s)
+                            : launch_gated_grad<T, kRowsShifted>(a, p, dG, dU, at.pitch_f, partials, bound, s);
     if (e != cudaSuccess) return e;
     if (p.dbg) {
         const int blocks = grad_plan(a.rows, a.F, read == kRowsSingle ? 1 : kVec<T>).rows;
@@ -145,19 +151,19 @@ cudaError_t launch_gated_backward(const GatedArgs &a, const GatedPtrs &p, void *
     }
     bool used = false;
     e = launch_gt_backward<T>(a, p, m[0], m[1], m[2], {dG, a.rows, a.F, at.pitch_f},
-                              {dU, a.rows, a.F, at.pitch_f}, (float *)(base + at.sums), true, s,
-                              &used);
+                              {dU, a.rows, a.F, at.pitch_f}, bound, (float *)(base + at.sums),
+                              true, s, &used);
     if (e != cudaSuccess || used) return e;
     if constexpr (sizeof(T) == 2) {
         const auto product = [&](SimtProduct q, void *out) {
             return launch_next(true, gated_simt_product_kernel<T>,
                                dim3((unsigned)simt_blocks(q.M, q.N)), kSimtThreads, 0, s, q, (T *)out);
         };
-        e = product({{dG, dU}, {p.Wg, p.Wu}, at.pitch_f, 1, 1, a.D, a.rows, a.D, a.F, 2}, p.dX);
+        e = product({{dG, dU}, {p.Wg, p.Wu}, at.pitch_f, 1, 1, a.D, a.rows, a.D, a.F, 2, bound}, p.dX);
         if (e != cudaSuccess) return e;
-        e = product({{dG, dG}, {p.X, p.X}, 1, at.pitch_f, 1, a.D, a.F, a.D, a.rows, 1}, p.dWg);
+        e = product({{dG, dG}, {p.X, p.X}, 1, at.pitch_f, 1, a.D, a.F, a.D, a.rows, 1, bound}, p.dWg);
         if (e != cudaSuccess) return e;
-        return product({{dU, dU}, {p.X, p.X}, 1, at.pitch_f, 1, a.D, a.F, a.D, a.rows, 1}, p.dWu);
+        return product({{dU, dU}, {p.X, p.X}, 1, at.pitch_f, 1, a.D, a.F, a.D, a.rows, 1, bound}, p.dWu);
     }
     return cudaErrorInvalidValue;   // not reached: planes are 16-byte aligned
 }

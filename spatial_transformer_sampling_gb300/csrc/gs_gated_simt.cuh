@@ -2,7 +2,7 @@
 // alignment: 64 x 64 tiles, 4 x 4 values per thread.
 #pragma once
 
-#include "gs_gated.cuh"
+#include "gs_gated_grad.cuh"
 
 namespace gs {
 
@@ -82,6 +82,7 @@ struct SimtProduct {
     int64_t am, ak, bn, bk;
     int64_t M, N, K;
     int segments;
+    const uint32_t *bound;   // fp16: what A is scaled by
 };
 template <typename T>
 __global__ void __launch_bounds__(kSimtThreads) gated_simt_product_kernel(SimtProduct p, T *C) {
@@ -99,11 +100,12 @@ __global__ void __launch_bounds__(kSimtThreads) gated_simt_product_kernel(SimtPr
             simt_multiply(sa, sb, c);
         }
     const int64_t m = m0 + threadIdx.x / 16 * 4, n = n0 + threadIdx.x % 16 * 4;
+    const float f = __is_same(T, __half) ? gated_scale(__ldg(p.bound), true) : 1.0f;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            if (m + i < p.M && n + j < p.N) C[(m + i) * p.N + n + j] = IO<T>::st(c[i][j]);
+            if (m + i < p.M && n + j < p.N) C[(m + i) * p.N + n + j] = IO<T>::st(c[i][j] * f);
 }
 
 inline int64_t simt_blocks(int64_t M, int64_t N) {

@@ -37,7 +37,7 @@
 #pragma once
 
 #include "gs_attn_tc.cuh"
-#include "gs_gated.cuh"
+#include "gs_gated_grad.cuh"
 
 namespace gs {
 
@@ -250,6 +250,7 @@ struct GtArgs {
     const void *bg, *bu;
     int F;
     ActNumbers act;
+    const uint32_t *bound;        // backward in fp16: what dG and dU are scaled by
     unsigned *err;
 };
 
@@ -734,6 +735,13 @@ __global__ void __launch_bounds__(GtShape<T, MODE, NT>::kThreads, 1)
                     gt_store_boxes<T, kRow, Sh::kBoxes>(p.out, box, row0, f0 + i * 32, policy);
                 }
             } else {
+                if constexpr (__is_same(T, __half)) {   // dG and dU are scaled
+                    const float f = gated_scale(__ldg(p.bound), true);
+#pragma unroll
+                    for (int i = 0; i < kRuns; ++i)
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) v[i][c] *= f;
+                }
                 const int half = kind.tiles_m / 2, which = w.kind == kGtDw && w.m >= half;
                 const GtOutput *out = &p.out[w.kind == kGtDw ? 1 + which : 0];
                 const int64_t out_row = row0 - (int64_t)which * half * kGtTile;
@@ -991,8 +999,8 @@ cudaError_t launch_gt_forward(const GatedArgs &a, const GatedPtrs &q, const GtMa
 template <typename T>
 cudaError_t launch_gt_backward(const GatedArgs &a, const GatedPtrs &q, const GtMatrix &X,
                                const GtMatrix &Wg, const GtMatrix &Wu, const GtMatrix &dG,
-                               const GtMatrix &dU, float *sums, bool follows, cudaStream_t s,
-                               bool *used) {
+                               const GtMatrix &dU, const uint32_t *bound, float *sums, bool follows,
+                               cudaStream_t s, bool *used) {
     GtArgs p = {};
     GtKind &x = p.kind[kGtDx], &w = p.kind[kGtDw];
     *used = gt_maps<T>(x.a[0], dG, kGtHalf) && gt_maps<T>(x.a[1], dU, kGtHalf) &&
@@ -1004,6 +1012,7 @@ cudaError_t launch_gt_backward(const GatedArgs &a, const GatedPtrs &q, const GtM
     gt_output<T>(&p.out[1], q.dWg, a.F, a.D, 128);
     gt_output<T>(&p.out[2], q.dWu, a.F, a.D, 128);
     p.err = a.err;
+    p.bound = bound;
     x.tiles_m = (int)((a.rows + kGtTile - 1) / kGtTile);
     x.k_steps = (a.F + kGtK - 1) / kGtK;
     w.tiles_m = 2 * ((a.F + kGtTile - 1) / kGtTile);

@@ -207,3 +207,26 @@ def test_gradient_against_differences(gs_cuda, act):
             # central differences are off by step^2 times a third derivative (under 100 here);
             # the kernel's fp32 gradient by 1e-5 of sums that stay below 50
             assert abs((up - down) / (2 * step) - grad[i]) <= 1e-3, (name, i)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,D,F", [(3, 16, 24), (300, 64, 72), (150, 65, 67)])
+@pytest.mark.parametrize("size", [2.0 ** -20, 2.0 ** 9, 2.0 ** 14])
+def test_gradients_of_any_size(gs_cuda, size, rows, D, F, dtype):
+    """dH among the type's smallest and near its largest numbers: dG and dU are off by half a
+    step, not by a subnormal number's, and stay finite (the results themselves may not be)."""
+    t, dH = _make(rows, D, F, dtype, True, 11)
+    _, G, U = gs_cuda.gs_gated_linear(**t, keep=True)
+    d = (dH.float().clamp(-3, 3) * size).to(ref.DT[dtype])
+    small = {k: None if v is None else (v.float() * 2.0 ** -6).to(ref.DT[dtype]) for k, v in t.items()}
+    back = gs_cuda.gs_gated_linear_backward(d, small["X"], small["Wg"], small["Wu"], G, U, bias=True)
+    ref.check_gated_backward(back, d, small["X"], small["Wg"], small["Wu"], G, U, "silu", dtype)
+    zero = torch.zeros_like(dH)
+    for b in gs_cuda.gs_gated_linear_backward(zero, t["X"], t["Wg"], t["Wu"], G, U, bias=True):
+        assert not b.any()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,D,F", [(40, 33000, 24), (3, 40000, 17), (2, 263000, 8)])
+def test_wide_rows(gs_cuda, rows, D, F, dtype):
+    _both(gs_cuda, rows, D, F, dtype, "silu", True, 6)
