@@ -268,8 +268,9 @@ constexpr int resnorm_backward_blocks(int L, int N) {
 }
 
 // dX, dZ and, into partials[block][vector], the block's column sums (for dScale, dB
-// and, with POST, dz_scale and dz_B); into gate_partials[segment] those for the gate.
-// The next row's loads are issued before this one is worked on.
+// and, with POST, dz_scale and dz_B); into gate_partials[segment] those for the gate, or
+// [block] where all rows share one.  The next row's loads are issued before this one is
+// worked on.
 template <typename T, int V, int L, int NV, bool POST, bool GATE>
 __global__ void __launch_bounds__(res_block(L), resnorm_backward_blocks(L, NV * V))
     resnorm_backward_kernel(ResNormArgs a, ResNormPtrs p, ResNormPlan q, float *partials,
@@ -382,7 +383,7 @@ __global__ void __launch_bounds__(res_block(L), resnorm_backward_blocks(L, NV * 
                 if (row >= 0 && d < a.D) IOV::store((T *)p.dZ + row * a.D + d, out);
             }
         }
-        if (GATE && ends) {
+        if (GATE && ends && q.groups > 1) {
             if (segment < (int64_t)q.groups * q.chunks) {
 #pragma unroll
                 for (int k = 0; k < NV; ++k) {
@@ -402,34 +403,37 @@ __global__ void __launch_bounds__(res_block(L), resnorm_backward_blocks(L, NV * 
                 for (int e = 0; e < V; ++e) gate_sum[k][e] = 0.0f;
         }
     }
-    if (!partials) return;
     // the teams of the block in order, one vector and run at a time
-    float *out = partials + (int64_t)blockIdx.x * kVectors * a.D;
     __shared__ float join[kTeams > 1 ? kThreads * V : 1];
-#pragma unroll
-    for (int j = 0; j < kVectors; ++j)
+    const auto leave = [&](const float (&sums)[NV][V], float *out) {
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             if (kTeams > 1) {
                 __syncthreads();
 #pragma unroll
-                for (int e = 0; e < V; ++e) join[threadIdx.x * V + e] = sum[j][k][e];
+                for (int e = 0; e < V; ++e) join[threadIdx.x * V + e] = sums[k][e];
                 __syncthreads();
                 for (int c = threadIdx.x; c < L * V; c += kThreads) {
                     const int d = k * L * V + c;
                     float t = 0.0f;
 #pragma unroll
                     for (int g = 0; g < kTeams; ++g) t += join[g * L * V + c];
-                    if (d < a.D) out[(int64_t)j * a.D + d] = t;
+                    if (d < a.D) out[d] = t;
                 }
             } else {
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
                     const int d = (k * L + part) * V + e;
-                    if (d < a.D) out[(int64_t)j * a.D + d] = sum[j][k][e];
+                    if (d < a.D) out[d] = sums[k][e];
                 }
             }
         }
+    };
+    if (GATE && q.groups == 1) leave(gate_sum, gate_partials + (int64_t)blockIdx.x * a.D);
+    if (!partials) return;
+#pragma unroll
+    for (int j = 0; j < kVectors; ++j)
+        leave(sum[j], partials + ((int64_t)blockIdx.x * kVectors + j) * a.D);
 }
 
 // ------------------------------------------------------------------ backward, staged
@@ -645,6 +649,30 @@ __global__ void __launch_bounds__(kStagedThreads, 1)
         }
     };
 
+    // The gate's gradient from a segment's sums, whose share of dz_scale and dz_B is added to
+    // the totals.
+    const auto gate_sums = [&](float2 (&d)[P], int gate) {
+#pragma unroll
+        for (int i = 0; i < P; ++i) d[i] = seg[0][i];
+        if (POST) {
+            float2 g[P], c[P], b[P];
+            param(p.gate, g, (int64_t)gate * a.D);
+            param(p.z_scale, c);
+            if (p.z_B) param(p.z_B, b);
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                d[i] = mul_f32x2(seg[0][i], c[i]);
+                if (p.z_B) d[i] = fma_f32x2(seg[1][i], b[i], d[i]);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    float *t = totals + (j * N + 2 * i) * kStagedThreads;
+                    t[0] = fmaf(seg[j][i].x, g[i].x, t[0]);
+                    t[kStagedThreads] = fmaf(seg[j][i].y, g[i].y, t[kStagedThreads]);
+                }
+            }
+        }
+    };
+
     bool ok = true;
     int slot = 0, s = 0;
     uint32_t parity = 0;
@@ -726,28 +754,10 @@ __global__ void __launch_bounds__(kStagedThreads, 1)
                 put(p.dZ, at, out);
             }
         }
-        if (GATE && place.w) {
+        if (GATE && place.w && q.groups > 1) {
             if (place.z >= 0) {
                 float2 d[P];
-#pragma unroll
-                for (int i = 0; i < P; ++i) d[i] = seg[0][i];
-                if (POST) {
-                    float2 b[P];
-                    param(p.gate, g, (int64_t)place.y * a.D);
-                    param(p.z_scale, c);
-                    if (p.z_B) param(p.z_B, b);
-#pragma unroll
-                    for (int i = 0; i < P; ++i) {
-                        d[i] = mul_f32x2(seg[0][i], c[i]);
-                        if (p.z_B) d[i] = fma_f32x2(seg[1][i], b[i], d[i]);
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            float *t = totals + (j * N + 2 * i) * kStagedThreads;
-                            t[0] = fmaf(seg[j][i].x, g[i].x, t[0]);
-                            t[kStagedThreads] = fmaf(seg[j][i].y, g[i].y, t[kStagedThreads]);
-                        }
-                    }
-                }
+                gate_sums(d, place.y);
                 if (q.chunks == 1) {
                     put(p.dgate, (int64_t)place.z * a.D, d);
                 } else {
@@ -770,25 +780,16 @@ __global__ void __launch_bounds__(kStagedThreads, 1)
     if (!ok && part == 0)
         for (int n = steps > stages ? steps - stages : 0; n < steps; ++n)
             mbar_wait_bounded(&full[team][n % stages], (n / stages) & 1, a.err);
-    if (!partials) return;
     // the teams of the block in order, one vector at a time, by way of the ring
-    float *out = partials + (int64_t)blockIdx.x * kVectors * a.D;
     float *join = reinterpret_cast<float *>(ring) + kTotals;
-#pragma unroll
-    for (int j = 0; j < kVectors; ++j) {
-        float x[N];
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-            x[i] = j < 2 ? element(sum[j % 2], i)
-                   : kTotals ? totals[((j % 2) * N + i) * kStagedThreads]
-                             : element(seg[j % 2], i);
+    const auto leave = [&](const float (&x)[N], float *out) {
         if (kTeams == 1) {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 const int d = (i / V * L + part) * V + i % V;
-                if (d < a.D) out[(int64_t)j * a.D + d] = x[i];
+                if (d < a.D) out[d] = x[i];
             }
-            continue;
+            return;
         }
         __syncthreads();
 #pragma unroll
@@ -799,8 +800,26 @@ __global__ void __launch_bounds__(kStagedThreads, 1)
             float t = 0.0f;
 #pragma unroll
             for (int g = 0; g < kTeams; ++g) t += join[g * N * L + c];
-            if (d < a.D) out[(int64_t)j * a.D + d] = t;
+            if (d < a.D) out[d] = t;
         }
+    };
+    float x[N];
+    if (GATE && q.groups == 1) {   // one segment of all the team's rows
+        float2 d[P];
+        gate_sums(d, 0);
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[i] = element(d, i);
+        leave(x, gate_partials + (int64_t)blockIdx.x * a.D);
+    }
+    if (!partials) return;
+#pragma unroll
+    for (int j = 0; j < kVectors; ++j) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            x[i] = j < 2 ? element(sum[j % 2], i)
+                   : kTotals ? totals[((j % 2) * N + i) * kStagedThreads]
+                             : element(seg[j % 2], i);
+        leave(x, partials + ((int64_t)blockIdx.x * kVectors + j) * a.D);
     }
 }
 
@@ -971,9 +990,12 @@ struct ResNormLayout {
     ResNormLayout(const ResNormArgs &a, const ResNormPlan &q) {
         const auto up = [](size_t n) { return (n + 255) & ~(size_t)255; };
         gate = up((size_t)q.blocks * 4 * a.D * sizeof(float));
-        means = gate + (a.groups > 0 && q.chunks > 1
-                            ? up((size_t)q.groups * q.chunks * a.D * sizeof(float))
-                            : 0);
+        // one gate: a row of sums per block, but per chunk for rows wider than kResOnChip
+        const size_t sums = a.groups == 0                        ? 0
+                            : a.groups == 1 && a.D <= kResOnChip ? q.blocks
+                            : q.chunks > 1                       ? (size_t)q.groups * q.chunks
+                                                                 : 0;
+        means = gate + up(sums * a.D * sizeof(float));
         bytes = means + (a.D > kResOnChip ? up((size_t)a.rows * sizeof(float2)) : 0);
     }
 };
@@ -1085,11 +1107,12 @@ cudaError_t launch_resnorm_backward(const ResNormArgs &a, const ResNormPtrs &p, 
         }
         if (e != cudaSuccess) return e;
         sum.from = partials;
-        if (a.groups > 0 && q.chunks > 1) {
+        const bool by_block = a.groups == 1 && !wide;
+        if (by_block || (a.groups > 0 && q.chunks > 1)) {
             sum.group_from = gates;
             sum.group_to = p.dgate;
             sum.groups = a.groups;
-            sum.group_count = q.chunks;
+            sum.group_count = by_block ? q.blocks : q.chunks;
         }
     }
     // without rows the sums are zeros
