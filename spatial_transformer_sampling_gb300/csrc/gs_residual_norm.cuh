@@ -94,74 +94,90 @@ __global__ void __launch_bounds__(res_block(L)) resnorm_kernel(ResNormArgs a, Re
         }
     }
     int slot = 0;
-    // v minus its mean, and the mean and reciprocal deviation
-    const auto normalise = [&](float (&v)[NV][V], float &mean, float &inv) {
-        mean = 0.0f;
-        if (a.layer) {
-            float s = 0.0f;
-#pragma unroll
-            for (int k = 0; k < NV; ++k)
-#pragma unroll
-                for (int e = 0; e < V; ++e) s += v[k][e];
-            mean = team_sum<L>(s, slot) * per_d;
-        }
-        float s = 0.0f;
+    constexpr int N = NV * V, P = (N + 1) / 2;   // a thread's elements, in pairs
+    const auto both = [](float x) { return make_float2(x, x); };
+    const auto inside = [&](int i) { return (i / V * L + part) * V < a.D; };   // element i
+    const auto pairs_of = [](const typename IOV::Raw (&raw)[NV], float2 (&v)[P]) {
+        float f[2 * P] = {};
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const float m = (k * L + part) * V < a.D ? mean : 0.0f;
+            float x[V];
+            IOV::widen(raw[k], x);
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                v[k][e] -= m;
-                s = fmaf(v[k][e], v[k][e], s);
-            }
+            for (int e = 0; e < V; ++e) f[k * V + e] = x[e];
         }
-        inv = 1.0f / sqrtf(fmaf(team_sum<L>(s, slot), per_d, a.eps));
+#pragma unroll
+        for (int i = 0; i < P; ++i) v[i] = make_float2(f[2 * i], f[2 * i + 1]);
+    };
+    const auto param = [&](const void *base, float2 (&v)[P]) {   // of the row's columns
+        typename IOV::Raw raw[NV];
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int d = (k * L + part) * V;
+            raw[k] = base && d < a.D ? IOV::load((const T *)base + d) : IOV::zero();
+        }
+        pairs_of(raw, v);
+    };
+    const auto put = [&](void *base, int64_t row, const float2 (&v)[P]) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int d = (k * L + part) * V;
+            float x[V];
+#pragma unroll
+            for (int e = 0; e < V; ++e) x[e] = (k * V + e) % 2 ? v[(k * V + e) / 2].y : v[(k * V + e) / 2].x;
+            if (row < a.rows && d < a.D) IOV::store((T *)base + row * a.D + d, x);
+        }
+    };
+    // v minus its mean, and the mean and reciprocal deviation; zeros behind a row's end
+    // stay zeros
+    const auto normalise = [&](float2 (&v)[P], float &mean, float &inv) {
+        mean = 0.0f;
+        if (a.layer) {
+            float2 t = both(0.0f);
+#pragma unroll
+            for (int i = 0; i < P; ++i) t = add_f32x2(t, v[i]);
+            mean = team_sum<L>(t.x + t.y, slot) * per_d;
+#pragma unroll
+            for (int i = 0; i < P; ++i)
+                v[i] = add_f32x2(v[i], make_float2(inside(2 * i) ? -mean : 0.0f,
+                                                   2 * i + 1 < N && inside(2 * i + 1) ? -mean : 0.0f));
+        }
+        float2 t = both(0.0f);
+#pragma unroll
+        for (int i = 0; i < P; ++i) t = fma_f32x2(v[i], v[i], t);
+        inv = 1.0f / sqrtf(fmaf(team_sum<L>(t.x + t.y, slot), per_d, a.eps));
     };
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         const int64_t row = row0 + r;
-        float v[NV][V];
+        float2 v[P], x[P], w[P], b[P];
         float4 stats = make_float4(0.0f, 1.0f, 0.0f, 1.0f);
+        pairs_of(rz[r], v);
+        if (POST) {
+            normalise(v, stats.x, stats.y);
+            param(p.z_scale, w);
+            param(p.z_B, b);
 #pragma unroll
-        for (int k = 0; k < NV; ++k) IOV::widen(rz[r][k], v[k]);
-        if (POST) normalise(v, stats.x, stats.y);
-#pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int d = (k * L + part) * V;
-            const bool on = d < a.D;
-            if (POST) {
-                float w[V], b[V] = {};
-                IOV::widen(on ? IOV::load((const T *)p.z_scale + d) : IOV::zero(), w);
-                if (p.z_B) IOV::widen(on ? IOV::load((const T *)p.z_B + d) : IOV::zero(), b);
-#pragma unroll
-                for (int e = 0; e < V; ++e) v[k][e] = on ? fmaf(v[k][e] * stats.y, w[e], b[e]) : 0.0f;
-            }
-            float x[V], g[V];
-            IOV::widen(rx[r][k], x);
-            if (a.groups > 0) {
-                IOV::widen(rg[r][k], g);
-#pragma unroll
-                for (int e = 0; e < V; ++e) v[k][e] = fmaf(g[e], v[k][e], a.alpha * x[e]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < V; ++e) v[k][e] = fmaf(a.alpha, x[e], v[k][e]);
-            }
-            if (row < a.rows && on) IOV::store((T *)p.S + row * a.D + d, v[k]);
+            for (int i = 0; i < P; ++i) v[i] = fma_f32x2(mul_f32x2(v[i], both(stats.y)), w[i], b[i]);
         }
+        pairs_of(rx[r], x);
+        if (a.groups > 0) {
+            float2 g[P];
+            pairs_of(rg[r], g);
+#pragma unroll
+            for (int i = 0; i < P; ++i) v[i] = fma_f32x2(g[i], v[i], mul_f32x2(x[i], both(a.alpha)));
+        } else {
+#pragma unroll
+            for (int i = 0; i < P; ++i) v[i] = fma_f32x2(x[i], both(a.alpha), v[i]);
+        }
+        put(p.S, row, v);
         normalise(v, stats.z, stats.w);
-        if (row >= a.rows) continue;
+        param(p.scale, w);
+        param(p.B, b);
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int d = (k * L + part) * V;
-            if (d >= a.D) continue;
-            float w[V], b[V] = {}, y[V];
-            IOV::widen(IOV::load((const T *)p.scale + d), w);
-            if (p.B) IOV::widen(IOV::load((const T *)p.B + d), b);
-#pragma unroll
-            for (int e = 0; e < V; ++e) y[e] = fmaf(v[k][e] * stats.w, w[e], b[e]);
-            IOV::store((T *)p.Y + row * a.D + d, y);
-        }
-        if (part == 0 && p.stats) *reinterpret_cast<float4 *>(p.stats + 4 * row) = stats;
+        for (int i = 0; i < P; ++i) v[i] = fma_f32x2(mul_f32x2(v[i], both(stats.w)), w[i], b[i]);
+        put(p.Y, row, v);
+        if (row < a.rows && part == 0 && p.stats) *reinterpret_cast<float4 *>(p.stats + 4 * row) = stats;
     }
 }
 
