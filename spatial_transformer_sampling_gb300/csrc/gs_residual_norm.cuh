@@ -71,27 +71,23 @@ template <int L> __device__ __forceinline__ float team_sum(float a, int &slot) {
     return a;
 }
 
-// R rows per team of L threads, loads of all of them first.
-template <typename T, int V, int L, int NV, int R, bool POST>
+// A row per team of L threads.
+template <typename T, int V, int L, int NV, bool POST>
 __global__ void __launch_bounds__(res_block(L)) resnorm_kernel(ResNormArgs a, ResNormPtrs p) {
     using IOV = Run<T, V>;
     constexpr int kTeams = res_block(L) / L;
     const int part = threadIdx.x % L;
-    const int64_t row0 = ((int64_t)blockIdx.x * kTeams + threadIdx.x / L) * R;
+    const int64_t row = (int64_t)blockIdx.x * kTeams + threadIdx.x / L;
     const float per_d = 1.0f / (float)a.D;
-    typename IOV::Raw rx[R][NV], rz[R][NV], rg[R][NV];
+    typename IOV::Raw rx[NV], rz[NV], rg[NV];
+    const int64_t gate = a.groups > 0 && row < a.rows ? row / a.group_rows * a.D : 0;
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-        const int64_t row = row0 + r;
-        const int64_t gate = a.groups > 0 && row < a.rows ? row / a.group_rows * a.D : 0;
-#pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int d = (k * L + part) * V;
-            const bool on = row < a.rows && d < a.D;
-            rx[r][k] = on ? IOV::load((const T *)p.X + row * a.D + d) : IOV::zero();
-            rz[r][k] = on ? IOV::load((const T *)p.Z + row * a.D + d) : IOV::zero();
-            if (a.groups > 0) rg[r][k] = on ? IOV::load((const T *)p.gate + gate + d) : IOV::zero();
-        }
+    for (int k = 0; k < NV; ++k) {
+        const int d = (k * L + part) * V;
+        const bool on = row < a.rows && d < a.D;
+        rx[k] = on ? IOV::load((const T *)p.X + row * a.D + d) : IOV::zero();
+        rz[k] = on ? IOV::load((const T *)p.Z + row * a.D + d) : IOV::zero();
+        if (a.groups > 0) rg[k] = on ? IOV::load((const T *)p.gate + gate + d) : IOV::zero();
     }
     int slot = 0;
     constexpr int N = NV * V, P = (N + 1) / 2;   // a thread's elements, in pairs
@@ -109,16 +105,41 @@ __global__ void __launch_bounds__(res_block(L)) resnorm_kernel(ResNormArgs a, Re
 #pragma unroll
         for (int i = 0; i < P; ++i) v[i] = make_float2(f[2 * i], f[2 * i + 1]);
     };
-    const auto param = [&](const void *base, float2 (&v)[P]) {   // of the row's columns
-        typename IOV::Raw raw[NV];
-#pragma unroll
-        for (int k = 0; k < NV; ++k) {
+    // f(i, w, b) for each pair i of the row's columns with two vectors' elements (zeros of
+    // none).  All loads first, but a run at a time in blocks whose threads hold eight:
+    // there they do not fit the registers (2048 x 8192 fp32 67 us, and 47 by runs; 32768 x
+    // 1024 bf16, a warp per row, 58 us and 96).
+    const auto with_params = [&](const void *wp, const void *bp, auto &&f) {
+        const auto load = [&](const void *base, int k) {
             const int d = (k * L + part) * V;
-            raw[k] = base && d < a.D ? IOV::load((const T *)base + d) : IOV::zero();
+            return base && d < a.D ? IOV::load((const T *)base + d) : IOV::zero();
+        };
+        if constexpr (L == 256 && NV == 8 && V > 1) {
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                float w[V], b[V] = {};
+                IOV::widen(load(wp, k), w);
+                if (bp) IOV::widen(load(bp, k), b);   // a branch, which loads do not move across
+#pragma unroll
+                for (int h = 0; h < V / 2; ++h)
+                    f(k * (V / 2) + h, make_float2(w[2 * h], w[2 * h + 1]),
+                      make_float2(b[2 * h], b[2 * h + 1]));
+            }
+        } else {
+            typename IOV::Raw rw[NV], rb[NV];
+            float2 w[P], b[P];
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                rw[k] = load(wp, k);
+                rb[k] = load(bp, k);
+            }
+            pairs_of(rw, w);
+            pairs_of(rb, b);
+#pragma unroll
+            for (int i = 0; i < P; ++i) f(i, w[i], b[i]);
         }
-        pairs_of(raw, v);
     };
-    const auto put = [&](void *base, int64_t row, const float2 (&v)[P]) {
+    const auto put = [&](void *base, const float2 (&v)[P]) {
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int d = (k * L + part) * V;
@@ -147,38 +168,32 @@ __global__ void __launch_bounds__(res_block(L)) resnorm_kernel(ResNormArgs a, Re
         for (int i = 0; i < P; ++i) t = fma_f32x2(v[i], v[i], t);
         inv = 1.0f / sqrtf(fmaf(team_sum<L>(t.x + t.y, slot), per_d, a.eps));
     };
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        const int64_t row = row0 + r;
-        float2 v[P], x[P], w[P], b[P];
-        float4 stats = make_float4(0.0f, 1.0f, 0.0f, 1.0f);
-        pairs_of(rz[r], v);
-        if (POST) {
-            normalise(v, stats.x, stats.y);
-            param(p.z_scale, w);
-            param(p.z_B, b);
-#pragma unroll
-            for (int i = 0; i < P; ++i) v[i] = fma_f32x2(mul_f32x2(v[i], both(stats.y)), w[i], b[i]);
-        }
-        pairs_of(rx[r], x);
-        if (a.groups > 0) {
-            float2 g[P];
-            pairs_of(rg[r], g);
-#pragma unroll
-            for (int i = 0; i < P; ++i) v[i] = fma_f32x2(g[i], v[i], mul_f32x2(x[i], both(a.alpha)));
-        } else {
-#pragma unroll
-            for (int i = 0; i < P; ++i) v[i] = fma_f32x2(x[i], both(a.alpha), v[i]);
-        }
-        put(p.S, row, v);
-        normalise(v, stats.z, stats.w);
-        param(p.scale, w);
-        param(p.B, b);
-#pragma unroll
-        for (int i = 0; i < P; ++i) v[i] = fma_f32x2(mul_f32x2(v[i], both(stats.w)), w[i], b[i]);
-        put(p.Y, row, v);
-        if (row < a.rows && part == 0 && p.stats) *reinterpret_cast<float4 *>(p.stats + 4 * row) = stats;
+    float2 v[P], x[P];
+    float4 stats = make_float4(0.0f, 1.0f, 0.0f, 1.0f);
+    pairs_of(rz, v);
+    if (POST) {
+        normalise(v, stats.x, stats.y);
+        with_params(p.z_scale, p.z_B, [&](int i, float2 w, float2 b) {
+            v[i] = fma_f32x2(mul_f32x2(v[i], both(stats.y)), w, b);
+        });
     }
+    pairs_of(rx, x);
+    if (a.groups > 0) {
+        float2 g[P];
+        pairs_of(rg, g);
+#pragma unroll
+        for (int i = 0; i < P; ++i) v[i] = fma_f32x2(g[i], v[i], mul_f32x2(x[i], both(a.alpha)));
+    } else {
+#pragma unroll
+        for (int i = 0; i < P; ++i) v[i] = fma_f32x2(x[i], both(a.alpha), v[i]);
+    }
+    put(p.S, v);
+    normalise(v, stats.z, stats.w);
+    with_params(p.scale, p.B, [&](int i, float2 w, float2 b) {
+        v[i] = fma_f32x2(mul_f32x2(v[i], both(stats.w)), w, b);
+    });
+    put(p.Y, v);
+    if (row < a.rows && part == 0 && p.stats) *reinterpret_cast<float4 *>(p.stats + 4 * row) = stats;
 }
 
 // Rows wider than kResOnChip: a block per row that reads it again for each sum.
@@ -1031,10 +1046,10 @@ template <typename T, int V>
 cudaError_t run_resnorm(const ResNormArgs &a, const ResNormPtrs &p, cudaStream_t s) {
     return resnorm_shape<V>((a.D + V - 1) / V, [&](auto l, auto nv) {
         constexpr int L = decltype(l)::value, NV = decltype(nv)::value;
-        constexpr int R = L == 256 || NV > 1 ? 1 : 2;
-        constexpr int kRows = res_block(L) / L * R;
-        const auto kernel = p.z_scale ? resnorm_kernel<T, V, L, NV, R, true>
-                                      : resnorm_kernel<T, V, L, NV, R, false>;
+        // (two rows per team 69.5 us for 524288 x 64 bf16, one 63)
+        constexpr int kRows = res_block(L) / L;
+        const auto kernel = p.z_scale ? resnorm_kernel<T, V, L, NV, true>
+                                      : resnorm_kernel<T, V, L, NV, false>;
         kernel<<<(unsigned)((a.rows + kRows - 1) / kRows), res_block(L), 0, s>>>(a, p);
         return cudaGetLastError();
     });
