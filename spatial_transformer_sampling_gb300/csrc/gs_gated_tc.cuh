@@ -14,15 +14,20 @@
 //   dW       A = dG or dU, M-major; B = X, N-major; the contraction runs over rows.
 //
 // The tiles of dX and of dWg, dWu are worked on in one launch, the longer contraction
-// first and the others where a pair is free: 16384 x 1024 x 4096 needs 3.4 and 1.7 tiles
-// per pair, 6 of one length in turn and 5.1 together.
+// first and the others where a pair is free (16384 x 1024 x 4096 bf16: 285 us, and 322 in
+// two launches of 3.4 and 1.7 tiles per pair).
+//
+// Bound by the tensor pipe from a contraction of 512 on: forward 16384 x 1024 x 4096
+// bf16 in 140 us, 1.96 PFLOP/s, and 173 us with G and U kept, whose 268 MB are written
+// meanwhile; backward 285 us, 1.93 PFLOP/s.  Short contractions are bound by the writes:
+// 262144 x 64 x 256, kept, 403 MB in 87 us (a fill of that size takes 108).
 //
 // Both operands are read where they lie: K-major or MN-major is a bit of the
 // instruction, nothing is transposed in memory.
 //
 // Where there are few tiles, a long contraction is shared out: each part's fp32 sums go
-// to the workspace and a second kernel adds them in order (262144 rows, D = F = 64:
-// TBD us and TBD).
+// to the workspace and a second kernel adds them in order (262144 rows, D = F = 64
+// fp16: 111 us, and a millisecond by the two pairs that dWg and dWu have tiles for).
 //
 // fp32 operands come as three bf16 planes, x = x0 + x1 + x2 to 2^-24 of x or better,
 // and a product is the sum of six of theirs, the small ones first: x2 y0, x0 y2, x1 y1,
@@ -56,8 +61,8 @@ enum { kGtDx = 0, kGtDw = 1 };   // kinds of a backward tile
 // T: type of the outputs.  An epilogue warp has 32 rows and kCols columns of a tile
 // (forward: as many of G as of U), which it stages for its stores in boxes of 32 rows:
 // sixteen warps of 64 columns in 16-bit types, where what waits for TMEM, the staging
-// and the stores is hidden by the other warps (eight warps of 128: 157 us and not TBD for
-// 262144 x 64 x 256, kept); eight warps of 128 in fp32, whose sums stay in registers.
+// and the stores is hidden by the other warps (eight warps of 128: 157 us and not 94
+// for 262144 x 64 x 256, kept); eight warps of 128 in fp32, whose sums stay in registers.
 template <typename T, int MODE, int NT> struct GtShape {
     static constexpr bool kForward = MODE == kGtForward || MODE == kGtForwardKeep;
     static constexpr int kPlanes = sizeof(T) == 4 ? 3 : 1;
@@ -747,16 +752,16 @@ __global__ void __launch_bounds__(GtShape<T, MODE, NT>::kThreads, 1)
                 const int64_t out_row = row0 - (int64_t)which * half * kGtTile;
                 const int col0 = w.n * NT + part * Sh::kCols;
                 if (kind.parts > 1) {   // this part's sums, for the kernel that adds them
-                    if (out_row + lane >= out->rows) continue;
                     float *to = kind.sums + w.part * kind.part_stride +
                                 (which * out->rows + out_row + lane) * kind.pitch + col0;
 #pragma unroll
-                    for (int i = 0; i < kRuns; ++i)
-                        if (col0 + i * 32 < kind.pitch)   // a multiple of 32
+                    for (int i = 0; i < kRuns; ++i)   // the pitch is a multiple of 32
+                        if (out_row + lane < out->rows && col0 + i * 32 < kind.pitch)
 #pragma unroll
                             for (int c = 0; c < 32; c += 4)
                                 *reinterpret_cast<float4 *>(to + i * 32 + c) =
                                     make_float4(v[i][c], v[i][c + 1], v[i][c + 2], v[i][c + 3]);
+                    __syncwarp();
                     continue;
                 }
                 // two runs at a time: a box of both, or one each

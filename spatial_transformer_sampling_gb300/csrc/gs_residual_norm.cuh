@@ -80,7 +80,8 @@ __global__ void __launch_bounds__(res_block(L)) resnorm_kernel(ResNormArgs a, Re
     const int64_t row = (int64_t)blockIdx.x * kTeams + threadIdx.x / L;
     const float per_d = 1.0f / (float)a.D;
     typename IOV::Raw rx[NV], rz[NV], rg[NV];
-    const int64_t gate = a.groups > 0 && row < a.rows ? row / a.group_rows * a.D : 0;
+    const int64_t gate =
+        a.groups > 1 && row < a.rows ? (int64_t)((uint32_t)row / (uint32_t)a.group_rows) * a.D : 0;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
         const int d = (k * L + part) * V;
