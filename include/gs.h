@@ -650,12 +650,24 @@ gs_status gs_gated_linear_backward_workspace_size(int64_t rows, int64_t D, int64
  *   workspace device, 256-byte aligned (GS_ERR_ALIGN), at least the size
  *             gs_gated_linear_workspace_size reports (GS_ERR_NULL for none,
  *             GS_ERR_SHAPE for less).
+ *             Calls that may run at the same time, replays of captured graphs among
+ *             them, need one each; calls in order on a stream may share one.
  *   H         device output, (rows, F).
  *   G, U      device outputs, (rows, F), both or neither: what the backward pass
  *             takes.
  *
  * The sums over D are fp32; G, U and H are each rounded once, at the store, and H
- * is formed of the unrounded G and U.
+ * is formed of the unrounded G and U.  Up to 32 rows need no workspace (rows of more
+ * than 2^18 16-bit elements aside).
+ *
+ * fp32, more than 32 rows: each factor is taken as three bf16 numbers, and six of their
+ * products are summed in fp32; that keeps fp32's precision, but of a factor below about
+ * 2^-110 the lowest bits are lost, and a factor that is infinite, or two whose product
+ * leaves fp32's range, may give NaN where a plain sum gives an infinity.
+ * The activations take hardware approximations of the exponential and the reciprocal
+ * (2 ulps each); where 1 / (1 + e^-g) is below 2^-126 it counts as 0.
+ * More than 32 rows of a 16-bit type run on plain FMAs, 7 to 50 times slower, where
+ * D > 32768, or where D is a multiple of 8 and X, Wg or Wu starts on no 16-byte boundary.
  */
 gs_status gs_gated_linear(const void *X, const void *Wg, const void *Wu, const void *bg,
                           const void *bu, int64_t rows, int64_t D, int64_t F, gs_activation act,
@@ -674,8 +686,12 @@ gs_status gs_gated_linear(const void *X, const void *Wg, const void *Wu, const v
  * dG = dH * U * act'(G), dU = dH * act(G); dX = dG Wg + dU Wu; dWg = dG^T X,
  * dWu = dU^T X; dbg and dbu are the sums of dG and dU over the rows.  relu's slope
  * at 0 is 0.  In 16-bit types dG and dU are rounded to the type as factors of the
- * products (half a step on every term); the biases' sums take them unrounded.  With
- * rows = 0 the gradients of the weights and biases are zeros.
+ * products (half a step on every term); the biases' sums take them unrounded.  In
+ * fp16 they are scaled by a power of two before that rounding, from the largest
+ * |dH| max(1.13 |U|, |G|) of the call, and the products are scaled back: neither a
+ * scaled loss nor a small one leaves the type's range; elements below 2^-39 of that
+ * bound count as 0.  With rows = 0 the gradients of the
+ * weights and biases are zeros.
  */
 gs_status gs_gated_linear_backward(const void *dH, const void *X, const void *Wg, const void *Wu,
                                    const void *G, const void *U, int64_t rows, int64_t D,

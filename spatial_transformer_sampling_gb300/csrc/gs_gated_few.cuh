@@ -18,6 +18,9 @@ constexpr int kFewMost = 32;   // rows of a block
 // Widest rows in 16-bit types: the matrix instruction cuts its sums off as the larger
 // tensor cores do, and a warp's run of them is not broken up.
 constexpr int kFewWidth = 262144;
+template <typename T> bool gated_few_takes(const GatedArgs &a) {
+    return a.rows <= kFewMost && (sizeof(T) == 4 || a.D <= kFewWidth);
+}
 
 template <typename T>
 __device__ __forceinline__ void few_mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,

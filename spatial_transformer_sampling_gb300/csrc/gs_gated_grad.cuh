@@ -125,14 +125,6 @@ __device__ __forceinline__ void store_factor(Factor<T> *to, int64_t plane, const
     }
 }
 
-inline int gated_grad_col_blocks(int F, int V) { return (F + 32 * V - 1) / (32 * V); }
-// Row blocks: about four blocks of 256 threads per SM.
-inline int gated_grad_row_blocks(int64_t rows, int F, int V) {
-    const int cols = gated_grad_col_blocks(F, V);
-    const int64_t most = (4 * kGatedSms + cols - 1) / cols, need = (rows + kGradWarps - 1) / kGradWarps;
-    return (int)(need < most ? need : most);
-}
-
 // In fp16 dG and dU are scaled by a power of two, so that as factors of the products they
 // neither leave the type's range nor fall among its subnormal numbers: 2^14 over the
 // power of two below `bound`, the largest |dH| max(1.13 |U|, |G|) of the call (no

@@ -78,7 +78,8 @@ template <typename T> struct GatedLayout {
 };
 
 template <typename T> size_t gated_ws_bytes(const GatedArgs &a, bool backward) {
-    return a.rows == 0 || a.F == 0 ? 0 : GatedLayout<T>(a, backward).bytes;
+    if (a.rows == 0 || a.F == 0 || (!backward && gated_few_takes<T>(a))) return 0;
+    return GatedLayout<T>(a, backward).bytes;
 }
 
 // X, Wg and Wu as TMA reads them: where they lie, or copied.
@@ -110,7 +111,7 @@ cudaError_t gated_operands(const GatedArgs &a, const GatedPtrs &p, const GatedLa
 
 template <typename T>
 cudaError_t launch_gated(const GatedArgs &a, const GatedPtrs &p, void *ws, cudaStream_t s) {
-    if (a.rows <= kFewMost && (sizeof(T) == 4 || a.D <= kFewWidth)) return launch_gated_few<T>(a, p, s);
+    if (gated_few_takes<T>(a)) return launch_gated_few<T>(a, p, s);
     GtMatrix m[3];
     const GatedLayout<T> at(a, false);
     bool used = false;

@@ -66,6 +66,12 @@ def test_gated_linear_workspace_queries(L):
         for dt in range(3):
             for rows in (1, 77, 5000):
                 assert _bytes(f, rows, 33, 50, dt) % 256 == 0
+    # few rows are multiplied where they lie; rows too long for that are not
+    for dt in range(3):
+        assert _bytes(L.gs_gated_linear_workspace_size, 32, 33, 50, dt) == 0
+        assert _bytes(L.gs_gated_linear_workspace_size, 33, 33, 50, dt) > 0
+    assert _bytes(L.gs_gated_linear_workspace_size, 32, 262144 + 1, 50, 0) == 0
+    assert _bytes(L.gs_gated_linear_workspace_size, 32, 262144 + 1, 50, 1) > 0
     # dG and dU at least
     assert _bytes(L.gs_gated_linear_backward_workspace_size, 1000, 64, 128, 1) >= 2 * 1000 * 128 * 2
 
