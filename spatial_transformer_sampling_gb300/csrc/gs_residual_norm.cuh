@@ -10,8 +10,8 @@
 //   dgate = sum ds z' over the rows that share it.
 //
 // Both read their inputs once: a row stays in the registers of the L threads that
-// share it, NV runs of V elements each, up to D = 8192; longer rows are read again
-// for each pass.  Backward, each team of L threads walks segments: rows that share a
+// share it, NV runs of V elements each, up to D = 8192 (backward up to 4096, and to 8192
+// with two sums); longer rows are read again for each pass.  Backward, each team of L threads walks segments: rows that share a
 // gate, or every chunks-th of them.  A thread keeps the sums of its columns over all
 // its rows, and those for the gate over a segment; a second kernel adds the teams'
 // sums in order.
@@ -24,9 +24,9 @@
 namespace gs {
 
 constexpr int kResThreads = 256;       // of a block, at least
-constexpr int kResOnChip = 8192;       // widest row held in registers
+constexpr int kResOnChip = 8192;       // widest row held in registers, forward
+constexpr int kResStaged = 4096;       // widest row that is staged, backward
 constexpr int kResSms = 152;
-constexpr int kResWideBlocks = 2;      // of the column sums of wider rows, per SM
 
 constexpr int res_block(int L) { return L > kResThreads ? L : kResThreads; }
 
@@ -71,7 +71,9 @@ template <int L> __device__ __forceinline__ float team_sum(float a, int &slot) {
     return a;
 }
 
-// A row per team of L threads.
+// A row per team of L threads.  Bound by memory where rows are runs (1,048,576 x 64 fp32,
+// 1.07 GB, 155 us: 1.03 of a copy's rate; 2048 x 8192 bf16 34 us, 3.9 TB/s), by the single
+// elements' instructions elsewhere (21760 x 771 bf16 62 us, 2.1 TB/s; fp32 60, 4.4).
 template <typename T, int V, int L, int NV, bool POST>
 __global__ void __launch_bounds__(res_block(L)) resnorm_kernel(ResNormArgs a, ResNormPtrs p) {
     using IOV = Run<T, V>;
@@ -198,42 +200,71 @@ __global__ void __launch_bounds__(res_block(L)) resnorm_kernel(ResNormArgs a, Re
 }
 
 // Rows wider than kResOnChip: a block per row that reads it again for each sum.
-template <typename T>
-__global__ void __launch_bounds__(kResThreads) resnorm_wide_kernel(ResNormArgs a, ResNormPtrs p) {
+template <typename T, int V, int L>
+__global__ void __launch_bounds__(L) resnorm_wide_kernel(ResNormArgs a, ResNormPtrs p) {
+    using IOV = Run<T, V>;
     const int64_t row = blockIdx.x, at = row * a.D;
-    const T *x = (const T *)p.X + at, *z = (const T *)p.Z + at;
-    const T *gate = a.groups > 0 ? (const T *)p.gate + row / a.group_rows * a.D : nullptr;
+    const int64_t gate = a.groups > 1 ? row / a.group_rows * a.D : 0;
     const float per_d = 1.0f / (float)a.D;
     int slot = 0;
+    const auto get = [](const void *base, int64_t i, float (&v)[V]) {
+        IOV::widen(base ? IOV::load((const T *)base + i) : IOV::zero(), v);
+    };
     const auto statistics = [&](auto value, float &mean, float &inv) {
-        float s = 0.0f;
+        float s = 0.0f, v[V];
         mean = 0.0f;
         if (a.layer) {
-            for (int d = threadIdx.x; d < a.D; d += kResThreads) s += value(d);
-            mean = team_sum<kResThreads>(s, slot) * per_d;
+#pragma unroll 4
+            for (int d = threadIdx.x * V; d < a.D; d += L * V) {
+                value(d, v);
+#pragma unroll
+                for (int e = 0; e < V; ++e) s += v[e];
+            }
+            mean = team_sum<L>(s, slot) * per_d;
         }
         s = 0.0f;
-        for (int d = threadIdx.x; d < a.D; d += kResThreads) {
-            const float c = value(d) - mean;
-            s = fmaf(c, c, s);
+#pragma unroll 4
+        for (int d = threadIdx.x * V; d < a.D; d += L * V) {
+            value(d, v);
+#pragma unroll
+            for (int e = 0; e < V; ++e) s = fmaf(v[e] - mean, v[e] - mean, s);
         }
-        inv = 1.0f / sqrtf(fmaf(team_sum<kResThreads>(s, slot), per_d, a.eps));
+        inv = 1.0f / sqrtf(fmaf(team_sum<L>(s, slot), per_d, a.eps));
     };
     float4 st = make_float4(0.0f, 1.0f, 0.0f, 1.0f);
-    if (p.z_scale) statistics([&](int d) { return IO<T>::ld(z + d); }, st.x, st.y);
-    const auto sum = [&](int d) {
-        float v = IO<T>::ld(z + d);
-        if (p.z_scale)
-            v = fmaf((v - st.x) * st.y, IO<T>::ld((const T *)p.z_scale + d),
-                     p.z_B ? IO<T>::ld((const T *)p.z_B + d) : 0.0f);
-        const float r = IO<T>::ld(x + d);
-        return gate ? fmaf(IO<T>::ld(gate + d), v, a.alpha * r) : fmaf(a.alpha, r, v);
+    if (p.z_scale) statistics([&](int d, float (&v)[V]) { get(p.Z, at + d, v); }, st.x, st.y);
+    const auto sum = [&](int d, float (&v)[V]) {
+        float x[V];
+        get(p.Z, at + d, v);
+        if (p.z_scale) {
+            float w[V], b[V];
+            get(p.z_scale, d, w);
+            get(p.z_B, d, b);
+#pragma unroll
+            for (int e = 0; e < V; ++e) v[e] = fmaf((v[e] - st.x) * st.y, w[e], b[e]);
+        }
+        get(p.X, at + d, x);
+        if (a.groups > 0) {
+            float g[V];
+            get(p.gate, gate + d, g);
+#pragma unroll
+            for (int e = 0; e < V; ++e) v[e] = fmaf(g[e], v[e], a.alpha * x[e]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < V; ++e) v[e] = fmaf(a.alpha, x[e], v[e]);
+        }
     };
     statistics(sum, st.z, st.w);
-    for (int d = threadIdx.x; d < a.D; d += kResThreads) {
-        const float s = sum(d), b = p.B ? IO<T>::ld((const T *)p.B + d) : 0.0f;
-        ((T *)p.S)[at + d] = IO<T>::st(s);
-        ((T *)p.Y)[at + d] = IO<T>::st(fmaf((s - st.z) * st.w, IO<T>::ld((const T *)p.scale + d), b));
+#pragma unroll 2
+    for (int d = threadIdx.x * V; d < a.D; d += L * V) {
+        float s[V], w[V], b[V];
+        sum(d, s);
+        get(p.scale, d, w);
+        get(p.B, d, b);
+        IOV::store((T *)p.S + at + d, s);
+#pragma unroll
+        for (int e = 0; e < V; ++e) s[e] = fmaf((s[e] - st.z) * st.w, w[e], b[e]);
+        IOV::store((T *)p.Y + at + d, s);
     }
     if (threadIdx.x == 0 && p.stats) *reinterpret_cast<float4 *>(p.stats + 4 * row) = st;
 }
@@ -473,7 +504,9 @@ __global__ void __launch_bounds__(res_block(L), resnorm_backward_blocks(L, NV * 
 // Rows wider than a warp's run: each team's rows come to shared memory by bulk copies
 // that its first threads issue, one array each, as many rows ahead as there is room
 // for, so that the registers hold sums and not loads in flight.  A block of 512 threads
-// per SM.
+// per SM.  Bound by the latency of a row's two sums and by instruction issue (44 % of the
+// slots): 16384 x 1024 bf16, all sums, sixteen gates, 201 MB in 53 us, 3.8 TB/s; 5003 x 771
+// fp32 in 21 us, 4.3 TB/s.
 constexpr int kStagedThreads = 512;
 constexpr int kStagedRing = 200 * 1024;   // bytes of all teams' rows, and of their totals
 constexpr int kStagedN = 8;               // elements of a thread
@@ -481,7 +514,7 @@ constexpr int kStagedMost = 4;            // rows of a team, being worked on and
 
 // Bytes of one array's row: it starts on a 16-byte boundary of memory, up to 15 bytes
 // ahead of its first element.
-__host__ __device__ inline int staged_pitch(int D, int size) { return (D * size + 15 + 15) / 16 * 16; }
+constexpr int staged_pitch(int D, int size) { return (D * size + 15 + 15) / 16 * 16; }
 
 // Arrays of a stage, and behind them the row's statistics and its place: row (-1: none),
 // gate, segment (-1: none), whether the segment ends with it.
@@ -490,9 +523,9 @@ struct StagedShape {
     int stages, pitch, arrays;
 };
 // Floats of the totals that a team keeps over its gates (dz_scale's and dz_B's).
-inline int staged_totals(bool post, bool gate) { return post && gate ? 2 * kStagedN * kStagedThreads : 0; }
-inline StagedShape staged_shape(int D, int size, int L, bool post, bool gate, bool dS) {
-    StagedShape q;
+constexpr int staged_totals(bool post, bool gate) { return post && gate ? 2 * kStagedN * kStagedThreads : 0; }
+constexpr StagedShape staged_shape(int D, int size, int L, bool post, bool gate, bool dS) {
+    StagedShape q = {};
     q.pitch = staged_pitch(D, size);
     q.arrays = 3 + dS + gate;
     const int per = kStagedThreads / L * (q.arrays * q.pitch + kStagedStats);
@@ -855,109 +888,196 @@ __global__ void __launch_bounds__(kStagedThreads, 1)
     }
 }
 
-// Rows wider than kResOnChip: a block per row for dX and dZ, which leaves the row's
-// two means in `means`; then a thread per column for the sums.
-template <typename T>
-__global__ void __launch_bounds__(kResThreads)
+// Wide rows (resnorm_wide): a block per row for dX and dZ, which leaves the row's two
+// means in `means`; then a thread per run of columns for the sums, which reads the inputs
+// once more: 10 rows of traffic instead of 6, at 3.8 TB/s in bf16 and 5.0 in fp32 (2048 x
+// 8192 with all sums, 48 + 34 us and 79 + 48).
+template <typename T, int V, int L>
+__global__ void __launch_bounds__(L)
     resnorm_wide_backward_kernel(ResNormArgs a, ResNormPtrs p, float2 *means) {
+    using IOV = Run<T, V>;
     const int64_t row = blockIdx.x, at = row * a.D;
-    const T *dS = p.dS ? (const T *)p.dS + at : nullptr, *dY = (const T *)p.dY + at;
-    const T *S = (const T *)p.S + at, *Z = (const T *)p.Z + at;
-    const T *gate = a.groups > 0 ? (const T *)p.gate + row / a.group_rows * a.D : nullptr;
+    const int64_t gate = a.groups > 1 ? row / a.group_rows * a.D : 0;
     const float4 st = __ldg(reinterpret_cast<const float4 *>(p.stats) + row);
     const float per_d = 1.0f / (float)a.D;
     int slot = 0;
+    const auto get = [](const void *base, int64_t i, float (&v)[V]) {
+        IOV::widen(base ? IOV::load((const T *)base + i) : IOV::zero(), v);
+    };
     float t0 = 0.0f, t1 = 0.0f;
-    for (int d = threadIdx.x; d < a.D; d += kResThreads) {
-        const float w = IO<T>::ld(dY + d) * IO<T>::ld((const T *)p.scale + d);
-        t0 += w;
-        t1 = fmaf(w, (IO<T>::ld(S + d) - st.z) * st.w, t1);
+#pragma unroll 4
+    for (int d = threadIdx.x * V; d < a.D; d += L * V) {
+        float y[V], c[V], s[V];
+        get(p.dY, at + d, y);
+        get(p.S, at + d, s);
+        get(p.scale, d, c);
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            const float w = y[e] * c[e];
+            t0 += w;
+            t1 = fmaf(w, (s[e] - st.z) * st.w, t1);
+        }
     }
-    team_sum2<kResThreads>(t0, t1, slot);
+    team_sum2<L>(t0, t1, slot);
     t0 = a.layer ? t0 * -per_d : 0.0f;
     t1 *= -per_d;
     if (threadIdx.x == 0) means[row] = make_float2(t0, t1);
-    const auto ds_of = [&](int d) {
-        const float w = IO<T>::ld(dY + d) * IO<T>::ld((const T *)p.scale + d);
-        const float sh = (IO<T>::ld(S + d) - st.z) * st.w;
-        return fmaf(fmaf(sh, t1, w + t0), st.w, dS ? IO<T>::ld(dS + d) : 0.0f);
+    const auto ds_of = [&](int d, float (&ds)[V]) {
+        float y[V], c[V], s[V];
+        get(p.dY, at + d, y);
+        get(p.S, at + d, s);
+        get(p.dS, at + d, ds);
+        get(p.scale, d, c);
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+            ds[e] = fmaf(fmaf((s[e] - st.z) * st.w, t1, fmaf(y[e], c[e], t0)), st.w, ds[e]);
     };
-    const auto to_z = [&](int d) {
-        float v = ds_of(d);
-        if (gate) v *= IO<T>::ld(gate + d);
-        return p.z_scale ? v * IO<T>::ld((const T *)p.z_scale + d) : v;
+    const auto to_z = [&](int d, float (&v)[V]) {   // from ds
+        float g[V];
+        if (a.groups > 0) {
+            get(p.gate, gate + d, g);
+#pragma unroll
+            for (int e = 0; e < V; ++e) v[e] *= g[e];
+        }
+        if (p.z_scale) {
+            get(p.z_scale, d, g);
+#pragma unroll
+            for (int e = 0; e < V; ++e) v[e] *= g[e];
+        }
     };
     float u0 = 0.0f, u1 = 0.0f;
-    for (int d = threadIdx.x; d < a.D; d += kResThreads) {
-        ((T *)p.dX)[at + d] = IO<T>::st(a.alpha * ds_of(d));
-        const float v = to_z(d);
+#pragma unroll 2
+    for (int d = threadIdx.x * V; d < a.D; d += L * V) {
+        float v[V], out[V], z[V];
+        ds_of(d, v);
+#pragma unroll
+        for (int e = 0; e < V; ++e) out[e] = a.alpha * v[e];
+        IOV::store((T *)p.dX + at + d, out);
+        to_z(d, v);
         if (p.z_scale) {
-            u0 += v;
-            u1 = fmaf(v, (IO<T>::ld(Z + d) - st.x) * st.y, u1);
+            get(p.Z, at + d, z);
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                u0 += v[e];
+                u1 = fmaf(v[e], (z[e] - st.x) * st.y, u1);
+            }
         } else {
-            ((T *)p.dZ)[at + d] = IO<T>::st(v);
+            IOV::store((T *)p.dZ + at + d, v);
         }
     }
     if (!p.z_scale) return;
-    team_sum2<kResThreads>(u0, u1, slot);
+    team_sum2<L>(u0, u1, slot);
     u0 = a.layer ? u0 * -per_d : 0.0f;
     u1 *= -per_d;
-    for (int d = threadIdx.x; d < a.D; d += kResThreads)
-        ((T *)p.dZ)[at + d] =
-            IO<T>::st(fmaf((IO<T>::ld(Z + d) - st.x) * st.y, u1, to_z(d) + u0) * st.y);
+#pragma unroll 2
+    for (int d = threadIdx.x * V; d < a.D; d += L * V) {
+        float v[V], z[V];
+        ds_of(d, v);
+        to_z(d, v);
+        get(p.Z, at + d, z);
+#pragma unroll
+        for (int e = 0; e < V; ++e) v[e] = fmaf((z[e] - st.x) * st.y, u1, v[e] + u0) * st.y;
+        IOV::store((T *)p.dZ + at + d, v);
+    }
 }
-template <typename T>
-__global__ void __launch_bounds__(kResThreads)
+
+// Blocks of the sums per SM, and over the columns.
+template <int V> constexpr int kResSumsBlocks = V == 1 ? 6 : 2;
+inline int resnorm_sums_columns(int D, int V) { return (D + kResThreads * V - 1) / (kResThreads * V); }
+template <typename T, int V>
+__global__ void __launch_bounds__(kResThreads, kResSumsBlocks<V>)
     resnorm_wide_sums_kernel(ResNormArgs a, ResNormPtrs p, ResNormPlan q, const float2 *means,
                              float *partials, float *gate_partials) {
+    using IOV = Run<T, V>;
     wait_for_previous_kernel(means);
-    const int d = blockIdx.x * kResThreads + threadIdx.x;
+    const int d = (blockIdx.x * kResThreads + threadIdx.x) * V;
     if (d >= a.D) return;
-    const float scale = IO<T>::ld((const T *)p.scale + d);
-    const float zs = p.z_scale ? IO<T>::ld((const T *)p.z_scale + d) : 1.0f;
-    const float zb = p.z_B ? IO<T>::ld((const T *)p.z_B + d) : 0.0f;
-    float sum[4] = {}, gate_sum = 0.0f;
-    ResNormWalk w;
-    w.start(q, blockIdx.y);
-    for (int64_t n = (int64_t)q.rounds * q.steps; n > 0; --n, w.next(q)) {
-        if (w.row >= 0) {
-            const int64_t at = (int64_t)w.row * a.D + d;
-            const float4 st = __ldg(reinterpret_cast<const float4 *>(p.stats) + w.row);
-            const float2 t = __ldg(means + w.row);
-            const float y = IO<T>::ld((const T *)p.dY + at);
-            const float sh = (IO<T>::ld((const T *)p.S + at) - st.z) * st.w;
-            const float zh = (IO<T>::ld((const T *)p.Z + at) - st.x) * st.y;
-            float ds = fmaf(fmaf(sh, t.y, y * scale + t.x), st.w,
-                            p.dS ? IO<T>::ld((const T *)p.dS + at) : 0.0f);
-            sum[0] = fmaf(y, sh, sum[0]);
-            sum[1] += y;
-            if (a.groups > 0) {
-                gate_sum = fmaf(ds, fmaf(zh, zs, zb), gate_sum);
-                ds *= IO<T>::ld((const T *)p.gate + (int64_t)w.gate * a.D + d);
+    const auto get = [](const void *base, int64_t i, float (&v)[V]) {
+        IOV::widen(base ? IOV::load((const T *)base + i) : IOV::zero(), v);
+    };
+    float scale[V], zs[V], zb[V], sum[4][V] = {}, gate_sum[V] = {};
+    get(p.scale, d, scale);
+    get(p.z_scale, d, zs);
+    get(p.z_B, d, zb);
+    if (!p.z_scale)
+#pragma unroll
+        for (int e = 0; e < V; ++e) zs[e] = 1.0f;
+    for (int64_t segment = blockIdx.y; segment < (int64_t)q.groups * q.chunks; segment += q.teams) {
+        const int64_t gate = segment / q.chunks, c = segment - gate * q.chunks;
+        const int64_t row0 = gate * q.group_rows + c;
+        int64_t at = row0 * a.D + d;
+        const float4 *stats = reinterpret_cast<const float4 *>(p.stats) + row0;
+        const float2 *mean = means + row0;
+        float g[V];
+        get(a.groups > 0 ? p.gate : nullptr, gate * a.D + d, g);
+        const int rows = (int)((q.group_rows - c + q.chunks - 1) / q.chunks);
+        const int64_t step = (int64_t)q.chunks * a.D;
+#pragma unroll V == 1 ? 4 : 2
+        for (int i = 0; i < rows; ++i, at += step, stats += q.chunks, mean += q.chunks) {
+            float y[V], s[V], z[V], ds[V];
+            get(p.dY, at, y);
+            get(p.S, at, s);
+            get(p.Z, at, z);
+            get(p.dS, at, ds);
+            const float4 st = __ldg(stats);
+            const float2 t = __ldg(mean);
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const float sh = (s[e] - st.z) * st.w, zh = (z[e] - st.x) * st.y;
+                float v = fmaf(fmaf(sh, t.y, fmaf(y[e], scale[e], t.x)), st.w, ds[e]);
+                sum[0][e] = fmaf(y[e], sh, sum[0][e]);
+                sum[1][e] += y[e];
+                if (a.groups > 0) {
+                    gate_sum[e] = fmaf(v, fmaf(zh, zs[e], zb[e]), gate_sum[e]);
+                    v *= g[e];
+                }
+                sum[2][e] = fmaf(v, zh, sum[2][e]);
+                sum[3][e] += v;
             }
-            sum[2] = fmaf(ds, zh, sum[2]);
-            sum[3] += ds;
         }
-        if (a.groups > 0 && w.step + 1 == q.steps) {
-            if (w.segment < (int64_t)q.groups * q.chunks) {
-                if (q.chunks == 1)
-                    ((T *)p.dgate)[(int64_t)w.segment * a.D + d] = IO<T>::st(gate_sum);
-                else
-                    gate_partials[(int64_t)w.segment * a.D + d] = gate_sum;
+        if (a.groups > 0) {
+            if (q.chunks == 1) {
+                IOV::store((T *)p.dgate + segment * a.D + d, gate_sum);
+            } else {
+#pragma unroll
+                for (int e = 0; e < V; ++e) gate_partials[segment * a.D + d + e] = gate_sum[e];
             }
-            gate_sum = 0.0f;
+#pragma unroll
+            for (int e = 0; e < V; ++e) gate_sum[e] = 0.0f;
         }
     }
     if (!partials) return;
     const int vectors = p.z_scale ? 4 : 2;
-    for (int j = 0; j < vectors; ++j)
-        partials[((int64_t)blockIdx.y * vectors + j) * a.D + d] = sum[j];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+            if (j < vectors) partials[((int64_t)blockIdx.y * vectors + j) * a.D + d + e] = sum[j][e];
 }
+
+// Rows that are read more than once by 512 threads and not 256: of more than 32 KB, so that
+// fewer of them are on their way through L2 at once (backward, 838 x 20001 bf16 159 us, and
+// 239 by 256; 2048 x 8192 61 and 47).
+template <typename T> bool resnorm_large(const ResNormArgs &a) { return a.D * sizeof(T) > 32768; }
 
 // Calls f(L, NV) with the threads per row and the runs per thread of the forward
 // pass for a row of `runs` runs.
+// Single elements: enough of them per thread that its sums' shuffles and barriers do not
+// lead, few of them behind the row's end (130055 x 129 bf16 66 us; 331 by 256 threads of one
+// element each, 87 by a warp of eight).
 template <int V, typename F> cudaError_t resnorm_shape(int runs, F &&f) {
     using std::integral_constant;
+    const auto fits = [&](auto l, auto nv) { return runs <= decltype(l)::value * decltype(nv)::value; };
+    if constexpr (V == 1) {
+#define GS_SHAPE(L, NV)                                                     \
+    if (fits(integral_constant<int, L>(), integral_constant<int, NV>()))    \
+        return f(integral_constant<int, L>(), integral_constant<int, NV>());
+        GS_SHAPE(8, 4) GS_SHAPE(8, 6) GS_SHAPE(8, 8) GS_SHAPE(16, 6) GS_SHAPE(16, 8) GS_SHAPE(32, 6)
+        GS_SHAPE(32, 8) GS_SHAPE(32, 12) GS_SHAPE(32, 16) GS_SHAPE(64, 12) GS_SHAPE(64, 16)
+        GS_SHAPE(128, 12) GS_SHAPE(128, 16) GS_SHAPE(256, 12) GS_SHAPE(256, 16) GS_SHAPE(256, 24)
+        GS_SHAPE(256, 32)
+#undef GS_SHAPE
+    }
     if (runs <= 8) return f(integral_constant<int, 8>(), integral_constant<int, 1>());
     if (runs <= 16) return f(integral_constant<int, 16>(), integral_constant<int, 1>());
     if (runs <= 32) return f(integral_constant<int, 32>(), integral_constant<int, 1>());
@@ -968,44 +1088,43 @@ template <int V, typename F> cudaError_t resnorm_shape(int runs, F &&f) {
     if (runs <= 1024) return f(integral_constant<int, 256>(), integral_constant<int, 4>());
     if constexpr (V <= 4)
         if (runs <= 2048) return f(integral_constant<int, 256>(), integral_constant<int, 8>());
-    if constexpr (V == 1)
-        return runs <= 4096 ? f(integral_constant<int, 256>(), integral_constant<int, 16>())
-                            : f(integral_constant<int, 256>(), integral_constant<int, 32>());
     return cudaErrorInvalidValue;   // not reached: D <= kResOnChip
 }
 
-// The same for the backward pass (`post`, `gate`, `dS`: what the call has).  f(staged, L, NV): a team's sums, five per element,
-// stay in registers, eight elements of a thread where rows are staged.  Rows of a
-// warp's run or less keep their loads in registers: a bulk copy of 128 bytes costs as
-// much to issue as one of a few KB; so do rows too wide for two of them in the ring, or
-// for eight elements of 512 threads.
-template <typename T, int V, typename F>
-cudaError_t resnorm_backward_shape(int D, bool post, bool gate, bool dS, F &&f) {
+// The same for the backward pass: f(staged, L, NV).  A team's sums, five
+// per element, stay in registers, eight elements of a thread where rows are staged.  Rows of
+// a warp's run or less keep their loads in registers: a bulk copy of 128 bytes costs as
+// much to issue as one of a few KB.
+template <int V, typename F> cudaError_t resnorm_backward_shape(int D, F &&f) {
     using std::integral_constant;
     using std::false_type;
     using std::true_type;
     const int runs = (D + V - 1) / V;
-    const auto pick = [&](auto l, auto nv) {
-        constexpr int L = decltype(l)::value, NV = decltype(nv)::value;
-        if (staged_shape(D, sizeof(T), L, post, gate, dS).stages >= 2) return f(true_type(), l, nv);
-        return f(false_type(), integral_constant<int, 512>(), integral_constant<int, kResOnChip / V / 512>());
-    };
     if (runs <= 8) return f(false_type(), integral_constant<int, 8>(), integral_constant<int, 1>());
     if (runs <= 16) return f(false_type(), integral_constant<int, 16>(), integral_constant<int, 1>());
     if (runs <= 32) return f(false_type(), integral_constant<int, 32>(), integral_constant<int, 1>());
     constexpr int NV = kStagedN / V;
-    if (D <= 256) return pick(integral_constant<int, 32>(), integral_constant<int, NV>());
-    if (D <= 512) return pick(integral_constant<int, 64>(), integral_constant<int, NV>());
-    if (D <= 1024) return pick(integral_constant<int, 128>(), integral_constant<int, NV>());
-    if (D <= 2048) return pick(integral_constant<int, 256>(), integral_constant<int, NV>());
-    if (D <= 4096) return pick(integral_constant<int, 512>(), integral_constant<int, NV>());
-    return f(false_type(), integral_constant<int, 512>(), integral_constant<int, kResOnChip / V / 512>());
+    if (D <= 256) return f(true_type(), integral_constant<int, 32>(), integral_constant<int, NV>());
+    if (D <= 512) return f(true_type(), integral_constant<int, 64>(), integral_constant<int, NV>());
+    if (D <= 1024) return f(true_type(), integral_constant<int, 128>(), integral_constant<int, NV>());
+    if (D <= 2048) return f(true_type(), integral_constant<int, 256>(), integral_constant<int, NV>());
+    if (D <= kResStaged) return f(true_type(), integral_constant<int, 512>(), integral_constant<int, NV>());
+    return f(false_type(), integral_constant<int, 512>(), integral_constant<int, 2 * NV>());
+}
+// Rows that are read again for the sums: those that do not fit a block's registers beside
+// more than two sums (2048 x 8192 bf16: two sums in registers 45 us, read again 84; five
+// 129 and 88; 4088 x 4104 fp32 77 and 126; 358 and 142).
+inline bool resnorm_wide(const ResNormArgs &a, bool post) {
+    return a.D > kResOnChip || (a.D > kResStaged && (post || a.groups > 0));
 }
 
-template <typename T, int V> ResNormPlan resnorm_plan_of(const ResNormArgs &a, bool post, bool dS) {
+template <typename T, int V> ResNormPlan resnorm_plan_of(const ResNormArgs &a, bool post) {
     ResNormPlan q = {};
-    if (a.D > kResOnChip) return resnorm_plan(a, 1, kResWideBlocks * kResSms);
-    resnorm_backward_shape<T, V>(a.D, post, a.groups > 0, dS, [&](auto staged, auto l, auto nv) {
+    if (resnorm_wide(a, post)) {
+        const int columns = resnorm_sums_columns(a.D, V);
+        return resnorm_plan(a, 1, std::max(1, kResSumsBlocks<V> * kResSms / columns));
+    }
+    resnorm_backward_shape<V>(a.D, [&](auto staged, auto l, auto nv) {
         constexpr int L = decltype(l)::value, NV = decltype(nv)::value;
         q = decltype(staged)::value
                 ? resnorm_plan(a, kStagedThreads / L, kResSms)
@@ -1016,29 +1135,28 @@ template <typename T, int V> ResNormPlan resnorm_plan_of(const ResNormArgs &a, b
 }
 
 // Workspace: the blocks' column sums, the segments' sums for the gate, and the means
-// of rows wider than kResOnChip.
+// of rows wider than kResStaged.
 struct ResNormLayout {
     size_t gate, means, bytes;
-    ResNormLayout(const ResNormArgs &a, const ResNormPlan &q) {
+    ResNormLayout(const ResNormArgs &a, const ResNormPlan &q, bool post) {
+        const bool wide = resnorm_wide(a, post);
         const auto up = [](size_t n) { return (n + 255) & ~(size_t)255; };
         gate = up((size_t)q.blocks * 4 * a.D * sizeof(float));
-        // one gate: a row of sums per block, but per chunk for rows wider than kResOnChip
+        // one gate: a row of sums per block, but per chunk for wide rows
         const size_t sums = a.groups == 0                        ? 0
-                            : a.groups == 1 && a.D <= kResOnChip ? q.blocks
+                            : a.groups == 1 && !wide             ? q.blocks
                             : q.chunks > 1                       ? (size_t)q.groups * q.chunks
                                                                  : 0;
         means = gate + up(sums * a.D * sizeof(float));
-        bytes = means + (a.D > kResOnChip ? up((size_t)a.rows * sizeof(float2)) : 0);
+        bytes = means + (wide ? up((size_t)a.rows * sizeof(float2)) : 0);
     }
 };
 
 template <typename T> size_t resnorm_ws_bytes(const ResNormArgs &a) {
-    size_t most = 0;   // whatever the alignment will be, with dS and z_scale or without
-    for (int form = 0; form < 4; ++form) {
-        const bool post = form & 1, dS = form & 2;
-        const size_t b1 = ResNormLayout(a, resnorm_plan_of<T, 1>(a, post, dS)).bytes;
-        const size_t bv = ResNormLayout(a, resnorm_plan_of<T, kVec<T>>(a, post, dS)).bytes;
-        most = std::max(most, std::max(b1, bv));
+    size_t most = 0;   // whatever the alignment will be, with z_scale or without
+    for (const bool post : {false, true}) {
+        most = std::max(most, ResNormLayout(a, resnorm_plan_of<T, 1>(a, post), post).bytes);
+        most = std::max(most, ResNormLayout(a, resnorm_plan_of<T, kVec<T>>(a, post), post).bytes);
     }
     return most;
 }
@@ -1058,20 +1176,25 @@ cudaError_t run_resnorm(const ResNormArgs &a, const ResNormPtrs &p, cudaStream_t
 
 template <typename T>
 cudaError_t launch_resnorm(const ResNormArgs &a, const ResNormPtrs &p, cudaStream_t s) {
+    const bool runs = a.D % kVec<T> == 0 && aligned16(p.X) && aligned16(p.Z) && aligned16(p.gate) &&
+                      aligned16(p.z_scale) && aligned16(p.z_B) && aligned16(p.scale) &&
+                      aligned16(p.B) && aligned16(p.S) && aligned16(p.Y);
     if (a.D > kResOnChip) {
-        resnorm_wide_kernel<T><<<(unsigned)a.rows, kResThreads, 0, s>>>(a, p);
+        constexpr int V = kVec<T>;
+        const bool large = resnorm_large<T>(a);
+        const auto kernel = large ? (runs ? resnorm_wide_kernel<T, V, 512> : resnorm_wide_kernel<T, 1, 512>)
+                                  : (runs ? resnorm_wide_kernel<T, V, 256> : resnorm_wide_kernel<T, 1, 256>);
+        kernel<<<(unsigned)a.rows, large ? 512 : 256, 0, s>>>(a, p);
         return cudaGetLastError();
     }
-    if (a.D % kVec<T> == 0 && aligned16(p.X) && aligned16(p.Z) && aligned16(p.gate) &&
-        aligned16(p.z_scale) && aligned16(p.z_B) && aligned16(p.scale) && aligned16(p.B) &&
-        aligned16(p.S) && aligned16(p.Y))
-        return run_resnorm<T, kVec<T>>(a, p, s);
-    return run_resnorm<T, 1>(a, p, s);
+    return runs ? run_resnorm<T, kVec<T>>(a, p, s) : run_resnorm<T, 1>(a, p, s);
 }
 
 template <typename T, int V, int L, int NV, bool POST, bool GATE>
 cudaError_t run_resnorm_staged(const ResNormArgs &a, const ResNormPtrs &p, const ResNormPlan &q,
                                float *partials, float *gate_partials, cudaStream_t s) {
+    static_assert(staged_shape(L * kStagedN, sizeof(T), L, POST, GATE, true).stages >= 2,
+                  "a row being worked on and one ahead");
     const auto kernel = resnorm_staged_kernel<T, V, L, NV, POST, GATE>;
     const StagedShape shape = staged_shape(a.D, sizeof(T), L, POST, GATE, p.dS);
     const int rows = kStagedThreads / L * shape.stages * (shape.arrays * shape.pitch + kStagedStats);
@@ -1091,7 +1214,7 @@ cudaError_t run_resnorm_backward(const ResNormArgs &a, const ResNormPtrs &p, con
                                  float *partials, float *gate_partials, cudaStream_t s) {
     const auto form = [&](auto post, auto gate) {
         constexpr bool POST = decltype(post)::value, GATE = decltype(gate)::value;
-        return resnorm_backward_shape<T, V>(a.D, POST, GATE, p.dS, [&](auto staged, auto l, auto nv) {
+        return resnorm_backward_shape<V>(a.D, [&](auto staged, auto l, auto nv) {
             constexpr int L = decltype(l)::value, NV = decltype(nv)::value;
             if constexpr (decltype(staged)::value) {
                 return run_resnorm_staged<T, V, L, NV, POST, GATE>(a, p, q, partials, gate_partials, s);
@@ -1108,11 +1231,25 @@ cudaError_t run_resnorm_backward(const ResNormArgs &a, const ResNormPtrs &p, con
     return a.groups > 0 ? form(false_type(), true_type()) : form(false_type(), false_type());
 }
 
+// Rows wider than kResStaged.
+template <typename T, int V>
+cudaError_t run_resnorm_wide(const ResNormArgs &a, const ResNormPtrs &p, const ResNormPlan &q,
+                             float2 *means, float *partials, float *gate_partials, cudaStream_t s) {
+    const bool large = resnorm_large<T>(a);
+    const auto kernel = large ? resnorm_wide_backward_kernel<T, V, 512> : resnorm_wide_backward_kernel<T, V, 256>;
+    kernel<<<(unsigned)a.rows, large ? 512 : 256, 0, s>>>(a, p, means);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || (!partials && a.groups == 0)) return e;
+    return launch_next(true, resnorm_wide_sums_kernel<T, V>,
+                       dim3(resnorm_sums_columns(a.D, V), q.blocks), kResThreads, 0, s, a, p, q, means,
+                       partials, gate_partials);
+}
+
 template <typename T>
 cudaError_t launch_resnorm_backward(const ResNormArgs &a, const ResNormPtrs &p, void *ws,
                                     cudaStream_t s) {
     const bool sums = p.dScale || p.dB || p.dz_scale || p.dz_B;
-    const bool wide = a.D > kResOnChip;
+    const bool wide = resnorm_wide(a, p.z_scale);
     const bool runs = a.D % kVec<T> == 0 && aligned16(p.dS) && aligned16(p.dY) && aligned16(p.S) &&
                       aligned16(p.Z) && aligned16(p.gate) && aligned16(p.z_scale) &&
                       aligned16(p.z_B) && aligned16(p.scale) && aligned16(p.dX) &&
@@ -1120,19 +1257,15 @@ cudaError_t launch_resnorm_backward(const ResNormArgs &a, const ResNormPtrs &p, 
     ResNormPlan q = {};
     SumArgs sum = {};
     if (a.rows > 0) {
-        q = runs ? resnorm_plan_of<T, kVec<T>>(a, p.z_scale, p.dS) : resnorm_plan_of<T, 1>(a, p.z_scale, p.dS);
-        const ResNormLayout at(a, q);
+        q = runs ? resnorm_plan_of<T, kVec<T>>(a, p.z_scale) : resnorm_plan_of<T, 1>(a, p.z_scale);
+        const ResNormLayout at(a, q, p.z_scale);
         char *base = (char *)ws;
         float *partials = sums ? (float *)base : nullptr, *gates = (float *)(base + at.gate);
         cudaError_t e;
         if (wide) {
             float2 *means = (float2 *)(base + at.means);
-            resnorm_wide_backward_kernel<T><<<(unsigned)a.rows, kResThreads, 0, s>>>(a, p, means);
-            e = cudaGetLastError();
-            if (e == cudaSuccess && (sums || a.groups > 0))
-                e = launch_next(true, resnorm_wide_sums_kernel<T>,
-                                dim3((a.D + kResThreads - 1) / kResThreads, q.blocks), kResThreads, 0,
-                                s, a, p, q, means, partials, gates);
+            e = runs ? run_resnorm_wide<T, kVec<T>>(a, p, q, means, partials, gates, s)
+                     : run_resnorm_wide<T, 1>(a, p, q, means, partials, gates, s);
         } else {
             e = runs ? run_resnorm_backward<T, kVec<T>>(a, p, q, partials, gates, s)
                      : run_resnorm_backward<T, 1>(a, p, q, partials, gates, s);

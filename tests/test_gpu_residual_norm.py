@@ -57,6 +57,22 @@ def test_sizes(gs_cuda, rows, D, dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("D", [20, 43, 61, 90, 127, 170, 250, 333, 500, 701, 1001, 1301, 1999, 2500,
+                               4001, 5001, 8191])
+def test_widths_of_single_elements(gs_cuda, D, dtype):
+    t, dS, dY = _make(38, D, dtype, True, 2, seed=D)
+    _check(gs_cuda, t, dS, dY, dtype)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("post,groups", [(False, 0), (False, 1), (False, 4), (True, 0), (True, 1)])
+@pytest.mark.parametrize("D", [4104, 6001, 8192, 8209, 16400, 20001])
+def test_forms_of_wide_rows(gs_cuda, D, post, groups, dtype):
+    t, dS, dY = _make(20, D, dtype, post, groups, seed=D)
+    _check(gs_cuda, t, dS if groups else None, dY, dtype, "rms" if post else "layer")
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("kind", ["layer", "rms"])
 @pytest.mark.parametrize("post", [False, True])
 @pytest.mark.parametrize("biases", [False, True])
