@@ -330,6 +330,7 @@ constexpr int resnorm_backward_blocks(int L, int N) {
     return L > kResThreads ? 1 : N <= 4 ? 3 : N <= 8 ? 2 : 1;
 }
 
+// 65536 x 256 bf16, all sums, 201 MB in 48 us, 4.2 TB/s; 266305 x 63 in 109, 1.8 TB/s.
 // dX, dZ and, into partials[block][vector], the block's column sums (for dScale, dB
 // and, with POST, dz_scale and dz_B); into gate_partials[segment] those for the gate, or
 // [block] where all rows share one.  The next row's loads are issued before this one is
@@ -605,7 +606,7 @@ __global__ void __launch_bounds__(kStagedThreads, 1)
     const int part = threadIdx.x % L, team = threadIdx.x / L;
     const int stages = sh_.stages, row_bytes = sh_.pitch, stats_at = sh_.arrays * row_bytes;
     const int stage_bytes = stats_at + kStagedStats;   // a multiple of 16
-    static_assert(N == kStagedN, "elements of a thread");
+    static_assert(N <= kStagedN && N % 2 == 0, "elements of a thread");
     constexpr int kTotals = POST && GATE ? 2 * N * kStagedThreads : 0;
     // this thread's totals, kStagedThreads floats apart
     float *totals = reinterpret_cast<float *>(ring) + threadIdx.x;
@@ -1091,15 +1092,26 @@ template <int V, typename F> cudaError_t resnorm_shape(int runs, F &&f) {
     return cudaErrorInvalidValue;   // not reached: D <= kResOnChip
 }
 
-// The same for the backward pass: f(staged, L, NV).  A team's sums, five
-// per element, stay in registers, eight elements of a thread where rows are staged.  Rows of
-// a warp's run or less keep their loads in registers: a bulk copy of 128 bytes costs as
-// much to issue as one of a few KB.
+// The same for the backward pass: f(staged, L, NV).  A team's sums, five per element, stay
+// in registers, up to eight elements of a thread where rows are staged.  Rows of a warp's run
+// or less keep their loads in registers: a bulk copy of 128 bytes costs as much to issue as
+// one of a few KB (508400 x 33 bf16 117 us, staged 481; 83886 x 200 130 and 64).
 template <int V, typename F> cudaError_t resnorm_backward_shape(int D, F &&f) {
     using std::integral_constant;
     using std::false_type;
     using std::true_type;
     const int runs = (D + V - 1) / V;
+    if constexpr (V == 1) {
+#define GS_SHAPE(STAGED, L, NV) \
+    if (D <= L * NV) return f(STAGED(), integral_constant<int, L>(), integral_constant<int, NV>());
+        GS_SHAPE(false_type, 8, 2) GS_SHAPE(false_type, 8, 3) GS_SHAPE(false_type, 8, 4)
+        GS_SHAPE(false_type, 8, 6) GS_SHAPE(false_type, 16, 4) GS_SHAPE(false_type, 16, 6)
+        GS_SHAPE(false_type, 32, 4) GS_SHAPE(false_type, 32, 5)
+        GS_SHAPE(true_type, 32, 6) GS_SHAPE(true_type, 32, 8) GS_SHAPE(true_type, 64, 6)
+        GS_SHAPE(true_type, 64, 8) GS_SHAPE(true_type, 128, 6) GS_SHAPE(true_type, 128, 8)
+        GS_SHAPE(true_type, 256, 6) GS_SHAPE(true_type, 256, 8) GS_SHAPE(true_type, 512, 6)
+#undef GS_SHAPE
+    }
     if (runs <= 8) return f(false_type(), integral_constant<int, 8>(), integral_constant<int, 1>());
     if (runs <= 16) return f(false_type(), integral_constant<int, 16>(), integral_constant<int, 1>());
     if (runs <= 32) return f(false_type(), integral_constant<int, 32>(), integral_constant<int, 1>());
