@@ -18,6 +18,7 @@
 #pragma once
 
 #include <algorithm>
+#include <initializer_list>
 
 #include "gs_sums.cuh"
 
@@ -72,8 +73,9 @@ template <int L> __device__ __forceinline__ float team_sum(float a, int &slot) {
 }
 
 // A row per team of L threads.  Bound by memory where rows are runs (1,048,576 x 64 fp32,
-// 1.07 GB, 155 us: 1.03 of a copy's rate; 2048 x 8192 bf16 34 us, 3.9 TB/s), by the single
-// elements' instructions elsewhere (21760 x 771 bf16 62 us, 2.1 TB/s; fp32 60, 4.4).
+// 1.07 GB, 155 us: 1.03 of a copy's rate; 2048 x 8192 bf16 34 us, 3.9 TB/s), by the
+// instructions of pairs and single elements elsewhere (21760 x 771 bf16 62 us, 2.1 TB/s; fp32
+// 60, 4.4).
 template <typename T, int V, int L, int NV, bool POST>
 __global__ void __launch_bounds__(res_block(L)) resnorm_kernel(ResNormArgs a, ResNormPtrs p) {
     using IOV = Run<T, V>;
@@ -117,7 +119,7 @@ __global__ void __launch_bounds__(res_block(L)) resnorm_kernel(ResNormArgs a, Re
             const int d = (k * L + part) * V;
             return base && d < a.D ? IOV::load((const T *)base + d) : IOV::zero();
         };
-        if constexpr (L == 256 && NV == 8 && V > 1) {
+        if constexpr (L == 256 && NV == 8 && V > 2) {
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
                 float w[V], b[V] = {};
@@ -600,6 +602,7 @@ __global__ void __launch_bounds__(kStagedThreads, 1)
                           float *gate_partials) {
     constexpr int kTeams = kStagedThreads / L, N = NV * V, P = N / 2, kVectors = POST ? 4 : 2;
     using IOV = Run<T, V>;
+    constexpr bool kWhole = V * sizeof(T) == 16;   // rows start on 16-byte boundaries
     extern __shared__ __align__(16) unsigned char ring[];
     __shared__ __align__(8) uint64_t full[kTeams][kStagedMost];
     __shared__ __align__(16) float shared_sums[kTeams][2][2][L / 32];
@@ -645,7 +648,7 @@ __global__ void __launch_bounds__(kStagedThreads, 1)
             mbar_arrive_expect_tx(bar, ahead.row >= 0 ? 16 : 0);
             if (ahead.row >= 0) bulk_copy_g2s(to, p.stats + (int64_t)ahead.row * 4, 16, bar);
         } else if (fetches && ahead.row >= 0)
-            staged_fetch<T, V == 1>(mine + s * stage_bytes + mine_of * row_bytes,
+            staged_fetch<T, !kWhole>(mine + s * stage_bytes + mine_of * row_bytes,
                                     array + (of_gate ? (int64_t)ahead.gate : (int64_t)ahead.row) * a.D, a.D,
                                     array, array_end, bar);
         else if (fetches)   // no row: the phase is over at once
@@ -662,7 +665,7 @@ __global__ void __launch_bounds__(kStagedThreads, 1)
     // a thread's elements of a staged row, in pairs; zeros behind the row's end
     const auto take = [&](const unsigned char *row, const void *base, int64_t offset, float2 (&v)[P]) {
         const T *e = reinterpret_cast<const T *>(
-            V > 1 ? row : row + ((uintptr_t)((const T *)base + offset) & 15));
+            kWhole ? row : row + ((uintptr_t)((const T *)base + offset) & 15));
         float f[N];
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
@@ -983,7 +986,7 @@ __global__ void __launch_bounds__(L)
 }
 
 // Blocks of the sums per SM, and over the columns.
-template <int V> constexpr int kResSumsBlocks = V == 1 ? 6 : 2;
+template <int V> constexpr int kResSumsBlocks = V <= 2 ? 6 / V : 2;
 inline int resnorm_sums_columns(int D, int V) { return (D + kResThreads * V - 1) / (kResThreads * V); }
 template <typename T, int V>
 __global__ void __launch_bounds__(kResThreads, kResSumsBlocks<V>)
@@ -1063,22 +1066,21 @@ template <typename T> bool resnorm_large(const ResNormArgs &a) { return a.D * si
 
 // Calls f(L, NV) with the threads per row and the runs per thread of the forward
 // pass for a row of `runs` runs.
-// Single elements: enough of them per thread that its sums' shuffles and barriers do not
+// Single elements and pairs: enough of them per thread that its sums' shuffles and barriers do not
 // lead, few of them behind the row's end (130055 x 129 bf16 66 us; 331 by 256 threads of one
 // element each, 87 by a warp of eight).
 template <int V, typename F> cudaError_t resnorm_shape(int runs, F &&f) {
     using std::integral_constant;
-    const auto fits = [&](auto l, auto nv) { return runs <= decltype(l)::value * decltype(nv)::value; };
-    if constexpr (V == 1) {
-#define GS_SHAPE(L, NV)                                                     \
-    if (fits(integral_constant<int, L>(), integral_constant<int, NV>()))    \
-        return f(integral_constant<int, L>(), integral_constant<int, NV>());
+    if constexpr (V <= 2) {
+#define GS_SHAPE(L, N) \
+    if (runs * V <= L * N) return f(integral_constant<int, L>(), integral_constant<int, N / V>());
         GS_SHAPE(8, 4) GS_SHAPE(8, 6) GS_SHAPE(8, 8) GS_SHAPE(16, 6) GS_SHAPE(16, 8) GS_SHAPE(32, 6)
         GS_SHAPE(32, 8) GS_SHAPE(32, 12) GS_SHAPE(32, 16) GS_SHAPE(64, 12) GS_SHAPE(64, 16)
         GS_SHAPE(128, 12) GS_SHAPE(128, 16) GS_SHAPE(256, 12) GS_SHAPE(256, 16) GS_SHAPE(256, 24)
         GS_SHAPE(256, 32)
 #undef GS_SHAPE
     }
+    if (runs <= 4) return f(integral_constant<int, 4>(), integral_constant<int, 1>());
     if (runs <= 8) return f(integral_constant<int, 8>(), integral_constant<int, 1>());
     if (runs <= 16) return f(integral_constant<int, 16>(), integral_constant<int, 1>());
     if (runs <= 32) return f(integral_constant<int, 32>(), integral_constant<int, 1>());
@@ -1101,9 +1103,10 @@ template <int V, typename F> cudaError_t resnorm_backward_shape(int D, F &&f) {
     using std::false_type;
     using std::true_type;
     const int runs = (D + V - 1) / V;
-    if constexpr (V == 1) {
-#define GS_SHAPE(STAGED, L, NV) \
-    if (D <= L * NV) return f(STAGED(), integral_constant<int, L>(), integral_constant<int, NV>());
+    if constexpr (V <= 2) {
+#define GS_SHAPE(STAGED, L, N)        \
+    if constexpr (N % V == 0)         \
+        if (D <= L * N) return f(STAGED(), integral_constant<int, L>(), integral_constant<int, N / V>());
         GS_SHAPE(false_type, 8, 2) GS_SHAPE(false_type, 8, 3) GS_SHAPE(false_type, 8, 4)
         GS_SHAPE(false_type, 8, 6) GS_SHAPE(false_type, 16, 4) GS_SHAPE(false_type, 16, 6)
         GS_SHAPE(false_type, 32, 4) GS_SHAPE(false_type, 32, 5)
@@ -1112,6 +1115,7 @@ template <int V, typename F> cudaError_t resnorm_backward_shape(int D, F &&f) {
         GS_SHAPE(true_type, 256, 6) GS_SHAPE(true_type, 256, 8) GS_SHAPE(true_type, 512, 6)
 #undef GS_SHAPE
     }
+    if (runs <= 4) return f(false_type(), integral_constant<int, 4>(), integral_constant<int, 1>());
     if (runs <= 8) return f(false_type(), integral_constant<int, 8>(), integral_constant<int, 1>());
     if (runs <= 16) return f(false_type(), integral_constant<int, 16>(), integral_constant<int, 1>());
     if (runs <= 32) return f(false_type(), integral_constant<int, 32>(), integral_constant<int, 1>());
@@ -1168,9 +1172,21 @@ template <typename T> size_t resnorm_ws_bytes(const ResNormArgs &a) {
     size_t most = 0;   // whatever the alignment will be, with z_scale or without
     for (const bool post : {false, true}) {
         most = std::max(most, ResNormLayout(a, resnorm_plan_of<T, 1>(a, post), post).bytes);
+        most = std::max(most, ResNormLayout(a, resnorm_plan_of<T, 2>(a, post), post).bytes);
         most = std::max(most, ResNormLayout(a, resnorm_plan_of<T, kVec<T>>(a, post), post).bytes);
     }
     return most;
+}
+
+// Calls f(V) with the elements of a run: 16 bytes, 2 or 1, as the width and the addresses
+// allow (21788 x 770 bf16 by pairs 42 us, by single elements 63; backward 78 and 96).
+template <typename T, typename F>
+auto resnorm_width(int D, std::initializer_list<const void *> tensors, F &&f) {
+    uintptr_t all = (uintptr_t)D * sizeof(T);
+    for (const void *t : tensors) all |= (uintptr_t)t;
+    if (all % 16 == 0) return f(std::integral_constant<int, kVec<T>>());
+    if (all % (2 * sizeof(T)) == 0) return f(std::integral_constant<int, 2>());
+    return f(std::integral_constant<int, 1>());
 }
 
 template <typename T, int V>
@@ -1188,18 +1204,15 @@ cudaError_t run_resnorm(const ResNormArgs &a, const ResNormPtrs &p, cudaStream_t
 
 template <typename T>
 cudaError_t launch_resnorm(const ResNormArgs &a, const ResNormPtrs &p, cudaStream_t s) {
-    const bool runs = a.D % kVec<T> == 0 && aligned16(p.X) && aligned16(p.Z) && aligned16(p.gate) &&
-                      aligned16(p.z_scale) && aligned16(p.z_B) && aligned16(p.scale) &&
-                      aligned16(p.B) && aligned16(p.S) && aligned16(p.Y);
-    if (a.D > kResOnChip) {
-        constexpr int V = kVec<T>;
-        const bool large = resnorm_large<T>(a);
-        const auto kernel = large ? (runs ? resnorm_wide_kernel<T, V, 512> : resnorm_wide_kernel<T, 1, 512>)
-                                  : (runs ? resnorm_wide_kernel<T, V, 256> : resnorm_wide_kernel<T, 1, 256>);
-        kernel<<<(unsigned)a.rows, large ? 512 : 256, 0, s>>>(a, p);
-        return cudaGetLastError();
-    }
-    return runs ? run_resnorm<T, kVec<T>>(a, p, s) : run_resnorm<T, 1>(a, p, s);
+    return resnorm_width<T>(
+        a.D, {p.X, p.Z, p.gate, p.z_scale, p.z_B, p.scale, p.B, p.S, p.Y}, [&](auto v) {
+            constexpr int V = decltype(v)::value;
+            if (a.D <= kResOnChip) return run_resnorm<T, V>(a, p, s);
+            const bool large = resnorm_large<T>(a);
+            const auto kernel = large ? resnorm_wide_kernel<T, V, 512> : resnorm_wide_kernel<T, V, 256>;
+            kernel<<<(unsigned)a.rows, large ? 512 : 256, 0, s>>>(a, p);
+            return cudaGetLastError();
+        });
 }
 
 template <typename T, int V, int L, int NV, bool POST, bool GATE>
@@ -1262,31 +1275,27 @@ cudaError_t launch_resnorm_backward(const ResNormArgs &a, const ResNormPtrs &p, 
                                     cudaStream_t s) {
     const bool sums = p.dScale || p.dB || p.dz_scale || p.dz_B;
     const bool wide = resnorm_wide(a, p.z_scale);
-    const bool runs = a.D % kVec<T> == 0 && aligned16(p.dS) && aligned16(p.dY) && aligned16(p.S) &&
-                      aligned16(p.Z) && aligned16(p.gate) && aligned16(p.z_scale) &&
-                      aligned16(p.z_B) && aligned16(p.scale) && aligned16(p.dX) &&
-                      aligned16(p.dZ) && aligned16(p.dgate);
     ResNormPlan q = {};
     SumArgs sum = {};
     if (a.rows > 0) {
-        q = runs ? resnorm_plan_of<T, kVec<T>>(a, p.z_scale) : resnorm_plan_of<T, 1>(a, p.z_scale);
-        const ResNormLayout at(a, q, p.z_scale);
-        char *base = (char *)ws;
-        float *partials = sums ? (float *)base : nullptr, *gates = (float *)(base + at.gate);
-        cudaError_t e;
-        if (wide) {
-            float2 *means = (float2 *)(base + at.means);
-            e = runs ? run_resnorm_wide<T, kVec<T>>(a, p, q, means, partials, gates, s)
-                     : run_resnorm_wide<T, 1>(a, p, q, means, partials, gates, s);
-        } else {
-            e = runs ? run_resnorm_backward<T, kVec<T>>(a, p, q, partials, gates, s)
-                     : run_resnorm_backward<T, 1>(a, p, q, partials, gates, s);
-        }
+        const cudaError_t e = resnorm_width<T>(
+            a.D,
+            {p.dS, p.dY, p.S, p.Z, p.gate, p.z_scale, p.z_B, p.scale, p.dX, p.dZ, p.dgate},
+            [&](auto v) {
+                constexpr int V = decltype(v)::value;
+                q = resnorm_plan_of<T, V>(a, p.z_scale);
+                const ResNormLayout at(a, q, p.z_scale);
+                char *base = (char *)ws;
+                float *partials = sums ? (float *)base : nullptr, *gates = (float *)(base + at.gate);
+                sum.from = partials;
+                sum.group_from = gates;
+                return wide ? run_resnorm_wide<T, V>(a, p, q, (float2 *)(base + at.means), partials,
+                                                     gates, s)
+                            : run_resnorm_backward<T, V>(a, p, q, partials, gates, s);
+            });
         if (e != cudaSuccess) return e;
-        sum.from = partials;
         const bool by_block = a.groups == 1 && !wide;
         if (by_block || (a.groups > 0 && q.chunks > 1)) {
-            sum.group_from = gates;
             sum.group_to = p.dgate;
             sum.groups = a.groups;
             sum.group_count = by_block ? q.blocks : q.chunks;
@@ -1304,7 +1313,15 @@ cudaError_t launch_resnorm_backward(const ResNormArgs &a, const ResNormPtrs &p, 
     return launch_sums<T>(sum, a.rows > 0, s);
 }
 
+// The gradient by single elements and by pairs is compiled by itself.
+#define GS_RESNORM_BACKWARD(T, V)                                                                \
+    template cudaError_t run_resnorm_backward<T, V>(const ResNormArgs &, const ResNormPtrs &,     \
+                                                    const ResNormPlan &, float *, float *,        \
+                                                    cudaStream_t);
+
 #define GS_RESNORM_INST(T)                                                                       \
+    extern GS_RESNORM_BACKWARD(T, 1)                                                              \
+    extern GS_RESNORM_BACKWARD(T, 2)                                                              \
     template size_t resnorm_ws_bytes<T>(const ResNormArgs &);                                     \
     template cudaError_t launch_resnorm<T>(const ResNormArgs &, const ResNormPtrs &, cudaStream_t); \
     template cudaError_t launch_resnorm_backward<T>(const ResNormArgs &, const ResNormPtrs &,     \

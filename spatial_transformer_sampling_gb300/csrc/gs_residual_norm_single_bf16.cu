@@ -1,0 +1,6 @@
+// The residual norm's gradient by single elements (bf16).
+#include "gs_residual_norm.cuh"
+
+namespace gs {
+GS_RESNORM_BACKWARD(__nv_bfloat16, 1)
+}

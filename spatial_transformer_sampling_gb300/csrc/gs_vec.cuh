@@ -1,5 +1,5 @@
-// gs_vec.cuh -- runs of V consecutive elements moved in one access (16 bytes, or 8,
-// or a single element where rows or bases are not 16-byte aligned), widened to
+// gs_vec.cuh -- runs of V consecutive elements moved in one access (16 bytes, or two
+// elements, or a single one where rows or bases are not 16-byte aligned), widened to
 // fp32.
 #pragma once
 
@@ -10,9 +10,10 @@ namespace gs {
 template <typename T> constexpr int kVec = 16 / (int)sizeof(T);
 
 template <typename T, int V> struct Run {
-    static_assert(V == 1 || V * sizeof(T) == 8 || V * sizeof(T) == 16,
-                  "a run is one element, 8 or 16 bytes");
-    using Raw = std::conditional_t<V == 1, T, std::conditional_t<V * sizeof(T) == 8, uint2, uint4>>;
+    static_assert(V == 1 || V == 2 || V * sizeof(T) == 16, "a run is one or two elements or 16 bytes");
+    using Raw = std::conditional_t<
+        V == 1, T, std::conditional_t<V * sizeof(T) == 16, uint4,
+                                      std::conditional_t<V * sizeof(T) == 8, uint2, uint32_t>>>;
     static __device__ __forceinline__ Raw load(const T *p) {
         return *reinterpret_cast<const Raw *>(p);
     }

@@ -65,6 +65,30 @@ def test_widths_of_single_elements(gs_cuda, D, dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("D", [2, 18, 22, 30, 42, 62, 90, 126, 150, 190, 250, 330, 510, 702, 1002, 1302,
+                               1998, 2502, 4002, 4102, 5002, 8190, 9002, 20002])
+def test_widths_of_pairs(gs_cuda, D, dtype):
+    t, dS, dY = _make(38, D, dtype, True, 2, seed=D)
+    _check(gs_cuda, t, dS, dY, dtype)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("D", [4, 12, 16, 24, 32])
+def test_widths_of_few_runs(gs_cuda, D, dtype):
+    t, dS, dY = _make(999, D, dtype, True, 3, seed=D)
+    _check(gs_cuda, t, dS, dY, dtype)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,D", [(30, 64), (30, 520), (5, 8208)])
+def test_bases_that_are_aligned_to_pairs(gs_cuda, rows, D, dtype):
+    t, dS, dY = _make(rows, D, dtype, seed=9)
+    room = torch.empty(rows * D + 2, dtype=ref.DT[dtype], device="cuda")
+    room[2:] = t["Z"].flatten()
+    _check(gs_cuda, dict(t, Z=room[2:].view(rows, D)), dS, dY, dtype)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("post,groups", [(False, 0), (False, 1), (False, 4), (True, 0), (True, 1)])
 @pytest.mark.parametrize("D", [4104, 6001, 8192, 8209, 16400, 20001])
 def test_forms_of_wide_rows(gs_cuda, D, post, groups, dtype):
