@@ -1066,9 +1066,9 @@ template <typename T> bool resnorm_large(const ResNormArgs &a) { return a.D * si
 
 // Calls f(L, NV) with the threads per row and the runs per thread of the forward
 // pass for a row of `runs` runs.
-// Single elements and pairs: enough of them per thread that its sums' shuffles and barriers do not
-// lead, few of them behind the row's end (130055 x 129 bf16 66 us; 331 by 256 threads of one
-// element each, 87 by a warp of eight).
+// Enough elements per thread that its sums' shuffles and barriers do not lead, few of them
+// behind the row's end (130055 x 129 bf16 66 us; 331 by 256 threads of one element each, 87
+// by a warp of eight; 32263 x 520 fp32 51, and 96 by 256 threads of one run).
 template <int V, typename F> cudaError_t resnorm_shape(int runs, F &&f) {
     using std::integral_constant;
     if constexpr (V <= 2) {
@@ -1080,17 +1080,15 @@ template <int V, typename F> cudaError_t resnorm_shape(int runs, F &&f) {
         GS_SHAPE(256, 32)
 #undef GS_SHAPE
     }
-    if (runs <= 4) return f(integral_constant<int, 4>(), integral_constant<int, 1>());
-    if (runs <= 8) return f(integral_constant<int, 8>(), integral_constant<int, 1>());
-    if (runs <= 16) return f(integral_constant<int, 16>(), integral_constant<int, 1>());
-    if (runs <= 32) return f(integral_constant<int, 32>(), integral_constant<int, 1>());
-    if (runs <= 64) return f(integral_constant<int, 32>(), integral_constant<int, 2>());
-    if (runs <= 128) return f(integral_constant<int, 32>(), integral_constant<int, 4>());
-    if (runs <= 256) return f(integral_constant<int, 256>(), integral_constant<int, 1>());
-    if (runs <= 512) return f(integral_constant<int, 256>(), integral_constant<int, 2>());
-    if (runs <= 1024) return f(integral_constant<int, 256>(), integral_constant<int, 4>());
-    if constexpr (V <= 4)
-        if (runs <= 2048) return f(integral_constant<int, 256>(), integral_constant<int, 8>());
+#define GS_SHAPE(L, NV) \
+    if (runs <= L * NV) return f(integral_constant<int, L>(), integral_constant<int, NV>());
+    GS_SHAPE(4, 1) GS_SHAPE(8, 1) GS_SHAPE(16, 1) GS_SHAPE(32, 1) GS_SHAPE(32, 2) GS_SHAPE(32, 3)
+    GS_SHAPE(32, 4) GS_SHAPE(64, 3) GS_SHAPE(64, 4) GS_SHAPE(128, 3) GS_SHAPE(128, 4)
+    GS_SHAPE(256, 3) GS_SHAPE(256, 4)
+    if constexpr (V <= 4) {
+        GS_SHAPE(256, 6) GS_SHAPE(256, 8)
+    }
+#undef GS_SHAPE
     return cudaErrorInvalidValue;   // not reached: D <= kResOnChip
 }
 
