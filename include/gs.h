@@ -755,12 +755,17 @@ gs_status gs_residual_norm_backward_workspace_size(const gs_residual_norm_attrs 
  *             dz_B need z_scale.  With rows = 0 they are written as zeros.
  *   workspace device, 256-byte aligned, at least the size
  *             gs_residual_norm_backward_workspace_size reports.
+ *             Calls that may run at the same time, replays of captured graphs among
+ *             them, need one each; calls in order on a stream may share one.
  *
  * With N(w, x^, inv) = inv * (w - mean(w) - x^ * mean(w * x^)) (no mean(w) for
  * GS_NORM_RMS), s^ and z^ the normalised S and Z:
  * ds = dS + N(dY * Scale, s^, inv_s);  dX = alpha * ds;  dScale = sum dY * s^,
  * dB = sum dY;  dgate = sum of ds * z' over the rows that share it;  e = gate * ds;
  * dz_scale = sum e * z^, dz_B = sum e;  dZ = N(e * z_scale, z^, inv_z), or e.
+ * The sums over rows are taken in an order that shapes and alignment decide: the same
+ * call gives the same bits.  Above D = 4096 with a gate or z_scale, and above 8192, the
+ * inputs are read twice.
  */
 gs_status gs_residual_norm_backward(const void *dS, const void *dY, const void *S, const void *Z,
                                     const float *Stats, const void *gate, const void *z_scale,
