@@ -657,16 +657,16 @@ gs_status gs_gated_linear_backward_workspace_size(int64_t rows, int64_t D, int64
  *             takes.
  *
  * The sums over D are fp32; G, U and H are each rounded once, at the store, and H
- * is formed of the unrounded G and U.  Up to 32 rows need no workspace (rows of more
- * than 2^18 16-bit elements aside).
+ * is formed of the unrounded G and U.  Up to 16 rows need no workspace, nor up to 32
+ * with F < 4864 (rows of more than 2^18 16-bit elements aside).
  *
- * fp32, more than 32 rows: each factor is taken as three bf16 numbers, and six of their
+ * fp32, more rows than those: each factor is taken as three bf16 numbers, and six of their
  * products are summed in fp32; that keeps fp32's precision, but of a factor below about
  * 2^-110 the lowest bits are lost, and a factor that is infinite, or two whose product
  * leaves fp32's range, may give NaN where a plain sum gives an infinity.
  * The activations take hardware approximations of the exponential and the reciprocal
  * (2 ulps each); where 1 / (1 + e^-g) is below 2^-126 it counts as 0.
- * More than 32 rows of a 16-bit type run on plain FMAs, 7 to 50 times slower, where
+ * More rows than those of a 16-bit type run on plain FMAs, 7 to 50 times slower, where
  * D > 32768, or where D is a multiple of 8 and X, Wg or Wu starts on no 16-byte boundary.
  */
 gs_status gs_gated_linear(const void *X, const void *Wg, const void *Wu, const void *bg,

@@ -18,8 +18,14 @@ constexpr int kFewMost = 32;   // rows of a block
 // Widest rows in 16-bit types: the matrix instruction cuts its sums off as the larger
 // tensor cores do, and a warp's run of them is not broken up.
 constexpr int kFewWidth = 262144;
+// From so many outputs on the large tiles of 64 give every pair of CTAs one; from half as
+// many, blocks of eight warps with two each give every SM one.
+constexpr int kFewFilled = 4864;
+// More than sixteen rows of as many outputs are left to the large tiles: 24 rows, 2048 x
+// 8192, bf16 18 us and here 25, fp32 121 and 128 (and 1024 x 4096, bf16 10.5 and 9.7, fp32
+// 49 and 44).
 template <typename T> bool gated_few_takes(const GatedArgs &a) {
-    return a.rows <= kFewMost && (sizeof(T) == 4 || a.D <= kFewWidth);
+    return a.rows <= (a.F < kFewFilled ? kFewMost : kFewMost / 2) && (sizeof(T) == 4 || a.D <= kFewWidth);
 }
 
 template <typename T>
@@ -102,61 +108,76 @@ __global__ void __launch_bounds__(kFewThreads) gated_few_kernel(GatedArgs a, Gat
     if (r + 1 < a.rows) few_store<T>(a, p, r + 1, f, s.y, s.w);
 }
 
-// fp32: a warp per output and up to R rows, V contiguous weights per lane and step.
-template <int R, int V>
+// fp32: a warp per O (1 or 2) outputs and up to R rows, V contiguous weights per lane and step.  A
+// row's loads serve O outputs: of eight rows they are most of the loads (2048 x 8192, 8 rows,
+// 46 us, and 64 with one output a warp; 1024 x 4096 14 and 23; four rows 45 and 38).
+template <int R, int V, int O>
 __global__ void __launch_bounds__(kFewThreads) gated_few_f32_kernel(GatedArgs a, GatedPtrs p) {
     using IOV = Run<float, V>;
     const int lane = threadIdx.x % 32;
-    const int f = blockIdx.x * kFewWarps + threadIdx.x / 32;
+    const int f = (blockIdx.x * kFewWarps + threadIdx.x / 32) * O;
     const int64_t r0 = (int64_t)blockIdx.y * R;
     if (f >= a.F) return;
     const float *wg = (const float *)p.Wg + (int64_t)f * a.D, *wu = (const float *)p.Wu + (int64_t)f * a.D;
+    const int64_t next = O > 1 && f + 1 < a.F ? a.D : 0;   // to the second output; behind the last, that one
     const float *x = (const float *)p.X + r0 * a.D;
-    float g[R] = {}, u[R] = {};
-#pragma unroll 4
+    float g[O][R] = {}, u[O][R] = {};
+#pragma unroll O == 1 ? 4 : 2
     for (int d = lane * V; d < a.D; d += 32 * V) {
-        float vg[V], vu[V];
-        IOV::widen(IOV::load(wg + d), vg);
-        IOV::widen(IOV::load(wu + d), vu);
+        float vg[O][V], vu[O][V];
+#pragma unroll
+        for (int o = 0; o < O; ++o) {
+            IOV::widen(IOV::load(wg + o * next + d), vg[o]);
+            IOV::widen(IOV::load(wu + o * next + d), vu[o]);
+        }
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             float vx[V];
             IOV::widen(r0 + r < a.rows ? IOV::load(x + (int64_t)r * a.D + d) : IOV::zero(), vx);
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                g[r] = fmaf(vg[e], vx[e], g[r]);
-                u[r] = fmaf(vu[e], vx[e], u[r]);
+            for (int o = 0; o < O; ++o)
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    g[o][r] = fmaf(vg[o][e], vx[e], g[o][r]);
+                    u[o][r] = fmaf(vu[o][e], vx[e], u[o][r]);
+                }
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < O; ++k)
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+                g[k][r] += __shfl_xor_sync(0xffffffffu, g[k][r], o);
+                u[k][r] += __shfl_xor_sync(0xffffffffu, u[k][r], o);
             }
-        }
-    }
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
+    for (int o = 0; o < O; ++o)
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            g[r] += __shfl_xor_sync(0xffffffffu, g[r], o);
-            u[r] += __shfl_xor_sync(0xffffffffu, u[r], o);
-        }
-    }
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-        if (lane == r && r0 + r < a.rows) few_store<float>(a, p, r0 + r, f, g[r], u[r]);
+        for (int r = 0; r < R; ++r)
+            if (lane == o * R + r && r0 + r < a.rows && f + o < a.F)
+                few_store<float>(a, p, r0 + r, f + o, g[o][r], u[o][r]);
 }
 
 template <typename T> cudaError_t launch_gated_few(const GatedArgs &a, const GatedPtrs &p, cudaStream_t s) {
     const bool runs = a.D % kVec<T> == 0 && aligned16(p.X) && aligned16(p.Wg) && aligned16(p.Wu);
     if constexpr (sizeof(T) == 4) {
-        const unsigned blocks = (a.F + kFewWarps - 1) / kFewWarps;
-        const auto run = [&](auto n) {
-            constexpr int R = decltype(n)::value;
-            const auto kernel = runs ? gated_few_f32_kernel<R, 4> : gated_few_f32_kernel<R, 1>;
-            kernel<<<dim3(blocks, (unsigned)((a.rows + R - 1) / R)), kFewThreads, 0, s>>>(a, p);
+        const auto run = [&](auto n, auto outputs) {
+            constexpr int R = decltype(n)::value, O = decltype(outputs)::value;
+            const auto kernel = runs ? gated_few_f32_kernel<R, 4, O> : gated_few_f32_kernel<R, 1, O>;
+            kernel<<<dim3((a.F + kFewWarps * O - 1) / (kFewWarps * O), (unsigned)((a.rows + R - 1) / R)),
+                     kFewThreads, 0, s>>>(a, p);
         };
+        using std::integral_constant;
         if (a.rows == 1)
-            run(std::integral_constant<int, 1>());
+            run(integral_constant<int, 1>(), integral_constant<int, 1>());
         else if (a.rows <= 4)
-            run(std::integral_constant<int, 4>());
+            run(integral_constant<int, 4>(), integral_constant<int, 1>());
+        else if (a.F < kFewFilled / 2)
+            run(integral_constant<int, 8>(), integral_constant<int, 1>());
         else
-            run(std::integral_constant<int, 8>());
+            run(integral_constant<int, 8>(), integral_constant<int, 2>());
     } else {
         const unsigned blocks = (a.F + kFewOutputs - 1) / kFewOutputs;
         const auto run = [&](auto n) {

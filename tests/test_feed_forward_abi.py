@@ -70,6 +70,8 @@ def test_gated_linear_workspace_queries(L):
     for dt in range(3):
         assert _bytes(L.gs_gated_linear_workspace_size, 32, 33, 50, dt) == 0
         assert _bytes(L.gs_gated_linear_workspace_size, 33, 33, 50, dt) > 0
+        assert _bytes(L.gs_gated_linear_workspace_size, 16, 33, 5000, dt) == 0
+        assert _bytes(L.gs_gated_linear_workspace_size, 17, 33, 5000, dt) > 0
     assert _bytes(L.gs_gated_linear_workspace_size, 32, 262144 + 1, 50, 0) == 0
     assert _bytes(L.gs_gated_linear_workspace_size, 32, 262144 + 1, 50, 1) > 0
     # dG and dU at least

@@ -75,6 +75,15 @@ def test_bases_that_are_not_16_byte_aligned(gs_cuda, which, rows, dtype):
     ref.check_gated_backward(back, dH, t["X"], t["Wg"], t["Wu"], G, U, "silu", dtype)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows", [1, 3, 4, 7, 16, 17, 31, 32])
+@pytest.mark.parametrize("D,F", [(40, 4863), (40, 4864), (36, 4867), (131, 5000)])
+def test_few_rows_of_many_outputs(gs_cuda, D, F, rows, dtype):
+    t, _ = _make(rows, D, F, dtype, True, rows)
+    got = gs_cuda.gs_gated_linear(**t, keep=True)
+    ref.check_gated(got, t["X"], t["Wg"], t["Wu"], t["bg"], t["bu"], "silu", dtype)
+
+
 def test_leading_axes_and_views_of_one_projection(gs_cuda):
     t, dH = _make(6, 40, 24, "bfloat16", False)
     packed = torch.cat((t["Wg"], t["Wu"]))
