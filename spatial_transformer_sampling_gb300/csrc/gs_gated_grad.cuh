@@ -127,14 +127,14 @@ __device__ __forceinline__ void store_factor(Factor<T> *to, int64_t plane, const
 
 // In fp16 dG and dU are scaled by a power of two, so that as factors of the products they
 // neither leave the type's range nor fall among its subnormal numbers: 2^14 over the
-// power of two below `bound`, the largest |dH| max(1.13 |U|, |G|) of the call (no
+// power of two below `bound`, the largest finite |dH| max(1.13 |U|, |G|) of the call (no
 // activation's slope is above 1.13, and no activation above |G|, sigmoid's above 1).
 // Finding it takes one more pass over the inputs; the second one finds up to 100 MB of
 // them in L2.
 constexpr float kMostSlope = 1.13f;
 __device__ __forceinline__ float gated_scale(uint32_t bound, bool inverse) {
     const int e = (int)(bound >> 23) - 127;            // of a number that is not negative
-    if (bound == 0 || e == 128) return 1.0f;           // nothing, or infinity
+    if (bound == 0) return 1.0f;                       // nothing
     const int s = max(-100, min(100, inverse ? e - 14 : 14 - e));
     return __int_as_float((s + 127) << 23);
 }
@@ -146,8 +146,11 @@ __global__ void __launch_bounds__(kGradThreads)
     const int64_t total = a.rows * a.F, runs = total / V;
     const float low = a.act == GS_ACT_SIGMOID ? 1.0f : 0.0f;
     float most = 0.0f;
+    // dG's bound and dU's: what is not finite (products of finite fp16 numbers are) is left
+    // out, so that it does not reach the scale of other rows
     const auto take = [&](float h, float g, float u) {
-        most = fmaxf(most, fabsf(h) * fmaxf(kMostSlope * fabsf(u), fmaxf(fabsf(g), low)));
+        const float dg = fabsf(h) * (kMostSlope * fabsf(u)), du = fabsf(h) * fmaxf(fabsf(g), low);
+        most = fmaxf(most, fmaxf(dg < INFINITY ? dg : 0.0f, du < INFINITY ? du : 0.0f));
     };
     // the rows are one array here
 #pragma unroll 2
