@@ -688,10 +688,11 @@ gs_status gs_gated_linear(const void *X, const void *Wg, const void *Wu, const v
  * at 0 is 0.  In 16-bit types dG and dU are rounded to the type as factors of the
  * products (half a step on every term); the biases' sums take them unrounded.  In
  * fp16 they are scaled by a power of two before that rounding, from the largest finite
- * |dH| max(1.13 |U|, |G|) of the call, and the products are scaled back: neither a
- * scaled loss nor a small one leaves the type's range; elements below 2^-39 of that
- * bound count as 0.  A value that is not finite stays in its row of dX and its output's
- * rows of dWg and dWu.  With rows = 0 the gradients of the weights and biases are zeros.
+ * |dG| or |dU| of the call, and the products are scaled back: neither a scaled loss nor
+ * a small one leaves the type's range.  Elements below 2^-28 of the largest are off by
+ * up to 2^-39 of it, where others are off by half a step; what is below that may count
+ * as 0.  A value that is not finite stays in its row of dX and its output's rows of dWg
+ * and dWu.  With rows = 0 the gradients of the weights and biases are zeros.
  */
 gs_status gs_gated_linear_backward(const void *dH, const void *X, const void *Wg, const void *Wu,
                                    const void *G, const void *U, int64_t rows, int64_t D,

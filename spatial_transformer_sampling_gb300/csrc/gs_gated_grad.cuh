@@ -126,12 +126,13 @@ __device__ __forceinline__ void store_factor(Factor<T> *to, int64_t plane, const
 }
 
 // In fp16 dG and dU are scaled by a power of two, so that as factors of the products they
-// neither leave the type's range nor fall among its subnormal numbers: 2^14 over the
-// power of two below `bound`, the largest finite |dH| max(1.13 |U|, |G|) of the call (no
-// activation's slope is above 1.13, and no activation above |G|, sigmoid's above 1).
-// Finding it takes one more pass over the inputs; the second one finds up to 100 MB of
-// them in L2.
-constexpr float kMostSlope = 1.13f;
+// do not leave the type's range: 2^14 over the power of two below `bound`, the largest
+// finite |dG| or |dU| of the call.  What is 2^-28 of that or more keeps the type's
+// precision; smaller elements are off by up to 2^-39 of it.
+// Finding it takes one more pass over the inputs, which forms dG and dU as the next one
+// does: a bound from |dH|, |U| and |G| would let rows far out, whose slopes are 0, take
+// the others' digits (gelu, 16384 x 1024 x 4096, the whole call 488 us, and 480 by a bound).
+// The second pass finds up to 100 MB of the inputs in L2.
 __device__ __forceinline__ float gated_scale(uint32_t bound, bool inverse) {
     const int e = (int)(bound >> 23) - 127;            // of a number that is not negative
     if (bound == 0) return 1.0f;                       // nothing
@@ -144,29 +145,31 @@ __global__ void __launch_bounds__(kGradThreads)
     constexpr int V = kRowsV<T, READ == kRowsSingle ? kRowsSingle : kRowsRuns>;
     using IOV = Run<T, V>;
     const int64_t total = a.rows * a.F, runs = total / V;
-    const float low = a.act == GS_ACT_SIGMOID ? 1.0f : 0.0f;
     float most = 0.0f;
-    // dG's bound and dU's: what is not finite (products of finite fp16 numbers are) is left
-    // out, so that it does not reach the scale of other rows
-    const auto take = [&](float h, float g, float u) {
-        const float dg = fabsf(h) * (kMostSlope * fabsf(u)), du = fabsf(h) * fmaxf(fabsf(g), low);
-        most = fmaxf(most, fmaxf(dg < INFINITY ? dg : 0.0f, du < INFINITY ? du : 0.0f));
-    };
-    // the rows are one array here
+    with_act(a.act, [&](auto act) {
+        // what is not finite is left out, so that it does not reach the scale of other rows
+        const auto take = [&](float h, float g, float u) {
+            float y, slope;
+            act_and_slope<T, decltype(act)::value>(g, y, slope);
+            const float dg = fabsf(h * u * slope), du = fabsf(h * y);
+            most = fmaxf(most, fmaxf(dg < INFINITY ? dg : 0.0f, du < INFINITY ? du : 0.0f));
+        };
+        // the rows are one array here
 #pragma unroll 2
-    for (int64_t i = (int64_t)blockIdx.x * kGradThreads + threadIdx.x; i < runs;
-         i += (int64_t)gridDim.x * kGradThreads) {
-        float h[V], g[V], u[V];
-        IOV::widen(IOV::load(dH + i * V), h);
-        IOV::widen(IOV::load(G + i * V), g);
-        IOV::widen(IOV::load(U + i * V), u);
+        for (int64_t i = (int64_t)blockIdx.x * kGradThreads + threadIdx.x; i < runs;
+             i += (int64_t)gridDim.x * kGradThreads) {
+            float h[V], g[V], u[V];
+            IOV::widen(IOV::load(dH + i * V), h);
+            IOV::widen(IOV::load(G + i * V), g);
+            IOV::widen(IOV::load(U + i * V), u);
 #pragma unroll
-        for (int e = 0; e < V; ++e) take(h[e], g[e], u[e]);
-    }
-    if (blockIdx.x == 0 && runs * V + threadIdx.x < total) {
-        const int64_t e = runs * V + threadIdx.x;
-        take(IO<T>::ld(dH + e), IO<T>::ld(G + e), IO<T>::ld(U + e));
-    }
+            for (int e = 0; e < V; ++e) take(h[e], g[e], u[e]);
+        }
+        if (blockIdx.x == 0 && runs * V + threadIdx.x < total) {
+            const int64_t e = runs * V + threadIdx.x;
+            take(IO<T>::ld(dH + e), IO<T>::ld(G + e), IO<T>::ld(U + e));
+        }
+    });
     // a maximum does not depend on the order, and numbers that are not negative compare
     // as their bits do
     __shared__ float warps[kGradWarps];
