@@ -99,9 +99,10 @@ template <typename T, int ACT> __device__ __forceinline__ void act_and_slope(flo
         a = g * phi;
         da = fmaf(g * 0.3989422804014327f, density, phi);
     } else if (ACT == GS_ACT_GELU_TANH) {
-        const float r = sigmoid_of(kGeluTanh2 * g * fmaf(kGeluCubic * g, g, 1.0f));
+        // the square is bounded: it may not make 0 * infinity of 1 - r = 0
+        const float g2 = fminf(g * g, 1e30f), r = sigmoid_of(kGeluTanh2 * g * fmaf(kGeluCubic, g2, 1.0f));
         a = g * r;
-        da = fmaf(a * (1.0f - r), kGeluTanh2 * fmaf(3.0f * kGeluCubic * g, g, 1.0f), r);
+        da = fmaf(a * (1.0f - r), kGeluTanh2 * fmaf(3.0f * kGeluCubic, g2, 1.0f), r);
     } else if (ACT == GS_ACT_RELU) {
         a = g < 0.0f ? 0.0f : g;
         da = g > 0.0f ? 1.0f : 0.0f;

@@ -71,3 +71,32 @@ def test_rows_of_very_unequal_gradients(gs_cuda, rows, D, F, act, dtype):
     t["dH"] = (t["dH"].float().clamp(-3, 3) * size[:, None]).to(ref.DT[dtype])
     got = gs_cuda.gs_gated_linear_backward(**t, activation=act, bias=True)
     ref.check_gated_backward(got, *(t[k] for k in ORDER), act, dtype)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("rows", [5, 200])
+def test_projections_as_large_as_the_type_holds(gs_cuda, rows, act, dtype):
+    """H is finite where act(G) U is, and the slopes far out are 0, 1 or the factor's own."""
+    dt = ref.DT[dtype]
+    far = [1e4, 65504.0] if dtype == "float16" else [3e4, 1e18, 1e20, 3e30, 3e38]
+    far = torch.tensor(far + [-v for v in far])
+    small = 2.0 ** -10 if dtype == "float16" else 2.0 ** -100
+    X = torch.zeros((rows, 8))
+    X[:, 0], X[:, 1] = far.repeat(-(-rows // len(far)))[:rows], small
+    W = torch.zeros((2, 16, 8))
+    W[0, :, 0] = W[1, :, 1] = 1.0
+    X, Wg, Wu = X.to(dt).cuda(), W[0].to(dt).cuda(), W[1].to(dt).cuda()
+    got = gs_cuda.gs_gated_linear(X, Wg, Wu, activation=act, keep=True)
+    ref.check_gated(got, X, Wg, Wu, None, None, act, dtype, act)
+    dH = torch.full((rows, 16), small, dtype=dt, device="cuda")
+    U = torch.ones_like(dH)
+    back = gs_cuda.gs_gated_linear_backward(dH, X, Wg, Wu, got[1], U, act, True)
+    ref.check_gated_backward(back[:1], dH, X, Wg, Wu, got[1], U, act, dtype, act)
+    # the biases' sums by themselves: a row at a time
+    for r in range(min(rows, len(far))):
+        one = [t[r:r + 1].contiguous() for t in (dH, X, got[1], U)]
+        back = gs_cuda.gs_gated_linear_backward(one[0], one[1], Wg, Wu, one[2], one[3], act, True)
+        _, slope = ref.act(act, ref.wide(one[2]))
+        ref.check(back[3], (ref.wide(one[0]) * slope)[0], (ref.wide(one[0]) * (slope.abs() + 1))[0],
+                  dtype, 64, what="dbg")
