@@ -665,7 +665,10 @@ gs_status gs_gated_linear_backward_workspace_size(int64_t rows, int64_t D, int64
  * 2^-110 the lowest bits are lost, and a factor that is infinite, or two whose product
  * leaves fp32's range, may give NaN where a plain sum gives an infinity.
  * The activations take hardware approximations of the exponential and the reciprocal
- * (2 ulps each); where 1 / (1 + e^-g) is below 2^-126 it counts as 0.
+ * (2 ulps each), whose argument is rounded: 1 / (1 + e^-g) is off by up to |g| 2^-23 of
+ * itself more, Phi and its density by 1.5 g^2 2^-24.  Phi is a polynomial times e^(-g^2/2),
+ * off by 1.1e-6 of itself in 16-bit types and 7e-9 in fp32.  Where 1 / (1 + e^-g) or Phi is
+ * below 2^-126 it counts as 0.
  * More rows than those of a 16-bit type run on plain FMAs, 7 to 50 times slower, where
  * D > 32768, or where D is a multiple of 8 and X, Wg or Wu starts on no 16-byte boundary.
  */

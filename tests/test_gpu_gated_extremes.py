@@ -100,3 +100,59 @@ def test_projections_as_large_as_the_type_holds(gs_cuda, rows, act, dtype):
         _, slope = ref.act(act, ref.wide(one[2]))
         ref.check(back[3], (ref.wide(one[0]) * slope)[0], (ref.wide(one[0]) * (slope.abs() + 1))[0],
                   dtype, 64, what="dbg")
+
+
+def _phi(g):
+    """By erfc: torch.special.ndtr loses its digits below -5 as 1 + erf does (at -8 it is 2 % off)."""
+    return 0.5 * torch.erfc(-g * 0.5 ** 0.5)
+
+
+def _phi_off(g, dtype):
+    """How far Phi(g) and e^(-g^2/2) may be off, relative to them, in steps of 2^-24: the argument of
+    the exponential is formed of three factors rounded by half a step each, which move it by up to
+    3 half steps of its g^2 / 2; 32 for the functions (up to 2 ulps each) and the formula around
+    them.  In 16-bit types Phi comes of a polynomial that is off by 1.1e-6 of it at most."""
+    return 1.5 * g * g + 32 + (0 if dtype == "float32" else 1.1e-6 * 2.0 ** 24)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,aligned", [(1, True), (24, True), (300, True), (300, False)])
+def test_gelu_keeps_its_digits_where_it_is_small(gs_cuda, rows, aligned, dtype):
+    """G = g and U = 2^12 exactly: H is off by half a step of itself, however small Phi(g) is."""
+    dt, F = ref.DT[dtype], 40
+    X = torch.zeros((rows, 8))
+    g = torch.linspace(-6.0 if dtype == "float16" else -8.0, 3.0, rows * F).to(dt)
+    # a row has one G in all columns or, by the weights, F of them
+    X[:, 0], X[:, 1] = (g.view(rows, F)[:, 0].float() if rows > 1 else 1.0), 1.0
+    Wg, Wu = torch.zeros((F, 8)), torch.zeros((F, 8))
+    Wg[:, 0] = 1.0 if rows > 1 else g.float()
+    Wu[:, 1] = 2.0 ** 12
+
+    def moved(t):   # a base that starts on no 16-byte boundary
+        room = torch.empty(t.numel() + 8, dtype=dt, device="cuda")
+        at = room[0 if aligned else 1:][:t.numel()].view(t.shape)
+        return at.copy_(t)
+
+    X, Wg, Wu = moved(X), moved(Wg), moved(Wu)
+    H, G, U = gs_cuda.gs_gated_linear(X, Wg, Wu, activation="gelu", keep=True)
+    exact = ref.wide(X)[:, :1] * ref.wide(Wg)[:, 0]
+    assert torch.equal(ref.wide(G), exact)
+    want = exact * _phi(exact) * 2.0 ** 12
+    ref.check(H, want, want.abs(), dtype, _phi_off(exact, dtype), what="H")
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_gelu_gradients_keep_their_digits_where_they_are_small(gs_cuda, dtype):
+    """The biases' gradients of a single row are dU and dG themselves."""
+    dt, F = ref.DT[dtype], 4000
+    g = torch.linspace(-6.0 if dtype == "float16" else -8.0, 3.0, F).to(dt).cuda()[None]
+    t = _given(1, 8, F, dtype, 2)
+    t.update(G=g, U=torch.full_like(g, 2.0 ** 6), dH=torch.full_like(g, 2.0 ** 6))
+    got = gs_cuda.gs_gated_linear_backward(**t, activation="gelu", bias=True)
+    g = ref.wide(g)[0]
+    density = torch.exp(-g * g / 2) / (2 * torch.pi) ** 0.5
+    a, slope = g * _phi(g), _phi(g) + g * density
+    off = _phi_off(g, dtype)
+    ref.check(got[4], a * 64, a.abs() * 64, dtype, off, what="dU")
+    ref.check(got[3], slope * 4096, (_phi(g) + g.abs() * density) * 4096, dtype, off,
+              what="dG")
