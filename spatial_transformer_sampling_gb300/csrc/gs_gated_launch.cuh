@@ -102,9 +102,10 @@ cudaError_t gated_operands(const GatedArgs &a, const GatedPtrs &p, const GatedLa
     const int runs = (a.D + kVec<T> - 1) / kVec<T>, team = runs <= 8 ? 8 : runs <= 16 ? 16 : 32;
     const int64_t need = ((a.rows > a.F ? a.rows : a.F) * team + 255) / 256;
     const dim3 grid((unsigned)(need < 8 * kGatedSms ? need : 8 * kGatedSms), 3);
-    const auto kernel = read == kRowsSingle ? gated_pad_kernel<T, kRowsSingle>
-                        : read == kRowsRuns ? gated_pad_kernel<T, kRowsRuns>
-                                            : gated_pad_kernel<T, kRowsShifted>;
+    auto kernel = read == kRowsSingle ? gated_pad_kernel<T, kRowsSingle> : gated_pad_kernel<T, kRowsShifted>;
+    if constexpr (sizeof(T) == 4) {   // 16-bit rows of whole runs are read where they lie
+        if (read == kRowsRuns) kernel = gated_pad_kernel<T, kRowsRuns>;
+    }
     kernel<<<grid, 256, 0, s>>>(q, team);
     return cudaGetLastError();
 }
@@ -137,7 +138,7 @@ cudaError_t launch_gated_backward(const GatedArgs &a, const GatedPtrs &p, void *
     cudaError_t e = gated_operands(a, p, at, base, m, s);
     if (e != cudaSuccess) return e;
     uint32_t *bound = (uint32_t *)(base + at.bound);
-    if (__is_same(T, __half)) {
+    if constexpr (__is_same(T, __half)) {
         e = launch_gated_bound<T>(a, p, read != kRowsSingle, bound, s);
         if (e != cudaSuccess) return e;
     }

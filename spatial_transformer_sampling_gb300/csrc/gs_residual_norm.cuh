@@ -1079,28 +1079,30 @@ template <int V, typename F> cudaError_t resnorm_shape(int runs, F &&f) {
         GS_SHAPE(128, 12) GS_SHAPE(128, 16) GS_SHAPE(256, 12) GS_SHAPE(256, 16) GS_SHAPE(256, 24)
         GS_SHAPE(256, 32)
 #undef GS_SHAPE
-    }
+    } else {
 #define GS_SHAPE(L, NV) \
     if (runs <= L * NV) return f(integral_constant<int, L>(), integral_constant<int, NV>());
-    GS_SHAPE(4, 1) GS_SHAPE(8, 1) GS_SHAPE(16, 1) GS_SHAPE(32, 1) GS_SHAPE(32, 2) GS_SHAPE(32, 3)
-    GS_SHAPE(32, 4) GS_SHAPE(64, 3) GS_SHAPE(64, 4) GS_SHAPE(128, 3) GS_SHAPE(128, 4)
-    GS_SHAPE(256, 3) GS_SHAPE(256, 4)
-    if constexpr (V <= 4) {
-        GS_SHAPE(256, 6) GS_SHAPE(256, 8)
-    }
+        GS_SHAPE(4, 1) GS_SHAPE(8, 1) GS_SHAPE(16, 1) GS_SHAPE(32, 1) GS_SHAPE(32, 2) GS_SHAPE(32, 3)
+        GS_SHAPE(32, 4) GS_SHAPE(64, 3) GS_SHAPE(64, 4) GS_SHAPE(128, 3) GS_SHAPE(128, 4)
+        GS_SHAPE(256, 3) GS_SHAPE(256, 4)
+        if constexpr (V == 4) {
+            GS_SHAPE(256, 6) GS_SHAPE(256, 8)
+        }
 #undef GS_SHAPE
+    }
     return cudaErrorInvalidValue;   // not reached: D <= kResOnChip
 }
 
 // The same for the backward pass: f(staged, L, NV).  A team's sums, five per element, stay
 // in registers, up to eight elements of a thread where rows are staged.  Rows of a warp's run
 // or less keep their loads in registers: a bulk copy of 128 bytes costs as much to issue as
-// one of a few KB (508400 x 33 bf16 117 us, staged 481; 83886 x 200 130 and 64).
-template <int V, typename F> cudaError_t resnorm_backward_shape(int D, F &&f) {
+// one of a few KB (508400 x 33 bf16 117 us, staged 481; 83886 x 200 130 and 64).  MORE: there
+// are more than two sums, and rows wider than kResStaged are read again (resnorm_wide).
+template <int V, bool MORE, typename F> cudaError_t resnorm_backward_shape(int D, F &&f) {
     using std::integral_constant;
     using std::false_type;
     using std::true_type;
-    const int runs = (D + V - 1) / V;
+    constexpr int NV = kStagedN / V;
     if constexpr (V <= 2) {
 #define GS_SHAPE(STAGED, L, N)        \
     if constexpr (N % V == 0)         \
@@ -1112,18 +1114,21 @@ template <int V, typename F> cudaError_t resnorm_backward_shape(int D, F &&f) {
         GS_SHAPE(true_type, 64, 8) GS_SHAPE(true_type, 128, 6) GS_SHAPE(true_type, 128, 8)
         GS_SHAPE(true_type, 256, 6) GS_SHAPE(true_type, 256, 8) GS_SHAPE(true_type, 512, 6)
 #undef GS_SHAPE
+    } else {
+        const int runs = (D + V - 1) / V;
+        if (runs <= 4) return f(false_type(), integral_constant<int, 4>(), integral_constant<int, 1>());
+        if (runs <= 8) return f(false_type(), integral_constant<int, 8>(), integral_constant<int, 1>());
+        if (runs <= 16) return f(false_type(), integral_constant<int, 16>(), integral_constant<int, 1>());
+        if (runs <= 32) return f(false_type(), integral_constant<int, 32>(), integral_constant<int, 1>());
+        if constexpr (V == 4)   // of eight elements, 32 runs are 256
+            if (D <= 256) return f(true_type(), integral_constant<int, 32>(), integral_constant<int, NV>());
+        if (D <= 512) return f(true_type(), integral_constant<int, 64>(), integral_constant<int, NV>());
+        if (D <= 1024) return f(true_type(), integral_constant<int, 128>(), integral_constant<int, NV>());
+        if (D <= 2048) return f(true_type(), integral_constant<int, 256>(), integral_constant<int, NV>());
     }
-    if (runs <= 4) return f(false_type(), integral_constant<int, 4>(), integral_constant<int, 1>());
-    if (runs <= 8) return f(false_type(), integral_constant<int, 8>(), integral_constant<int, 1>());
-    if (runs <= 16) return f(false_type(), integral_constant<int, 16>(), integral_constant<int, 1>());
-    if (runs <= 32) return f(false_type(), integral_constant<int, 32>(), integral_constant<int, 1>());
-    constexpr int NV = kStagedN / V;
-    if (D <= 256) return f(true_type(), integral_constant<int, 32>(), integral_constant<int, NV>());
-    if (D <= 512) return f(true_type(), integral_constant<int, 64>(), integral_constant<int, NV>());
-    if (D <= 1024) return f(true_type(), integral_constant<int, 128>(), integral_constant<int, NV>());
-    if (D <= 2048) return f(true_type(), integral_constant<int, 256>(), integral_constant<int, NV>());
     if (D <= kResStaged) return f(true_type(), integral_constant<int, 512>(), integral_constant<int, NV>());
-    return f(false_type(), integral_constant<int, 512>(), integral_constant<int, 2 * NV>());
+    if constexpr (!MORE) return f(false_type(), integral_constant<int, 512>(), integral_constant<int, 2 * NV>());
+    return cudaErrorInvalidValue;   // not reached: rows that are read again
 }
 // Rows that are read again for the sums: those that do not fit a block's registers beside
 // more than two sums (2048 x 8192 bf16: two sums in registers 45 us, read again 84; five
@@ -1138,7 +1143,7 @@ template <typename T, int V> ResNormPlan resnorm_plan_of(const ResNormArgs &a, b
         const int columns = resnorm_sums_columns(a.D, V);
         return resnorm_plan(a, 1, std::max(1, kResSumsBlocks<V> * kResSms / columns));
     }
-    resnorm_backward_shape<V>(a.D, [&](auto staged, auto l, auto nv) {
+    resnorm_backward_shape<V, false>(a.D, [&](auto staged, auto l, auto nv) {
         constexpr int L = decltype(l)::value, NV = decltype(nv)::value;
         q = decltype(staged)::value
                 ? resnorm_plan(a, kStagedThreads / L, kResSms)
@@ -1206,9 +1211,11 @@ cudaError_t launch_resnorm(const ResNormArgs &a, const ResNormPtrs &p, cudaStrea
         a.D, {p.X, p.Z, p.gate, p.z_scale, p.z_B, p.scale, p.B, p.S, p.Y}, [&](auto v) {
             constexpr int V = decltype(v)::value;
             if (a.D <= kResOnChip) return run_resnorm<T, V>(a, p, s);
-            const bool large = resnorm_large<T>(a);
-            const auto kernel = large ? resnorm_wide_kernel<T, V, 512> : resnorm_wide_kernel<T, V, 256>;
-            kernel<<<(unsigned)a.rows, large ? 512 : 256, 0, s>>>(a, p);
+            if (sizeof(T) == 4 || resnorm_large<T>(a)) {   // in fp32 they all are
+                resnorm_wide_kernel<T, V, 512><<<(unsigned)a.rows, 512, 0, s>>>(a, p);
+            } else if constexpr (sizeof(T) == 2) {
+                resnorm_wide_kernel<T, V, 256><<<(unsigned)a.rows, 256, 0, s>>>(a, p);
+            }
             return cudaGetLastError();
         });
 }
@@ -1237,7 +1244,7 @@ cudaError_t run_resnorm_backward(const ResNormArgs &a, const ResNormPtrs &p, con
                                  float *partials, float *gate_partials, cudaStream_t s) {
     const auto form = [&](auto post, auto gate) {
         constexpr bool POST = decltype(post)::value, GATE = decltype(gate)::value;
-        return resnorm_backward_shape<V>(a.D, [&](auto staged, auto l, auto nv) {
+        return resnorm_backward_shape<V, POST || GATE>(a.D, [&](auto staged, auto l, auto nv) {
             constexpr int L = decltype(l)::value, NV = decltype(nv)::value;
             if constexpr (decltype(staged)::value) {
                 return run_resnorm_staged<T, V, L, NV, POST, GATE>(a, p, q, partials, gate_partials, s);
