@@ -113,12 +113,14 @@ cudaError_t gated_operands(const GatedArgs &a, const GatedPtrs &p, const GatedLa
 template <typename T>
 cudaError_t launch_gated(const GatedArgs &a, const GatedPtrs &p, void *ws, cudaStream_t s) {
     if (gated_few_takes<T>(a)) return launch_gated_few<T>(a, p, s);
-    GtMatrix m[3];
-    const GatedLayout<T> at(a, false);
-    bool used = false;
-    cudaError_t e = gated_operands(a, p, at, (char *)ws, m, s);
-    if (e == cudaSuccess) e = launch_gt_forward<T>(a, p, m[0], m[1], m[2], at.copy, s, &used);
-    if (e != cudaSuccess || used) return e;
+    if (gt_forward_takes<T>(a)) {   // longer rows are read where they lie, not copied
+        GtMatrix m[3];
+        const GatedLayout<T> at(a, false);
+        bool used = false;
+        cudaError_t e = gated_operands(a, p, at, (char *)ws, m, s);
+        if (e == cudaSuccess) e = launch_gt_forward<T>(a, p, m[0], m[1], m[2], at.copy, s, &used);
+        if (e != cudaSuccess || used) return e;
+    }
     if constexpr (sizeof(T) == 2) {
         gated_simt_kernel<T><<<(unsigned)simt_blocks(a.rows, a.F), kSimtThreads, 0, s>>>(a, p);
         return cudaGetLastError();

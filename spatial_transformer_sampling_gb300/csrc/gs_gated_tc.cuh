@@ -960,14 +960,17 @@ template <typename T> __global__ void __launch_bounds__(256) gated_join_kernel(G
     }
 }
 
+// Whether a forward row's sum in TMEM is not too long.
+template <typename T> bool gt_forward_takes(const GatedArgs &a) {
+    return sizeof(T) == 4 || a.D <= kGtLongest * kGtK;
+}
+
 // Forward pass from 16-bit operands (T float: planes); *used: TMA takes them.
 template <typename T>
 cudaError_t launch_gt_forward(const GatedArgs &a, const GatedPtrs &q, const GtMatrix &X,
                               const GtMatrix &Wg, const GtMatrix &Wu, bool follows, cudaStream_t s,
                               bool *used) {
     GtArgs p = {};
-    *used = false;
-    if (sizeof(T) == 2 && a.D > kGtLongest * kGtK) return cudaSuccess;
     GtKind &k = p.kind[0];
     k.tiles_m = (int)((a.rows + kGtTile - 1) / kGtTile);
     k.k_steps = (a.D + kGtK - 1) / kGtK;

@@ -156,3 +156,16 @@ def test_gelu_gradients_keep_their_digits_where_they_are_small(gs_cuda, dtype):
     ref.check(got[4], a * 64, a.abs() * 64, dtype, off, what="dU")
     ref.check(got[3], slope * 4096, (_phi(g) + g.abs() * density) * 4096, dtype, off,
               what="dG")
+
+
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+def test_rows_that_no_copy_serves_are_not_copied(gs_cuda, dtype):
+    """Forward rows beyond 32768 elements are read where they lie: the workspace stays as it was."""
+    rows, D, F = 40, 32777, 24
+    t = _given(rows, D, F, dtype, 8)
+    t = {k: t[k] for k in ("X", "Wg", "Wu")}
+    n = gs_cuda.gs_gated_linear_workspace_size(rows, D, F, ref.DT[dtype])
+    ws = torch.full((max(n, 256),), 255, dtype=torch.uint8, device="cuda")
+    got = gs_cuda.gs_gated_linear(**t, keep=True, workspace=ws)
+    ref.check_gated(got, t["X"], t["Wg"], t["Wu"], None, None, "silu", dtype)
+    assert (ws == 255).all()
