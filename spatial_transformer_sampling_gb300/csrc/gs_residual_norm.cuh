@@ -587,6 +587,7 @@ __device__ __forceinline__ void staged_fetch(unsigned char *to, const T *from, i
         T *row = reinterpret_cast<T *>(to + ((uintptr_t)from & 15));
         for (int d = 0; d < D && (uintptr_t)(from + d) < a; ++d) row[d] = from[d];
         for (int d = D - 1; d >= 0 && (uintptr_t)(from + d) >= b; --d) row[d] = from[d];
+        fence_proxy_async_smem();   // before this thread's later copies to the same place
     }
     const uint32_t bytes = (uint32_t)(b - a);
     mbar_arrive_expect_tx(bar, bytes);
