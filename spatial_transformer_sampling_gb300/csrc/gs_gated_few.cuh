@@ -44,7 +44,8 @@ __device__ __forceinline__ void few_mma(float (&c)[4], uint32_t a0, uint32_t a1,
 }
 
 // Eight elements from d on of a row of D; zeros behind its end and for a row that is
-// not there.  RUNS: rows are multiples of 16 bytes and start on one.
+// not there.  RUNS: rows are multiples of 16 bytes and start on one; others are loaded an
+// element at a time (8192 outputs bf16, one row of 2048 16 us, of 2047 27; 16 rows 17 and 36).
 template <typename T, bool RUNS>
 __device__ __forceinline__ uint4 few_load(const T *row, bool here, int d, int D) {
     if (RUNS) return here && d < D ? __ldg(reinterpret_cast<const uint4 *>(row + d)) : uint4();
@@ -110,7 +111,8 @@ __global__ void __launch_bounds__(kFewThreads) gated_few_kernel(GatedArgs a, Gat
 
 // fp32: a warp per O (1 or 2) outputs and up to R rows, V contiguous weights per lane and step.  A
 // row's loads serve O outputs: of eight rows they are most of the loads (2048 x 8192, 8 rows,
-// 46 us, and 64 with one output a warp; 1024 x 4096 14 and 23; four rows 45 and 38).
+// 46 us, and 64 with one output a warp; 1024 x 4096 14 and 23; four rows 45 and 38).  More than
+// eight rows are R at a time on the grid's y axis, and each reads the weights: 16 rows 84 us.
 template <int R, int V, int O>
 __global__ void __launch_bounds__(kFewThreads) gated_few_f32_kernel(GatedArgs a, GatedPtrs p) {
     using IOV = Run<float, V>;

@@ -104,7 +104,9 @@ template <typename T> int rows_read(int width, std::initializer_list<const void 
 }
 
 // Stores a run where the products read it: rounded to the type, or, of fp32, in three
-// planes `plane` elements apart.
+// planes `plane` elements apart.  In 16-bit types that rounding shows in the products (2.3e-3
+// of them in bf16 and 2.9e-4 in fp16, 1.7e-3 and 2.1e-4 by the store alone): a second plane
+// would take it away for twice the products, which are 289 of the 414 us of 16384 x 1024 x 4096.
 template <typename T> using Factor = std::conditional_t<sizeof(T) == 4, __nv_bfloat16, T>;
 template <typename T, int V>
 __device__ __forceinline__ void store_factor(Factor<T> *to, int64_t plane, const float (&v)[V]) {

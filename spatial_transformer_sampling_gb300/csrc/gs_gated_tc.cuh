@@ -37,8 +37,8 @@
 // sixteen products a result is off by up to n 2^-24 of its size, always towards 0.  In
 // fp32 the contraction is cut into runs of 4 stages of six products, each accumulated in
 // TMEM by itself and added up in the epilogue's registers, rounded to nearest (2.4e-7 of
-// the result at D = 2048); in 16-bit types no sum in TMEM is longer than 512 stages,
-// 1.2e-4 of the result, a quarter of fp16's half step.
+// the result at D = 2048, the root of the mean square); in 16-bit types no sum in TMEM is
+// longer than 512 stages, 1.2e-4 of the result, a quarter of fp16's half step.
 #pragma once
 
 #include "gs_attn_tc.cuh"
