@@ -117,6 +117,7 @@ def gs_gated_linear(X, Wg, Wu, bg=None, bu=None, activation="silu", keep=False, 
     X (..., D), Wg and Wu (F, D), bg and bu (F) or both None; ``activation`` is "silu", "gelu",
     "gelu_tanh", "relu", "sigmoid" or "identity".  H is (..., F); with ``keep`` the call returns
     (H, G, U), where G and U are the two projections, which the backward pass takes.
+    ``out``: a tensor for H that overlaps no input.
     ``workspace``: "auto", or a device tensor of at least gs_gated_linear_workspace_size bytes."""
     act = ACTIVATIONS.get(activation)
     if act is None:
